@@ -64,7 +64,13 @@ enum { ZERO_BF16 = 0, ZERO_F32 = 1 };                 /* source element type */
 enum { ZERO_OUT_FULL = 0, ZERO_OUT_SHARD = 1 };       /* where the bf16 result goes */
 enum { ZERO_ACC_LOCAL = 0, ZERO_ACC_REDUCE = 1 };     /* accumulation mode */
 
+enum { ZERO_ACT_NONE = 0, ZERO_ACT_RELU = 1, ZERO_ACT_GELU = 2,       /* activation of a linear: GELU by erf, */
+       ZERO_ACT_GELU_TANH = 3, ZERO_ACT_SILU = 4 };                   /* by its tanh form; z * sigmoid(z) */
+enum { ZERO_ROPE_HALF = 0, ZERO_ROPE_INTERLEAVED = 1 };               /* pairs (i, i + rot/2) or (2i, 2i + 1) */
+enum { ZERO_ROPE_NONE = 0, ZERO_ROPE_LINEAR = 1, ZERO_ROPE_NTK = 2, ZERO_ROPE_YARN = 3 };   /* context scaling */
+
 #define ZERO_MAX_SRC 64   /* most source buffers one call reads */
+#define ZERO_ROPE_MAX 256 /* most elements of a head that zero_rope turns */
 
 /* ---- structures --------------------------------------------------------- */
 
@@ -96,6 +102,30 @@ typedef struct {
      * step can be replayed step after step.  4-byte aligned. */
     const float* sched;
 } zero_adamw_t;
+
+/* One place and pass of dropout: which elements are dropped is a function of
+ * (seed, site, step, row, column) alone. */
+typedef struct {
+    double p;               /* share of elements dropped, 0..1, taken to the nearest 2^-16 */
+    uint64_t seed;
+    uint32_t site;          /* numbers the places of a model that drop */
+    uint32_t reserved;      /* zero */
+    uint64_t step;          /* numbers the passes through it, below 2^32 */
+    /* NULL, or a DEVICE pointer to an integer added to step (modulo 2^32), read
+     * by the kernels: a captured graph then drops other elements at each replay
+     * (zero_schedule_advance's step_index serves). */
+    const uint64_t* step_ptr;
+} zero_dropout_t;
+
+/* What zero_rope turns by, filled by zero_rope_fill (host memory, read during
+ * the call). */
+typedef struct {
+    int32_t rot;            /* elements of a head that are turned, even, 2..ZERO_ROPE_MAX */
+    int32_t layout;         /* ZERO_ROPE_HALF or ZERO_ROPE_INTERLEAVED */
+    float scale;            /* factor on the turned elements */
+    int32_t reserved;       /* zero */
+    uint64_t turn[ZERO_ROPE_MAX / 2];   /* 2^-64ths of a turn a position, by pair */
+} zero_rope_plan_t;
 
 /* ---- layout --------------------------------------------------------------
  * "ZeRO and FSDP", "The idea, one stage at a time" (flatten into one vector,
@@ -474,6 +504,85 @@ int zero_ckpt_payload_crc(const char* path, uint32_t* crc);
 int zero_ckpt_read_shard(const char* path, zero_ckpt_header_t* h, float* master, float* m,
                          float* v, uint16_t* w_bf16, int64_t capacity);
 uint32_t zero_crc32(const void* data, int64_t n);
+
+/* ---- the dense operators of a unit -------------------------------------------
+ * What runs between the bf16 weights that a step gathers and the bf16 gradient
+ * buffer that it reduces: products with their elementwise ends, dropout and
+ * rotary positions, each with its gradient.  The pages leave forward and backward
+ * to the model ("ZeRO Optimizer, in depth", "Running it with DeepSpeed":
+ * loss = engine(batch); engine.backward(loss)); these calls are an addition.
+ *
+ * Matrices are row-major with rows `ld*` elements apart (ld >= columns) and their
+ * own element type; any element-aligned pointer and any ld are taken.  w, dw and
+ * db may be slices of the flat weight and gradient buffers.  Where the reads
+ * of a call are 16-byte aligned, pointer and ld, the tiles come by TMA.  Sizes of zero are allowed:
+ * an empty result is left alone, an empty sum is 0.  An output may be the very
+ * matrix of the residual, acc or db_acc it is added to (same pointer and ld);
+ * outputs overlap no other argument.  Products and sums are held in fp32.
+ *
+ * zero_linear:              y[m,n] = residual + D(act(z)),  z = x[m,k] w[n,k]^T + bias[n]
+ *   pre (or NULL) receives z in bf16 for the gradient.  bias, residual, drop may
+ *   be NULL.  y and residual are y_dtype (bf16 or fp32); the rest is bf16.
+ * zero_linear_grad_input:   dx[m,k] = residual + D'(dz[m,n] w[n,k]) act'(pre[m,k])
+ *   act, pre and drop are those of the layer below, whose y was this layer's x,
+ *   so that dx is that layer's dz; pre is given exactly where act is not NONE.
+ * zero_linear_grad_weight:  dw[n,k] = acc + dz[m,n]^T x[m,k],  db[n] = db_acc + sum over m of dz
+ *   acc, db, db_acc may be NULL; acc, dw, db_acc and db are dw_dtype.
+ * zero_dropout:             y = residual + D(x), all `dtype`; residual may be NULL.
+ * zero_dropout_grad:        dx = D'(dy) act'(pre),  db[c] = db_acc[c] + sum over rows of dx
+ *   the dz of a linear whose epilogue dropped and activated; dx may be dy itself
+ *   (same type and ld).  The sum is of the fp32 values, before dx is rounded.
+ * D multiplies an element by 65536 / (65536 - cut), cut = round(65536 p), where
+ *   its 16 random bits are at least cut and puts 0 elsewhere (whatever stood
+ *   there); D' drops the same elements.  The bits of column c of row r are half
+ *   (c % 8) % 2, low first, of word (c % 8) / 2 of Philox4x32-10 at counter
+ *   (c / 8, r, site, step) under key (low, high half of seed).  No mask is
+ *   stored.  drop NULL or cut 0 keeps everything; cut 65536 drops everything.
+ * Results repeat from run to run: no sum depends on the order of atomics.
+ * Errors: ZERO_EINVAL (negative size, ld below the columns, bad type, act, p or
+ *   combination, a null or non-device pointer), ZERO_ERANGE (a byte count past 63
+ *   bits; with dropout more than 2^32 rows; step of 2^32 or more), ZERO_EALIGN,
+ *   ZERO_ECUDA. */
+int zero_linear(int64_t m, int64_t n, int64_t k, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                int64_t ldw, const uint16_t* bias, int32_t act, const zero_dropout_t* drop,
+                const void* residual, int64_t ldr, uint16_t* pre, int64_t ldp, void* y, int32_t y_dtype,
+                int64_t ldy, void* stream);
+int zero_linear_grad_input(int64_t m, int64_t n, int64_t k, const uint16_t* dz, int64_t lddz,
+                           const uint16_t* w, int64_t ldw, int32_t act, const zero_dropout_t* drop,
+                           const uint16_t* pre, int64_t ldp, const void* residual, int64_t ldr, void* dx,
+                           int32_t dx_dtype, int64_t lddx, void* stream);
+int zero_linear_grad_weight(int64_t m, int64_t n, int64_t k, const uint16_t* dz, int64_t lddz,
+                            const uint16_t* x, int64_t ldx, const void* acc, int64_t ldacc, void* dw,
+                            int32_t dw_dtype, int64_t lddw, const void* db_acc, void* db, void* stream);
+int zero_dropout(int64_t rows, int64_t cols, const void* x, int64_t ldx, int32_t dtype,
+                 const zero_dropout_t* drop, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                 void* stream);
+int zero_dropout_grad(int64_t rows, int64_t cols, const void* dy, int64_t lddy, int32_t dy_dtype,
+                      const zero_dropout_t* drop, int32_t act, const uint16_t* pre, int64_t ldp, void* dx,
+                      int32_t dx_dtype, int64_t lddx, const void* db_acc, void* db, int32_t db_dtype,
+                      void* stream);
+
+/* Rotary positions (Su et al., "RoFormer", 2021): the first plan->rot elements of
+ * every head, in pairs (a, b), become
+ *   scale * (a cos t - b sin t, b cos t + a sin t),  t = position * theta_i,
+ * or with inverse = 1 the turn back by the same scale, which is the gradient.
+ * Elements past rot are copied.  x and y are [tokens, heads, dim] with element
+ * strides per token and head, dim contiguous, both `dtype`; y may be x itself
+ * (same strides).  positions: device int64 [tokens], or NULL for pos0 + token.
+ * Any 64-bit position is reduced to one turn exactly.
+ * zero_rope_fill (host only): theta_i = base^(-2i/rot), scaled for contexts
+ *   `factor` times as long: LINEAR theta / factor (position interpolation), NTK
+ *   base * factor^(rot/(rot-2)), YARN by wavelength (Peng et al., 2023): with
+ *   r = context * theta / 2 pi turns in the first context, theta / factor where
+ *   r < 1, theta where r > 32, linear in r between, and scale = 0.1 ln factor + 1.
+ * Errors: ZERO_EINVAL (rot odd or out of range, dim < rot, layout, scaling, base
+ *   <= 1, factor < 1, negative strides, heads of y that overlap, pointers),
+ *   ZERO_ERANGE, ZERO_EALIGN, ZERO_ECUDA. */
+int zero_rope_fill(int32_t rot, int32_t layout, double base, int32_t scaling, double factor, double context,
+                   zero_rope_plan_t* plan);
+int zero_rope(const zero_rope_plan_t* plan, int64_t tokens, int64_t heads, int64_t dim, const void* x,
+              int64_t x_token, int64_t x_head, void* y, int64_t y_token, int64_t y_head, int32_t dtype,
+              const int64_t* positions, int64_t pos0, int32_t inverse, void* stream);
 
 /* ---- status ---------------------------------------------------------------
  * Synchronizes `stream` and returns ZERO_ECUDA if it (or an earlier launch on

@@ -22,6 +22,11 @@ _BINDING_NAMES = {
     "ZERO_EIO", "ZERO_ECORRUPT",
     "ZERO_BF16", "ZERO_F32", "ZERO_OUT_FULL", "ZERO_OUT_SHARD",
     "ZERO_ACC_LOCAL", "ZERO_ACC_REDUCE", "ZERO_MAX_SRC",
+    "ZeroDropout", "ZeroRopePlan", "zero_linear", "zero_linear_grad_input", "zero_linear_grad_weight",
+    "zero_dropout", "zero_dropout_grad", "zero_rope_plan", "zero_rope",
+    "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU", "ZERO_ACT_GELU_TANH", "ZERO_ACT_SILU",
+    "ZERO_ROPE_HALF", "ZERO_ROPE_INTERLEAVED", "ZERO_ROPE_NONE", "ZERO_ROPE_LINEAR", "ZERO_ROPE_NTK",
+    "ZERO_ROPE_YARN", "ZERO_ROPE_MAX",
 }
 
 

@@ -23,6 +23,10 @@ ZERO_BF16, ZERO_F32 = 0, 1
 ZERO_OUT_FULL, ZERO_OUT_SHARD = 0, 1
 ZERO_ACC_LOCAL, ZERO_ACC_REDUCE = 0, 1
 ZERO_MAX_SRC = 64
+ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_SILU = 0, 1, 2, 3, 4
+ZERO_ROPE_HALF, ZERO_ROPE_INTERLEAVED = 0, 1
+ZERO_ROPE_NONE, ZERO_ROPE_LINEAR, ZERO_ROPE_NTK, ZERO_ROPE_YARN = 0, 1, 2, 3
+ZERO_ROPE_MAX = 256
 
 
 class ZeroError(RuntimeError):
@@ -71,6 +75,30 @@ class ZeroAdamW(ctypes.Structure):
         hp = cls(lr, beta1, beta2, eps, weight_decay, 0, step, ptr)
         hp._sched_tensor = sched
         return hp
+
+
+class ZeroDropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("site", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("step", ctypes.c_uint64),
+                ("step_ptr", ctypes.c_void_p)]
+
+    @classmethod
+    def make(cls, p: float, seed: int = 0, site: int = 0, step: int = 0, step_ptr=None):
+        """One place (site) and pass (step) of dropout with share p.  step_ptr:
+        None, or a CUDA int64 tensor whose element the kernels add to step (a
+        StepSchedule's step_index, so that each replay of a captured step drops
+        other elements); the block keeps a reference to it."""
+        if not (0 <= seed < 1 << 64 and 0 <= site < 1 << 32 and 0 <= step < 1 << 32):
+            raise ValueError("seed must fit 64 bits, site and step 32, none negative")
+        ptr = None if step_ptr is None else _tensor(step_ptr, "step_ptr", torch.int64, 1)
+        drop = cls(p, seed, site, 0, step, ptr)
+        drop._step_tensor = step_ptr
+        return drop
+
+
+class ZeroRopePlan(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turn", ctypes.c_uint64 * (ZERO_ROPE_MAX // 2))]
 
 
 _lock = threading.Lock()
@@ -133,6 +161,20 @@ def load():
                                              i32, p]
         lib.zero_accumulate.argtypes = [P(ZeroLayout), i32, P(p), i32, i32, i64, p, i64, i64, i64,
                                         i32, p]
+        D = P(ZeroDropout)
+        lib.zero_linear.argtypes = [i64, i64, i64, p, i64, p, i64, p, i32, D, p, i64, p, i64, p, i32,
+                                    i64, p]
+        lib.zero_linear_grad_input.argtypes = [i64, i64, i64, p, i64, p, i64, i32, D, p, i64, p, i64, p,
+                                               i32, i64, p]
+        lib.zero_linear_grad_weight.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i32, i64, p,
+                                                p, p]
+        lib.zero_dropout.argtypes = [i64, i64, p, i64, i32, D, p, i64, p, i64, p]
+        lib.zero_dropout_grad.argtypes = [i64, i64, p, i64, i32, D, i32, p, i64, p, i32, i64, p, p, i32,
+                                          p]
+        lib.zero_rope_fill.argtypes = [i32, i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double,
+                                       P(ZeroRopePlan)]
+        lib.zero_rope.argtypes = [P(ZeroRopePlan), i64, i64, i64, p, i64, i64, p, i64, i64, i32, p, i64,
+                                  i32, p]
         lib.zero_status_check.argtypes = [p]
         lib.zero_strerror.argtypes = [ctypes.c_int]
         lib.zero_strerror.restype = ctypes.c_char_p
@@ -154,7 +196,9 @@ def load():
                      "zero_schedule_fill", "zero_schedule_advance",
                      "zero_accumulate_int8", "zero_gather_layer", "zero_accumulate",
                      "zero_status_check", "zero_memory_bytes", "zero_comm_bytes",
-                     "zero_lr_warmup_decay"):
+                     "zero_lr_warmup_decay", "zero_linear", "zero_linear_grad_input",
+                     "zero_linear_grad_weight", "zero_dropout", "zero_dropout_grad",
+                     "zero_rope_fill", "zero_rope"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -570,3 +614,171 @@ def zero_selftest_bounded_wait(limit_cycles: int, stream=None):
     """Run the bounded-wait self test (see zero_gb300.h); follow with zero_status_check."""
     _check(load().zero_selftest_bounded_wait(int(limit_cycles), _stream_ptr(stream)),
            "zero_selftest_bounded_wait")
+
+
+# --------------------------------------------------------------------------
+# the dense operators of a unit
+# --------------------------------------------------------------------------
+
+_DT_CODE = {torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
+_BF16_ONLY = {torch.bfloat16: ZERO_BF16}
+
+
+def _matrix(t, name, rows, cols, dtypes):
+    """Pointer, row stride and type code of a [rows, cols] matrix whose rows are
+    contiguous; None gives a null pointer."""
+    if t is None:
+        return None, cols, ZERO_BF16
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device}); there is no CPU path")
+    code = dtypes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must have shape ({rows}, {cols}), got {tuple(t.shape)}")
+    ld, inner = t.stride()
+    if rows <= 1 or cols == 0:
+        ld = cols
+    if (cols > 1 and inner != 1) or ld < cols:
+        raise ValueError(f"{name} must have rows of contiguous elements (strides {t.stride()})")
+    return t.data_ptr(), ld, code
+
+
+def _vector(t, name, n, code):
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    return _tensor(t, name, _SRC_DT[code], n)
+
+
+def _sizes(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape
+
+
+def _same_type(name, code, t, other):
+    if t is not None and _DT_CODE.get(t.dtype) != code:
+        raise TypeError(f"{name} must have the type of {other}, got {t.dtype}")
+
+
+def zero_linear(x, w, y, bias=None, act: int = ZERO_ACT_NONE, residual=None,
+                drop: ZeroDropout | None = None, pre=None, stream=None):
+    """y[m, n] = residual + D(act(x[m, k] w[n, k]^T + bias)); pre, if given,
+    receives the value before the activation (bf16), for the gradient.  x, w, bias
+    and pre are bf16; y and residual bf16 or fp32."""
+    (m, k), n = _sizes(x, "x"), _sizes(w, "w")[0]
+    xp, ldx, _ = _matrix(x, "x", m, k, _BF16_ONLY)
+    wp, ldw, _ = _matrix(w, "w", n, k, _BF16_ONLY)
+    yp, ldy, code = _matrix(y, "y", m, n, _DT_CODE)
+    _same_type("residual", code, residual, "y")
+    rp, ldr, _ = _matrix(residual, "residual", m, n, _DT_CODE)
+    pp, ldp, _ = _matrix(pre, "pre", m, n, _BF16_ONLY)
+    _check(load().zero_linear(m, n, k, xp, ldx, wp, ldw, _vector(bias, "bias", n, ZERO_BF16), act, drop,
+                              rp, ldr, pp, ldp, yp, code, ldy, _stream_ptr(stream)), "zero_linear")
+
+
+def zero_linear_grad_input(dz, w, dx, act: int = ZERO_ACT_NONE, pre=None,
+                           drop: ZeroDropout | None = None, residual=None, stream=None):
+    """dx[m, k] = residual + D'(dz[m, n] w[n, k]) act'(pre); act, pre and drop are
+    those of the layer below (whose y was this layer's x), so that dx is its dz."""
+    (m, n), k = _sizes(dz, "dz"), _sizes(w, "w")[1]
+    zp, lddz, _ = _matrix(dz, "dz", m, n, _BF16_ONLY)
+    wp, ldw, _ = _matrix(w, "w", n, k, _BF16_ONLY)
+    xp, lddx, code = _matrix(dx, "dx", m, k, _DT_CODE)
+    _same_type("residual", code, residual, "dx")
+    rp, ldr, _ = _matrix(residual, "residual", m, k, _DT_CODE)
+    pp, ldp, _ = _matrix(pre, "pre", m, k, _BF16_ONLY)
+    _check(load().zero_linear_grad_input(m, n, k, zp, lddz, wp, ldw, act, drop, pp, ldp, rp, ldr, xp,
+                                         code, lddx, _stream_ptr(stream)), "zero_linear_grad_input")
+
+
+def zero_linear_grad_weight(dz, x, dw, db=None, acc=None, db_acc=None, stream=None):
+    """dw[n, k] = acc + dz[m, n]^T x[m, k] and db[n] = db_acc + the column sums of
+    dz.  dw, acc, db and db_acc have one type, bf16 or fp32; dw may be acc itself
+    (and db db_acc): gradients are then accumulated in place."""
+    (m, n), k = _sizes(dz, "dz"), _sizes(x, "x")[1]
+    zp, lddz, _ = _matrix(dz, "dz", m, n, _BF16_ONLY)
+    xp, ldx, _ = _matrix(x, "x", m, k, _BF16_ONLY)
+    wp, lddw, code = _matrix(dw, "dw", n, k, _DT_CODE)
+    _same_type("acc", code, acc, "dw")
+    ap, ldacc, _ = _matrix(acc, "acc", n, k, _DT_CODE)
+    _check(load().zero_linear_grad_weight(m, n, k, zp, lddz, xp, ldx, ap, ldacc, wp, code, lddw,
+                                          _vector(db_acc, "db_acc", n, code),
+                                          _vector(db, "db", n, code), _stream_ptr(stream)),
+           "zero_linear_grad_weight")
+
+
+def zero_dropout(x, y, drop: ZeroDropout | None, residual=None, stream=None):
+    """y = residual + D(x), matrices of one type (bf16 or fp32)."""
+    rows, cols = _sizes(x, "x")
+    xp, ldx, code = _matrix(x, "x", rows, cols, _DT_CODE)
+    _same_type("y", code, y, "x")
+    _same_type("residual", code, residual, "x")
+    yp, ldy, _ = _matrix(y, "y", rows, cols, _DT_CODE)
+    rp, ldr, _ = _matrix(residual, "residual", rows, cols, _DT_CODE)
+    _check(load().zero_dropout(rows, cols, xp, ldx, code, drop, rp, ldr, yp, ldy, _stream_ptr(stream)),
+           "zero_dropout")
+
+
+def zero_dropout_grad(dy, dx, drop: ZeroDropout | None = None, act: int = ZERO_ACT_NONE, pre=None,
+                      db=None, db_acc=None, stream=None):
+    """dx = D'(dy) act'(pre) and db = db_acc + the column sums of dx: with a
+    linear's act, pre and drop, its dz and bias gradient.  dx may be dy itself."""
+    rows, cols = _sizes(dy, "dy")
+    dp, lddy, dcode = _matrix(dy, "dy", rows, cols, _DT_CODE)
+    xp, lddx, xcode = _matrix(dx, "dx", rows, cols, _DT_CODE)
+    pp, ldp, _ = _matrix(pre, "pre", rows, cols, _BF16_ONLY)
+    bcode = ZERO_BF16
+    if db is not None:
+        bcode = _DT_CODE.get(getattr(db, "dtype", None), -1)
+        if bcode < 0:
+            raise TypeError("db must be a bfloat16 or float32 tensor")
+    _check(load().zero_dropout_grad(rows, cols, dp, lddy, dcode, drop, act, pp, ldp, xp, xcode, lddx,
+                                    _vector(db_acc, "db_acc", cols, bcode),
+                                    _vector(db, "db", cols, bcode), bcode, _stream_ptr(stream)),
+           "zero_dropout_grad")
+
+
+def zero_rope_plan(rot: int, layout: int = ZERO_ROPE_HALF, base: float = 10000.0,
+                   scaling: int = ZERO_ROPE_NONE, factor: float = 1.0,
+                   context: float = 0.0) -> ZeroRopePlan:
+    """The plan zero_rope turns by: the first `rot` elements of a head, pairs by
+    `layout`, frequencies base^(-2i/rot) scaled for contexts `factor` times as long
+    (YARN also needs the first context's length)."""
+    plan = ZeroRopePlan()
+    _check(load().zero_rope_fill(int(rot), int(layout), float(base), int(scaling), float(factor),
+                                 float(context), ctypes.byref(plan)), "zero_rope_fill")
+    return plan
+
+
+def _heads(t, name, dtypes):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [tokens, heads, dim] tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device}); there is no CPU path")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
+    st, sh, inner = t.stride()
+    if t.shape[2] > 1 and inner != 1:
+        raise ValueError(f"{name} must have contiguous heads (strides {t.stride()})")
+    return t.data_ptr(), st, sh
+
+
+def zero_rope(plan: ZeroRopePlan, x, y, positions=None, pos0: int = 0, inverse: bool = False,
+              stream=None):
+    """Turns the pairs of x [tokens, heads, dim] into y (which may be x) by the
+    int64 positions, or pos0 + token; inverse turns back, which is the gradient."""
+    xp, xt, xh = _heads(x, "x", _DT_CODE)
+    yp, yt, yh = _heads(y, "y", _DT_CODE)
+    if x.shape != y.shape or x.dtype != y.dtype:
+        raise ValueError("x and y must have one shape and type")
+    tokens, heads, dim = x.shape
+    if positions is not None and positions.numel() != tokens:
+        raise ValueError(f"positions must have {tokens} elements, got {positions.numel()}")
+    _check(load().zero_rope(plan, tokens, heads, dim, xp, xt, xh, yp, yt, yh, _DT_CODE[x.dtype],
+                            None if positions is None else _tensor(positions, "positions", torch.int64, tokens),
+                            pos0, bool(inverse), _stream_ptr(stream)), "zero_rope")

@@ -1,0 +1,179 @@
+// What the dense operators of a unit share: the counter-based random bits of
+// dropout, the activations with their slopes, and the elementwise end of a
+// product (bias, activation, dropout, residual) on eight neighbouring columns.
+#pragma once
+
+#include "zero_common.cuh"
+
+namespace zgb {
+
+// ---- dropout ----------------------------------------------------------------
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
+// easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64 bit products on a
+// 128-bit counter under a 64-bit key.  One block of 128 bits serves the eight
+// elements of columns 8 c .. 8 c + 7 of one row, 16 bits each, low halves
+// first, so a 128-bit vector of bf16 needs one block and the bits of an element
+// depend on its row and column alone, not on strides, tiles or the launch.
+// 16 bits quantise p to a multiple of 2^-16; the factor on kept elements is
+// formed from the quantised p, so the expectation is exact.  32 bits an element
+// would double the integer work, which already stands beside the memory time.
+struct DropParams {
+    uint32_t cut;               // keep where bits >= cut; 0 = no dropout, 65536 = drop everything
+    float scale;                // 65536 / (65536 - cut), 0 where everything is dropped
+    uint32_t key0, key1, site, step;
+    const uint64_t* step_ptr;   // null, or added to step
+};
+
+__device__ __forceinline__ uint32_t drop_step(const DropParams& d) {
+    return d.step + (d.step_ptr ? (uint32_t)*d.step_ptr : 0u);
+}
+
+__device__ __forceinline__ uint4 philox_block(const DropParams& d, uint32_t step, uint32_t row, uint32_t col_block) {
+    uint32_t c0 = col_block, c1 = row, c2 = d.site, c3 = step;
+    uint32_t k0 = d.key0, k1 = d.key1;
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u;
+        const uint64_t p1 = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)p1;
+        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)p0;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
+// v[j] = kept ? v[j] * scale : 0 for the eight elements of (row, 8 col_block + j);
+// a dropped element is 0 whatever it held.
+__device__ __forceinline__ void drop8(const DropParams& d, uint32_t step, int64_t row, int64_t col_block, float* v) {
+    const uint4 b = philox_block(d, step, (uint32_t)row, (uint32_t)col_block);
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = (w[j] & 0xffffu) >= d.cut ? v[2 * j] * d.scale : 0.0f;
+        v[2 * j + 1] = (w[j] >> 16) >= d.cut ? v[2 * j + 1] * d.scale : 0.0f;
+    }
+}
+
+// Checks a caller's block and forms the kernels' parameters; null = no dropout.
+int drop_params(const zero_dropout_t* d, int64_t rows, int64_t cols, DropParams* out);
+
+// db[c] = db_acc[c] + the sum over rows of dz[r, c] (zero_dropout.cu).
+int launch_column_sum(int64_t rows, int64_t cols, const uint16_t* dz, int64_t lddz, const void* db_acc, void* db,
+                      bool db_f32, cudaStream_t s);
+
+// ---- activations ------------------------------------------------------------
+// Evaluated in fp32.  The tanh form of the GELU is x sigmoid(2u), which like the
+// SiLU needs one exponential and one division; the fast forms of both (relative
+// error about 2^-21) are far inside the rounding of a bf16 result and of an fp32
+// one's tolerance.
+__device__ __forceinline__ float sigmoid_f(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
+constexpr float kGeluC = 0.79788456080286535588f;   // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+__device__ __forceinline__ float act_apply(int act, float z) {
+    switch (act) {
+        case ZERO_ACT_RELU: return z < 0.0f ? 0.0f : z;   // a NaN stays
+        case ZERO_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
+        case ZERO_ACT_GELU_TANH: return __fdividef(z, 1.0f + __expf(-2.0f * kGeluC * (z + kGeluA * z * z * z)));
+        case ZERO_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+        default: return z;
+    }
+}
+
+// Past the clamps the second term of a slope is below fp32's resolution; without
+// them it would be 0 * infinity.  A NaN passes both comparisons and stays.
+__device__ __forceinline__ float clamp_keep_nan(float z, float c) { return z > c ? c : z < -c ? -c : z; }
+
+__device__ __forceinline__ float act_slope(int act, float z) {
+    switch (act) {
+        case ZERO_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+        case ZERO_ACT_GELU: {
+            z = clamp_keep_nan(z, 20.0f);
+            return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) +
+                   z * 0.39894228040143267794f * __expf(-0.5f * z * z);
+        }
+        case ZERO_ACT_GELU_TANH: {
+            z = clamp_keep_nan(z, 20.0f);
+            const float s = sigmoid_f(2.0f * kGeluC * (z + kGeluA * z * z * z));
+            return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+        }
+        case ZERO_ACT_SILU: {
+            z = clamp_keep_nan(z, 104.0f);   // past 89 the exponential is already infinite
+            const float s = sigmoid_f(z);
+            return s * (1.0f + z * (1.0f - s));
+        }
+        default: return 1.0f;
+    }
+}
+
+// ---- eight neighbouring columns ---------------------------------------------
+__device__ __forceinline__ void unpack8(uint4 u, float* v) {
+    v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x);
+    v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+    v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z);
+    v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+}
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
+
+// p points at the first of the eight; `vec`: p is 16-byte aligned and count == 8.
+__device__ __forceinline__ void load8(const void* p, bool f32, bool vec, int count, float* v) {
+    if (vec) {
+        if (f32) {
+            const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            unpack8(*reinterpret_cast<const uint4*>(p), v);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = j >= count ? 0.0f : f32 ? static_cast<const float*>(p)[j] : bf16_one(static_cast<const uint16_t*>(p)[j]);
+    }
+}
+__device__ __forceinline__ void store8(void* p, bool f32, bool vec, int count, const float* v) {
+    if (vec) {
+        if (f32) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(p) = pack8(v);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < count) {
+                if (f32)
+                    static_cast<float*>(p)[j] = v[j];
+                else
+                    static_cast<uint16_t*>(p)[j] = to_bf16(v[j]);
+            }
+    }
+}
+
+// Whether rows of `ld` elements of `size` bytes from p keep eight-column groups
+// on 16-byte boundaries.
+inline bool rows_aligned16(const void* p, int64_t ld, int size) {
+    return aligned16(p) && (ld * size) % 16 == 0;
+}
+
+inline int dtype_size(int32_t dtype) { return dtype == ZERO_F32 ? 4 : 2; }
+
+// 0, or why a matrix argument is refused: rows of at least `cols` elements, an
+// element-aligned pointer (any, where there is no element), and rows * ld * size
+// within 63 bits.
+inline int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+    if (ld < cols) return ZERO_EINVAL;
+    if (rows == 0 || cols == 0) return ZERO_OK;
+    if (!p) return ZERO_EINVAL;
+    if (ld > 0 && rows > INT64_MAX / 8 / ld) return ZERO_ERANGE;
+    return check_aligned(p, dtype_size(dtype));
+}
+
+}  // namespace zgb
