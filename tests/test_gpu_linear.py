@@ -156,6 +156,21 @@ def test_grad_input_ends(zlib, cuda_device, act, dtype):
         _check_grad_input(zlib, 133, 96, 200, dtype=dtype, act=act, p=p, residual=residual, seed=act)
 
 
+# enough tiles of 256 x 256 for the kernel of large products; widths that leave a
+# narrow last tile, an unused half tile, rows past one half of a tile
+BIG = [(2000, 2100, 96), (257, 10008, 72), (2305, 1600, 200), (2560, 1032, 1600), (300, 5000, 1000)]
+
+
+@pytest.mark.parametrize("size", BIG)
+@pytest.mark.parametrize("places", [((0, 0), (0, 0)), ((8, 16), (3, 1)), ((16, 8), (8, 8))])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_large_products(zlib, cuda_device, size, places, dtype):
+    _check_linear(zlib, *size, *places, dtype=dtype, act=dp.GELU_TANH, p=0.1)
+    m, n, k = size
+    _check_grad_input(zlib, m, k, n, *places, dtype=dtype, act=dp.GELU, p=0.1)
+    _check_grad_weight(zlib, k, m, n, *places, dtype=dtype)
+
+
 def _check_grad_weight(zlib, m, n, k, pin=(0, 0), pout=(0, 0), dtype=BF, acc=True, db=True, db_acc=True, seed=0):
     g = torch.Generator().manual_seed(seed * 1000 + m + 3 * n + 7 * k + 2)
     dz, x = _mat(g, m, n), _mat(g, m, k, 1 / math.sqrt(m))

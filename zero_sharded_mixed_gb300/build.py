@@ -27,7 +27,8 @@ CUDA_SOURCES = ["zero_runtime.cu", "zero_rs_adamw.cu", "zero_accumulate.cu", "ze
                 "zero_schedule.cu", "zero_cast.cu", "zero_linear.cu", "zero_dropout.cu",
                 "zero_rope.cu"]
 HOST_SOURCES = ["zero_host.cpp", "zero_ckpt.cpp"]
-HEADERS = ["zero_common.cuh", "zero_update.cuh", "zero_quant.cuh", "zero_tma.cuh", "zero_dense.cuh"]
+HEADERS = ["zero_common.cuh", "zero_update.cuh", "zero_quant.cuh", "zero_tma.cuh", "zero_dense.cuh",
+           "zero_tensor.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # Host code: no FMA contraction either (the bias corrections are formed on the host).

@@ -2,16 +2,44 @@
 //   zero_linear              y  = residual + D(act(x w^T + bias))
 //   zero_linear_grad_input   dx = residual + D'(dz w) act'(pre)
 //   zero_linear_grad_weight  dw = acc + dz^T x,  db = db_acc + sum over rows of dz
+#include <mutex>
+
 #include "zero_dense.cuh"
+#include "zero_tensor.cuh"
 
 namespace zgb {
 
-// C[rows, cols] = sum over `depth` of A B with a strided element A(i, t) at
-// a[i * a_row + t * a_depth], B(j, t) at b[j * b_row + t * b_depth], and the end.
+__device__ int g_linear_status;   // ZERO_OK, or ZERO_ETIMEOUT once a bounded wait gave up
+
+int take_linear_status() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_linear_status, sizeof v) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ZERO_ECUDA;
+    }
+    if (v != ZERO_OK) {
+        const int zero = ZERO_OK;
+        if (cudaMemcpyToSymbol(g_linear_status, &zero, sizeof zero) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return ZERO_ECUDA;
+        }
+    }
+    return v == ZERO_OK ? ZERO_OK : ZERO_ETIMEOUT;
+}
+
+// ---- operands ------------------------------------------------------------------
+
+// A matrix as it is stored, row-major.  The product C[i, j] = sum over t of
+// A(i, t) B(j, t) reads an operand with its reduced dimension t along the columns
+// (K-major) or along the rows (MN-major).
+struct Operand {
+    const uint16_t* p;
+    int64_t ld, rows, cols;
+    bool mn;
+};
 struct Product {
     int64_t rows, cols, depth;
-    const uint16_t* a; int64_t a_row, a_depth;
-    const uint16_t* b; int64_t b_row, b_depth;
+    Operand a, b;
 };
 struct Ending {
     const uint16_t* bias;                       // per column, or null
@@ -21,69 +49,720 @@ struct Ending {
     void* out; int64_t ld_out;
     int32_t act;
     bool out_f32;
+    bool vec;                                   // every matrix above keeps 8-column groups on 16-byte boundaries
     DropParams drop;
 };
 
-constexpr int kTile = 64, kDepth = 16;
+// ---- the end of a product --------------------------------------------------------
+// Accumulators reach the end in units of 8 rows x 32 columns of fp32 in shared
+// memory (a part of a 32 x 32 chunk), one warp a unit.  Row r of a chunk is 128
+// bytes; its 16-byte group g stands at group_place(r, g), so that neither the rows
+// written by 32 lanes nor the pairs of groups read by 4 x 8 lanes share a bank.
+__device__ __forceinline__ uint32_t group_place(int r, int g) {
+    const int s = ((r & 1) << 2) | ((r >> 1) & 3);
+    return (uint32_t)r * 128u + (uint32_t)((((g >> 1) | ((g & 1) << 2)) ^ s) << 4);
+}
 
-__device__ __forceinline__ void end8(const Ending& e, uint32_t step, int64_t row, int64_t col, int count, float* v) {
-    const bool f32 = e.out_f32;
-    const int size = f32 ? 4 : 2;
-    float t[8];
-    if (e.bias) {
-        load8(e.bias + col, false, false, count, t);
-        for (int j = 0; j < 8; ++j) v[j] += t[j];
+template <bool kF32>
+struct Sides {   // what an aligned unit reads beside its accumulators, as loaded
+    uint4 add[kF32 ? 2 : 1];
+    uint4 slope;
+};
+
+template <bool kF32>
+__device__ __forceinline__ void load_sides(const Ending& e, int64_t row, int64_t col, Sides<kF32>* s) {
+    if (e.add) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(e.add) + (row * e.ld_add + col) * (kF32 ? 4 : 2));
+        s->add[0] = q[0];
+        if constexpr (kF32) s->add[1] = q[1];
     }
-    if (e.pre) store8(e.pre + row * e.ld_pre + col, false, false, count, v);
+    if (e.slope) s->slope = *reinterpret_cast<const uint4*>(e.slope + row * e.ld_slope + col);
+}
+
+// Eight whole, aligned columns.
+template <bool kF32>
+__device__ __forceinline__ void end_vector(const Ending& e, uint32_t step, int64_t row, int64_t col, const float* bias,
+                                           const Sides<kF32>& s, float* v) {
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += bias[j];
+    if (e.pre) *reinterpret_cast<uint4*>(e.pre + row * e.ld_pre + col) = pack8(v);
     if (e.slope) {
-        load8(e.slope + row * e.ld_slope + col, false, false, count, t);
+        unpack8(s.slope, t);
+#pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= act_slope(e.act, t[j]);
     } else if (e.act) {
+#pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = act_apply(e.act, v[j]);
     }
     if (e.drop.cut) drop8(e.drop, step, row, col >> 3, v);
     if (e.add) {
-        load8(static_cast<const char*>(e.add) + (row * e.ld_add + col) * size, f32, false, count, t);
+        if constexpr (kF32) {
+            const uint32_t u[8] = {s.add[0].x, s.add[0].y, s.add[0].z, s.add[0].w,
+                                   s.add[1].x, s.add[1].y, s.add[1].z, s.add[1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = __uint_as_float(u[j]);
+        } else {
+            unpack8(s.add[0], t);
+        }
+#pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += t[j];
     }
-    store8(static_cast<char*>(e.out) + (row * e.ld_out + col) * size, f32, false, count, v);
+    store8(static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2), kF32, true, 8, v);
 }
 
-// The plain kernel: a 64 x 64 tile a CTA, 2 x 8 results a thread, fp32 products.
-__global__ void __launch_bounds__(kThreads) product_kernel(const Product p, const Ending e) {
-    __shared__ float as[kDepth][kTile + 1], bs[kDepth][kTile + 1];
-    const int64_t row0 = (int64_t)blockIdx.y * kTile, col0 = (int64_t)blockIdx.x * kTile;
-    const int tr = threadIdx.x / 8 * 2, tc = threadIdx.x % 8 * 8;
-    float acc[2][8] = {};
-    for (int64_t t0 = 0; t0 < p.depth; t0 += kDepth) {
-        for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-            // neighbouring threads along whichever of the two is contiguous
-            const int r = p.a_depth == 1 ? i / kDepth : i % kTile, t = p.a_depth == 1 ? i % kDepth : i / kTile;
-            as[t][r] = row0 + r < p.rows && t0 + t < p.depth
-                           ? bf16_one(p.a[(row0 + r) * p.a_row + (t0 + t) * p.a_depth]) : 0.0f;
-            const int c = p.b_depth == 1 ? i / kDepth : i % kTile, u = p.b_depth == 1 ? i % kDepth : i / kTile;
-            bs[u][c] = col0 + c < p.cols && t0 + u < p.depth
-                           ? bf16_one(p.b[(col0 + c) * p.b_row + (t0 + u) * p.b_depth]) : 0.0f;
-        }
-        __syncthreads();
-        for (int t = 0; t < kDepth; ++t)
-            for (int i = 0; i < 2; ++i)
-                for (int j = 0; j < 8; ++j) acc[i][j] += as[t][tr + i] * bs[t][tc + j];
-        __syncthreads();
+// One element.
+template <bool kF32>
+__device__ __forceinline__ void end_element(const Ending& e, int64_t row, int64_t col, float bias, uint32_t bits, float v) {
+    v += bias;
+    if (e.pre) e.pre[row * e.ld_pre + col] = to_bf16(v);
+    if (e.slope)
+        v *= act_slope(e.act, bf16_one(e.slope[row * e.ld_slope + col]));
+    else if (e.act)
+        v = act_apply(e.act, v);
+    if (e.drop.cut) v = bits >= e.drop.cut ? v * e.drop.scale : 0.0f;
+    if constexpr (kF32) {
+        if (e.add) v += static_cast<const float*>(e.add)[row * e.ld_add + col];
+        static_cast<float*>(e.out)[row * e.ld_out + col] = v;
+    } else {
+        if (e.add) v += bf16_one(static_cast<const uint16_t*>(e.add)[row * e.ld_add + col]);
+        static_cast<uint16_t*>(e.out)[row * e.ld_out + col] = to_bf16(v);
     }
-    const uint32_t step = e.drop.cut ? drop_step(e.drop) : 0u;
-    const int64_t col = col0 + tc;
-    if (col >= p.cols) return;
-    const int count = p.cols - col < 8 ? (int)(p.cols - col) : 8;
-    for (int i = 0; i < 2; ++i)
-        if (row0 + tr + i < p.rows) end8(e, step, row0 + tr + i, col, count, acc[i]);
 }
 
-static int launch_product(const Product& p, const Ending& e, cudaStream_t s) {
-    const int64_t gx = (p.cols + kTile - 1) / kTile, gy = (p.rows + kTile - 1) / kTile;
-    if (gx > INT32_MAX || gy > 65535) return ZERO_ERANGE;
-    product_kernel<<<dim3((unsigned)gx, (unsigned)gy), kThreads, 0, s>>>(p, e);
-    return launch_status();
+// A unit whose rows are not aligned, or whose columns end inside a group: a lane a
+// column, row by row, so that a row's accesses still fall together.  get(r) gives
+// this lane's accumulator of row r; every lane of the warp calls.
+template <bool kF32, class Get>
+__device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                         Get get) {
+    const int lane = threadIdx.x & 31;
+    const int64_t col = col0 + lane;
+    const float bias = e.bias && col < cols ? bf16_one(e.bias[col]) : 0.0f;
+    uint4 block = make_uint4(0u, 0u, 0u, 0u);   // lane l forms the bits of row l % 8 and column group l / 8
+    if (e.drop.cut) block = philox_block(e.drop, step, (uint32_t)(row0 + (lane & 7)), (uint32_t)((col0 >> 3) + (lane >> 3)));
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        uint32_t bits = 0;
+        if (e.drop.cut) {
+            const int from = (lane & 24) | r;
+            const uint32_t w0 = __shfl_sync(0xffffffffu, block.x, from), w1 = __shfl_sync(0xffffffffu, block.y, from);
+            const uint32_t w2 = __shfl_sync(0xffffffffu, block.z, from), w3 = __shfl_sync(0xffffffffu, block.w, from);
+            const uint32_t w = lane & 4 ? (lane & 2 ? w3 : w2) : (lane & 2 ? w1 : w0);
+            bits = lane & 1 ? w >> 16 : w & 0xffffu;
+        }
+        const float v = get(r);
+        if (row0 + r < rows && col < cols) end_element<kF32>(e, row0 + r, col, bias, bits, v);
+    }
+}
+
+__device__ __forceinline__ void load_bias8(const Ending& e, int64_t col, float* b) {
+    if (e.bias) {
+        unpack8(*reinterpret_cast<const uint4*>(e.bias + col), b);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = 0.0f;
+    }
+}
+
+// ---- waits -------------------------------------------------------------------------
+constexpr long long kWaitCycles = 1ll << 31;   // SM cycles (about a second) before a wait gives up
+
+__device__ __forceinline__ bool wait_or_report(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_wait_bounded(bar, parity, kWaitCycles)) return true;
+    atomicExch(&g_linear_status, ZERO_ETIMEOUT);
+    return false;
+}
+
+// ---- the pair kernel -----------------------------------------------------------------
+// Large aligned products: pairs of CTAs, each pair one 256 x bn tile at a time (its
+// rows split between the two tensor memories, its B tile between the two shared
+// memories), tiles taken in turn from a grouped order.  Warp 0 copies, warp 1 of the
+// even CTA issues the products, warps 4..11 end the previous tile out of the other
+// half of the tensor memory meanwhile.
+struct PairParams {
+    CUtensorMap map_a, map_b;
+    int64_t rows, cols, depth;
+    int32_t tiles_m, tiles_n, bn, k_blocks;
+    bool a_mn, b_mn;
+    Ending e;
+};
+
+constexpr int kStageBytes = 32768;      // 128 rows of A and 128 of B, 64 reduced elements each
+constexpr int kPairStages = 6;
+constexpr int kPairThreads = 384;
+constexpr int kEndWarps = 8;
+constexpr int kChunkBytes = 4096;       // 32 x 32 fp32
+constexpr int kPairSmem = 1024 + kPairStages * kStageBytes + kEndWarps * kChunkBytes + 256;
+constexpr int kRasterRows = 8;          // row tiles that are gone through together
+
+__device__ __forceinline__ void tile_place(const PairParams& p, int t, int* tm, int* tn) {
+    const int per_group = kRasterRows * p.tiles_n;
+    const int g = t / per_group, in = t - g * per_group, first = g * kRasterRows;
+    const int size = p.tiles_m - first < kRasterRows ? p.tiles_m - first : kRasterRows;
+    *tn = in / size;
+    *tm = first + in - *tn * size;
+}
+__device__ __forceinline__ int tile_width(const PairParams& p, int tn) {   // columns of the tile, up to a multiple of 32
+    const int64_t left = p.cols - (int64_t)tn * p.bn;
+    return left >= p.bn ? p.bn : (int)((left + 31) / 32 * 32);
+}
+
+template <bool kF32>
+__global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ PairParams p) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+    uint8_t* chunks = smem + kPairStages * kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kEndWarps * kChunkBytes);
+    uint64_t* empty = full + kPairStages;
+    uint64_t* acc_full = empty + kPairStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drained = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int tiles = p.tiles_m * p.tiles_n;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 2 * kEndWarps);
+        }
+        mbar_init(drained, 1);
+        fence_barrier_init();
+        tensor_map_prefetch(&p.map_a);
+        tensor_map_prefetch(&p.map_b);
+    }
+    if (warp == 2) tmem_alloc<true>(tmem_slot, 512);
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tcgen05_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int half = p.bn / 2;
+    const int b_boxes = p.b_mn ? (half + 63) / 64 : 1;
+    const uint32_t stage_bytes = 16384u + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)half * 128u);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t round = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                int tm, tn;
+                tile_place(p, t, &tm, &tn);
+                const int row = tm * 256 + (int)rank * 128;
+                const int col = tn * p.bn + (int)rank * (tile_width(p, tn) / 2);
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (round > 0 && !(ok = wait_or_report(empty + s, (round - 1) & 1))) break;
+                    const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384;
+                    const uint32_t bar = peer_addr(smem_addr(full + s), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * stage_bytes);
+                    const int k = kb * 64;
+                    if (p.a_mn) {
+                        tensor_load_pair(a, &p.map_a, row, k, bar);
+                        tensor_load_pair(a + kSubTileBytes, &p.map_a, row + 64, k, bar);
+                    } else {
+                        tensor_load_pair(a, &p.map_a, k, row, bar);
+                    }
+                    if (p.b_mn) {
+                        for (int i = 0; i < b_boxes; ++i) tensor_load_pair(b + i * kSubTileBytes, &p.map_b, col + 64 * i, k, bar);
+                    } else {
+                        tensor_load_pair(b, &p.map_b, k, col, bar);
+                    }
+                    if (++s == kPairStages) s = 0, ++round;
+                }
+            }
+            if (!ok && rank == 0)   // copies in flight land before the CTAs end
+                for (int i = 0; i < kPairStages; ++i) {
+                    const uint32_t done = i < s ? round : round - 1;   // the last round issued on stage i
+                    if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int s = 0, n_tile = 0;
+            uint32_t round = 0;
+            bool ok = true;
+            const uint32_t a_step = descriptor_step(p.a_mn), b_step = descriptor_step(p.b_mn);
+            for (int t = pair; ok && t < tiles; t += pairs, ++n_tile) {
+                int tm, tn;
+                tile_place(p, t, &tm, &tn);
+                const uint32_t idesc = instruction_descriptor(256, tile_width(p, tn), p.a_mn, p.b_mn);
+                const int buf = n_tile & 1;
+                if (n_tile >= 2 && !(ok = wait_or_report(acc_empty + buf, (n_tile / 2 - 1) & 1))) break;
+                tcgen05_fence_after();
+                const uint32_t d = tmem + buf * 256;
+                for (int kb = 0; kb < p.k_blocks; ++kb) {
+                    if (!(ok = wait_or_report(full + s, round & 1))) break;
+                    tcgen05_fence_after();
+                    const uint32_t a = smem_addr(smem + s * kStageBytes);
+                    uint64_t da = smem_descriptor(a, p.a_mn), db = smem_descriptor(a + 16384, p.b_mn);
+                    const int64_t left = p.depth - (int64_t)kb * 64;
+                    const int steps = left >= 64 ? 4 : (int)((left + 15) / 16);
+                    for (int i = 0; i < steps; ++i, da += a_step, db += b_step) mma_bf16<true>(d, da, db, idesc, kb + i > 0);
+                    mma_commit<true>(empty + s);
+                    if (++s == kPairStages) s = 0, ++round;
+                }
+                if (ok) mma_commit<true>(acc_full + buf);
+            }
+            if (!ok) {   // products in flight end before the tensor memory is freed
+                mma_commit<true>(drained);
+                (void)mbar_wait_bounded(drained, 0, kWaitCycles / 8);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int w = warp - 4, q = warp & 3, h = w / 4;
+        uint8_t* chunk = chunks + w * kChunkBytes;
+        const uint32_t chunk_addr = smem_addr(chunk);
+        (void)chunk_addr;
+        const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
+        int n_tile = 0;
+        for (int t = pair; t < tiles; t += pairs, ++n_tile) {
+            int tm, tn;
+            tile_place(p, t, &tm, &tn);
+            const int buf = n_tile & 1, width = tile_width(p, tn);
+            const bool ok = wait_or_report(acc_full + buf, (n_tile / 2) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tcgen05_fence_after();
+            const int64_t row0 = (int64_t)tm * 256 + rank * 128 + q * 32, col_tile = (int64_t)tn * p.bn;
+            const int n_chunks = width / 32;
+            for (int c = h; c < n_chunks; c += 2) {
+                const int64_t col0 = col_tile + c * 32;
+                const bool vec = p.e.vec && col0 + 32 <= p.cols;
+                const int64_t col = col0 + (lane & 3) * 8;
+                Sides<kF32> sides[4];
+                float bias[8];
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t row = row0 + i * 8 + (lane >> 2);
+                        if (row < p.rows) load_sides<kF32>(p.e, row, col, &sides[i]);
+                    }
+                    load_bias8(p.e, col, bias);
+                }
+                uint32_t acc[32];
+                tmem_load32(tmem + buf * 256 + c * 32 + ((uint32_t)(q * 32) << 16), acc);
+                if (c + 2 >= n_chunks) {   // this warp's last read of the buffer
+                    tcgen05_fence_before();
+                    __syncwarp();
+                    if (lane == 0) peer_arrive(peer_addr(smem_addr(acc_empty + buf), 0));
+                }
+                __syncwarp();   // the chunk's previous readers are done
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                    *reinterpret_cast<uint4*>(chunk + group_place(lane, g)) = make_uint4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
+                __syncwarp();
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + (lane >> 2);
+                        if (row0 + r < p.rows) {
+                            const float4 a = *reinterpret_cast<const float4*>(chunk + group_place(r, 2 * (lane & 3)));
+                            const float4 b = *reinterpret_cast<const float4*>(chunk + group_place(r, 2 * (lane & 3) + 1));
+                            float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                            end_vector<kF32>(p.e, step, row0 + r, col, bias, sides[i], v);
+                        }
+                    }
+                } else {
+                    for (int i = 0; i < 4; ++i)
+                        end_rows<kF32>(p.e, step, row0 + i * 8, col0, p.rows, p.cols, [&](int r) {
+                            return *reinterpret_cast<const float*>(chunk + group_place(i * 8 + r, lane >> 2) + (lane & 3) * 4);
+                        });
+                }
+            }
+            // a warp without a chunk of this tile (a narrow last tile) still frees the buffer
+            if (h >= n_chunks) {
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) peer_arrive(peer_addr(smem_addr(acc_empty + buf), 0));
+            }
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tcgen05_fence_after();
+    if (warp == 2) tmem_free<true>(tmem, 512);
+}
+
+// ---- the split kernel ------------------------------------------------------------------
+// Smaller products, and those whose operands are not aligned: a 128 x bn tile a
+// cluster, its reduced dimension split over the cluster's CTAs.  Each CTA leaves its
+// part in its shared memory; the parts are added in the order of the CTAs (so the
+// result repeats) while the end is applied.
+// kSoft: warps 0..7 bring the tiles by plain loads, realigned in registers, in place
+// of tensor-map copies, which start on 16-byte boundaries only.
+struct SplitParams {
+    CUtensorMap map_a, map_b;
+    Operand a, b;
+    int64_t rows, cols, depth;
+    int32_t tiles_m, tiles_n, bn, k_blocks;
+    Ending e;
+};
+
+constexpr int kSplitStages = 3;
+constexpr int kSplitThreads = 288;
+constexpr int kSplitSmem = 1024 + kSplitStages * kStageBytes + 128;
+
+// Eight elements (r, c) .. (r, c + 7) of an operand, zeros outside it, from any
+// element-aligned place: the two 16-byte blocks that hold them, shifted together.
+// Blocks are read only where they lie wholly inside the operand's own memory.
+__device__ __forceinline__ uint4 fetch8(const Operand& o, int64_t r, int64_t c) {
+    uint4 out = make_uint4(0u, 0u, 0u, 0u);
+    if (r >= o.rows || c >= o.cols) return out;
+    const uint16_t* q = o.p + r * o.ld + c;
+    const int64_t left = o.cols - c;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(q), lo = at & ~(uintptr_t)15;
+    const uint32_t shift = (uint32_t)(at & 15);
+    const uintptr_t first = reinterpret_cast<uintptr_t>(o.p), last = reinterpret_cast<uintptr_t>(o.p + (o.rows - 1) * o.ld + o.cols);
+    if (shift == 0 && left >= 8) return *reinterpret_cast<const uint4*>(q);
+    if (left >= 8 && lo >= first && lo + 32 <= last) {
+        const uint4 x = *reinterpret_cast<const uint4*>(lo), y = *reinterpret_cast<const uint4*>(lo + 16);
+        uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        if (shift & 8) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (shift & 4) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        const uint32_t bits = (shift & 2) * 8;
+        out.x = __funnelshift_r(w[0], w[1], bits);
+        out.y = __funnelshift_r(w[1], w[2], bits);
+        out.z = __funnelshift_r(w[2], w[3], bits);
+        out.w = __funnelshift_r(w[3], w[4], bits);
+        return out;
+    }
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < left) w[j / 2] |= (uint32_t)q[j] << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 256 threads bring `rows` (at most 128) sub-tile rows of an operand's tile.
+__device__ __forceinline__ void fetch_tile(const Operand& o, int64_t mn0, int64_t k0, int rows, uint8_t* dst) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int chunk = i * 256 + threadIdx.x, r = chunk >> 3, g = chunk & 7;
+        if (r < rows)
+            v[i] = o.mn ? fetch8(o, k0 + (r & 63), mn0 + (r & ~63) + g * 8) : fetch8(o, mn0 + r, k0 + g * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int chunk = i * 256 + threadIdx.x, r = chunk >> 3, g = chunk & 7;
+        if (r < rows) *reinterpret_cast<uint4*>(dst + r * 128 + ((g ^ (r & 7)) << 4)) = v[i];
+    }
+}
+
+template <bool kF32, bool kSoft>
+__global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_constant__ SplitParams p) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSplitStages * kStageBytes);
+    uint64_t* empty = full + kSplitStages;
+    uint64_t* acc_full = empty + kSplitStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int parts = (int)cluster_size(), rank = (int)cluster_rank();
+    const int tile = blockIdx.x / parts;
+    const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
+    const int64_t row_tile = (int64_t)tm * 128, col_tile = (int64_t)tn * p.bn;
+    const int kb0 = (int)((int64_t)p.k_blocks * rank / parts), kb1 = (int)((int64_t)p.k_blocks * (rank + 1) / parts);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSplitStages; ++s) {
+            mbar_init(full + s, kSoft ? 256 : 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(acc_full, 1);
+        fence_barrier_init();
+        if (!kSoft) {
+            tensor_map_prefetch(&p.map_a);
+            tensor_map_prefetch(&p.map_b);
+        }
+    }
+    if (warp == 8) tmem_alloc<false>(tmem_slot, 128);
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // sub-tile rows of a stage: tile rows (K-major), or 64 for every 64 columns
+    const int a_left = p.rows - row_tile < 128 ? (int)(p.rows - row_tile) : 128;
+    const int a_rows = p.a.mn ? (a_left + 63) / 64 * 64 : kSoft ? a_left : 128;
+    const int b_rows = p.b.mn ? (p.bn + 63) / 64 * 64 : p.bn;
+    bool ok = true;
+
+    if (warp < 8) {
+        if (kSoft) {
+            int s = 0;
+            uint32_t round = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (round > 0 && !(ok = wait_or_report(empty + s, (round - 1) & 1))) break;
+                uint8_t* a = smem + s * kStageBytes;
+                fetch_tile(p.a, row_tile, (int64_t)kb * 64, a_rows, a);
+                fetch_tile(p.b, col_tile, (int64_t)kb * 64, b_rows, a + 16384);
+                fence_async_shared();
+                mbar_arrive(full + s);
+                if (++s == kSplitStages) s = 0, ++round;
+            }
+        } else if (threadIdx.x == 0) {
+            int s = 0;
+            uint32_t round = 0;
+            const int a_boxes = p.a.mn ? a_rows / 64 : 1, b_boxes = p.b.mn ? b_rows / 64 : 1;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (round > 0 && !(ok = wait_or_report(empty + s, (round - 1) & 1))) break;
+                const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384, bar = smem_addr(full + s);
+                mbar_arrive_expect_tx(full + s, (uint32_t)(a_rows + b_rows) * 128u);
+                const int k = kb * 64;
+                if (p.a.mn) {
+                    for (int i = 0; i < a_boxes; ++i) tensor_load(a + i * kSubTileBytes, &p.map_a, (int)row_tile + 64 * i, k, bar);
+                } else {
+                    tensor_load(a, &p.map_a, k, (int)row_tile, bar);
+                }
+                if (p.b.mn) {
+                    for (int i = 0; i < b_boxes; ++i) tensor_load(b + i * kSubTileBytes, &p.map_b, (int)col_tile + 64 * i, k, bar);
+                } else {
+                    tensor_load(b, &p.map_b, k, (int)col_tile, bar);
+                }
+                if (++s == kSplitStages) s = 0, ++round;
+            }
+            if (!ok)   // copies in flight land before the CTA ends
+                for (int i = 0; i < kSplitStages; ++i) {
+                    const uint32_t done = i < s ? round : round - 1;
+                    if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
+                }
+        }
+        __syncwarp();
+    } else if (lane == 0) {
+        int s = 0;
+        uint32_t round = 0;
+        const uint32_t idesc = instruction_descriptor(128, p.bn, p.a.mn, p.b.mn);
+        const uint32_t a_step = descriptor_step(p.a.mn), b_step = descriptor_step(p.b.mn);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!(ok = wait_or_report(full + s, round & 1))) break;
+            tcgen05_fence_after();
+            const uint32_t a = smem_addr(smem + s * kStageBytes);
+            uint64_t da = smem_descriptor(a, p.a.mn), db = smem_descriptor(a + 16384, p.b.mn);
+            const int64_t left = p.depth - (int64_t)kb * 64;
+            const int steps = left >= 64 ? 4 : (int)((left + 15) / 16);
+            for (int i = 0; i < steps; ++i, da += a_step, db += b_step) mma_bf16<false>(tmem, da, db, idesc, kb > kb0 || i > 0);
+            mma_commit<false>(empty + s);
+            if (++s == kSplitStages) s = 0, ++round;
+        }
+        mma_commit<false>(acc_full);   // after a failed wait too: the tensor memory is free once it arrives
+    }
+    __syncwarp();
+    ok = wait_or_report(acc_full, 0) && ok;
+    tcgen05_fence_after();
+
+    // this CTA's part to its shared memory, chunk (q, c) of the tile at 4 KB each
+    const int64_t cols_left = p.cols - col_tile;
+    const int n_chunks = cols_left >= p.bn ? p.bn / 32 : (int)((cols_left + 31) / 32);
+    if (warp < 8) {
+        const int q = warp & 3;
+        if (q * 32 < a_left) {
+            for (int c = warp / 4; c < n_chunks; c += 2) {
+                uint32_t acc[32];
+                tmem_load32(tmem + c * 32 + ((uint32_t)(q * 32) << 16), acc);
+                uint8_t* chunk = smem + (q * 4 + c) * kChunkBytes;
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                    *reinterpret_cast<uint4*>(chunk + group_place(lane, g)) =
+                        p.k_blocks ? make_uint4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    if (parts > 1) cluster_sync();
+    tcgen05_fence_after();
+    if (warp == 8) tmem_free<false>(tmem, 128);
+
+    if (warp < 8 && ok) {
+        const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
+        const uint32_t base = smem_addr(smem);
+        const int units = (a_left + 7) / 8 * n_chunks;
+        for (int u = rank * 8 + warp; u < units; u += parts * 8) {
+            const int rb = u / n_chunks, c = u - rb * n_chunks;   // rows 8 rb .., chunk column c
+            const uint32_t chunk = base + ((rb / 4) * 4 + c) * kChunkBytes;
+            const int r0 = (rb & 3) * 8;
+            const int64_t row0 = row_tile + rb * 8, col0 = col_tile + c * 32;
+            if (p.e.vec && col0 + 32 <= p.cols) {
+                const int r = r0 + (lane >> 2);
+                const int64_t row = row_tile + (rb / 4) * 32 + r, col = col0 + (lane & 3) * 8;
+                if (row < p.rows) {
+                    Sides<kF32> sides;
+                    float bias[8];
+                    load_sides<kF32>(p.e, row, col, &sides);
+                    load_bias8(p.e, col, bias);
+                    float v[8] = {};
+                    const uint32_t g0 = group_place(r, 2 * (lane & 3)), g1 = group_place(r, 2 * (lane & 3) + 1);
+                    for (int i = 0; i < parts; ++i) {
+                        const uint32_t at = peer_addr(chunk, i);
+                        const float4 x = peer_load(at + g0), y = peer_load(at + g1);
+                        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+                    }
+                    end_vector<kF32>(p.e, step, row, col, bias, sides, v);
+                }
+            } else {
+                end_rows<kF32>(p.e, step, row0, col0, p.rows, p.cols, [&](int r) {
+                    float v = 0.0f;
+                    for (int i = 0; i < parts; ++i)
+                        v += peer_load1(peer_addr(chunk, i) + group_place(r0 + r, lane >> 2) + (lane & 3) * 4);
+                    return v;
+                });
+            }
+        }
+    }
+    __syncwarp();
+    if (parts > 1) cluster_sync();   // the parts are read before their CTAs end
+}
+
+// ---- launches -----------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiled encode_tiled() {
+    static EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Whether tensor-map copies can read the operand: 16-byte aligned rows, and sizes
+// and row pitch within the map's fields.
+static bool copies_reach(const Operand& o) {
+    return o.rows > 0 && o.cols > 0 && aligned16(o.p) && (o.rows == 1 || o.ld % 8 == 0) && o.rows < (1ll << 31) - 512 &&
+           o.cols < (1ll << 31) - 512 && o.ld < (1ll << 38);
+}
+static bool make_map(const Operand& o, int box_rows, CUtensorMap* map) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows};
+    const cuuint64_t pitch[1] = {(cuuint64_t)((o.ld + 7) / 8 * 16)};   // of a single row any
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, unit[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(o.p), dims, pitch, box, unit,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Raises a kernel's shared-memory limit once per device.
+static int allow_smem(const void* kernel, int bytes, std::once_flag* once) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ZERO_ECUDA;
+    cudaError_t e = cudaSuccess;
+    std::call_once(once[dev], [&] { e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+    if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+        return ZERO_ECUDA;
+    }
+    return ZERO_OK;
+}
+
+static int launch_cluster(const void* kernel, unsigned grid, unsigned threads, unsigned cluster, int smem, const void* params,
+                          cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<void*>(params)};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+    if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+        return ZERO_ECUDA;
+    }
+    return ZERO_OK;
+}
+
+static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
+    static std::once_flag once[2][64];
+    const void* kernel = e.out_f32 ? (const void*)pair_kernel<true> : (const void*)pair_kernel<false>;
+    if (const int rc = allow_smem(kernel, kPairSmem, once[e.out_f32])) return rc;
+    PairParams q{};
+    q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
+    q.tiles_m = (int32_t)((p.rows + 255) / 256);
+    const int pairs = sm_count() / 2;
+    // the tile width whose waves of pairs cover the columns with the least work
+    int64_t best = INT64_MAX;
+    const int64_t fewest = (p.cols + 255) / 256;
+    for (int64_t tn = fewest; tn < fewest + 4; ++tn) {
+        const int64_t bn = ((p.cols + tn - 1) / tn + 31) / 32 * 32;
+        const int64_t n = (p.cols + bn - 1) / bn;
+        const int64_t cost = (q.tiles_m * n + pairs - 1) / pairs * (bn + 16);
+        if (cost < best) best = cost, q.bn = (int32_t)bn, q.tiles_n = (int32_t)n;
+    }
+    q.k_blocks = (int32_t)((p.depth + 63) / 64);
+    q.a_mn = p.a.mn; q.b_mn = p.b.mn;
+    q.e = e;
+    if (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
+    const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
+    return launch_cluster(kernel, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, 2, kPairSmem, &q, s);
+}
+
+static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream_t s) {
+    static std::once_flag once[4][64];
+    const void* kernel = e.out_f32 ? (soft ? (const void*)split_kernel<true, true> : (const void*)split_kernel<true, false>)
+                                   : (soft ? (const void*)split_kernel<false, true> : (const void*)split_kernel<false, false>);
+    if (const int rc = allow_smem(kernel, kSplitSmem, once[e.out_f32 * 2 + soft])) return rc;
+    SplitParams q{};
+    q.a = p.a; q.b = p.b;
+    q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
+    const int64_t tiles_m = (p.rows + 127) / 128, resident = 2 * (int64_t)sm_count();
+    q.bn = 128;
+    while (q.bn > 32 && tiles_m * ((p.cols + q.bn - 1) / q.bn) * 8 < resident) q.bn /= 2;
+    const int64_t tiles_n = (p.cols + q.bn - 1) / q.bn, tiles = tiles_m * tiles_n, k_blocks = (p.depth + 63) / 64;
+    int parts = 1;
+    while (parts < 8 && tiles * parts * 2 <= resident && k_blocks >= parts * 4) parts *= 2;
+    if (tiles > INT32_MAX / 8 || k_blocks > INT32_MAX) return ZERO_ERANGE;
+    q.tiles_m = (int32_t)tiles_m; q.tiles_n = (int32_t)tiles_n; q.k_blocks = (int32_t)k_blocks;
+    q.e = e;
+    if (!soft && (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
+    return launch_cluster(kernel, (unsigned)(tiles * parts), kSplitThreads, (unsigned)parts, kSplitSmem, &q, s);
+}
+
+static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
+    const int size = e.out_f32 ? 4 : 2;
+    e.vec = aligned16(e.bias) && (!e.slope || rows_aligned16(e.slope, e.ld_slope, 2)) && (!e.pre || rows_aligned16(e.pre, e.ld_pre, 2)) &&
+            (!e.add || rows_aligned16(e.add, e.ld_add, size)) && rows_aligned16(e.out, e.ld_out, size);
+    const bool reach = copies_reach(p.a) && copies_reach(p.b);
+    const int64_t pair_tiles = ((p.rows + 255) / 256) * ((p.cols + 255) / 256);
+    if (reach && pair_tiles >= sm_count() / 4 && pair_tiles < INT32_MAX / 8) return launch_pair(p, e, s);
+    return launch_split(p, e, !reach, s);
 }
 
 static bool act_ok(int32_t act) { return act >= ZERO_ACT_NONE && act <= ZERO_ACT_SILU; }
@@ -117,7 +796,7 @@ extern "C" int zero_linear(int64_t m, int64_t n, int64_t k, const uint16_t* x, i
     e.add = residual; e.ld_add = ldr;
     e.out = y; e.ld_out = ldy; e.out_f32 = y_dtype == ZERO_F32;
     e.act = act;
-    return launch_product(Product{m, n, k, x, ldx, 1, w, ldw, 1}, e, static_cast<cudaStream_t>(stream));
+    return launch_product(Product{m, n, k, {x, ldx, m, k, false}, {w, ldw, n, k, false}}, e, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int zero_linear_grad_input(int64_t m, int64_t n, int64_t k, const uint16_t* dz, int64_t lddz,
@@ -145,7 +824,7 @@ extern "C" int zero_linear_grad_input(int64_t m, int64_t n, int64_t k, const uin
     e.add = residual; e.ld_add = ldr;
     e.out = dx; e.ld_out = lddx; e.out_f32 = dx_dtype == ZERO_F32;
     e.act = act;
-    return launch_product(Product{m, k, n, dz, lddz, 1, w, 1, ldw}, e, static_cast<cudaStream_t>(stream));
+    return launch_product(Product{m, k, n, {dz, lddz, m, n, false}, {w, ldw, n, k, true}}, e, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int zero_linear_grad_weight(int64_t m, int64_t n, int64_t k, const uint16_t* dz, int64_t lddz,
@@ -173,5 +852,5 @@ extern "C" int zero_linear_grad_weight(int64_t m, int64_t n, int64_t k, const ui
     Ending e{};
     e.add = acc; e.ld_add = ldacc;
     e.out = dw; e.ld_out = lddw; e.out_f32 = dw_dtype == ZERO_F32;
-    return launch_product(Product{n, k, m, dz, 1, lddz, x, 1, ldx}, e, s);
+    return launch_product(Product{n, k, m, {dz, lddz, m, n, true}, {x, ldx, m, k, true}}, e, s);
 }

@@ -11,6 +11,8 @@ namespace zgb {
 // Reads and clears the status word of the opt-in staged 8-bit gradient
 // kernel's bounded waits (zero_qgrad.cu): ZERO_OK or ZERO_ETIMEOUT.
 int take_qgrad_status();
+// The same for the waits of the products' kernels (zero_linear.cu).
+int take_linear_status();
 }  // namespace zgb
 
 namespace zgb {
@@ -116,6 +118,7 @@ extern "C" int zero_status_check(void* stream) {
     if (e != cudaSuccess || last != cudaSuccess) return ZERO_ECUDA;
     const int rc = zgb::take_device_status();   // ZERO_ETIMEOUT if a bounded device wait gave up
     const int rq = zgb::take_qgrad_status();    // the same for the 8-bit gradient kernels' waits
+    const int rl = zgb::take_linear_status();   // and for those of the products
     const int rs = zgb::take_schedule_status();  // ZERO_ERANGE if a schedule index left its table
-    return rc != ZERO_OK ? rc : rq != ZERO_OK ? rq : rs;
+    return rc != ZERO_OK ? rc : rq != ZERO_OK ? rq : rl != ZERO_OK ? rl : rs;
 }
