@@ -57,6 +57,16 @@ __device__ __forceinline__ void drop8(const DropParams& d, uint32_t step, int64_
     }
 }
 
+// Where lane l of a warp holds the block of row l % 8 and column group l / 8 of an
+// 8 x 32 part: the 16 bits of row r in this lane's column.  Every lane calls.
+__device__ __forceinline__ uint32_t row_bits(const uint4& block, int r) {
+    const int lane = threadIdx.x & 31, from = (lane & 24) | r;
+    const uint32_t w0 = __shfl_sync(0xffffffffu, block.x, from), w1 = __shfl_sync(0xffffffffu, block.y, from);
+    const uint32_t w2 = __shfl_sync(0xffffffffu, block.z, from), w3 = __shfl_sync(0xffffffffu, block.w, from);
+    const uint32_t w = lane & 4 ? (lane & 2 ? w3 : w2) : (lane & 2 ? w1 : w0);
+    return lane & 1 ? w >> 16 : w & 0xffffu;
+}
+
 // Checks a caller's block and forms the kernels' parameters; null = no dropout.
 int drop_params(const zero_dropout_t* d, int64_t rows, int64_t cols, DropParams* out);
 
@@ -73,40 +83,66 @@ __device__ __forceinline__ float sigmoid_f(float u) { return __fdividef(1.0f, 1.
 constexpr float kGeluC = 0.79788456080286535588f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float act_apply(int act, float z) {
-    switch (act) {
-        case ZERO_ACT_RELU: return z < 0.0f ? 0.0f : z;   // a NaN stays
-        case ZERO_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
-        case ZERO_ACT_GELU_TANH: return __fdividef(z, 1.0f + __expf(-2.0f * kGeluC * (z + kGeluA * z * z * z)));
-        case ZERO_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
-        default: return z;
-    }
+template <int kAct>
+__device__ __forceinline__ float act_one(float z) {
+    if constexpr (kAct == ZERO_ACT_RELU) return z < 0.0f ? 0.0f : z;   // a NaN stays
+    if constexpr (kAct == ZERO_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
+    if constexpr (kAct == ZERO_ACT_GELU_TANH)
+        return __fdividef(z, 1.0f + __expf(-2.0f * kGeluC * (z + kGeluA * z * z * z)));
+    if constexpr (kAct == ZERO_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+    return z;
 }
 
 // Past the clamps the second term of a slope is below fp32's resolution; without
 // them it would be 0 * infinity.  A NaN passes both comparisons and stays.
 __device__ __forceinline__ float clamp_keep_nan(float z, float c) { return z > c ? c : z < -c ? -c : z; }
 
-__device__ __forceinline__ float act_slope(int act, float z) {
-    switch (act) {
-        case ZERO_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-        case ZERO_ACT_GELU: {
-            z = clamp_keep_nan(z, 20.0f);
-            return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) +
-                   z * 0.39894228040143267794f * __expf(-0.5f * z * z);
-        }
-        case ZERO_ACT_GELU_TANH: {
-            z = clamp_keep_nan(z, 20.0f);
-            const float s = sigmoid_f(2.0f * kGeluC * (z + kGeluA * z * z * z));
-            return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
-        }
-        case ZERO_ACT_SILU: {
-            z = clamp_keep_nan(z, 104.0f);   // past 89 the exponential is already infinite
-            const float s = sigmoid_f(z);
-            return s * (1.0f + z * (1.0f - s));
-        }
-        default: return 1.0f;
+template <int kAct>
+__device__ __forceinline__ float slope_one(float z) {
+    if constexpr (kAct == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (kAct == ZERO_ACT_GELU) {
+        z = clamp_keep_nan(z, 20.0f);
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) + z * 0.39894228040143267794f * __expf(-0.5f * z * z);
     }
+    if constexpr (kAct == ZERO_ACT_GELU_TANH) {
+        z = clamp_keep_nan(z, 20.0f);
+        const float s = sigmoid_f(2.0f * kGeluC * (z + kGeluA * z * z * z));
+        return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+    }
+    if constexpr (kAct == ZERO_ACT_SILU) {
+        z = clamp_keep_nan(z, 104.0f);   // past 89 the exponential is already infinite
+        const float s = sigmoid_f(z);
+        return s * (1.0f + z * (1.0f - s));
+    }
+    return 1.0f;
+}
+
+// Over kCount values at once: one branch on the activation, so that the chains of
+// the values interleave (a branch a value made the end of a product five times as
+// long as the product).
+template <int kCount>
+__device__ __forceinline__ void act_apply(int act, float* v) {
+#define ZGB_EACH(A) _Pragma("unroll") for (int j = 0; j < kCount; ++j) v[j] = act_one<A>(v[j])
+    switch (act) {
+        case ZERO_ACT_RELU: ZGB_EACH(ZERO_ACT_RELU); break;
+        case ZERO_ACT_GELU: ZGB_EACH(ZERO_ACT_GELU); break;
+        case ZERO_ACT_GELU_TANH: ZGB_EACH(ZERO_ACT_GELU_TANH); break;
+        case ZERO_ACT_SILU: ZGB_EACH(ZERO_ACT_SILU); break;
+        default: break;
+    }
+#undef ZGB_EACH
+}
+template <int kCount>
+__device__ __forceinline__ void slope_apply(int act, const float* z, float* v) {
+#define ZGB_EACH(A) _Pragma("unroll") for (int j = 0; j < kCount; ++j) v[j] *= slope_one<A>(z[j])
+    switch (act) {
+        case ZERO_ACT_RELU: ZGB_EACH(ZERO_ACT_RELU); break;
+        case ZERO_ACT_GELU: ZGB_EACH(ZERO_ACT_GELU); break;
+        case ZERO_ACT_GELU_TANH: ZGB_EACH(ZERO_ACT_GELU_TANH); break;
+        case ZERO_ACT_SILU: ZGB_EACH(ZERO_ACT_SILU); break;
+        default: break;
+    }
+#undef ZGB_EACH
 }
 
 // ---- eight neighbouring columns ---------------------------------------------
@@ -119,6 +155,16 @@ __device__ __forceinline__ void unpack8(uint4 u, float* v) {
 __device__ __forceinline__ uint4 pack8(const float* v) {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                       pack_bf16x2(v[6], v[7]));
+}
+
+template <bool kF32>
+__device__ __forceinline__ void raw8(const uint4* u, float* v) {   // as loaded: one vector of bf16, two of fp32
+    if constexpr (kF32) {
+        v[0] = __uint_as_float(u[0].x); v[1] = __uint_as_float(u[0].y); v[2] = __uint_as_float(u[0].z); v[3] = __uint_as_float(u[0].w);
+        v[4] = __uint_as_float(u[1].x); v[5] = __uint_as_float(u[1].y); v[6] = __uint_as_float(u[1].z); v[7] = __uint_as_float(u[1].w);
+    } else {
+        unpack8(u[0], v);
+    }
 }
 
 // p points at the first of the eight; `vec`: p is 16-byte aligned and count == 8.
@@ -174,6 +220,30 @@ inline int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, i
     if (!p) return ZERO_EINVAL;
     if (ld > 0 && rows > INT64_MAX / 8 / ld) return ZERO_ERANGE;
     return check_aligned(p, dtype_size(dtype));
+}
+
+// A launch with clusters of `cluster` CTAs along x.
+template <class... Params, class... Args>
+int launch_cluster(void (*kernel)(Params...), unsigned grid, unsigned threads, unsigned cluster, int smem, cudaStream_t s,
+                   Args&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+    if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+        return ZERO_ECUDA;
+    }
+    return ZERO_OK;
 }
 
 }  // namespace zgb

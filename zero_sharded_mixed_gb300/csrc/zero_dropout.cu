@@ -9,6 +9,7 @@
 #include <cmath>
 
 #include "zero_dense.cuh"
+#include "zero_tensor.cuh"
 
 namespace zgb {
 
@@ -38,102 +39,222 @@ struct DropoutParams {
     int64_t rows, cols, col_blocks;
     const void* x; int64_t ldx;            // x or dy
     const void* side; int64_t lds;         // the residual or pre, or null
-    void* y; int64_t ldy;
+    void* y; int64_t ldy;                  // null: only the sums are wanted
+    const void* db_acc; void* db;
     int32_t act;
-    bool x_f32, y_f32, x_vec, side_vec, y_vec;
+    bool x_f32, y_f32, side_f32, db_f32;
     DropParams drop;
 };
 
-// One thread takes eight columns of a row at a time, over the whole matrix in
-// steps of the grid.
-template <bool kGrad>
+// Whole, aligned rows: one thread takes eight columns at a time, kBatch groups of
+// loads in flight, over the matrix in steps of the grid (row and column carried
+// along, without a division a step).
+constexpr int kBatch = 4;
+
+template <bool kGrad, bool kF32>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
-    const int64_t total = p.rows * p.col_blocks;
     const int64_t stride = (int64_t)gridDim.x * kThreads;
+    const int64_t step_rows = stride / p.col_blocks, step_cols = stride - step_rows * p.col_blocks;
     const uint32_t step = p.drop.cut ? drop_step(p.drop) : 0u;
-    const int xs = p.x_f32 ? 4 : 2, ys = p.y_f32 ? 4 : 2;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += stride) {
-        const int64_t row = i / p.col_blocks, cb = i - row * p.col_blocks, col = cb * 8;
-        const int count = p.cols - col < 8 ? (int)(p.cols - col) : 8;
-        const bool full = count == 8;
-        float v[8];
-        load8(static_cast<const char*>(p.x) + (row * p.ldx + col) * xs, p.x_f32, p.x_vec && full, count, v);
-        if (kGrad && p.side) {
-            float z[8];
-            load8(static_cast<const uint16_t*>(p.side) + row * p.lds + col, false, p.side_vec && full, count, z);
+    constexpr int xs = kF32 ? 4 : 2;
+    int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    int64_t row = i / p.col_blocks, cb = i - row * p.col_blocks;
+    while (row < p.rows) {
+        int64_t r[kBatch], c[kBatch];
+        uint4 x[kBatch][kF32 ? 2 : 1], side[kBatch][kF32 && !kGrad ? 2 : 1];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= act_slope(p.act, z[j]);
+        for (int j = 0; j < kBatch; ++j) {
+            r[j] = row;
+            c[j] = cb;
+            if (row < p.rows) {
+                const char* q = static_cast<const char*>(p.x) + (row * p.ldx + cb * 8) * xs;
+                x[j][0] = ld_stream_u4(q);
+                if constexpr (kF32) x[j][1] = ld_stream_u4(q + 16);
+                if (p.side) {
+                    const char* t = static_cast<const char*>(p.side) + (row * p.lds + cb * 8) * (kGrad ? 2 : xs);
+                    side[j][0] = ld_stream_u4(t);
+                    if constexpr (kF32 && !kGrad) side[j][1] = ld_stream_u4(t + 16);
+                }
+            }
+            row += step_rows;
+            cb += step_cols;
+            if (cb >= p.col_blocks) cb -= p.col_blocks, ++row;
         }
-        if (p.drop.cut) drop8(p.drop, step, row, cb, v);
-        if (!kGrad && p.side) {
-            float r[8];
-            load8(static_cast<const char*>(p.side) + (row * p.lds + col) * xs, p.x_f32, p.side_vec && full, count, r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += r[j];
+        for (int j = 0; j < kBatch; ++j) {
+            if (r[j] >= p.rows) break;
+            float v[8], t[8];
+            raw8<kF32>(x[j], v);
+            if (p.side) raw8<kF32 && !kGrad>(side[j], t);
+            if (kGrad && p.side) slope_apply<8>(p.act, t, v);
+            if (p.drop.cut) drop8(p.drop, step, r[j], c[j], v);
+            if (!kGrad && p.side) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] += t[k];
+            }
+            store8(static_cast<char*>(p.y) + (r[j] * p.ldy + c[j] * 8) * (p.y_f32 ? 4 : 2), p.y_f32, true, 8, v);
         }
-        store8(static_cast<char*>(p.y) + (row * p.ldy + col) * ys, p.y_f32, p.y_vec && full, count, v);
     }
 }
 
-// db for dropout_kernel<true>: one thread a column, recomputing dx in fp32.
-__global__ void __launch_bounds__(kThreads)
-dropout_column_sum_kernel(const DropoutParams p, const void* db_acc, void* db, bool db_f32) {
-    const int64_t cb = ((int64_t)blockIdx.x * kThreads + threadIdx.x);
-    if (cb >= p.col_blocks) return;
-    const int64_t col = cb * 8;
-    const int count = p.cols - col < 8 ? (int)(p.cols - col) : 8;
+// With column sums, or rows that are not aligned: a CTA takes a strip of 64
+// columns over a share of the rows.  Aligned (kVec): 8 threads a row, 32 rows at a
+// time.  Otherwise a warp takes 8 rows x 32 columns, a lane a column, so that a
+// row's accesses fall together; each lane forms the random bits of one row and
+// column group and the lanes of that group fetch them from it.
+// Sums (kSums): the shares of a strip are the CTAs of a cluster.  Each thread sums
+// its rows in order, the CTA its threads, then the cluster its CTAs, every time in
+// the same order.
+constexpr int kStrip = 64, kShares = 8;
+
+template <bool kGrad, bool kVec, bool kSums>
+__global__ void __launch_bounds__(kThreads) dropout_strip_kernel(const DropoutParams p, int shares) {
+    __shared__ float part[kThreads / 8][kStrip + 1];
+    __shared__ float total[kStrip];
+    const int share = blockIdx.x % shares;
+    const int64_t col0 = (int64_t)(blockIdx.x / shares) * kStrip;
+    const int64_t row_a = p.rows / shares * share + (p.rows % shares) * share / shares;
+    const int64_t row_b = p.rows / shares * (share + 1) + (p.rows % shares) * (share + 1) / shares;
     const uint32_t step = p.drop.cut ? drop_step(p.drop) : 0u;
-    const int xs = p.x_f32 ? 4 : 2, bs = db_f32 ? 4 : 2;
-    float sum[8] = {};
-    for (int64_t row = 0; row < p.rows; ++row) {
-        float v[8];
-        load8(static_cast<const char*>(p.x) + (row * p.ldx + col) * xs, p.x_f32, false, count, v);
-        if (p.side) {
-            float z[8];
-            load8(static_cast<const uint16_t*>(p.side) + row * p.lds + col, false, false, count, z);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int xs = p.x_f32 ? 4 : 2, ys = p.y_f32 ? 4 : 2, ss = p.side_f32 ? 4 : 2;
+    if constexpr (kVec) {
+        const int64_t col = col0 + (threadIdx.x & 7) * 8;
+        float sum[8] = {};
+        if (col < p.cols) {   // whole groups: the columns are a multiple of 8
+#pragma unroll 4
+            for (int64_t row = row_a + threadIdx.x / 8; row < row_b; row += kThreads / 8) {
+                float v[8], t[8];
+                load8(static_cast<const char*>(p.x) + (row * p.ldx + col) * xs, p.x_f32, true, 8, v);
+                if (p.side) {
+                    load8(static_cast<const char*>(p.side) + (row * p.lds + col) * ss, p.side_f32, true, 8, t);
+                    if (kGrad) slope_apply<8>(p.act, t, v);
+                }
+                if (p.drop.cut) drop8(p.drop, step, row, col >> 3, v);
+                if (!kGrad && p.side) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= act_slope(p.act, z[j]);
+                    for (int k = 0; k < 8; ++k) v[k] += t[k];
+                }
+                if (p.y) store8(static_cast<char*>(p.y) + (row * p.ldy + col) * ys, p.y_f32, true, 8, v);
+                if constexpr (kSums) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sum[k] += v[k];
+                }
+            }
         }
-        if (p.drop.cut) drop8(p.drop, step, row, cb, v);
+        if constexpr (kSums) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += v[j];
-    }
-    if (db_acc) {
-        float a[8];
-        load8(static_cast<const char*>(db_acc) + col * bs, db_f32, false, count, a);
+            for (int k = 0; k < 8; ++k) part[threadIdx.x / 8][(threadIdx.x & 7) * 8 + k] = sum[k];
+        }
+    } else {
+        const int64_t col = col0 + (warp & 1) * 32 + lane;
+        float sum = 0.0f;
+        for (int64_t row0 = row_a + (warp >> 1) * 8; row0 < row_b; row0 += kThreads / 8) {
+            float v[8], t[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += a[j];
+            for (int r = 0; r < 8; ++r) {
+                const bool in = row0 + r < row_b && col < p.cols;
+                const int64_t at = (row0 + r) * p.ldx + col, side_at = (row0 + r) * p.lds + col;
+                v[r] = !in ? 0.0f : p.x_f32 ? static_cast<const float*>(p.x)[at] : bf16_one(static_cast<const uint16_t*>(p.x)[at]);
+                t[r] = !in || !p.side ? 0.0f
+                       : p.side_f32   ? static_cast<const float*>(p.side)[side_at]
+                                      : bf16_one(static_cast<const uint16_t*>(p.side)[side_at]);
+            }
+            if (kGrad && p.side) slope_apply<8>(p.act, t, v);
+            uint4 block = make_uint4(0u, 0u, 0u, 0u);
+            if (p.drop.cut)
+                block = philox_block(p.drop, step, (uint32_t)(row0 + (lane & 7)),
+                                     (uint32_t)((col0 >> 3) + (warp & 1) * 4 + (lane >> 3)));
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (p.drop.cut) v[r] = row_bits(block, r) >= p.drop.cut ? v[r] * p.drop.scale : 0.0f;
+                if (!kGrad) v[r] += t[r];
+                if (row0 + r < row_b && col < p.cols) {
+                    if (p.y) {
+                        const int64_t at = (row0 + r) * p.ldy + col;
+                        if (p.y_f32)
+                            static_cast<float*>(p.y)[at] = v[r];
+                        else
+                            static_cast<uint16_t*>(p.y)[at] = to_bf16(v[r]);
+                    }
+                    if constexpr (kSums) sum += v[r];
+                }
+            }
+        }
+        if constexpr (kSums) part[warp >> 1][(warp & 1) * 32 + lane] = sum;
     }
-    store8(static_cast<char*>(db) + col * bs, db_f32, false, count, sum);
+    if constexpr (kSums) {
+        __syncthreads();
+        if (threadIdx.x < kStrip) {
+            float s = 0.0f;
+            for (int i = 0; i < (kVec ? kThreads / 8 : kThreads / 64); ++i) s += part[i][threadIdx.x];
+            total[threadIdx.x] = s;
+        }
+        __syncthreads();
+        cluster_sync();
+        const int c = (int)cluster_rank() * (kStrip / kShares) + threadIdx.x;   // eight columns a CTA
+        if (threadIdx.x < kStrip / kShares && col0 + c < p.cols) {
+            float s = 0.0f;
+            for (int i = 0; i < kShares; ++i) s += peer_load1(peer_addr(smem_addr(total + c), i));
+            const int64_t at = col0 + c;
+            if (p.db_f32) {
+                if (p.db_acc) s += static_cast<const float*>(p.db_acc)[at];
+                static_cast<float*>(p.db)[at] = s;
+            } else {
+                if (p.db_acc) s += bf16_one(static_cast<const uint16_t*>(p.db_acc)[at]);
+                static_cast<uint16_t*>(p.db)[at] = to_bf16(s);
+            }
+        }
+        __syncwarp();
+        cluster_sync();   // the totals are read before their CTAs end
+    }
 }
 
-static int launch_sums(const DropoutParams& p, const void* db_acc, void* db, bool db_f32, cudaStream_t s) {
-    dropout_column_sum_kernel<<<(unsigned)((p.col_blocks + kThreads - 1) / kThreads), kThreads, 0, s>>>(p, db_acc, db,
-                                                                                                        db_f32);
+template <bool kVec>
+static int launch_sums(const DropoutParams& p, cudaStream_t s) {
+    const int64_t strips = (p.cols + kStrip - 1) / kStrip;
+    if (strips > INT32_MAX / kShares) return ZERO_ERANGE;
+    return launch_cluster(dropout_strip_kernel<true, kVec, true>, (unsigned)(strips * kShares), kThreads, kShares, 0, s, p,
+                          (int)kShares);
+}
+
+template <bool kGrad>
+static int launch_dropout(DropoutParams& p, cudaStream_t s) {
+    p.col_blocks = (p.cols + 7) / 8;
+    const bool vec = p.cols % 8 == 0 && rows_aligned16(p.x, p.ldx, p.x_f32 ? 4 : 2) &&
+                     (!p.side || rows_aligned16(p.side, p.lds, p.side_f32 ? 4 : 2)) &&
+                     (!p.y || rows_aligned16(p.y, p.ldy, p.y_f32 ? 4 : 2));
+    if constexpr (kGrad)
+        if (p.db) return vec ? launch_sums<true>(p, s) : launch_sums<false>(p, s);
+    if (!vec) {
+        // enough shares of at least 32 rows to fill the GPU about four times over
+        const int64_t strips = (p.cols + kStrip - 1) / kStrip, most = (p.rows + 31) / 32;
+        int64_t shares = (int64_t)sm_count() * 32 / strips;
+        shares = shares < 1 ? 1 : shares > most ? most : shares;
+        if (strips > INT32_MAX / shares) return ZERO_ERANGE;
+        dropout_strip_kernel<kGrad, false, false><<<(unsigned)(strips * shares), kThreads, 0, s>>>(p, (int)shares);
+        return launch_status();
+    }
+    const void* kernel = p.x_f32 ? (const void*)dropout_kernel<kGrad, true> : (const void*)dropout_kernel<kGrad, false>;
+    const int64_t resident = (int64_t)sm_count() * ctas_per_sm(kernel, kThreads, 0);
+    const unsigned grid = grid_for(p.rows * p.col_blocks, kThreads * kBatch, resident * 2);
+    if (p.x_f32)
+        dropout_kernel<kGrad, true><<<grid, kThreads, 0, s>>>(p);
+    else
+        dropout_kernel<kGrad, false><<<grid, kThreads, 0, s>>>(p);
     return launch_status();
 }
 
 int launch_column_sum(int64_t rows, int64_t cols, const uint16_t* dz, int64_t lddz, const void* db_acc, void* db,
                       bool db_f32, cudaStream_t s) {
     DropoutParams p{};
-    p.rows = rows; p.cols = cols; p.col_blocks = (cols + 7) / 8;
+    p.rows = rows; p.cols = cols;
     p.x = dz; p.ldx = lddz;
-    p.x_vec = rows_aligned16(dz, lddz, 2);
-    return launch_sums(p, db_acc, db, db_f32, s);
+    p.db_acc = db_acc; p.db = db; p.db_f32 = db_f32;
+    return launch_dropout<true>(p, s);
 }
 
 static bool dtype_ok(int32_t d) { return d == ZERO_BF16 || d == ZERO_F32; }
-
-static int launch_dropout(const DropoutParams& p, bool grad, cudaStream_t s) {
-    const void* kernel = grad ? (const void*)dropout_kernel<true> : (const void*)dropout_kernel<false>;
-    const int64_t resident = (int64_t)sm_count() * ctas_per_sm(kernel, kThreads, 0);
-    const unsigned grid = grid_for(p.rows * p.col_blocks, kThreads, resident * 4);
-    if (grad)
-        dropout_kernel<true><<<grid, kThreads, 0, s>>>(p);
-    else
-        dropout_kernel<false><<<grid, kThreads, 0, s>>>(p);
-    return launch_status();
-}
 
 }  // namespace zgb
 
@@ -152,14 +273,10 @@ extern "C" int zero_dropout(int64_t rows, int64_t cols, const void* x, int64_t l
     if (check_device_ptr(x) || check_device_ptr(y) || (residual && check_device_ptr(residual)) ||
         (p.drop.step_ptr && check_device_ptr(p.drop.step_ptr)))
         return ZERO_EINVAL;
-    const int size = dtype_size(dtype);
-    p.rows = rows; p.cols = cols; p.col_blocks = (cols + 7) / 8;
+      p.rows = rows; p.cols = cols;
     p.x = x; p.ldx = ldx; p.side = residual; p.lds = ldr; p.y = y; p.ldy = ldy;
-    p.x_f32 = p.y_f32 = dtype == ZERO_F32;
-    p.x_vec = rows_aligned16(x, ldx, size);
-    p.side_vec = residual && rows_aligned16(residual, ldr, size);
-    p.y_vec = rows_aligned16(y, ldy, size);
-    return launch_dropout(p, false, static_cast<cudaStream_t>(stream));
+    p.x_f32 = p.y_f32 = p.side_f32 = dtype == ZERO_F32;
+    return launch_dropout<false>(p, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int zero_dropout_grad(int64_t rows, int64_t cols, const void* dy, int64_t lddy, int32_t dy_dtype,
@@ -183,17 +300,11 @@ extern "C" int zero_dropout_grad(int64_t rows, int64_t cols, const void* dy, int
         (db && check_device_ptr(db)) || (db_acc && check_device_ptr(db_acc)) ||
         (p.drop.step_ptr && check_device_ptr(p.drop.step_ptr)))
         return ZERO_EINVAL;
-    p.rows = rows; p.cols = cols; p.col_blocks = (cols + 7) / 8;
+    p.rows = rows; p.cols = cols;
     p.x = dy; p.ldx = lddy; p.side = pre; p.lds = ldp; p.y = dx; p.ldy = lddx;
     p.act = act;
     p.x_f32 = dy_dtype == ZERO_F32;
     p.y_f32 = dx_dtype == ZERO_F32;
-    p.x_vec = rows_aligned16(dy, lddy, dtype_size(dy_dtype));
-    p.side_vec = pre && rows_aligned16(pre, ldp, 2);
-    p.y_vec = rows_aligned16(dx, lddx, dtype_size(dx_dtype));
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (db) {   // first: dx may be written over dy
-        if (const int rc = launch_sums(p, db_acc, db, db_dtype == ZERO_F32, s)) return rc;
-    }
-    return rows ? launch_dropout(p, true, s) : ZERO_OK;
+    p.db_acc = db_acc; p.db = db; p.db_f32 = db_dtype == ZERO_F32;
+    return launch_dropout<true>(p, static_cast<cudaStream_t>(stream));
 }

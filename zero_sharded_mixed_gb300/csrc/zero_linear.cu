@@ -89,11 +89,9 @@ __device__ __forceinline__ void end_vector(const Ending& e, uint32_t step, int64
     if (e.pre) *reinterpret_cast<uint4*>(e.pre + row * e.ld_pre + col) = pack8(v);
     if (e.slope) {
         unpack8(s.slope, t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= act_slope(e.act, t[j]);
+        slope_apply<8>(e.act, t, v);
     } else if (e.act) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = act_apply(e.act, v[j]);
+        act_apply<8>(e.act, v);
     }
     if (e.drop.cut) drop8(e.drop, step, row, col >> 3, v);
     if (e.add) {
@@ -111,25 +109,6 @@ __device__ __forceinline__ void end_vector(const Ending& e, uint32_t step, int64
     store8(static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2), kF32, true, 8, v);
 }
 
-// One element.
-template <bool kF32>
-__device__ __forceinline__ void end_element(const Ending& e, int64_t row, int64_t col, float bias, uint32_t bits, float v) {
-    v += bias;
-    if (e.pre) e.pre[row * e.ld_pre + col] = to_bf16(v);
-    if (e.slope)
-        v *= act_slope(e.act, bf16_one(e.slope[row * e.ld_slope + col]));
-    else if (e.act)
-        v = act_apply(e.act, v);
-    if (e.drop.cut) v = bits >= e.drop.cut ? v * e.drop.scale : 0.0f;
-    if constexpr (kF32) {
-        if (e.add) v += static_cast<const float*>(e.add)[row * e.ld_add + col];
-        static_cast<float*>(e.out)[row * e.ld_out + col] = v;
-    } else {
-        if (e.add) v += bf16_one(static_cast<const uint16_t*>(e.add)[row * e.ld_add + col]);
-        static_cast<uint16_t*>(e.out)[row * e.ld_out + col] = to_bf16(v);
-    }
-}
-
 // A unit whose rows are not aligned, or whose columns end inside a group: a lane a
 // column, row by row, so that a row's accesses still fall together.  get(r) gives
 // this lane's accumulator of row r; every lane of the warp calls.
@@ -141,18 +120,37 @@ __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t
     const float bias = e.bias && col < cols ? bf16_one(e.bias[col]) : 0.0f;
     uint4 block = make_uint4(0u, 0u, 0u, 0u);   // lane l forms the bits of row l % 8 and column group l / 8
     if (e.drop.cut) block = philox_block(e.drop, step, (uint32_t)(row0 + (lane & 7)), (uint32_t)((col0 >> 3) + (lane >> 3)));
+    float v[8], add[8], slope[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-        uint32_t bits = 0;
-        if (e.drop.cut) {
-            const int from = (lane & 24) | r;
-            const uint32_t w0 = __shfl_sync(0xffffffffu, block.x, from), w1 = __shfl_sync(0xffffffffu, block.y, from);
-            const uint32_t w2 = __shfl_sync(0xffffffffu, block.z, from), w3 = __shfl_sync(0xffffffffu, block.w, from);
-            const uint32_t w = lane & 4 ? (lane & 2 ? w3 : w2) : (lane & 2 ? w1 : w0);
-            bits = lane & 1 ? w >> 16 : w & 0xffffu;
+        const bool in = row0 + r < rows && col < cols;
+        add[r] = slope[r] = 0.0f;
+        if (in && e.add) {
+            const int64_t at = (row0 + r) * e.ld_add + col;
+            add[r] = kF32 ? static_cast<const float*>(e.add)[at] : bf16_one(static_cast<const uint16_t*>(e.add)[at]);
         }
-        const float v = get(r);
-        if (row0 + r < rows && col < cols) end_element<kF32>(e, row0 + r, col, bias, bits, v);
+        if (in && e.slope) slope[r] = bf16_one(e.slope[(row0 + r) * e.ld_slope + col]);
+        v[r] = get(r) + bias;
+    }
+    if (e.pre) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (row0 + r < rows && col < cols) e.pre[(row0 + r) * e.ld_pre + col] = to_bf16(v[r]);
+    }
+    if (e.slope)
+        slope_apply<8>(e.act, slope, v);
+    else if (e.act)
+        act_apply<8>(e.act, v);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        if (e.drop.cut) v[r] = row_bits(block, r) >= e.drop.cut ? v[r] * e.drop.scale : 0.0f;
+        if (row0 + r < rows && col < cols) {
+            const int64_t at = (row0 + r) * e.ld_out + col;
+            if (kF32)
+                static_cast<float*>(e.out)[at] = v[r] + add[r];
+            else
+                static_cast<uint16_t*>(e.out)[at] = to_bf16(v[r] + add[r]);
+        }
     }
 }
 
@@ -324,8 +322,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
     } else if (warp >= 4) {
         const int w = warp - 4, q = warp & 3, h = w / 4;
         uint8_t* chunk = chunks + w * kChunkBytes;
-        const uint32_t chunk_addr = smem_addr(chunk);
-        (void)chunk_addr;
         const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
         int n_tile = 0;
         for (int t = pair; t < tiles; t += pairs, ++n_tile) {
@@ -686,33 +682,10 @@ static int allow_smem(const void* kernel, int bytes, std::once_flag* once) {
     return ZERO_OK;
 }
 
-static int launch_cluster(const void* kernel, unsigned grid, unsigned threads, unsigned cluster, int smem, const void* params,
-                          cudaStream_t s) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    void* args[] = {const_cast<void*>(params)};
-    const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
-    if (e != cudaSuccess) {
-        note_cuda_error(e);
-        (void)cudaGetLastError();
-        return ZERO_ECUDA;
-    }
-    return ZERO_OK;
-}
-
 static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
     static std::once_flag once[2][64];
-    const void* kernel = e.out_f32 ? (const void*)pair_kernel<true> : (const void*)pair_kernel<false>;
-    if (const int rc = allow_smem(kernel, kPairSmem, once[e.out_f32])) return rc;
+    void (*kernel)(PairParams) = e.out_f32 ? pair_kernel<true> : pair_kernel<false>;
+    if (const int rc = allow_smem((const void*)kernel, kPairSmem, once[e.out_f32])) return rc;
     PairParams q{};
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
     q.tiles_m = (int32_t)((p.rows + 255) / 256);
@@ -731,14 +704,14 @@ static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
     q.e = e;
     if (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
     const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
-    return launch_cluster(kernel, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, 2, kPairSmem, &q, s);
+    return launch_cluster(kernel, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, 2, kPairSmem, s, q);
 }
 
 static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream_t s) {
     static std::once_flag once[4][64];
-    const void* kernel = e.out_f32 ? (soft ? (const void*)split_kernel<true, true> : (const void*)split_kernel<true, false>)
-                                   : (soft ? (const void*)split_kernel<false, true> : (const void*)split_kernel<false, false>);
-    if (const int rc = allow_smem(kernel, kSplitSmem, once[e.out_f32 * 2 + soft])) return rc;
+    void (*kernel)(SplitParams) = e.out_f32 ? (soft ? split_kernel<true, true> : split_kernel<true, false>)
+                                            : (soft ? split_kernel<false, true> : split_kernel<false, false>);
+    if (const int rc = allow_smem((const void*)kernel, kSplitSmem, once[e.out_f32 * 2 + soft])) return rc;
     SplitParams q{};
     q.a = p.a; q.b = p.b;
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
@@ -752,7 +725,7 @@ static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream
     q.tiles_m = (int32_t)tiles_m; q.tiles_n = (int32_t)tiles_n; q.k_blocks = (int32_t)k_blocks;
     q.e = e;
     if (!soft && (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
-    return launch_cluster(kernel, (unsigned)(tiles * parts), kSplitThreads, (unsigned)parts, kSplitSmem, &q, s);
+    return launch_cluster(kernel, (unsigned)(tiles * parts), kSplitThreads, (unsigned)parts, kSplitSmem, s, q);
 }
 
 static int launch_product(const Product& p, Ending& e, cudaStream_t s) {

@@ -23,53 +23,159 @@ struct RopeParams {
     void* y; int64_t yt, yh;
     const int64_t* positions;
     int64_t pos0;
-    bool f32, half, copy_rest;
+    bool copy_rest;
     float sin_sign;
+    int32_t cta_tokens, cta_heads;   // what one CTA takes
     zero_rope_plan_t plan;
 };
 
-__device__ __forceinline__ float rope_load(const void* p, int64_t i, bool f32) {
-    return f32 ? static_cast<const float*>(p)[i] : bf16_one(static_cast<const uint16_t*>(p)[i]);
+constexpr int kRopeItems = 2048;   // work items of a CTA, eight a thread
+
+template <bool kF32>
+__device__ __forceinline__ float rope_load(const void* p, int64_t i) {
+    return kF32 ? static_cast<const float*>(p)[i] : bf16_one(static_cast<const uint16_t*>(p)[i]);
 }
-__device__ __forceinline__ void rope_store(void* p, int64_t i, bool f32, float v) {
-    if (f32)
+template <bool kF32>
+__device__ __forceinline__ void rope_store(void* p, int64_t i, float v) {
+    if (kF32)
         static_cast<float*>(p)[i] = v;
     else
         static_cast<uint16_t*>(p)[i] = to_bf16(v);
 }
 
-// One CTA a token: the sines of its pairs once in shared memory, then every head.
+template <bool kF32>
+struct RopeVector {   // 16 bytes of a head
+    static constexpr int kCount = kF32 ? 4 : 8;
+    static __device__ __forceinline__ void open(uint4 u, float* v) {
+        if constexpr (kF32) {
+            v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+        } else {
+            unpack8(u, v);
+        }
+    }
+    static __device__ __forceinline__ uint4 close(const float* v) {
+        if constexpr (kF32)
+            return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else
+            return pack8(v);
+    }
+};
+
+// One rounding order for every path, so that a result does not depend on alignment.
+__device__ __forceinline__ void turn_pair(float2 c, float& first, float& second) {
+    const float f = first, o = second;
+    first = __fmaf_rn(f, c.x, -__fmul_rn(o, c.y));
+    second = __fmaf_rn(o, c.x, __fmul_rn(f, c.y));
+}
+
+// A CTA takes cta_tokens tokens of cta_heads heads: it forms the sines of those
+// tokens' pairs once in shared memory (one a thread or so), then turns the heads.
+// kVec: two 16-byte vectors an item, which hold kCount whole pairs (a's and b's in
+// the half layout, neighbours in the interleaved one); else a pair an item.
+template <bool kF32, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ float2 turn[ZERO_ROPE_MAX / 2];
+    __shared__ float2 turn[kThreads > ZERO_ROPE_MAX / 2 ? kThreads : ZERO_ROPE_MAX / 2];   // [cta_tokens][pairs]
     const int pairs = p.plan.rot / 2;
-    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-        const int64_t pos = p.positions ? p.positions[t] : p.pos0 + t;
-        for (int i = threadIdx.x; i < pairs; i += kThreads) {
-            const int64_t turns = (int64_t)((uint64_t)pos * p.plan.turn[i]);
-            float sn, cs;
-            sincospif((float)(int32_t)(turns >> 32) * 4.656612873077392578125e-10f, &sn, &cs);
-            turn[i] = make_float2(cs * p.plan.scale, sn * p.plan.scale * p.sin_sign);
-        }
-        __syncthreads();
-        for (int64_t j = threadIdx.x; j < p.heads * pairs; j += kThreads) {
-            const int64_t h = j / pairs;
-            const int i = (int)(j - h * pairs);
-            const int64_t ia = p.half ? i : 2 * i, ib = p.half ? i + pairs : 2 * i + 1;
-            const int64_t xb = t * p.xt + h * p.xh, yb = t * p.yt + h * p.yh;
-            const float a = rope_load(p.x, xb + ia, p.f32), b = rope_load(p.x, xb + ib, p.f32);
-            const float2 cs = turn[i];
-            rope_store(p.y, yb + ia, p.f32, a * cs.x - b * cs.y);
-            rope_store(p.y, yb + ib, p.f32, b * cs.x + a * cs.y);
-        }
-        if (p.copy_rest) {
-            const int rest = (int)(p.dim - p.plan.rot);
-            for (int64_t j = threadIdx.x; j < p.heads * rest; j += kThreads) {
-                const int64_t h = j / rest, i = j - h * rest + p.plan.rot;
-                rope_store(p.y, t * p.yt + h * p.yh + i, p.f32, rope_load(p.x, t * p.xt + h * p.xh + i, p.f32));
+    const int64_t t0 = (int64_t)blockIdx.x * p.cta_tokens, h0 = (int64_t)blockIdx.y * p.cta_heads;
+    const int nt = (int)(p.tokens - t0 < p.cta_tokens ? p.tokens - t0 : p.cta_tokens);
+    const int nh = (int)(p.heads - h0 < p.cta_heads ? p.heads - h0 : p.cta_heads);
+    for (int j = threadIdx.x; j < nt * pairs; j += kThreads) {
+        const int t = j / pairs, i = j - t * pairs;
+        const int64_t pos = p.positions ? p.positions[t0 + t] : (int64_t)((uint64_t)p.pos0 + (uint64_t)(t0 + t));
+        const uint64_t turns = (uint64_t)pos * p.plan.turn[i];
+        float sn, cs;
+        sincospif((float)(int32_t)(turns >> 32) * 4.656612873077392578125e-10f, &sn, &cs);   // 2^-31 half turns
+        turn[j] = make_float2(cs * p.plan.scale, sn * p.plan.scale * p.sin_sign);
+    }
+    __syncthreads();
+    if constexpr (kVec) {
+        using V = RopeVector<kF32>;
+        constexpr int kBatch = 4, size = kF32 ? 4 : 2;
+        const int per_head = pairs / V::kCount, items = nt * nh * per_head;
+        for (int j0 = threadIdx.x; j0 < items; j0 += kBatch * kThreads) {
+            uint4 a[kBatch], b[kBatch];
+            char* out[kBatch];
+            const float2* cs[kBatch];
+            const int second = (kHalf ? pairs : V::kCount) * size;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int j = j0 + k * kThreads;
+                if (j < items) {
+                    const int th = j / per_head, i = j - th * per_head, t = th / nh, h = th - t * nh;
+                    const int64_t in_head = (int64_t)i * V::kCount * (kHalf ? 1 : 2);
+                    const char* q = static_cast<const char*>(p.x) + ((t0 + t) * p.xt + (h0 + h) * p.xh + in_head) * size;
+                    a[k] = ld_stream_u4(q);
+                    b[k] = ld_stream_u4(q + second);
+                    out[k] = static_cast<char*>(p.y) + ((t0 + t) * p.yt + (h0 + h) * p.yh + in_head) * size;
+                    cs[k] = turn + t * pairs + i * V::kCount;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (j0 + k * kThreads < items) {
+                    float u[V::kCount], v[V::kCount];
+                    V::open(a[k], u);
+                    V::open(b[k], v);
+#pragma unroll
+                    for (int i = 0; i < V::kCount; ++i) {
+                        const float2 c = cs[k][i];
+                        // the pair's two elements: one of each vector, or neighbours of one
+                        float& first = kHalf ? u[i] : i < V::kCount / 2 ? u[2 * i] : v[2 * i - V::kCount];
+                        float& other = kHalf ? v[i] : i < V::kCount / 2 ? u[2 * i + 1] : v[2 * i + 1 - V::kCount];
+                        turn_pair(c, first, other);
+                    }
+                    st_stream_u4(out[k], V::close(u));
+                    st_stream_u4(out[k] + second, V::close(v));
+                }
             }
         }
-        __syncthreads();
+        if (p.copy_rest) {
+            const int rest = (int)((p.dim - p.plan.rot) / V::kCount);
+            for (int64_t j = threadIdx.x; j < (int64_t)nt * nh * rest; j += kThreads) {
+                const int64_t th = j / rest, t = th / nh, h = th - t * nh, in_head = p.plan.rot + (j - th * rest) * V::kCount;
+                st_stream_u4(static_cast<char*>(p.y) + ((t0 + t) * p.yt + (h0 + h) * p.yh + in_head) * size,
+                             ld_stream_u4(static_cast<const char*>(p.x) + ((t0 + t) * p.xt + (h0 + h) * p.xh + in_head) * size));
+            }
+        }
+    } else {
+        for (int j = threadIdx.x; j < nt * nh * pairs; j += kThreads) {
+            const int th = j / pairs, i = j - th * pairs, t = th / nh, h = th - t * nh;
+            const int64_t ia = kHalf ? i : 2 * i, ib = kHalf ? i + pairs : 2 * i + 1;
+            const int64_t xb = (t0 + t) * p.xt + (h0 + h) * p.xh, yb = (t0 + t) * p.yt + (h0 + h) * p.yh;
+            float a = rope_load<kF32>(p.x, xb + ia), b = rope_load<kF32>(p.x, xb + ib);
+            turn_pair(turn[t * pairs + i], a, b);
+            rope_store<kF32>(p.y, yb + ia, a);
+            rope_store<kF32>(p.y, yb + ib, b);
+        }
+        if (p.copy_rest) {
+            const int64_t rest = p.dim - p.plan.rot;
+            for (int64_t j = threadIdx.x; j < nt * nh * rest; j += kThreads) {
+                const int64_t th = j / rest, i = j - th * rest + p.plan.rot, t = th / nh, h = th - t * nh;
+                rope_store<kF32>(p.y, (t0 + t) * p.yt + (h0 + h) * p.yh + i, rope_load<kF32>(p.x, (t0 + t) * p.xt + (h0 + h) * p.xh + i));
+            }
+        }
     }
+}
+
+template <bool kF32, bool kHalf>
+static int launch_rope(RopeParams& p, cudaStream_t s) {
+    constexpr int count = RopeVector<kF32>::kCount;
+    const int pairs = p.plan.rot / 2;
+    const bool vec = pairs % count == 0 && p.dim % count == 0 && aligned16(p.x) && aligned16(p.y) && p.xt % count == 0 &&
+                     p.xh % count == 0 && p.yt % count == 0 && p.yh % count == 0;
+    const int per_head = vec ? pairs / count : pairs;
+    const int64_t tokens = kThreads / pairs > 1 ? kThreads / pairs : 1;
+    p.cta_tokens = (int32_t)(tokens < p.tokens ? tokens : p.tokens);
+    const int64_t heads = kRopeItems / (p.cta_tokens * per_head);
+    p.cta_heads = (int32_t)(heads < 1 ? 1 : heads < p.heads ? heads : p.heads);
+    const int64_t gx = (p.tokens + p.cta_tokens - 1) / p.cta_tokens, gy = (p.heads + p.cta_heads - 1) / p.cta_heads;
+    if (gx > INT32_MAX || gy > 65535) return ZERO_ERANGE;
+    const dim3 grid((unsigned)gx, (unsigned)gy);
+    if (vec)
+        rope_kernel<kF32, kHalf, true><<<grid, kThreads, 0, s>>>(p);
+    else
+        rope_kernel<kF32, kHalf, false><<<grid, kThreads, 0, s>>>(p);
+    return launch_status();
 }
 
 }  // namespace zgb
@@ -139,12 +245,11 @@ extern "C" int zero_rope(const zero_rope_plan_t* plan, int64_t tokens, int64_t h
     p.x = x; p.xt = x_token; p.xh = x_head;
     p.y = y; p.yt = y_token; p.yh = y_head;
     p.positions = positions; p.pos0 = pos0;
-    p.f32 = dtype == ZERO_F32;
-    p.half = plan->layout == ZERO_ROPE_HALF;
     p.copy_rest = dim > plan->rot && x != y;
     p.sin_sign = inverse ? -1.0f : 1.0f;
     p.plan = *plan;
-    const int64_t cap = (int64_t)sm_count() * ctas_per_sm((const void*)rope_kernel, kThreads, 0) * 8;
-    rope_kernel<<<(unsigned)(tokens < cap ? tokens : cap), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launch_status();
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool half = plan->layout == ZERO_ROPE_HALF;
+    if (dtype == ZERO_F32) return half ? launch_rope<true, true>(p, s) : launch_rope<true, false>(p, s);
+    return half ? launch_rope<false, true>(p, s) : launch_rope<false, false>(p, s);
 }
