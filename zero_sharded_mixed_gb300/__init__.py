@@ -36,7 +36,10 @@ _ENGINE_NAMES = {"ZeroEngine", "Zero3Engine"}
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
-        return getattr(binding, name)
+        value = getattr(binding, name)
+        if callable(value):             # looked up once: 0.7 us a call otherwise
+            globals()[name] = value
+        return value
     if name in _ENGINE_NAMES:
         from . import engine
         return getattr(engine, name)

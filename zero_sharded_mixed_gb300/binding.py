@@ -108,6 +108,9 @@ _lib = None
 def load():
     """Load the library (raises if it has not been built)."""
     global _lib
+    lib = _lib
+    if lib is not None:
+        return lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -270,8 +273,15 @@ def zero_comm_bytes(n, n_dp, stage, param_bytes=2.0, grad_bytes=2.0) -> float:
 # device calls
 # --------------------------------------------------------------------------
 
+# The current stream's handle without a Stream object around it (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device_index = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream_ptr(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and _device_index is not None and torch.cuda.is_initialized():
+            return _raw_stream(_device_index()) or None
         stream = torch.cuda.current_stream()
     if isinstance(stream, int):
         return stream or None
@@ -636,12 +646,12 @@ def _matrix(t, name, rows, cols, dtypes):
     code = dtypes.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape ({rows}, {cols}), got {tuple(t.shape)}")
     ld, inner = t.stride()
     if rows <= 1 or cols == 0:
         ld = cols
-    if (cols > 1 and inner != 1) or ld < cols:
+    if (inner != 1 and cols > 1) or ld < cols:
         raise ValueError(f"{name} must have rows of contiguous elements (strides {t.stride()})")
     return t.data_ptr(), ld, code
 

@@ -3,8 +3,9 @@
 //   zero_linear_grad_input   dx = residual + D'(dz w) act'(pre)
 //   zero_linear_grad_weight  dw = acc + dz^T x,  db = db_acc + sum over rows of dz
 #include <mutex>
+#include <type_traits>
 
-#include "zero_dense.cuh"
+#include "zero_product.cuh"
 #include "zero_tensor.cuh"
 
 namespace zgb {
@@ -26,32 +27,6 @@ int take_linear_status() {
     }
     return v == ZERO_OK ? ZERO_OK : ZERO_ETIMEOUT;
 }
-
-// ---- operands ------------------------------------------------------------------
-
-// A matrix as it is stored, row-major.  The product C[i, j] = sum over t of
-// A(i, t) B(j, t) reads an operand with its reduced dimension t along the columns
-// (K-major) or along the rows (MN-major).
-struct Operand {
-    const uint16_t* p;
-    int64_t ld, rows, cols;
-    bool mn;
-};
-struct Product {
-    int64_t rows, cols, depth;
-    Operand a, b;
-};
-struct Ending {
-    const uint16_t* bias;                       // per column, or null
-    const uint16_t* slope; int64_t ld_slope;    // pre of the layer below: times act'(slope), or null
-    uint16_t* pre; int64_t ld_pre;              // receives the product with its bias, or null
-    const void* add; int64_t ld_add;            // residual or acc, of the output's type, or null
-    void* out; int64_t ld_out;
-    int32_t act;
-    bool out_f32;
-    bool vec;                                   // every matrix above keeps 8-column groups on 16-byte boundaries
-    DropParams drop;
-};
 
 // ---- the end of a product --------------------------------------------------------
 // Accumulators reach the end in units of 8 rows x 32 columns of fp32 in shared
@@ -109,6 +84,9 @@ __device__ __forceinline__ void end_vector(const Ending& e, uint32_t step, int64
     store8(static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2), kF32, true, 8, v);
 }
 
+__device__ __forceinline__ float element(float x) { return x; }
+__device__ __forceinline__ float element(uint16_t x) { return bf16_one(x); }
+
 // A unit whose rows are not aligned, or whose columns end inside a group: a lane a
 // column, row by row, so that a row's accesses still fall together.  get(r) gives
 // this lane's accumulator of row r; every lane of the warp calls.
@@ -120,38 +98,46 @@ __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t
     const float bias = e.bias && col < cols ? bf16_one(e.bias[col]) : 0.0f;
     uint4 block = make_uint4(0u, 0u, 0u, 0u);   // lane l forms the bits of row l % 8 and column group l / 8
     if (e.drop.cut) block = philox_block(e.drop, step, (uint32_t)(row0 + (lane & 7)), (uint32_t)((col0 >> 3) + (lane >> 3)));
-    float v[8], add[8], slope[8];
+    // rows of this unit that exist, none where the column does not: one comparison a row
+    const int n = col < cols ? (rows - row0 < 8 ? (int)(rows - row0) : 8) : 0;
+    float v[8], t[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const bool in = row0 + r < rows && col < cols;
-        add[r] = slope[r] = 0.0f;
-        if (in && e.add) {
-            const int64_t at = (row0 + r) * e.ld_add + col;
-            add[r] = kF32 ? static_cast<const float*>(e.add)[at] : bf16_one(static_cast<const uint16_t*>(e.add)[at]);
-        }
-        if (in && e.slope) slope[r] = bf16_one(e.slope[(row0 + r) * e.ld_slope + col]);
-        v[r] = get(r) + bias;
-    }
+    for (int r = 0; r < 8; ++r) v[r] = get(r) + bias;
     if (e.pre) {
+        uint16_t* q = e.pre + row0 * e.ld_pre + col;
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (row0 + r < rows && col < cols) e.pre[(row0 + r) * e.ld_pre + col] = to_bf16(v[r]);
+        for (int r = 0; r < 8; ++r, q += e.ld_pre)
+            if (r < n) *q = to_bf16(v[r]);
     }
-    if (e.slope)
-        slope_apply<8>(e.act, slope, v);
-    else if (e.act)
+    if (e.slope) {
+        const uint16_t* q = e.slope + row0 * e.ld_slope + col;
+#pragma unroll
+        for (int r = 0; r < 8; ++r, q += e.ld_slope) t[r] = r < n ? bf16_one(*q) : 0.0f;
+        slope_apply<8>(e.act, t, v);
+    } else if (e.act) {
         act_apply<8>(e.act, v);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        if (e.drop.cut) v[r] = row_bits(block, r) >= e.drop.cut ? v[r] * e.drop.scale : 0.0f;
-        if (row0 + r < rows && col < cols) {
-            const int64_t at = (row0 + r) * e.ld_out + col;
-            if (kF32)
-                static_cast<float*>(e.out)[at] = v[r] + add[r];
-            else
-                static_cast<uint16_t*>(e.out)[at] = to_bf16(v[r] + add[r]);
-        }
     }
+    if (e.drop.cut) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = row_bits(block, r) >= e.drop.cut ? v[r] * e.drop.scale : 0.0f;
+    }
+    using T = typename std::conditional<kF32, float, uint16_t>::type;
+    if (e.add) {
+        const T* q = static_cast<const T*>(e.add) + row0 * e.ld_add + col;
+#pragma unroll
+        for (int r = 0; r < 8; ++r, q += e.ld_add) t[r] = r < n ? element(*q) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] += t[r];
+    }
+    T* q = static_cast<T*>(e.out) + row0 * e.ld_out + col;
+#pragma unroll
+    for (int r = 0; r < 8; ++r, q += e.ld_out)
+        if (r < n) {
+            if constexpr (kF32)
+                *q = v[r];
+            else
+                *q = to_bf16(v[r]);
+        }
 }
 
 __device__ __forceinline__ void load_bias8(const Ending& e, int64_t col, float* b) {
@@ -169,6 +155,14 @@ constexpr long long kWaitCycles = 1ll << 31;   // SM cycles (about a second) bef
 __device__ __forceinline__ bool wait_or_report(uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
     if (mbar_wait_bounded(bar, parity, kWaitCycles)) return true;
+    atomicExch(&g_linear_status, ZERO_ETIMEOUT);
+    return false;
+}
+
+// For a converged warp that goes on as a whole: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitCycles))) return true;
     atomicExch(&g_linear_status, ZERO_ETIMEOUT);
     return false;
 }
@@ -219,7 +213,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
     uint64_t* drained = acc_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int tiles = p.tiles_m * p.tiles_n;
@@ -250,21 +244,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
     const uint32_t stage_bytes = 16384u + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)half * 128u);
 
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t round = 0;
-            bool ok = true;
-            for (int t = pair; ok && t < tiles; t += pairs) {
-                int tm, tn;
-                tile_place(p, t, &tm, &tn);
-                const int row = tm * 256 + (int)rank * 128;
-                const int col = tn * p.bn + (int)rank * (tile_width(p, tn) / 2);
-                for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (round > 0 && !(ok = wait_or_report(empty + s, (round - 1) & 1))) break;
-                    const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384;
-                    const uint32_t bar = peer_addr(smem_addr(full + s), 0);
+        int s = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
+            int tm, tn;
+            tile_place(p, t, &tm, &tn);
+            const int row = tm * 256 + (int)rank * 128;
+            const int col = tn * p.bn + (int)rank * (tile_width(p, tn) / 2);
+            for (int kb = 0; kb < p.k_blocks; ++kb) {
+                if (round > 0 && !(ok = warp_wait(empty + s, (round - 1) & 1))) break;
+                const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384;
+                const uint32_t bar = peer_addr(smem_addr(full + s), 0);
+                const int k = kb * 64;
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * stage_bytes);
-                    const int k = kb * 64;
                     if (p.a_mn) {
                         tensor_load_pair(a, &p.map_a, row, k, bar);
                         tensor_load_pair(a + kSubTileBytes, &p.map_a, row + 64, k, bar);
@@ -276,49 +270,48 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
                     } else {
                         tensor_load_pair(b, &p.map_b, k, col, bar);
                     }
-                    if (++s == kPairStages) s = 0, ++round;
                 }
+                if (++s == kPairStages) s = 0, ++round;
             }
-            if (!ok && rank == 0)   // copies in flight land before the CTAs end
-                for (int i = 0; i < kPairStages; ++i) {
-                    const uint32_t done = i < s ? round : round - 1;   // the last round issued on stage i
-                    if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
-                }
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            int s = 0, n_tile = 0;
-            uint32_t round = 0;
-            bool ok = true;
-            const uint32_t a_step = descriptor_step(p.a_mn), b_step = descriptor_step(p.b_mn);
-            for (int t = pair; ok && t < tiles; t += pairs, ++n_tile) {
-                int tm, tn;
-                tile_place(p, t, &tm, &tn);
-                const uint32_t idesc = instruction_descriptor(256, tile_width(p, tn), p.a_mn, p.b_mn);
-                const int buf = n_tile & 1;
-                if (n_tile >= 2 && !(ok = wait_or_report(acc_empty + buf, (n_tile / 2 - 1) & 1))) break;
+        if (!ok && rank == 0)   // copies in flight land before the CTAs end
+            for (int i = 0; i < kPairStages; ++i) {
+                const uint32_t done = i < s ? round : round - 1;   // the last round issued on stage i
+                if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
+            }
+    } else if (warp == 1 && rank == 0) {
+        int s = 0, n_tile = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        const uint32_t a_step = descriptor_step(p.a_mn), b_step = descriptor_step(p.b_mn);
+        for (int t = pair; ok && t < tiles; t += pairs, ++n_tile) {
+            int tm, tn;
+            tile_place(p, t, &tm, &tn);
+            const uint32_t idesc = instruction_descriptor(256, tile_width(p, tn), p.a_mn, p.b_mn);
+            const int buf = n_tile & 1;
+            if (n_tile >= 2 && !(ok = warp_wait(acc_empty + buf, (n_tile / 2 - 1) & 1))) break;
+            tcgen05_fence_after();
+            const uint32_t d = tmem + buf * 256;
+            for (int kb = 0; kb < p.k_blocks; ++kb) {
+                if (!(ok = warp_wait(full + s, round & 1))) break;
                 tcgen05_fence_after();
-                const uint32_t d = tmem + buf * 256;
-                for (int kb = 0; kb < p.k_blocks; ++kb) {
-                    if (!(ok = wait_or_report(full + s, round & 1))) break;
-                    tcgen05_fence_after();
-                    const uint32_t a = smem_addr(smem + s * kStageBytes);
-                    uint64_t da = smem_descriptor(a, p.a_mn), db = smem_descriptor(a + 16384, p.b_mn);
-                    const int64_t left = p.depth - (int64_t)kb * 64;
-                    const int steps = left >= 64 ? 4 : (int)((left + 15) / 16);
-                    for (int i = 0; i < steps; ++i, da += a_step, db += b_step) mma_bf16<true>(d, da, db, idesc, kb + i > 0);
+                const uint32_t a = smem_addr(smem + s * kStageBytes);
+                const uint64_t da = smem_descriptor(a, p.a_mn), db = smem_descriptor(a + 16384, p.b_mn);
+                const int64_t left = p.depth - (int64_t)kb * 64;
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)   // the last step of all may end early
+                        if (left > 16 * i) mma_bf16<true>(d, da + i * a_step, db + i * b_step, idesc, kb + i > 0);
                     mma_commit<true>(empty + s);
-                    if (++s == kPairStages) s = 0, ++round;
                 }
-                if (ok) mma_commit<true>(acc_full + buf);
+                if (++s == kPairStages) s = 0, ++round;
             }
-            if (!ok) {   // products in flight end before the tensor memory is freed
-                mma_commit<true>(drained);
-                (void)mbar_wait_bounded(drained, 0, kWaitCycles / 8);
-            }
+            if (ok && elect_one()) mma_commit<true>(acc_full + buf);
         }
-        __syncwarp();
+        if (!ok) {   // products in flight end before the tensor memory is freed
+            if (elect_one()) mma_commit<true>(drained);
+            (void)mbar_wait_bounded(drained, 0, kWaitCycles / 8);
+        }
     } else if (warp >= 4) {
         const int w = warp - 4, q = warp & 3, h = w / 4;
         uint8_t* chunk = chunks + w * kChunkBytes;
@@ -328,8 +321,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
             int tm, tn;
             tile_place(p, t, &tm, &tn);
             const int buf = n_tile & 1, width = tile_width(p, tn);
-            const bool ok = wait_or_report(acc_full + buf, (n_tile / 2) & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!warp_wait(acc_full + buf, (n_tile / 2) & 1)) break;
             tcgen05_fence_after();
             const int64_t row0 = (int64_t)tm * 256 + rank * 128 + q * 32, col_tile = (int64_t)tn * p.bn;
             const int n_chunks = width / 32;
@@ -411,43 +403,6 @@ constexpr int kSplitStages = 3;
 constexpr int kSplitThreads = 288;
 constexpr int kSplitSmem = 1024 + kSplitStages * kStageBytes + 128;
 
-// Eight elements (r, c) .. (r, c + 7) of an operand, zeros outside it, from any
-// element-aligned place: the two 16-byte blocks that hold them, shifted together.
-// Blocks are read only where they lie wholly inside the operand's own memory.
-__device__ __forceinline__ uint4 fetch8(const Operand& o, int64_t r, int64_t c) {
-    uint4 out = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= o.rows || c >= o.cols) return out;
-    const uint16_t* q = o.p + r * o.ld + c;
-    const int64_t left = o.cols - c;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(q), lo = at & ~(uintptr_t)15;
-    const uint32_t shift = (uint32_t)(at & 15);
-    const uintptr_t first = reinterpret_cast<uintptr_t>(o.p), last = reinterpret_cast<uintptr_t>(o.p + (o.rows - 1) * o.ld + o.cols);
-    if (shift == 0 && left >= 8) return *reinterpret_cast<const uint4*>(q);
-    if (left >= 8 && lo >= first && lo + 32 <= last) {
-        const uint4 x = *reinterpret_cast<const uint4*>(lo), y = *reinterpret_cast<const uint4*>(lo + 16);
-        uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        if (shift & 8) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-        }
-        if (shift & 4) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-        }
-        const uint32_t bits = (shift & 2) * 8;
-        out.x = __funnelshift_r(w[0], w[1], bits);
-        out.y = __funnelshift_r(w[1], w[2], bits);
-        out.z = __funnelshift_r(w[2], w[3], bits);
-        out.w = __funnelshift_r(w[3], w[4], bits);
-        return out;
-    }
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < left) w[j / 2] |= (uint32_t)q[j] << (16 * (j & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // 256 threads bring `rows` (at most 128) sub-tile rows of an operand's tile.
 __device__ __forceinline__ void fetch_tile(const Operand& o, int64_t mn0, int64_t k0, int rows, uint8_t* dst) {
     uint4 v[4];
@@ -473,7 +428,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
     uint64_t* acc_full = empty + kSplitStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int parts = (int)cluster_size(), rank = (int)cluster_rank();
     const int tile = blockIdx.x / parts;
     const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
@@ -517,24 +472,26 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
                 mbar_arrive(full + s);
                 if (++s == kSplitStages) s = 0, ++round;
             }
-        } else if (threadIdx.x == 0) {
+        } else if (warp == 0) {
             int s = 0;
             uint32_t round = 0;
             const int a_boxes = p.a.mn ? a_rows / 64 : 1, b_boxes = p.b.mn ? b_rows / 64 : 1;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (round > 0 && !(ok = wait_or_report(empty + s, (round - 1) & 1))) break;
+                if (round > 0 && !(ok = warp_wait(empty + s, (round - 1) & 1))) break;
                 const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384, bar = smem_addr(full + s);
-                mbar_arrive_expect_tx(full + s, (uint32_t)(a_rows + b_rows) * 128u);
                 const int k = kb * 64;
-                if (p.a.mn) {
-                    for (int i = 0; i < a_boxes; ++i) tensor_load(a + i * kSubTileBytes, &p.map_a, (int)row_tile + 64 * i, k, bar);
-                } else {
-                    tensor_load(a, &p.map_a, k, (int)row_tile, bar);
-                }
-                if (p.b.mn) {
-                    for (int i = 0; i < b_boxes; ++i) tensor_load(b + i * kSubTileBytes, &p.map_b, (int)col_tile + 64 * i, k, bar);
-                } else {
-                    tensor_load(b, &p.map_b, k, (int)col_tile, bar);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full + s, (uint32_t)(a_rows + b_rows) * 128u);
+                    if (p.a.mn) {
+                        for (int i = 0; i < a_boxes; ++i) tensor_load(a + i * kSubTileBytes, &p.map_a, (int)row_tile + 64 * i, k, bar);
+                    } else {
+                        tensor_load(a, &p.map_a, k, (int)row_tile, bar);
+                    }
+                    if (p.b.mn) {
+                        for (int i = 0; i < b_boxes; ++i) tensor_load(b + i * kSubTileBytes, &p.map_b, (int)col_tile + 64 * i, k, bar);
+                    } else {
+                        tensor_load(b, &p.map_b, k, (int)col_tile, bar);
+                    }
                 }
                 if (++s == kSplitStages) s = 0, ++round;
             }
@@ -544,27 +501,29 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
                     if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
                 }
         }
-        __syncwarp();
-    } else if (lane == 0) {
+    } else {
         int s = 0;
         uint32_t round = 0;
         const uint32_t idesc = instruction_descriptor(128, p.bn, p.a.mn, p.b.mn);
         const uint32_t a_step = descriptor_step(p.a.mn), b_step = descriptor_step(p.b.mn);
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!(ok = wait_or_report(full + s, round & 1))) break;
+            if (!(ok = warp_wait(full + s, round & 1))) break;
             tcgen05_fence_after();
             const uint32_t a = smem_addr(smem + s * kStageBytes);
-            uint64_t da = smem_descriptor(a, p.a.mn), db = smem_descriptor(a + 16384, p.b.mn);
+            const uint64_t da = smem_descriptor(a, p.a.mn), db = smem_descriptor(a + 16384, p.b.mn);
             const int64_t left = p.depth - (int64_t)kb * 64;
-            const int steps = left >= 64 ? 4 : (int)((left + 15) / 16);
-            for (int i = 0; i < steps; ++i, da += a_step, db += b_step) mma_bf16<false>(tmem, da, db, idesc, kb > kb0 || i > 0);
-            mma_commit<false>(empty + s);
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (left > 16 * i) mma_bf16<false>(tmem, da + i * a_step, db + i * b_step, idesc, kb > kb0 || i > 0);
+                mma_commit<false>(empty + s);
+            }
             if (++s == kSplitStages) s = 0, ++round;
         }
-        mma_commit<false>(acc_full);   // after a failed wait too: the tensor memory is free once it arrives
+        if (elect_one()) mma_commit<false>(acc_full);   // after a failed wait too: the tensor memory is free once it arrives
     }
     __syncwarp();
-    ok = wait_or_report(acc_full, 0) && ok;
+    ok = warp_wait(acc_full, 0) && ok;
     tcgen05_fence_after();
 
     // this CTA's part to its shared memory, chunk (q, c) of the tile at 4 KB each
@@ -732,6 +691,7 @@ static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
     const int size = e.out_f32 ? 4 : 2;
     e.vec = aligned16(e.bias) && (!e.slope || rows_aligned16(e.slope, e.ld_slope, 2)) && (!e.pre || rows_aligned16(e.pre, e.ld_pre, 2)) &&
             (!e.add || rows_aligned16(e.add, e.ld_add, size)) && rows_aligned16(e.out, e.ld_out, size);
+    if (p.rows <= kMostRows && !p.a.mn && !p.b.mn) return launch_rows(p, e, s);
     const bool reach = copies_reach(p.a) && copies_reach(p.b);
     const int64_t pair_tiles = ((p.rows + 255) / 256) * ((p.cols + 255) / 256);
     if (reach && pair_tiles >= sm_count() / 4 && pair_tiles < INT32_MAX / 8) return launch_pair(p, e, s);

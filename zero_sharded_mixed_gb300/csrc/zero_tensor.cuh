@@ -16,6 +16,17 @@ namespace zgb {
 
 constexpr int kSubTileBytes = 64 * 128;      // 64 rows of 128 bytes
 
+// One lane of a converged warp.  The copies and products below are issued under
+// this predicate by a warp that runs its loop as a whole: their operands are uniform
+// registers, and under `lane == 0` a step of four products took 770 cycles to issue
+// where the tensor core needs 512.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x / 32), 0); }
+
 // ---- descriptors ---------------------------------------------------------------
 // Shared-memory matrix descriptor: address, leading and stride offsets in units of
 // 16 bytes, the fixed version bit 46 and the 128-byte swizzle (2 in bits 61..63).
@@ -120,8 +131,10 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Hands over tensor memory alone (its reads are ordered by the tcgen05 fences), so
+// the arrival need not order other memory.
 __device__ __forceinline__ void peer_arrive(uint32_t bar_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
 }
 __device__ __forceinline__ float4 peer_load(uint32_t addr) {
     float4 v;
