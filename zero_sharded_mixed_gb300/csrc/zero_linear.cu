@@ -38,51 +38,214 @@ __device__ __forceinline__ uint32_t group_place(int r, int g) {
     return (uint32_t)r * 128u + (uint32_t)((((g >> 1) | ((g & 1) << 2)) ^ s) << 4);
 }
 
+// The pair kernel's end of 16 rows x 32 whole, aligned columns, a warp together,
+// with the accumulators as tensor memory gives them (tmem_load_fragment): lane
+// 4 i + j holds two columns of every group of eight.  What moves in 16-byte vectors,
+// a lane a group (bf16 results and residuals, a Philox block), is exchanged between
+// the four lanes of a row by a 4 x 4 transposition of words.  Shared memory is left
+// alone: the products and their copies use its whole bandwidth, and a transposition
+// through it took 5900 cycles a tile against the 12800 of a product of depth 1600.
+__device__ __forceinline__ void quad_transpose(uint32_t* w) {   // w[g] of lane j becomes w[j] of lane g
+    const int lane = threadIdx.x & 31;
+    const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+    for (int a = 0; a < 4; a += 2) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? w[a] : w[a + 1], 1);
+        w[a] = odd ? r : w[a];
+        w[a + 1] = odd ? w[a + 1] : r;
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, high ? w[a] : w[a + 2], 2);
+        w[a] = high ? r : w[a];
+        w[a + 2] = high ? w[a + 2] : r;
+    }
+}
+__device__ __forceinline__ void quad_transpose(uint4& u) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    quad_transpose(w);
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <bool kF32>
-struct Sides {   // what an aligned unit reads beside its accumulators, as loaded
-    uint4 add[kF32 ? 2 : 1];
-    uint4 slope;
+struct FragmentEnd {
+    uint4 slope[2], add[2];             // rows i and i + 8: group j
+    float2 add32[kF32 ? 4 : 1][2];      // fp32: the fragment's own columns
+    bool in[2];
+
+    __device__ __forceinline__ void load(const Ending& e, int64_t row, int64_t col0, int64_t rows) {
+        const int j = threadIdx.x & 3;
+        in[0] = row < rows;
+        in[1] = row + 8 < rows;
+        if (e.add) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t at = (row + 8 * h) * e.ld_add + col0;
+                if (!in[h]) continue;
+                if constexpr (kF32) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) add32[g][h] = *reinterpret_cast<const float2*>(static_cast<const float*>(e.add) + at + 8 * g + 2 * j);
+                } else {
+                    add[h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.add) + at + 8 * j);
+                }
+            }
+        }
+        if (e.slope) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (in[h]) slope[h] = *reinterpret_cast<const uint4*>(e.slope + (row + 8 * h) * e.ld_slope + col0 + 8 * j);
+        }
+    }
+
+    // bf16 rows i and i + 8 of the fragment, 16 bytes a lane
+    __device__ __forceinline__ void store_bf16(uint16_t* q, int64_t ld, const float (&v)[4][4]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) w[g] = pack_bf16x2(v[g][2 * h], v[g][2 * h + 1]);
+            quad_transpose(w);
+            if (in[h]) *reinterpret_cast<uint4*>(q + 8 * h * ld) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+
+    __device__ __forceinline__ void finish(const Ending& e, uint32_t step, int64_t row, int64_t col0, float (&v)[4][4]) {
+        const int j = threadIdx.x & 3;
+        if (e.bias) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t b = *reinterpret_cast<const uint32_t*>(e.bias + col0 + 8 * g + 2 * j);
+                v[g][0] += bf16_lo(b); v[g][1] += bf16_hi(b);
+                v[g][2] += bf16_lo(b); v[g][3] += bf16_hi(b);
+            }
+        }
+        if (e.pre) store_bf16(e.pre + row * e.ld_pre + col0 + 8 * j, e.ld_pre, v);
+        if (e.slope) {
+            float t[4][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                quad_transpose(slope[h]);
+                const uint32_t w[4] = {slope[h].x, slope[h].y, slope[h].z, slope[h].w};
+#pragma unroll
+                for (int g = 0; g < 4; ++g) t[g][2 * h] = bf16_lo(w[g]), t[g][2 * h + 1] = bf16_hi(w[g]);
+            }
+            slope_apply<16>(e.act, t[0], v[0]);
+        } else if (e.act) {
+            act_apply<16>(e.act, v[0]);
+        }
+        if (e.drop.cut) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 b = philox_block(e.drop, step, (uint32_t)(row + 8 * h), (uint32_t)((col0 >> 3) + j));
+                quad_transpose(b);
+                const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    v[g][2 * h] = (w[g] & 0xffffu) >= e.drop.cut ? v[g][2 * h] * e.drop.scale : 0.0f;
+                    v[g][2 * h + 1] = (w[g] >> 16) >= e.drop.cut ? v[g][2 * h + 1] * e.drop.scale : 0.0f;
+                }
+            }
+        }
+        if constexpr (kF32) {
+            float* q = static_cast<float*>(e.out) + row * e.ld_out + col0 + 2 * j;
+#pragma unroll
+            for (int h = 0; h < 2; ++h, q += 8 * e.ld_out) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (e.add) v[g][2 * h] += add32[g][h].x, v[g][2 * h + 1] += add32[g][h].y;
+                    if (in[h]) *reinterpret_cast<float2*>(q + 8 * g) = make_float2(v[g][2 * h], v[g][2 * h + 1]);
+                }
+            }
+        } else {
+            if (e.add) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    quad_transpose(add[h]);
+                    const uint32_t w[4] = {add[h].x, add[h].y, add[h].z, add[h].w};
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) v[g][2 * h] += bf16_lo(w[g]), v[g][2 * h + 1] += bf16_hi(w[g]);
+                }
+            }
+            store_bf16(static_cast<uint16_t*>(e.out) + row * e.ld_out + col0 + 8 * j, e.ld_out, v);
+        }
+    }
 };
 
-template <bool kF32>
-__device__ __forceinline__ void load_sides(const Ending& e, int64_t row, int64_t col, Sides<kF32>* s) {
-    if (e.add) {
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(e.add) + (row * e.ld_add + col) * (kF32 ? 4 : 2));
-        s->add[0] = q[0];
-        if constexpr (kF32) s->add[1] = q[1];
-    }
-    if (e.slope) s->slope = *reinterpret_cast<const uint4*>(e.slope + row * e.ld_slope + col);
-}
+// kParts parts of eight whole, aligned columns each, 8 rows apart, to the end
+// together: each branch of the end is taken once for all of them, and their chains
+// interleave.  in[i]: part i has a row.  load() before the accumulators are there.
+template <bool kF32, int kParts>
+struct VectorEnd {
+    uint4 add[kParts][kF32 ? 2 : 1], slope[kParts];   // what the parts read beside their accumulators, as loaded
+    float bias[8];
+    bool in[kParts];
 
-// Eight whole, aligned columns.
-template <bool kF32>
-__device__ __forceinline__ void end_vector(const Ending& e, uint32_t step, int64_t row, int64_t col, const float* bias,
-                                           const Sides<kF32>& s, float* v) {
-    float t[8];
+    __device__ __forceinline__ void load(const Ending& e, int64_t row, int64_t col, int64_t rows) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += bias[j];
-    if (e.pre) *reinterpret_cast<uint4*>(e.pre + row * e.ld_pre + col) = pack8(v);
-    if (e.slope) {
-        unpack8(s.slope, t);
-        slope_apply<8>(e.act, t, v);
-    } else if (e.act) {
-        act_apply<8>(e.act, v);
-    }
-    if (e.drop.cut) drop8(e.drop, step, row, col >> 3, v);
-    if (e.add) {
-        if constexpr (kF32) {
-            const uint32_t u[8] = {s.add[0].x, s.add[0].y, s.add[0].z, s.add[0].w,
-                                   s.add[1].x, s.add[1].y, s.add[1].z, s.add[1].w};
+        for (int i = 0; i < kParts; ++i) in[i] = row + 8 * i < rows;
+        if (e.add) {
+            const char* q = static_cast<const char*>(e.add) + (row * e.ld_add + col) * (kF32 ? 4 : 2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = __uint_as_float(u[j]);
-        } else {
-            unpack8(s.add[0], t);
+            for (int i = 0; i < kParts; ++i, q += 8 * e.ld_add * (kF32 ? 4 : 2))
+                if (in[i]) {
+                    add[i][0] = reinterpret_cast<const uint4*>(q)[0];
+                    if constexpr (kF32) add[i][1] = reinterpret_cast<const uint4*>(q)[1];
+                }
         }
+        if (e.slope) {
+            const uint16_t* q = e.slope + row * e.ld_slope + col;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += t[j];
+            for (int i = 0; i < kParts; ++i, q += 8 * e.ld_slope)
+                if (in[i]) slope[i] = *reinterpret_cast<const uint4*>(q);
+        }
+        if (e.bias) {
+            unpack8(*reinterpret_cast<const uint4*>(e.bias + col), bias);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bias[j] = 0.0f;
+        }
     }
-    store8(static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2), kF32, true, 8, v);
-}
+
+    __device__ __forceinline__ void finish(const Ending& e, uint32_t step, int64_t row, int64_t col, float (&v)[kParts][8]) {
+        if (e.bias) {
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] += bias[j];
+        }
+        if (e.pre) {
+            uint16_t* q = e.pre + row * e.ld_pre + col;
+#pragma unroll
+            for (int i = 0; i < kParts; ++i, q += 8 * e.ld_pre)
+                if (in[i]) *reinterpret_cast<uint4*>(q) = pack8(v[i]);
+        }
+        if (e.slope) {
+            float t[kParts][8];
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) unpack8(slope[i], t[i]);
+            slope_apply<8 * kParts>(e.act, t[0], v[0]);
+        } else if (e.act) {
+            act_apply<8 * kParts>(e.act, v[0]);
+        }
+        if (e.drop.cut) {
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) drop8(e.drop, step, row + 8 * i, col >> 3, v[i]);
+        }
+        if (e.add) {
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                float t[8];
+                raw8<kF32>(add[i], t);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] += t[j];
+            }
+        }
+        char* q = static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i, q += 8 * e.ld_out * (kF32 ? 4 : 2))
+            if (in[i]) store8(q, kF32, true, 8, v[i]);
+    }
+};
 
 __device__ __forceinline__ float element(float x) { return x; }
 __device__ __forceinline__ float element(uint16_t x) { return bf16_one(x); }
@@ -140,15 +303,6 @@ __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t
         }
 }
 
-__device__ __forceinline__ void load_bias8(const Ending& e, int64_t col, float* b) {
-    if (e.bias) {
-        unpack8(*reinterpret_cast<const uint4*>(e.bias + col), b);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = 0.0f;
-    }
-}
-
 // ---- waits -------------------------------------------------------------------------
 constexpr long long kWaitCycles = 1ll << 31;   // SM cycles (about a second) before a wait gives up
 
@@ -158,6 +312,8 @@ __device__ __forceinline__ bool wait_or_report(uint64_t* bar, uint32_t parity) {
     atomicExch(&g_linear_status, ZERO_ETIMEOUT);
     return false;
 }
+
+__device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // For a converged warp that goes on as a whole: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -171,7 +327,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // Large aligned products: pairs of CTAs, each pair one 256 x bn tile at a time (its
 // rows split between the two tensor memories, its B tile between the two shared
 // memories), tiles taken in turn from a grouped order.  Warp 0 copies, warp 1 of the
-// even CTA issues the products, warps 4..11 end the previous tile out of the other
+// even CTA issues the products, warps 4..19 end the previous tile out of the other
 // half of the tensor memory meanwhile.
 struct PairParams {
     CUtensorMap map_a, map_b;
@@ -182,9 +338,9 @@ struct PairParams {
 };
 
 constexpr int kStageBytes = 32768;      // 128 rows of A and 128 of B, 64 reduced elements each
-constexpr int kPairStages = 6;
-constexpr int kPairThreads = 384;
-constexpr int kEndWarps = 8;
+constexpr int kPairStages = 5;
+constexpr int kEndWarps = 16;
+constexpr int kPairThreads = 128 + 32 * kEndWarps;
 constexpr int kChunkBytes = 4096;       // 32 x 32 fp32
 constexpr int kPairSmem = 1024 + kPairStages * kStageBytes + kEndWarps * kChunkBytes + 256;
 constexpr int kRasterRows = 8;          // row tiles that are gone through together
@@ -199,6 +355,13 @@ __device__ __forceinline__ void tile_place(const PairParams& p, int t, int* tm, 
 __device__ __forceinline__ int tile_width(const PairParams& p, int tn) {   // columns of the tile, up to a multiple of 32
     const int64_t left = p.cols - (int64_t)tn * p.bn;
     return left >= p.bn ? p.bn : (int)((left + 31) / 32 * 32);
+}
+
+// A warp of either CTA is done reading an accumulator: one arrival at the even CTA.
+__device__ __forceinline__ void release(uint64_t* bar) {
+    tcgen05_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) peer_arrive(peer_addr(smem_addr(bar), 0));
 }
 
 template <bool kF32>
@@ -321,60 +484,49 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
             int tm, tn;
             tile_place(p, t, &tm, &tn);
             const int buf = n_tile & 1, width = tile_width(p, tn);
-            if (!warp_wait(acc_full + buf, (n_tile / 2) & 1)) break;
-            tcgen05_fence_after();
             const int64_t row0 = (int64_t)tm * 256 + rank * 128 + q * 32, col_tile = (int64_t)tn * p.bn;
             const int n_chunks = width / 32;
-            for (int c = h; c < n_chunks; c += 2) {
+            if ((p.e.add || p.e.slope) && row0 + lane < p.rows)   // on their way to L2 while the product runs
+                for (int c = h; c < n_chunks; c += kEndWarps / 4) {
+                    const int64_t col = col_tile + c * 32;
+                    if (col >= p.cols) break;
+                    if (p.e.add) l2_prefetch(static_cast<const char*>(p.e.add) + ((row0 + lane) * p.e.ld_add + col) * (kF32 ? 4 : 2));
+                    if (p.e.slope) l2_prefetch(p.e.slope + (row0 + lane) * p.e.ld_slope + col);
+                }
+            if (!warp_wait(acc_full + buf, (n_tile / 2) & 1)) break;
+            tcgen05_fence_after();
+            for (int c = h; c < n_chunks; c += kEndWarps / 4) {
                 const int64_t col0 = col_tile + c * 32;
                 const bool vec = p.e.vec && col0 + 32 <= p.cols;
-                const int64_t col = col0 + (lane & 3) * 8;
-                Sides<kF32> sides[4];
-                float bias[8];
+                const uint32_t taddr = tmem + buf * 256 + c * 32 + ((uint32_t)(q * 32) << 16);
+                const bool last = c + kEndWarps / 4 >= n_chunks;   // this warp's last read of the buffer
                 if (vec) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t row = row0 + i * 8 + (lane >> 2);
-                        if (row < p.rows) load_sides<kF32>(p.e, row, col, &sides[i]);
-                    }
-                    load_bias8(p.e, col, bias);
-                }
-                uint32_t acc[32];
-                tmem_load32(tmem + buf * 256 + c * 32 + ((uint32_t)(q * 32) << 16), acc);
-                if (c + 2 >= n_chunks) {   // this warp's last read of the buffer
-                    tcgen05_fence_before();
-                    __syncwarp();
-                    if (lane == 0) peer_arrive(peer_addr(smem_addr(acc_empty + buf), 0));
-                }
-                __syncwarp();   // the chunk's previous readers are done
-#pragma unroll
-                for (int g = 0; g < 8; ++g)
-                    *reinterpret_cast<uint4*>(chunk + group_place(lane, g)) = make_uint4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
-                __syncwarp();
-                if (vec) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + (lane >> 2);
-                        if (row0 + r < p.rows) {
-                            const float4 a = *reinterpret_cast<const float4*>(chunk + group_place(r, 2 * (lane & 3)));
-                            const float4 b = *reinterpret_cast<const float4*>(chunk + group_place(r, 2 * (lane & 3) + 1));
-                            float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                            end_vector<kF32>(p.e, step, row0 + r, col, bias, sides[i], v);
-                        }
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        FragmentEnd<kF32> end;
+                        const int64_t row = row0 + 16 * i + (lane >> 2);
+                        float v[4][4];
+                        end.load(p.e, row, col0, p.rows);
+                        tmem_load_fragment(taddr + ((uint32_t)(16 * i) << 16), v);
+                        if (last && i) release(acc_empty + buf);
+                        end.finish(p.e, step, row, col0, v);
                     }
                 } else {
+                    uint32_t acc[32];
+                    tmem_load32(taddr, acc);
+                    if (last) release(acc_empty + buf);
+                    __syncwarp();   // the chunk's previous readers are done
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        *reinterpret_cast<uint4*>(chunk + group_place(lane, g)) = make_uint4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
+                    __syncwarp();
                     for (int i = 0; i < 4; ++i)
                         end_rows<kF32>(p.e, step, row0 + i * 8, col0, p.rows, p.cols, [&](int r) {
                             return *reinterpret_cast<const float*>(chunk + group_place(i * 8 + r, lane >> 2) + (lane & 3) * 4);
                         });
                 }
             }
-            // a warp without a chunk of this tile (a narrow last tile) still frees the buffer
-            if (h >= n_chunks) {
-                tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0) peer_arrive(peer_addr(smem_addr(acc_empty + buf), 0));
-            }
+            if (h >= n_chunks) release(acc_empty + buf);   // a narrow last tile: no chunk for this warp
         }
     }
     tcgen05_fence_before();
@@ -562,19 +714,17 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
                 const int r = r0 + (lane >> 2);
                 const int64_t row = row_tile + (rb / 4) * 32 + r, col = col0 + (lane & 3) * 8;
                 if (row < p.rows) {
-                    Sides<kF32> sides;
-                    float bias[8];
-                    load_sides<kF32>(p.e, row, col, &sides);
-                    load_bias8(p.e, col, bias);
-                    float v[8] = {};
+                    VectorEnd<kF32, 1> end;
+                    end.load(p.e, row, col, p.rows);
+                    float v[1][8] = {};
                     const uint32_t g0 = group_place(r, 2 * (lane & 3)), g1 = group_place(r, 2 * (lane & 3) + 1);
                     for (int i = 0; i < parts; ++i) {
                         const uint32_t at = peer_addr(chunk, i);
                         const float4 x = peer_load(at + g0), y = peer_load(at + g1);
-                        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-                        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+                        v[0][0] += x.x; v[0][1] += x.y; v[0][2] += x.z; v[0][3] += x.w;
+                        v[0][4] += y.x; v[0][5] += y.y; v[0][6] += y.z; v[0][7] += y.w;
                     }
-                    end_vector<kF32>(p.e, step, row, col, bias, sides, v);
+                    end.finish(p.e, step, row, col, v);
                 }
             } else {
                 end_rows<kF32>(p.e, step, row0, col0, p.rows, p.cols, [&](int r) {
