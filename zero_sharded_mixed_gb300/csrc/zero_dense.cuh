@@ -20,8 +20,9 @@ namespace zgb {
 struct DropParams {
     uint32_t cut;               // keep where bits >= cut; 0 = no dropout, 65536 = drop everything
     float scale;                // 65536 / (65536 - cut), 0 where everything is dropped
-    uint32_t key0, key1, site, step;
+    uint32_t site, step;
     const uint64_t* step_ptr;   // null, or added to step
+    uint32_t key[10][2];        // of each round, formed on the host
 };
 
 __device__ __forceinline__ uint32_t drop_step(const DropParams& d) {
@@ -30,17 +31,14 @@ __device__ __forceinline__ uint32_t drop_step(const DropParams& d) {
 
 __device__ __forceinline__ uint4 philox_block(const DropParams& d, uint32_t step, uint32_t row, uint32_t col_block) {
     uint32_t c0 = col_block, c1 = row, c2 = d.site, c3 = step;
-    uint32_t k0 = d.key0, k1 = d.key1;
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u;
         const uint64_t p1 = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ d.key[r][0];
         c1 = (uint32_t)p1;
-        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ d.key[r][1];
         c3 = (uint32_t)p0;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     return make_uint4(c0, c1, c2, c3);
 }

@@ -14,7 +14,8 @@
 namespace zgb {
 
 int drop_params(const zero_dropout_t* d, int64_t rows, int64_t cols, DropParams* out) {
-    *out = DropParams{0u, 1.0f, 0u, 0u, 0u, 0u, nullptr};
+    *out = DropParams{};
+    out->scale = 1.0f;
     if (!d) return ZERO_OK;
     if (!(d->p >= 0.0 && d->p <= 1.0)) return ZERO_EINVAL;
     if (d->reserved != 0) return ZERO_EINVAL;
@@ -27,8 +28,10 @@ int drop_params(const zero_dropout_t* d, int64_t rows, int64_t cols, DropParams*
     // the counter holds 32 bits of the row and 32 of the group of eight columns
     if (rows > (int64_t)1 << 32 || cols > (int64_t)1 << 35) return ZERO_ERANGE;
     out->scale = out->cut < 65536u ? (float)(65536.0 / (65536.0 - out->cut)) : 0.0f;
-    out->key0 = (uint32_t)d->seed;
-    out->key1 = (uint32_t)(d->seed >> 32);
+    for (uint32_t r = 0; r < 10; ++r) {   // the key grows by a constant a round
+        out->key[r][0] = (uint32_t)d->seed + r * 0x9E3779B9u;
+        out->key[r][1] = (uint32_t)(d->seed >> 32) + r * 0xBB67AE85u;
+    }
     out->site = d->site;
     out->step = (uint32_t)d->step;
     out->step_ptr = d->step_ptr;
@@ -49,10 +52,10 @@ struct DropoutParams {
 // Whole, aligned rows: one thread takes eight columns at a time, kBatch groups of
 // loads in flight, over the matrix in steps of the grid (row and column carried
 // along, without a division a step).
-constexpr int kBatch = 4;
+constexpr int kBatch = 2;
 
 template <bool kGrad, bool kF32>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
+__global__ void __launch_bounds__(kThreads, 4) dropout_kernel(const DropoutParams p) {
     const int64_t stride = (int64_t)gridDim.x * kThreads;
     const int64_t step_rows = stride / p.col_blocks, step_cols = stride - step_rows * p.col_blocks;
     const uint32_t step = p.drop.cut ? drop_step(p.drop) : 0u;
@@ -97,11 +100,41 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
     }
 }
 
+template <class T>
+__device__ __forceinline__ void load_column_of(const T* q, int64_t ld, int n, float* v) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r, q += ld) {
+        if constexpr (sizeof(T) == 4)
+            v[r] = r < n ? *q : 0.0f;
+        else
+            v[r] = r < n ? bf16_one(*q) : 0.0f;
+    }
+}
+__device__ __forceinline__ void load_column(const void* p, bool f32, int64_t row, int64_t ld, int64_t col, int n, float* v) {
+    if (f32)
+        load_column_of(static_cast<const float*>(p) + row * ld + col, ld, n, v);
+    else
+        load_column_of(static_cast<const uint16_t*>(p) + row * ld + col, ld, n, v);
+}
+__device__ __forceinline__ void store_column(void* p, bool f32, int64_t row, int64_t ld, int64_t col, int n, const float* v) {
+    if (f32) {
+        float* q = static_cast<float*>(p) + row * ld + col;
+#pragma unroll
+        for (int r = 0; r < 8; ++r, q += ld)
+            if (r < n) *q = v[r];
+    } else {
+        uint16_t* q = static_cast<uint16_t*>(p) + row * ld + col;
+#pragma unroll
+        for (int r = 0; r < 8; ++r, q += ld)
+            if (r < n) *q = to_bf16(v[r]);
+    }
+}
+
 // With column sums, or rows that are not aligned: a CTA takes a strip of 64
 // columns over a share of the rows.  Aligned (kVec): 8 threads a row, 32 rows at a
 // time.  Otherwise a warp takes 8 rows x 32 columns, a lane a column, so that a
 // row's accesses fall together; each lane forms the random bits of one row and
-// column group and the lanes of that group fetch them from it.
+// column group and leaves them in shared memory for the lanes of that group.
 // Sums (kSums): the shares of a strip are the CTAs of a cluster.  Each thread sums
 // its rows in order, the CTA its threads, then the cluster its CTAs, every time in
 // the same order.
@@ -111,6 +144,7 @@ template <bool kGrad, bool kVec, bool kSums>
 __global__ void __launch_bounds__(kThreads) dropout_strip_kernel(const DropoutParams p, int shares) {
     __shared__ float part[kThreads / 8][kStrip + 1];
     __shared__ float total[kStrip];
+    __shared__ uint4 bits[kVec ? 1 : kThreads / 32][8][4];   // a warp's part: row, column group
     const int share = blockIdx.x % shares;
     const int64_t col0 = (int64_t)(blockIdx.x / shares) * kStrip;
     const int64_t row_a = p.rows / shares * share + (p.rows % shares) * share / shares;
@@ -150,35 +184,29 @@ __global__ void __launch_bounds__(kThreads) dropout_strip_kernel(const DropoutPa
         const int64_t col = col0 + (warp & 1) * 32 + lane;
         float sum = 0.0f;
         for (int64_t row0 = row_a + (warp >> 1) * 8; row0 < row_b; row0 += kThreads / 8) {
+            // rows of the part that exist, none where the column does not
+            const int n = col < p.cols ? (row_b - row0 < 8 ? (int)(row_b - row0) : 8) : 0;
             float v[8], t[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const bool in = row0 + r < row_b && col < p.cols;
-                const int64_t at = (row0 + r) * p.ldx + col, side_at = (row0 + r) * p.lds + col;
-                v[r] = !in ? 0.0f : p.x_f32 ? static_cast<const float*>(p.x)[at] : bf16_one(static_cast<const uint16_t*>(p.x)[at]);
-                t[r] = !in || !p.side ? 0.0f
-                       : p.side_f32   ? static_cast<const float*>(p.side)[side_at]
-                                      : bf16_one(static_cast<const uint16_t*>(p.side)[side_at]);
-            }
+            load_column(p.x, p.x_f32, row0, p.ldx, col, n, v);
+            if (p.side) load_column(p.side, p.side_f32, row0, p.lds, col, n, t);
             if (kGrad && p.side) slope_apply<8>(p.act, t, v);
-            uint4 block = make_uint4(0u, 0u, 0u, 0u);
-            if (p.drop.cut)
-                block = philox_block(p.drop, step, (uint32_t)(row0 + (lane & 7)),
-                                     (uint32_t)((col0 >> 3) + (warp & 1) * 4 + (lane >> 3)));
+            if (p.drop.cut) {
+                __syncwarp();
+                bits[warp][lane & 7][lane >> 3] =
+                    philox_block(p.drop, step, (uint32_t)(row0 + (lane & 7)), (uint32_t)((col0 >> 3) + (warp & 1) * 4 + (lane >> 3)));
+                __syncwarp();
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                if (p.drop.cut) v[r] = row_bits(block, r) >= p.drop.cut ? v[r] * p.drop.scale : 0.0f;
-                if (!kGrad) v[r] += t[r];
-                if (row0 + r < row_b && col < p.cols) {
-                    if (p.y) {
-                        const int64_t at = (row0 + r) * p.ldy + col;
-                        if (p.y_f32)
-                            static_cast<float*>(p.y)[at] = v[r];
-                        else
-                            static_cast<uint16_t*>(p.y)[at] = to_bf16(v[r]);
-                    }
-                    if constexpr (kSums) sum += v[r];
-                }
+                for (int r = 0; r < 8; ++r)
+                    v[r] = reinterpret_cast<const uint16_t*>(bits[warp][r])[lane] >= p.drop.cut ? v[r] * p.drop.scale : 0.0f;
+            }
+            if (!kGrad && p.side) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v[r] += t[r];
+            }
+            if (p.y) store_column(p.y, p.y_f32, row0, p.ldy, col, n, v);
+            if constexpr (kSums) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) sum += r < n ? v[r] : 0.0f;
             }
         }
         if constexpr (kSums) part[warp >> 1][(warp & 1) * 32 + lane] = sum;
@@ -237,7 +265,7 @@ static int launch_dropout(DropoutParams& p, cudaStream_t s) {
     }
     const void* kernel = p.x_f32 ? (const void*)dropout_kernel<kGrad, true> : (const void*)dropout_kernel<kGrad, false>;
     const int64_t resident = (int64_t)sm_count() * ctas_per_sm(kernel, kThreads, 0);
-    const unsigned grid = grid_for(p.rows * p.col_blocks, kThreads * kBatch, resident * 2);
+    const unsigned grid = grid_for(p.rows * p.col_blocks, kThreads * kBatch, resident * 8);
     if (p.x_f32)
         dropout_kernel<kGrad, true><<<grid, kThreads, 0, s>>>(p);
     else

@@ -12,6 +12,7 @@
 // an angle is off by at most position * 2^-65 turns (and theta's own 53 bits)
 // plus the fp32 rounding of the reduced angle.  No table of sines is read.
 #include <cmath>
+#include <type_traits>
 
 #include "zero_dense.cuh"
 
@@ -26,10 +27,15 @@ struct RopeParams {
     bool copy_rest;
     float sin_sign;
     int32_t cta_tokens, cta_heads;   // what one CTA takes
+    int32_t per_head;                // work items of a head
+    uint32_t by_head, by_heads;      // ceil(2^32 / per_head), ceil(2^32 / cta_heads)
     zero_rope_plan_t plan;
 };
 
-constexpr int kRopeItems = 2048;   // work items of a CTA, eight a thread
+#ifndef ZGB_ROPE_ITEMS
+#define ZGB_ROPE_ITEMS 2048   // work items of a CTA, eight a thread
+#endif
+constexpr int kRopeItems = ZGB_ROPE_ITEMS;
 
 template <bool kF32>
 __device__ __forceinline__ float rope_load(const void* p, int64_t i) {
@@ -68,14 +74,21 @@ __device__ __forceinline__ void turn_pair(float2 c, float& first, float& second)
     second = __fmaf_rn(o, c.x, __fmul_rn(f, c.y));
 }
 
+// n / d for n * d < 2^32, from m = ceil(2^32 / d); d = 1 has no such m.
+__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t m) { return m ? __umulhi(n, m) : n; }
+
 // A CTA takes cta_tokens tokens of cta_heads heads: it forms the sines of those
 // tokens' pairs once in shared memory (one a thread or so), then turns the heads.
 // kVec: two 16-byte vectors an item, which hold kCount whole pairs (a's and b's in
-// the half layout, neighbours in the interleaved one); else a pair an item.
+// the half layout, neighbours in the interleaved one) or up to two of the vectors
+// that are copied; else a pair an item, or up to two copied elements.
 template <bool kF32, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 turn[kThreads > ZERO_ROPE_MAX / 2 ? kThreads : ZERO_ROPE_MAX / 2];   // [cta_tokens][pairs]
-    const int pairs = p.plan.rot / 2;
+    using V = RopeVector<kF32>;
+    using T = typename std::conditional<kF32, float, uint16_t>::type;
+    constexpr int kBatch = 4, kCount = kVec ? V::kCount : 1;
+    const int pairs = p.plan.rot / 2, turned = pairs / kCount, rest = (int)((p.dim - p.plan.rot) / kCount);
     const int64_t t0 = (int64_t)blockIdx.x * p.cta_tokens, h0 = (int64_t)blockIdx.y * p.cta_heads;
     const int nt = (int)(p.tokens - t0 < p.cta_tokens ? p.tokens - t0 : p.cta_tokens);
     const int nh = (int)(p.heads - h0 < p.cta_heads ? p.heads - h0 : p.cta_heads);
@@ -88,74 +101,67 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         turn[j] = make_float2(cs * p.plan.scale, sn * p.plan.scale * p.sin_sign);
     }
     __syncthreads();
-    if constexpr (kVec) {
-        using V = RopeVector<kF32>;
-        constexpr int kBatch = 4, size = kF32 ? 4 : 2;
-        const int per_head = pairs / V::kCount, items = nt * nh * per_head;
-        for (int j0 = threadIdx.x; j0 < items; j0 += kBatch * kThreads) {
-            uint4 a[kBatch], b[kBatch];
-            char* out[kBatch];
-            const float2* cs[kBatch];
-            const int second = (kHalf ? pairs : V::kCount) * size;
+    const int items = nt * p.cta_heads * p.per_head;   // those of heads past the last do nothing
+    for (int j0 = threadIdx.x; j0 < items; j0 += kBatch * kThreads) {
+        typename std::conditional<kVec, uint4, float>::type a[kBatch], b[kBatch];
+        T* out[kBatch];
+        const float2* cs[kBatch];
+        int second[kBatch];   // elements from an item's first to its second; 0: no second; -1: no item
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int j = j0 + k * kThreads;
-                if (j < items) {
-                    const int th = j / per_head, i = j - th * per_head, t = th / nh, h = th - t * nh;
-                    const int64_t in_head = (int64_t)i * V::kCount * (kHalf ? 1 : 2);
-                    const char* q = static_cast<const char*>(p.x) + ((t0 + t) * p.xt + (h0 + h) * p.xh + in_head) * size;
+        for (int k = 0; k < kBatch; ++k) {
+            const uint32_t j = j0 + k * kThreads, th = divide(j, p.by_head), i = j - th * p.per_head;
+            const uint32_t t = divide(th, p.by_heads), h = th - t * p.cta_heads;
+            second[k] = -1;
+            if ((int)j < items && (int)h < nh) {
+                const bool turns = (int)i < turned;
+                const int left = rest - 2 * ((int)i - turned);   // copied vectors from this item on
+                const int64_t in_head = turns ? (int64_t)i * kCount * (kHalf ? 1 : 2) : p.plan.rot + (int64_t)(i - turned) * 2 * kCount;
+                second[k] = turns ? (kHalf ? pairs : kCount) : left > 1 ? kCount : 0;
+                const T* q = static_cast<const T*>(p.x) + (t0 + t) * p.xt + (h0 + h) * p.xh + in_head;
+                out[k] = static_cast<T*>(p.y) + (t0 + t) * p.yt + (h0 + h) * p.yh + in_head;
+                cs[k] = turns ? turn + t * pairs + i * kCount : nullptr;
+                if constexpr (kVec) {
                     a[k] = ld_stream_u4(q);
-                    b[k] = ld_stream_u4(q + second);
-                    out[k] = static_cast<char*>(p.y) + ((t0 + t) * p.yt + (h0 + h) * p.yh + in_head) * size;
-                    cs[k] = turn + t * pairs + i * V::kCount;
+                    if (second[k]) b[k] = ld_stream_u4(q + second[k]);
+                } else {
+                    a[k] = rope_load<kF32>(q, 0);
+                    if (second[k]) b[k] = rope_load<kF32>(q, second[k]);
                 }
             }
+        }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (j0 + k * kThreads < items) {
-                    float u[V::kCount], v[V::kCount];
+        for (int k = 0; k < kBatch; ++k) {
+            if (second[k] < 0) continue;
+            if (cs[k]) {
+                if constexpr (kVec) {
+                    float u[kCount], v[kCount];
                     V::open(a[k], u);
                     V::open(b[k], v);
 #pragma unroll
-                    for (int i = 0; i < V::kCount; ++i) {
-                        const float2 c = cs[k][i];
+                    for (int i = 0; i < kCount; ++i) {
                         // the pair's two elements: one of each vector, or neighbours of one
-                        float& first = kHalf ? u[i] : i < V::kCount / 2 ? u[2 * i] : v[2 * i - V::kCount];
-                        float& other = kHalf ? v[i] : i < V::kCount / 2 ? u[2 * i + 1] : v[2 * i + 1 - V::kCount];
-                        turn_pair(c, first, other);
+                        float& first = kHalf ? u[i] : i < kCount / 2 ? u[2 * i] : v[2 * i - kCount];
+                        float& other = kHalf ? v[i] : i < kCount / 2 ? u[2 * i + 1] : v[2 * i + 1 - kCount];
+                        turn_pair(cs[k][i], first, other);
                     }
-                    st_stream_u4(out[k], V::close(u));
-                    st_stream_u4(out[k] + second, V::close(v));
+                    a[k] = V::close(u);
+                    b[k] = V::close(v);
+                } else {
+                    turn_pair(cs[k][0], a[k], b[k]);
                 }
             }
-        }
-        if (p.copy_rest) {
-            const int rest = (int)((p.dim - p.plan.rot) / V::kCount);
-            for (int64_t j = threadIdx.x; j < (int64_t)nt * nh * rest; j += kThreads) {
-                const int64_t th = j / rest, t = th / nh, h = th - t * nh, in_head = p.plan.rot + (j - th * rest) * V::kCount;
-                st_stream_u4(static_cast<char*>(p.y) + ((t0 + t) * p.yt + (h0 + h) * p.yh + in_head) * size,
-                             ld_stream_u4(static_cast<const char*>(p.x) + ((t0 + t) * p.xt + (h0 + h) * p.xh + in_head) * size));
-            }
-        }
-    } else {
-        for (int j = threadIdx.x; j < nt * nh * pairs; j += kThreads) {
-            const int th = j / pairs, i = j - th * pairs, t = th / nh, h = th - t * nh;
-            const int64_t ia = kHalf ? i : 2 * i, ib = kHalf ? i + pairs : 2 * i + 1;
-            const int64_t xb = (t0 + t) * p.xt + (h0 + h) * p.xh, yb = (t0 + t) * p.yt + (h0 + h) * p.yh;
-            float a = rope_load<kF32>(p.x, xb + ia), b = rope_load<kF32>(p.x, xb + ib);
-            turn_pair(turn[t * pairs + i], a, b);
-            rope_store<kF32>(p.y, yb + ia, a);
-            rope_store<kF32>(p.y, yb + ib, b);
-        }
-        if (p.copy_rest) {
-            const int64_t rest = p.dim - p.plan.rot;
-            for (int64_t j = threadIdx.x; j < nt * nh * rest; j += kThreads) {
-                const int64_t th = j / rest, i = j - th * rest + p.plan.rot, t = th / nh, h = th - t * nh;
-                rope_store<kF32>(p.y, (t0 + t) * p.yt + (h0 + h) * p.yh + i, rope_load<kF32>(p.x, (t0 + t) * p.xt + (h0 + h) * p.xh + i));
+            if constexpr (kVec) {
+                st_stream_u4(out[k], a[k]);
+                if (second[k]) st_stream_u4(out[k] + second[k], b[k]);
+            } else {
+                rope_store<kF32>(out[k], 0, a[k]);
+                if (second[k]) rope_store<kF32>(out[k], second[k], b[k]);
             }
         }
     }
 }
+
+static uint32_t reciprocal(int32_t d) { return d == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); }
 
 template <bool kF32, bool kHalf>
 static int launch_rope(RopeParams& p, cudaStream_t s) {
@@ -163,11 +169,19 @@ static int launch_rope(RopeParams& p, cudaStream_t s) {
     const int pairs = p.plan.rot / 2;
     const bool vec = pairs % count == 0 && p.dim % count == 0 && aligned16(p.x) && aligned16(p.y) && p.xt % count == 0 &&
                      p.xh % count == 0 && p.yt % count == 0 && p.yh % count == 0;
-    const int per_head = vec ? pairs / count : pairs;
-    const int64_t tokens = kThreads / pairs > 1 ? kThreads / pairs : 1;
-    p.cta_tokens = (int32_t)(tokens < p.tokens ? tokens : p.tokens);
-    const int64_t heads = kRopeItems / (p.cta_tokens * per_head);
-    p.cta_heads = (int32_t)(heads < 1 ? 1 : heads < p.heads ? heads : p.heads);
+    const int64_t unit = vec ? count : 1, rest = p.copy_rest ? (p.dim - p.plan.rot) / unit : 0;
+    const int64_t per_head = pairs / unit + (rest + 1) / 2;
+    if (per_head > kRopeItems * 8) return ZERO_ERANGE;   // a head of more than 2^15 elements
+    p.per_head = (int32_t)per_head;
+    const int64_t tokens = kThreads / pairs > 1 ? kThreads / pairs : 1;   // a sine a thread
+    int64_t share = kRopeItems / per_head;                                // heads of a CTA, over its tokens
+    share = share < 1 ? 1 : share;
+    p.cta_tokens = (int32_t)(tokens < share ? tokens : share);
+    if (p.cta_tokens > p.tokens) p.cta_tokens = (int32_t)p.tokens;
+    const int64_t heads = share / p.cta_tokens;
+    p.cta_heads = (int32_t)(heads < p.heads ? heads : p.heads);
+    p.by_head = reciprocal(p.per_head);
+    p.by_heads = reciprocal(p.cta_heads);
     const int64_t gx = (p.tokens + p.cta_tokens - 1) / p.cta_tokens, gy = (p.heads + p.cta_heads - 1) / p.cta_heads;
     if (gx > INT32_MAX || gy > 65535) return ZERO_ERANGE;
     const dim3 grid((unsigned)gx, (unsigned)gy);
