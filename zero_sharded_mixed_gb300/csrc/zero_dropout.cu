@@ -49,53 +49,62 @@ struct DropoutParams {
     DropParams drop;
 };
 
-// Whole, aligned rows: one thread takes eight columns at a time, kBatch groups of
-// loads in flight, over the matrix in steps of the grid (row and column carried
-// along, without a division a step).
-constexpr int kBatch = 2;
+// Whole, aligned rows: a thread keeps its eight columns and goes down the rows,
+// four of them (two of fp32) in flight, so that addresses are additions and the
+// first products of its random numbers, which see the column and constants alone,
+// are formed once.  A warp takes `lanes` neighbouring column groups of 32 / lanes
+// rows; warps with neighbouring numbers take neighbouring columns, and one wave of
+// CTAs goes through the matrix together.  Bound by memory with the random numbers
+// close behind: 8192 x 1600 bf16 with a residual in 16.1 us (4.9 TB/s, caches and
+// launch included), 65536 x 1600 in 105 us (6.0 TB/s; 98 us without the random
+// numbers).  One vector a thread and many waves: 23 and 169 us; more rows in flight
+// cost residency: 25 and 182 us.
+template <bool kF32>
+constexpr int kBatchOf = kF32 ? 2 : 4;
 
 template <bool kGrad, bool kF32>
-__global__ void __launch_bounds__(kThreads, 4) dropout_kernel(const DropoutParams p) {
-    const int64_t stride = (int64_t)gridDim.x * kThreads;
-    const int64_t step_rows = stride / p.col_blocks, step_cols = stride - step_rows * p.col_blocks;
+__global__ void __launch_bounds__(kThreads, 3) dropout_kernel(const DropoutParams p, int lanes, int col_warps, int64_t row_step) {
+    await_predecessor();
+    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t rg = w / col_warps, cb = (w - rg * col_warps) * lanes + lane % lanes;
+    int64_t row = rg * (32 / lanes) + lane / lanes;
+    if (cb >= p.col_blocks || rg * (32 / lanes) >= row_step) return;   // the last CTA may hold a warp too many
     const uint32_t step = p.drop.cut ? drop_step(p.drop) : 0u;
-    constexpr int xs = kF32 ? 4 : 2;
-    int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    int64_t row = i / p.col_blocks, cb = i - row * p.col_blocks;
-    while (row < p.rows) {
-        int64_t r[kBatch], c[kBatch];
-        uint4 x[kBatch][kF32 ? 2 : 1], side[kBatch][kF32 && !kGrad ? 2 : 1];
+    constexpr int kBatch = kBatchOf<kF32>, xs = kF32 ? 4 : 2, ss = kGrad ? 2 : xs;
+    const int ys = p.y_f32 ? 4 : 2;
+    const char* x = static_cast<const char*>(p.x) + (row * p.ldx + cb * 8) * xs;
+    const char* side = p.side ? static_cast<const char*>(p.side) + (row * p.lds + cb * 8) * ss : nullptr;
+    char* y = static_cast<char*>(p.y) + (row * p.ldy + cb * 8) * ys;
+    const int64_t dx = row_step * p.ldx * xs, ds = row_step * p.lds * ss, dy = row_step * p.ldy * ys;
+    for (; row < p.rows; row += kBatch * row_step) {
+        uint4 xv[kBatch][kF32 ? 2 : 1], sv[kBatch][kF32 && !kGrad ? 2 : 1];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            r[j] = row;
-            c[j] = cb;
-            if (row < p.rows) {
-                const char* q = static_cast<const char*>(p.x) + (row * p.ldx + cb * 8) * xs;
-                x[j][0] = ld_stream_u4(q);
-                if constexpr (kF32) x[j][1] = ld_stream_u4(q + 16);
-                if (p.side) {
-                    const char* t = static_cast<const char*>(p.side) + (row * p.lds + cb * 8) * (kGrad ? 2 : xs);
-                    side[j][0] = ld_stream_u4(t);
-                    if constexpr (kF32 && !kGrad) side[j][1] = ld_stream_u4(t + 16);
+            if (row + j * row_step < p.rows) {
+                xv[j][0] = ld_stream_u4(x);
+                if constexpr (kF32) xv[j][1] = ld_stream_u4(x + 16);
+                if (side) {
+                    sv[j][0] = ld_stream_u4(side);
+                    if constexpr (kF32 && !kGrad) sv[j][1] = ld_stream_u4(side + 16);
                 }
             }
-            row += step_rows;
-            cb += step_cols;
-            if (cb >= p.col_blocks) cb -= p.col_blocks, ++row;
+            x += dx;
+            side += side ? ds : 0;
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (r[j] >= p.rows) break;
+        for (int j = 0; j < kBatch; ++j, y += dy) {
+            if (row + j * row_step >= p.rows) break;
             float v[8], t[8];
-            raw8<kF32>(x[j], v);
-            if (p.side) raw8<kF32 && !kGrad>(side[j], t);
-            if (kGrad && p.side) slope_apply<8>(p.act, t, v);
-            if (p.drop.cut) drop8(p.drop, step, r[j], c[j], v);
-            if (!kGrad && p.side) {
+            raw8<kF32>(xv[j], v);
+            if (side) raw8<kF32 && !kGrad>(sv[j], t);
+            if (kGrad && side) slope_apply<8>(p.act, t, v);
+            if (p.drop.cut) drop8(p.drop, step, row + j * row_step, cb, v);
+            if (!kGrad && side) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] += t[k];
             }
-            store8(static_cast<char*>(p.y) + (r[j] * p.ldy + c[j] * 8) * (p.y_f32 ? 4 : 2), p.y_f32, true, 8, v);
+            store8(y, p.y_f32, true, 8, v);
         }
     }
 }
@@ -145,6 +154,7 @@ __global__ void __launch_bounds__(kThreads) dropout_strip_kernel(const DropoutPa
     __shared__ float part[kThreads / 8][kStrip + 1];
     __shared__ float total[kStrip];
     __shared__ uint4 bits[kVec ? 1 : kThreads / 32][8][4];   // a warp's part: row, column group
+    await_predecessor();
     const int share = blockIdx.x % shares;
     const int64_t col0 = (int64_t)(blockIdx.x / shares) * kStrip;
     const int64_t row_a = p.rows / shares * share + (p.rows % shares) * share / shares;
@@ -242,8 +252,8 @@ template <bool kVec>
 static int launch_sums(const DropoutParams& p, cudaStream_t s) {
     const int64_t strips = (p.cols + kStrip - 1) / kStrip;
     if (strips > INT32_MAX / kShares) return ZERO_ERANGE;
-    return launch_cluster(dropout_strip_kernel<true, kVec, true>, (unsigned)(strips * kShares), kThreads, kShares, 0, s, p,
-                          (int)kShares);
+    return launch_dense(dropout_strip_kernel<true, kVec, true>, dim3((unsigned)(strips * kShares)), kThreads, kShares, 0, s, p,
+                        (int)kShares);
 }
 
 template <bool kGrad>
@@ -260,17 +270,24 @@ static int launch_dropout(DropoutParams& p, cudaStream_t s) {
         int64_t shares = (int64_t)sm_count() * 32 / strips;
         shares = shares < 1 ? 1 : shares > most ? most : shares;
         if (strips > INT32_MAX / shares) return ZERO_ERANGE;
-        dropout_strip_kernel<kGrad, false, false><<<(unsigned)(strips * shares), kThreads, 0, s>>>(p, (int)shares);
-        return launch_status();
+        return launch_dense(dropout_strip_kernel<kGrad, false, false>, dim3((unsigned)(strips * shares)), kThreads, 1, 0, s, p,
+                            (int)shares);
     }
-    const void* kernel = p.x_f32 ? (const void*)dropout_kernel<kGrad, true> : (const void*)dropout_kernel<kGrad, false>;
-    const int64_t resident = (int64_t)sm_count() * ctas_per_sm(kernel, kThreads, 0);
-    const unsigned grid = grid_for(p.rows * p.col_blocks, kThreads * kBatch, resident * 8);
-    if (p.x_f32)
-        dropout_kernel<kGrad, true><<<grid, kThreads, 0, s>>>(p);
-    else
-        dropout_kernel<kGrad, false><<<grid, kThreads, 0, s>>>(p);
-    return launch_status();
+    // lanes of a warp along a row, and as many groups of rows as give every thread a
+    // batch, up to the warps that are resident at once
+    void (*kernel)(DropoutParams, int, int, int64_t) = p.x_f32 ? dropout_kernel<kGrad, true> : dropout_kernel<kGrad, false>;
+    const int kBatch = p.x_f32 ? kBatchOf<true> : kBatchOf<false>;
+    int lanes = 32;
+    while (lanes / 2 >= p.col_blocks) lanes /= 2;
+    const int64_t col_warps = (p.col_blocks + lanes - 1) / lanes, rows_of_warp = 32 / lanes;
+    if (col_warps > INT32_MAX) return ZERO_ERANGE;
+    const int64_t groups = (p.rows + rows_of_warp * kBatch - 1) / (rows_of_warp * kBatch);
+    int64_t row_groups = (int64_t)sm_count() * ctas_per_sm((const void*)kernel, kThreads, 0) * (kThreads / 32) / col_warps;
+    row_groups = row_groups < 1 ? 1 : row_groups > groups ? groups : row_groups;
+    const int64_t grid = (row_groups * col_warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (grid > INT32_MAX) return ZERO_ERANGE;
+    const int64_t row_step = row_groups * rows_of_warp;
+    return launch_dense(kernel, dim3((unsigned)grid), kThreads, 1, 0, s, p, lanes, (int)col_warps, row_step);
 }
 
 int launch_column_sum(int64_t rows, int64_t cols, const uint16_t* dz, int64_t lddz, const void* db_acc, void* db,

@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
     __syncthreads();
     cluster_sync();
     tcgen05_fence_after();
+    await_predecessor();
     const uint32_t tmem = *tmem_slot;
 
     const int half = p.bn / 2;
@@ -603,6 +604,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
+    await_predecessor();
     const uint32_t tmem = *tmem_slot;
 
     // sub-tile rows of a stage: tile rows (K-major), or 64 for every 64 columns
@@ -813,7 +815,7 @@ static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
     q.e = e;
     if (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
     const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
-    return launch_cluster(kernel, (unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, 2, kPairSmem, s, q);
+    return launch_dense(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, 2, kPairSmem, s, q);
 }
 
 static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream_t s) {
@@ -834,7 +836,7 @@ static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream
     q.tiles_m = (int32_t)tiles_m; q.tiles_n = (int32_t)tiles_n; q.k_blocks = (int32_t)k_blocks;
     q.e = e;
     if (!soft && (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
-    return launch_cluster(kernel, (unsigned)(tiles * parts), kSplitThreads, (unsigned)parts, kSplitSmem, s, q);
+    return launch_dense(kernel, dim3((unsigned)(tiles * parts)), kSplitThreads, (unsigned)parts, kSplitSmem, s, q);
 }
 
 static int launch_product(const Product& p, Ending& e, cudaStream_t s) {

@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int64_t t0 = (int64_t)blockIdx.x * p.cta_tokens, h0 = (int64_t)blockIdx.y * p.cta_heads;
     const int nt = (int)(p.tokens - t0 < p.cta_tokens ? p.tokens - t0 : p.cta_tokens);
     const int nh = (int)(p.heads - h0 < p.cta_heads ? p.heads - h0 : p.cta_heads);
+    await_predecessor();
     for (int j = threadIdx.x; j < nt * pairs; j += kThreads) {
         const int t = j / pairs, i = j - t * pairs;
         const int64_t pos = p.positions ? p.positions[t0 + t] : (int64_t)((uint64_t)p.pos0 + (uint64_t)(t0 + t));
@@ -184,12 +185,8 @@ static int launch_rope(RopeParams& p, cudaStream_t s) {
     p.by_heads = reciprocal(p.cta_heads);
     const int64_t gx = (p.tokens + p.cta_tokens - 1) / p.cta_tokens, gy = (p.heads + p.cta_heads - 1) / p.cta_heads;
     if (gx > INT32_MAX || gy > 65535) return ZERO_ERANGE;
-    const dim3 grid((unsigned)gx, (unsigned)gy);
-    if (vec)
-        rope_kernel<kF32, kHalf, true><<<grid, kThreads, 0, s>>>(p);
-    else
-        rope_kernel<kF32, kHalf, false><<<grid, kThreads, 0, s>>>(p);
-    return launch_status();
+    return launch_dense(vec ? rope_kernel<kF32, kHalf, true> : rope_kernel<kF32, kHalf, false>, dim3((unsigned)gx, (unsigned)gy),
+                        kThreads, 1, 0, s, p);
 }
 
 }  // namespace zgb

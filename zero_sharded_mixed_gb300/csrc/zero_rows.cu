@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Product p, const E
     const int64_t col0 = ((int64_t)blockIdx.x * groups + group) * kCols;
     const int64_t k = p.depth;
     float acc[kCols][kM] = {};
+    await_predecessor();
     if (col0 < p.cols) {
         // a column past the end reads the last one again and is not stored
         const int64_t last = p.cols - 1;
@@ -90,11 +91,8 @@ static int launch_rows_of(const Product& p, const Ending& e, cudaStream_t s) {
     const int64_t grid = (pairs * split + kWarps - 1) / kWarps;
     if (grid > INT32_MAX) return ZERO_ERANGE;
     const bool aligned = rows_aligned16(p.b.p, p.b.ld, 2) && (p.rows == 1 ? aligned16(p.a.p) : rows_aligned16(p.a.p, p.a.ld, 2));
-    if (aligned)
-        rows_kernel<kM, kF32, true><<<(unsigned)grid, kThreads, 0, s>>>(p, e, split);
-    else
-        rows_kernel<kM, kF32, false><<<(unsigned)grid, kThreads, 0, s>>>(p, e, split);
-    return launch_status();
+    return launch_dense(aligned ? rows_kernel<kM, kF32, true> : rows_kernel<kM, kF32, false>, dim3((unsigned)grid), kThreads, 1, 0,
+                        s, p, e, split);
 }
 
 int launch_rows(const Product& p, const Ending& e, cudaStream_t s) {
