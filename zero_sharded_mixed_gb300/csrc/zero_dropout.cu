@@ -49,6 +49,27 @@ struct DropoutParams {
     DropParams drop;
 };
 
+// The last step of the sums: `total` holds this CTA's of `width` columns from col0;
+// each CTA of the cluster adds a share of the columns over all of them.
+__device__ __forceinline__ void join_sums(const DropoutParams& p, const float* total, int64_t col0, int width) {
+    cluster_sync();
+    const int n = (int)cluster_size(), c = (int)cluster_rank() * (width / n) + threadIdx.x;
+    if ((int)threadIdx.x < width / n && col0 + c < p.cols) {
+        float s = 0.0f;
+        for (int i = 0; i < n; ++i) s += peer_load1(peer_addr(smem_addr(total + c), i));
+        const int64_t at = col0 + c;
+        if (p.db_f32) {
+            if (p.db_acc) s += static_cast<const float*>(p.db_acc)[at];
+            static_cast<float*>(p.db)[at] = s;
+        } else {
+            if (p.db_acc) s += bf16_one(static_cast<const uint16_t*>(p.db_acc)[at]);
+            static_cast<uint16_t*>(p.db)[at] = to_bf16(s);
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // the totals are read before their CTAs end
+}
+
 // Whole, aligned rows: a thread keeps its eight columns and goes down the rows,
 // four of them (two of fp32) in flight, so that addresses are additions and the
 // first products of its random numbers, which see the column and constants alone,
@@ -62,14 +83,26 @@ struct DropoutParams {
 template <bool kF32>
 constexpr int kBatchOf = kF32 ? 2 : 4;
 
-template <bool kGrad, bool kF32>
+//
+// Sums (kSums): the CTAs of a cluster share the column groups of one warp, and their
+// warps the rows.  Each thread sums its rows in order, the CTA its threads, then the
+// cluster its CTAs, every time in the same order.
+constexpr int kShares = 8;
+
+template <bool kGrad, bool kF32, bool kSums>
 __global__ void __launch_bounds__(kThreads, 3) dropout_kernel(const DropoutParams p, int lanes, int col_warps, int64_t row_step) {
     await_predecessor();
-    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t rg = w / col_warps, cb = (w - rg * col_warps) * lanes + lane % lanes;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+    const int64_t rg = kSums ? blockIdx.x % kShares * (kThreads / 32) + warp : w / col_warps;
+    const int64_t cb = (kSums ? blockIdx.x / kShares : w - rg * col_warps) * lanes + lane % lanes;
     int64_t row = rg * (32 / lanes) + lane / lanes;
-    if (cb >= p.col_blocks || rg * (32 / lanes) >= row_step) return;   // the last CTA may hold a warp too many
+    float sum[kSums ? 8 : 1] = {};
+    if constexpr (kSums) {
+        if (cb >= p.col_blocks) row = p.rows;
+    } else {
+        if (cb >= p.col_blocks || rg * (32 / lanes) >= row_step) return;   // the last CTA may hold a warp too many
+    }
     const uint32_t step = p.drop.cut ? drop_step(p.drop) : 0u;
     constexpr int kBatch = kBatchOf<kF32>, xs = kF32 ? 4 : 2, ss = kGrad ? 2 : xs;
     const int ys = p.y_f32 ? 4 : 2;
@@ -104,8 +137,28 @@ __global__ void __launch_bounds__(kThreads, 3) dropout_kernel(const DropoutParam
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] += t[k];
             }
-            store8(y, p.y_f32, true, 8, v);
+            if (!kSums || p.y) store8(y, p.y_f32, true, 8, v);
+            if constexpr (kSums) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] += v[k];
+            }
         }
+    }
+    if constexpr (kSums) {
+        __shared__ float part[kThreads / 32 * 8 * 32];   // [warp][row of the warp][8 lanes columns]
+        __shared__ float total[8 * 32];
+        const int width = 8 * lanes;
+        float* q = part + (warp * (32 / lanes) + lane / lanes) * width + lane % lanes * 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = sum[k];
+        __syncthreads();
+        if ((int)threadIdx.x < width) {
+            float s = 0.0f;
+            for (int i = 0; i < kThreads / lanes; ++i) s += part[i * width + threadIdx.x];
+            total[threadIdx.x] = s;
+        }
+        __syncthreads();
+        join_sums(p, total, (int64_t)(blockIdx.x / kShares) * width, width);
     }
 }
 
@@ -139,21 +192,18 @@ __device__ __forceinline__ void store_column(void* p, bool f32, int64_t row, int
     }
 }
 
-// With column sums, or rows that are not aligned: a CTA takes a strip of 64
-// columns over a share of the rows.  Aligned (kVec): 8 threads a row, 32 rows at a
-// time.  Otherwise a warp takes 8 rows x 32 columns, a lane a column, so that a
-// row's accesses fall together; each lane forms the random bits of one row and
-// column group and leaves them in shared memory for the lanes of that group.
-// Sums (kSums): the shares of a strip are the CTAs of a cluster.  Each thread sums
-// its rows in order, the CTA its threads, then the cluster its CTAs, every time in
-// the same order.
-constexpr int kStrip = 64, kShares = 8;
+// Rows that are not aligned: a CTA takes a strip of 64 columns over a share of the
+// rows, a warp 8 rows x 32 columns at a time, a lane a column, so that a row's
+// accesses fall together; each lane forms the random bits of one row and column group
+// and leaves them in shared memory for the lanes of that group.  Sums as above, the
+// shares of a strip being the CTAs of a cluster.
+constexpr int kStrip = 64;
 
-template <bool kGrad, bool kVec, bool kSums>
+template <bool kGrad, bool kSums>
 __global__ void __launch_bounds__(kThreads) dropout_strip_kernel(const DropoutParams p, int shares) {
-    __shared__ float part[kThreads / 8][kStrip + 1];
+    __shared__ float part[kThreads / 64][kStrip];
     __shared__ float total[kStrip];
-    __shared__ uint4 bits[kVec ? 1 : kThreads / 32][8][4];   // a warp's part: row, column group
+    __shared__ uint4 bits[kThreads / 32][8][4];   // a warp's part: row, column group
     await_predecessor();
     const int share = blockIdx.x % shares;
     const int64_t col0 = (int64_t)(blockIdx.x / shares) * kStrip;
@@ -161,99 +211,45 @@ __global__ void __launch_bounds__(kThreads) dropout_strip_kernel(const DropoutPa
     const int64_t row_b = p.rows / shares * (share + 1) + (p.rows % shares) * (share + 1) / shares;
     const uint32_t step = p.drop.cut ? drop_step(p.drop) : 0u;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int xs = p.x_f32 ? 4 : 2, ys = p.y_f32 ? 4 : 2, ss = p.side_f32 ? 4 : 2;
-    if constexpr (kVec) {
-        const int64_t col = col0 + (threadIdx.x & 7) * 8;
-        float sum[8] = {};
-        if (col < p.cols) {   // whole groups: the columns are a multiple of 8
-#pragma unroll 4
-            for (int64_t row = row_a + threadIdx.x / 8; row < row_b; row += kThreads / 8) {
-                float v[8], t[8];
-                load8(static_cast<const char*>(p.x) + (row * p.ldx + col) * xs, p.x_f32, true, 8, v);
-                if (p.side) {
-                    load8(static_cast<const char*>(p.side) + (row * p.lds + col) * ss, p.side_f32, true, 8, t);
-                    if (kGrad) slope_apply<8>(p.act, t, v);
-                }
-                if (p.drop.cut) drop8(p.drop, step, row, col >> 3, v);
-                if (!kGrad && p.side) {
+    const int64_t col = col0 + (warp & 1) * 32 + lane;
+    float sum = 0.0f;
+    for (int64_t row0 = row_a + (warp >> 1) * 8; row0 < row_b; row0 += kThreads / 8) {
+        // rows of the part that exist, none where the column does not
+        const int n = col < p.cols ? (row_b - row0 < 8 ? (int)(row_b - row0) : 8) : 0;
+        float v[8], t[8];
+        load_column(p.x, p.x_f32, row0, p.ldx, col, n, v);
+        if (p.side) load_column(p.side, p.side_f32, row0, p.lds, col, n, t);
+        if (kGrad && p.side) slope_apply<8>(p.act, t, v);
+        if (p.drop.cut) {
+            __syncwarp();
+            bits[warp][lane & 7][lane >> 3] =
+                philox_block(p.drop, step, (uint32_t)(row0 + (lane & 7)), (uint32_t)((col0 >> 3) + (warp & 1) * 4 + (lane >> 3)));
+            __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] += t[k];
-                }
-                if (p.y) store8(static_cast<char*>(p.y) + (row * p.ldy + col) * ys, p.y_f32, true, 8, v);
-                if constexpr (kSums) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) sum[k] += v[k];
-                }
-            }
+            for (int r = 0; r < 8; ++r)
+                v[r] = reinterpret_cast<const uint16_t*>(bits[warp][r])[lane] >= p.drop.cut ? v[r] * p.drop.scale : 0.0f;
         }
+        if (!kGrad && p.side) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] += t[r];
+        }
+        if (p.y) store_column(p.y, p.y_f32, row0, p.ldy, col, n, v);
         if constexpr (kSums) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) part[threadIdx.x / 8][(threadIdx.x & 7) * 8 + k] = sum[k];
+            for (int r = 0; r < 8; ++r) sum += r < n ? v[r] : 0.0f;
         }
-    } else {
-        const int64_t col = col0 + (warp & 1) * 32 + lane;
-        float sum = 0.0f;
-        for (int64_t row0 = row_a + (warp >> 1) * 8; row0 < row_b; row0 += kThreads / 8) {
-            // rows of the part that exist, none where the column does not
-            const int n = col < p.cols ? (row_b - row0 < 8 ? (int)(row_b - row0) : 8) : 0;
-            float v[8], t[8];
-            load_column(p.x, p.x_f32, row0, p.ldx, col, n, v);
-            if (p.side) load_column(p.side, p.side_f32, row0, p.lds, col, n, t);
-            if (kGrad && p.side) slope_apply<8>(p.act, t, v);
-            if (p.drop.cut) {
-                __syncwarp();
-                bits[warp][lane & 7][lane >> 3] =
-                    philox_block(p.drop, step, (uint32_t)(row0 + (lane & 7)), (uint32_t)((col0 >> 3) + (warp & 1) * 4 + (lane >> 3)));
-                __syncwarp();
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    v[r] = reinterpret_cast<const uint16_t*>(bits[warp][r])[lane] >= p.drop.cut ? v[r] * p.drop.scale : 0.0f;
-            }
-            if (!kGrad && p.side) {
-#pragma unroll
-                for (int r = 0; r < 8; ++r) v[r] += t[r];
-            }
-            if (p.y) store_column(p.y, p.y_f32, row0, p.ldy, col, n, v);
-            if constexpr (kSums) {
-#pragma unroll
-                for (int r = 0; r < 8; ++r) sum += r < n ? v[r] : 0.0f;
-            }
-        }
-        if constexpr (kSums) part[warp >> 1][(warp & 1) * 32 + lane] = sum;
     }
     if constexpr (kSums) {
+        part[warp >> 1][(warp & 1) * 32 + lane] = sum;
         __syncthreads();
         if (threadIdx.x < kStrip) {
             float s = 0.0f;
-            for (int i = 0; i < (kVec ? kThreads / 8 : kThreads / 64); ++i) s += part[i][threadIdx.x];
+            for (int i = 0; i < kThreads / 64; ++i) s += part[i][threadIdx.x];
             total[threadIdx.x] = s;
         }
         __syncthreads();
-        cluster_sync();
-        const int c = (int)cluster_rank() * (kStrip / kShares) + threadIdx.x;   // eight columns a CTA
-        if (threadIdx.x < kStrip / kShares && col0 + c < p.cols) {
-            float s = 0.0f;
-            for (int i = 0; i < kShares; ++i) s += peer_load1(peer_addr(smem_addr(total + c), i));
-            const int64_t at = col0 + c;
-            if (p.db_f32) {
-                if (p.db_acc) s += static_cast<const float*>(p.db_acc)[at];
-                static_cast<float*>(p.db)[at] = s;
-            } else {
-                if (p.db_acc) s += bf16_one(static_cast<const uint16_t*>(p.db_acc)[at]);
-                static_cast<uint16_t*>(p.db)[at] = to_bf16(s);
-            }
-        }
-        __syncwarp();
-        cluster_sync();   // the totals are read before their CTAs end
+        join_sums(p, total, col0, kStrip);
     }
-}
-
-template <bool kVec>
-static int launch_sums(const DropoutParams& p, cudaStream_t s) {
-    const int64_t strips = (p.cols + kStrip - 1) / kStrip;
-    if (strips > INT32_MAX / kShares) return ZERO_ERANGE;
-    return launch_dense(dropout_strip_kernel<true, kVec, true>, dim3((unsigned)(strips * kShares)), kThreads, kShares, 0, s, p,
-                        (int)kShares);
 }
 
 template <bool kGrad>
@@ -262,23 +258,39 @@ static int launch_dropout(DropoutParams& p, cudaStream_t s) {
     const bool vec = p.cols % 8 == 0 && rows_aligned16(p.x, p.ldx, p.x_f32 ? 4 : 2) &&
                      (!p.side || rows_aligned16(p.side, p.lds, p.side_f32 ? 4 : 2)) &&
                      (!p.y || rows_aligned16(p.y, p.ldy, p.y_f32 ? 4 : 2));
-    if constexpr (kGrad)
-        if (p.db) return vec ? launch_sums<true>(p, s) : launch_sums<false>(p, s);
     if (!vec) {
-        // enough shares of at least 32 rows to fill the GPU about four times over
         const int64_t strips = (p.cols + kStrip - 1) / kStrip, most = (p.rows + 31) / 32;
+        if (strips > INT32_MAX / kShares) return ZERO_ERANGE;
+        if constexpr (kGrad)
+            if (p.db)
+                return launch_dense(dropout_strip_kernel<true, true>, dim3((unsigned)(strips * kShares)), kThreads, kShares, 0, s, p,
+                                    (int)kShares);
+        // enough shares of at least 32 rows to fill the GPU about four times over
         int64_t shares = (int64_t)sm_count() * 32 / strips;
         shares = shares < 1 ? 1 : shares > most ? most : shares;
         if (strips > INT32_MAX / shares) return ZERO_ERANGE;
-        return launch_dense(dropout_strip_kernel<kGrad, false, false>, dim3((unsigned)(strips * shares)), kThreads, 1, 0, s, p,
+        return launch_dense(dropout_strip_kernel<kGrad, false>, dim3((unsigned)(strips * shares)), kThreads, 1, 0, s, p,
                             (int)shares);
     }
-    // lanes of a warp along a row, and as many groups of rows as give every thread a
-    // batch, up to the warps that are resident at once
-    void (*kernel)(DropoutParams, int, int, int64_t) = p.x_f32 ? dropout_kernel<kGrad, true> : dropout_kernel<kGrad, false>;
-    const int kBatch = p.x_f32 ? kBatchOf<true> : kBatchOf<false>;
+    // lanes of a warp along a row
     int lanes = 32;
     while (lanes / 2 >= p.col_blocks) lanes /= 2;
+    if constexpr (kGrad)
+        if (p.db) {
+            // narrower warps where clusters of whole ones would leave SMs idle
+            void (*kernel)(DropoutParams, int, int, int64_t) = p.x_f32 ? dropout_kernel<true, true, true> : dropout_kernel<true, false, true>;
+            const int64_t resident = (int64_t)sm_count() * 3;
+            while (lanes > 8 && (p.col_blocks + lanes - 1) / lanes * kShares < resident * 3 / 4) lanes /= 2;
+            if (lanes < 8) lanes = 8;   // at least a column for each CTA of a cluster
+            const int64_t col_warps = (p.col_blocks + lanes - 1) / lanes;
+            if (col_warps > INT32_MAX / kShares) return ZERO_ERANGE;
+            return launch_dense(kernel, dim3((unsigned)(col_warps * kShares)), kThreads, kShares, 0, s, p, lanes, (int)col_warps,
+                                (int64_t)kShares * (kThreads / 32) * (32 / lanes));
+        }
+    // as many groups of rows as give every thread a batch, up to the warps that are
+    // resident at once
+    void (*kernel)(DropoutParams, int, int, int64_t) = p.x_f32 ? dropout_kernel<kGrad, true, false> : dropout_kernel<kGrad, false, false>;
+    const int kBatch = p.x_f32 ? kBatchOf<true> : kBatchOf<false>;
     const int64_t col_warps = (p.col_blocks + lanes - 1) / lanes, rows_of_warp = 32 / lanes;
     if (col_warps > INT32_MAX) return ZERO_ERANGE;
     const int64_t groups = (p.rows + rows_of_warp * kBatch - 1) / (rows_of_warp * kBatch);
@@ -286,8 +298,7 @@ static int launch_dropout(DropoutParams& p, cudaStream_t s) {
     row_groups = row_groups < 1 ? 1 : row_groups > groups ? groups : row_groups;
     const int64_t grid = (row_groups * col_warps + kThreads / 32 - 1) / (kThreads / 32);
     if (grid > INT32_MAX) return ZERO_ERANGE;
-    const int64_t row_step = row_groups * rows_of_warp;
-    return launch_dense(kernel, dim3((unsigned)grid), kThreads, 1, 0, s, p, lanes, (int)col_warps, row_step);
+    return launch_dense(kernel, dim3((unsigned)grid), kThreads, 1, 0, s, p, lanes, (int)col_warps, row_groups * rows_of_warp);
 }
 
 int launch_column_sum(int64_t rows, int64_t cols, const uint16_t* dz, int64_t lddz, const void* db_acc, void* db,

@@ -251,11 +251,11 @@ __device__ __forceinline__ float element(float x) { return x; }
 __device__ __forceinline__ float element(uint16_t x) { return bf16_one(x); }
 
 // A unit whose rows are not aligned, or whose columns end inside a group: a lane a
-// column, row by row, so that a row's accesses still fall together.  get(r) gives
-// this lane's accumulator of row r; every lane of the warp calls.
-template <bool kF32, class Get>
+// column, row by row, so that a row's accesses still fall together.  v: this lane's
+// accumulators of the 8 rows; every lane of the warp calls.
+template <bool kF32>
 __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
-                                         Get get) {
+                                         float (&v)[8]) {
     const int lane = threadIdx.x & 31;
     const int64_t col = col0 + lane;
     const float bias = e.bias && col < cols ? bf16_one(e.bias[col]) : 0.0f;
@@ -263,9 +263,9 @@ __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t
     if (e.drop.cut) block = philox_block(e.drop, step, (uint32_t)(row0 + (lane & 7)), (uint32_t)((col0 >> 3) + (lane >> 3)));
     // rows of this unit that exist, none where the column does not: one comparison a row
     const int n = col < cols ? (rows - row0 < 8 ? (int)(rows - row0) : 8) : 0;
-    float v[8], t[8];
+    float t[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) v[r] = get(r) + bias;
+    for (int r = 0; r < 8; ++r) v[r] += bias;
     if (e.pre) {
         uint16_t* q = e.pre + row0 * e.ld_pre + col;
 #pragma unroll
@@ -305,13 +305,6 @@ __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t
 
 // ---- waits -------------------------------------------------------------------------
 constexpr long long kWaitCycles = 1ll << 31;   // SM cycles (about a second) before a wait gives up
-
-__device__ __forceinline__ bool wait_or_report(uint64_t* bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (mbar_wait_bounded(bar, parity, kWaitCycles)) return true;
-    atomicExch(&g_linear_status, ZERO_ETIMEOUT);
-    return false;
-}
 
 __device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
@@ -521,10 +514,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
                     for (int g = 0; g < 8; ++g)
                         *reinterpret_cast<uint4*>(chunk + group_place(lane, g)) = make_uint4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
                     __syncwarp();
-                    for (int i = 0; i < 4; ++i)
-                        end_rows<kF32>(p.e, step, row0 + i * 8, col0, p.rows, p.cols, [&](int r) {
-                            return *reinterpret_cast<const float*>(chunk + group_place(i * 8 + r, lane >> 2) + (lane & 3) * 4);
-                        });
+                    for (int i = 0; i < 4; ++i) {
+                        float v[8];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            v[r] = *reinterpret_cast<const float*>(chunk + group_place(i * 8 + r, lane >> 2) + (lane & 3) * 4);
+                        end_rows<kF32>(p.e, step, row0 + i * 8, col0, p.rows, p.cols, v);
+                    }
                 }
             }
             if (h >= n_chunks) release(acc_empty + buf);   // a narrow last tile: no chunk for this warp
@@ -556,20 +552,124 @@ constexpr int kSplitStages = 3;
 constexpr int kSplitThreads = 288;
 constexpr int kSplitSmem = 1024 + kSplitStages * kStageBytes + 128;
 
-// 256 threads bring `rows` (at most 128) sub-tile rows of an operand's tile.
-__device__ __forceinline__ void fetch_tile(const Operand& o, int64_t mn0, int64_t k0, int rows, uint8_t* dst) {
-    uint4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int chunk = i * 256 + threadIdx.x, r = chunk >> 3, g = chunk & 7;
-        if (r < rows)
-            v[i] = o.mn ? fetch8(o, k0 + (r & 63), mn0 + (r & ~63) + g * 8) : fetch8(o, mn0 + r, k0 + g * 8);
+// What one of the 8 loading warps brings of an operand's tile: sub-tile rows r with
+// r % 8 == warp, 64 elements each from any element-aligned place, as the one or two
+// 16-byte blocks that hold a lane's 8 elements; 8 lanes a row, 4 rows at a time.  Rows
+// 8 apart lie 16 ld bytes apart, so a warp's rows all start at the same place `shift`
+// of a block: the blocks are shifted by branches that the warp takes together and one
+// funnel shift a word.  (Lanes with shifts of their own: 4400 cycles a stage.  A word
+// a lane, 6 instructions a row: 10000.)  K-major, sub-tile row r is tile row r;
+// MN-major, reduced row r % 64 at kept elements 64 (r / 64) on.
+// Blocks reach up to 7 elements past a row's own, into its neighbours; the few that
+// would reach past the operand's own memory come element by element.
+struct SoftTile {
+    const uint16_t* q;          // this lane's elements of rows `warp + 8 (lane / 8)` of the next stage
+    int64_t step;               // elements to 32 rows on
+    int row, rows;              // the operand row of q and their number, from the tile's first
+    int extent;                 // kept elements from the tile's first, at most 128
+    uint32_t shift;             // bytes
+    bool mn;
+
+    __device__ __forceinline__ SoftTile(const Operand& o, int64_t mn0, int64_t k0, int warp) : step(32 * o.ld), mn(o.mn) {
+        const int lane = threadIdx.x & 31, g = lane & 7;
+        const int64_t first = o.mn ? k0 : mn0, left = (o.mn ? o.cols : o.rows) - mn0, more = o.rows - first;
+        row = warp + 8 * (lane >> 3);
+        rows = more < INT32_MAX ? (int)more : INT32_MAX;
+        q = o.p + (first + row) * o.ld + (o.mn ? mn0 : k0) + 8 * g;
+        extent = left < 128 ? (int)left : 128;
+        shift = (uint32_t)__shfl_sync(0xffffffffu, (int)(reinterpret_cast<uintptr_t>(q) & 15), 0);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int chunk = i * 256 + threadIdx.x, r = chunk >> 3, g = chunk & 7;
-        if (r < rows) *reinterpret_cast<uint4*>(dst + r * 128 + ((g ^ (r & 7)) << 4)) = v[i];
+    // quad j of 4: where, and how many of the lane's 8 elements exist (any number at
+    // least 8 or below 1 for all or none), `left` reduced ones from here on
+    __device__ __forceinline__ const uint16_t* place(int j) const { return mn ? q + (j & 1) * step + (j >> 1) * 64 : q + j * step; }
+    __device__ __forceinline__ int count(int j, int left) const {
+        if (row + 32 * (mn ? j & 1 : j) >= rows) return 0;
+        return (mn ? extent - (j >> 1) * 64 : left) - 8 * (int)(threadIdx.x & 7);
     }
+    // whether a block of a lane's elements reaches past the operand's memory, and
+    // whether any of a stage's tile (from mn0, k0) does
+    static __device__ __forceinline__ bool past(const Operand& o, uintptr_t first, uintptr_t last) {   // elements' addresses
+        return (first & ~(uintptr_t)15) < operand_begin(o) || (last & ~(uintptr_t)15) + 16 > operand_end(o);
+    }
+    static __device__ __forceinline__ bool at_edge(const Operand& o, int64_t mn0, int64_t k0) {
+        const int64_t r0 = o.mn ? k0 : mn0, c0 = o.mn ? mn0 : k0, r1 = r0 + (o.mn ? 63 : 127), c1 = c0 + (o.mn ? 127 : 63);
+        return past(o, reinterpret_cast<uintptr_t>(o.p + r0 * o.ld + c0),
+                    reinterpret_cast<uintptr_t>(o.p + (r1 < o.rows ? r1 : o.rows - 1) * o.ld + (c1 < o.cols ? c1 : o.cols - 1)));
+    }
+
+    template <bool kEdge>
+    __device__ __forceinline__ void load(const Operand& o, int n, int left, Blocks8* b) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            b[j].x = b[j].y = make_uint4(0u, 0u, 0u, 0u);
+            if (32 * j >= n) continue;
+            const uint16_t* e = place(j);
+            const int have = count(j, left);
+            if (kEdge && have > 0 && past(o, reinterpret_cast<uintptr_t>(e), reinterpret_cast<uintptr_t>(e + (have < 8 ? have : 8) - 1))) {
+                uint32_t w[4];   // in place: not to be shifted
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = (2 * i < have ? e[2 * i] : 0u) | (2 * i + 1 < have ? (uint32_t)e[2 * i + 1] << 16 : 0u);
+                b[j].x = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(e) - shift);
+                if (have > 0) b[j].x = at[0];
+                if ((int)shift + 2 * (have < 8 ? have : 8) > 16) b[j].y = at[1];
+            }
+        }
+    }
+    template <bool kEdge, int kWords>
+    __device__ __forceinline__ void store_shifted(const Operand& o, int n, int left, const Blocks8* b, uint8_t* d) const {
+        const uint32_t bits = (shift & 2) * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (32 * j >= n) continue;
+            const uint32_t w[9] = {b[j].x.x, b[j].x.y, b[j].x.z, b[j].x.w, b[j].y.x, b[j].y.y, b[j].y.z, b[j].y.w, 0u};
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(w[i + kWords], w[i + kWords + 1], bits);
+            const int have = count(j, left);
+            if (have < 8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] &= have >= 2 * i + 2 ? 0xffffffffu : have == 2 * i + 1 ? 0xffffu : 0u;
+            }
+            if (kEdge && have > 0) {
+                const uint16_t* e = place(j);
+                if (past(o, reinterpret_cast<uintptr_t>(e), reinterpret_cast<uintptr_t>(e + (have < 8 ? have : 8) - 1)))
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = w[i];
+            }
+            *reinterpret_cast<uint4*>(d + j * 4096) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    template <bool kEdge>
+    __device__ __forceinline__ void store(const Operand& o, int n, int left, const Blocks8* b, uint8_t* dst, int warp) const {
+        const int lane = threadIdx.x & 31;
+        uint8_t* d = dst + (warp + 8 * (lane >> 3)) * 128 + (((lane & 7) ^ warp) << 4);   // row % 8 is the warp
+        switch (shift >> 2) {
+            case 0: store_shifted<kEdge, 0>(o, n, left, b, d); break;
+            case 1: store_shifted<kEdge, 1>(o, n, left, b, d); break;
+            case 2: store_shifted<kEdge, 2>(o, n, left, b, d); break;
+            default: store_shifted<kEdge, 3>(o, n, left, b, d); break;
+        }
+    }
+    __device__ __forceinline__ void advance() {
+        q += mn ? 2 * step : 64;
+        rows -= mn ? 64 : 0;
+    }
+};
+
+// One stage of both operands; the loads of all of it fly before the wait for room.
+template <bool kEdge>
+__device__ __forceinline__ bool soft_stage(const Operand& oa, const Operand& ob, const SoftTile& ta, const SoftTile& tb, int a_rows,
+                                           int b_rows, int left, uint64_t* empty, bool wait, uint32_t parity, uint8_t* stage, int warp) {
+    Blocks8 a[4], b[4];
+    ta.load<kEdge>(oa, a_rows, left, a);
+    tb.load<kEdge>(ob, b_rows, left, b);
+    if (wait && !warp_wait(empty, parity)) return false;
+    ta.store<kEdge>(oa, a_rows, left, a, stage, warp);
+    tb.store<kEdge>(ob, b_rows, left, b, stage + 16384, warp);
+    return true;
 }
 
 template <bool kF32, bool kSoft>
@@ -590,7 +690,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kSplitStages; ++s) {
-            mbar_init(full + s, kSoft ? 256 : 1);
+            mbar_init(full + s, kSoft ? 8 : 1);
             mbar_init(empty + s, 1);
         }
         mbar_init(acc_full, 1);
@@ -607,6 +707,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
     await_predecessor();
     const uint32_t tmem = *tmem_slot;
 
+    // Tile-map copies start each tile at another place of the reduced dimension: with
+    // few rows all CTAs would otherwise ask for the same lines of A at the same time
+    // (9 x 1600 times 4800 x 1600: 12.7 us; 16 rows, spread wider, 8).
+    const int turn = kSoft || kb1 == kb0 ? 0 : tile % (kb1 - kb0);
     // sub-tile rows of a stage: tile rows (K-major), or 64 for every 64 columns
     const int a_left = p.rows - row_tile < 128 ? (int)(p.rows - row_tile) : 128;
     const int a_rows = p.a.mn ? (a_left + 63) / 64 * 64 : kSoft ? a_left : 128;
@@ -617,32 +721,41 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
         if (kSoft) {
             int s = 0;
             uint32_t round = 0;
+            SoftTile ta(p.a, row_tile, (int64_t)kb0 * 64, warp), tb(p.b, col_tile, (int64_t)kb0 * 64, warp);
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (round > 0 && !(ok = wait_or_report(empty + s, (round - 1) & 1))) break;
-                uint8_t* a = smem + s * kStageBytes;
-                fetch_tile(p.a, row_tile, (int64_t)kb * 64, a_rows, a);
-                fetch_tile(p.b, col_tile, (int64_t)kb * 64, b_rows, a + 16384);
+                const int64_t more = p.depth - (int64_t)kb * 64;
+                const int left = more < 64 ? (int)more : 64;
+                uint8_t* stage = smem + s * kStageBytes;
+                const int64_t k0 = (int64_t)kb * 64;
+                ok = SoftTile::at_edge(p.a, row_tile, k0) || SoftTile::at_edge(p.b, col_tile, k0)
+                         ? soft_stage<true>(p.a, p.b, ta, tb, a_rows, b_rows, left, empty + s, round > 0, (round - 1) & 1, stage, warp)
+                         : soft_stage<false>(p.a, p.b, ta, tb, a_rows, b_rows, left, empty + s, round > 0, (round - 1) & 1, stage, warp);
+                if (!ok) break;
+                ta.advance();
+                tb.advance();
                 fence_async_shared();
-                mbar_arrive(full + s);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + s);
                 if (++s == kSplitStages) s = 0, ++round;
             }
         } else if (warp == 0) {
             int s = 0;
             uint32_t round = 0;
             const int a_boxes = p.a.mn ? a_rows / 64 : 1, b_boxes = p.b.mn ? b_rows / 64 : 1;
-            for (int kb = kb0; kb < kb1; ++kb) {
+            for (int i = kb0; i < kb1; ++i) {
+                const int kb = i + turn < kb1 ? i + turn : i + turn - (kb1 - kb0);
                 if (round > 0 && !(ok = warp_wait(empty + s, (round - 1) & 1))) break;
                 const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384, bar = smem_addr(full + s);
                 const int k = kb * 64;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(full + s, (uint32_t)(a_rows + b_rows) * 128u);
                     if (p.a.mn) {
-                        for (int i = 0; i < a_boxes; ++i) tensor_load(a + i * kSubTileBytes, &p.map_a, (int)row_tile + 64 * i, k, bar);
+                        for (int j = 0; j < a_boxes; ++j) tensor_load(a + j * kSubTileBytes, &p.map_a, (int)row_tile + 64 * j, k, bar);
                     } else {
                         tensor_load(a, &p.map_a, k, (int)row_tile, bar);
                     }
                     if (p.b.mn) {
-                        for (int i = 0; i < b_boxes; ++i) tensor_load(b + i * kSubTileBytes, &p.map_b, (int)col_tile + 64 * i, k, bar);
+                        for (int j = 0; j < b_boxes; ++j) tensor_load(b + j * kSubTileBytes, &p.map_b, (int)col_tile + 64 * j, k, bar);
                     } else {
                         tensor_load(b, &p.map_b, k, (int)col_tile, bar);
                     }
@@ -660,7 +773,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
         uint32_t round = 0;
         const uint32_t idesc = instruction_descriptor(128, p.bn, p.a.mn, p.b.mn);
         const uint32_t a_step = descriptor_step(p.a.mn), b_step = descriptor_step(p.b.mn);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int n = kb0; n < kb1; ++n) {
+            const int kb = n + turn < kb1 ? n + turn : n + turn - (kb1 - kb0);
             if (!(ok = warp_wait(full + s, round & 1))) break;
             tcgen05_fence_after();
             const uint32_t a = smem_addr(smem + s * kStageBytes);
@@ -669,7 +783,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
             if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (left > 16 * i) mma_bf16<false>(tmem, da + i * a_step, db + i * b_step, idesc, kb > kb0 || i > 0);
+                    if (left > 16 * i) mma_bf16<false>(tmem, da + i * a_step, db + i * b_step, idesc, n > kb0 || i > 0);
                 mma_commit<false>(empty + s);
             }
             if (++s == kSplitStages) s = 0, ++round;
@@ -729,12 +843,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
                     end.finish(p.e, step, row, col, v);
                 }
             } else {
-                end_rows<kF32>(p.e, step, row0, col0, p.rows, p.cols, [&](int r) {
-                    float v = 0.0f;
-                    for (int i = 0; i < parts; ++i)
-                        v += peer_load1(peer_addr(chunk, i) + group_place(r0 + r, lane >> 2) + (lane & 3) * 4);
-                    return v;
-                });
+                float v[8] = {};
+                for (int i = 0; i < parts; ++i) {
+                    const uint32_t at = peer_addr(chunk, i) + (lane & 3) * 4;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) v[r] += peer_load1(at + group_place(r0 + r, lane >> 2));
+                }
+                end_rows<kF32>(p.e, step, row0, col0, p.rows, p.cols, v);
             }
         }
     }

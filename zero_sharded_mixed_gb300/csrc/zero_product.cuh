@@ -30,40 +30,49 @@ struct Ending {
     DropParams drop;
 };
 
-// Eight elements (r, c) .. (r, c + 7) of an operand, zeros outside it, from any
-// element-aligned place: the two 16-byte blocks that hold them, shifted together.
-// Blocks are read only where they lie wholly inside the operand's own memory.
-__device__ __forceinline__ uint4 fetch8(const Operand& o, int64_t r, int64_t c) {
-    uint4 out = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= o.rows || c >= o.cols) return out;
-    const uint16_t* q = o.p + r * o.ld + c;
-    const int64_t left = o.cols - c;
+// Eight elements from any element-aligned place q of an operand, of which the first
+// n exist (none for n <= 0; the others come as zeros): the one or two 16-byte blocks
+// that hold them are loaded first, without a branch around the loads, so that a
+// thread's loads of several places fly together, and shifted into one vector later.
+// Blocks are read only where they lie wholly inside the operand's own memory; the few
+// places where one does not are read element by element.
+struct Blocks8 {
+    uint4 x, y;
+};
+__device__ __forceinline__ uintptr_t operand_begin(const Operand& o) { return reinterpret_cast<uintptr_t>(o.p); }
+__device__ __forceinline__ uintptr_t operand_end(const Operand& o) {
+    return reinterpret_cast<uintptr_t>(o.p + (o.rows - 1) * o.ld + o.cols);
+}
+__device__ __forceinline__ Blocks8 load_blocks(uintptr_t begin, uintptr_t end, const uint16_t* q, int n) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(q), lo = at & ~(uintptr_t)15;
+    Blocks8 b;
+    b.x = b.y = make_uint4(0u, 0u, 0u, 0u);
+    if (n > 0 && lo >= begin && lo + 16 <= end) b.x = *reinterpret_cast<const uint4*>(lo);
+    if ((int)(at & 15) + 2 * (n < 8 ? n : 8) > 16 && lo + 32 <= end) b.y = *reinterpret_cast<const uint4*>(lo + 16);
+    return b;
+}
+__device__ __forceinline__ uint4 shift_blocks(uintptr_t begin, uintptr_t end, const uint16_t* q, int n, const Blocks8& b) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(q), lo = at & ~(uintptr_t)15;
     const uint32_t shift = (uint32_t)(at & 15);
-    const uintptr_t first = reinterpret_cast<uintptr_t>(o.p), last = reinterpret_cast<uintptr_t>(o.p + (o.rows - 1) * o.ld + o.cols);
-    if (shift == 0 && left >= 8) return *reinterpret_cast<const uint4*>(q);
-    if (left >= 8 && lo >= first && lo + 32 <= last) {
-        const uint4 x = *reinterpret_cast<const uint4*>(lo), y = *reinterpret_cast<const uint4*>(lo + 16);
-        uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        if (shift & 8) {
+    uint32_t w[8] = {b.x.x, b.x.y, b.x.z, b.x.w, b.y.x, b.y.y, b.y.z, b.y.w};
 #pragma unroll
-            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-        }
-        if (shift & 4) {
+    for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
 #pragma unroll
-            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
+    if (n < 8) {
+        if (n > 0 && (lo < begin || lo + (shift + 2 * n > 16 ? 32 : 16) > end)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = (2 * i < n ? q[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)q[2 * i + 1] << 16 : 0u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] &= n >= 2 * i + 2 ? 0xffffffffu : n == 2 * i + 1 ? 0xffffu : 0u;
         }
-        const uint32_t bits = (shift & 2) * 8;
-        out.x = __funnelshift_r(w[0], w[1], bits);
-        out.y = __funnelshift_r(w[1], w[2], bits);
-        out.z = __funnelshift_r(w[2], w[3], bits);
-        out.w = __funnelshift_r(w[3], w[4], bits);
-        return out;
+    } else if (lo < begin || lo + (shift ? 32 : 16) > end) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = q[2 * i] | ((uint32_t)q[2 * i + 1] << 16);
     }
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < left) w[j / 2] |= (uint32_t)q[j] << (16 * (j & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -93,7 +102,7 @@ __device__ __forceinline__ void end_one(const Ending& e, uint32_t step, int64_t 
 }
 
 // The kernel of a few rows (zero_rows.cu), both operands K-major.
-constexpr int kMostRows = 8;
+constexpr int kMostRows = 4;
 int launch_rows(const Product& p, const Ending& e, cudaStream_t s);
 
 }  // namespace zgb

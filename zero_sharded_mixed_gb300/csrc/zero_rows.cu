@@ -1,6 +1,6 @@
 // A linear of a few rows (one new token, a handful of sequences), sm_103a.
 //
-// Such a product is a read of its weights: every element of w meets at most eight
+// Such a product is a read of its weights: every element of w meets at most four
 // elements of x, far below what a tensor core could use, and a tile of 128 rows
 // would stay almost empty.  A warp takes two columns and runs along their rows of w
 // in 16-byte vectors, 512 bytes a step; x comes from the caches.  fp32 products and
@@ -49,17 +49,37 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Product p, const E
                     for (int t = 0; t < 8; ++t) acc[j][i] += wv[j][t] * xv[t];
             }
         }
-        for (; c < k; c += stride) {   // unaligned rows, or the last few elements of aligned ones
-            float wv[kCols][8], xv[8];
+        if constexpr (kAligned) {
+            if (c == whole)   // one lane has the last few elements
+                for (; c < k; ++c)
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) unpack8(fetch8(p.b, bc[j], c), wv[j]);
+                    for (int i = 0; i < kM; ++i)
+                        if (i < p.rows) {
+                            const float x = bf16_one(p.a.p[i * p.a.ld + c]);
 #pragma unroll
-            for (int i = 0; i < kM; ++i) {
-                unpack8(fetch8(p.a, i, c), xv);   // zeros past the last row
+                            for (int j = 0; j < kCols; ++j) acc[j][i] += bf16_one(p.b.p[bc[j] * p.b.ld + c]) * x;
+                        }
+        } else {
+            const uintptr_t a0 = operand_begin(p.a), a1 = operand_end(p.a), b0 = operand_begin(p.b), b1 = operand_end(p.b);
+#pragma unroll(kM <= 2 ? 3 : 1)
+            for (; c < k; c += stride) {
+                const int n = k - c < 8 ? (int)(k - c) : 8;
+                Blocks8 wb[kCols], xb[kM];
 #pragma unroll
-                for (int j = 0; j < kCols; ++j)
+                for (int j = 0; j < kCols; ++j) wb[j] = load_blocks(b0, b1, p.b.p + bc[j] * p.b.ld + c, n);
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) acc[j][i] += wv[j][t] * xv[t];
+                for (int i = 0; i < kM; ++i) xb[i] = load_blocks(a0, a1, p.a.p + i * p.a.ld + c, i < p.rows ? n : 0);
+                float wv[kCols][8], xv[8];
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) unpack8(shift_blocks(b0, b1, p.b.p + bc[j] * p.b.ld + c, n, wb[j]), wv[j]);
+#pragma unroll
+                for (int i = 0; i < kM; ++i) {
+                    unpack8(shift_blocks(a0, a1, p.a.p + i * p.a.ld + c, i < p.rows ? n : 0, xb[i]), xv);   // zeros past the last row
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j)
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) acc[j][i] += wv[j][t] * xv[t];
+                }
             }
         }
     }
@@ -96,11 +116,10 @@ static int launch_rows_of(const Product& p, const Ending& e, cudaStream_t s) {
 }
 
 int launch_rows(const Product& p, const Ending& e, cudaStream_t s) {
+    static_assert(kMostRows == 4, "the sizes below");
     if (e.out_f32)
-        return p.rows == 1 ? launch_rows_of<1, true>(p, e, s) : p.rows == 2 ? launch_rows_of<2, true>(p, e, s)
-             : p.rows <= 4 ? launch_rows_of<4, true>(p, e, s) : launch_rows_of<8, true>(p, e, s);
-    return p.rows == 1 ? launch_rows_of<1, false>(p, e, s) : p.rows == 2 ? launch_rows_of<2, false>(p, e, s)
-         : p.rows <= 4 ? launch_rows_of<4, false>(p, e, s) : launch_rows_of<8, false>(p, e, s);
+        return p.rows == 1 ? launch_rows_of<1, true>(p, e, s) : p.rows == 2 ? launch_rows_of<2, true>(p, e, s) : launch_rows_of<4, true>(p, e, s);
+    return p.rows == 1 ? launch_rows_of<1, false>(p, e, s) : p.rows == 2 ? launch_rows_of<2, false>(p, e, s) : launch_rows_of<4, false>(p, e, s);
 }
 
 }  // namespace zgb
