@@ -544,7 +544,7 @@ struct SplitParams {
     CUtensorMap map_a, map_b;
     Operand a, b;
     int64_t rows, cols, depth;
-    int32_t tiles_m, tiles_n, bn, k_blocks;
+    int32_t tiles_m, tiles_n, bn, k_blocks, box_a;
     Ending e;
 };
 
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
     const int turn = kSoft || kb1 == kb0 ? 0 : tile % (kb1 - kb0);
     // sub-tile rows of a stage: tile rows (K-major), or 64 for every 64 columns
     const int a_left = p.rows - row_tile < 128 ? (int)(p.rows - row_tile) : 128;
-    const int a_rows = p.a.mn ? (a_left + 63) / 64 * 64 : kSoft ? a_left : 128;
+    const int a_rows = p.a.mn ? (a_left + 63) / 64 * 64 : kSoft ? a_left : p.box_a;
     const int b_rows = p.b.mn ? (p.bn + 63) / 64 * 64 : p.bn;
     bool ok = true;
 
@@ -950,7 +950,8 @@ static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream
     if (tiles > INT32_MAX / 8 || k_blocks > INT32_MAX) return ZERO_ERANGE;
     q.tiles_m = (int32_t)tiles_m; q.tiles_n = (int32_t)tiles_n; q.k_blocks = (int32_t)k_blocks;
     q.e = e;
-    if (!soft && (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
+    q.box_a = p.rows < 128 ? (int32_t)((p.rows + 7) / 8 * 8) : 128;
+    if (!soft && (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
     return launch_dense(kernel, dim3((unsigned)(tiles * parts)), kSplitThreads, (unsigned)parts, kSplitSmem, s, q);
 }
 
