@@ -241,9 +241,12 @@ __device__ __forceinline__ void await_predecessor() {
 }
 
 // A launch on grid.x * grid.y CTAs in clusters of `cluster` along x, of a kernel
-// that calls await_predecessor.
+// that calls await_predecessor.  early: before its predecessor has ended.  Its CTAs
+// then take the SMs as they come free, which packs large clusters unevenly: the
+// column sums of 8192 x 6400, 400 CTAs in clusters of 8, took 136 us after a product
+// so, and 80 launched to a free GPU.
 template <class... Params, class... Args>
-int launch_dense(void (*kernel)(Params...), dim3 grid, unsigned threads, unsigned cluster, int smem, cudaStream_t s,
+int launch_dense(void (*kernel)(Params...), dim3 grid, unsigned threads, unsigned cluster, bool early, int smem, cudaStream_t s,
                  Args&&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
@@ -251,13 +254,13 @@ int launch_dense(void (*kernel)(Params...), dim3 grid, unsigned threads, unsigne
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = early ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
     if (e != cudaSuccess) {
         note_cuda_error(e);

@@ -263,13 +263,13 @@ static int launch_dropout(DropoutParams& p, cudaStream_t s) {
         if (strips > INT32_MAX / kShares) return ZERO_ERANGE;
         if constexpr (kGrad)
             if (p.db)
-                return launch_dense(dropout_strip_kernel<true, true>, dim3((unsigned)(strips * kShares)), kThreads, kShares, 0, s, p,
+                return launch_dense(dropout_strip_kernel<true, true>, dim3((unsigned)(strips * kShares)), kThreads, kShares, false, 0, s, p,
                                     (int)kShares);
         // enough shares of at least 32 rows to fill the GPU about four times over
         int64_t shares = (int64_t)sm_count() * 32 / strips;
         shares = shares < 1 ? 1 : shares > most ? most : shares;
         if (strips > INT32_MAX / shares) return ZERO_ERANGE;
-        return launch_dense(dropout_strip_kernel<kGrad, false>, dim3((unsigned)(strips * shares)), kThreads, 1, 0, s, p,
+        return launch_dense(dropout_strip_kernel<kGrad, false>, dim3((unsigned)(strips * shares)), kThreads, 1, true, 0, s, p,
                             (int)shares);
     }
     // lanes of a warp along a row
@@ -284,7 +284,7 @@ static int launch_dropout(DropoutParams& p, cudaStream_t s) {
             if (lanes < 8) lanes = 8;   // at least a column for each CTA of a cluster
             const int64_t col_warps = (p.col_blocks + lanes - 1) / lanes;
             if (col_warps > INT32_MAX / kShares) return ZERO_ERANGE;
-            return launch_dense(kernel, dim3((unsigned)(col_warps * kShares)), kThreads, kShares, 0, s, p, lanes, (int)col_warps,
+            return launch_dense(kernel, dim3((unsigned)(col_warps * kShares)), kThreads, kShares, false, 0, s, p, lanes, (int)col_warps,
                                 (int64_t)kShares * (kThreads / 32) * (32 / lanes));
         }
     // as many groups of rows as give every thread a batch, up to the warps that are
@@ -298,7 +298,7 @@ static int launch_dropout(DropoutParams& p, cudaStream_t s) {
     row_groups = row_groups < 1 ? 1 : row_groups > groups ? groups : row_groups;
     const int64_t grid = (row_groups * col_warps + kThreads / 32 - 1) / (kThreads / 32);
     if (grid > INT32_MAX) return ZERO_ERANGE;
-    return launch_dense(kernel, dim3((unsigned)grid), kThreads, 1, 0, s, p, lanes, (int)col_warps, row_groups * rows_of_warp);
+    return launch_dense(kernel, dim3((unsigned)grid), kThreads, 1, true, 0, s, p, lanes, (int)col_warps, row_groups * rows_of_warp);
 }
 
 int launch_column_sum(int64_t rows, int64_t cols, const uint16_t* dz, int64_t lddz, const void* db_acc, void* db,

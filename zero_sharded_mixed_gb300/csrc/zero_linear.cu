@@ -930,7 +930,7 @@ static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
     q.e = e;
     if (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
     const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
-    return launch_dense(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, 2, kPairSmem, s, q);
+    return launch_dense(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, 2, true, kPairSmem, s, q);
 }
 
 static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream_t s) {
@@ -952,7 +952,7 @@ static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream
     q.e = e;
     q.box_a = p.rows < 128 ? (int32_t)((p.rows + 7) / 8 * 8) : 128;
     if (!soft && (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
-    return launch_dense(kernel, dim3((unsigned)(tiles * parts)), kSplitThreads, (unsigned)parts, kSplitSmem, s, q);
+    return launch_dense(kernel, dim3((unsigned)(tiles * parts)), kSplitThreads, (unsigned)parts, true, kSplitSmem, s, q);
 }
 
 static int launch_product(const Product& p, Ending& e, cudaStream_t s) {

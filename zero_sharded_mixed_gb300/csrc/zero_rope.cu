@@ -186,7 +186,7 @@ static int launch_rope(RopeParams& p, cudaStream_t s) {
     const int64_t gx = (p.tokens + p.cta_tokens - 1) / p.cta_tokens, gy = (p.heads + p.cta_heads - 1) / p.cta_heads;
     if (gx > INT32_MAX || gy > 65535) return ZERO_ERANGE;
     return launch_dense(vec ? rope_kernel<kF32, kHalf, true> : rope_kernel<kF32, kHalf, false>, dim3((unsigned)gx, (unsigned)gy),
-                        kThreads, 1, 0, s, p);
+                        kThreads, 1, true, 0, s, p);
 }
 
 }  // namespace zgb

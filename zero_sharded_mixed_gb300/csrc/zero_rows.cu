@@ -111,7 +111,7 @@ static int launch_rows_of(const Product& p, const Ending& e, cudaStream_t s) {
     const int64_t grid = (pairs * split + kWarps - 1) / kWarps;
     if (grid > INT32_MAX) return ZERO_ERANGE;
     const bool aligned = rows_aligned16(p.b.p, p.b.ld, 2) && (p.rows == 1 ? aligned16(p.a.p) : rows_aligned16(p.a.p, p.a.ld, 2));
-    return launch_dense(aligned ? rows_kernel<kM, kF32, true> : rows_kernel<kM, kF32, false>, dim3((unsigned)grid), kThreads, 1, 0,
+    return launch_dense(aligned ? rows_kernel<kM, kF32, true> : rows_kernel<kM, kF32, false>, dim3((unsigned)grid), kThreads, 1, true, 0,
                         s, p, e, split);
 }
 
