@@ -81,44 +81,60 @@ int launch_column_sum(int64_t rows, int64_t cols, const uint16_t* dz, int64_t ld
                       bool db_f32, cudaStream_t s);
 
 // ---- activations ------------------------------------------------------------
-// Evaluated in fp32.  The tanh form of the GELU is x sigmoid(2u), which like the
-// SiLU needs one exponential and one division; the fast forms of both (relative
-// error about 2^-21) are far inside the rounding of a bf16 result and of an fp32
-// one's tolerance.
-__device__ __forceinline__ float sigmoid_f(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
-constexpr float kGeluC = 0.79788456080286535588f;   // sqrt(2 / pi)
+// Evaluated in fp32.  The tanh form of the GELU is z sigmoid(2u), which like the
+// SiLU needs one base-2 exponential (its factor folded into the polynomial) and one
+// reciprocal; the approximate forms of both (about 2^-22 relative) are far inside
+// the rounding of a bf16 result and of an fp32 one's tolerance.
+__device__ __forceinline__ float exp2_f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_f(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Past the clamps the second term of a slope is below fp32's resolution; without
+// them it would be 0 * infinity.  A NaN stays.
+__device__ __forceinline__ float clamp_keep_nan(float z, float c) {
+    float y;
+    asm("{\n\tmin.NaN.f32 %0, %1, %2;\n\tmax.NaN.f32 %0, %0, %3;\n\t}" : "=&f"(y) : "f"(z), "f"(c), "f"(-c));
+    return y;
+}
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kGelu2C = 2.0f * 0.79788456080286535588f;   // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
+
+__device__ __forceinline__ float sigmoid_2u(float z) {   // sigmoid(2 sqrt(2 / pi) (z + kGeluA z^3))
+    return rcp_f(1.0f + exp2_f(z * (-kGelu2C * kLog2E - kGelu2C * kLog2E * kGeluA * (z * z))));
+}
 
 template <int kAct>
 __device__ __forceinline__ float act_one(float z) {
     if constexpr (kAct == ZERO_ACT_RELU) return z < 0.0f ? 0.0f : z;   // a NaN stays
     if constexpr (kAct == ZERO_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
-    if constexpr (kAct == ZERO_ACT_GELU_TANH)
-        return __fdividef(z, 1.0f + __expf(-2.0f * kGeluC * (z + kGeluA * z * z * z)));
-    if constexpr (kAct == ZERO_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+    if constexpr (kAct == ZERO_ACT_GELU_TANH) return z * sigmoid_2u(z);
+    if constexpr (kAct == ZERO_ACT_SILU) return z * rcp_f(1.0f + exp2_f(-kLog2E * z));
     return z;
 }
-
-// Past the clamps the second term of a slope is below fp32's resolution; without
-// them it would be 0 * infinity.  A NaN passes both comparisons and stays.
-__device__ __forceinline__ float clamp_keep_nan(float z, float c) { return z > c ? c : z < -c ? -c : z; }
 
 template <int kAct>
 __device__ __forceinline__ float slope_one(float z) {
     if constexpr (kAct == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
     if constexpr (kAct == ZERO_ACT_GELU) {
         z = clamp_keep_nan(z, 20.0f);
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) + z * 0.39894228040143267794f * __expf(-0.5f * z * z);
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) + z * 0.39894228040143267794f * exp2_f(-0.5f * kLog2E * z * z);
     }
     if constexpr (kAct == ZERO_ACT_GELU_TANH) {
         z = clamp_keep_nan(z, 20.0f);
-        const float s = sigmoid_f(2.0f * kGeluC * (z + kGeluA * z * z * z));
-        return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+        const float s = sigmoid_2u(z);
+        return s + (s - s * s) * (z * (kGelu2C + 3.0f * kGelu2C * kGeluA * (z * z)));
     }
     if constexpr (kAct == ZERO_ACT_SILU) {
         z = clamp_keep_nan(z, 104.0f);   // past 89 the exponential is already infinite
-        const float s = sigmoid_f(z);
-        return s * (1.0f + z * (1.0f - s));
+        const float s = rcp_f(1.0f + exp2_f(-kLog2E * z));
+        return s + (s - s * s) * z;
     }
     return 1.0f;
 }

@@ -67,28 +67,35 @@ __device__ __forceinline__ void quad_transpose(uint4& u) {
     u = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// fp32: between the fragment's two columns of groups g and g + 1 (g even) and four
+// columns of one of them, group g in even lanes and g + 1 in odd ones, which start
+// pair_column() after the first of the 32 columns (plus 8 g).  Its own inverse.
+__device__ __forceinline__ void pair_exchange(float (&v)[4][4]) {
+    const bool odd = threadIdx.x & 1;
+#pragma unroll
+    for (int g = 0; g < 4; g += 2)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float r = __shfl_xor_sync(0xffffffffu, odd ? v[g][c] : v[g + 1][c], 1);
+            v[g][c] = odd ? r : v[g][c];
+            v[g + 1][c] = odd ? v[g + 1][c] : r;
+        }
+}
+__device__ __forceinline__ int pair_column() { return 8 * (threadIdx.x & 1) + 4 * ((threadIdx.x & 3) >> 1); }
+
 template <bool kF32>
 struct FragmentEnd {
-    uint4 slope[2], add[2];             // rows i and i + 8: group j
-    float2 add32[kF32 ? 4 : 1][2];      // fp32: the fragment's own columns
+    uint4 slope[2], add[2];             // rows i and i + 8: group j (an fp32 residual is read where it is added)
     bool in[2];
 
     __device__ __forceinline__ void load(const Ending& e, int64_t row, int64_t col0, int64_t rows) {
         const int j = threadIdx.x & 3;
         in[0] = row < rows;
         in[1] = row + 8 < rows;
-        if (e.add) {
+        if (!kF32 && e.add) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t at = (row + 8 * h) * e.ld_add + col0;
-                if (!in[h]) continue;
-                if constexpr (kF32) {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) add32[g][h] = *reinterpret_cast<const float2*>(static_cast<const float*>(e.add) + at + 8 * g + 2 * j);
-                } else {
-                    add[h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.add) + at + 8 * j);
-                }
-            }
+            for (int h = 0; h < 2; ++h)
+                if (in[h]) add[h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.add) + (row + 8 * h) * e.ld_add + col0 + 8 * j);
         }
         if (e.slope) {
 #pragma unroll
@@ -109,7 +116,7 @@ struct FragmentEnd {
         }
     }
 
-    __device__ __forceinline__ void finish(const Ending& e, uint32_t step, int64_t row, int64_t col0, float (&v)[4][4]) {
+    __device__ __forceinline__ void finish(const Ending& e, uint32_t step, int64_t row, int64_t col0, float (&v)[4][4], bool add_it = true) {
         const int j = threadIdx.x & 3;
         if (e.bias) {
 #pragma unroll
@@ -147,14 +154,30 @@ struct FragmentEnd {
             }
         }
         if constexpr (kF32) {
-            float* q = static_cast<float*>(e.out) + row * e.ld_out + col0 + 2 * j;
+            // sixteen bytes a lane: a vector holds four columns of one group
+            pair_exchange(v);
+            const int64_t at = col0 + pair_column();
+            float* q = static_cast<float*>(e.out) + row * e.ld_out + at;
+            const float* r = static_cast<const float*>(e.add) + row * e.ld_add + at;
 #pragma unroll
-            for (int h = 0; h < 2; ++h, q += 8 * e.ld_out) {
+            for (int h = 0; h < 2; ++h, q += 8 * e.ld_out, r += 8 * e.ld_add) {
+                if (!in[h]) continue;
+                if (e.add && add_it) {
+                    float4 t[2];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    if (e.add) v[g][2 * h] += add32[g][h].x, v[g][2 * h + 1] += add32[g][h].y;
-                    if (in[h]) *reinterpret_cast<float2*>(q + 8 * g) = make_float2(v[g][2 * h], v[g][2 * h + 1]);
+                    for (int p = 0; p < 2; ++p) t[p] = *reinterpret_cast<const float4*>(r + 16 * p);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        v[2 * p][2 * h] += t[p].x;
+                        v[2 * p][2 * h + 1] += t[p].y;
+                        v[2 * p + 1][2 * h] += t[p].z;
+                        v[2 * p + 1][2 * h + 1] += t[p].w;
+                    }
                 }
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    *reinterpret_cast<float4*>(q + 16 * p) =
+                        make_float4(v[2 * p][2 * h], v[2 * p][2 * h + 1], v[2 * p + 1][2 * h], v[2 * p + 1][2 * h + 1]);
             }
         } else {
             if (e.add) {
@@ -250,51 +273,57 @@ struct VectorEnd {
 __device__ __forceinline__ float element(float x) { return x; }
 __device__ __forceinline__ float element(uint16_t x) { return bf16_one(x); }
 
-// A unit whose rows are not aligned, or whose columns end inside a group: a lane a
-// column, row by row, so that a row's accesses still fall together.  v: this lane's
-// accumulators of the 8 rows; every lane of the warp calls.
-template <bool kF32>
+// Rows that are not aligned, or whose columns end inside a group: a lane a column, row
+// by row, so that a row's accesses still fall together.  v: this lane's accumulators
+// of kRows rows; every lane of the warp calls.
+template <bool kF32, int kRows>
 __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
-                                         float (&v)[8]) {
+                                         float (&v)[kRows]) {
+    using T = typename std::conditional<kF32, float, uint16_t>::type;
     const int lane = threadIdx.x & 31;
     const int64_t col = col0 + lane;
-    const float bias = e.bias && col < cols ? bf16_one(e.bias[col]) : 0.0f;
-    uint4 block = make_uint4(0u, 0u, 0u, 0u);   // lane l forms the bits of row l % 8 and column group l / 8
-    if (e.drop.cut) block = philox_block(e.drop, step, (uint32_t)(row0 + (lane & 7)), (uint32_t)((col0 >> 3) + (lane >> 3)));
-    // rows of this unit that exist, none where the column does not: one comparison a row
-    const int n = col < cols ? (rows - row0 < 8 ? (int)(rows - row0) : 8) : 0;
-    float t[8];
+    // rows that exist, none where the column does not: one comparison a row
+    const int n = col < cols ? (rows - row0 < kRows ? (int)(rows - row0) : kRows) : 0;
+    if (e.bias) {
+        const float bias = col < cols ? bf16_one(e.bias[col]) : 0.0f;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) v[r] += bias;
-    if (e.pre) {
-        uint16_t* q = e.pre + row0 * e.ld_pre + col;
-#pragma unroll
-        for (int r = 0; r < 8; ++r, q += e.ld_pre)
-            if (r < n) *q = to_bf16(v[r]);
+        for (int r = 0; r < kRows; ++r) v[r] += bias;
     }
-    if (e.slope) {
-        const uint16_t* q = e.slope + row0 * e.ld_slope + col;
+    if (!e.bare) {   // one branch for the common case of none of these
+        float t[kRows];
+        if (e.pre) {
+            uint16_t* q = e.pre + row0 * e.ld_pre + col;
 #pragma unroll
-        for (int r = 0; r < 8; ++r, q += e.ld_slope) t[r] = r < n ? bf16_one(*q) : 0.0f;
-        slope_apply<8>(e.act, t, v);
-    } else if (e.act) {
-        act_apply<8>(e.act, v);
-    }
-    if (e.drop.cut) {
+            for (int r = 0; r < kRows; ++r, q += e.ld_pre)
+                if (r < n) *q = to_bf16(v[r]);
+        }
+        if (e.slope) {
+            const uint16_t* q = e.slope + row0 * e.ld_slope + col;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = row_bits(block, r) >= e.drop.cut ? v[r] * e.drop.scale : 0.0f;
-    }
-    using T = typename std::conditional<kF32, float, uint16_t>::type;
-    if (e.add) {
-        const T* q = static_cast<const T*>(e.add) + row0 * e.ld_add + col;
+            for (int r = 0; r < kRows; ++r, q += e.ld_slope) t[r] = r < n ? bf16_one(*q) : 0.0f;
+            slope_apply<kRows>(e.act, t, v);
+        } else if (e.act) {
+            act_apply<kRows>(e.act, v);
+        }
+        if (e.drop.cut) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r, q += e.ld_add) t[r] = r < n ? element(*q) : 0.0f;
+            for (int r0 = 0; r0 < kRows; r0 += 8) {   // lane l forms the bits of row l % 8 and column group l / 8
+                const uint4 block = philox_block(e.drop, step, (uint32_t)(row0 + r0 + (lane & 7)), (uint32_t)((col0 >> 3) + (lane >> 3)));
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] += t[r];
+                for (int r = 0; r < 8; ++r) v[r0 + r] = row_bits(block, r) >= e.drop.cut ? v[r0 + r] * e.drop.scale : 0.0f;
+            }
+        }
+        if (e.add) {
+            const T* q = static_cast<const T*>(e.add) + row0 * e.ld_add + col;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r, q += e.ld_add) t[r] = r < n ? element(*q) : 0.0f;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) v[r] += t[r];
+        }
     }
     T* q = static_cast<T*>(e.out) + row0 * e.ld_out + col;
 #pragma unroll
-    for (int r = 0; r < 8; ++r, q += e.ld_out)
+    for (int r = 0; r < kRows; ++r, q += e.ld_out)
         if (r < n) {
             if constexpr (kF32)
                 *q = v[r];
@@ -326,16 +355,26 @@ struct PairParams {
     CUtensorMap map_a, map_b;
     int64_t rows, cols, depth;
     int32_t tiles_m, tiles_n, bn, k_blocks;
+    int32_t run;   // blocks after which an accumulator is handed over
     bool a_mn, b_mn;
     Ending e;
 };
 
 constexpr int kStageBytes = 32768;      // 128 rows of A and 128 of B, 64 reduced elements each
-constexpr int kPairStages = 5;
+constexpr int kPairStages = 6;
 constexpr int kEndWarps = 16;
 constexpr int kPairThreads = 128 + 32 * kEndWarps;
 constexpr int kChunkBytes = 4096;       // 32 x 32 fp32
-constexpr int kPairSmem = 1024 + kPairStages * kStageBytes + kEndWarps * kChunkBytes + 256;
+constexpr int kUnitBytes = 2048;        // 16 x 32 fp32
+constexpr int kPairSmem = 1024 + kPairStages * kStageBytes + kEndWarps * kUnitBytes + 256;
+// fp32 results: the tensor core cuts its sums where an fp32 addition would round
+// them, and 100 additions in a row were off by 1.6e-6 of the result, five times a
+// plain fp32 sum's error.  Their accumulators are therefore read after at most kRun
+// blocks and added up in registers (0.75e-6), 48 of them a thread, which fixes the
+// widest tile.  A bf16 result's own rounding is a thousand times larger.
+constexpr int kRun = 13;                // blocks of 64 reduced elements
+constexpr int kUnits = 4;               // 16 x 32 parts of a tile that a warp ends
+constexpr int kWidest = 256, kWidestF32 = kUnits * 4 * 16;
 constexpr int kRasterRows = 8;          // row tiles that are gone through together
 
 __device__ __forceinline__ void tile_place(const PairParams& p, int t, int* tm, int* tn) {
@@ -358,11 +397,46 @@ __device__ __forceinline__ void release(uint64_t* bar) {
 }
 
 template <bool kF32>
+__device__ __forceinline__ void prefetch_sides(const PairParams& p, int t, uint32_t rank, int q, int h) {
+    int tm, tn;
+    tile_place(p, t, &tm, &tn);
+    const int64_t row = (int64_t)tm * 256 + rank * 128 + q * 32 + (threadIdx.x & 31);
+    if (row >= p.rows) return;
+    const int n = tile_width(p, tn) / 32;
+    for (int c = h; c < n; c += 4) {
+        const int64_t col = (int64_t)tn * p.bn + c * 32;
+        if (col >= p.cols) break;
+        if (p.e.add) l2_prefetch(static_cast<const char*>(p.e.add) + (row * p.e.ld_add + col) * (kF32 ? 4 : 2));
+        if (p.e.slope) l2_prefetch(p.e.slope + row * p.e.ld_slope + col);
+    }
+}
+
+// 16 rows x 32 columns that are not aligned or not whole: through 2 KB of shared
+// memory to a lane a column.
+template <bool kF32>
+__device__ __forceinline__ void end_staged(const Ending& e, uint32_t step, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                           const float (&v)[4][4], uint8_t* chunk) {
+    const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
+    __syncwarp();   // the last unit's readers are done
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int group = 2 * g + (j >> 1), in = (j & 1) * 8;
+        *reinterpret_cast<float2*>(chunk + group_place(i, group) + in) = make_float2(v[g][0], v[g][1]);
+        *reinterpret_cast<float2*>(chunk + group_place(i + 8, group) + in) = make_float2(v[g][2], v[g][3]);
+    }
+    __syncwarp();
+    float t[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) t[r] = *reinterpret_cast<const float*>(chunk + group_place(r, lane >> 2) + (lane & 3) * 4);
+    end_rows<kF32, 16>(e, step, row0, col0, rows, cols, t);
+}
+
+template <bool kF32>
 __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
     uint8_t* chunks = smem + kPairStages * kStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kEndWarps * kChunkBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kEndWarps * kUnitBytes);
     uint64_t* empty = full + kPairStages;
     uint64_t* acc_full = empty + kPairStages;
     uint64_t* acc_empty = acc_full + 2;
@@ -437,93 +511,132 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
                 if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
             }
     } else if (warp == 1 && rank == 0) {
-        int s = 0, n_tile = 0;
+        int s = 0, use = 0;   // use: accumulators handed over so far
         uint32_t round = 0;
         bool ok = true;
         const uint32_t a_step = descriptor_step(p.a_mn), b_step = descriptor_step(p.b_mn);
-        for (int t = pair; ok && t < tiles; t += pairs, ++n_tile) {
+        for (int t = pair; ok && t < tiles; t += pairs) {
             int tm, tn;
             tile_place(p, t, &tm, &tn);
             const uint32_t idesc = instruction_descriptor(256, tile_width(p, tn), p.a_mn, p.b_mn);
-            const int buf = n_tile & 1;
-            if (n_tile >= 2 && !(ok = warp_wait(acc_empty + buf, (n_tile / 2 - 1) & 1))) break;
-            tcgen05_fence_after();
-            const uint32_t d = tmem + buf * 256;
-            for (int kb = 0; kb < p.k_blocks; ++kb) {
-                if (!(ok = warp_wait(full + s, round & 1))) break;
+            for (int first = 0; ok && first < p.k_blocks; first += p.run, ++use) {
+                const int buf = use & 1, end = first + p.run < p.k_blocks ? first + p.run : p.k_blocks;
+                if (use >= 2 && !(ok = warp_wait(acc_empty + buf, (use / 2 - 1) & 1))) break;
                 tcgen05_fence_after();
-                const uint32_t a = smem_addr(smem + s * kStageBytes);
-                const uint64_t da = smem_descriptor(a, p.a_mn), db = smem_descriptor(a + 16384, p.b_mn);
-                const int64_t left = p.depth - (int64_t)kb * 64;
-                if (elect_one()) {
+                const uint32_t d = tmem + buf * 256;
+                for (int kb = first; kb < end; ++kb) {
+                    if (!(ok = warp_wait(full + s, round & 1))) break;
+                    tcgen05_fence_after();
+                    const uint32_t a = smem_addr(smem + s * kStageBytes);
+                    const uint64_t da = smem_descriptor(a, p.a_mn), db = smem_descriptor(a + 16384, p.b_mn);
+                    const int64_t left = p.depth - (int64_t)kb * 64;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)   // the last step of all may end early
-                        if (left > 16 * i) mma_bf16<true>(d, da + i * a_step, db + i * b_step, idesc, kb + i > 0);
-                    mma_commit<true>(empty + s);
+                        for (int i = 0; i < 4; ++i)   // the last step of all may end early
+                            if (left > 16 * i) mma_bf16<true>(d, da + i * a_step, db + i * b_step, idesc, kb > first || i > 0);
+                        mma_commit<true>(empty + s);
+                    }
+                    if (++s == kPairStages) s = 0, ++round;
                 }
-                if (++s == kPairStages) s = 0, ++round;
+                if (ok && elect_one()) mma_commit<true>(acc_full + buf);
             }
-            if (ok && elect_one()) mma_commit<true>(acc_full + buf);
         }
         if (!ok) {   // products in flight end before the tensor memory is freed
             if (elect_one()) mma_commit<true>(drained);
             (void)mbar_wait_bounded(drained, 0, kWaitCycles / 8);
         }
     } else if (warp >= 4) {
+        // units of 16 rows x 32 columns: this warp's are every fourth of its 32 rows'
         const int w = warp - 4, q = warp & 3, h = w / 4;
-        uint8_t* chunk = chunks + w * kChunkBytes;
+        uint8_t* chunk = chunks + w * kUnitBytes;
         const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
-        int n_tile = 0;
-        for (int t = pair; t < tiles; t += pairs, ++n_tile) {
+        int use = 0;   // accumulators read so far
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
             int tm, tn;
             tile_place(p, t, &tm, &tn);
-            const int buf = n_tile & 1, width = tile_width(p, tn);
             const int64_t row0 = (int64_t)tm * 256 + rank * 128 + q * 32, col_tile = (int64_t)tn * p.bn;
-            const int n_chunks = width / 32;
-            if ((p.e.add || p.e.slope) && row0 + lane < p.rows)   // on their way to L2 while the product runs
-                for (int c = h; c < n_chunks; c += kEndWarps / 4) {
-                    const int64_t col = col_tile + c * 32;
-                    if (col >= p.cols) break;
-                    if (p.e.add) l2_prefetch(static_cast<const char*>(p.e.add) + ((row0 + lane) * p.e.ld_add + col) * (kF32 ? 4 : 2));
-                    if (p.e.slope) l2_prefetch(p.e.slope + (row0 + lane) * p.e.ld_slope + col);
+            const int units = tile_width(p, tn) / 16;
+            // what the end reads beside the accumulators, on its way to L2 while the product
+            // runs (a tile ahead was slower: the reads then stand in the operands' way)
+            if (p.e.add || p.e.slope) prefetch_sides<kF32>(p, t, rank, q, h);
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+            const auto place = [&](int buf, int u) { return lanes + buf * 256 + (u >> 1) * 32 + ((uint32_t)((u & 1) * 16) << 16); };
+            if constexpr (kF32) {
+                float acc[kUnits][4][4];
+                // a residual that only the sum meets is where the sum starts: its loads
+                // are done while the product runs
+                const bool early = p.e.vec && p.e.add && !p.e.act && !p.e.pre && !p.e.slope && !p.e.drop.cut;
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    const int u = h + 4 * i;
+                    const int64_t row = row0 + (u & 1) * 16 + (lane >> 2), col0 = col_tile + (u >> 1) * 32;
+                    const bool starts = early && u < units && col0 + 32 <= p.cols;
+#pragma unroll
+                    for (int g = 0; g < 4; g += 2)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (starts && row + 8 * r < p.rows)
+                                t = *reinterpret_cast<const float4*>(static_cast<const float*>(p.e.add) + (row + 8 * r) * p.e.ld_add + col0 + 8 * g + pair_column());
+                            acc[i][g][2 * r] = t.x;
+                            acc[i][g][2 * r + 1] = t.y;
+                            acc[i][g + 1][2 * r] = t.z;
+                            acc[i][g + 1][2 * r + 1] = t.w;
+                        }
                 }
-            if (!warp_wait(acc_full + buf, (n_tile / 2) & 1)) break;
-            tcgen05_fence_after();
-            for (int c = h; c < n_chunks; c += kEndWarps / 4) {
-                const int64_t col0 = col_tile + c * 32;
-                const bool vec = p.e.vec && col0 + 32 <= p.cols;
-                const uint32_t taddr = tmem + buf * 256 + c * 32 + ((uint32_t)(q * 32) << 16);
-                const bool last = c + kEndWarps / 4 >= n_chunks;   // this warp's last read of the buffer
-                if (vec) {
-#pragma unroll 1
-                    for (int i = 0; i < 2; ++i) {
-                        FragmentEnd<kF32> end;
-                        const int64_t row = row0 + 16 * i + (lane >> 2);
+                for (int kb = 0; kb < p.k_blocks; kb += p.run, ++use) {
+                    const int buf = use & 1;
+                    if (!(ok = warp_wait(acc_full + buf, (use / 2) & 1))) break;
+                    tcgen05_fence_after();
+#pragma unroll
+                    for (int i = 0; i < kUnits; ++i) {
+                        if (h + 4 * i >= units) continue;
                         float v[4][4];
-                        end.load(p.e, row, col0, p.rows);
-                        tmem_load_fragment(taddr + ((uint32_t)(16 * i) << 16), v);
-                        if (last && i) release(acc_empty + buf);
-                        end.finish(p.e, step, row, col0, v);
-                    }
-                } else {
-                    uint32_t acc[32];
-                    tmem_load32(taddr, acc);
-                    if (last) release(acc_empty + buf);
-                    __syncwarp();   // the chunk's previous readers are done
+                        tmem_load_fragment(place(buf, h + 4 * i), v);
+                        if (kb == 0 && early) pair_exchange(acc[i]);
 #pragma unroll
-                    for (int g = 0; g < 8; ++g)
-                        *reinterpret_cast<uint4*>(chunk + group_place(lane, g)) = make_uint4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
-                    __syncwarp();
-                    for (int i = 0; i < 4; ++i) {
-                        float v[8];
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            v[r] = *reinterpret_cast<const float*>(chunk + group_place(i * 8 + r, lane >> 2) + (lane & 3) * 4);
-                        end_rows<kF32>(p.e, step, row0 + i * 8, col0, p.rows, p.cols, v);
+                        for (int g = 0; g < 16; ++g) acc[i][g / 4][g % 4] += v[g / 4][g % 4];
                     }
+                    release(acc_empty + buf);
                 }
+                if (!ok) break;
+#pragma unroll 1
+                for (int u = h; u < units; u += 4) {   // one copy of the code: three outgrow the instruction cache
+                    const int64_t row = row0 + (u & 1) * 16, col0 = col_tile + (u >> 1) * 32;
+                    FragmentEnd<kF32> end;
+                    if (p.e.vec && col0 + 32 <= p.cols) {
+                        end.load(p.e, row + (lane >> 2), col0, p.rows);
+                        end.finish(p.e, step, row + (lane >> 2), col0, acc[0], !early);
+                    } else {
+                        end_staged<kF32>(p.e, step, row, col0, p.rows, p.cols, acc[0], chunk);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 16; ++g)
+#pragma unroll
+                        for (int i = 0; i + 1 < kUnits; ++i) acc[i][g / 4][g % 4] = acc[i + 1][g / 4][g % 4];
+                }
+            } else {
+                const int buf = use & 1;
+                if (!(ok = warp_wait(acc_full + buf, (use / 2) & 1))) break;
+                tcgen05_fence_after();
+#pragma unroll 1
+                for (int u = h; u < units; u += 4) {
+                    const int64_t row = row0 + (u & 1) * 16, col0 = col_tile + (u >> 1) * 32;
+                    const bool vec = p.e.vec && col0 + 32 <= p.cols;
+                    FragmentEnd<kF32> end;
+                    float v[4][4];
+                    if (vec) end.load(p.e, row + (lane >> 2), col0, p.rows);
+                    tmem_load_fragment(place(buf, u), v);
+                    if (u + 4 >= units) release(acc_empty + buf);   // this warp's last read
+                    if (vec)
+                        end.finish(p.e, step, row + (lane >> 2), col0, v);
+                    else
+                        end_staged<kF32>(p.e, step, row, col0, p.rows, p.cols, v, chunk);
+                }
+                if (h >= units) release(acc_empty + buf);   // a narrow last tile: no unit for this warp
+                ++use;
             }
-            if (h >= n_chunks) release(acc_empty + buf);   // a narrow last tile: no chunk for this warp
         }
     }
     tcgen05_fence_before();
@@ -849,7 +962,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
 #pragma unroll
                     for (int r = 0; r < 8; ++r) v[r] += peer_load1(at + group_place(r0 + r, lane >> 2));
                 }
-                end_rows<kF32>(p.e, step, row0, col0, p.rows, p.cols, v);
+                end_rows<kF32, 8>(p.e, step, row0, col0, p.rows, p.cols, v);
             }
         }
     }
@@ -918,7 +1031,7 @@ static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
     const int pairs = sm_count() / 2;
     // the tile width whose waves of pairs cover the columns with the least work
     int64_t best = INT64_MAX;
-    const int64_t fewest = (p.cols + 255) / 256;
+    const int64_t widest = e.out_f32 ? kWidestF32 : kWidest, fewest = (p.cols + widest - 1) / widest;
     for (int64_t tn = fewest; tn < fewest + 4; ++tn) {
         const int64_t bn = ((p.cols + tn - 1) / tn + 31) / 32 * 32;
         const int64_t n = (p.cols + bn - 1) / bn;
@@ -926,6 +1039,8 @@ static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
         if (cost < best) best = cost, q.bn = (int32_t)bn, q.tiles_n = (int32_t)n;
     }
     q.k_blocks = (int32_t)((p.depth + 63) / 64);
+    const int runs = e.out_f32 ? (q.k_blocks + kRun - 1) / kRun : 1;
+    q.run = (q.k_blocks + runs - 1) / runs;
     q.a_mn = p.a.mn; q.b_mn = p.b.mn;
     q.e = e;
     if (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
@@ -947,6 +1062,8 @@ static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream
     const int64_t tiles_n = (p.cols + q.bn - 1) / q.bn, tiles = tiles_m * tiles_n, k_blocks = (p.depth + 63) / 64;
     int parts = 1;
     while (parts < 8 && tiles * parts * 2 <= resident && k_blocks >= parts * 4) parts *= 2;
+    if (e.out_f32)   // short runs of the tensor core's sums, as in the pair kernel
+        while (parts < 8 && k_blocks > (int64_t)parts * kRun) parts *= 2;
     if (tiles > INT32_MAX / 8 || k_blocks > INT32_MAX) return ZERO_ERANGE;
     q.tiles_m = (int32_t)tiles_m; q.tiles_n = (int32_t)tiles_n; q.k_blocks = (int32_t)k_blocks;
     q.e = e;
@@ -960,6 +1077,7 @@ static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
     e.vec = aligned16(e.bias) && (!e.slope || rows_aligned16(e.slope, e.ld_slope, 2)) && (!e.pre || rows_aligned16(e.pre, e.ld_pre, 2)) &&
             (!e.add || rows_aligned16(e.add, e.ld_add, size)) && rows_aligned16(e.out, e.ld_out, size);
     if (p.rows <= kMostRows && !p.a.mn && !p.b.mn) return launch_rows(p, e, s);
+    e.bare = !e.pre && !e.slope && !e.act && !e.drop.cut && !e.add;
     const bool reach = copies_reach(p.a) && copies_reach(p.b);
     const int64_t pair_tiles = ((p.rows + 255) / 256) * ((p.cols + 255) / 256);
     if (reach && pair_tiles >= sm_count() / 4 && pair_tiles < INT32_MAX / 8) return launch_pair(p, e, s);

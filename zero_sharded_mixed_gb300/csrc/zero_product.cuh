@@ -27,6 +27,7 @@ struct Ending {
     int32_t act;
     bool out_f32;
     bool vec;                                   // every matrix above keeps 8-column groups on 16-byte boundaries
+    bool bare;                                  // nothing but a bias beside the product
     DropParams drop;
 };
 
