@@ -276,11 +276,12 @@ def zero_comm_bytes(n, n_dp, stage, param_bytes=2.0, grad_bytes=2.0) -> float:
 # The current stream's handle without a Stream object around it (3 us a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device_index = getattr(torch._C, "_cuda_getDevice", None)
+_cuda_ready = torch.cuda.is_initialized
 
 
 def _stream_ptr(stream) -> int | None:
     if stream is None:
-        if _raw_stream is not None and _device_index is not None and torch.cuda.is_initialized():
+        if _raw_stream is not None and _device_index is not None and _cuda_ready():
             return _raw_stream(_device_index()) or None
         stream = torch.cuda.current_stream()
     if isinstance(stream, int):
@@ -291,12 +292,12 @@ def _stream_ptr(stream) -> int | None:
 def _tensor(t: torch.Tensor, name: str, dtype, min_numel: int, pinned_ok: bool = False) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if pinned_ok and t.device.type == "cpu":
+    if not t.is_cuda:
+        if not (pinned_ok and t.device.type == "cpu"):
+            raise ValueError(f"{name} must be a CUDA tensor (got {t.device}); there is no CPU path")
         if not t.is_pinned():
             raise ValueError(f"{name} is host memory but not pinned; the kernels read only "
                              "device memory or pinned host memory")
-    elif t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor (got {t.device}); there is no CPU path")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -641,12 +642,12 @@ def _matrix(t, name, rows, cols, dtypes):
         return None, cols, ZERO_BF16
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (got {t.device}); there is no CPU path")
     code = dtypes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
-    if t.shape != (rows, cols):
+    if code is None or not t.is_cuda or t.shape != (rows, cols):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (got {t.device}); there is no CPU path")
+        if code is None:
+            raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
         raise ValueError(f"{name} must have shape ({rows}, {cols}), got {tuple(t.shape)}")
     ld, inner = t.stride()
     if rows <= 1 or cols == 0:
