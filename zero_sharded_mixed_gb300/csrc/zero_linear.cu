@@ -667,125 +667,108 @@ constexpr int kSplitSmem = 1024 + kSplitStages * kStageBytes + 128;
 
 // What one of the 8 loading warps brings of an operand's tile: sub-tile rows r with
 // r % 8 == warp, 64 elements each from any element-aligned place, as the one or two
-// 16-byte blocks that hold a lane's 8 elements; 8 lanes a row, 4 rows at a time.  Rows
-// 8 apart lie 16 ld bytes apart, so a warp's rows all start at the same place `shift`
-// of a block: the blocks are shifted by branches that the warp takes together and one
-// funnel shift a word.  (Lanes with shifts of their own: 4400 cycles a stage.  A word
-// a lane, 6 instructions a row: 10000.)  K-major, sub-tile row r is tile row r;
-// MN-major, reduced row r % 64 at kept elements 64 (r / 64) on.
+// 16-byte blocks that hold a lane's 8 elements; 8 lanes a row, 4 rows (a quad) at a
+// time.  Rows 8 apart lie 16 ld bytes apart, so a warp's rows all start at the same
+// place `shift` of a block: the blocks are shifted by branches that the warp takes
+// together and one funnel shift a word.  (Lanes with shifts of their own: 4400 cycles
+// a stage.  A word a lane, 6 instructions a row: 10000.)  K-major, sub-tile row r is
+// tile row r; MN-major, reduced row r % 64 at kept elements 64 (r / 64) on.
 // Blocks reach up to 7 elements past a row's own, into its neighbours; the few that
 // would reach past the operand's own memory come element by element.
+__device__ __noinline__ uint4 fetch_elements(const uint16_t* e, int n) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) w[i / 2] |= (uint32_t)e[i] << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool kMn>
 struct SoftTile {
     const uint16_t* q;          // this lane's elements of rows `warp + 8 (lane / 8)` of the next stage
     int64_t step;               // elements to 32 rows on
     int row, rows;              // the operand row of q and their number, from the tile's first
     int extent;                 // kept elements from the tile's first, at most 128
     uint32_t shift;             // bytes
-    bool mn;
 
-    __device__ __forceinline__ SoftTile(const Operand& o, int64_t mn0, int64_t k0, int warp) : step(32 * o.ld), mn(o.mn) {
+    __device__ __forceinline__ SoftTile(const Operand& o, int64_t mn0, int64_t k0, int warp) : step(32 * o.ld) {
         const int lane = threadIdx.x & 31, g = lane & 7;
-        const int64_t first = o.mn ? k0 : mn0, left = (o.mn ? o.cols : o.rows) - mn0, more = o.rows - first;
+        const int64_t first = kMn ? k0 : mn0, left = (kMn ? o.cols : o.rows) - mn0, more = o.rows - first;
         row = warp + 8 * (lane >> 3);
         rows = more < INT32_MAX ? (int)more : INT32_MAX;
-        q = o.p + (first + row) * o.ld + (o.mn ? mn0 : k0) + 8 * g;
+        q = o.p + (first + row) * o.ld + (kMn ? mn0 : k0) + 8 * g;
         extent = left < 128 ? (int)left : 128;
         shift = (uint32_t)__shfl_sync(0xffffffffu, (int)(reinterpret_cast<uintptr_t>(q) & 15), 0);
     }
     // quad j of 4: where, and how many of the lane's 8 elements exist (any number at
     // least 8 or below 1 for all or none), `left` reduced ones from here on
-    __device__ __forceinline__ const uint16_t* place(int j) const { return mn ? q + (j & 1) * step + (j >> 1) * 64 : q + j * step; }
+    __device__ __forceinline__ const uint16_t* place(int j) const { return kMn ? q + (j & 1) * step + (j >> 1) * 64 : q + j * step; }
     __device__ __forceinline__ int count(int j, int left) const {
-        if (row + 32 * (mn ? j & 1 : j) >= rows) return 0;
-        return (mn ? extent - (j >> 1) * 64 : left) - 8 * (int)(threadIdx.x & 7);
+        if (row + 32 * (kMn ? j & 1 : j) >= rows) return 0;
+        return (kMn ? extent - (j >> 1) * 64 : left) - 8 * (int)(threadIdx.x & 7);
     }
-    // whether a block of a lane's elements reaches past the operand's memory, and
-    // whether any of a stage's tile (from mn0, k0) does
-    static __device__ __forceinline__ bool past(const Operand& o, uintptr_t first, uintptr_t last) {   // elements' addresses
-        return (first & ~(uintptr_t)15) < operand_begin(o) || (last & ~(uintptr_t)15) + 16 > operand_end(o);
+    // whether the blocks from that of one element to that of another (addresses) reach
+    // past the operand's memory, and whether any of a stage's tile (from mn0, k0) do
+    static __device__ __forceinline__ bool past(const Operand& o, const uint16_t* first, const uint16_t* last) {
+        return (reinterpret_cast<uintptr_t>(first) & ~(uintptr_t)15) < operand_begin(o) ||
+               (reinterpret_cast<uintptr_t>(last) & ~(uintptr_t)15) + 16 > operand_end(o);
     }
     static __device__ __forceinline__ bool at_edge(const Operand& o, int64_t mn0, int64_t k0) {
-        const int64_t r0 = o.mn ? k0 : mn0, c0 = o.mn ? mn0 : k0, r1 = r0 + (o.mn ? 63 : 127), c1 = c0 + (o.mn ? 127 : 63);
-        return past(o, reinterpret_cast<uintptr_t>(o.p + r0 * o.ld + c0),
-                    reinterpret_cast<uintptr_t>(o.p + (r1 < o.rows ? r1 : o.rows - 1) * o.ld + (c1 < o.cols ? c1 : o.cols - 1)));
+        const int64_t r0 = kMn ? k0 : mn0, c0 = kMn ? mn0 : k0, r1 = r0 + (kMn ? 63 : 127), c1 = c0 + (kMn ? 127 : 63);
+        return past(o, o.p + r0 * o.ld + c0, o.p + (r1 < o.rows ? r1 : o.rows - 1) * o.ld + (c1 < o.cols ? c1 : o.cols - 1));
+    }
+    __device__ __forceinline__ bool lone(const Operand& o, int j, int have) const {
+        return past(o, place(j), place(j) + (have < 8 ? have : 8) - 1);
     }
 
-    template <bool kEdge>
-    __device__ __forceinline__ void load(const Operand& o, int n, int left, Blocks8* b) const {
+    __device__ __forceinline__ void load(const Operand& o, bool edge, int n, int left, Blocks8* b) const {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             b[j].x = b[j].y = make_uint4(0u, 0u, 0u, 0u);
             if (32 * j >= n) continue;
-            const uint16_t* e = place(j);
             const int have = count(j, left);
-            if (kEdge && have > 0 && past(o, reinterpret_cast<uintptr_t>(e), reinterpret_cast<uintptr_t>(e + (have < 8 ? have : 8) - 1))) {
-                uint32_t w[4];   // in place: not to be shifted
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = (2 * i < have ? e[2 * i] : 0u) | (2 * i + 1 < have ? (uint32_t)e[2 * i + 1] << 16 : 0u);
-                b[j].x = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-                const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(e) - shift);
-                if (have > 0) b[j].x = at[0];
-                if ((int)shift + 2 * (have < 8 ? have : 8) > 16) b[j].y = at[1];
-            }
+            bool whole = have > 0;
+            if (edge && whole) whole = !lone(o, j, have);
+            const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(place(j)) - shift);
+            if (whole) b[j].x = at[0];
+            if (whole && (int)shift + 2 * (have < 8 ? have : 8) > 16) b[j].y = at[1];
         }
     }
-    template <bool kEdge, int kWords>
-    __device__ __forceinline__ void store_shifted(const Operand& o, int n, int left, const Blocks8* b, uint8_t* d) const {
+    __device__ __forceinline__ void store(const Operand& o, bool edge, int n, int left, const Blocks8* b, uint8_t* dst, int warp) const {
+        const int lane = threadIdx.x & 31;
+        uint8_t* d = dst + (warp + 8 * (lane >> 3)) * 128 + (((lane & 7) ^ warp) << 4);   // row % 8 is the warp
         const uint32_t bits = (shift & 2) * 8;
+        const bool by4 = shift & 4, by8 = shift & 8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (32 * j >= n) continue;
-            const uint32_t w[9] = {b[j].x.x, b[j].x.y, b[j].x.z, b[j].x.w, b[j].y.x, b[j].y.y, b[j].y.z, b[j].y.w, 0u};
-            uint32_t v[4];
+            uint32_t w[8] = {b[j].x.x, b[j].x.y, b[j].x.z, b[j].x.w, b[j].y.x, b[j].y.y, b[j].y.z, b[j].y.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(w[i + kWords], w[i + kWords + 1], bits);
+            for (int i = 0; i < 6; ++i) w[i] = by8 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = by4 ? w[i + 1] : w[i];
+            uint4 v = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                                 __funnelshift_r(w[3], w[4], bits));
             const int have = count(j, left);
             if (have < 8) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] &= have >= 2 * i + 2 ? 0xffffffffu : have == 2 * i + 1 ? 0xffffu : 0u;
+                v.x &= have >= 2 ? 0xffffffffu : have == 1 ? 0xffffu : 0u;
+                v.y &= have >= 4 ? 0xffffffffu : have == 3 ? 0xffffu : 0u;
+                v.z &= have >= 6 ? 0xffffffffu : have == 5 ? 0xffffu : 0u;
+                v.w &= have == 7 ? 0xffffu : 0u;
             }
-            if (kEdge && have > 0) {
-                const uint16_t* e = place(j);
-                if (past(o, reinterpret_cast<uintptr_t>(e), reinterpret_cast<uintptr_t>(e + (have < 8 ? have : 8) - 1)))
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = w[i];
-            }
-            *reinterpret_cast<uint4*>(d + j * 4096) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-    }
-    template <bool kEdge>
-    __device__ __forceinline__ void store(const Operand& o, int n, int left, const Blocks8* b, uint8_t* dst, int warp) const {
-        const int lane = threadIdx.x & 31;
-        uint8_t* d = dst + (warp + 8 * (lane >> 3)) * 128 + (((lane & 7) ^ warp) << 4);   // row % 8 is the warp
-        switch (shift >> 2) {
-            case 0: store_shifted<kEdge, 0>(o, n, left, b, d); break;
-            case 1: store_shifted<kEdge, 1>(o, n, left, b, d); break;
-            case 2: store_shifted<kEdge, 2>(o, n, left, b, d); break;
-            default: store_shifted<kEdge, 3>(o, n, left, b, d); break;
+            if (edge && have > 0 && lone(o, j, have)) v = fetch_elements(place(j), have);
+            *reinterpret_cast<uint4*>(d + j * 4096) = v;
         }
     }
     __device__ __forceinline__ void advance() {
-        q += mn ? 2 * step : 64;
-        rows -= mn ? 64 : 0;
+        q += kMn ? 2 * step : 64;
+        rows -= kMn ? 64 : 0;
     }
 };
 
-// One stage of both operands; the loads of all of it fly before the wait for room.
-template <bool kEdge>
-__device__ __forceinline__ bool soft_stage(const Operand& oa, const Operand& ob, const SoftTile& ta, const SoftTile& tb, int a_rows,
-                                           int b_rows, int left, uint64_t* empty, bool wait, uint32_t parity, uint8_t* stage, int warp) {
-    Blocks8 a[4], b[4];
-    ta.load<kEdge>(oa, a_rows, left, a);
-    tb.load<kEdge>(ob, b_rows, left, b);
-    if (wait && !warp_wait(empty, parity)) return false;
-    ta.store<kEdge>(oa, a_rows, left, a, stage, warp);
-    tb.store<kEdge>(ob, b_rows, left, b, stage + 16384, warp);
-    return true;
-}
-
-template <bool kF32, bool kSoft>
+// kSoft: kCopied, or which operands the loading warps find MN-major.
+enum { kCopied = 0, kSoftKK = 1, kSoftKMn = 2, kSoftMnMn = 3 };
+template <bool kF32, int kSoft>
 __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_constant__ SplitParams p) {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
@@ -834,16 +817,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
         if (kSoft) {
             int s = 0;
             uint32_t round = 0;
-            SoftTile ta(p.a, row_tile, (int64_t)kb0 * 64, warp), tb(p.b, col_tile, (int64_t)kb0 * 64, warp);
+            SoftTile<kSoft == kSoftMnMn> ta(p.a, row_tile, (int64_t)kb0 * 64, warp);
+            SoftTile<kSoft != kSoftKK> tb(p.b, col_tile, (int64_t)kb0 * 64, warp);
             for (int kb = kb0; kb < kb1; ++kb) {
-                const int64_t more = p.depth - (int64_t)kb * 64;
+                const int64_t k0 = (int64_t)kb * 64, more = p.depth - k0;
                 const int left = more < 64 ? (int)more : 64;
+                // only the ends of the reduced dimension meet those of the memory
+                const bool ends = kb == 0 || kb >= p.k_blocks - 2;
+                const bool edge_a = ends && ta.at_edge(p.a, row_tile, k0), edge_b = ends && tb.at_edge(p.b, col_tile, k0);
                 uint8_t* stage = smem + s * kStageBytes;
-                const int64_t k0 = (int64_t)kb * 64;
-                ok = SoftTile::at_edge(p.a, row_tile, k0) || SoftTile::at_edge(p.b, col_tile, k0)
-                         ? soft_stage<true>(p.a, p.b, ta, tb, a_rows, b_rows, left, empty + s, round > 0, (round - 1) & 1, stage, warp)
-                         : soft_stage<false>(p.a, p.b, ta, tb, a_rows, b_rows, left, empty + s, round > 0, (round - 1) & 1, stage, warp);
-                if (!ok) break;
+                Blocks8 a[4], b[4];   // all of a stage's loads fly before the wait for room
+                ta.load(p.a, edge_a, a_rows, left, a);
+                tb.load(p.b, edge_b, b_rows, left, b);
+                if (round > 0 && !(ok = warp_wait(empty + s, (round - 1) & 1))) break;
+                ta.store(p.a, edge_a, a_rows, left, a, stage, warp);
+                tb.store(p.b, edge_b, b_rows, left, b, stage + 16384, warp);
                 ta.advance();
                 tb.advance();
                 fence_async_shared();
@@ -1049,10 +1037,13 @@ static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
 }
 
 static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream_t s) {
-    static std::once_flag once[4][64];
-    void (*kernel)(SplitParams) = e.out_f32 ? (soft ? split_kernel<true, true> : split_kernel<true, false>)
-                                            : (soft ? split_kernel<false, true> : split_kernel<false, false>);
-    if (const int rc = allow_smem((const void*)kernel, kSplitSmem, once[e.out_f32 * 2 + soft])) return rc;
+    static std::once_flag once[8][64];
+    static void (*const kernels[2][4])(SplitParams) = {
+        {split_kernel<false, kCopied>, split_kernel<false, kSoftKK>, split_kernel<false, kSoftKMn>, split_kernel<false, kSoftMnMn>},
+        {split_kernel<true, kCopied>, split_kernel<true, kSoftKK>, split_kernel<true, kSoftKMn>, split_kernel<true, kSoftMnMn>}};
+    const int kind = !soft ? kCopied : p.a.mn ? kSoftMnMn : p.b.mn ? kSoftKMn : kSoftKK;
+    void (*kernel)(SplitParams) = kernels[e.out_f32][kind];
+    if (const int rc = allow_smem((const void*)kernel, kSplitSmem, once[e.out_f32 * 4 + kind])) return rc;
     SplitParams q{};
     q.a = p.a; q.b = p.b;
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
