@@ -1047,14 +1047,23 @@ static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream
     SplitParams q{};
     q.a = p.a; q.b = p.b;
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
-    const int64_t tiles_m = (p.rows + 127) / 128, resident = 2 * (int64_t)sm_count();
-    q.bn = 128;
-    while (q.bn > 32 && tiles_m * ((p.cols + q.bn - 1) / q.bn) * 8 < resident) q.bn /= 2;
-    const int64_t tiles_n = (p.cols + q.bn - 1) / q.bn, tiles = tiles_m * tiles_n, k_blocks = (p.depth + 63) / 64;
+    const int64_t tiles_m = (p.rows + 127) / 128, resident = 2 * (int64_t)sm_count(), k_blocks = (p.depth + 63) / 64;
+    // the tile width and number of parts with the least estimated time (cycles, from
+    // the phases' measured times): waves of CTAs, each a start, its blocks by the
+    // groups of 32 rows they bring, and the join
+    int64_t best = INT64_MAX, tiles_n = 0;
     int parts = 1;
-    while (parts < 8 && tiles * parts * 2 <= resident && k_blocks >= parts * 4) parts *= 2;
-    if (e.out_f32)   // short runs of the tensor core's sums, as in the pair kernel
-        while (parts < 8 && k_blocks > (int64_t)parts * kRun) parts *= 2;
+    for (int bn = 128; bn >= 32; bn /= 2)
+        for (int n = 1; n <= 8 && (n == 1 || k_blocks >= 2 * n); n *= 2) {
+            // fp32 results: short runs of the tensor core's sums, as in the pair kernel
+            if (e.out_f32 && n < 8 && k_blocks > (int64_t)n * kRun && k_blocks >= 4 * n) continue;
+            const int64_t tn = (p.cols + bn - 1) / bn;
+            if (tn > INT32_MAX / 8 / tiles_m) return ZERO_ERANGE;
+            const int64_t waves = (tiles_m * tn * n + resident - 1) / resident;
+            const int64_t time = waves * (5000 + (k_blocks + n - 1) / n * (4 + bn / 32) * (soft ? 300 : 80) + (n > 1 ? 2000 + 100 * n : 0) + 10 * bn);
+            if (time < best) best = time, q.bn = bn, parts = n, tiles_n = tn;
+        }
+    const int64_t tiles = tiles_m * tiles_n;
     if (tiles > INT32_MAX / 8 || k_blocks > INT32_MAX) return ZERO_ERANGE;
     q.tiles_m = (int32_t)tiles_m; q.tiles_n = (int32_t)tiles_n; q.k_blocks = (int32_t)k_blocks;
     q.e = e;
