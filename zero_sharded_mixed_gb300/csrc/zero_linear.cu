@@ -370,11 +370,10 @@ constexpr int kPairSmem = 1024 + kPairStages * kStageBytes + kEndWarps * kUnitBy
 // fp32 results: the tensor core cuts its sums where an fp32 addition would round
 // them, and 100 additions in a row were off by 1.6e-6 of the result, five times a
 // plain fp32 sum's error.  Their accumulators are therefore read after at most kRun
-// blocks and added up in registers (0.75e-6), 48 of them a thread, which fixes the
-// widest tile.  A bf16 result's own rounding is a thousand times larger.
+// blocks and added up in registers (0.75e-6), 64 of them a thread.  A bf16 result's own rounding is a thousand times larger.
 constexpr int kRun = 13;                // blocks of 64 reduced elements
 constexpr int kUnits = 4;               // 16 x 32 parts of a tile that a warp ends
-constexpr int kWidest = 256, kWidestF32 = kUnits * 4 * 16;
+constexpr int kWidest = kUnits * 4 * 16;
 constexpr int kRasterRows = 8;          // row tiles that are gone through together
 
 __device__ __forceinline__ void tile_place(const PairParams& p, int t, int* tm, int* tn) {
@@ -1009,34 +1008,74 @@ static int allow_smem(const void* kernel, int bytes, std::once_flag* once) {
     return ZERO_OK;
 }
 
-static int launch_pair(const Product& p, const Ending& e, cudaStream_t s) {
+// What a launch takes and its estimated cycles, from the measured times of each
+// kernel's phases on GB300; the least decides.  (Measured either way, in us, pair and
+// split kernel: 333 x 1600 x 1600 8.8 and 8.4; 1024 x 1600 x 1600 9.2 and 13; 64 tokens
+// by 4800 x 1600 10.7 and 7.1; its 64 x 1600 gradient 20 and 8.5.)
+struct Plan {
+    int64_t cycles, tiles_m, tiles_n;
+    int bn, parts;
+};
+
+// Waves of pairs, each a tile's blocks (bound by the tensor core, or for narrow tiles
+// by shared memory) and the part of its end that nothing hides.
+static Plan plan_pair(const Product& p) {
+    const int64_t pairs = sm_count() / 2, k_blocks = (p.depth + 63) / 64;
+    Plan best{INT64_MAX, (p.rows + 255) / 256, 0, 0, 1};
+    for (int bn = kWidest; bn >= 32; bn -= 32) {
+        const int64_t tn = (p.cols + bn - 1) / bn;
+        if (tn > INT32_MAX / 8 / best.tiles_m) break;
+        const int64_t waves = (best.tiles_m * tn + pairs - 1) / pairs;
+        const int64_t cycles = 4000 + waves * (k_blocks * (2 * bn > 256 + bn ? 2 * bn : 256 + bn) + 24 * bn);
+        if (cycles < best.cycles) best.cycles = cycles, best.tiles_n = tn, best.bn = bn;
+    }
+    return best;
+}
+
+// Waves of CTAs, two to an SM: each a start, its blocks by the groups of 32 rows they
+// bring, its share of the end, and the join.  Loading warps wait longer for a block
+// than copies do and lose less to a second CTA beside them.
+struct Costs {
+    int start, group, end, crowd, join, part;   // crowd: percent more with two CTAs to each SM
+};
+static Plan plan_split(const Product& p, bool f32, bool soft) {
+    const Costs t = soft ? Costs{5000, 300, 2500, 60, 2000, 300} : Costs{2000, 112, 5000, 90, 500, 1460};
+    const int64_t sms = sm_count(), k_blocks = (p.depth + 63) / 64, rows = p.rows < 128 ? p.rows : 128;
+    Plan best{INT64_MAX, (p.rows + 127) / 128, 0, 0, 1};
+    for (int bn = 128; bn >= 32; bn /= 2) {
+        const int64_t tn = (p.cols + bn - 1) / bn;
+        if (tn > INT32_MAX / 8 / best.tiles_m) break;
+        for (int n = 1; n <= 8 && (n == 1 || k_blocks >= 2 * n); n *= 2) {
+            // fp32 results: short runs of the tensor core's sums, as in the pair kernel
+            if (f32 && n < 8 && k_blocks > (int64_t)n * kRun && k_blocks >= 4 * n) continue;
+            const int64_t ctas = best.tiles_m * tn * n, waves = (ctas + 2 * sms - 1) / (2 * sms);
+            const int64_t crowd = 100 + (ctas <= sms ? 0 : ctas >= 2 * sms ? t.crowd : t.crowd * (ctas - sms) / sms);
+            const int64_t blocks = (k_blocks + n - 1) / n * (4 + bn / 32) * t.group + t.end * rows * bn / (128 * 128) / n;
+            const int64_t cycles = waves * (t.start + blocks * crowd / 100 + (n > 1 ? t.join + t.part * rows * bn / (128 * 64) * n : 0));
+            if (cycles < best.cycles) best.cycles = cycles, best.tiles_n = tn, best.bn = bn, best.parts = n;
+        }
+    }
+    return best;
+}
+
+static int launch_pair(const Product& p, const Ending& e, const Plan& plan, cudaStream_t s) {
     static std::once_flag once[2][64];
     void (*kernel)(PairParams) = e.out_f32 ? pair_kernel<true> : pair_kernel<false>;
     if (const int rc = allow_smem((const void*)kernel, kPairSmem, once[e.out_f32])) return rc;
     PairParams q{};
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
-    q.tiles_m = (int32_t)((p.rows + 255) / 256);
-    const int pairs = sm_count() / 2;
-    // the tile width whose waves of pairs cover the columns with the least work
-    int64_t best = INT64_MAX;
-    const int64_t widest = e.out_f32 ? kWidestF32 : kWidest, fewest = (p.cols + widest - 1) / widest;
-    for (int64_t tn = fewest; tn < fewest + 4; ++tn) {
-        const int64_t bn = ((p.cols + tn - 1) / tn + 31) / 32 * 32;
-        const int64_t n = (p.cols + bn - 1) / bn;
-        const int64_t cost = (q.tiles_m * n + pairs - 1) / pairs * (bn + 16);
-        if (cost < best) best = cost, q.bn = (int32_t)bn, q.tiles_n = (int32_t)n;
-    }
+    q.tiles_m = (int32_t)plan.tiles_m; q.tiles_n = (int32_t)plan.tiles_n; q.bn = plan.bn;
     q.k_blocks = (int32_t)((p.depth + 63) / 64);
     const int runs = e.out_f32 ? (q.k_blocks + kRun - 1) / kRun : 1;
     q.run = (q.k_blocks + runs - 1) / runs;
     q.a_mn = p.a.mn; q.b_mn = p.b.mn;
     q.e = e;
     if (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
-    const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
+    const int64_t tiles = plan.tiles_m * plan.tiles_n, pairs = sm_count() / 2;
     return launch_dense(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, 2, true, kPairSmem, s, q);
 }
 
-static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream_t s) {
+static int launch_split(const Product& p, const Ending& e, const Plan& plan, bool soft, cudaStream_t s) {
     static std::once_flag once[8][64];
     static void (*const kernels[2][4])(SplitParams) = {
         {split_kernel<false, kCopied>, split_kernel<false, kSoftKK>, split_kernel<false, kSoftKMn>, split_kernel<false, kSoftMnMn>},
@@ -1044,32 +1083,17 @@ static int launch_split(const Product& p, const Ending& e, bool soft, cudaStream
     const int kind = !soft ? kCopied : p.a.mn ? kSoftMnMn : p.b.mn ? kSoftKMn : kSoftKK;
     void (*kernel)(SplitParams) = kernels[e.out_f32][kind];
     if (const int rc = allow_smem((const void*)kernel, kSplitSmem, once[e.out_f32 * 4 + kind])) return rc;
+    const int64_t k_blocks = (p.depth + 63) / 64;
+    if (!plan.tiles_n || k_blocks > INT32_MAX) return ZERO_ERANGE;
     SplitParams q{};
     q.a = p.a; q.b = p.b;
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
-    const int64_t tiles_m = (p.rows + 127) / 128, resident = 2 * (int64_t)sm_count(), k_blocks = (p.depth + 63) / 64;
-    // the tile width and number of parts with the least estimated time (cycles, from
-    // the phases' measured times): waves of CTAs, each a start, its blocks by the
-    // groups of 32 rows they bring, and the join
-    int64_t best = INT64_MAX, tiles_n = 0;
-    int parts = 1;
-    for (int bn = 128; bn >= 32; bn /= 2)
-        for (int n = 1; n <= 8 && (n == 1 || k_blocks >= 2 * n); n *= 2) {
-            // fp32 results: short runs of the tensor core's sums, as in the pair kernel
-            if (e.out_f32 && n < 8 && k_blocks > (int64_t)n * kRun && k_blocks >= 4 * n) continue;
-            const int64_t tn = (p.cols + bn - 1) / bn;
-            if (tn > INT32_MAX / 8 / tiles_m) return ZERO_ERANGE;
-            const int64_t waves = (tiles_m * tn * n + resident - 1) / resident;
-            const int64_t time = waves * (5000 + (k_blocks + n - 1) / n * (4 + bn / 32) * (soft ? 300 : 80) + (n > 1 ? 2000 + 100 * n : 0) + 10 * bn);
-            if (time < best) best = time, q.bn = bn, parts = n, tiles_n = tn;
-        }
-    const int64_t tiles = tiles_m * tiles_n;
-    if (tiles > INT32_MAX / 8 || k_blocks > INT32_MAX) return ZERO_ERANGE;
-    q.tiles_m = (int32_t)tiles_m; q.tiles_n = (int32_t)tiles_n; q.k_blocks = (int32_t)k_blocks;
+    q.tiles_m = (int32_t)plan.tiles_m; q.tiles_n = (int32_t)plan.tiles_n; q.bn = plan.bn; q.k_blocks = (int32_t)k_blocks;
     q.e = e;
     q.box_a = p.rows < 128 ? (int32_t)((p.rows + 7) / 8 * 8) : 128;
     if (!soft && (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
-    return launch_dense(kernel, dim3((unsigned)(tiles * parts)), kSplitThreads, (unsigned)parts, true, kSplitSmem, s, q);
+    return launch_dense(kernel, dim3((unsigned)(plan.tiles_m * plan.tiles_n * plan.parts)), kSplitThreads, (unsigned)plan.parts, true,
+                        kSplitSmem, s, q);
 }
 
 static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
@@ -1078,10 +1102,14 @@ static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
             (!e.add || rows_aligned16(e.add, e.ld_add, size)) && rows_aligned16(e.out, e.ld_out, size);
     if (p.rows <= kMostRows && !p.a.mn && !p.b.mn) return launch_rows(p, e, s);
     e.bare = !e.pre && !e.slope && !e.act && !e.drop.cut && !e.add;
+    if ((p.rows + 127) / 128 > INT32_MAX / 64) return ZERO_ERANGE;
     const bool reach = copies_reach(p.a) && copies_reach(p.b);
-    const int64_t pair_tiles = ((p.rows + 255) / 256) * ((p.cols + 255) / 256);
-    if (reach && pair_tiles >= sm_count() / 4 && pair_tiles < INT32_MAX / 8) return launch_pair(p, e, s);
-    return launch_split(p, e, !reach, s);
+    const Plan split = plan_split(p, e.out_f32, !reach);
+    if (reach) {
+        const Plan pair = plan_pair(p);
+        if (pair.tiles_n && pair.cycles < split.cycles) return launch_pair(p, e, pair, s);
+    }
+    return launch_split(p, e, split, !reach, s);
 }
 
 static bool act_ok(int32_t act) { return act >= ZERO_ACT_NONE && act <= ZERO_ACT_SILU; }
