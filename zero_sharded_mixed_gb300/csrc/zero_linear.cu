@@ -356,6 +356,7 @@ struct PairParams {
     int64_t rows, cols, depth;
     int32_t tiles_m, tiles_n, bn, k_blocks;
     int32_t run;   // blocks after which an accumulator is handed over
+    int32_t box_a; // rows of A that a K-major copy brings
     bool a_mn, b_mn;
     Ending e;
 };
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
 
     const int half = p.bn / 2;
     const int b_boxes = p.b_mn ? (half + 63) / 64 : 1;
-    const uint32_t stage_bytes = 16384u + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)half * 128u);
+    const uint32_t stage_bytes = (p.a_mn ? 16384u : (uint32_t)p.box_a * 128u) + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)half * 128u);
 
     if (warp == 0) {
         int s = 0;
@@ -1021,12 +1022,12 @@ struct Plan {
 // by shared memory) and the part of its end that nothing hides.
 static Plan plan_pair(const Product& p) {
     const int64_t pairs = sm_count() / 2, k_blocks = (p.depth + 63) / 64;
-    Plan best{INT64_MAX, (p.rows + 255) / 256, 0, 0, 1};
+    Plan best{INT64_MAX, (p.rows + 255) / 256, 0, 0, 1};   // no width fits: not taken
     for (int bn = kWidest; bn >= 32; bn -= 32) {
         const int64_t tn = (p.cols + bn - 1) / bn;
         if (tn > INT32_MAX / 8 / best.tiles_m) break;
         const int64_t waves = (best.tiles_m * tn + pairs - 1) / pairs;
-        const int64_t cycles = 4000 + waves * (k_blocks * (2 * bn > 256 + bn ? 2 * bn : 256 + bn) + 24 * bn);
+        const int64_t cycles = 4000 + waves * (1500 + k_blocks * (2 * bn > 256 + bn ? 2 * bn : 256 + bn) + 24 * bn);
         if (cycles < best.cycles) best.cycles = cycles, best.tiles_n = tn, best.bn = bn;
     }
     return best;
@@ -1058,6 +1059,10 @@ static Plan plan_split(const Product& p, bool f32, bool soft) {
     return best;
 }
 
+// Rows of A that a copy brings: no more than there are.  (Boxes of 128 rows over a
+// matrix of 5 to 14 took two to three times as long as over one of 16.)
+static int32_t box_rows(int64_t rows) { return rows < 128 ? (int32_t)((rows + 7) / 8 * 8) : 128; }
+
 static int launch_pair(const Product& p, const Ending& e, const Plan& plan, cudaStream_t s) {
     static std::once_flag once[2][64];
     void (*kernel)(PairParams) = e.out_f32 ? pair_kernel<true> : pair_kernel<false>;
@@ -1070,7 +1075,8 @@ static int launch_pair(const Product& p, const Ending& e, const Plan& plan, cuda
     q.run = (q.k_blocks + runs - 1) / runs;
     q.a_mn = p.a.mn; q.b_mn = p.b.mn;
     q.e = e;
-    if (!make_map(p.a, p.a.mn ? 64 : 128, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
+    q.box_a = box_rows(p.rows);
+    if (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
     const int64_t tiles = plan.tiles_m * plan.tiles_n, pairs = sm_count() / 2;
     return launch_dense(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, 2, true, kPairSmem, s, q);
 }
@@ -1090,7 +1096,7 @@ static int launch_split(const Product& p, const Ending& e, const Plan& plan, boo
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
     q.tiles_m = (int32_t)plan.tiles_m; q.tiles_n = (int32_t)plan.tiles_n; q.bn = plan.bn; q.k_blocks = (int32_t)k_blocks;
     q.e = e;
-    q.box_a = p.rows < 128 ? (int32_t)((p.rows + 7) / 8 * 8) : 128;
+    q.box_a = box_rows(p.rows);
     if (!soft && (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
     return launch_dense(kernel, dim3((unsigned)(plan.tiles_m * plan.tiles_n * plan.parts)), kSplitThreads, (unsigned)plan.parts, true,
                         kSplitSmem, s, q);
@@ -1100,16 +1106,18 @@ static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
     const int size = e.out_f32 ? 4 : 2;
     e.vec = aligned16(e.bias) && (!e.slope || rows_aligned16(e.slope, e.ld_slope, 2)) && (!e.pre || rows_aligned16(e.pre, e.ld_pre, 2)) &&
             (!e.add || rows_aligned16(e.add, e.ld_add, size)) && rows_aligned16(e.out, e.ld_out, size);
-    if (p.rows <= kMostRows && !p.a.mn && !p.b.mn) return launch_rows(p, e, s);
     e.bare = !e.pre && !e.slope && !e.act && !e.drop.cut && !e.add;
     if ((p.rows + 127) / 128 > INT32_MAX / 64) return ZERO_ERANGE;
     const bool reach = copies_reach(p.a) && copies_reach(p.b);
-    const Plan split = plan_split(p, e.out_f32, !reach);
-    if (reach) {
-        const Plan pair = plan_pair(p);
-        if (pair.tiles_n && pair.cycles < split.cycles) return launch_pair(p, e, pair, s);
+    const Plan split = plan_split(p, e.out_f32, !reach), pair = reach ? plan_pair(p) : Plan{INT64_MAX, 0, 0, 0, 0};
+    const int64_t tiled = pair.cycles < split.cycles ? pair.cycles : split.cycles;
+    // the kernel of a few rows reads the weights at about 2950 bytes a cycle for one row
+    // (11008 x 4096: 16 us, 18 by tiles) and half of it for three or four
+    if (p.rows <= kMostRows && !p.a.mn && !p.b.mn) {
+        const int64_t read = p.cols * (p.depth / 8) * 16 / 2950;
+        if (p.rows == 1 || 3000 + read * (p.rows == 2 ? 14 : 23) / 10 < tiled) return launch_rows(p, e, s);
     }
-    return launch_split(p, e, split, !reach, s);
+    return pair.cycles < split.cycles ? launch_pair(p, e, pair, s) : launch_split(p, e, split, !reach, s);
 }
 
 static bool act_ok(int32_t act) { return act >= ZERO_ACT_NONE && act <= ZERO_ACT_SILU; }
