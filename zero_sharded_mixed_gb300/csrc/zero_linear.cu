@@ -83,9 +83,11 @@ __device__ __forceinline__ void pair_exchange(float (&v)[4][4]) {
 }
 __device__ __forceinline__ int pair_column() { return 8 * (threadIdx.x & 1) + 4 * ((threadIdx.x & 3) >> 1); }
 
-template <bool kF32>
+// kLate: an fp32 residual is read where it is added, for want of registers.
+template <bool kF32, bool kLate>
 struct FragmentEnd {
-    uint4 slope[2], add[2];             // rows i and i + 8: group j (an fp32 residual is read where it is added)
+    uint4 slope[2], add[2];             // rows i and i + 8: group j
+    float4 add32[kF32 && !kLate ? 2 : 1][2];
     bool in[2];
 
     __device__ __forceinline__ void load(const Ending& e, int64_t row, int64_t col0, int64_t rows) {
@@ -96,6 +98,13 @@ struct FragmentEnd {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (in[h]) add[h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.add) + (row + 8 * h) * e.ld_add + col0 + 8 * j);
+        }
+        if (kF32 && !kLate && e.add) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    if (in[h]) add32[h][p] = *reinterpret_cast<const float4*>(static_cast<const float*>(e.add) + (row + 8 * h) * e.ld_add + col0 + 16 * p + pair_column());
         }
         if (e.slope) {
 #pragma unroll
@@ -116,7 +125,7 @@ struct FragmentEnd {
         }
     }
 
-    __device__ __forceinline__ void finish(const Ending& e, uint32_t step, int64_t row, int64_t col0, float (&v)[4][4], bool add_it = true) {
+    __device__ __forceinline__ void finish(const Ending& e, uint32_t step, int64_t row, int64_t col0, float (&v)[4][4]) {
         const int j = threadIdx.x & 3;
         if (e.bias) {
 #pragma unroll
@@ -127,18 +136,23 @@ struct FragmentEnd {
             }
         }
         if (e.pre) store_bf16(e.pre + row * e.ld_pre + col0 + 8 * j, e.ld_pre, v);
+        constexpr int kAtOnce = kF32 ? 1 : 4;   // groups whose chains interleave: the sums leave fp32 few registers
         if (e.slope) {
-            float t[4][4];
+            quad_transpose(slope[0]);
+            quad_transpose(slope[1]);
+            const uint32_t w[2][4] = {{slope[0].x, slope[0].y, slope[0].z, slope[0].w}, {slope[1].x, slope[1].y, slope[1].z, slope[1].w}};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                quad_transpose(slope[h]);
-                const uint32_t w[4] = {slope[h].x, slope[h].y, slope[h].z, slope[h].w};
+            for (int g = 0; g < 4; g += kAtOnce) {
+                float t[kAtOnce][4];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) t[g][2 * h] = bf16_lo(w[g]), t[g][2 * h + 1] = bf16_hi(w[g]);
+                for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) t[i][2 * h] = bf16_lo(w[h][g + i]), t[i][2 * h + 1] = bf16_hi(w[h][g + i]);
+                slope_apply<4 * kAtOnce>(e.act, t[0], v[g]);
             }
-            slope_apply<16>(e.act, t[0], v[0]);
         } else if (e.act) {
-            act_apply<16>(e.act, v[0]);
+#pragma unroll
+            for (int g = 0; g < 4; g += kAtOnce) act_apply<4 * kAtOnce>(e.act, v[g]);
         }
         if (e.drop.cut) {
 #pragma unroll
@@ -162,10 +176,14 @@ struct FragmentEnd {
 #pragma unroll
             for (int h = 0; h < 2; ++h, q += 8 * e.ld_out, r += 8 * e.ld_add) {
                 if (!in[h]) continue;
-                if (e.add && add_it) {
+                if (e.add) {
                     float4 t[2];
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) t[p] = *reinterpret_cast<const float4*>(r + 16 * p);
+                    for (int p = 0; p < 2; ++p)
+                        if constexpr (kLate)
+                            t[p] = *reinterpret_cast<const float4*>(r + 16 * p);
+                        else
+                            t[p] = add32[h][p];
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         v[2 * p][2 * h] += t[p].x;
@@ -371,10 +389,11 @@ constexpr int kPairSmem = 1024 + kPairStages * kStageBytes + kEndWarps * kUnitBy
 // fp32 results: the tensor core cuts its sums where an fp32 addition would round
 // them, and 100 additions in a row were off by 1.6e-6 of the result, five times a
 // plain fp32 sum's error.  Their accumulators are therefore read after at most kRun
-// blocks and added up in registers (0.75e-6), 64 of them a thread.  A bf16 result's own rounding is a thousand times larger.
+// blocks and added up in registers (0.75e-6).  A bf16 result's own rounding is a
+// thousand times larger.
 constexpr int kRun = 13;                // blocks of 64 reduced elements
-constexpr int kUnits = 4;               // 16 x 32 parts of a tile that a warp ends
-constexpr int kWidest = kUnits * 4 * 16;
+constexpr int kUnits = 3;               // 16 x 32 parts that a warp sums so, in 48 registers; a fourth would spill
+constexpr int kWidest = 256, kWidestRuns = kUnits * 4 * 16;
 constexpr int kRasterRows = 8;          // row tiles that are gone through together
 
 __device__ __forceinline__ void tile_place(const PairParams& p, int t, int* tm, int* tn) {
@@ -431,7 +450,8 @@ __device__ __forceinline__ void end_staged(const Ending& e, uint32_t step, int64
     end_rows<kF32, 16>(e, step, row0, col0, rows, cols, t);
 }
 
-template <bool kF32>
+// kRuns: fp32 results of more than one run, added up in registers.
+template <bool kF32, bool kRuns>
 __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
@@ -546,7 +566,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
             (void)mbar_wait_bounded(drained, 0, kWaitCycles / 8);
         }
     } else if (warp >= 4) {
-        // units of 16 rows x 32 columns: this warp's are every fourth of its 32 rows'
+        // units of 16 rows x 32 columns: of its 32 rows this warp ends one half, over one
+        // half of the columns, side by side so that whole lines are written together
         const int w = warp - 4, q = warp & 3, h = w / 4;
         uint8_t* chunk = chunks + w * kUnitBytes;
         const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
@@ -556,60 +577,44 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
             int tm, tn;
             tile_place(p, t, &tm, &tn);
             const int64_t row0 = (int64_t)tm * 256 + rank * 128 + q * 32, col_tile = (int64_t)tn * p.bn;
-            const int units = tile_width(p, tn) / 16;
+            const int chunks_n = tile_width(p, tn) / 32, first = (h >> 1) * ((chunks_n + 1) / 2);
+            const int units = h >> 1 ? chunks_n - first : (chunks_n + 1) / 2;   // of this warp
+            const int64_t row_u = row0 + (h & 1) * 16;
             // what the end reads beside the accumulators, on its way to L2 while the product
             // runs (a tile ahead was slower: the reads then stand in the operands' way)
             if (p.e.add || p.e.slope) prefetch_sides<kF32>(p, t, rank, q, h);
-            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-            const auto place = [&](int buf, int u) { return lanes + buf * 256 + (u >> 1) * 32 + ((uint32_t)((u & 1) * 16) << 16); };
-            if constexpr (kF32) {
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32 + (h & 1) * 16) << 16);
+            const auto place = [&](int buf, int u) { return lanes + buf * 256 + (first + u) * 32; };
+            if constexpr (kRuns) {
                 float acc[kUnits][4][4];
-                // a residual that only the sum meets is where the sum starts: its loads
-                // are done while the product runs
-                const bool early = p.e.vec && p.e.add && !p.e.act && !p.e.pre && !p.e.slope && !p.e.drop.cut;
-#pragma unroll
-                for (int i = 0; i < kUnits; ++i) {
-                    const int u = h + 4 * i;
-                    const int64_t row = row0 + (u & 1) * 16 + (lane >> 2), col0 = col_tile + (u >> 1) * 32;
-                    const bool starts = early && u < units && col0 + 32 <= p.cols;
-#pragma unroll
-                    for (int g = 0; g < 4; g += 2)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (starts && row + 8 * r < p.rows)
-                                t = *reinterpret_cast<const float4*>(static_cast<const float*>(p.e.add) + (row + 8 * r) * p.e.ld_add + col0 + 8 * g + pair_column());
-                            acc[i][g][2 * r] = t.x;
-                            acc[i][g][2 * r + 1] = t.y;
-                            acc[i][g + 1][2 * r] = t.z;
-                            acc[i][g + 1][2 * r + 1] = t.w;
-                        }
-                }
                 for (int kb = 0; kb < p.k_blocks; kb += p.run, ++use) {
                     const int buf = use & 1;
                     if (!(ok = warp_wait(acc_full + buf, (use / 2) & 1))) break;
                     tcgen05_fence_after();
 #pragma unroll
                     for (int i = 0; i < kUnits; ++i) {
-                        if (h + 4 * i >= units) continue;
-                        float v[4][4];
-                        tmem_load_fragment(place(buf, h + 4 * i), v);
-                        if (kb == 0 && early) pair_exchange(acc[i]);
+                        if (i >= units) continue;
+                        if (kb == 0) {
+                            tmem_load_fragment(place(buf, i), acc[i]);
+                        } else {
+                            float v[4][4];
+                            tmem_load_fragment(place(buf, i), v);
 #pragma unroll
-                        for (int g = 0; g < 16; ++g) acc[i][g / 4][g % 4] += v[g / 4][g % 4];
+                            for (int g = 0; g < 16; ++g) acc[i][g / 4][g % 4] += v[g / 4][g % 4];
+                        }
                     }
                     release(acc_empty + buf);
                 }
                 if (!ok) break;
 #pragma unroll 1
-                for (int u = h; u < units; u += 4) {   // one copy of the code: three outgrow the instruction cache
-                    const int64_t row = row0 + (u & 1) * 16, col0 = col_tile + (u >> 1) * 32;
-                    FragmentEnd<kF32> end;
+                for (int u = 0; u < units; ++u) {   // one copy of the code: four outgrow the instruction cache
+                    const int64_t col0 = col_tile + (first + u) * 32;
+                    FragmentEnd<kF32, true> end;
                     if (p.e.vec && col0 + 32 <= p.cols) {
-                        end.load(p.e, row + (lane >> 2), col0, p.rows);
-                        end.finish(p.e, step, row + (lane >> 2), col0, acc[0], !early);
+                        end.load(p.e, row_u + (lane >> 2), col0, p.rows);
+                        end.finish(p.e, step, row_u + (lane >> 2), col0, acc[0]);
                     } else {
-                        end_staged<kF32>(p.e, step, row, col0, p.rows, p.cols, acc[0], chunk);
+                        end_staged<kF32>(p.e, step, row_u, col0, p.rows, p.cols, acc[0], chunk);
                     }
 #pragma unroll
                     for (int g = 0; g < 16; ++g)
@@ -621,20 +626,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
                 if (!(ok = warp_wait(acc_full + buf, (use / 2) & 1))) break;
                 tcgen05_fence_after();
 #pragma unroll 1
-                for (int u = h; u < units; u += 4) {
-                    const int64_t row = row0 + (u & 1) * 16, col0 = col_tile + (u >> 1) * 32;
+                for (int u = 0; u < units; ++u) {
+                    const int64_t col0 = col_tile + (first + u) * 32;
                     const bool vec = p.e.vec && col0 + 32 <= p.cols;
-                    FragmentEnd<kF32> end;
+                    FragmentEnd<kF32, false> end;
                     float v[4][4];
-                    if (vec) end.load(p.e, row + (lane >> 2), col0, p.rows);
+                    if (vec) end.load(p.e, row_u + (lane >> 2), col0, p.rows);
                     tmem_load_fragment(place(buf, u), v);
-                    if (u + 4 >= units) release(acc_empty + buf);   // this warp's last read
+                    if (u + 1 == units) release(acc_empty + buf);   // this warp's last read
                     if (vec)
-                        end.finish(p.e, step, row + (lane >> 2), col0, v);
+                        end.finish(p.e, step, row_u + (lane >> 2), col0, v);
                     else
-                        end_staged<kF32>(p.e, step, row, col0, p.rows, p.cols, v, chunk);
+                        end_staged<kF32>(p.e, step, row_u, col0, p.rows, p.cols, v, chunk);
                 }
-                if (h >= units) release(acc_empty + buf);   // a narrow last tile: no unit for this warp
+                if (units == 0) release(acc_empty + buf);   // a narrow last tile: no unit for this warp
                 ++use;
             }
         }
@@ -1020,10 +1025,11 @@ struct Plan {
 
 // Waves of pairs, each a tile's blocks (bound by the tensor core, or for narrow tiles
 // by shared memory) and the part of its end that nothing hides.
-static Plan plan_pair(const Product& p) {
+static Plan plan_pair(const Product& p, bool f32) {
     const int64_t pairs = sm_count() / 2, k_blocks = (p.depth + 63) / 64;
+    const int widest = f32 && k_blocks > kRun ? kWidestRuns : kWidest;
     Plan best{INT64_MAX, (p.rows + 255) / 256, 0, 0, 1};   // no width fits: not taken
-    for (int bn = kWidest; bn >= 32; bn -= 32) {
+    for (int bn = widest; bn >= 32; bn -= 32) {
         const int64_t tn = (p.cols + bn - 1) / bn;
         if (tn > INT32_MAX / 8 / best.tiles_m) break;
         const int64_t waves = (best.tiles_m * tn + pairs - 1) / pairs;
@@ -1040,7 +1046,7 @@ struct Costs {
     int start, group, end, crowd, join, part;   // crowd: percent more with two CTAs to each SM
 };
 static Plan plan_split(const Product& p, bool f32, bool soft) {
-    const Costs t = soft ? Costs{5000, 300, 2500, 60, 2000, 300} : Costs{2000, 112, 5000, 90, 500, 1460};
+    const Costs t = soft ? Costs{5000, 300, 2500, 60, 2000, 300} : Costs{2000, 112, 11000, 90, 500, 1460};
     const int64_t sms = sm_count(), k_blocks = (p.depth + 63) / 64, rows = p.rows < 128 ? p.rows : 128;
     Plan best{INT64_MAX, (p.rows + 127) / 128, 0, 0, 1};
     for (int bn = 128; bn >= 32; bn /= 2) {
@@ -1064,14 +1070,14 @@ static Plan plan_split(const Product& p, bool f32, bool soft) {
 static int32_t box_rows(int64_t rows) { return rows < 128 ? (int32_t)((rows + 7) / 8 * 8) : 128; }
 
 static int launch_pair(const Product& p, const Ending& e, const Plan& plan, cudaStream_t s) {
-    static std::once_flag once[2][64];
-    void (*kernel)(PairParams) = e.out_f32 ? pair_kernel<true> : pair_kernel<false>;
-    if (const int rc = allow_smem((const void*)kernel, kPairSmem, once[e.out_f32])) return rc;
+    static std::once_flag once[3][64];
+    const int blocks = (int)((p.depth + 63) / 64), runs = e.out_f32 ? (blocks + kRun - 1) / kRun : 1;
+    void (*kernel)(PairParams) = runs > 1 ? pair_kernel<true, true> : e.out_f32 ? pair_kernel<true, false> : pair_kernel<false, false>;
+    if (const int rc = allow_smem((const void*)kernel, kPairSmem, once[runs > 1 ? 2 : e.out_f32])) return rc;
     PairParams q{};
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
     q.tiles_m = (int32_t)plan.tiles_m; q.tiles_n = (int32_t)plan.tiles_n; q.bn = plan.bn;
-    q.k_blocks = (int32_t)((p.depth + 63) / 64);
-    const int runs = e.out_f32 ? (q.k_blocks + kRun - 1) / kRun : 1;
+    q.k_blocks = blocks;
     q.run = (q.k_blocks + runs - 1) / runs;
     q.a_mn = p.a.mn; q.b_mn = p.b.mn;
     q.e = e;
@@ -1109,7 +1115,7 @@ static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
     e.bare = !e.pre && !e.slope && !e.act && !e.drop.cut && !e.add;
     if ((p.rows + 127) / 128 > INT32_MAX / 64) return ZERO_ERANGE;
     const bool reach = copies_reach(p.a) && copies_reach(p.b);
-    const Plan split = plan_split(p, e.out_f32, !reach), pair = reach ? plan_pair(p) : Plan{INT64_MAX, 0, 0, 0, 0};
+    const Plan split = plan_split(p, e.out_f32, !reach), pair = reach ? plan_pair(p, e.out_f32) : Plan{INT64_MAX, 0, 0, 0, 0};
     const int64_t tiled = pair.cycles < split.cycles ? pair.cycles : split.cycles;
     // the kernel of a few rows reads the weights at about 2950 bytes a cycle for one row
     // (11008 x 4096: 16 us, 18 by tiles) and half of it for three or four
