@@ -32,10 +32,7 @@ struct RopeParams {
     zero_rope_plan_t plan;
 };
 
-#ifndef ZGB_ROPE_ITEMS
-#define ZGB_ROPE_ITEMS 2048   // work items of a CTA, eight a thread
-#endif
-constexpr int kRopeItems = ZGB_ROPE_ITEMS;
+constexpr int kRopeItems = 4096;   // work items of a CTA, sixteen a thread
 
 template <bool kF32>
 __device__ __forceinline__ float rope_load(const void* p, int64_t i) {
@@ -87,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     __shared__ float2 turn[kThreads > ZERO_ROPE_MAX / 2 ? kThreads : ZERO_ROPE_MAX / 2];   // [cta_tokens][pairs]
     using V = RopeVector<kF32>;
     using T = typename std::conditional<kF32, float, uint16_t>::type;
-    constexpr int kBatch = 4, kCount = kVec ? V::kCount : 1;
+    constexpr int kBatch = kF32 ? 4 : 2, kCount = kVec ? V::kCount : 1;   // items whose loads fly together
     const int pairs = p.plan.rot / 2, turned = pairs / kCount, rest = (int)((p.dim - p.plan.rot) / kCount);
     const int64_t t0 = (int64_t)blockIdx.x * p.cta_tokens, h0 = (int64_t)blockIdx.y * p.cta_heads;
     const int nt = (int)(p.tokens - t0 < p.cta_tokens ? p.tokens - t0 : p.cta_tokens);
