@@ -587,7 +587,7 @@ int zero_rope(const zero_rope_plan_t* plan, int64_t tokens, int64_t heads, int64
 /* ---- status ---------------------------------------------------------------
  * Synchronizes `stream` and returns ZERO_ECUDA if it (or an earlier launch on
  * this thread) failed; ZERO_ETIMEOUT if a bounded device-side wait (the
- * mbarrier waits of the TMA-staged update) gave up since the last check -- the
+ * mbarrier waits of the TMA-staged update and of the linear calls) gave up since the last check -- the
  * kernel that gave up recorded it, drained its own copies and returned, so
  * the context stays usable; the record is cleared by this call.  ZERO_ERANGE
  * if a zero_schedule_advance found its index past the table since the last

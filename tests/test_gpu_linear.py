@@ -329,6 +329,109 @@ def test_strides_of_slices(zlib, cuda_device):
         zlib.zero_linear(wide[:, :128], w, ref, residual=ref.float())
 
 
+def test_calls_in_a_row_wait_for_one_another(zlib, cuda_device):
+    """Kernels are launched while their predecessors end: chains in which each call
+    reads what the last one wrote, through every kernel, equal the same calls with a
+    synchronisation after each."""
+    g = torch.Generator().manual_seed(14)
+    drop = zlib.ZeroDropout.make(0.1, seed=3)
+    plan = zlib.zero_rope_plan(64)
+    for rows, d in [(2, 320), (96, 320), (700, 1280), (2304, 1280), (77, 333)]:
+        w = [_mat(g, d, d, 1 / math.sqrt(d)).cuda() for _ in range(3)]
+        x0 = _mat(g, rows, d).cuda()
+
+        def chain(wait):
+            x, out = x0.clone(), []
+            for i in range(6):
+                y, dz = torch.empty_like(x), torch.empty_like(x)
+                pre, dx, dw, db = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w[0]), torch.empty(d, dtype=BF, device="cuda")
+                for call in (lambda: zlib.zero_linear(x, w[i % 3], y, act=dp.SILU, pre=pre),
+                             lambda: zlib.zero_dropout(y, y, drop, residual=x),
+                             lambda: zlib.zero_rope(plan, y[:, :320].view(rows, 5, 64), y[:, :320].view(rows, 5, 64)) if d >= 320 and d % 8 == 0 else None,
+                             lambda: zlib.zero_dropout_grad(y, dz, drop, act=dp.SILU, pre=pre, db=db),
+                             lambda: zlib.zero_linear_grad_input(dz, w[i % 3], dx, residual=dz),
+                             lambda: zlib.zero_linear_grad_weight(dz, y, dw, db=db)):
+                    call()
+                    if wait:
+                        torch.cuda.synchronize()
+                out += [y, dw, db]
+                x = dx
+            torch.cuda.synchronize()
+            return out + [x]
+
+        want = chain(True)
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(chain(False), want)), (rows, d)
+
+
+def test_products_on_two_streams(zlib, cuda_device):
+    """Large and small products side by side on two streams (they share SMs, shared
+    and tensor memory) give what they give alone."""
+    g = torch.Generator().manual_seed(15)
+    jobs = [(_mat(g, m, k).cuda(), _mat(g, n, k).cuda()) for m, n, k in ((2048, 2048, 512), (64, 1600, 1600), (300, 515, 333), (1500, 1504, 200))]
+    want = []
+    for x, w in jobs:
+        y = torch.empty(x.shape[0], w.shape[0], dtype=BF, device="cuda")
+        zlib.zero_linear(x, w, y)
+        want.append(y)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        j = i % len(jobs)
+        y = torch.empty_like(want[j])
+        with torch.cuda.stream(streams[i % 3 % 2]):
+            zlib.zero_linear(*jobs[j], y)
+        got.append((j, y))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[j]) for j, y in got)
+    zlib.zero_status_check()
+
+
+def test_captured_products(zlib, cuda_device):
+    """Every kind of product captured in a graph and replayed on new inputs."""
+    g = torch.Generator().manual_seed(16)
+    cases = []
+    for m, n, k in ((3, 200, 128), (64, 320, 256), (2304, 1280, 320), (77, 333, 129)):
+        x, w = _mat(g, m, k).cuda(), _mat(g, n, k).cuda()
+        dz = torch.empty(m, n, dtype=BF, device="cuda")
+        cases.append((x, w, dz, torch.empty_like(x), torch.empty(n, k, device="cuda"), torch.empty(n, device="cuda")))
+
+    def run():
+        for x, w, y, dx, dw, db in cases:
+            zlib.zero_linear(x, w, y)
+            zlib.zero_linear_grad_input(y, w, dx)
+            zlib.zero_linear_grad_weight(y, x, dw, db=db)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for x, *_ in cases:
+        x.copy_(_mat(g, *x.shape))
+    graph.replay()
+    torch.cuda.synchronize()
+    first = [[t.clone() for t in c[2:]] for c in cases]
+    run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for c, f in zip(cases, first) for a, b in zip(c[2:], f))
+
+
+def test_long_sums_in_32_bits(zlib, cuda_device):
+    """fp32 results stay within 1.2e-6 of the exact ones by norm: runs of at most 13
+    blocks of 64 are cut at 2^-24 a step of 16, so at most 52 2^-24 / 2 = 1.5e-6 of a
+    sum that grows evenly and two thirds of it, 1.0e-6, of one that wanders; the
+    additions of the runs round at 2^-24."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+    for m, n, k in ((1024, 2048, 4096), (64, 512, 4096), (333, 250, 2050)):
+        x, w = (torch.randn(r, k, generator=g, device="cuda").to(BF) for r in (m, n))
+        y = torch.empty(m, n, device="cuda")
+        zlib.zero_linear(x, w, y)
+        ref = x.double() @ w.double().t()
+        assert float((y.double() - ref).norm() / ref.norm()) <= 1.2e-6, (m, n, k)
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits(zlib, cuda_device):
     """Rows whose element offsets pass 2^32, in each operand and result."""
