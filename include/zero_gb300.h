@@ -528,7 +528,8 @@ uint32_t zero_crc32(const void* data, int64_t n);
  *   so that dx is that layer's dz; pre is given exactly where act is not NONE.
  * zero_linear_grad_weight:  dw[n,k] = acc + dz[m,n]^T x[m,k],  db[n] = db_acc + sum over m of dz
  *   acc, db, db_acc may be NULL; acc, dw, db_acc and db are dw_dtype.
- * zero_dropout:             y = residual + D(x), all `dtype`; residual may be NULL.
+ * zero_dropout:             y = residual + D(x), all `dtype`; residual may be NULL; y
+ *   may be x itself (same ld).
  * zero_dropout_grad:        dx = D'(dy) act'(pre),  db[c] = db_acc[c] + sum over rows of dx
  *   the dz of a linear whose epilogue dropped and activated; dx may be dy itself
  *   (same type and ld).  The sum is of the fp32 values, before dx is rounded.

@@ -197,6 +197,16 @@ def test_grad_weight_sizes_and_places(zlib, cuda_device, size, pin, pout):
     _check_grad_weight(zlib, *size, pin, pout)
 
 
+@pytest.mark.parametrize("size", [(129, 290, 330), (260, 129, 387), (135, 96, 256), (391, 330, 127)])
+@pytest.mark.parametrize("pin", [(1, 3), (0, 5), (7, 0), (2, 6)])
+def test_whole_and_partial_tiles_at_odd_places(zlib, cuda_device, size, pin):
+    """Unaligned operands of a few whole tiles and stages beside ones that end inside
+    a group of eight rows."""
+    _check_linear(zlib, *size, pin)
+    _check_grad_input(zlib, *size, pin)
+    _check_grad_weight(zlib, *size, pin)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_grad_weight_ends(zlib, cuda_device, dtype):
     for acc, db, db_acc in [(False, False, False), (True, False, False), (False, True, False), (False, True, True)]:

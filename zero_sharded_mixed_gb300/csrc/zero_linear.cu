@@ -2,7 +2,7 @@
 //   zero_linear              y  = residual + D(act(x w^T + bias))
 //   zero_linear_grad_input   dx = residual + D'(dz w) act'(pre)
 //   zero_linear_grad_weight  dw = acc + dz^T x,  db = db_acc + sum over rows of dz
-#include <mutex>
+#include <atomic>
 #include <type_traits>
 
 #include "zero_product.cuh"
@@ -656,8 +656,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
 // cluster, its reduced dimension split over the cluster's CTAs.  Each CTA leaves its
 // part in its shared memory; the parts are added in the order of the CTAs (so the
 // result repeats) while the end is applied.
-// kSoft: warps 0..7 bring the tiles by plain loads, realigned in registers, in place
-// of tensor-map copies, which start on 16-byte boundaries only.
+// kSoft: warps 0..7 bring the tiles by 16-byte copies and realign them, in place of
+// tensor-map copies, which start on 16-byte boundaries only.
 struct SplitParams {
     CUtensorMap map_a, map_b;
     Operand a, b;
@@ -669,105 +669,157 @@ struct SplitParams {
 constexpr int kSplitStages = 3;
 constexpr int kSplitThreads = 288;
 constexpr int kSplitSmem = 1024 + kSplitStages * kStageBytes + 128;
+constexpr int kSoftSmem = 1024 + kStageBytes + 2 * (256 * 144) + 128;
 
 // What one of the 8 loading warps brings of an operand's tile: sub-tile rows r with
-// r % 8 == warp, 64 elements each from any element-aligned place, as the one or two
-// 16-byte blocks that hold a lane's 8 elements; 8 lanes a row, 4 rows (a quad) at a
-// time.  Rows 8 apart lie 16 ld bytes apart, so a warp's rows all start at the same
-// place `shift` of a block: the blocks are shifted by branches that the warp takes
-// together and one funnel shift a word.  (Lanes with shifts of their own: 4400 cycles
-// a stage.  A word a lane, 6 instructions a row: 10000.)  K-major, sub-tile row r is
-// tile row r; MN-major, reduced row r % 64 at kept elements 64 (r / 64) on.
-// Blocks reach up to 7 elements past a row's own, into its neighbours; the few that
-// would reach past the operand's own memory come element by element.
-__device__ __noinline__ uint4 fetch_elements(const uint16_t* e, int n) {
+// r % 8 == warp, 16 of them, 64 elements each from any element-aligned place.  K-major,
+// sub-tile row r is tile row r; MN-major, reduced row r % 64 at kept elements
+// 64 (r / 64) on.  Rows 8 apart lie 16 ld bytes apart, so a warp's rows all start at the
+// same place `shift` of a 16-byte block.  The eight or nine blocks that hold a row come
+// by asynchronous copies, a stage ahead, to a raw buffer of 144 bytes a row; from there
+// each lane takes the two that hold its 8 elements, and a funnel shift a word puts them
+// in place, by branches that the warp takes together.  4095 x 1601 times 4097 x 1601:
+// 224 us, against 257 with each lane's two blocks loaded straight to registers (2047 x
+// 1599 times 1601 x 1599: 62 and 70; 333 x 500 x 9869: 42 and 50; small ones alike).
+// Blocks hold up to 7 elements before and after a row's own, its neighbours'; where one
+// would reach past the operand's own memory its elements come one by one.
+constexpr int kRawPitch = 144, kRawBytes = 256 * kRawPitch;   // 128 rows of A, 128 of B
+
+__device__ __forceinline__ void copy_block(uint32_t dst, uintptr_t src, bool want) {   // zeros where not wanted
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(want ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
+__device__ __noinline__ void fetch_block(uint32_t dst, uintptr_t at, uintptr_t begin, uintptr_t end) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (i < n) w[i / 2] |= (uint32_t)e[i] << (16 * (i & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+        if (at + 2 * i >= begin && at + 2 * i < end)
+            w[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(at + 2 * i) << (16 * (i & 1));
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
+
+// A lane's blocks of 16 rows of 9: block i = lane + 32 c, of row i / 9.
+struct LaneBlocks {
+    uint32_t to[5];   // in a raw buffer
+    __device__ __forceinline__ static int row(int c) { return (int)((threadIdx.x & 31) + 32 * c) / 9; }
+    __device__ __forceinline__ static int block(int c) { return (int)((threadIdx.x & 31) + 32 * c) - 9 * row(c); }
+    __device__ __forceinline__ explicit LaneBlocks(int warp) {
+#pragma unroll
+        for (int c = 0; c < 5; ++c) to[c] = (uint32_t)((warp + 8 * row(c)) * kRawPitch + 16 * block(c));
+    }
+};
 
 template <bool kMn>
 struct SoftTile {
-    const uint16_t* q;          // this lane's elements of rows `warp + 8 (lane / 8)` of the next stage
-    int64_t step;               // elements to 32 rows on
-    int row, rows;              // the operand row of q and their number, from the tile's first
+    uintptr_t from[5];          // this lane's blocks in the next stage
+    int64_t step;               // bytes to the stage after
     int extent;                 // kept elements from the tile's first, at most 128
     uint32_t shift;             // bytes
+    uint32_t mine;              // which of the lane's blocks hold an element, in a whole stage
+    int n;                      // sub-tile rows that are wanted
 
-    __device__ __forceinline__ SoftTile(const Operand& o, int64_t mn0, int64_t k0, int warp) : step(32 * o.ld) {
-        const int lane = threadIdx.x & 31, g = lane & 7;
-        const int64_t first = kMn ? k0 : mn0, left = (kMn ? o.cols : o.rows) - mn0, more = o.rows - first;
-        row = warp + 8 * (lane >> 3);
-        rows = more < INT32_MAX ? (int)more : INT32_MAX;
-        q = o.p + (first + row) * o.ld + (kMn ? mn0 : k0) + 8 * g;
+    __device__ __forceinline__ SoftTile(const Operand& o, int64_t mn0, int64_t k0, int rows, int warp) : n(rows) {
+        const uintptr_t q = reinterpret_cast<uintptr_t>(o.p + ((kMn ? k0 : mn0) + warp) * o.ld + (kMn ? mn0 : k0));
+        const int64_t left = (kMn ? o.cols : o.rows) - mn0, pitch = 16 * o.ld;   // pitch: to 8 rows on
+        shift = (uint32_t)(q & 15);
         extent = left < 128 ? (int)left : 128;
-        shift = (uint32_t)__shfl_sync(0xffffffffu, (int)(reinterpret_cast<uintptr_t>(q) & 15), 0);
-    }
-    // quad j of 4: where, and how many of the lane's 8 elements exist (any number at
-    // least 8 or below 1 for all or none), `left` reduced ones from here on
-    __device__ __forceinline__ const uint16_t* place(int j) const { return kMn ? q + (j & 1) * step + (j >> 1) * 64 : q + j * step; }
-    __device__ __forceinline__ int count(int j, int left) const {
-        if (row + 32 * (kMn ? j & 1 : j) >= rows) return 0;
-        return (kMn ? extent - (j >> 1) * 64 : left) - 8 * (int)(threadIdx.x & 7);
-    }
-    // whether the blocks from that of one element to that of another (addresses) reach
-    // past the operand's memory, and whether any of a stage's tile (from mn0, k0) do
-    static __device__ __forceinline__ bool past(const Operand& o, const uint16_t* first, const uint16_t* last) {
-        return (reinterpret_cast<uintptr_t>(first) & ~(uintptr_t)15) < operand_begin(o) ||
-               (reinterpret_cast<uintptr_t>(last) & ~(uintptr_t)15) + 16 > operand_end(o);
-    }
-    static __device__ __forceinline__ bool at_edge(const Operand& o, int64_t mn0, int64_t k0) {
-        const int64_t r0 = kMn ? k0 : mn0, c0 = kMn ? mn0 : k0, r1 = r0 + (kMn ? 63 : 127), c1 = c0 + (kMn ? 127 : 63);
-        return past(o, o.p + r0 * o.ld + c0, o.p + (r1 < o.rows ? r1 : o.rows - 1) * o.ld + (c1 < o.cols ? c1 : o.cols - 1));
-    }
-    __device__ __forceinline__ bool lone(const Operand& o, int j, int have) const {
-        return past(o, place(j), place(j) + (have < 8 ? have : 8) - 1);
-    }
-
-    __device__ __forceinline__ void load(const Operand& o, bool edge, int n, int left, Blocks8* b) const {
+        step = kMn ? 8 * pitch : 128;
+        mine = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            b[j].x = b[j].y = make_uint4(0u, 0u, 0u, 0u);
-            if (32 * j >= n) continue;
-            const int have = count(j, left);
-            bool whole = have > 0;
-            if (edge && whole) whole = !lone(o, j, have);
-            const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(place(j)) - shift);
-            if (whole) b[j].x = at[0];
-            if (whole && (int)shift + 2 * (have < 8 ? have : 8) > 16) b[j].y = at[1];
+        for (int c = 0; c < 5; ++c) {
+            const int t = LaneBlocks::row(c), g = LaneBlocks::block(c);
+            from[c] = q - shift + (kMn ? (t & 7) * pitch + (t >> 3) * 128 : t * pitch) + 16 * g;
+            if (t < 16 && 8 * t < n && wanted(count(t, 64, warp), g)) mine |= 1u << c;
         }
     }
-    __device__ __forceinline__ void store(const Operand& o, bool edge, int n, int left, const Blocks8* b, uint8_t* dst, int warp) const {
-        const int lane = threadIdx.x & 31;
-        uint8_t* d = dst + (warp + 8 * (lane >> 3)) * 128 + (((lane & 7) ^ warp) << 4);   // row % 8 is the warp
+    // how many of the 64 elements of row t of 16 exist, `left` reduced ones from here
+    // on (at least 64: all)
+    __device__ __forceinline__ int count(int t, int left, int warp) const {
+        if (kMn) return warp + 8 * (t & 7) < left ? extent - (t >> 3) * 64 : 0;
+        return warp + 8 * t < extent ? left : 0;
+    }
+    // whether block g holds any of a row's first `have` elements
+    __device__ __forceinline__ bool wanted(int have, int g) const { return have > 0 && 16 * g < 2 * have + (int)shift && (g < 8 || shift); }
+    // whether any block of a stage's tile (from mn0, k0) reaches past the operand's memory
+    static __device__ __forceinline__ bool at_edge(const Operand& o, int64_t mn0, int64_t k0) {
+        const int64_t r0 = kMn ? k0 : mn0, c0 = kMn ? mn0 : k0, r1 = r0 + (kMn ? 63 : 127), c1 = c0 + (kMn ? 127 : 63);
+        const uintptr_t first = reinterpret_cast<uintptr_t>(o.p + r0 * o.ld + c0);
+        const uintptr_t last = reinterpret_cast<uintptr_t>(o.p + (r1 < o.rows ? r1 : o.rows - 1) * o.ld + (c1 < o.cols ? c1 : o.cols - 1));
+        return (first & ~(uintptr_t)15) < operand_begin(o) || (last & ~(uintptr_t)15) + 16 > operand_end(o);
+    }
+    // whole: the stage has 64 reduced elements and none of its blocks reaches past the
+    // memory; the lane's addresses only move on (formed anew for each block:
+    // 2900 cycles a stage, so 1100)
+    __device__ __forceinline__ void bring(const Operand& o, const LaneBlocks& lb, bool whole, bool edge, int left, uint32_t raw, int warp) {
+        if (whole) {
+#pragma unroll
+            for (int c = 0; c < 5; ++c) {
+                if (mine >> c & 1) copy_block(raw + lb.to[c], from[c], true);
+                from[c] += step;
+            }
+            return;
+        }
+#pragma unroll 1
+        for (int c = 0; c < 5; ++c) {
+            const int t = LaneBlocks::row(c), g = LaneBlocks::block(c);
+            uintptr_t b = from[0];
+            uint32_t dst = lb.to[0];
+#pragma unroll
+            for (int i = 1; i < 5; ++i)
+                if (c == i) b = from[i], dst = lb.to[i];
+            dst += raw;
+            if (t < 16 && 8 * t < n) {
+                const int have = count(t, left, warp);
+                const bool want = wanted(have, g);
+                if (edge && want && (b < operand_begin(o) || b + 16 > operand_end(o)))
+                    fetch_block(dst, b, operand_begin(o), operand_end(o));
+                else
+                    copy_block(dst, b, want);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 5; ++c) from[c] += step;
+    }
+    // Past the reduced dimension's end there have to be zeros; what is past the kept one's
+    // (neighbours, or what the buffer held) only reaches results that are not stored.
+    template <int kWords, bool kWhole>   // kWords: whole words of the shift
+    __device__ __forceinline__ void place_shifted(int left, const uint8_t* raw, uint8_t* d, int warp) const {
+        const int lane = threadIdx.x & 31, g = lane & 7;
         const uint32_t bits = (shift & 2) * 8;
-        const bool by4 = shift & 4, by8 = shift & 8;
+        const uint8_t* s = raw + (warp + 8 * (lane >> 3)) * kRawPitch + 16 * g;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (32 * j >= n) continue;
-            uint32_t w[8] = {b[j].x.x, b[j].x.y, b[j].x.z, b[j].x.w, b[j].y.x, b[j].y.y, b[j].y.z, b[j].y.w};
-#pragma unroll
-            for (int i = 0; i < 6; ++i) w[i] = by8 ? w[i + 2] : w[i];
-#pragma unroll
-            for (int i = 0; i < 5; ++i) w[i] = by4 ? w[i + 1] : w[i];
-            uint4 v = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
-                                 __funnelshift_r(w[3], w[4], bits));
-            const int have = count(j, left);
-            if (have < 8) {
-                v.x &= have >= 2 ? 0xffffffffu : have == 1 ? 0xffffu : 0u;
-                v.y &= have >= 4 ? 0xffffffffu : have == 3 ? 0xffffu : 0u;
-                v.z &= have >= 6 ? 0xffffffffu : have == 5 ? 0xffffu : 0u;
-                v.w &= have == 7 ? 0xffffu : 0u;
+            if (32 * j >= n) break;
+            const uint4 x = *reinterpret_cast<const uint4*>(s + 32 * kRawPitch * j);
+            const uint4 y = *reinterpret_cast<const uint4*>(s + 32 * kRawPitch * j + 16);
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            uint4 v = make_uint4(__funnelshift_r(w[kWords], w[kWords + 1], bits), __funnelshift_r(w[kWords + 1], w[kWords + 2], bits),
+                                 __funnelshift_r(w[kWords + 2], w[kWords + 3], bits), __funnelshift_r(w[kWords + 3], w[kWords + 4], bits));
+            if constexpr (!kWhole) {
+                const int have = count(4 * j + (lane >> 3), left, warp) - 8 * g;
+                if (have < 8) {
+                    v.x &= have >= 2 ? 0xffffffffu : have == 1 ? 0xffffu : 0u;
+                    v.y &= have >= 4 ? 0xffffffffu : have == 3 ? 0xffffu : 0u;
+                    v.z &= have >= 6 ? 0xffffffffu : have == 5 ? 0xffffu : 0u;
+                    v.w &= have == 7 ? 0xffffu : 0u;
+                }
             }
-            if (edge && have > 0 && lone(o, j, have)) v = fetch_elements(place(j), have);
             *reinterpret_cast<uint4*>(d + j * 4096) = v;
         }
     }
-    __device__ __forceinline__ void advance() {
-        q += kMn ? 2 * step : 64;
-        rows -= kMn ? 64 : 0;
+    template <bool kWhole>
+    __device__ __forceinline__ void place(int left, const uint8_t* raw, uint8_t* dst, int warp) const {
+        const int lane = threadIdx.x & 31;
+        uint8_t* d = dst + (warp + 8 * (lane >> 3)) * 128 + (((lane & 7) ^ warp) << 4);   // row % 8 is the warp
+        switch (shift >> 2) {
+            case 0: place_shifted<0, kWhole>(left, raw, d, warp); break;
+            case 1: place_shifted<1, kWhole>(left, raw, d, warp); break;
+            case 2: place_shifted<2, kWhole>(left, raw, d, warp); break;
+            default: place_shifted<3, kWhole>(left, raw, d, warp); break;
+        }
     }
 };
 
@@ -777,9 +829,10 @@ template <bool kF32, int kSoft>
 __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_constant__ SplitParams p) {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSplitStages * kStageBytes);
-    uint64_t* empty = full + kSplitStages;
-    uint64_t* acc_full = empty + kSplitStages;
+    constexpr int kStages = kSoft ? 1 : kSplitStages;   // a stage's products are short beside its loads
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes + (kSoft ? 2 * kRawBytes : 0));
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -790,7 +843,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
     const int kb0 = (int)((int64_t)p.k_blocks * rank / parts), kb1 = (int)((int64_t)p.k_blocks * (rank + 1) / parts);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kSplitStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(full + s, kSoft ? 8 : 1);
             mbar_init(empty + s, 1);
         }
@@ -822,28 +875,49 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
         if (kSoft) {
             int s = 0;
             uint32_t round = 0;
-            SoftTile<kSoft == kSoftMnMn> ta(p.a, row_tile, (int64_t)kb0 * 64, warp);
-            SoftTile<kSoft != kSoftKK> tb(p.b, col_tile, (int64_t)kb0 * 64, warp);
+            SoftTile<kSoft == kSoftMnMn> ta(p.a, row_tile, (int64_t)kb0 * 64, a_rows, warp);
+            SoftTile<kSoft != kSoftKK> tb(p.b, col_tile, (int64_t)kb0 * 64, b_rows, warp);
+            uint8_t* raw = smem + kStages * kStageBytes;
+            const auto left_at = [&](int kb) {
+                const int64_t more = p.depth - (int64_t)kb * 64;
+                return more < 64 ? (int)more : 64;
+            };
+            const LaneBlocks lb(warp);
+            const auto bring = [&](int kb) {
+                if (kb < kb1) {
+                    // only the ends of the reduced dimension meet those of the memory
+                    const bool ends = kb == 0 || kb >= p.k_blocks - 2;
+                    const bool edge_a = ends && ta.at_edge(p.a, row_tile, (int64_t)kb * 64), edge_b = ends && tb.at_edge(p.b, col_tile, (int64_t)kb * 64);
+                    const uint32_t to = smem_addr(raw + ((kb - kb0) & 1) * kRawBytes);
+                    const int left = left_at(kb);
+                    ta.bring(p.a, lb, left == 64 && !edge_a, edge_a, left, to, warp);
+                    tb.bring(p.b, lb, left == 64 && !edge_b, edge_b, left, to + 128 * kRawPitch, warp);
+                }
+                copies_commit();   // a group a stage, empty past the last
+            };
+            bring(kb0);
+            bring(kb0 + 1);
             for (int kb = kb0; kb < kb1; ++kb) {
-                const int64_t k0 = (int64_t)kb * 64, more = p.depth - k0;
-                const int left = more < 64 ? (int)more : 64;
-                // only the ends of the reduced dimension meet those of the memory
-                const bool ends = kb == 0 || kb >= p.k_blocks - 2;
-                const bool edge_a = ends && ta.at_edge(p.a, row_tile, k0), edge_b = ends && tb.at_edge(p.b, col_tile, k0);
-                uint8_t* stage = smem + s * kStageBytes;
-                Blocks8 a[4], b[4];   // all of a stage's loads fly before the wait for room
-                ta.load(p.a, edge_a, a_rows, left, a);
-                tb.load(p.b, edge_b, b_rows, left, b);
+                copies_wait<1>();
+                __syncwarp();
                 if (round > 0 && !(ok = warp_wait(empty + s, (round - 1) & 1))) break;
-                ta.store(p.a, edge_a, a_rows, left, a, stage, warp);
-                tb.store(p.b, edge_b, b_rows, left, b, stage + 16384, warp);
-                ta.advance();
-                tb.advance();
+                uint8_t* stage = smem + s * kStageBytes;
+                const uint8_t* from = raw + ((kb - kb0) & 1) * kRawBytes;
+                const int left = left_at(kb);
+                if (left == 64) {
+                    ta.template place<true>(left, from, stage, warp);
+                    tb.template place<true>(left, from + 128 * kRawPitch, stage + 16384, warp);
+                } else {
+                    ta.template place<false>(left, from, stage, warp);
+                    tb.template place<false>(left, from + 128 * kRawPitch, stage + 16384, warp);
+                }
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full + s);
-                if (++s == kSplitStages) s = 0, ++round;
+                bring(kb + 2);   // where this stage's blocks were
+                if (++s == kStages) s = 0, ++round;
             }
+            copies_wait<0>();   // none are left but after a failed wait
         } else if (warp == 0) {
             int s = 0;
             uint32_t round = 0;
@@ -866,10 +940,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
                         tensor_load(b, &p.map_b, k, (int)col_tile, bar);
                     }
                 }
-                if (++s == kSplitStages) s = 0, ++round;
+                if (++s == kStages) s = 0, ++round;
             }
             if (!ok)   // copies in flight land before the CTA ends
-                for (int i = 0; i < kSplitStages; ++i) {
+                for (int i = 0; i < kStages; ++i) {
                     const uint32_t done = i < s ? round : round - 1;
                     if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
                 }
@@ -892,7 +966,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
                     if (left > 16 * i) mma_bf16<false>(tmem, da + i * a_step, db + i * b_step, idesc, n > kb0 || i > 0);
                 mma_commit<false>(empty + s);
             }
-            if (++s == kSplitStages) s = 0, ++round;
+            if (++s == kStages) s = 0, ++round;
         }
         if (elect_one()) mma_commit<false>(acc_full);   // after a failed wait too: the tensor memory is free once it arrives
     }
@@ -1000,17 +1074,19 @@ static bool make_map(const Operand& o, int box_rows, CUtensorMap* map) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Raises a kernel's shared-memory limit once per device.
-static int allow_smem(const void* kernel, int bytes, std::once_flag* once) {
+// Raises a kernel's shared-memory limit, once per device (again after a failure).
+typedef std::atomic<bool> Done[64];
+static int allow_smem(const void* kernel, int bytes, Done& done) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ZERO_ECUDA;
-    cudaError_t e = cudaSuccess;
-    std::call_once(once[dev], [&] { e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+    if (done[dev].load(std::memory_order_acquire)) return ZERO_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) {
         note_cuda_error(e);
         (void)cudaGetLastError();
         return ZERO_ECUDA;
     }
+    done[dev].store(true, std::memory_order_release);
     return ZERO_OK;
 }
 
@@ -1070,10 +1146,10 @@ static Plan plan_split(const Product& p, bool f32, bool soft) {
 static int32_t box_rows(int64_t rows) { return rows < 128 ? (int32_t)((rows + 7) / 8 * 8) : 128; }
 
 static int launch_pair(const Product& p, const Ending& e, const Plan& plan, cudaStream_t s) {
-    static std::once_flag once[3][64];
+    static Done done[3];
     const int blocks = (int)((p.depth + 63) / 64), runs = e.out_f32 ? (blocks + kRun - 1) / kRun : 1;
     void (*kernel)(PairParams) = runs > 1 ? pair_kernel<true, true> : e.out_f32 ? pair_kernel<true, false> : pair_kernel<false, false>;
-    if (const int rc = allow_smem((const void*)kernel, kPairSmem, once[runs > 1 ? 2 : e.out_f32])) return rc;
+    if (const int rc = allow_smem((const void*)kernel, kPairSmem, done[runs > 1 ? 2 : e.out_f32])) return rc;
     PairParams q{};
     q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
     q.tiles_m = (int32_t)plan.tiles_m; q.tiles_n = (int32_t)plan.tiles_n; q.bn = plan.bn;
@@ -1088,13 +1164,14 @@ static int launch_pair(const Product& p, const Ending& e, const Plan& plan, cuda
 }
 
 static int launch_split(const Product& p, const Ending& e, const Plan& plan, bool soft, cudaStream_t s) {
-    static std::once_flag once[8][64];
+    static Done done[8];
     static void (*const kernels[2][4])(SplitParams) = {
         {split_kernel<false, kCopied>, split_kernel<false, kSoftKK>, split_kernel<false, kSoftKMn>, split_kernel<false, kSoftMnMn>},
         {split_kernel<true, kCopied>, split_kernel<true, kSoftKK>, split_kernel<true, kSoftKMn>, split_kernel<true, kSoftMnMn>}};
     const int kind = !soft ? kCopied : p.a.mn ? kSoftMnMn : p.b.mn ? kSoftKMn : kSoftKK;
     void (*kernel)(SplitParams) = kernels[e.out_f32][kind];
-    if (const int rc = allow_smem((const void*)kernel, kSplitSmem, once[e.out_f32 * 4 + kind])) return rc;
+    const int smem = soft ? kSoftSmem : kSplitSmem;
+    if (const int rc = allow_smem((const void*)kernel, smem, done[e.out_f32 * 4 + kind])) return rc;
     const int64_t k_blocks = (p.depth + 63) / 64;
     if (!plan.tiles_n || k_blocks > INT32_MAX) return ZERO_ERANGE;
     SplitParams q{};
@@ -1105,7 +1182,7 @@ static int launch_split(const Product& p, const Ending& e, const Plan& plan, boo
     q.box_a = box_rows(p.rows);
     if (!soft && (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn, &q.map_b))) return ZERO_ECUDA;
     return launch_dense(kernel, dim3((unsigned)(plan.tiles_m * plan.tiles_n * plan.parts)), kSplitThreads, (unsigned)plan.parts, true,
-                        kSplitSmem, s, q);
+                        smem, s, q);
 }
 
 static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
