@@ -212,33 +212,20 @@ struct FragmentEnd {
     }
 };
 
-// kParts parts of eight whole, aligned columns each, 8 rows apart, to the end
-// together: each branch of the end is taken once for all of them, and their chains
-// interleave.  in[i]: part i has a row.  load() before the accumulators are there.
-template <bool kF32, int kParts>
+// The split kernel's end of eight whole, aligned columns.  load(): what it reads
+// beside its accumulators, before they are there.
+template <bool kF32>
 struct VectorEnd {
-    uint4 add[kParts][kF32 ? 2 : 1], slope[kParts];   // what the parts read beside their accumulators, as loaded
+    uint4 add[kF32 ? 2 : 1], slope;   // as loaded
     float bias[8];
-    bool in[kParts];
 
-    __device__ __forceinline__ void load(const Ending& e, int64_t row, int64_t col, int64_t rows) {
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) in[i] = row + 8 * i < rows;
+    __device__ __forceinline__ void load(const Ending& e, int64_t row, int64_t col) {
         if (e.add) {
             const char* q = static_cast<const char*>(e.add) + (row * e.ld_add + col) * (kF32 ? 4 : 2);
-#pragma unroll
-            for (int i = 0; i < kParts; ++i, q += 8 * e.ld_add * (kF32 ? 4 : 2))
-                if (in[i]) {
-                    add[i][0] = reinterpret_cast<const uint4*>(q)[0];
-                    if constexpr (kF32) add[i][1] = reinterpret_cast<const uint4*>(q)[1];
-                }
+            add[0] = reinterpret_cast<const uint4*>(q)[0];
+            if constexpr (kF32) add[1] = reinterpret_cast<const uint4*>(q)[1];
         }
-        if (e.slope) {
-            const uint16_t* q = e.slope + row * e.ld_slope + col;
-#pragma unroll
-            for (int i = 0; i < kParts; ++i, q += 8 * e.ld_slope)
-                if (in[i]) slope[i] = *reinterpret_cast<const uint4*>(q);
-        }
+        if (e.slope) slope = *reinterpret_cast<const uint4*>(e.slope + row * e.ld_slope + col);
         if (e.bias) {
             unpack8(*reinterpret_cast<const uint4*>(e.bias + col), bias);
         } else {
@@ -247,44 +234,26 @@ struct VectorEnd {
         }
     }
 
-    __device__ __forceinline__ void finish(const Ending& e, uint32_t step, int64_t row, int64_t col, float (&v)[kParts][8]) {
+    __device__ __forceinline__ void finish(const Ending& e, uint32_t step, int64_t row, int64_t col, float (&v)[8]) {
+        float t[8];
         if (e.bias) {
 #pragma unroll
-            for (int i = 0; i < kParts; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += bias[j];
+            for (int j = 0; j < 8; ++j) v[j] += bias[j];
         }
-        if (e.pre) {
-            uint16_t* q = e.pre + row * e.ld_pre + col;
-#pragma unroll
-            for (int i = 0; i < kParts; ++i, q += 8 * e.ld_pre)
-                if (in[i]) *reinterpret_cast<uint4*>(q) = pack8(v[i]);
-        }
+        if (e.pre) *reinterpret_cast<uint4*>(e.pre + row * e.ld_pre + col) = pack8(v);
         if (e.slope) {
-            float t[kParts][8];
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) unpack8(slope[i], t[i]);
-            slope_apply<8 * kParts>(e.act, t[0], v[0]);
+            unpack8(slope, t);
+            slope_apply<8>(e.act, t, v);
         } else if (e.act) {
-            act_apply<8 * kParts>(e.act, v[0]);
+            act_apply<8>(e.act, v);
         }
-        if (e.drop.cut) {
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) drop8(e.drop, step, row + 8 * i, col >> 3, v[i]);
-        }
+        if (e.drop.cut) drop8(e.drop, step, row, col >> 3, v);
         if (e.add) {
+            raw8<kF32>(add, t);
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-                float t[8];
-                raw8<kF32>(add[i], t);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += t[j];
-            }
+            for (int j = 0; j < 8; ++j) v[j] += t[j];
         }
-        char* q = static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2);
-#pragma unroll
-        for (int i = 0; i < kParts; ++i, q += 8 * e.ld_out * (kF32 ? 4 : 2))
-            if (in[i]) store8(q, kF32, true, 8, v[i]);
+        store8(static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2), kF32, true, 8, v);
     }
 };
 
@@ -1010,15 +979,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
                 const int r = r0 + (lane >> 2);
                 const int64_t row = row_tile + (rb / 4) * 32 + r, col = col0 + (lane & 3) * 8;
                 if (row < p.rows) {
-                    VectorEnd<kF32, 1> end;
-                    end.load(p.e, row, col, p.rows);
-                    float v[1][8] = {};
+                    VectorEnd<kF32> end;
+                    end.load(p.e, row, col);
+                    float v[8] = {};
                     const uint32_t g0 = group_place(r, 2 * (lane & 3)), g1 = group_place(r, 2 * (lane & 3) + 1);
                     for (int i = 0; i < parts; ++i) {
                         const uint32_t at = peer_addr(chunk, i);
                         const float4 x = peer_load(at + g0), y = peer_load(at + g1);
-                        v[0][0] += x.x; v[0][1] += x.y; v[0][2] += x.z; v[0][3] += x.w;
-                        v[0][4] += y.x; v[0][5] += y.y; v[0][6] += y.z; v[0][7] += y.w;
+                        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
                     }
                     end.finish(p.e, step, row, col, v);
                 }
