@@ -29,14 +29,10 @@ int take_linear_status() {
 }
 
 // ---- the end of a product --------------------------------------------------------
-// Accumulators reach the end in units of 8 rows x 32 columns of fp32 in shared
-// memory (a part of a 32 x 32 chunk), one warp a unit.  Row r of a chunk is 128
-// bytes; its 16-byte group g stands at group_place(r, g), so that neither the rows
-// written by 32 lanes nor the pairs of groups read by 4 x 8 lanes share a bank.
-__device__ __forceinline__ uint32_t group_place(int r, int g) {
-    const int s = ((r & 1) << 2) | ((r >> 1) & 3);
-    return (uint32_t)r * 128u + (uint32_t)((((g >> 1) | ((g & 1) << 2)) ^ s) << 4);
-}
+// Accumulators that pass through shared memory stand there in 32 x 32 chunks of fp32.
+// Row r of a chunk is 128 bytes; its 16-byte group g stands at group_place(r, g), so
+// that rows written by 32 lanes share no bank, and 8 rows (a unit, a warp's) lie on end.
+__device__ __forceinline__ uint32_t group_place(int r, int g) { return (uint32_t)r * 128u + (uint32_t)((g ^ (r & 7)) << 4); }
 
 // The pair kernel's end of 16 rows x 32 whole, aligned columns, a warp together,
 // with the accumulators as tensor memory gives them (tmem_load_fragment): lane
@@ -970,33 +966,71 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
         const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
         const uint32_t base = smem_addr(smem);
         const int units = (a_left + 7) / 8 * n_chunks;
-        for (int u = rank * 8 + warp; u < units; u += parts * 8) {
+        for (int u = warp * parts + rank; u < units; u += parts * 8) {   // few units: over all CTAs
             const int rb = u / n_chunks, c = u - rb * n_chunks;   // rows 8 rb .., chunk column c
             const uint32_t chunk = base + ((rb / 4) * 4 + c) * kChunkBytes;
             const int r0 = (rb & 3) * 8;
             const int64_t row0 = row_tile + rb * 8, col0 = col_tile + c * 32;
             if (p.e.vec && col0 + 32 <= p.cols) {
-                const int r = r0 + (lane >> 2);
-                const int64_t row = row_tile + (rb / 4) * 32 + r, col = col0 + (lane & 3) * 8;
-                if (row < p.rows) {
-                    VectorEnd<kF32> end;
-                    end.load(p.e, row, col);
-                    float v[8] = {};
-                    const uint32_t g0 = group_place(r, 2 * (lane & 3)), g1 = group_place(r, 2 * (lane & 3) + 1);
-                    for (int i = 0; i < parts; ++i) {
-                        const uint32_t at = peer_addr(chunk, i);
-                        const float4 x = peer_load(at + g0), y = peer_load(at + g1);
-                        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-                        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-                    }
-                    end.finish(p.e, step, row, col, v);
+                // The unit is 1 KB on end in every part: read as it lies, 16 bytes a lane,
+                // group g of row lane / 8 and group g ^ 4 four rows on; then lanes of even
+                // g take their neighbour's half of the first row, the others of the second.
+                // (Two loads of 32 scattered groups: 8 bytes a cycle from other CTAs.)
+                const int g = (lane & 7) ^ ((r0 + (lane >> 3)) & 7);
+                const bool odd = g & 1;
+                const int64_t row = row0 + (lane >> 3) + (odd ? 4 : 0), col = col0 + (odd ? g ^ 4 : g) / 2 * 8;
+                VectorEnd<kF32> end;
+                if (row < p.rows) end.load(p.e, row, col);
+                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), t = s;
+                if (parts == 1) {   // half the latency of a peer's
+                    const float4* own = reinterpret_cast<const float4*>(smem + (chunk - base) + r0 * 128) + lane;
+                    s = own[0];
+                    t = own[32];
                 }
+                constexpr int kFly = kF32 ? 2 : 4;   // parts whose loads fly together; an fp32 end has fewer registers
+                for (int i = 0; parts > 1 && i < parts; i += kFly) {
+                    float4 x[kFly], y[kFly];
+#pragma unroll
+                    for (int j = 0; j < kFly; ++j)
+                        if (i + j < parts) {
+                            const uint32_t at = peer_addr(chunk, i + j) + r0 * 128 + lane * 16;
+                            x[j] = peer_load(at);
+                            y[j] = peer_load(at + 512);
+                        }
+#pragma unroll
+                    for (int j = 0; j < kFly; ++j)
+                        if (i + j < parts) {
+                            s.x += x[j].x; s.y += x[j].y; s.z += x[j].z; s.w += x[j].w;
+                            t.x += y[j].x; t.y += y[j].y; t.z += y[j].z; t.w += y[j].w;
+                        }
+                }
+                const float4 give = odd ? s : t, keep = odd ? t : s;
+                const float4 got = make_float4(__shfl_xor_sync(0xffffffffu, give.x, 1), __shfl_xor_sync(0xffffffffu, give.y, 1),
+                                               __shfl_xor_sync(0xffffffffu, give.z, 1), __shfl_xor_sync(0xffffffffu, give.w, 1));
+                const float4 lo = odd ? got : keep, hi = odd ? keep : got;
+                float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                if (row < p.rows) end.finish(p.e, step, row, col, v);
             } else {
                 float v[8] = {};
-                for (int i = 0; i < parts; ++i) {
-                    const uint32_t at = peer_addr(chunk, i) + (lane & 3) * 4;
+                if (parts == 1) {
+                    const uint8_t* own = smem + (chunk - base) + (lane & 3) * 4;
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) v[r] += peer_load1(at + group_place(r0 + r, lane >> 2));
+                    for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const float*>(own + group_place(r0 + r, lane >> 2));
+                }
+                for (int i = 0; parts > 1 && i < parts; i += 2) {
+                    float x[2][8];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (i + j < parts) {
+                            const uint32_t at = peer_addr(chunk, i + j) + (lane & 3) * 4;
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) x[j][r] = peer_load1(at + group_place(r0 + r, lane >> 2));
+                        }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (i + j < parts)
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) v[r] += x[j][r];
                 }
                 end_rows<kF32, 8>(p.e, step, row0, col0, p.rows, p.cols, v);
             }
