@@ -197,6 +197,20 @@ def test_grad_weight_sizes_and_places(zlib, cuda_device, size, pin, pout):
     _check_grad_weight(zlib, *size, pin, pout)
 
 
+# few tiles and a long sum, ended inside a block and inside either half of a tile
+LONG = [(65, 96, 4096), (129, 250, 4104), (200, 1000, 6400), (257, 136, 5000), (128, 40, 8192), (384, 72, 2056)]
+
+
+@pytest.mark.parametrize("size", LONG)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_sums_of_few_tiles(zlib, cuda_device, size, dtype):
+    m, n, k = size
+    _check_linear(zlib, m, n, k, (8, 8), (8, 16), dtype=dtype, act=dp.GELU, p=0.1)
+    _check_linear(zlib, m, n, k, (0, 0), (1, 3), dtype=dtype, bias=False, pre=False)
+    _check_grad_input(zlib, m, k, n, (8, 8), (8, 16), dtype=dtype, act=dp.SILU, p=0.1)
+    _check_grad_weight(zlib, k, m, n, (8, 8), (8, 16), dtype=dtype)
+
+
 @pytest.mark.parametrize("size", [(129, 290, 330), (260, 129, 387), (135, 96, 256), (391, 330, 127)])
 @pytest.mark.parametrize("pin", [(1, 3), (0, 5), (7, 0), (2, 6)])
 def test_whole_and_partial_tiles_at_odd_places(zlib, cuda_device, size, pin):

@@ -315,6 +315,79 @@ __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t
         }
 }
 
+// A unit of 8 rows x 32 columns whose parts stand at the same place `chunk` (and row r0
+// of it) of the shared memories of CTAs first, first + stride, ..: added in that order,
+// then to the end.  A warp together.
+template <bool kF32>
+__device__ __forceinline__ void end_joined(const Ending& e, uint32_t step, const uint8_t* smem, uint32_t chunk, int r0, int64_t row0, int64_t col0,
+                                           int64_t rows, int64_t cols, int parts, int first, int stride) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_addr(smem);
+    if (e.vec && col0 + 32 <= cols) {
+        // The unit is 1 KB on end in every part: read as it lies, 16 bytes a lane,
+        // group g of row lane / 8 and group g ^ 4 four rows on; then lanes of even
+        // g take their neighbour's half of the first row, the others of the second.
+        // (Two loads of 32 scattered groups: 8 bytes a cycle from other CTAs.)
+        const int g = (lane & 7) ^ ((r0 + (lane >> 3)) & 7);
+        const bool odd = g & 1;
+        const int64_t row = row0 + (lane >> 3) + (odd ? 4 : 0), col = col0 + (odd ? g ^ 4 : g) / 2 * 8;
+        VectorEnd<kF32> end;
+        if (row < rows) end.load(e, row, col);
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), t = s;
+        if (parts == 1) {   // half the latency of a peer's
+            const float4* own = reinterpret_cast<const float4*>(smem + chunk + r0 * 128) + lane;
+            s = own[0];
+            t = own[32];
+        }
+        constexpr int kFly = kF32 ? 2 : 4;   // parts whose loads fly together; an fp32 end has fewer registers
+        for (int i = 0; parts > 1 && i < parts; i += kFly) {
+            float4 x[kFly], y[kFly];
+#pragma unroll
+            for (int j = 0; j < kFly; ++j)
+                if (i + j < parts) {
+                    const uint32_t at = peer_addr(base + chunk, first + (i + j) * stride) + r0 * 128 + lane * 16;
+                    x[j] = peer_load(at);
+                    y[j] = peer_load(at + 512);
+                }
+#pragma unroll
+            for (int j = 0; j < kFly; ++j)
+                if (i + j < parts) {
+                    s.x += x[j].x; s.y += x[j].y; s.z += x[j].z; s.w += x[j].w;
+                    t.x += y[j].x; t.y += y[j].y; t.z += y[j].z; t.w += y[j].w;
+                }
+        }
+        const float4 give = odd ? s : t, keep = odd ? t : s;
+        const float4 got = make_float4(__shfl_xor_sync(0xffffffffu, give.x, 1), __shfl_xor_sync(0xffffffffu, give.y, 1),
+                                       __shfl_xor_sync(0xffffffffu, give.z, 1), __shfl_xor_sync(0xffffffffu, give.w, 1));
+        const float4 lo = odd ? got : keep, hi = odd ? keep : got;
+        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (row < rows) end.finish(e, step, row, col, v);
+    } else {
+        float v[8] = {};
+        if (parts == 1) {
+            const uint8_t* own = smem + chunk + (lane & 3) * 4;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const float*>(own + group_place(r0 + r, lane >> 2));
+        }
+        for (int i = 0; parts > 1 && i < parts; i += 2) {
+            float x[2][8];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (i + j < parts) {
+                    const uint32_t at = peer_addr(base + chunk, first + (i + j) * stride) + (lane & 3) * 4;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) x[j][r] = peer_load1(at + group_place(r0 + r, lane >> 2));
+                }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (i + j < parts)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) v[r] += x[j][r];
+        }
+        end_rows<kF32, 8>(e, step, row0, col0, rows, cols, v);
+    }
+}
+
 // ---- waits -------------------------------------------------------------------------
 constexpr long long kWaitCycles = 1ll << 31;   // SM cycles (about a second) before a wait gives up
 
@@ -450,7 +523,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
     if (warp == 2) tmem_alloc<true>(tmem_slot, 512);
     tcgen05_fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_started();
     tcgen05_fence_after();
     await_predecessor();
     const uint32_t tmem = *tmem_slot;
@@ -964,80 +1037,154 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
 
     if (warp < 8 && ok) {
         const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
-        const uint32_t base = smem_addr(smem);
         const int units = (a_left + 7) / 8 * n_chunks;
         for (int u = warp * parts + rank; u < units; u += parts * 8) {   // few units: over all CTAs
             const int rb = u / n_chunks, c = u - rb * n_chunks;   // rows 8 rb .., chunk column c
-            const uint32_t chunk = base + ((rb / 4) * 4 + c) * kChunkBytes;
+            const uint32_t chunk = ((rb / 4) * 4 + c) * kChunkBytes;
             const int r0 = (rb & 3) * 8;
             const int64_t row0 = row_tile + rb * 8, col0 = col_tile + c * 32;
-            if (p.e.vec && col0 + 32 <= p.cols) {
-                // The unit is 1 KB on end in every part: read as it lies, 16 bytes a lane,
-                // group g of row lane / 8 and group g ^ 4 four rows on; then lanes of even
-                // g take their neighbour's half of the first row, the others of the second.
-                // (Two loads of 32 scattered groups: 8 bytes a cycle from other CTAs.)
-                const int g = (lane & 7) ^ ((r0 + (lane >> 3)) & 7);
-                const bool odd = g & 1;
-                const int64_t row = row0 + (lane >> 3) + (odd ? 4 : 0), col = col0 + (odd ? g ^ 4 : g) / 2 * 8;
-                VectorEnd<kF32> end;
-                if (row < p.rows) end.load(p.e, row, col);
-                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), t = s;
-                if (parts == 1) {   // half the latency of a peer's
-                    const float4* own = reinterpret_cast<const float4*>(smem + (chunk - base) + r0 * 128) + lane;
-                    s = own[0];
-                    t = own[32];
-                }
-                constexpr int kFly = kF32 ? 2 : 4;   // parts whose loads fly together; an fp32 end has fewer registers
-                for (int i = 0; parts > 1 && i < parts; i += kFly) {
-                    float4 x[kFly], y[kFly];
-#pragma unroll
-                    for (int j = 0; j < kFly; ++j)
-                        if (i + j < parts) {
-                            const uint32_t at = peer_addr(chunk, i + j) + r0 * 128 + lane * 16;
-                            x[j] = peer_load(at);
-                            y[j] = peer_load(at + 512);
-                        }
-#pragma unroll
-                    for (int j = 0; j < kFly; ++j)
-                        if (i + j < parts) {
-                            s.x += x[j].x; s.y += x[j].y; s.z += x[j].z; s.w += x[j].w;
-                            t.x += y[j].x; t.y += y[j].y; t.z += y[j].z; t.w += y[j].w;
-                        }
-                }
-                const float4 give = odd ? s : t, keep = odd ? t : s;
-                const float4 got = make_float4(__shfl_xor_sync(0xffffffffu, give.x, 1), __shfl_xor_sync(0xffffffffu, give.y, 1),
-                                               __shfl_xor_sync(0xffffffffu, give.z, 1), __shfl_xor_sync(0xffffffffu, give.w, 1));
-                const float4 lo = odd ? got : keep, hi = odd ? keep : got;
-                float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                if (row < p.rows) end.finish(p.e, step, row, col, v);
-            } else {
-                float v[8] = {};
-                if (parts == 1) {
-                    const uint8_t* own = smem + (chunk - base) + (lane & 3) * 4;
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const float*>(own + group_place(r0 + r, lane >> 2));
-                }
-                for (int i = 0; parts > 1 && i < parts; i += 2) {
-                    float x[2][8];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (i + j < parts) {
-                            const uint32_t at = peer_addr(chunk, i + j) + (lane & 3) * 4;
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) x[j][r] = peer_load1(at + group_place(r0 + r, lane >> 2));
-                        }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (i + j < parts)
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) v[r] += x[j][r];
-                }
-                end_rows<kF32, 8>(p.e, step, row0, col0, p.rows, p.cols, v);
-            }
+            end_joined<kF32>(p.e, step, smem, chunk, r0, row0, col0, p.rows, p.cols, parts, 0, 1);
         }
     }
     __syncwarp();
     if (parts > 1) cluster_sync();   // the parts are read before their CTAs end
+}
+
+// ---- the deep kernel -------------------------------------------------------------------
+// Few tiles with a long reduced dimension: the pair kernel's 256 x bn tile on a cluster
+// of two or four pairs, each with a share of the reduced dimension and six stages of its
+// own, joined like the split kernel's.  An operand's element is brought to half as many
+// SMs as by the split kernel's tiles, whose copies meet the limit of L2 (about 53 bytes a
+// cycle and SM), and more SMs work than there are whole tiles.
+constexpr int kDeepThreads = 576;   // 16 warps for the end, one for the products, one for the copies
+constexpr int kDeepSmem = 1024 + kPairStages * kStageBytes + 256;
+
+template <bool kF32>
+__global__ void __launch_bounds__(kDeepThreads, 1) deep_kernel(const __grid_constant__ PairParams p) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kStageBytes);
+    uint64_t* empty = full + kPairStages;
+    uint64_t* acc_full = empty + kPairStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int ctas = (int)cluster_size(), rank = (int)cluster_rank();
+    const int parts = ctas / 2, part = rank / 2, half = rank & 1, even = rank & ~1;
+    const int tile = blockIdx.x / ctas, tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
+    const int width = tile_width(p, tn);
+    const int kb0 = (int)((int64_t)p.k_blocks * part / parts), kb1 = (int)((int64_t)p.k_blocks * (part + 1) / parts);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(acc_full, 1);
+        fence_barrier_init();
+        tensor_map_prefetch(&p.map_a);
+        tensor_map_prefetch(&p.map_b);
+    }
+    if (warp == 16) tmem_alloc<true>(tmem_slot, 256);
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_started();
+    tcgen05_fence_after();
+    await_predecessor();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+
+    if (warp == 17) {
+        int s = 0;
+        uint32_t round = 0;
+        const int own_b = p.bn / 2, b_boxes = p.b_mn ? (own_b + 63) / 64 : 1;
+        const uint32_t stage_bytes = (p.a_mn ? 16384u : (uint32_t)p.box_a * 128u) + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)own_b * 128u);
+        const int row = tm * 256 + half * 128, col = tn * p.bn + half * (width / 2);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (round > 0 && !(ok = warp_wait(empty + s, (round - 1) & 1))) break;
+            const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384;
+            const uint32_t bar = peer_addr(smem_addr(full + s), even);
+            const int k = kb * 64;
+            if (elect_one()) {
+                if (half == 0) mbar_arrive_expect_tx(full + s, 2 * stage_bytes);
+                if (p.a_mn) {
+                    tensor_load_pair(a, &p.map_a, row, k, bar);
+                    tensor_load_pair(a + kSubTileBytes, &p.map_a, row + 64, k, bar);
+                } else {
+                    tensor_load_pair(a, &p.map_a, k, row, bar);
+                }
+                if (p.b_mn) {
+                    for (int i = 0; i < b_boxes; ++i) tensor_load_pair(b + i * kSubTileBytes, &p.map_b, col + 64 * i, k, bar);
+                } else {
+                    tensor_load_pair(b, &p.map_b, k, col, bar);
+                }
+            }
+            if (++s == kPairStages) s = 0, ++round;
+        }
+        if (!ok && half == 0)   // copies in flight land before the CTAs end
+            for (int i = 0; i < kPairStages; ++i) {
+                const uint32_t done = i < s ? round : round - 1;   // the last round issued on stage i
+                if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
+            }
+    } else if (warp == 16 && half == 0) {
+        int s = 0;
+        uint32_t round = 0;
+        const uint32_t idesc = instruction_descriptor(256, width, p.a_mn, p.b_mn);
+        const uint32_t a_step = descriptor_step(p.a_mn), b_step = descriptor_step(p.b_mn);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!(ok = warp_wait(full + s, round & 1))) break;
+            tcgen05_fence_after();
+            const uint32_t a = smem_addr(smem + s * kStageBytes);
+            const uint64_t da = smem_descriptor(a, p.a_mn), db = smem_descriptor(a + 16384, p.b_mn);
+            const int64_t left = p.depth - (int64_t)kb * 64;
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)   // the last step of all may end early
+                    if (left > 16 * i) mma_bf16<true>(tmem, da + i * a_step, db + i * b_step, idesc, kb > kb0 || i > 0);
+                mma_commit<true>(empty + s, 3u << even);
+            }
+            if (++s == kPairStages) s = 0, ++round;
+        }
+        if (elect_one()) mma_commit<true>(acc_full, 3u << even);   // after a failed wait too: the tensor memory is free once it arrives
+    }
+    __syncwarp();
+    ok = warp_wait(acc_full, 0) && ok;
+    tcgen05_fence_after();
+
+    // this CTA's 128 rows of its pair's part, chunk (q, c) at 4 KB each, where the stages were
+    const int64_t row_half = (int64_t)tm * 256 + half * 128, col_tile = (int64_t)tn * p.bn;
+    const int rows_left = p.rows - row_half < 0 ? 0 : p.rows - row_half < 128 ? (int)(p.rows - row_half) : 128;
+    const int n_chunks = width / 32;
+    if (warp < 16 && ok) {
+        const int q = warp & 3;
+        if (q * 32 < rows_left) {
+            for (int c = warp / 4; c < n_chunks; c += 4) {
+                uint32_t acc[32];
+                tmem_load32(tmem + c * 32 + ((uint32_t)(q * 32) << 16), acc);
+                uint8_t* chunk = smem + (q * 8 + c) * kChunkBytes;
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                    *reinterpret_cast<uint4*>(chunk + group_place(lane, g)) = make_uint4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
+            }
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tcgen05_fence_after();
+    if (warp == 16) tmem_free<true>(tmem, 256);
+
+    if (warp < 16 && ok) {
+        const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
+        const int units = (rows_left + 7) / 8 * n_chunks;
+        for (int u = warp * parts + part; u < units; u += parts * 16) {
+            const int rb = u / n_chunks, c = u - rb * n_chunks;
+            end_joined<kF32>(p.e, step, smem, ((rb / 4) * 8 + c) * kChunkBytes, (rb & 3) * 8, row_half + rb * 8, col_tile + c * 32, p.rows, p.cols,
+                             parts, half, 2);
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // the parts are read before their CTAs end
 }
 
 // ---- launches -----------------------------------------------------------------------------
@@ -1144,6 +1291,28 @@ static Plan plan_split(const Product& p, bool f32, bool soft) {
     return best;
 }
 
+// Clusters of `pairs` pairs that run at the same time, once per device.
+static int deep_clusters(const void* kernel, int pairs, std::atomic<int> (&known)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t c{};
+        cudaLaunchAttribute a{};
+        a.id = cudaLaunchAttributeClusterDimension;
+        a.val.clusterDim.x = 2 * pairs;
+        a.val.clusterDim.y = a.val.clusterDim.z = 1;
+        c.gridDim = dim3((unsigned)(2 * pairs));
+        c.blockDim = dim3(kDeepThreads);
+        c.dynamicSmemBytes = kDeepSmem;
+        c.attrs = &a;
+        c.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) n = 0;
+        if (n > 0) known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 // Rows of A that a copy brings: no more than there are.  (Boxes of 128 rows over a
 // matrix of 5 to 14 took two to three times as long as over one of 16.)
 static int32_t box_rows(int64_t rows) { return rows < 128 ? (int32_t)((rows + 7) / 8 * 8) : 128; }
@@ -1164,6 +1333,47 @@ static int launch_pair(const Product& p, const Ending& e, const Plan& plan, cuda
     if (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
     const int64_t tiles = plan.tiles_m * plan.tiles_n, pairs = sm_count() / 2;
     return launch_dense(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, 2, true, kPairSmem, s, q);
+}
+
+// Waves of clusters of pairs, as many at a time as the SMs' groups hold: a start, the
+// share's blocks, and the join at about ten bytes a cycle from other SMs.  Not for up to
+// 64 rows, of which the split kernel's copies bring no more than there are.  (Measured
+// without and with this kernel, in us: 256 x 11008 times 4096 x 11008 36.9 and 26.7;
+// 512 x 6400 times 1600 x 6400 21.9 and 16.1; 1024 x 16384 times 1600 x 16384 55 and 38.6;
+// 64 x 11008 times 4096 x 11008 21.4 and 24.3; 384 x 4096 times 4096 x 4096 17.4 and 19.1.)
+static Plan plan_deep(const Product& p, bool f32) {
+    static Done done[2];
+    static std::atomic<int> at_once[2][2][64];
+    const void* kernel = f32 ? (const void*)deep_kernel<true> : (const void*)deep_kernel<false>;
+    const int64_t k_blocks = (p.depth + 63) / 64;
+    Plan best{INT64_MAX, (p.rows + 255) / 256, 0, 0, 0};
+    if (p.rows <= 64 || k_blocks < 8 || k_blocks > INT32_MAX || allow_smem(kernel, kDeepSmem, done[f32]) != ZERO_OK) return best;
+    for (int n = 2; n <= 4; n *= 2) {
+        const int64_t clusters = deep_clusters(kernel, n, at_once[f32][n / 4]), blocks = (k_blocks + n - 1) / n;
+        if (clusters <= 0 || (f32 && blocks > kRun)) continue;   // fp32 results: short runs, as in the pair kernel
+        for (int bn = 64; bn <= kWidest; bn += 32) {
+            const int64_t tn = (p.cols + bn - 1) / bn;
+            if (tn > INT32_MAX / 16 / best.tiles_m) continue;
+            const int64_t waves = (best.tiles_m * tn + clusters - 1) / clusters;
+            const int64_t join = 3000 + 512 * bn * (n - 1) / n / 10;
+            const int64_t cycles = 5500 + waves * (2000 + blocks * (2 * bn > 256 + bn ? 2 * bn : 256 + bn) * 11 / 10 + join);
+            if (cycles < best.cycles) best.cycles = cycles, best.tiles_n = tn, best.bn = bn, best.parts = n;
+        }
+    }
+    return best;
+}
+
+static int launch_deep(const Product& p, const Ending& e, const Plan& plan, cudaStream_t s) {
+    PairParams q{};
+    q.rows = p.rows; q.cols = p.cols; q.depth = p.depth;
+    q.tiles_m = (int32_t)plan.tiles_m; q.tiles_n = (int32_t)plan.tiles_n; q.bn = plan.bn;
+    q.k_blocks = (int32_t)((p.depth + 63) / 64);
+    q.a_mn = p.a.mn; q.b_mn = p.b.mn;
+    q.e = e;
+    q.box_a = box_rows(p.rows);
+    if (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
+    return launch_dense(e.out_f32 ? deep_kernel<true> : deep_kernel<false>, dim3((unsigned)(plan.tiles_m * plan.tiles_n * plan.parts * 2)),
+                        kDeepThreads, (unsigned)plan.parts * 2, true, kDeepSmem, s, q);
 }
 
 static int launch_split(const Product& p, const Ending& e, const Plan& plan, bool soft, cudaStream_t s) {
@@ -1196,13 +1406,15 @@ static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
     if ((p.rows + 127) / 128 > INT32_MAX / 64) return ZERO_ERANGE;
     const bool reach = copies_reach(p.a) && copies_reach(p.b);
     const Plan split = plan_split(p, e.out_f32, !reach), pair = reach ? plan_pair(p, e.out_f32) : Plan{INT64_MAX, 0, 0, 0, 0};
-    const int64_t tiled = pair.cycles < split.cycles ? pair.cycles : split.cycles;
+    const Plan deep = reach ? plan_deep(p, e.out_f32) : Plan{INT64_MAX, 0, 0, 0, 0};
+    const int64_t whole = pair.cycles < split.cycles ? pair.cycles : split.cycles, tiled = deep.cycles < whole ? deep.cycles : whole;
     // the kernel of a few rows reads the weights at about 2950 bytes a cycle for one row
     // (11008 x 4096: 16 us, 18 by tiles) and half of it for three or four
     if (p.rows <= kMostRows && !p.a.mn && !p.b.mn) {
         const int64_t read = p.cols * (p.depth / 8) * 16 / 2950;
         if (p.rows == 1 || 3000 + read * (p.rows == 2 ? 14 : 23) / 10 < tiled) return launch_rows(p, e, s);
     }
+    if (deep.cycles < whole) return launch_deep(p, e, deep, s);
     return pair.cycles < split.cycles ? launch_pair(p, e, pair, s) : launch_split(p, e, split, !reach, s);
 }
 

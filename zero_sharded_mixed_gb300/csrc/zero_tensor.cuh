@@ -83,14 +83,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
             "r"((uint32_t)accumulate) : "memory");
 }
 
-// The barrier (of both CTAs of a pair, at the same offset) receives one arrival
-// when the products issued so far are done.
+// The barrier (of both CTAs of a pair, `ctas` of the cluster, at the same offset)
+// receives one arrival when the products issued so far are done.
 template <bool kPair>
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t ctas = 3) {
     if constexpr (kPair)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                smem_addr(bar)), "h"((uint16_t)3) : "memory");
+                smem_addr(bar)), "h"((uint16_t)ctas) : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -143,6 +143,10 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// After fence_barrier_init: the CTAs' barriers exist, and nothing else is ordered.
+__device__ __forceinline__ void cluster_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Hands over tensor memory alone (its reads are ordered by the tcgen05 fences), so
 // the arrival need not order other memory.
