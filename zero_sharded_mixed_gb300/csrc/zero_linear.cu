@@ -406,7 +406,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // rows split between the two tensor memories, its B tile between the two shared
 // memories), tiles taken in turn from a grouped order.  Warp 0 copies, warp 1 of the
 // even CTA issues the products, warps 4..19 end the previous tile out of the other
-// half of the tensor memory meanwhile.
+// half of the tensor memory meanwhile.  Bound by the tensor core: 256 x 256 x 64 take 512
+// cycles, in which 64 KB come in, what an SM's share of L2 gives; a CTA alone would need
+// half as much again for the same products.  8192 x 8192 x 8192 in 555 us (1.98 PFLOP/s,
+// cuBLAS 2.01), where the clock falls to about 1.4 GHz; 8192 x 1600 times 6400 x 1600 with
+// the tanh GELU and its pre-activation 101 us (1.66 PFLOP/s), without either 88.
 struct PairParams {
     CUtensorMap map_a, map_b;
     int64_t rows, cols, depth;
@@ -693,7 +697,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_cons
 // Smaller products, and those whose operands are not aligned: a 128 x bn tile a
 // cluster, its reduced dimension split over the cluster's CTAs.  Each CTA leaves its
 // part in its shared memory; the parts are added in the order of the CTAs (so the
-// result repeats) while the end is applied.
+// result repeats) while the end is applied.  Bound by latency where it is small (64 x 1600
+// times 1600 x 1600 in 6.0 us, of which the start, the first copies, the two cluster
+// barriers and the join take two thirds) and by L2 or the weights' bytes where it is not
+// (128 x 4096 times 11008 x 4096 in 22 us, 4.1 TB/s of weights).
 // kSoft: warps 0..7 bring the tiles by 16-byte copies and realign them, in place of
 // tensor-map copies, which start on 16-byte boundaries only.
 struct SplitParams {
@@ -1055,7 +1062,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
 // of two or four pairs, each with a share of the reduced dimension and six stages of its
 // own, joined like the split kernel's.  An operand's element is brought to half as many
 // SMs as by the split kernel's tiles, whose copies meet the limit of L2 (about 53 bytes a
-// cycle and SM), and more SMs work than there are whole tiles.
+// cycle and SM), and more SMs work than there are whole tiles.  512 x 6400 times 1600 x
+// 6400 in 16.1 us (650 TFLOP/s): 50 blocks at 390 cycles, of which the tensor core needs
+// half, then some 10000 cycles of start, cluster barriers and join.  Bound by L2 while it
+// runs and by the join, at ten bytes a cycle from another SM, where the sum is short.
 constexpr int kDeepThreads = 576;   // 16 warps for the end, one for the products, one for the copies
 constexpr int kDeepSmem = 1024 + kPairStages * kStageBytes + 256;
 
@@ -1408,8 +1418,9 @@ static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
     const Plan split = plan_split(p, e.out_f32, !reach), pair = reach ? plan_pair(p, e.out_f32) : Plan{INT64_MAX, 0, 0, 0, 0};
     const Plan deep = reach ? plan_deep(p, e.out_f32) : Plan{INT64_MAX, 0, 0, 0, 0};
     const int64_t whole = pair.cycles < split.cycles ? pair.cycles : split.cycles, tiled = deep.cycles < whole ? deep.cycles : whole;
-    // the kernel of a few rows reads the weights at about 2950 bytes a cycle for one row
-    // (11008 x 4096: 16 us, 18 by tiles) and half of it for three or four
+    // The kernel of a few rows reads the weights at about 2950 bytes a cycle for one row
+    // (weights 4800 x 1600 4.9 us, 6.7 by tiles; 4096 x 11008 16.4 and 18.6; the one size
+    // found where tiles are faster is 11008 x 4096, 21 and 19) and half of it for more.
     if (p.rows <= kMostRows && !p.a.mn && !p.b.mn) {
         const int64_t read = p.cols * (p.depth / 8) * 16 / 2950;
         if (p.rows == 1 || 3000 + read * (p.rows == 2 ? 14 : 23) / 10 < tiled) return launch_rows(p, e, s);

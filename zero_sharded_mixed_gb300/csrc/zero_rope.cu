@@ -79,6 +79,10 @@ __device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t m) { return m ? 
 // kVec: two 16-byte vectors an item, which hold kCount whole pairs (a's and b's in
 // the half layout, neighbours in the interleaved one) or up to two of the vectors
 // that are copied; else a pair an item, or up to two copied elements.
+// Bound by memory: 8192 tokens x 64 heads of 128 bf16 inside a packed projection in
+// 45.9 us (5.9 TB/s), 6001 x 25 x 64 fp32 with half of each head turned in 14.6 us
+// (5.3 TB/s).  Sixteen items a thread, two bf16 ones (four fp32) in flight: 49 us with
+// four of either.
 template <bool kF32, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 turn[kThreads > ZERO_ROPE_MAX / 2 ? kThreads : ZERO_ROPE_MAX / 2];   // [cta_tokens][pairs]
