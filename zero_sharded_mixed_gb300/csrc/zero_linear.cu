@@ -318,9 +318,11 @@ __device__ __forceinline__ void end_rows(const Ending& e, uint32_t step, int64_t
 // A unit of 8 rows x 32 columns whose parts stand at the same place `chunk` (and row r0
 // of it) of the shared memories of CTAs first, first + stride, ..: added in that order,
 // then to the end.  A warp together.
+// last: the warp reads no more parts after this unit, and arrives at the cluster's
+// barrier before its end and its stores.
 template <bool kF32>
 __device__ __forceinline__ void end_joined(const Ending& e, uint32_t step, const uint8_t* smem, uint32_t chunk, int r0, int64_t row0, int64_t col0,
-                                           int64_t rows, int64_t cols, int parts, int first, int stride) {
+                                           int64_t rows, int64_t cols, int parts, int first, int stride, bool last) {
     const int lane = threadIdx.x & 31;
     const uint32_t base = smem_addr(smem);
     if (e.vec && col0 + 32 <= cols) {
@@ -359,6 +361,10 @@ __device__ __forceinline__ void end_joined(const Ending& e, uint32_t step, const
         const float4 give = odd ? s : t, keep = odd ? t : s;
         const float4 got = make_float4(__shfl_xor_sync(0xffffffffu, give.x, 1), __shfl_xor_sync(0xffffffffu, give.y, 1),
                                        __shfl_xor_sync(0xffffffffu, give.z, 1), __shfl_xor_sync(0xffffffffu, give.w, 1));
+        if (last) {
+            __syncwarp();
+            cluster_arrive();
+        }
         const float4 lo = odd ? got : keep, hi = odd ? keep : got;
         float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
         if (row < rows) end.finish(e, step, row, col, v);
@@ -383,6 +389,10 @@ __device__ __forceinline__ void end_joined(const Ending& e, uint32_t step, const
                 if (i + j < parts)
 #pragma unroll
                     for (int r = 0; r < 8; ++r) v[r] += x[j][r];
+        }
+        if (last) {
+            __syncwarp();
+            cluster_arrive();
         }
         end_rows<kF32, 8>(e, step, row0, col0, rows, cols, v);
     }
@@ -1042,19 +1052,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_kernel(const __grid_co
     tcgen05_fence_after();
     if (warp == 8) tmem_free<false>(tmem, 128);
 
-    if (warp < 8 && ok) {
+    const int units = (a_left + 7) / 8 * n_chunks, unit0 = warp * parts + rank;   // few units: over all CTAs
+    if (warp < 8 && ok && unit0 < units) {
         const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
-        const int units = (a_left + 7) / 8 * n_chunks;
-        for (int u = warp * parts + rank; u < units; u += parts * 8) {   // few units: over all CTAs
+        for (int u = unit0; u < units; u += parts * 8) {
             const int rb = u / n_chunks, c = u - rb * n_chunks;   // rows 8 rb .., chunk column c
             const uint32_t chunk = ((rb / 4) * 4 + c) * kChunkBytes;
             const int r0 = (rb & 3) * 8;
             const int64_t row0 = row_tile + rb * 8, col0 = col_tile + c * 32;
-            end_joined<kF32>(p.e, step, smem, chunk, r0, row0, col0, p.rows, p.cols, parts, 0, 1);
+            end_joined<kF32>(p.e, step, smem, chunk, r0, row0, col0, p.rows, p.cols, parts, 0, 1, parts > 1 && u + parts * 8 >= units);
         }
+    } else if (parts > 1) {
+        cluster_arrive();
     }
     __syncwarp();
-    if (parts > 1) cluster_sync();   // the parts are read before their CTAs end
+    if (parts > 1) cluster_wait();   // the parts are read before their CTAs end
 }
 
 // ---- the deep kernel -------------------------------------------------------------------
@@ -1184,17 +1196,19 @@ __global__ void __launch_bounds__(kDeepThreads, 1) deep_kernel(const __grid_cons
     tcgen05_fence_after();
     if (warp == 16) tmem_free<true>(tmem, 256);
 
-    if (warp < 16 && ok) {
+    const int units = (rows_left + 7) / 8 * n_chunks, unit0 = warp * parts + part;
+    if (warp < 16 && ok && unit0 < units) {
         const uint32_t step = p.e.drop.cut ? drop_step(p.e.drop) : 0u;
-        const int units = (rows_left + 7) / 8 * n_chunks;
-        for (int u = warp * parts + part; u < units; u += parts * 16) {
+        for (int u = unit0; u < units; u += parts * 16) {
             const int rb = u / n_chunks, c = u - rb * n_chunks;
             end_joined<kF32>(p.e, step, smem, ((rb / 4) * 8 + c) * kChunkBytes, (rb & 3) * 8, row_half + rb * 8, col_tile + c * 32, p.rows, p.cols,
-                             parts, half, 2);
+                             parts, half, 2, u + parts * 16 >= units);
         }
+    } else {
+        cluster_arrive();
     }
     __syncwarp();
-    cluster_sync();   // the parts are read before their CTAs end
+    cluster_wait();   // the parts are read before their CTAs end
 }
 
 // ---- launches -----------------------------------------------------------------------------
