@@ -84,6 +84,12 @@ def test_dropout_grad_with_slope_and_sums(zlib, cuda_device, size, place):
         assert ok() and b_ok()
 
 
+@pytest.mark.parametrize("size", [(1025, 264), (2049, 1600), (600, 4800), (5000, 24), (129, 6400), (1100, 32)])
+def test_sums_of_aligned_rows(zlib, cuda_device, size):
+    """Every share of rows and width of a warp that the sums are split by."""
+    test_dropout_grad_with_slope_and_sums(zlib, cuda_device, size, (8, 8))
+
+
 @pytest.mark.parametrize("shape", [(300, 520), (77, 41)])
 def test_dropout_grad_in_place_and_repeatable(zlib, cuda_device, shape):
     g = torch.Generator().manual_seed(4)
