@@ -456,6 +456,33 @@ def test_long_sums_in_32_bits(zlib, cuda_device):
         assert float((y.double() - ref).norm() / ref.norm()) <= 1.2e-6, (m, n, k)
 
 
+def test_longest_sums_in_32_bits(zlib, cuda_device):
+    """The same bound at any depth, of every call that sums, on the 16-byte grid and
+    off it: what a run's cut loses goes with the run's own sum, so that the loss of
+    the whole stays the fraction of it that a run loses, however many runs there are,
+    and their additions, rounded, add 2^-24 times half the root of their number."""
+    g = torch.Generator(device="cuda").manual_seed(18)
+
+    def mat(rows, cols):
+        return torch.randn(rows, cols, generator=g, device="cuda").to(BF)
+
+    def check(got, ref, what):
+        assert float((got.double() - ref).norm() / ref.norm()) <= 1.2e-6, what
+
+    for m, n, k in ((64, 512, 16384), (64, 4096, 11008), (256, 768, 16384), (9, 300, 50257), (333, 250, 9001), (3, 200, 50257)):
+        x, w, y = mat(m, k), mat(n, k), torch.empty(m, n, device="cuda")
+        zlib.zero_linear(x, w, y)
+        check(y, x.double() @ w.double().t(), ("y", m, n, k))
+    for m, n, k in ((64, 16384, 512), (100, 50257, 200), (333, 9001, 250)):
+        dz, w, dx = mat(m, n), mat(n, k), torch.empty(m, k, device="cuda")
+        zlib.zero_linear_grad_input(dz, w, dx)
+        check(dx, dz.double() @ w.double(), ("dx", m, n, k))
+    for m, n, k in ((65536, 512, 512), (50257, 40, 48), (50257, 41, 47), (9001, 250, 333)):
+        dz, x, dw = mat(m, n), mat(m, k), torch.empty(n, k, device="cuda")
+        zlib.zero_linear_grad_weight(dz, x, dw)
+        check(dw, dz.double().t() @ x.double(), ("dw", m, n, k))
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits(zlib, cuda_device):
     """Rows whose element offsets pass 2^32, in each operand and result."""
