@@ -388,6 +388,54 @@ def test_calls_in_a_row_wait_for_one_another(zlib, cuda_device):
             assert all(torch.equal(a, b) for a, b in zip(chain(False), want)), (rows, d)
 
 
+@pytest.mark.parametrize("rows", [1, 2, 4])
+@pytest.mark.parametrize("d", [2048, 5120])
+def test_few_wide_rows_in_a_row(zlib, cuda_device, rows, d):
+    """One to four rows, as a few new tokens have: each call reads a buffer that the last
+    one wrote, over and over the same two, without a synchronisation and in a graph,
+    beside the same calls with one after each."""
+    g = torch.Generator().manual_seed(19)
+    w = [_mat(g, d, d, 1 / math.sqrt(d)).cuda() for _ in range(2)]
+    x0 = _mat(g, rows, d).cuda()
+    plan, drop = zlib.zero_rope_plan(64), zlib.ZeroDropout.make(0.1, seed=3)
+    a, b = torch.empty_like(x0), torch.empty_like(x0)
+    kept = torch.empty(24, rows, d, dtype=BF, device="cuda")
+
+    def chain(wait):
+        def run(call):
+            call()
+            if wait:
+                torch.cuda.synchronize()
+
+        a.copy_(x0)
+        for i in range(12):
+            run(lambda: zlib.zero_linear(a, w[i % 2], b, act=dp.SILU, residual=a))
+            run(lambda: zlib.zero_rope(plan, b.view(rows, d // 64, 64), b.view(rows, d // 64, 64), pos0=i))
+            run(lambda: zlib.zero_linear(b, w[1 - i % 2], a, residual=x0))
+            run(lambda: zlib.zero_dropout(a, kept[2 * i], drop, residual=b))
+            run(lambda: zlib.zero_dropout(b, kept[2 * i + 1], None))
+        torch.cuda.synchronize()
+        return kept.clone()
+
+    want = chain(True)
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.copy_(x0)
+        for i in range(12):
+            zlib.zero_linear(a, w[i % 2], b, act=dp.SILU, residual=a)
+            zlib.zero_rope(plan, b.view(rows, d // 64, 64), b.view(rows, d // 64, 64), pos0=i)
+            zlib.zero_linear(b, w[1 - i % 2], a, residual=x0)
+            zlib.zero_dropout(a, kept[2 * i], drop, residual=b)
+            zlib.zero_dropout(b, kept[2 * i + 1], None)
+    for _ in range(5):
+        kept.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want)
+
+
 def test_products_on_two_streams(zlib, cuda_device):
     """Large and small products side by side on two streams (they share SMs, shared
     and tensor memory) give what they give alone."""

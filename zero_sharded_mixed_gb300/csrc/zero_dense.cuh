@@ -189,6 +189,12 @@ __device__ __forceinline__ void raw8(const uint4* u, float* v) {   // as loaded:
     }
 }
 
+// A 128-bit load of a stream.  Kernels of this file's launches (below) start before
+// their predecessor's writes have ended, so that nothing they read is read-only for
+// their lifetime: coherent loads alone, never the read-only path (ld.global.nc), which
+// may give a stale line and which the compiler may move above the wait.
+__device__ __forceinline__ uint4 ld_live_u4(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
+
 // p points at the first of the eight; `vec`: p is 16-byte aligned and count == 8.
 __device__ __forceinline__ void load8(const void* p, bool f32, bool vec, int count, float* v) {
     if (vec) {

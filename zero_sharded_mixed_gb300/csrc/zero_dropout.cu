@@ -115,11 +115,11 @@ __global__ void __launch_bounds__(kThreads, 3) dropout_kernel(const DropoutParam
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (row + j * row_step < p.rows) {
-                xv[j][0] = ld_stream_u4(x);
-                if constexpr (kF32) xv[j][1] = ld_stream_u4(x + 16);
+                xv[j][0] = ld_live_u4(x);
+                if constexpr (kF32) xv[j][1] = ld_live_u4(x + 16);
                 if (side) {
-                    sv[j][0] = ld_stream_u4(side);
-                    if constexpr (kF32 && !kGrad) sv[j][1] = ld_stream_u4(side + 16);
+                    sv[j][0] = ld_live_u4(side);
+                    if constexpr (kF32 && !kGrad) sv[j][1] = ld_live_u4(side + 16);
                 }
             }
             x += dx;

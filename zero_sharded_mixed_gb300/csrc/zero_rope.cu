@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                 out[k] = static_cast<T*>(p.y) + (t0 + t) * p.yt + (h0 + h) * p.yh + in_head;
                 cs[k] = turns ? turn + t * pairs + i * kCount : nullptr;
                 if constexpr (kVec) {
-                    a[k] = ld_stream_u4(q);
-                    if (second[k]) b[k] = ld_stream_u4(q + second[k]);
+                    a[k] = ld_live_u4(q);
+                    if (second[k]) b[k] = ld_live_u4(q + second[k]);
                 } else {
                     a[k] = rope_load<kF32>(q, 0);
                     if (second[k]) b[k] = rope_load<kF32>(q, second[k]);

@@ -37,9 +37,9 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Product p, const E
         for (; c < whole; c += stride) {
             uint4 w[kCols], x[kM];
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) w[j] = ld_stream_u4(p.b.p + bc[j] * p.b.ld + c);
+            for (int j = 0; j < kCols; ++j) w[j] = ld_live_u4(p.b.p + bc[j] * p.b.ld + c);
 #pragma unroll
-            for (int i = 0; i < kM; ++i) x[i] = i < p.rows ? __ldg(reinterpret_cast<const uint4*>(p.a.p + i * p.a.ld + c)) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < kM; ++i) x[i] = i < p.rows ? *reinterpret_cast<const uint4*>(p.a.p + i * p.a.ld + c) : make_uint4(0u, 0u, 0u, 0u);
             float wv[kCols][8], xv[8];
 #pragma unroll
             for (int j = 0; j < kCols; ++j) unpack8(w[j], wv[j]);
