@@ -1346,10 +1346,16 @@ struct Plan {
     int bn, parts;
 };
 
+// Pairs of SMs; one where the runtime could not say how many there are.
+static int64_t sm_pairs() {
+    const int n = sm_count();
+    return n < 2 ? 1 : n / 2;
+}
+
 // Waves of pairs, each a tile's blocks (bound by the tensor core, or for narrow tiles
 // by shared memory) and the part of its end that nothing hides.
 static Plan plan_pair(const Product& p, bool f32) {
-    const int64_t pairs = sm_count() / 2, k_blocks = (p.depth + 63) / 64;
+    const int64_t pairs = sm_pairs(), k_blocks = (p.depth + 63) / 64;
     const int widest = f32 && k_blocks > kRun ? kWidestRuns : kWidest;
     Plan best{INT64_MAX, (p.rows + 255) / 256, 0, 0, 1};   // no width fits: not taken
     for (int bn = widest; bn >= 32; bn -= 32) {
@@ -1428,7 +1434,7 @@ static int launch_pair(const Product& p, const Ending& e, const Plan& plan, cuda
     q.e = e;
     q.box_a = box_rows(p.rows);
     if (!make_map(p.a, p.a.mn ? 64 : q.box_a, &q.map_a) || !make_map(p.b, p.b.mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
-    const int64_t tiles = plan.tiles_m * plan.tiles_n, pairs = sm_count() / 2;
+    const int64_t tiles = plan.tiles_m * plan.tiles_n, pairs = sm_pairs();
     return launch_dense(kernel, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), kPairThreads, 2, true, kPairSmem, s, q);
 }
 
