@@ -1,6 +1,9 @@
 """What a failed runtime call leaves behind.  The library's own objects are linked
 over a runtime without a device (tests/c/fake_cudart.c) in which one chosen call
-fails, so no GPU is needed and none sees a fault."""
+fails, so no GPU is needed and none sees a fault.  A dense operator whose call
+succeeds all the same (another kernel took it) has to leave no error for
+zero_status_check to blame on it, and one that fails reports that by its code,
+once, and the next call stands on its own."""
 import ctypes
 import os
 import shutil
@@ -116,3 +119,12 @@ def test_a_failed_question_is_answered(zlib, fake, call, failing, first):
     for nth, code, launched, _ in _sweep(zlib, fake, call, failing, first):
         assert code in (0, zlib.ZERO_EINVAL, zlib.ZERO_ECUDA), (nth, code)
         assert code != 0 or launched > 0, nth
+
+
+@pytest.mark.filterwarnings("ignore:This process:DeprecationWarning")
+@pytest.mark.parametrize("first", [True, False], ids=["first call", "later call"])
+@pytest.mark.parametrize("failing", FAILING)
+@pytest.mark.parametrize("call", CALLS)
+def test_no_error_is_left_behind(zlib, fake, call, failing, first):
+    for nth, code, _, status in _sweep(zlib, fake, call, failing, first):
+        assert status == 0, f"call {nth} of {failing} failed, the operator returned {code}, and its error stayed"

@@ -1321,11 +1321,22 @@ static bool make_map(const Operand& o, int box_rows, CUtensorMap* map) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The current device, if there is one below `most`.  A failed question leaves no error
+// behind: a caller goes on without the answer or reports it by its code.
+static bool device_below(int most, int* dev) {
+    const cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+    }
+    return e == cudaSuccess && *dev >= 0 && *dev < most;
+}
+
 // Raises a kernel's shared-memory limit, once per device (again after a failure).
 typedef std::atomic<bool> Done[64];
 static int allow_smem(const void* kernel, int bytes, Done& done) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ZERO_ECUDA;
+    if (!device_below(64, &dev)) return ZERO_ECUDA;
     if (done[dev].load(std::memory_order_acquire)) return ZERO_OK;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) {
@@ -1397,7 +1408,7 @@ static Plan plan_split(const Product& p, bool f32, bool soft) {
 // Clusters of `pairs` pairs that run at the same time, once per device.
 static int deep_clusters(const void* kernel, int pairs, std::atomic<int> (&known)[64]) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (!device_below(64, &dev)) return 0;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n == 0) {
         cudaLaunchConfig_t c{};
@@ -1410,7 +1421,12 @@ static int deep_clusters(const void* kernel, int pairs, std::atomic<int> (&known
         c.dynamicSmemBytes = kDeepSmem;
         c.attrs = &a;
         c.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &c);
+        if (e != cudaSuccess) {
+            note_cuda_error(e);
+            (void)cudaGetLastError();
+            n = 0;
+        }
         if (n > 0) known[dev].store(n, std::memory_order_relaxed);
     }
     return n;

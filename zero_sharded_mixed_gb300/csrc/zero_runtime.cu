@@ -26,8 +26,11 @@ int check_device_ptr(const void* p) {
     }
     if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return ZERO_EINVAL;
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || a.device != dev) return ZERO_EINVAL;
-    return ZERO_OK;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ZERO_EINVAL;
+    }
+    return a.device == dev ? ZERO_OK : ZERO_EINVAL;
 }
 
 int check_source_ptr(const void* p) {
@@ -48,16 +51,21 @@ std::atomic<int> g_sm_count[kMaxDevices];
 
 int sm_count() {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
+        (void)cudaGetLastError();
+        return 1;
+    }
     if (dev >= kMaxDevices) {
         int n = 1;
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) (void)cudaGetLastError();
         return n > 0 ? n : 1;
     }
     int n = g_sm_count[dev].load(std::memory_order_relaxed);
     if (n <= 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-            n = 1;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+            (void)cudaGetLastError();
+            return 1;   // asked again by the next call
+        }
         g_sm_count[dev].store(n, std::memory_order_relaxed);
     }
     return n;
