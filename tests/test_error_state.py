@@ -85,9 +85,16 @@ def _apart(work):
     return [int(v) for v in said.split()]
 
 
+_swept = {}
+
+
 def _sweep(zlib, fake, call, failing, first):
     """For every call of `failing` that the operator makes, on the library's first call
-    or a later one: (which, the operator's answer, what it launched, the status after)."""
+    or a later one: (which, the operator's answer, what it launched, the status after);
+    an answer of None where the process ended.  Asked once for the tests below."""
+    key = call, failing, first
+    if key in _swept:
+        return _swept[key]
     run = _calls(zlib)[call]
 
     def scenario(nth):
@@ -99,14 +106,13 @@ def _sweep(zlib, fake, call, failing, first):
         fake.fake_fail(b"", 0)
         return code, seen, fake.fake_launches() - before, fake.zero_status_check(None)
 
+    found = _swept[key] = []
     for nth in range(1, 64):
-        answer = _apart(lambda: scenario(nth))
-        assert len(answer) == 4, f"the process ended when call {nth} of {failing} failed"
-        code, seen, launched, status = answer
+        code, seen, launched, status = _apart(lambda: scenario(nth)) or (None, nth, 0, 0)
         if seen < nth:
             assert code == 0
-            return
-        yield nth, code, launched, status
+            return found
+        found.append((nth, code, launched, status))
     raise AssertionError("no end")
 
 

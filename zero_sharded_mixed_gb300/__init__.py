@@ -33,13 +33,16 @@ _BINDING_NAMES = {
 _ENGINE_NAMES = {"ZeroEngine", "Zero3Engine"}
 
 
+_binding = None   # the module, looked up once; its names anew each time, so that a replaced one is seen
+
+
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        from . import binding
-        value = getattr(binding, name)
-        if callable(value):             # looked up once: 0.7 us a call otherwise
-            globals()[name] = value
-        return value
+        global _binding
+        if _binding is None:
+            from . import binding
+            _binding = binding
+        return getattr(_binding, name)
     if name in _ENGINE_NAMES:
         from . import engine
         return getattr(engine, name)
