@@ -195,39 +195,13 @@ __device__ __forceinline__ void raw8(const uint4* u, float* v) {   // as loaded:
 // may give a stale line and which the compiler may move above the wait.
 __device__ __forceinline__ uint4 ld_live_u4(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 
-// p points at the first of the eight; `vec`: p is 16-byte aligned and count == 8.
-__device__ __forceinline__ void load8(const void* p, bool f32, bool vec, int count, float* v) {
-    if (vec) {
-        if (f32) {
-            const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            unpack8(*reinterpret_cast<const uint4*>(p), v);
-        }
+// p: the first of the eight, 16-byte aligned.
+__device__ __forceinline__ void store8(void* p, bool f32, const float* v) {
+    if (f32) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = j >= count ? 0.0f : f32 ? static_cast<const float*>(p)[j] : bf16_one(static_cast<const uint16_t*>(p)[j]);
-    }
-}
-__device__ __forceinline__ void store8(void* p, bool f32, bool vec, int count, const float* v) {
-    if (vec) {
-        if (f32) {
-            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            *reinterpret_cast<uint4*>(p) = pack8(v);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < count) {
-                if (f32)
-                    static_cast<float*>(p)[j] = v[j];
-                else
-                    static_cast<uint16_t*>(p)[j] = to_bf16(v[j]);
-            }
+        *reinterpret_cast<uint4*>(p) = pack8(v);
     }
 }
 

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 3) dropout_kernel(const DropoutParam
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] += t[k];
             }
-            if (!kSums || p.y) store8(y, p.y_f32, true, 8, v);
+            if (!kSums || p.y) store8(y, p.y_f32, v);
             if constexpr (kSums) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) sum[k] += v[k];

@@ -249,7 +249,7 @@ struct VectorEnd {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += t[j];
         }
-        store8(static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2), kF32, true, 8, v);
+        store8(static_cast<char*>(e.out) + (row * e.ld_out + col) * (kF32 ? 4 : 2), kF32, v);
     }
 };
 

@@ -77,17 +77,12 @@ __device__ __forceinline__ uint4 shift_blocks(uintptr_t begin, uintptr_t end, co
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The end of a product for one element.
+// The end of a forward product for one element (no slope).
 template <bool kF32>
 __device__ __forceinline__ void end_one(const Ending& e, uint32_t step, int64_t row, int64_t col, float v) {
     if (e.bias) v += bf16_one(e.bias[col]);
     if (e.pre) e.pre[row * e.ld_pre + col] = to_bf16(v);
-    if (e.slope) {
-        const float z = bf16_one(e.slope[row * e.ld_slope + col]);
-        slope_apply<1>(e.act, &z, &v);
-    } else if (e.act) {
-        act_apply<1>(e.act, &v);
-    }
+    if (e.act) act_apply<1>(e.act, &v);
     if (e.drop.cut) {
         const uint4 b = philox_block(e.drop, step, (uint32_t)row, (uint32_t)(col >> 3));
         const uint32_t w = col & 4 ? (col & 2 ? b.w : b.z) : (col & 2 ? b.y : b.x);
@@ -102,7 +97,7 @@ __device__ __forceinline__ void end_one(const Ending& e, uint32_t step, int64_t 
     }
 }
 
-// The kernel of a few rows (zero_rows.cu), both operands K-major.
+// The kernel of a few rows (zero_rows.cu), both operands K-major: forward products alone.
 constexpr int kMostRows = 4;
 int launch_rows(const Product& p, const Ending& e, cudaStream_t s);
 
