@@ -83,8 +83,11 @@ int launch_column_sum(int64_t rows, int64_t cols, const uint16_t* dz, int64_t ld
 // ---- activations ------------------------------------------------------------
 // Evaluated in fp32.  The tanh form of the GELU is z sigmoid(2u), which like the
 // SiLU needs one base-2 exponential (its factor folded into the polynomial) and one
-// reciprocal; the approximate forms of both (about 2^-22 relative) are far inside
-// the rounding of a bf16 result and of an fp32 one's tolerance.
+// reciprocal, in their approximate forms: about 2^-22 relative, and in the tails
+// |z| 2^-24, since the exponential's argument is rounded to 32 bits.  That is far inside
+// the rounding of a bf16 result; of an fp32 one it takes the last two bits,
+// and more in the tails.
+// The erf form's lower tail is 1 + erf in 32 bits, exact to 2^-24 of z itself.
 __device__ __forceinline__ float exp2_f(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

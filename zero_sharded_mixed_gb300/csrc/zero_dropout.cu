@@ -278,9 +278,10 @@ static int launch_dropout(DropoutParams& p, cudaStream_t s) {
     while (lanes / 2 >= p.col_blocks) lanes /= 2;
     if constexpr (kGrad)
         if (p.db) {
-            // narrower warps, and so more clusters, as long as all are resident at once and
-            // a thread has more than two rows (8192 x 1600: 8 lanes 14.4 us, 4 lanes 11.5;
-            // past one wave, 2048 x 4096 with a slope: 16 lanes 16.1, 8 lanes 19.4)
+            // narrower warps, and so more clusters, as long as three CTAs an SM hold them all
+            // and a thread has more than two rows (8192 x 1600: 8 lanes 14.4 us, 4 lanes 11.5;
+            // past one wave, 2048 x 4096 with a slope: 16 lanes 16.1, 8 lanes 19.4).  Clusters
+            // of 8 may fill an SM group less evenly than that counts.
             void (*kernel)(DropoutParams, int, int, int64_t) = p.x_f32 ? dropout_kernel<true, true, true> : dropout_kernel<true, false, true>;
             const int64_t resident = (int64_t)sm_count() * 3;
             const auto rows_of = [](int lanes) { return (int64_t)kShares * (kThreads / 32) * (32 / lanes); };   // of a cluster's pass

@@ -418,9 +418,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // even CTA issues the products, warps 4..19 end the previous tile out of the other
 // half of the tensor memory meanwhile.  Bound by the tensor core: 256 x 256 x 64 take 512
 // cycles, in which 64 KB come in, what an SM's share of L2 gives; a CTA alone would need
-// half as much again for the same products.  8192 x 8192 x 8192 in 555 us (1.98 PFLOP/s,
-// cuBLAS 2.01), where the clock falls to about 1.4 GHz; 8192 x 1600 times 6400 x 1600 with
-// the tanh GELU and its pre-activation 101 us (1.66 PFLOP/s), without either 88.
+// half as much again for the same products.  Launched from a graph, by how far
+// the power limit lets the clock fall: 8192 x 8192 x 8192 in 567 to 619 us (1.78 to 1.94
+// PFLOP/s; cuBLAS 545 to 604), 8192 x 1600 times 6400 x 1600 with the tanh GELU and its
+// pre-activation in 102 us (1.65 PFLOP/s), with a bias alone in 90; in a program that
+// makes other calls between, 119.
 struct PairParams {
     CUtensorMap map_a, map_b;
     int64_t rows, cols, depth;
@@ -441,8 +443,9 @@ constexpr int kPairSmem = 1024 + kPairStages * kStageBytes + kEndWarps * kUnitBy
 // fp32 results: the tensor core cuts its sums where an fp32 addition would round
 // them, and 100 additions in a row were off by 1.6e-6 of the result, five times a
 // plain fp32 sum's error.  Their accumulators are therefore read after at most kRun
-// blocks and added up in registers (0.75e-6).  A bf16 result's own rounding is a
-// thousand times larger.
+// blocks and added up in registers (0.75e-6; the split kernel adds them up in tensor
+// memory).  A bf16 result's sums run on: about 7e-8 of it a block, where its own
+// rounding is 1.7e-3.
 constexpr int kRun = 13;                // blocks of 64 reduced elements
 constexpr int kUnits = 3;               // 16 x 32 parts that a warp sums so, in 48 registers; a fourth would spill
 constexpr int kWidest = 256, kWidestRuns = kUnits * 4 * 16;
@@ -1531,8 +1534,9 @@ static int launch_product(const Product& p, Ending& e, cudaStream_t s) {
     const Plan deep = reach ? plan_deep(p, e.out_f32) : Plan{INT64_MAX, 0, 0, 0, 0};
     const int64_t whole = pair.cycles < split.cycles ? pair.cycles : split.cycles, tiled = deep.cycles < whole ? deep.cycles : whole;
     // The kernel of a few rows reads the weights at about 2950 bytes a cycle for one row
-    // (weights 4800 x 1600 4.9 us, 6.7 by tiles; 4096 x 11008 16.4 and 18.6; the one size
-    // found where tiles are faster is 11008 x 4096, 21 and 19) and half of it for more.
+    // (weights 4800 x 1600, in L2, 4.9 us, 6.7 by tiles; 4096 x 11008 16.4 and 18.6) and
+    // half of it for more.  One row always goes there: the one size found where tiles
+    // are faster, 11008 x 4096, 21 and 19, is not told apart by the estimates.
     if (p.rows <= kMostRows && !p.a.mn && !p.b.mn) {
         const int64_t read = p.cols * (p.depth / 8) * 16 / 2950;
         if (p.rows == 1 || 3000 + read * (p.rows == 2 ? 14 : 23) / 10 < tiled) return launch_rows(p, e, s);

@@ -80,8 +80,8 @@ __device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t m) { return m ? 
 // the half layout, neighbours in the interleaved one) or up to two of the vectors
 // that are copied; else a pair an item, or up to two copied elements.
 // Bound by memory: 8192 tokens x 64 heads of 128 bf16 inside a packed projection in
-// 45.9 us (5.9 TB/s), 6001 x 25 x 64 fp32 with half of each head turned in 14.6 us
-// (5.3 TB/s).  Sixteen items a thread, two bf16 ones (four fp32) in flight: 49 us with
+// 45.9 us (5.9 TB/s), 6001 x 25 x 64 fp32 with half of each head turned in 15.5 us
+// (5.0 TB/s).  Sixteen items a thread, two bf16 ones (four fp32) in flight: 49 us with
 // four of either.
 template <bool kF32, bool kHalf, bool kVec>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {

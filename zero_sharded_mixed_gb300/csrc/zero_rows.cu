@@ -8,7 +8,7 @@
 // there are few columns) the warps among which the reduced dimension was split, all
 // in a fixed order.  Bound by the weights' bytes (4096 x 11008, one row, weights not in
 // L2: 16.4 us, 5.5 TB/s; 11008 x 4096: 21, 4.3 TB/s) or, below some 20 MB, by the launch
-// and one memory latency: 4800 x 1600 in 4.9 us.  Each pair of columns starting at
+// and one memory latency: 4800 x 1600 in 6.5 us, 5.0 where the weights are still in L2.  Each pair of columns starting at
 // another place of its rows was slower (18 and 25 us).
 #include "zero_product.cuh"
 
