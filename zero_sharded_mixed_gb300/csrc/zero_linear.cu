@@ -41,28 +41,6 @@ __device__ __forceinline__ uint32_t group_place(int r, int g) { return (uint32_t
 // the four lanes of a row by a 4 x 4 transposition of words.  Shared memory is left
 // alone: the products and their copies use its whole bandwidth, and a transposition
 // through it took 5900 cycles a tile against the 12800 of a product of depth 1600.
-__device__ __forceinline__ void quad_transpose(uint32_t* w) {   // w[g] of lane j becomes w[j] of lane g
-    const int lane = threadIdx.x & 31;
-    const bool odd = lane & 1, high = lane & 2;
-#pragma unroll
-    for (int a = 0; a < 4; a += 2) {
-        const uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? w[a] : w[a + 1], 1);
-        w[a] = odd ? r : w[a];
-        w[a + 1] = odd ? w[a + 1] : r;
-    }
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-        const uint32_t r = __shfl_xor_sync(0xffffffffu, high ? w[a] : w[a + 2], 2);
-        w[a] = high ? r : w[a];
-        w[a + 2] = high ? w[a + 2] : r;
-    }
-}
-__device__ __forceinline__ void quad_transpose(uint4& u) {
-    uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    quad_transpose(w);
-    u = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // fp32: between the fragment's two columns of groups g and g + 1 (g even) and four
 // columns of one of them, group g in even lanes and g + 1 in odd ones, which start
 // pair_column() after the first of the 32 columns (plus 8 g).  Its own inverse.
@@ -398,18 +376,9 @@ __device__ __forceinline__ void end_joined(const Ending& e, uint32_t step, const
     }
 }
 
-// ---- waits -------------------------------------------------------------------------
-constexpr long long kWaitCycles = 1ll << 31;   // SM cycles (about a second) before a wait gives up
-
 __device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// For a converged warp that goes on as a whole: every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitCycles))) return true;
-    atomicExch(&g_linear_status, ZERO_ETIMEOUT);
-    return false;
-}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, &g_linear_status); }
 
 // ---- the pair kernel -----------------------------------------------------------------
 // Large aligned products: pairs of CTAs, each pair one 256 x bn tile at a time (its
@@ -1289,24 +1258,6 @@ __global__ void __launch_bounds__(kDeepThreads, 1) deep_kernel(const __grid_cons
 
 // ---- launches -----------------------------------------------------------------------------
 
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiled encode_tiled() {
-    static EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess) {
-            (void)cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // Whether tensor-map copies can read the operand: 16-byte aligned rows, and sizes
 // and row pitch within the map's fields.
 static bool copies_reach(const Operand& o) {
@@ -1324,33 +1275,6 @@ static bool make_map(const Operand& o, int box_rows, CUtensorMap* map) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The current device, if there is one below `most`.  A failed question leaves no error
-// behind: a caller goes on without the answer or reports it by its code.
-static bool device_below(int most, int* dev) {
-    const cudaError_t e = cudaGetDevice(dev);
-    if (e != cudaSuccess) {
-        note_cuda_error(e);
-        (void)cudaGetLastError();
-    }
-    return e == cudaSuccess && *dev >= 0 && *dev < most;
-}
-
-// Raises a kernel's shared-memory limit, once per device (again after a failure).
-typedef std::atomic<bool> Done[64];
-static int allow_smem(const void* kernel, int bytes, Done& done) {
-    int dev = 0;
-    if (!device_below(64, &dev)) return ZERO_ECUDA;
-    if (done[dev].load(std::memory_order_acquire)) return ZERO_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) {
-        note_cuda_error(e);
-        (void)cudaGetLastError();
-        return ZERO_ECUDA;
-    }
-    done[dev].store(true, std::memory_order_release);
-    return ZERO_OK;
-}
-
 // What a launch takes and its estimated cycles, from the measured times of each
 // kernel's phases on GB300; the least decides.  (Measured either way, in us, pair and
 // split kernel: 333 x 1600 x 1600 8.8 and 8.4; 1024 x 1600 x 1600 9.2 and 13; 64 tokens
@@ -1359,12 +1283,6 @@ struct Plan {
     int64_t cycles, tiles_m, tiles_n;
     int bn, parts;
 };
-
-// Pairs of SMs; one where the runtime could not say how many there are.
-static int64_t sm_pairs() {
-    const int n = sm_count();
-    return n < 2 ? 1 : n / 2;
-}
 
 // Waves of pairs, each a tile's blocks (bound by the tensor core, or for narrow tiles
 // by shared memory) and the part of its end that nothing hides.

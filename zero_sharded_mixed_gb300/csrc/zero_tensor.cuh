@@ -10,6 +10,9 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
+#include "zero_common.cuh"
 #include "zero_tma.cuh"
 
 namespace zgb {
@@ -213,5 +216,92 @@ __device__ __forceinline__ void tensor_map_prefetch(const CUtensorMap* map) {
 // Orders this thread's writes to shared memory before later reads by the tensor core.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_barrier_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+
+// ---- four lanes of a fragment's row ----------------------------------------------------
+__device__ __forceinline__ void quad_transpose(uint32_t* w) {   // w[g] of lane j becomes w[j] of lane g
+    const int lane = threadIdx.x & 31;
+    const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+    for (int a = 0; a < 4; a += 2) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? w[a] : w[a + 1], 1);
+        w[a] = odd ? r : w[a];
+        w[a + 1] = odd ? w[a + 1] : r;
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, high ? w[a] : w[a + 2], 2);
+        w[a] = high ? r : w[a];
+        w[a + 2] = high ? w[a + 2] : r;
+    }
+}
+__device__ __forceinline__ void quad_transpose(uint4& u) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    quad_transpose(w);
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---- waits -------------------------------------------------------------------------
+constexpr long long kWaitCycles = 1ll << 31;   // SM cycles (about a second) before a wait gives up
+
+// For a converged warp that goes on as a whole: every lane gets the same answer.  A
+// wait that gives up leaves ZERO_ETIMEOUT in *status, device memory.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitCycles))) return true;
+    atomicExch(status, ZERO_ETIMEOUT);
+    return false;
+}
+
+// ---- launches, host --------------------------------------------------------------------
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+    static EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// The current device, if there is one below `most`.  A failed question leaves no error
+// behind: a caller goes on without the answer or reports it by its code.
+inline bool device_below(int most, int* dev) {
+    const cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+    }
+    return e == cudaSuccess && *dev >= 0 && *dev < most;
+}
+
+// Raises a kernel's shared-memory limit, once per device (again after a failure).
+typedef std::atomic<bool> Done[64];
+inline int allow_smem(const void* kernel, int bytes, Done& done) {
+    int dev = 0;
+    if (!device_below(64, &dev)) return ZERO_ECUDA;
+    if (done[dev].load(std::memory_order_acquire)) return ZERO_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+        return ZERO_ECUDA;
+    }
+    done[dev].store(true, std::memory_order_release);
+    return ZERO_OK;
+}
+
+// Pairs of SMs; one where the runtime could not say how many there are.
+inline int64_t sm_pairs() {
+    const int n = sm_count();
+    return n < 2 ? 1 : n / 2;
+}
 
 }  // namespace zgb
