@@ -103,6 +103,17 @@ typedef struct {
     const float* sched;
 } zero_adamw_t;
 
+/* Hyper-parameters of one step by orthogonalised momentum (Muon). */
+typedef struct {
+    float lr;
+    float momentum;      /* mu, 0 <= mu < 1 */
+    float weight_decay;
+    float scale;         /* the update is lr * scale times the orthogonalised matrix */
+    int32_t nesterov;    /* 1: u = g + mu m, 0: u = m */
+    int32_t reserved;    /* zero */
+    const float* sched;  /* NULL, or a DEVICE pointer to lr (zero_adamw_t's sched serves), read in its place */
+} zero_muon_t;
+
 /* One place and pass of dropout: which elements are dropped is a function of
  * (seed, site, step, row, column) alone. */
 typedef struct {
@@ -585,10 +596,93 @@ int zero_rope(const zero_rope_plan_t* plan, int64_t tokens, int64_t heads, int64
               int64_t x_token, int64_t x_head, void* y, int64_t y_token, int64_t y_head, int32_t dtype,
               const int64_t* positions, int64_t pos0, int32_t inverse, void* stream);
 
+/* Layer norm over the columns (Ba, Kiros and Hinton, 2016), with the residual's
+ * addition before it, and its gradient.
+ * zero_layer_norm:  h = x + residual, rounded to dtype and kept in sum, or h = x where
+ *   residual and sum are NULL (both or neither);
+ *   y = (h - mean) rstd gamma + beta, mean and 1 / sqrt(variance + eps) over a row.
+ *   x, residual and sum are dtype, y is dtype or bf16, gamma and beta (or NULL: 1, 0)
+ *   bf16 [cols], mean and rstd (or NULL) fp32 [rows].  sum may be x or residual itself
+ *   (same ld); outputs overlap no other argument.
+ * zero_layer_norm_grad: with xhat = (x - mean) rstd and g = dy gamma,
+ *   dx = residual + rstd (g - avg(g) - xhat avg(g xhat)), averages over a row;
+ *   dgamma = dgamma_acc + sum over rows of dy xhat,  dbeta = dbeta_acc + sum of dy.
+ *   x is what was normalised (the forward call's sum, where it had a residual), mean and
+ *   rstd what it kept; x, residual (or NULL) and dx are dtype, dy is dtype or bf16, the
+ *   weights' gradients and accumulators (each or all NULL) weight_dtype.  dx may be
+ *   residual itself (same ld), dgamma dgamma_acc, dbeta dbeta_acc.
+ *   workspace: device, 16-byte aligned, of zero_layer_norm_grad_workspace bytes for these
+ *   sizes on the current device; needed where dgamma or dbeta is asked for.  Calls that
+ *   share one must not overlap on the GPU.
+ * Sums are fp32 in an order that sizes and device fix: results repeat.  No columns: the
+ * calls do nothing; no rows: the weights' gradients are their accumulators, or 0.
+ * Errors: ZERO_EINVAL (negative size, ld below the columns, types, eps negative or not
+ *   finite, a null or non-device pointer, residual without sum), ZERO_ERANGE (more than
+ *   2^30 - 1 columns, a byte count past 63 bits, workspace too small), ZERO_EALIGN, ZERO_ECUDA. */
+int zero_layer_norm(int64_t rows, int64_t cols, const void* x, int64_t ldx, int32_t dtype, const void* residual,
+                    int64_t ldr, void* sum, int64_t lds, const uint16_t* gamma, const uint16_t* beta, float eps,
+                    void* y, int32_t y_dtype, int64_t ldy, float* mean, float* rstd, void* stream);
+int zero_layer_norm_grad_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, int64_t lddy, int32_t dy_dtype, const void* x,
+                         int64_t ldx, const float* mean, const float* rstd, const uint16_t* gamma,
+                         const void* residual, int64_t ldr, void* dx, int32_t dtype, int64_t lddx,
+                         const void* dgamma_acc, void* dgamma, const void* dbeta_acc, void* dbeta,
+                         int32_t weight_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---- a step by orthogonalised momentum ---------------------------------------
+ * The Muon optimizer (Jordan et al., 2024) for the matrices of a unit under ZeRO, in
+ * three calls: the ranks' gradients reduced into the owners' momentum, the gathered
+ * momentum orthogonalised matrix by matrix, the owners' weights moved by the result.
+ * The pages step with AdamW alone; these calls are an addition.
+ *
+ * zero_reduce_scatter_momentum: for every flat i in [begin, end), owners as in
+ *   zero_reduce_scatter_adamw,
+ *     g = (sum over r of src[r][i - src_base]) / divisor
+ *     m = mu*m + g;   u = nesterov ? g + mu*m : m
+ *   every operation one IEEE fp32 rounding, ranks ascending from +0.0f.  m (fp32) stands
+ *   at [i - rank_begin*S]; u (bf16, rounded to nearest even) at [i] for ZERO_OUT_FULL --
+ *   the gather -- or [i - rank_begin*S] for ZERO_OUT_SHARD.  Sources as for
+ *   zero_reduce_scatter_adamw, pinned host memory among them.
+ * zero_muon_update: w = w - (lr*weight_decay)*w;  w = w - (lr*scale)*update[i - update_base];
+ *   out = bf16 of w, master at [i - rank_begin*S] and out by out_mode as there.
+ *   0 <= src_base, update_base <= begin.
+ * zero_orthogonalize: for each of batch matrices U [rows, cols],
+ *     X = U / (|U| + eps), |U| the Frobenius norm;
+ *     steps times:  A = X X^T,  X = a X + (b A + c A A) X,  {a, b, c} = coefficients;
+ *     y = X in bf16
+ *   (the Gram matrix of the shorter side).  With (3.4445, -4.7750, 2.0315) and 5 steps the
+ *   singular values of U come to within about 0.3 of 1 and its singular vectors stay.
+ *   x is x_dtype, matrices x_stride elements apart (any stride >= 0), y bf16, y_stride
+ *   apart and not overlapping; rows ldx and ldy apart.  y may be x itself.  Any
+ *   element-aligned place.  A matrix of zeros gives zeros; one that is not finite NaN.
+ *   The products take fp16 operands with fp32 sums, on two fp16 numbers for each element
+ *   of X: with steps and coefficients like these the result is about 1e-3 off the exact
+ *   one by norm (4e-3 at most, small matrices of a few strong directions), beside its
+ *   rounding to bf16.  Singular values have to stay below 2 from
+ *   step to step (coefficients that let them grow run into fp16's range, and NaN).
+ *   workspace: device, 128-byte aligned, of zero_orthogonalize_workspace bytes; its
+ *   contents on entry do not matter.  Calls that share one must not overlap on the GPU.
+ *   Results repeat.
+ * Errors: ZERO_EINVAL (as zero_reduce_scatter_adamw; momentum outside [0, 1), nesterov
+ *   not 0 or 1, a value that is not finite; steps outside 1..100, eps negative, null
+ *   coefficients, results that overlap), ZERO_ERANGE (n_src > ZERO_MAX_SRC; a shorter side above
+ *   32768, 2^33 elements a matrix, 65535 matrices, workspace too small), ZERO_EALIGN, ZERO_ECUDA. */
+int zero_reduce_scatter_momentum(const zero_layout_t* L, const void* const* src, int32_t n_src, int32_t src_dtype,
+                                 int64_t src_base, float divisor, int32_t rank_begin, int32_t rank_end,
+                                 int64_t begin, int64_t end, float* m, uint16_t* u, int32_t out_mode,
+                                 const zero_muon_t* hp, void* stream);
+int zero_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, int64_t* bytes);
+int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void* x, int64_t x_stride, int64_t ldx,
+                       int32_t x_dtype, uint16_t* y, int64_t y_stride, int64_t ldy, int32_t steps,
+                       const float* coefficients, float eps, void* workspace, int64_t workspace_bytes, void* stream);
+int zero_muon_update(const zero_layout_t* L, const uint16_t* update, int64_t update_base, int32_t rank_begin,
+                     int32_t rank_end, int64_t begin, int64_t end, float* master, uint16_t* out, int32_t out_mode,
+                     const zero_muon_t* hp, void* stream);
+
 /* ---- status ---------------------------------------------------------------
  * Synchronizes `stream` and returns ZERO_ECUDA if it (or an earlier launch on
  * this thread) failed; ZERO_ETIMEOUT if a bounded device-side wait (the
- * mbarrier waits of the TMA-staged update and of the linear calls) gave up since the last check -- the
+ * mbarrier waits of the TMA-staged update, of the linear calls and of zero_orthogonalize) gave up since the last check -- the
  * kernel that gave up recorded it, drained its own copies and returned, so
  * the context stays usable; the record is cleared by this call.  ZERO_ERANGE
  * if a zero_schedule_advance found its index past the table since the last

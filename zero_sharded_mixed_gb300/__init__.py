@@ -27,6 +27,8 @@ _BINDING_NAMES = {
     "ZERO_ACT_NONE", "ZERO_ACT_RELU", "ZERO_ACT_GELU", "ZERO_ACT_GELU_TANH", "ZERO_ACT_SILU",
     "ZERO_ROPE_HALF", "ZERO_ROPE_INTERLEAVED", "ZERO_ROPE_NONE", "ZERO_ROPE_LINEAR", "ZERO_ROPE_NTK",
     "ZERO_ROPE_YARN", "ZERO_ROPE_MAX",
+    "ZeroMuon", "zero_layer_norm", "zero_layer_norm_grad", "zero_layer_norm_grad_workspace",
+    "zero_reduce_scatter_momentum", "zero_muon_update", "zero_orthogonalize", "zero_orthogonalize_workspace",
 }
 
 

@@ -77,6 +77,23 @@ class ZeroAdamW(ctypes.Structure):
         return hp
 
 
+class ZeroMuon(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float), ("nesterov", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("sched", ctypes.c_void_p)]
+
+    @classmethod
+    def make(cls, lr=0.02, momentum=0.95, weight_decay=0.0, scale=1.0, nesterov=True, sched=None):
+        """scale: what the orthogonalised matrix is multiplied with beside lr (for one
+        of n rows and k columns 0.2 sqrt(max(n, k)) gives updates of AdamW's size).
+        sched: None, or a CUDA float32 tensor whose first element the update reads in
+        place of lr (a StepSchedule's sched); the block keeps a reference to it."""
+        ptr = None if sched is None else _tensor(sched, "sched", torch.float32, 1)
+        hp = cls(lr, momentum, weight_decay, scale, int(bool(nesterov)), 0, ptr)
+        hp._sched_tensor = sched
+        return hp
+
+
 class ZeroDropout(ctypes.Structure):
     _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("site", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32), ("step", ctypes.c_uint64),
@@ -178,6 +195,17 @@ def load():
                                        P(ZeroRopePlan)]
         lib.zero_rope.argtypes = [P(ZeroRopePlan), i64, i64, i64, p, i64, i64, p, i64, i64, i32, p, i64,
                                   i32, p]
+        lib.zero_layer_norm.argtypes = [i64, i64, p, i64, i32, p, i64, p, i64, p, p, f32, p, i32, i64, p, p, p]
+        lib.zero_layer_norm_grad_workspace.argtypes = [i64, i64, P(i64)]
+        lib.zero_layer_norm_grad.argtypes = [i64, i64, p, i64, i32, p, i64, p, p, p, p, i64, p, i32, i64,
+                                             p, p, p, p, i32, p, i64, p]
+        M = P(ZeroMuon)
+        lib.zero_reduce_scatter_momentum.argtypes = [P(ZeroLayout), P(p), i32, i32, i64, f32, i32, i32, i64, i64,
+                                                     p, p, i32, M, p]
+        lib.zero_muon_update.argtypes = [P(ZeroLayout), p, i64, i32, i32, i64, i64, p, p, i32, M, p]
+        lib.zero_orthogonalize_workspace.argtypes = [i64, i64, i64, P(i64)]
+        lib.zero_orthogonalize.argtypes = [i64, i64, i64, p, i64, i64, i32, p, i64, i64, i32, P(f32), f32,
+                                           p, i64, p]
         lib.zero_status_check.argtypes = [p]
         lib.zero_strerror.argtypes = [ctypes.c_int]
         lib.zero_strerror.restype = ctypes.c_char_p
@@ -201,7 +229,9 @@ def load():
                      "zero_status_check", "zero_memory_bytes", "zero_comm_bytes",
                      "zero_lr_warmup_decay", "zero_linear", "zero_linear_grad_input",
                      "zero_linear_grad_weight", "zero_dropout", "zero_dropout_grad",
-                     "zero_rope_fill", "zero_rope"):
+                     "zero_rope_fill", "zero_rope", "zero_layer_norm", "zero_layer_norm_grad_workspace",
+                     "zero_layer_norm_grad", "zero_reduce_scatter_momentum", "zero_muon_update",
+                     "zero_orthogonalize_workspace", "zero_orthogonalize"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -793,3 +823,171 @@ def zero_rope(plan: ZeroRopePlan, x, y, positions=None, pos0: int = 0, inverse: 
     _check(load().zero_rope(plan, tokens, heads, dim, xp, xt, xh, yp, yt, yh, _DT_CODE[x.dtype],
                             None if positions is None else _tensor(positions, "positions", torch.int64, tokens),
                             pos0, bool(inverse), _stream_ptr(stream)), "zero_rope")
+
+
+def _workspace(t, need: int):
+    """Pointer and bytes of a workspace; None where none is given."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    size = t.numel() * t.element_size()
+    if size < need:
+        raise ValueError(f"workspace has {size} bytes, the call needs {need}")
+    return t.data_ptr(), size
+
+
+def zero_layer_norm(x, y, gamma=None, beta=None, eps: float = 1e-5, residual=None, sum=None, mean=None,
+                    rstd=None, stream=None):
+    """sum = x + residual (both or neither given) and y = (sum - mean) rstd gamma + beta
+    over the rows of a matrix; mean and rstd (fp32, one a row), if given, receive the
+    statistics for the gradient.  x, residual and sum are bf16 or fp32 alike, y the same
+    or bf16, gamma and beta bf16."""
+    rows, cols = _sizes(x, "x")
+    xp, ldx, code = _matrix(x, "x", rows, cols, _DT_CODE)
+    yp, ldy, ycode = _matrix(y, "y", rows, cols, _DT_CODE)
+    if ycode not in (code, ZERO_BF16):
+        raise TypeError(f"y must be bfloat16 or have the type of x, got {y.dtype}")
+    _same_type("residual", code, residual, "x")
+    _same_type("sum", code, sum, "x")
+    if (residual is None) != (sum is None):
+        raise ValueError("residual and sum are given together")
+    rp, ldr, _ = _matrix(residual, "residual", rows, cols, _DT_CODE)
+    sp, lds, _ = _matrix(sum, "sum", rows, cols, _DT_CODE)
+    _check(load().zero_layer_norm(rows, cols, xp, ldx, code, rp, ldr, sp, lds, _vector(gamma, "gamma", cols, ZERO_BF16),
+                                  _vector(beta, "beta", cols, ZERO_BF16), eps, yp, ycode, ldy,
+                                  _vector(mean, "mean", rows, ZERO_F32), _vector(rstd, "rstd", rows, ZERO_F32),
+                                  _stream_ptr(stream)), "zero_layer_norm")
+
+
+def zero_layer_norm_grad_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace zero_layer_norm_grad needs for dgamma or dbeta on the current device."""
+    out = ctypes.c_int64()
+    _check(load().zero_layer_norm_grad_workspace(rows, cols, ctypes.byref(out)), "zero_layer_norm_grad_workspace")
+    return out.value
+
+
+def zero_layer_norm_grad(dy, x, mean, rstd, dx, gamma=None, residual=None, dgamma=None, dbeta=None,
+                         dgamma_acc=None, dbeta_acc=None, workspace=None, stream=None):
+    """dx = residual + the gradient of zero_layer_norm by its input x (the sum, where it
+    had a residual), dgamma = dgamma_acc + and dbeta = dbeta_acc + those by its weights.
+    x, residual and dx are bf16 or fp32 alike, dy the same or bf16; dgamma, dbeta and
+    what they are added to (which may be themselves) have one type.  workspace: a CUDA
+    tensor of zero_layer_norm_grad_workspace(rows, cols) bytes, where dgamma or dbeta is given."""
+    rows, cols = _sizes(x, "x")
+    xp, ldx, code = _matrix(x, "x", rows, cols, _DT_CODE)
+    dp, lddy, dcode = _matrix(dy, "dy", rows, cols, _DT_CODE)
+    if dcode not in (code, ZERO_BF16):
+        raise TypeError(f"dy must be bfloat16 or have the type of x, got {dy.dtype}")
+    _same_type("residual", code, residual, "x")
+    _same_type("dx", code, dx, "x")
+    gp, lddx, _ = _matrix(dx, "dx", rows, cols, _DT_CODE)
+    rp, ldr, _ = _matrix(residual, "residual", rows, cols, _DT_CODE)
+    first = dgamma if dgamma is not None else dbeta
+    wcode, wsp, ws = ZERO_BF16, None, 0
+    if first is not None:
+        wcode = _DT_CODE.get(getattr(first, "dtype", None), -1)
+        if wcode < 0:
+            raise TypeError("dgamma and dbeta must be bfloat16 or float32 tensors")
+        need = zero_layer_norm_grad_workspace(rows, cols)
+        if need and workspace is None:
+            raise ValueError("dgamma and dbeta need a workspace")
+        wsp, ws = _workspace(workspace, need)
+    _check(load().zero_layer_norm_grad(rows, cols, dp, lddy, dcode, xp, ldx, _vector(mean, "mean", rows, ZERO_F32),
+                                       _vector(rstd, "rstd", rows, ZERO_F32), _vector(gamma, "gamma", cols, ZERO_BF16),
+                                       rp, ldr, gp, code, lddx, _vector(dgamma_acc, "dgamma_acc", cols, wcode),
+                                       _vector(dgamma, "dgamma", cols, wcode), _vector(dbeta_acc, "dbeta_acc", cols, wcode),
+                                       _vector(dbeta, "dbeta", cols, wcode), wcode, wsp, ws, _stream_ptr(stream)),
+           "zero_layer_norm_grad")
+
+
+# --------------------------------------------------------------------------
+# a step by orthogonalised momentum
+# --------------------------------------------------------------------------
+
+def zero_reduce_scatter_momentum(L: ZeroLayout, srcs, src_dtype: int, src_base: int, divisor: float,
+                                 rank_begin: int, rank_end: int, begin: int, end: int, m: torch.Tensor,
+                                 u: torch.Tensor, out_mode: int, hp: ZeroMuon, stream=None):
+    """Mean reduce-scatter into the momentum m (fp32) over [begin, end), and the bf16
+    matrices u to orthogonalise, gathered (ZERO_OUT_FULL) or left with their owners."""
+    if end <= begin:
+        src_need = state_need = out_need = 0
+    else:
+        src_need = end - src_base
+        state_need = end - rank_begin * L.shard
+        out_need = end if out_mode == ZERO_OUT_FULL else state_need
+    arr, n = _src_array(srcs, _SRC_DT.get(src_dtype, None), src_need, pinned_ok=True)
+    rc = load().zero_reduce_scatter_momentum(
+        ctypes.byref(L), arr, n, int(src_dtype), int(src_base), float(divisor), int(rank_begin), int(rank_end),
+        int(begin), int(end), _tensor(m, "m", torch.float32, state_need), _tensor(u, "u", torch.bfloat16, out_need),
+        int(out_mode), ctypes.byref(hp), _stream_ptr(stream))
+    _check(rc, "zero_reduce_scatter_momentum")
+
+
+def zero_muon_update(L: ZeroLayout, update: torch.Tensor, update_base: int, rank_begin: int, rank_end: int,
+                     begin: int, end: int, master: torch.Tensor, out: torch.Tensor, out_mode: int, hp: ZeroMuon,
+                     stream=None):
+    """w = w - lr weight_decay w - lr scale update over [begin, end) of the owners'
+    master weights, and the bf16 cast with its gather write."""
+    if end <= begin:
+        up_need = state_need = out_need = 0
+    else:
+        up_need = end - update_base
+        state_need = end - rank_begin * L.shard
+        out_need = end if out_mode == ZERO_OUT_FULL else state_need
+    rc = load().zero_muon_update(
+        ctypes.byref(L), _tensor(update, "update", torch.bfloat16, up_need), int(update_base), int(rank_begin),
+        int(rank_end), int(begin), int(end), _tensor(master, "master", torch.float32, state_need),
+        _tensor(out, "out", torch.bfloat16, out_need), int(out_mode), ctypes.byref(hp), _stream_ptr(stream))
+    _check(rc, "zero_muon_update")
+
+
+def zero_orthogonalize_workspace(batch: int, rows: int, cols: int) -> int:
+    """Bytes of workspace zero_orthogonalize needs."""
+    out = ctypes.c_int64()
+    _check(load().zero_orthogonalize_workspace(batch, rows, cols, ctypes.byref(out)), "zero_orthogonalize_workspace")
+    return out.value
+
+
+def _matrices(t, name, dtypes):
+    """Batch, rows, columns, pointer, matrix and row stride and type code of a matrix or
+    a batch of them whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a matrix or a batch of them")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device}); there is no CPU path")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
+    if t.dim() == 2:
+        t = t.unsqueeze(0)
+    b, rows, cols = t.shape
+    sb, ld, inner = t.stride()
+    if rows <= 1 or cols == 0:
+        ld = cols
+    if (inner != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have rows of contiguous elements (strides {t.stride()})")
+    return b, rows, cols, t.data_ptr(), (sb if b > 1 else 0), ld, dtypes[t.dtype]
+
+
+_NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def zero_orthogonalize(x, y, steps: int = 5, coefficients=_NEWTON_SCHULZ, eps: float = 1e-7, workspace=None,
+                       stream=None):
+    """y (bf16) = the orthogonalised matrix, or batch of matrices, x (bf16 or fp32) by
+    `steps` of the Newton-Schulz iteration with the quintic's coefficients; y may be x.
+    workspace: a CUDA tensor of zero_orthogonalize_workspace(batch, rows, cols) bytes."""
+    b, rows, cols, xp, xs, ldx, code = _matrices(x, "x", _DT_CODE)
+    yb, yrows, ycols, yp, ys, ldy, _ = _matrices(y, "y", _BF16_ONLY)
+    if (yb, yrows, ycols) != (b, rows, cols):
+        raise ValueError(f"y must have the shape of x, {(b, rows, cols)}, got {(yb, yrows, ycols)}")
+    coefficients = tuple(coefficients)
+    if len(coefficients) != 3:
+        raise ValueError("coefficients are three: of X, A X and A A X")
+    need = zero_orthogonalize_workspace(b, rows, cols)
+    if need and workspace is None:
+        raise ValueError("zero_orthogonalize needs a workspace")
+    wsp, ws = _workspace(workspace, need)
+    _check(load().zero_orthogonalize(b, rows, cols, xp, xs, ldx, code, yp, ys, ldy, steps,
+                                     (ctypes.c_float * 3)(*coefficients), eps, wsp, ws, _stream_ptr(stream)),
+           "zero_orthogonalize")

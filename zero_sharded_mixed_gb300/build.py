@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libzero_gb300.so")
 CUDA_SOURCES = ["zero_runtime.cu", "zero_rs_adamw.cu", "zero_accumulate.cu", "zero_gather.cu",
                 "zero_norm.cu", "zero_quant.cu", "zero_rs_adamw_tma.cu", "zero_qgrad.cu",
                 "zero_schedule.cu", "zero_cast.cu", "zero_linear.cu", "zero_rows.cu", "zero_dropout.cu",
-                "zero_rope.cu"]
+                "zero_rope.cu", "zero_layer_norm.cu", "zero_muon.cu", "zero_orthogonal.cu"]
 HOST_SOURCES = ["zero_host.cpp", "zero_ckpt.cpp"]
 HEADERS = ["zero_common.cuh", "zero_update.cuh", "zero_quant.cuh", "zero_tma.cuh", "zero_dense.cuh",
            "zero_tensor.cuh", "zero_product.cuh"]

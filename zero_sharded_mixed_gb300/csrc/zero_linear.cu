@@ -41,6 +41,7 @@ __device__ __forceinline__ uint32_t group_place(int r, int g) { return (uint32_t
 // the four lanes of a row by a 4 x 4 transposition of words.  Shared memory is left
 // alone: the products and their copies use its whole bandwidth, and a transposition
 // through it took 5900 cycles a tile against the 12800 of a product of depth 1600.
+//
 // fp32: between the fragment's two columns of groups g and g + 1 (g even) and four
 // columns of one of them, group g in even lanes and g + 1 in odd ones, which start
 // pair_column() after the first of the 32 columns (plus 8 g).  Its own inverse.

@@ -191,7 +191,7 @@ extern "C" int zero_reduce_scatter_momentum(const zero_layout_t* L, const void* 
         if (check_aligned(src[r], size)) return ZERO_EALIGN;
     if (begin == end) return ZERO_OK;
     for (int r = 0; r < n_src; ++r)
-        if (check_device_ptr(src[r])) return ZERO_EINVAL;
+        if (check_source_ptr(src[r])) return ZERO_EINVAL;
     if (const int rc = check_target_ptrs(t)) return rc;
     p.m = t.w;
     p.u = t.out;

@@ -1,0 +1,699 @@
+// Orthogonalised matrices by a quintic Newton-Schulz iteration, sm_103a:
+//   X = U / (|U| + eps);  S times:  A = X X^T,  B = b A + c A A,  X = a X + B X
+// on the shorter side (A = X^T X and X = a X + X B for a matrix taller than wide), for a
+// batch of equal matrices.  The singular values of U go to the neighbourhood of 1, its
+// singular vectors stay: what the Muon optimizer (Jordan et al., 2024) makes of a momentum.
+//
+// Numbers.  All products run on the tensor core with fp16 operands and fp32 sums: fp16
+// has 11 bits where bf16 has 8, at the same rate, and every range here is known: |X| <= 1
+// at first and near 1 later, |A| and |B| below 15.  X is stored times 2^12, A and B times
+// 2^10, so that even entries of 2^-26 are not subnormal.  An fp16 X alone would lose what
+// lies below 2^-11 of its largest directions, which the iteration raises (3.4 times a
+// step): a momentum of low rank with a faint rest came out 2 % off, 16 % in bf16.  So X is
+// held as the sum of two fp16 numbers, `hi` and `lo` (22 bits), of which the products take
+// `hi`, and what they do to `lo` is put in by B's diagonal, its largest part:
+//   X' = (a + B_ii - fp16(B_ii)) hi + (a + B_ii) lo + fp16(B) hi
+// the first factor also taking back the rounding of the diagonal.  Against 64 bits:
+// 0.3e-3 to 1e-3 of the result by norm (2.5e-3 for 40 x 100 with two directions a
+// thousand times above the rest), before the 1.7e-3 of its own rounding to bf16.
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "zero_dense.cuh"
+#include "zero_tensor.cuh"
+
+namespace zgb {
+
+__device__ int g_orthogonal_status;   // ZERO_OK, or ZERO_ETIMEOUT once a bounded wait gave up
+
+int take_orthogonal_status() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_orthogonal_status, sizeof v) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ZERO_ECUDA;
+    }
+    if (v != ZERO_OK) {
+        const int zero = ZERO_OK;
+        if (cudaMemcpyToSymbol(g_orthogonal_status, &zero, sizeof zero) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return ZERO_ECUDA;
+        }
+    }
+    return v == ZERO_OK ? ZERO_OK : ZERO_ETIMEOUT;
+}
+
+constexpr float kX = 4096.0f, kA = 1024.0f, kLo = 2048.0f;   // powers of two that X, A and B, and lo beside hi, are stored times
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+__device__ __forceinline__ float round_f16(float x) { return __half2float(__float2half_rn(x)); }
+
+// ---- the input: its norm, and the two fp16 parts of the scaled matrix ---------------------
+struct SourceParams {
+    const void* x; int64_t ldx, stride;
+    int32_t rows, cols, groups;        // groups of eight columns a row
+    int32_t parts;
+    bool f32, vec;
+    double* norm;                      // [batch][parts]
+    float* scale;                      // [batch]: X = scale * hi
+    uint16_t* hi;
+    uint16_t* lo;                      // null: hi is exact
+    int64_t ld, to;                    // of hi and lo: row and matrix stride
+    float eps;
+};
+constexpr int kSourceThreads = 256;
+
+__device__ __forceinline__ void source8(const SourceParams& p, int64_t at, int n, float (&v)[8]) {
+    if (p.vec) {
+        uint4 u[2];
+        if (p.f32) {
+            u[0] = ld_live_u4(static_cast<const float*>(p.x) + at);
+            u[1] = ld_live_u4(static_cast<const float*>(p.x) + at + 4);
+            raw8<true>(u, v);
+        } else {
+            u[0] = ld_live_u4(static_cast<const uint16_t*>(p.x) + at);
+            raw8<false>(u, v);
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = k >= n ? 0.0f : p.f32 ? static_cast<const float*>(p.x)[at + k] : bf16_one(static_cast<const uint16_t*>(p.x)[at + k]);
+}
+
+// The sum over the CTA in a fixed order, to every thread.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double part[kSourceThreads / 32];
+    for (int o = 16; o; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int w = 0; w < kSourceThreads / 32; ++w) v += part[w];
+    return v;
+}
+
+// Squares are summed in fp32 by a thread where none can leave fp32's range, else in
+// fp64, and in fp64 over the threads.
+__global__ void __launch_bounds__(kSourceThreads) orthogonal_norm_kernel(const SourceParams p) {
+    await_predecessor();
+    const int64_t from = (int64_t)blockIdx.y * p.stride;
+    float sum = 0.0f;
+    double far = 0.0;
+    const uint32_t all = (uint32_t)p.rows * (uint32_t)p.groups;
+    for (uint32_t g = blockIdx.x * kSourceThreads + threadIdx.x; g < all; g += gridDim.x * kSourceThreads) {
+        const uint32_t row = g / (uint32_t)p.groups, c = (g - row * (uint32_t)p.groups) * 8;
+        float v[8], most = 0.0f, s = 0.0f;
+        source8(p, from + (int64_t)row * p.ldx + c, p.cols - (int)c, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            most = fmaxf(most, fabsf(v[k]));
+            s += v[k] * v[k];
+        }
+        if ((most > 1e-12f && most < 1e16f && s == s) || (most == 0.0f && s == 0.0f)) {
+            sum += s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) far += (double)v[k] * (double)v[k];
+        }
+    }
+    const double t = block_sum((double)sum + far);
+    if (threadIdx.x == 0) p.norm[(int64_t)blockIdx.y * p.parts + blockIdx.x] = t;
+}
+
+// hi + lo / 2^11 = x 2^(12 - e) with e the norm's exponent, and scale = 2^e / norm: the
+// power of two costs a bf16 x no bit, and the first step's products take in the scale.
+__global__ void __launch_bounds__(kSourceThreads) orthogonal_source_kernel(const SourceParams p) {
+    await_predecessor();
+    double t = 0.0;
+    for (int i = threadIdx.x; i < p.parts; i += kSourceThreads) t += p.norm[(int64_t)blockIdx.y * p.parts + i];
+    const double norm = sqrt(block_sum(t)) + (double)p.eps;
+    int e = 0;
+    const double f = norm > 0.0 && norm < INFINITY ? frexp(norm, &e) : norm;
+    if (blockIdx.x == 0 && threadIdx.x == 0)   // of zeros, zeros; of what is not finite, NaN
+        p.scale[blockIdx.y] = norm == 0.0 ? 0.0f : norm < INFINITY ? (float)(1.0 / f) : NAN;
+    const int k = 12 - e;
+    const float f1 = ldexpf(1.0f, k / 2), f2 = ldexpf(1.0f, k - k / 2);
+    const int64_t from = (int64_t)blockIdx.y * p.stride, to = (int64_t)blockIdx.y * p.to;
+    const uint32_t all = (uint32_t)p.rows * (uint32_t)p.groups;
+    for (uint32_t g = blockIdx.x * kSourceThreads + threadIdx.x; g < all; g += gridDim.x * kSourceThreads) {
+        const uint32_t row = g / (uint32_t)p.groups, c = (g - row * (uint32_t)p.groups) * 8;
+        float v[8], r[8];
+        source8(p, from + (int64_t)row * p.ldx + c, p.cols - (int)c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = v[j] * f1 * f2;
+            r[j] = (v[j] - round_f16(v[j])) * kLo;
+        }
+        const int64_t at = to + (int64_t)row * p.ld + c;
+        *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+        if (p.lo)
+            *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
+    }
+}
+
+// ---- products --------------------------------------------------------------------------------
+// Pairs of CTAs on 256 x bn tiles, as for the large dense products: warp 0 copies, warp 1
+// of the even CTA issues, warps 4..19 end the last tile meanwhile.  A symmetric result is
+// computed for the tiles that reach below its diagonal and written to both sides.
+enum Step { kGram, kSquare, kApply };
+
+struct StepParams {
+    CUtensorMap map_a, map_b;
+    int32_t rows, cols, depth;             // of the result, and the reduced dimension
+    int32_t tiles_n, tiles, all;           // column tiles; tiles a matrix, and of the batch
+    int32_t bn, k_blocks;
+    bool a_mn, b_mn;
+    bool first, tall;                      // first: X = scale * hi
+    // what the end reads and writes: ld and stride a matrix, of all of them
+    int64_t ld, stride;
+    const uint16_t* c_hi;                  // kSquare: A; kApply: X
+    const uint16_t* c_lo;                  // or null
+    uint16_t* d_hi;                        // A, B or the next X
+    uint16_t* d_lo;
+    uint16_t* y; int64_t ldy, y_stride;    // kApply, last: bf16 in place of d
+    bool y_vec;
+    float2* factors; int64_t factor_stride;   // a + B_ii - fp16(B_ii), a + B_ii
+    const float* scale;
+    float a, b, c;
+};
+
+constexpr int kStageBytes = 32768;      // 128 rows of A and 128 of B, 64 reduced elements each
+constexpr int kStages = 6;
+constexpr int kEndWarps = 16;
+constexpr int kStepThreads = 128 + 32 * kEndWarps;
+constexpr int kStepSmem = 1024 + kStages * kStageBytes + 256;
+
+struct Place {
+    int z, tm, tn;
+};
+template <Step kStep>
+__device__ __forceinline__ Place place_of(const StepParams& p, int t) {
+    Place w;
+    w.z = t / p.tiles;
+    t -= w.z * p.tiles;
+    if (kStep == kApply) {
+        w.tm = t / p.tiles_n;
+        w.tn = t - w.tm * p.tiles_n;
+    } else {   // row tile i has the column tiles up to its own columns' end
+        const int step = 256 / p.bn;
+        int n = step < p.tiles_n ? step : p.tiles_n;
+        for (w.tm = 0; t >= n; ++w.tm) {
+            t -= n;
+            n = n + step < p.tiles_n ? n + step : p.tiles_n;
+        }
+        w.tn = t;
+    }
+    return w;
+}
+__device__ __forceinline__ int width_of(const StepParams& p, int tn) {   // columns of the tile, up to a multiple of 32
+    const int left = p.cols - tn * p.bn;
+    return left >= p.bn ? p.bn : (left + 31) / 32 * 32;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// 16 rows x 32 columns of the result from row0, col0, a warp together: lane 4 i + j has
+// columns 8 g + 2 j, + 1 of rows i (v[g][0..1]) and i + 8 (v[g][2..3]).  What moves in
+// 16-byte vectors, a lane a group of eight, is exchanged between the four lanes of a row.
+// Matrices of the workspace have rows of whole units, so that only rows are checked.
+template <Step kStep>
+struct StepEnd {
+    uint4 hi[2], lo[2];
+    float2 f[2];
+    float s;
+    __device__ __forceinline__ void load(const StepParams& p, const Place& w, int row0, int col0) {
+        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
+        s = p.first ? p.scale[w.z] : 1.0f;
+        if constexpr (kStep != kGram) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = row0 + i + 8 * h;
+                const int64_t at = w.z * p.stride + row * p.ld + col0 + 8 * j;
+                hi[h] = lo[h] = make_uint4(0u, 0u, 0u, 0u);
+                if (row < p.rows) {
+                    hi[h] = *reinterpret_cast<const uint4*>(p.c_hi + at);
+                    if (kStep == kApply && p.c_lo) lo[h] = *reinterpret_cast<const uint4*>(p.c_lo + at);
+                    if (kStep == kApply && !p.tall) f[h] = p.factors[w.z * p.factor_stride + row];
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ static void store(uint16_t* q, int64_t ld, int rows_left, uint32_t (&a)[4], uint32_t (&b)[4]) {
+        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
+        quad_transpose(a);
+        quad_transpose(b);
+        if (i < rows_left) *reinterpret_cast<uint4*>(q + i * ld + 8 * j) = make_uint4(a[0], a[1], a[2], a[3]);
+        if (i + 8 < rows_left) *reinterpret_cast<uint4*>(q + (i + 8) * ld + 8 * j) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+    __device__ __forceinline__ void finish(const StepParams& p, const Place& w, int row0, int col0, bool mirror, float (&v)[4][4]) {
+        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
+        if constexpr (kStep == kGram) {
+            const float t = s * s * (kA / (kX * kX));
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[g][c] *= t;
+        }
+        if constexpr (kStep != kGram) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                quad_transpose(hi[h]);
+                if (kStep == kApply) quad_transpose(lo[h]);
+            }
+            const uint32_t x[2][4] = {{hi[0].x, hi[0].y, hi[0].z, hi[0].w}, {hi[1].x, hi[1].y, hi[1].z, hi[1].w}};
+            const uint32_t z[2][4] = {{lo[0].x, lo[0].y, lo[0].z, lo[0].w}, {lo[1].x, lo[1].y, lo[1].z, lo[1].w}};
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float4 fc;   // factors of two columns
+                if (kStep == kApply && p.tall)
+                    fc = *reinterpret_cast<const float4*>(p.factors + w.z * p.factor_stride + col0 + 8 * g + 2 * j);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 t = unpack_f16x2(x[h][g]);
+                    if constexpr (kStep == kSquare) {
+                        v[g][2 * h] = p.b * t.x + v[g][2 * h] * (p.c / kA);
+                        v[g][2 * h + 1] = p.b * t.y + v[g][2 * h + 1] * (p.c / kA);
+                    } else {
+                        const float2 u = unpack_f16x2(z[h][g]);
+                        const float2 f0 = p.tall ? make_float2(fc.x, fc.y) : f[h], f1 = p.tall ? make_float2(fc.z, fc.w) : f[h];
+                        v[g][2 * h] = s * (f0.x * t.x + (f0.y * (1.0f / kLo)) * u.x + v[g][2 * h] * (1.0f / kA));
+                        v[g][2 * h + 1] = s * (f1.x * t.y + (f1.y * (1.0f / kLo)) * u.y + v[g][2 * h + 1] * (1.0f / kA));
+                    }
+                }
+            }
+        }
+        if (kStep == kApply && p.y) {
+            uint16_t* q = p.y + w.z * p.y_stride + row0 * p.ldy + col0;
+            if (p.y_vec && col0 + 32 <= p.cols) {
+                uint32_t a[4], b[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    a[g] = pack_bf16x2(v[g][0] * (1.0f / kX), v[g][1] * (1.0f / kX));
+                    b[g] = pack_bf16x2(v[g][2] * (1.0f / kX), v[g][3] * (1.0f / kX));
+                }
+                store(q, p.ldy, p.rows - row0, a, b);
+            } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int row = i + 8 * (c >> 1), col = 8 * g + 2 * j + (c & 1);
+                        if (row0 + row < p.rows && col0 + col < p.cols) q[row * p.ldy + col] = to_bf16(v[g][c] * (1.0f / kX));
+                    }
+            }
+            return;
+        }
+        if (kStep == kSquare && row0 < col0 + 32 && col0 < row0 + 16) {   // the unit meets the diagonal
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int row = row0 + i + 8 * (c >> 1), col = col0 + 8 * g + 2 * j + (c & 1);
+                    if (row == col && row < p.rows)
+                        p.factors[w.z * p.factor_stride + row] =
+                            make_float2(p.a + (v[g][c] - round_f16(v[g][c])) * (1.0f / kA), p.a + v[g][c] * (1.0f / kA));
+                }
+        }
+        const int64_t at = w.z * p.stride + row0 * p.ld + col0;
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            a[g] = pack_f16x2(v[g][0], v[g][1]);
+            b[g] = pack_f16x2(v[g][2], v[g][3]);
+        }
+        if (kStep == kApply) {
+            uint32_t e[4], g2[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float2 t = unpack_f16x2(a[g]), u = unpack_f16x2(b[g]);
+                e[g] = pack_f16x2((v[g][0] - t.x) * kLo, (v[g][1] - t.y) * kLo);
+                g2[g] = pack_f16x2((v[g][2] - u.x) * kLo, (v[g][3] - u.y) * kLo);
+            }
+            store(p.d_lo + at, p.ld, p.rows - row0, e, g2);
+        } else if (mirror) {
+            // transposed, a lane has two rows of column i of each group of eight: after the
+            // exchange, column 8 j + i and all eight rows
+            uint32_t e[4], g2[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) e[g] = transpose8x8(a[g]), g2[g] = transpose8x8(b[g]);
+            quad_transpose(e);
+            quad_transpose(g2);
+            const int col = col0 + 8 * j + i;
+            if (col < p.cols) {
+                uint16_t* q = p.d_hi + w.z * p.stride + col * p.ld + row0;
+                *reinterpret_cast<uint4*>(q) = make_uint4(e[0], e[1], e[2], e[3]);
+                *reinterpret_cast<uint4*>(q + 8) = make_uint4(g2[0], g2[1], g2[2], g2[3]);
+            }
+        }
+        store(p.d_hi + at, p.ld, p.rows - row0, a, b);
+    }
+};
+
+// A warp of either CTA is done reading an accumulator: one arrival at the even CTA.
+__device__ __forceinline__ void release_accumulator(uint64_t* bar) {
+    tcgen05_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) peer_arrive(peer_addr(smem_addr(bar), 0));
+}
+
+__device__ __forceinline__ bool step_wait(uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, &g_orthogonal_status); }
+
+template <Step kStep>
+__global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const __grid_constant__ StepParams p) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drained = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+
+    const int warp = uniform_warp();
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 2 * kEndWarps);
+        }
+        mbar_init(drained, 1);
+        fence_barrier_init();
+        tensor_map_prefetch(&p.map_a);
+        tensor_map_prefetch(&p.map_b);
+    }
+    if (warp == 2) tmem_alloc<true>(tmem_slot, 512);
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_started();
+    tcgen05_fence_after();
+    await_predecessor();
+    const uint32_t tmem = *tmem_slot;
+
+    const int b_boxes = p.b_mn ? (p.bn / 2 + 63) / 64 : 1;
+    const uint32_t stage_bytes = 16384u + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)p.bn * 64u);
+
+    if (warp == 0) {
+        int s = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < p.all; t += pairs) {
+            const Place w = place_of<kStep>(p, t);
+            const int row = w.tm * 256 + (int)rank * 128;
+            const int col = w.tn * p.bn + (int)rank * (width_of(p, w.tn) / 2);
+            for (int kb = 0; kb < p.k_blocks; ++kb) {
+                if (round > 0 && !(ok = step_wait(empty + s, (round - 1) & 1))) break;
+                const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384;
+                const uint32_t bar = peer_addr(smem_addr(full + s), 0);
+                const int k = kb * 64;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * stage_bytes);
+                    if (p.a_mn) {
+                        tensor_load_pair(a, &p.map_a, row, k, w.z, bar);
+                        tensor_load_pair(a + kSubTileBytes, &p.map_a, row + 64, k, w.z, bar);
+                    } else {
+                        tensor_load_pair(a, &p.map_a, k, row, w.z, bar);
+                    }
+                    if (p.b_mn) {
+                        for (int i = 0; i < b_boxes; ++i) tensor_load_pair(b + i * kSubTileBytes, &p.map_b, col + 64 * i, k, w.z, bar);
+                    } else {
+                        tensor_load_pair(b, &p.map_b, k, col, w.z, bar);
+                    }
+                }
+                if (++s == kStages) s = 0, ++round;
+            }
+        }
+        if (!ok && rank == 0)   // copies in flight land before the CTAs end
+            for (int i = 0; i < kStages; ++i) {
+                const uint32_t done = i < s ? round : round - 1;   // the last round issued on stage i
+                if (round > 0 || i < s) (void)mbar_wait_bounded(full + i, done & 1, kWaitCycles / 8);
+            }
+    } else if (warp == 1 && rank == 0) {
+        int s = 0, use = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        const uint32_t a_step = descriptor_step(p.a_mn), b_step = descriptor_step(p.b_mn);
+        for (int t = pair; ok && t < p.all; t += pairs, ++use) {
+            const Place w = place_of<kStep>(p, t);
+            const uint32_t idesc = instruction_descriptor(256, width_of(p, w.tn), p.a_mn, p.b_mn, false);
+            const int buf = use & 1;
+            if (use >= 2 && !(ok = step_wait(acc_empty + buf, (use / 2 - 1) & 1))) break;
+            tcgen05_fence_after();
+            const uint32_t d = tmem + buf * 256;
+            for (int kb = 0; kb < p.k_blocks; ++kb) {
+                if (!(ok = step_wait(full + s, round & 1))) break;
+                tcgen05_fence_after();
+                const uint32_t a = smem_addr(smem + s * kStageBytes);
+                const uint64_t da = smem_descriptor(a, p.a_mn), db = smem_descriptor(a + 16384, p.b_mn);
+                const int left = p.depth - kb * 64;
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)   // the last step of all may end early
+                        if (left > 16 * i) mma_bf16<true>(d, da + i * a_step, db + i * b_step, idesc, kb > 0 || i > 0);
+                    mma_commit<true>(empty + s);
+                }
+                if (++s == kStages) s = 0, ++round;
+            }
+            if (ok && elect_one()) mma_commit<true>(acc_full + buf);
+        }
+        if (!ok) {   // products in flight end before the tensor memory is freed
+            if (elect_one()) mma_commit<true>(drained);
+            (void)mbar_wait_bounded(drained, 0, kWaitCycles / 8);
+        }
+    } else if (warp >= 4) {
+        // units of 16 rows x 32 columns: of its 32 rows this warp ends one half, over one
+        // half of the columns, side by side so that whole lines are written together
+        const int q = warp & 3, h = (warp - 4) / 4;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32 + (h & 1) * 16) << 16);
+        int use = 0;
+        for (int t = pair; t < p.all; t += pairs, ++use) {
+            const Place w = place_of<kStep>(p, t);
+            const int chunks_n = width_of(p, w.tn) / 32, first = (h >> 1) * ((chunks_n + 1) / 2);
+            const int units = h >> 1 ? chunks_n - first : (chunks_n + 1) / 2;   // of this warp
+            const int row0 = w.tm * 256 + (int)rank * 128 + q * 32 + (h & 1) * 16, buf = use & 1;
+            const bool mirror = (w.tn + 1) * p.bn <= w.tm * 256;
+            if (!step_wait(acc_full + buf, (use / 2) & 1)) break;
+            tcgen05_fence_after();
+#pragma unroll 1
+            for (int u = 0; u < units; ++u) {
+                const int col0 = w.tn * p.bn + (first + u) * 32;
+                StepEnd<kStep> end;
+                float v[4][4];
+                if (row0 < p.rows) end.load(p, w, row0, col0);
+                tmem_load_fragment(lanes + buf * 256 + (first + u) * 32, v);
+                if (u + 1 == units) release_accumulator(acc_empty + buf);   // this warp's last read
+                if (row0 < p.rows) end.finish(p, w, row0, col0, mirror, v);
+            }
+            if (units == 0) release_accumulator(acc_empty + buf);   // a narrow last tile: no unit for this warp
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tcgen05_fence_after();
+    if (warp == 2) tmem_free<true>(tmem, 512);
+}
+
+// ---- launches ------------------------------------------------------------------------------
+// A batch of equal matrices of the workspace: rows `ld` apart, 16-byte aligned.
+struct Matrices {
+    const uint16_t* p;
+    int64_t rows, cols, ld, batch;
+};
+static bool make_map3(const Matrices& m, int box_rows, CUtensorMap* map) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.batch};
+    const cuuint64_t pitch[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.ld * m.rows) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(m.p), dims, pitch, box, unit,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The tile width with the least estimated time: waves of pairs, each a tile's blocks
+// (bound by the tensor core, or for narrow tiles by shared memory) and the part of its
+// end that nothing hides.  A symmetric result takes widths that divide 256.
+struct StepPlan {
+    int64_t tiles;
+    int bn, tiles_n;
+};
+static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, int64_t batch) {
+    const int64_t pairs = sm_pairs(), k_blocks = (depth + 63) / 64, tm = (rows + 255) / 256;
+    StepPlan best{0, 0, 0};
+    int64_t least = INT64_MAX;
+    for (int bn = 256; bn >= 32; bn = step == kApply ? bn - 32 : bn / 2) {
+        const int64_t tn = (cols + bn - 1) / bn;
+        int64_t tiles = tm * tn;
+        if (step != kApply) {
+            tiles = 0;
+            for (int64_t i = 1; i <= tm; ++i) tiles += i * (256 / bn) < tn ? i * (256 / bn) : tn;
+        }
+        if (tiles > INT32_MAX / 4 / batch) continue;
+        const int64_t waves = (tiles * batch + pairs - 1) / pairs;
+        const int64_t cycles = waves * (1500 + k_blocks * (2 * bn > 256 + bn ? 2 * bn : 256 + bn) + 24 * bn);
+        if (cycles < least) least = cycles, best = StepPlan{tiles, bn, (int)tn};
+    }
+    return best;
+}
+
+template <Step kStep>
+static int launch_step(StepParams& q, const Matrices& a, bool a_mn, const Matrices& b, bool b_mn, cudaStream_t s) {
+    static Done done;
+    if (const int rc = allow_smem((const void*)orthogonal_step_kernel<kStep>, kStepSmem, done)) return rc;
+    const StepPlan plan = plan_step(kStep, q.rows, q.cols, q.depth, a.batch);
+    if (!plan.bn) return ZERO_ERANGE;
+    q.bn = plan.bn;
+    q.tiles_n = plan.tiles_n;
+    q.tiles = (int32_t)plan.tiles;
+    q.all = (int32_t)(plan.tiles * a.batch);
+    q.k_blocks = (q.depth + 63) / 64;
+    q.a_mn = a_mn; q.b_mn = b_mn;
+    if (!make_map3(a, a_mn ? 64 : 128, &q.map_a) || !make_map3(b, b_mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
+    const int64_t pairs = sm_pairs();
+    return launch_dense(orthogonal_step_kernel<kStep>, dim3((unsigned)(2 * (q.all < pairs ? q.all : pairs))), kStepThreads, 2, true, kStepSmem,
+                        s, q);
+}
+
+// Where everything stands in the workspace.
+struct OrthogonalSpace {
+    int64_t ldx, lds, parts;                       // rows of X; of A and B
+    int64_t hi[2], lo[2], a, b, factors, norm, scale, bytes;
+};
+constexpr int64_t kLongest = (int64_t)1 << 30;
+
+static int orthogonal_space(int64_t batch, int64_t rows, int64_t cols, OrthogonalSpace* w) {
+    const int64_t side = rows < cols ? rows : cols, longer = rows < cols ? cols : rows;
+    // a side's square and a matrix's groups of eight are counted in 31 bits, a batch's bytes in 62
+    if (longer > kLongest || side > 32768 || rows * ((cols + 7) / 8) > INT32_MAX / 2) return ZERO_ERANGE;
+    w->ldx = (cols + 63) / 64 * 64;
+    w->lds = (side + 63) / 64 * 64;
+    const int64_t x = rows * w->ldx * 2, a = side * w->lds * 2;
+    const int64_t groups = rows * ((cols + 7) / 8), most = 1024;
+    w->parts = (groups + 4 * kSourceThreads - 1) / (4 * kSourceThreads);
+    if (w->parts > most) w->parts = most;
+    if (batch > ((int64_t)1 << 60) / (4 * x + 2 * a + 16 * w->lds + 16 * w->parts + 4096)) return ZERO_ERANGE;
+    int64_t at = 0;
+    const auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    for (int i = 0; i < 2; ++i) w->hi[i] = take(batch * x), w->lo[i] = take(batch * x);
+    w->a = take(batch * a);
+    w->b = take(batch * a);
+    w->factors = take(batch * w->lds * (int64_t)sizeof(float2));
+    w->norm = take(batch * w->parts * 8);
+    w->scale = take(batch * 4);
+    w->bytes = at;
+    return ZERO_OK;
+}
+
+}  // namespace zgb
+
+extern "C" int zero_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, int64_t* bytes) {
+    using namespace zgb;
+    if (batch < 0 || rows < 0 || cols < 0 || !bytes) return ZERO_EINVAL;
+    *bytes = 0;
+    if (batch == 0 || rows == 0 || cols == 0) return ZERO_OK;
+    OrthogonalSpace w{};
+    if (const int rc = orthogonal_space(batch, rows, cols, &w)) return rc;
+    *bytes = w.bytes;
+    return ZERO_OK;
+}
+
+extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void* x, int64_t x_stride, int64_t ldx,
+                                  int32_t x_dtype, uint16_t* y, int64_t y_stride, int64_t ldy, int32_t steps,
+                                  const float* coefficients, float eps, void* workspace, int64_t workspace_bytes, void* stream) {
+    using namespace zgb;
+    if (batch < 0 || rows < 0 || cols < 0 || (x_dtype != ZERO_BF16 && x_dtype != ZERO_F32)) return ZERO_EINVAL;
+    if (steps < 1 || steps > 100 || !coefficients || !(eps >= 0.0f) || !std::isfinite(eps)) return ZERO_EINVAL;
+    for (int i = 0; i < 3; ++i)
+        if (!std::isfinite(coefficients[i])) return ZERO_EINVAL;
+    if (batch == 0 || rows == 0 || cols == 0) return ZERO_OK;
+    if (const int rc = check_matrix(x, rows, cols, ldx, x_dtype)) return rc;
+    if (const int rc = check_matrix(y, rows, cols, ldy, ZERO_BF16)) return rc;
+    if (batch > 1) {
+        const int64_t most = INT64_MAX / 8 / batch, extent = (rows - 1) * ldy + cols;
+        if (x_stride < 0 || y_stride < extent) return ZERO_EINVAL;   // results that overlap
+        if (x_stride > most || y_stride > most) return ZERO_ERANGE;
+    }
+    if (batch > 65535) return ZERO_ERANGE;
+    OrthogonalSpace w{};
+    if (const int rc = orthogonal_space(batch, rows, cols, &w)) return rc;
+    if (!workspace) return ZERO_EINVAL;
+    if (reinterpret_cast<uintptr_t>(workspace) % 128) return ZERO_EALIGN;
+    if (workspace_bytes < w.bytes) return ZERO_ERANGE;
+    if (check_device_ptr(x) || check_device_ptr(y) || check_device_ptr(workspace)) return ZERO_EINVAL;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* base = static_cast<char*>(workspace);
+    const auto at = [&](int64_t offset) { return reinterpret_cast<uint16_t*>(base + offset); };
+    const bool f32 = x_dtype == ZERO_F32, tall = rows > cols;
+    const int64_t side = tall ? cols : rows;
+
+    SourceParams src{};
+    src.x = x; src.ldx = ldx; src.stride = batch > 1 ? x_stride : 0;
+    src.rows = (int32_t)rows; src.cols = (int32_t)cols; src.groups = (int32_t)((cols + 7) / 8);
+    src.parts = (int32_t)w.parts;
+    src.f32 = f32;
+    src.vec = cols % 8 == 0 && rows_aligned16(x, ldx, f32 ? 4 : 2) && (batch == 1 || x_stride * (f32 ? 4 : 2) % 16 == 0);
+    src.norm = reinterpret_cast<double*>(base + w.norm);
+    src.scale = reinterpret_cast<float*>(base + w.scale);
+    src.hi = at(w.hi[0]);
+    src.lo = f32 ? at(w.lo[0]) : nullptr;
+    src.ld = w.ldx; src.to = rows * w.ldx;
+    src.eps = eps;
+    const dim3 grid((unsigned)w.parts, (unsigned)batch);
+    if (const int rc = launch_dense(orthogonal_norm_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
+    if (const int rc = launch_dense(orthogonal_source_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
+
+    const Matrices gram{at(w.a), side, side, w.lds, batch}, poly{at(w.b), side, side, w.lds, batch};
+    for (int i = 0; i < steps; ++i) {
+        const Matrices now{at(w.hi[i & 1]), rows, cols, w.ldx, batch};
+        StepParams q{};
+        q.tall = tall;
+        q.factors = reinterpret_cast<float2*>(base + w.factors); q.factor_stride = w.lds;
+        q.scale = src.scale;
+        q.a = coefficients[0]; q.b = coefficients[1]; q.c = coefficients[2];
+        q.ld = w.lds; q.stride = side * w.lds;
+        q.rows = q.cols = (int32_t)side;
+        q.depth = (int32_t)(tall ? rows : cols);
+        q.first = i == 0;
+        q.d_hi = at(w.a);
+        if (const int rc = launch_step<kGram>(q, now, tall, now, tall, s)) return rc;
+        q.depth = (int32_t)side;
+        q.first = false;
+        q.c_hi = at(w.a);
+        q.d_hi = at(w.b);
+        if (const int rc = launch_step<kSquare>(q, gram, false, gram, false, s)) return rc;
+        q.rows = (int32_t)rows; q.cols = (int32_t)cols;
+        q.ld = w.ldx; q.stride = rows * w.ldx;
+        q.first = i == 0;
+        q.c_hi = now.p;
+        q.c_lo = i == 0 && !f32 ? nullptr : at(w.lo[i & 1]);
+        q.d_hi = at(w.hi[~i & 1]);
+        q.d_lo = at(w.lo[~i & 1]);
+        if (i + 1 == steps) {
+            q.y = y; q.ldy = ldy; q.y_stride = batch > 1 ? y_stride : 0;
+            q.y_vec = rows_aligned16(y, ldy, 2) && (batch == 1 || y_stride % 8 == 0);
+        }
+        // wide: B X, X read along its rows; tall: X B, B being its own transpose
+        if (const int rc = tall ? launch_step<kApply>(q, now, false, poly, false, s) : launch_step<kApply>(q, poly, false, now, true, s)) return rc;
+    }
+    return ZERO_OK;
+}

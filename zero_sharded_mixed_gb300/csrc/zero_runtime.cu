@@ -13,6 +13,8 @@ namespace zgb {
 int take_qgrad_status();
 // The same for the waits of the products' kernels (zero_linear.cu).
 int take_linear_status();
+// And of the orthogonalisation's (zero_orthogonal.cu).
+int take_orthogonal_status();
 }  // namespace zgb
 
 namespace zgb {
@@ -127,6 +129,7 @@ extern "C" int zero_status_check(void* stream) {
     const int rc = zgb::take_device_status();   // ZERO_ETIMEOUT if a bounded device wait gave up
     const int rq = zgb::take_qgrad_status();    // the same for the 8-bit gradient kernels' waits
     const int rl = zgb::take_linear_status();   // and for those of the products
+    const int ro = zgb::take_orthogonal_status();   // and of the orthogonalisation
     const int rs = zgb::take_schedule_status();  // ZERO_ERANGE if a schedule index left its table
-    return rc != ZERO_OK ? rc : rq != ZERO_OK ? rq : rl != ZERO_OK ? rl : rs;
+    return rc != ZERO_OK ? rc : rq != ZERO_OK ? rq : rl != ZERO_OK ? rl : ro != ZERO_OK ? ro : rs;
 }

@@ -44,11 +44,11 @@ __device__ __forceinline__ uint64_t smem_descriptor(uint32_t addr, bool mn_major
 }
 __device__ __forceinline__ uint32_t descriptor_step(bool mn_major) { return (mn_major ? 2048u : 32u) >> 4; }
 
-// Instruction descriptor of kind::f16: fp32 accumulator (1 in bit 4), bf16 operands
-// (1 in bits 7 and 10), MN-major flags in bits 15 and 16, N / 8 from bit 17, M / 16
-// from bit 24.
-__device__ __forceinline__ uint32_t instruction_descriptor(int m, int n, bool a_mn, bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+// Instruction descriptor of kind::f16: fp32 accumulator (1 in bit 4), the operands' type
+// in bits 7 and 10 (1 bf16, 0 fp16), MN-major flags in bits 15 and 16, N / 8 from bit 17,
+// M / 16 from bit 24.
+__device__ __forceinline__ uint32_t instruction_descriptor(int m, int n, bool a_mn, bool b_mn, bool bf16 = true) {
+    return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
@@ -72,6 +72,7 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
 }
 
+// bf16 or fp16 operands, as the instruction descriptor says.
 template <bool kPair>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     if constexpr (kPair)
@@ -209,6 +210,12 @@ __device__ __forceinline__ void tensor_load_pair(uint32_t dst, const CUtensorMap
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// The same from matrix z of a batch.
+__device__ __forceinline__ void tensor_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tensor_map_prefetch(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
