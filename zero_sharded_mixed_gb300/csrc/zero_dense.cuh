@@ -198,6 +198,14 @@ __device__ __forceinline__ void raw8(const uint4* u, float* v) {   // as loaded:
 // may give a stale line and which the compiler may move above the wait.
 __device__ __forceinline__ uint4 ld_live_u4(const void* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 
+// Asynchronous copies of 16 bytes to shared memory, coherent as well.
+__device__ __forceinline__ void copy_block(uint32_t dst, uintptr_t src, bool want) {   // zeros where not wanted
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(want ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
 // p: the first of the eight, 16-byte aligned.
 __device__ __forceinline__ void store8(void* p, bool f32, const float* v) {
     if (f32) {

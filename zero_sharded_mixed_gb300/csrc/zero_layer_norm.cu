@@ -6,21 +6,23 @@
 //           dx = residual + rstd (g - mean(g) - xhat mean(g xhat)),
 //           dgamma = acc + sum over rows of dy xhat,  dbeta = acc + sum over rows of dy
 //
-// A row belongs to a team: some lanes of a warp (up to 512 columns) or a CTA (up to
-// 16384), whose threads hold the same columns of every row they see, so that gamma,
-// beta and the sums of the weights' gradients stay in registers.  The statistics come
-// from the values that a thread holds: the mean first, then the deviations from it with
-// their sum, which corrects both, so that neither a large mean nor the order of the
-// sum costs digits.  Everything is fp32.
+// A row belongs to a team: some lanes of a warp, a warp, or up to 16 warps of a CTA
+// (16384 columns), whose threads hold the same columns, up to 32, of every row they see,
+// so that gamma, beta and the sums of the weights' gradients stay in registers.  Rows to
+// come are copied to shared memory ahead of their turn.  Everything is fp32.
 #include <cmath>
+#include <type_traits>
 
+#include "zero_tensor.cuh"
 #include "zero_dense.cuh"
 
 namespace zgb {
 
 struct NormParams {
     int64_t rows;
-    int32_t cols, lanes, take;             // lanes of a warp's team; rows that a team takes at a time
+    int32_t cols, lanes, warps;            // lanes of a team within a warp, or warps of a team
+    int32_t ahead;                         // rows of a team that are on their way while one is worked on
+    uint32_t slot, part_bytes, at[3];      // bytes: of a row's slot; of a thread (kVec) or a team in it; where its streams begin there
     int64_t ldx, ldr, lds, ldy;
     const void* x;
     const void* residual;                  // forward: joins x; backward: joins dx; or null
@@ -31,414 +33,532 @@ struct NormParams {
     const uint16_t* beta;
     float* mean;
     float* rstd;
-    float* part;                           // [2][parts][cols]: the teams' sums of dy xhat and dy, or null
+    float* part;                           // [2][parts][cols]: the CTAs' sums of dy xhat and dy, or null
     float eps;
     bool y_f32, weights_vec;
 };
 
-// ---- a thread's eight columns (a piece), of which it has kPer ----------------------
+// ---- a thread's eight columns (a piece), of which it has up to kPer -----------------------
 // kVec: rows on 16-byte boundaries of whole pieces, columns 8 (t + team j) .. + 7.
 // Otherwise column t + team (8 j + k), so that the team's accesses fall together.
 struct Team {
-    int t, size;
+    int t, size, have;   // this thread, the threads, the pieces (kVec) or elements that this one has
 };
 template <bool kVec>
 __device__ __forceinline__ int column(const Team& m, int j, int k) {
     return kVec ? 8 * (m.t + m.size * j) + k : m.t + m.size * (8 * j + k);
 }
-__device__ __forceinline__ float one(const float* p) { return __ldcs(p); }
-__device__ __forceinline__ float one(const uint16_t* p) { return bf16_one(__ldcs(p)); }
+template <bool kVec>
+__device__ __forceinline__ bool exists(const Team& m, int j, int k) {   // k 0: any of the piece
+    return (kVec ? j : 8 * j + k) < m.have;
+}
 
-template <bool kF32, bool kVec>
-struct Piece {
-    uint4 u[kVec ? (kF32 ? 2 : 1) : 2];    // not kVec: eight fp32 values
-    __device__ __forceinline__ void load(const void* row, const Team& m, int j, int cols) {
-        using T = typename std::conditional<kF32, float, uint16_t>::type;
-        const T* q = static_cast<const T*>(row);
-        if constexpr (kVec) {
-            const int c = column<true>(m, j, 0);
-            u[0] = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (kF32) u[1] = u[0];
-            if (c < cols) {
-                u[0] = ld_live_u4(q + c);
-                if constexpr (kF32) u[1] = ld_live_u4(q + c + 4);
-            }
-        } else {
-            float v[8];
+// Pairs of fp32 operations in one instruction: the kernels are bound by how many they issue
+// (one at a time, 8192 x 1600 took 44 instructions an element and 27 us forward).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// Eight neighbours of a piece as they are stored: fp32 words or bf16 pairs.
+template <bool kF32>
+struct Words {
+    uint32_t w[kF32 ? 8 : 4];
+    __device__ __forceinline__ float2 pair(int k) const {
+        if constexpr (kF32)
+            return make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+        else
+            return make_float2(bf16_lo(w[k]), bf16_hi(w[k]));
+    }
+    // Added, one rounding to the type.
+    __device__ __forceinline__ void add(const Words& o) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int c = column<false>(m, j, k);
-                v[k] = c < cols ? one(q + c) : 0.0f;
-            }
-            u[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-            u[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+        for (int k = 0; k < (kF32 ? 8 : 4); ++k) {
+            if constexpr (kF32)
+                w[k] = __float_as_uint(__uint_as_float(w[k]) + __uint_as_float(o.w[k]));
+            else
+                asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(w[k]) : "r"(o.w[k]));
         }
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const { raw8<!kVec || kF32>(u, v); }
 };
 
-template <bool kVec>
-__device__ __forceinline__ void store_piece(void* row, bool f32, const Team& m, int j, int cols, const float (&v)[8]) {
+constexpr int kMostWarps = 16;   // of a CTA, and of a team
+
+// A matrix's rows on their way through shared memory: asynchronous copies, some rows
+// ahead of their turn, keep the memory busy behind the sums over the team.  A stream goes
+// down a team's rows, `hop` elements from one to the next.
+// kVec: every thread copies its own pieces to places of its own, so that nothing but its
+// own copies have to be waited for; kAt counts the places, of 16 bytes, before this
+// stream's.  The threads' places of one number lie side by side, kPitch from one number to
+// the next: a warp's copies fill whole lines (a thread's places side by side, with an odd
+// pitch for the banks' sake, took a third longer), and at offsets known to the compiler.
+// Otherwise the team copies the row's 16-byte blocks as they lie, which hold up to 15
+// bytes of the neighbours' on either side, from byte `at` of its slot, and reads elements
+// from there; where a block would reach past the matrix's own memory its elements come
+// one by one.
+template <bool kF32, bool kVec, int kPer, int kPitch, int kAt>
+struct Stream {
+    static constexpr int kSize = kF32 ? 4 : 2, kPlaces = kF32 ? 2 : 1;
+    using T = typename std::conditional<kF32, float, uint16_t>::type;
+    const T* to_send;   // the next row to send: kVec this thread's first piece of it
+    int64_t hop;
+    uint32_t at, shift, turn;   // not kVec: where the row to read begins in its first block, and how that moves on
+    uintptr_t begin, end;
+
+    __device__ __forceinline__ Stream(const void* q, int64_t ld, uint32_t at, int64_t row, int64_t stride, int64_t rows, int cols, const Team& m)
+        : hop(stride * ld), at(at) {
+        const T* p = static_cast<const T*>(q);
+        to_send = p + row * ld + (kVec ? 8 * m.t : 0);
+        if constexpr (!kVec) {
+            shift = (uint32_t)(reinterpret_cast<uintptr_t>(to_send) & 15);
+            turn = (uint32_t)(hop * kSize) & 15;
+            begin = reinterpret_cast<uintptr_t>(p);
+            end = reinterpret_cast<uintptr_t>(p + (rows - 1) * ld + cols);
+        }
+    }
+    // slot: kVec a shared address, this thread's; else the team's
+    __device__ __forceinline__ void send(uint32_t slot, const Team& m, int cols) {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (!exists<true>(m, j, 0)) break;
+#pragma unroll
+                for (int i = 0; i < kPlaces; ++i)
+                    copy_block(slot + kPitch * (kAt + j * kPlaces + i), reinterpret_cast<uintptr_t>(to_send + 8 * m.size * j) + 16 * i, true);
+            }
+        } else {
+            const uintptr_t from = reinterpret_cast<uintptr_t>(to_send), first = from & ~(uintptr_t)15, last = from + cols * kSize;
+            for (uintptr_t b = first + 16 * m.t; b < last; b += 16 * m.size) {
+                const uint32_t to = slot + at + (uint32_t)(b - first);
+                if (b >= begin && b + 16 <= end) {
+                    copy_block(to, b, true);
+                } else {
+                    for (uintptr_t e = b; e < b + 16; e += kSize) {
+                        if (e < from || e >= last) continue;
+                        if constexpr (kF32)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (uint32_t)(e - b)), "r"(*reinterpret_cast<const uint32_t*>(e)) : "memory");
+                        else
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + (uint32_t)(e - b)), "h"(*reinterpret_cast<const uint16_t*>(e)) : "memory");
+                    }
+                }
+            }
+        }
+        to_send += hop;
+    }
+    __device__ __forceinline__ void next_row() {   // to read
+        if (!kVec) shift = (shift + turn) & 15;
+    }
+    __device__ __forceinline__ Words<kF32> get(const uint8_t* slot, const Team& m, int j) const {
+        Words<kF32> v;
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i = 0; i < kPlaces; ++i) {
+                const uint4 u = *reinterpret_cast<const uint4*>(slot + kPitch * (kAt + j * kPlaces + i));
+                v.w[4 * i] = u.x; v.w[4 * i + 1] = u.y; v.w[4 * i + 2] = u.z; v.w[4 * i + 3] = u.w;
+            }
+        } else {
+            const T* q = reinterpret_cast<const T*>(slot + at + shift) + column<false>(m, j, 0);
+            uint32_t e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if constexpr (kF32)
+                    e[k] = exists<false>(m, j, k) ? __float_as_uint(q[m.size * k]) : 0u;
+                else
+                    e[k] = exists<false>(m, j, k) ? q[m.size * k] : 0u;
+            }
+#pragma unroll
+            for (int k = 0; k < (kF32 ? 8 : 4); ++k) v.w[k] = kF32 ? e[k] : e[(2 * k) % 8] | e[(2 * k + 1) % 8] << 16;
+        }
+        return v;
+    }
+};
+
+// A piece to a row, q: kVec this thread's first piece of it, else its first column.
+template <bool kVec, bool kF32>
+__device__ __forceinline__ void store_words(void* q, const Team& m, int j, const Words<kF32>& v) {
     if constexpr (kVec) {
-        const int c = column<true>(m, j, 0);
-        if (c < cols) store8(static_cast<char*>(row) + (int64_t)c * (f32 ? 4 : 2), f32, v);
+        uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(q) + m.size * j * (kF32 ? 32 : 16));
+        to[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+        if constexpr (kF32) to[1] = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int c = column<false>(m, j, k);
-            if (c >= cols) continue;
-            if (f32)
-                static_cast<float*>(row)[c] = v[k];
+            if (!exists<false>(m, j, k)) break;
+            if constexpr (kF32)
+                static_cast<uint32_t*>(q)[m.size * (8 * j + k)] = v.w[k];
             else
-                static_cast<uint16_t*>(row)[c] = to_bf16(v[k]);
+                static_cast<uint16_t*>(q)[m.size * (8 * j + k)] = (uint16_t)(k & 1 ? v.w[k / 2] >> 16 : v.w[k / 2]);
         }
     }
+}
+template <bool kVec>
+__device__ __forceinline__ void store_pairs(void* q, bool f32, const Team& m, int j, const float2 (&v)[4]) {
+    if (f32) {
+        Words<true> w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w.w[2 * k] = __float_as_uint(v[k].x), w.w[2 * k + 1] = __float_as_uint(v[k].y);
+        store_words<kVec, true>(q, m, j, w);
+    } else {
+        Words<false> w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w.w[k] = pack_bf16x2(v[k].x, v[k].y);
+        store_words<kVec, false>(q, m, j, w);
+    }
+}
+// This thread's place in a row of an output, and the bytes from one row of the team to the next.
+template <bool kVec>
+__device__ __forceinline__ char* output(void* q, int64_t ld, int size, int64_t row, const Team& m) {
+    return static_cast<char*>(q) + (row * ld + (kVec ? 8 : 1) * m.t) * size;
 }
 
 // A piece of gamma or beta as bf16 pairs; `fill` (a pair) where the vector is absent.
 template <bool kVec>
-__device__ __forceinline__ uint4 weight_piece(const uint16_t* w, bool vec, const Team& m, int j, int cols, uint32_t fill) {
-    if (!w) return make_uint4(fill, fill, fill, fill);
-    if (kVec && vec) return column<true>(m, j, 0) < cols ? *reinterpret_cast<const uint4*>(w + column<true>(m, j, 0)) : make_uint4(0u, 0u, 0u, 0u);
-    uint32_t p[8];
+__device__ __forceinline__ Words<false> weight_piece(const uint16_t* w, bool vec, const Team& m, int j, uint32_t fill) {
+    Words<false> v;
+    if (!w) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) p[k] = column<kVec>(m, j, k) < cols ? w[column<kVec>(m, j, k)] : 0u;
-    return make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
+        for (int k = 0; k < 4; ++k) v.w[k] = fill;
+    } else if (kVec && vec) {
+        const uint4 u = exists<true>(m, j, 0) ? *reinterpret_cast<const uint4*>(w + column<true>(m, j, 0)) : make_uint4(0u, 0u, 0u, 0u);
+        v.w[0] = u.x; v.w[1] = u.y; v.w[2] = u.z; v.w[3] = u.w;
+    } else {
+        uint32_t e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = exists<kVec>(m, j, k) ? w[column<kVec>(m, j, k)] : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v.w[k] = e[2 * k] | e[2 * k + 1] << 16;
+    }
+    return v;
 }
 constexpr uint32_t kOnes = 0x3f803f80u;
 
-// ---- sums over a team ---------------------------------------------------------------
-// kCount values of every thread of a warp, a power of two: halves are exchanged while
-// there are several, so that 8 values take 9 shuffles; lane l ends with value
-// l / (32 / kCount).
+// ---- teams ----------------------------------------------------------------------------
+// kMany: several warps; else `lanes` lanes (a power of two) of one.
+template <bool kVec, bool kMany>
+__device__ __forceinline__ Team team_of(const NormParams& p, int* which, int* teams) {
+    const int size = kMany ? 32 * p.warps : p.lanes;
+    *which = threadIdx.x / size;
+    *teams = blockDim.x / size;
+    const int t = threadIdx.x - *which * size, all = kVec ? p.cols / 8 : p.cols;
+    return Team{t, size, all > t ? (all - t + size - 1) / size : 0};
+}
+__device__ __forceinline__ void team_barrier(int which, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(which + 1), "r"(threads) : "memory");
+}
+// Over `lanes` neighbouring lanes (32: a literal for teams of warps); every lane gets it.
 template <int kCount>
-__device__ __forceinline__ float warp_sums(float (&v)[kCount]) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void lane_sums(float (&v)[kCount], int lanes) {
 #pragma unroll
-    for (int n = kCount / 2, o = 16; o; n /= 2, o /= 2) {
-        if (n) {
+    for (int o = 16; o; o /= 2) {
+        if (o >= lanes) continue;
 #pragma unroll
-            for (int i = 0; i < n; ++i) {
-                const float give = lane & o ? v[i] : v[i + n], keep = lane & o ? v[i + n] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-            }
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-        }
+        for (int i = 0; i < kCount; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
-    return v[0];
 }
 
-constexpr int kMostWarps = 16, kMostValues = 8;
-struct TeamSums {   // shared memory of a CTA that is one team
-    float part[2][kMostWarps][kMostValues];
+template <bool kMany>
+__device__ __forceinline__ void team_meet(int which, const Team& m) {
+    if (kMany)
+        team_barrier(which, m.size);
+    else
+        __syncwarp();
+}
+__device__ __forceinline__ void await_copies(int left) {
+    if (left == 0)
+        copies_wait<0>();
+    else if (left == 1)
+        copies_wait<1>();
+    else if (left == 2)
+        copies_wait<2>();
+    else
+        copies_wait<3>();
+}
+
+// The ring of slots: row after row of a team, `ahead` of them on their way.  send(slot)
+// copies the next row, if there is one.  next() is called once a row, by all threads, and
+// gives the slot that holds it.
+template <bool kVec, bool kMany>
+struct Ring {
+    uint8_t* base;   // of the first slot: kVec this thread's places, else the team's part
+    uint32_t size;
+    int ahead, which, i = 0;
+    template <class Send>
+    __device__ __forceinline__ Ring(uint8_t* base, uint32_t size, int ahead, int which, Send send)
+        : base(base), size(size), ahead(ahead), which(which) {
+        for (int a = 0; a < ahead; ++a) {
+            send(smem_addr(base) + a * size);
+            copies_commit();
+        }
+    }
+    template <class Send>
+    __device__ __forceinline__ const uint8_t* next(const Team& m, Send send) {
+        const uint8_t* here = base + i * size;
+        const uint32_t free = smem_addr(base) + (i ? i - 1 : ahead) * size;   // the last row's
+        i = i == ahead ? 0 : i + 1;
+        if (kVec) {
+            send(free);
+            copies_commit();
+            await_copies(ahead);
+        } else if (ahead) {
+            await_copies(ahead - 1);
+            team_meet<kMany>(which, m);   // the whole row is there, and the last one read
+            send(free);
+            copies_commit();
+        } else {
+            team_meet<kMany>(which, m);
+            send(smem_addr(here));
+            copies_commit();
+            await_copies(0);
+            team_meet<kMany>(which, m);
+        }
+        return here;
+    }
 };
 
-// Sums v over the team in a fixed order; every thread gets them.  kCta: one barrier,
-// two buffers in turn (a buffer is written again two sums later, after a barrier that
-// follows its last read).
-template <bool kCta, int kCount>
-__device__ __forceinline__ void team_sums(float (&v)[kCount], TeamSums& s, int& turn, int lanes) {
-    if constexpr (kCta) {
-        const float mine = warp_sums<kCount>(v);
-        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-        if (lane % (32 / kCount) == 0) s.part[turn][warp][lane / (32 / kCount)] = mine;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kCount; ++i) v[i] = 0.0f;
-        for (int w = 0; w < warps; ++w)
-#pragma unroll
-            for (int i = 0; i < kCount; ++i) v[i] += s.part[turn][w][i];
-        turn ^= 1;
-    } else {
-        for (int o = lanes / 2; o; o /= 2)
-#pragma unroll
-            for (int i = 0; i < kCount; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    }
-}
-
-// Rows that a team has in hand at a time.
-template <bool kCta, int kPer>
-constexpr int kRowsOf = kCta ? 4 / kPer : 2;
-
-template <bool kCta>
-__device__ __forceinline__ Team team_of(const NormParams& p, int64_t* index, int64_t* teams) {
-    if (kCta) {
-        *index = blockIdx.x;
-        *teams = gridDim.x;
-        return Team{(int)threadIdx.x, (int)blockDim.x};
-    }
-    const int per = blockDim.x / p.lanes;
-    *index = (int64_t)blockIdx.x * per + threadIdx.x / p.lanes;
-    *teams = (int64_t)gridDim.x * per;
-    return Team{(int)threadIdx.x % p.lanes, p.lanes};
-}
-
 // ---- forward ------------------------------------------------------------------------
-template <bool kF32, bool kVec, int kPer, bool kCta>
-__global__ void __launch_bounds__(kCta ? 512 : 256) norm_kernel(const NormParams p) {
-    __shared__ TeamSums sums;
-    constexpr int kRows = kRowsOf<kCta, kPer>, kSize = kF32 ? 4 : 2;
+// The mean first over the warp's own columns, then the deviations from that number, whose
+// sum corrects it and whose squares give the variance; warps are joined by their counts,
+// means and squares, the means as differences from the first warp's, so that a mean far
+// from the deviations costs no digits: all that is kept of it is one fp32 number `base`
+// and the small distance from there.
+struct WarpStats {
+    float n, base, off, squares;   // columns, a number near their mean, the mean's distance from it, squared deviations
+};
+
+template <bool kF32, bool kVec, int kPer, int kThreads, bool kMany>
+__global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
+    extern __shared__ uint4 slots[];
+    __shared__ WarpStats stats[2][kMostWarps];
+    constexpr int kSize = kF32 ? 4 : 2;
     await_predecessor();
-    int64_t index, teams;
-    const Team m = team_of<kCta>(p, &index, &teams);
-    uint4 gamma[kPer], beta[kPer];
+    int which, teams, turn = 0;
+    const Team m = team_of<kVec, kMany>(p, &which, &teams);
+    const int64_t stride = (int64_t)gridDim.x * teams;
+    // teams of one warp shuffle together: all go on until the first of them has no row
+    const int back = kMany ? 0 : threadIdx.x % 32 / p.lanes;
+    int64_t row = (int64_t)blockIdx.x * teams + which;
+    constexpr int kPlaces = kPer * (kF32 ? 2 : 1);
+    Stream<kF32, kVec, kPer, 16 * kThreads, 0> xs(p.x, p.ldx, p.at[0], row, stride, p.rows, p.cols, m);
+    Stream<kF32, kVec, kPer, 16 * kThreads, kPlaces> rs(p.residual, p.ldr, p.at[1], row, stride, p.rows, p.cols, m);
+    int64_t sent = row;
+    const auto send = [&](uint32_t slot) {
+        if (sent < p.rows) {
+            xs.send(slot, m, p.cols);
+            if (p.residual) rs.send(slot, m, p.cols);
+        }
+        sent += stride;
+    };
+    Ring<kVec, kMany> ring(reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes), p.slot, p.ahead, which, send);
+    char* sum = output<kVec>(p.sum, p.lds, kSize, row, m);
+    char* y = output<kVec>(p.y, p.ldy, p.y_f32 ? 4 : 2, row, m);
+    const int64_t sum_hop = stride * p.lds * kSize, y_hop = stride * p.ldy * (p.y_f32 ? 4 : 2);
+    Words<false> gamma[kPer], beta[kPer];
+    float n = 0.0f;   // this warp's columns, or the team's
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        gamma[j] = weight_piece<kVec>(p.gamma, p.weights_vec, m, j, p.cols, kOnes);
-        beta[j] = weight_piece<kVec>(p.beta, p.weights_vec, m, j, p.cols, 0u);
+        gamma[j] = weight_piece<kVec>(p.gamma, p.weights_vec, m, j, kOnes);
+        beta[j] = weight_piece<kVec>(p.beta, p.weights_vec, m, j, 0u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) n += exists<kVec>(m, j, k) ? 1.0f : 0.0f;
     }
-    const float share = 1.0f / (float)p.cols;
-    int turn = 0;
-    // teams of one warp shuffle together: all go on until the last has no row
-    const int64_t first = kCta ? index : index - threadIdx.x % 32 / p.lanes;
-    for (int64_t at = first * p.take; at < p.rows; at += teams * p.take) {
-        const int64_t row0 = at + (index - first) * p.take;
-        Piece<kF32, kVec> x[kRows][kPer], r[kRows][kPer];
-        const auto has = [&](int i) { return i < p.take && row0 + i < p.rows; };
+    {
+        float t[1] = {n};
+        lane_sums<1>(t, kMany ? 32 : p.lanes);
+        n = t[0];
+    }
+    const float share = n > 0.0f ? 1.0f / n : 0.0f;
+    for (; row - back < p.rows; row += stride, sum += sum_hop, y += y_hop, xs.next_row(), rs.next_row()) {
+        const bool has = kMany || row < p.rows;
+        const uint8_t* slot = ring.next(m, send);
+        float2 h[kPer][4], s2 = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int cols = has(i) ? p.cols : 0;
-                x[i][j].load(static_cast<const char*>(p.x) + (row0 + i) * p.ldx * kSize, m, j, cols);
-                if (p.residual) r[i][j].load(static_cast<const char*>(p.residual) + (row0 + i) * p.ldr * kSize, m, j, cols);
+        for (int j = 0; j < kPer; ++j) {
+            if (!has || !exists<kVec>(m, j, 0)) break;
+            Words<kF32> x = xs.get(slot, m, j);
+            if (p.residual) {
+                x.add(rs.get(slot, m, j));   // as kept, and as the gradient will read it
+                store_words<kVec, kF32>(sum, m, j, x);
             }
-        float h[kRows][kPer][8], mean[kRows];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            mean[i] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                x[i][j].get(h[i][j]);
-                if (p.residual) {
-                    float t[8];
-                    r[i][j].get(t);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        h[i][j][k] += t[k];
-                        if (!kF32) h[i][j][k] = bf16_one(to_bf16(h[i][j][k]));   // as kept, and as the gradient will read it
-                    }
-                    if (has(i)) store_piece<kVec>(static_cast<char*>(p.sum) + (row0 + i) * p.lds * kSize, kF32, m, j, p.cols, h[i][j]);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mean[i] += h[i][j][k];
+            for (int k = 0; k < 4; ++k) {   // an absent column is 0
+                h[j][k] = x.pair(k);
+                s2 = add2(s2, h[j][k]);
             }
         }
-        team_sums<kCta, kRows>(mean, sums, turn, p.lanes);
-        float v[2 * kRows];
+        float s[1] = {s2.x + s2.y};
+        lane_sums<1>(s, kMany ? 32 : p.lanes);
+        const float base = s[0] * share;
+        float2 d1 = both(0.0f), d2 = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            mean[i] *= share;
-            float d1 = 0.0f, d2 = 0.0f;
+        for (int j = 0; j < kPer; ++j) {   // from here on h is the distance from base
+            if (!has || !exists<kVec>(m, j, 0)) break;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float d = column<kVec>(m, j, k) < p.cols ? h[i][j][k] - mean[i] : 0.0f;
-                    h[i][j][k] = d;
-                    d1 += d;
-                    d2 += d * d;
-                }
-            v[2 * i] = d1;
-            v[2 * i + 1] = d2;
+            for (int k = 0; k < 4; ++k) {
+                h[j][k] = add2(h[j][k], both(-base));
+                if (!kVec) h[j][k] = make_float2(exists<kVec>(m, j, 2 * k) ? h[j][k].x : 0.0f, exists<kVec>(m, j, 2 * k + 1) ? h[j][k].y : 0.0f);
+                d1 = add2(d1, h[j][k]);
+                d2 = fma2(h[j][k], h[j][k], d2);
+            }
         }
-        team_sums<kCta, 2 * kRows>(v, sums, turn, p.lanes);
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const float off = v[2 * i] * share;
-            const float rstd = 1.0f / sqrtf(v[2 * i + 1] * share - off * off + p.eps);
-            if (!has(i)) continue;
-            if (m.t == 0) {
-                if (p.mean) p.mean[row0 + i] = mean[i] + off;
-                if (p.rstd) p.rstd[row0 + i] = rstd;
+        float d[2] = {d1.x + d1.y, d2.x + d2.y};
+        lane_sums<2>(d, kMany ? 32 : p.lanes);
+        float middle = base, off = d[0] * share, squares = d[1] - d[0] * off;   // the mean is middle + off
+        if constexpr (kMany) {
+            if ((threadIdx.x & 31) == 0) stats[turn][threadIdx.x / 32] = WarpStats{n, base, off, squares};
+            team_barrier(which, m.size);
+            const WarpStats* w = stats[turn] + which * p.warps;
+            turn ^= 1;   // written again after the next row's barrier
+            middle = w[0].base;
+            off = squares = 0.0f;
+            for (int i = 0; i < p.warps; ++i) off += w[i].n * (w[i].base - middle + w[i].off);
+            off *= 1.0f / (float)p.cols;
+            for (int i = 0; i < p.warps; ++i) {
+                const float t = w[i].base - middle + w[i].off - off;
+                squares += w[i].squares + w[i].n * t * t;
             }
+        }
+        const float rstd = 1.0f / sqrtf(squares * (1.0f / (float)p.cols) + p.eps);
+        if (!has) continue;
+        if (m.t == 0) {
+            if (p.mean) p.mean[row] = middle + off;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        const float2 move = both(base - middle - off), scale = both(rstd);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                float a[8], b[8];
-                unpack8(gamma[j], a);
-                unpack8(beta[j], b);
+        for (int j = 0; j < kPer; ++j) {
+            if (!exists<kVec>(m, j, 0)) break;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) a[k] = (h[i][j][k] - off) * rstd * a[k] + b[k];
-                store_piece<kVec>(static_cast<char*>(p.y) + (row0 + i) * p.ldy * (p.y_f32 ? 4 : 2), p.y_f32, m, j, p.cols, a);
-            }
+            for (int k = 0; k < 4; ++k) h[j][k] = fma2(mul2(add2(h[j][k], move), scale), gamma[j].pair(k), beta[j].pair(k));
+            store_pairs<kVec>(y, p.y_f32, m, j, h[j]);
         }
     }
 }
 
 // ---- backward -----------------------------------------------------------------------
-// Sums of dy xhat and dy by column: in registers, or (kPer 4, which has too few) in
-// shared memory, each thread its own places.
-template <int kPer>
-struct WeightSums {
-    static constexpr bool kShared = kPer > 2;
-    float g[kShared ? 1 : kPer][8], b[kShared ? 1 : kPer][8];
-    float4* at;
-    __device__ __forceinline__ void clear(float4* mine) {
-        at = mine;
-        if constexpr (kShared) {
-#pragma unroll
-            for (int i = 0; i < 4 * kPer; ++i) at[i * blockDim.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) g[j][k] = b[j][k] = 0.0f;
-        }
-    }
-    __device__ __forceinline__ void add(int j, const float (&dg)[8], const float (&db)[8]) {
-        if constexpr (kShared) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float* s = q < 2 ? dg + 4 * q : db + 4 * (q - 2);
-                float4 t = at[(4 * j + q) * blockDim.x];
-                t.x += s[0]; t.y += s[1]; t.z += s[2]; t.w += s[3];
-                at[(4 * j + q) * blockDim.x] = t;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) g[j][k] += dg[k], b[j][k] += db[k];
-        }
-    }
-    __device__ __forceinline__ void get(int j, float (&dg)[8], float (&db)[8]) const {
-        if constexpr (kShared) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 t = at[(4 * j + q) * blockDim.x];
-                float* s = q < 2 ? dg + 4 * q : db + 4 * (q - 2);
-                s[0] = t.x; s[1] = t.y; s[2] = t.z; s[3] = t.w;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) dg[k] = g[j][k], db[k] = b[j][k];
-        }
-    }
-};
-
-template <bool kF32, bool kDyF32, bool kVec, int kPer, bool kCta>
-__global__ void __launch_bounds__(kCta ? 512 : 256) norm_grad_kernel(const NormParams p) {
-    extern __shared__ float4 shared_sums[];
-    __shared__ TeamSums sums;
-    constexpr int kRows = kRowsOf<kCta, kPer>, kSize = kF32 ? 4 : 2, kDySize = kDyF32 ? 4 : 2;
+// Each thread sums dy xhat and dy of its columns down its team's rows, the CTA its teams,
+// a second kernel the CTAs, every time in the same order.
+template <bool kF32, bool kDyF32, bool kVec, int kPer, int kThreads, bool kMany>
+__global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams p) {
+    extern __shared__ uint4 slots[];
+    __shared__ float2 stats[2][kMostWarps];
+    constexpr int kSize = kF32 ? 4 : 2;
     await_predecessor();
-    int64_t index, teams;
-    const Team m = team_of<kCta>(p, &index, &teams);
-    uint4 gamma[kPer];
+    int which, teams, turn = 0;
+    const Team m = team_of<kVec, kMany>(p, &which, &teams);
+    const int64_t stride = (int64_t)gridDim.x * teams;
+    const int back = kMany ? 0 : threadIdx.x % 32 / p.lanes;
+    int64_t row = (int64_t)blockIdx.x * teams + which;
+    constexpr int kXPlaces = kPer * (kF32 ? 2 : 1), kDyPlaces = kPer * (kDyF32 ? 2 : 1);
+    Stream<kF32, kVec, kPer, 16 * kThreads, 0> xs(p.x, p.ldx, p.at[0], row, stride, p.rows, p.cols, m);
+    Stream<kDyF32, kVec, kPer, 16 * kThreads, kXPlaces> ds(p.dy, p.lddy, p.at[1], row, stride, p.rows, p.cols, m);
+    Stream<kF32, kVec, kPer, 16 * kThreads, kXPlaces + kDyPlaces> rs(p.residual, p.ldr, p.at[2], row, stride, p.rows, p.cols, m);
+    int64_t sent = row;
+    const auto send = [&](uint32_t slot) {
+        if (sent < p.rows) {
+            xs.send(slot, m, p.cols);
+            ds.send(slot, m, p.cols);
+            if (p.residual) rs.send(slot, m, p.cols);
+        }
+        sent += stride;
+    };
+    Ring<kVec, kMany> ring(reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes), p.slot, p.ahead, which, send);
+    char* dx = output<kVec>(p.y, p.ldy, kSize, row, m);
+    const int64_t dx_hop = stride * p.ldy * kSize;
+    Words<false> gamma[kPer];
+    float2 sum_g[kPer][4], sum_b[kPer][4];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) gamma[j] = weight_piece<kVec>(p.gamma, p.weights_vec, m, j, p.cols, kOnes);
-    WeightSums<kPer> acc;
-    acc.clear(shared_sums + threadIdx.x);
+    for (int j = 0; j < kPer; ++j) {
+        gamma[j] = weight_piece<kVec>(p.gamma, p.weights_vec, m, j, kOnes);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum_g[j][k] = sum_b[j][k] = both(0.0f);
+    }
     const float share = 1.0f / (float)p.cols;
-    int turn = 0;
-    const int64_t first = kCta ? index : index - threadIdx.x % 32 / p.lanes;
-    for (int64_t at = first * p.take; at < p.rows; at += teams * p.take) {
-        const int64_t row0 = at + (index - first) * p.take;
-        Piece<kF32, kVec> x[kRows][kPer];
-        Piece<kDyF32, kVec> dy[kRows][kPer];
-        float mean[kRows], rstd[kRows];
-        const auto has = [&](int i) { return i < p.take && row0 + i < p.rows; };
+    for (; row - back < p.rows; row += stride, dx += dx_hop, xs.next_row(), ds.next_row(), rs.next_row()) {
+        const bool has = kMany || row < p.rows;
+        const float mean = has ? p.mean[row] : 0.0f, rstd = has ? p.rstd[row] : 0.0f;
+        const uint8_t* slot = ring.next(m, send);
+        const float2 move = both(-mean), scale = both(rstd);
+        float2 v1 = both(0.0f), v2 = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            mean[i] = has(i) ? p.mean[row0 + i] : 0.0f;
-            rstd[i] = has(i) ? p.rstd[row0 + i] : 0.0f;
+        for (int j = 0; j < kPer; ++j) {
+            if (!has || !exists<kVec>(m, j, 0)) break;
+            const Words<kF32> x = xs.get(slot, m, j);
+            const Words<kDyF32> dy = ds.get(slot, m, j);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int cols = has(i) ? p.cols : 0;
-                x[i][j].load(static_cast<const char*>(p.x) + (row0 + i) * p.ldx * kSize, m, j, cols);
-                dy[i][j].load(static_cast<const char*>(p.dy) + (row0 + i) * p.lddy * kDySize, m, j, cols);
+            for (int k = 0; k < 4; ++k) {   // an absent column has dy = 0
+                const float2 g = mul2(dy.pair(k), gamma[j].pair(k));
+                v1 = add2(v1, g);
+                v2 = fma2(g, mul2(add2(x.pair(k), move), scale), v2);
             }
         }
-        float v[2 * kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                float a[8], d[8], w[8];
-                x[i][j].get(a);
-                dy[i][j].get(d);
-                unpack8(gamma[j], w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {   // an absent column has dy = 0 and a finite xhat
-                    const float g = d[k] * w[k];
-                    s1 += g;
-                    s2 += g * ((a[k] - mean[i]) * rstd[i]);
-                }
-            }
-            v[2 * i] = s1;
-            v[2 * i + 1] = s2;
+        float v[2] = {v1.x + v1.y, v2.x + v2.y};
+        lane_sums<2>(v, kMany ? 32 : p.lanes);
+        if constexpr (kMany) {
+            if ((threadIdx.x & 31) == 0) stats[turn][threadIdx.x / 32] = make_float2(v[0], v[1]);
+            team_barrier(which, m.size);
+            const float2* w = stats[turn] + which * p.warps;
+            turn ^= 1;   // written again after the next row's barrier
+            v[0] = v[1] = 0.0f;
+            for (int i = 0; i < p.warps; ++i) v[0] += w[i].x, v[1] += w[i].y;
         }
-        team_sums<kCta, 2 * kRows>(v, sums, turn, p.lanes);
+        if (!has) continue;
+        const float2 m1 = both(-v[0] * share), m2 = both(-v[1] * share);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (!has(i)) continue;
-            const float m1 = v[2 * i] * share, m2 = v[2 * i + 1] * share;
+        for (int j = 0; j < kPer; ++j) {
+            if (!exists<kVec>(m, j, 0)) break;
+            const Words<kF32> x = xs.get(slot, m, j);
+            const Words<kDyF32> dy = ds.get(slot, m, j);
+            float2 out[4];
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                float a[8], d[8], w[8];
-                x[i][j].get(a);
-                dy[i][j].get(d);
-                unpack8(gamma[j], w);
-                float out[8], dg[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float xhat = (a[k] - mean[i]) * rstd[i];
-                    out[k] = rstd[i] * (d[k] * w[k] - m1 - xhat * m2);
-                    dg[k] = d[k] * xhat;
-                }
-                if (p.part) acc.add(j, dg, d);
-                if (p.residual) {
-                    Piece<kF32, kVec> r;
-                    r.load(static_cast<const char*>(p.residual) + (row0 + i) * p.ldr * kSize, m, j, p.cols);
-                    r.get(a);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) out[k] += a[k];
-                }
-                store_piece<kVec>(static_cast<char*>(p.y) + (row0 + i) * p.ldy * kSize, kF32, m, j, p.cols, out);
+            for (int k = 0; k < 4; ++k) {
+                const float2 d = dy.pair(k), xhat = mul2(add2(x.pair(k), move), scale);
+                out[k] = mul2(fma2(xhat, m2, fma2(d, gamma[j].pair(k), m1)), scale);
+                sum_g[j][k] = fma2(d, xhat, sum_g[j][k]);
+                sum_b[j][k] = add2(sum_b[j][k], d);
             }
+            if (p.residual) {
+                const Words<kF32> r = rs.get(slot, m, j);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) out[k] = add2(out[k], r.pair(k));
+            }
+            store_pairs<kVec>(dx, kF32, m, j, out);
         }
     }
     if (!p.part) return;
+    // the teams' sums to shared memory, 8 kPer floats a thread, and in order to the parts
+    float* all = reinterpret_cast<float*>(slots);
+    const int width = 8 * kPer * m.size;
     float* part = p.part + (int64_t)blockIdx.x * p.cols;
     const int64_t half = (int64_t)gridDim.x * p.cols;
-    if constexpr (kCta) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            float dg[8], db[8];
-            acc.get(j, dg, db);
-            if constexpr (kVec) {
-                if (column<true>(m, j, 0) < p.cols) {
-                    store8(part + column<true>(m, j, 0), true, dg);
-                    store8(part + half + column<true>(m, j, 0), true, db);
+    for (int h = 0; h < 2; ++h) {
+        __syncthreads();   // the rows, or the first half, have been read
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 v = h ? sum_b[j][k] : sum_g[j][k];
+                float* q = all + which * width;
+                if constexpr (kVec) {
+                    // two floats at a time, the pairs of a piece `size` apart: no two lanes share a bank
+                    *reinterpret_cast<float2*>(q + 2 * (m.t + m.size * (4 * j + k))) = v;
+                } else {
+                    q[column<false>(m, j, 2 * k)] = v.x;
+                    q[column<false>(m, j, 2 * k + 1)] = v.y;
                 }
+            }
+        __syncthreads();
+        // the pairs (or columns) of thread m.t of a team, shared out to the teams
+        for (int i = which; i < (kVec ? 4 : 8) * kPer; i += teams) {
+            const int c = kVec ? 8 * (m.t + m.size * (i / 4)) + 2 * (i % 4) : m.t + m.size * i;
+            if (c >= p.cols) break;
+            if constexpr (kVec) {
+                float2 s = both(0.0f);
+                for (int t = 0; t < teams; ++t) s = add2(s, *reinterpret_cast<const float2*>(all + t * width + 2 * (m.t + m.size * i)));
+                *reinterpret_cast<float2*>(part + h * half + c) = s;
             } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (column<false>(m, j, k) < p.cols) {
-                        part[column<false>(m, j, k)] = dg[k];
-                        part[half + column<false>(m, j, k)] = db[k];
-                    }
-            }
-        }
-    } else {
-        // the CTA's teams in order; a team of l lanes has 8 kPer l columns, so that
-        // the teams' sums fill 8 kPer floats a thread
-        float* all = reinterpret_cast<float*>(shared_sums);
-        const int width = 8 * kPer * p.lanes, n = blockDim.x / p.lanes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                float dg[8], db[8];
-                acc.get(j, dg, db);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) all[(int)threadIdx.x / p.lanes * width + column<kVec>(m, j, k)] = h ? db[k] : dg[k];
-            }
-            __syncthreads();
-            for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
                 float s = 0.0f;
-                for (int i = 0; i < n; ++i) s += all[i * width + c];
+                for (int t = 0; t < teams; ++t) s += all[t * width + c];
                 part[h * half + c] = s;
             }
         }
@@ -448,6 +568,25 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) norm_grad_kernel(const NormP
 // ---- rows of more than 16384 columns ---------------------------------------------------
 // A CTA a row, in three passes (two backward) over it, the later ones out of L2.
 constexpr int kWideThreads = 512;
+
+// Sums over the CTA in a fixed order, to every thread: one barrier, two buffers in turn.
+struct CtaSums {
+    float part[2][kWideThreads / 32][2];
+};
+template <int kCount>
+__device__ __forceinline__ void cta_sums(float (&v)[kCount], CtaSums& s, int& turn) {
+    lane_sums<kCount>(v, 32);
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) s.part[turn][threadIdx.x / 32][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+        v[i] = 0.0f;
+        for (int w = 0; w < kWideThreads / 32; ++w) v[i] += s.part[turn][w][i];
+    }
+    turn ^= 1;
+}
 
 template <bool kF32>
 __device__ __forceinline__ float value(const void* p, int64_t i) {
@@ -465,7 +604,7 @@ __device__ __forceinline__ void put(void* p, bool f32, int64_t i, float v) {
 
 template <bool kF32>
 __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormParams p) {
-    __shared__ TeamSums sums;
+    __shared__ CtaSums sums;
     await_predecessor();
     const float share = 1.0f / (float)p.cols;
     int turn = 0;
@@ -480,7 +619,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormParam
             }
             m[0] += h;
         }
-        team_sums<true, 1>(m, sums, turn, 0);
+        cta_sums<1>(m, sums, turn);
         const float mean = m[0] * share;
         const void* from = p.residual ? p.sum : p.x;   // a thread's own writes
         const int64_t ld = p.residual ? p.lds : p.ldx;
@@ -490,7 +629,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormParam
             v[0] += d;
             v[1] += d * d;
         }
-        team_sums<true, 2>(v, sums, turn, 0);
+        cta_sums<2>(v, sums, turn);
         const float off = v[0] * share, rstd = 1.0f / sqrtf(v[1] * share - off * off + p.eps);
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[row] = mean + off;
@@ -506,7 +645,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormParam
 
 template <bool kF32, bool kDyF32>
 __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const NormParams p) {
-    __shared__ TeamSums sums;
+    __shared__ CtaSums sums;
     await_predecessor();
     const float share = 1.0f / (float)p.cols;
     int turn = 0;
@@ -518,7 +657,7 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(const Norm
             v[0] += g;
             v[1] += g * ((value<kF32>(p.x, row * p.ldx + c) - mean) * rstd);
         }
-        team_sums<true, 2>(v, sums, turn, 0);
+        cta_sums<2>(v, sums, turn);
         const float m1 = v[0] * share, m2 = v[1] * share;
         for (int c = threadIdx.x; c < p.cols; c += kWideThreads) {
             const float g = value<kDyF32>(p.dy, row * p.lddy + c) * (p.gamma ? bf16_one(p.gamma[c]) : 1.0f);
@@ -559,59 +698,57 @@ struct FinishParams {
 __global__ void __launch_bounds__(32 * kFinishWarps) norm_finish_kernel(const FinishParams p) {
     __shared__ float s[kFinishWarps][32];
     await_predecessor();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, which = blockIdx.y;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int c = blockIdx.x * 32 + lane;
+    void* out = blockIdx.y ? p.out[1] : p.out[0];
+    const void* acc = blockIdx.y ? p.acc[1] : p.acc[0];
+    if (!out) return;
     float v = 0.0f;
-    if (p.out[which]) {
-        const float* q = p.part + (int64_t)which * p.parts * p.cols + c;
-        if (c < p.cols)
-#pragma unroll 8
-            for (int i = warp; i < p.parts; i += kFinishWarps) v += q[(int64_t)i * p.cols];
-        s[warp][lane] = v;
+    if (c < p.cols) {
+        const float* q = p.part + (int64_t)blockIdx.y * p.parts * p.cols + c;
+#pragma unroll 10
+        for (int i = warp; i < p.parts; i += kFinishWarps) v += q[(int64_t)i * p.cols];
     }
+    s[warp][lane] = v;
     __syncthreads();
-    if (warp || c >= p.cols || !p.out[which]) return;
+    if (warp || c >= p.cols) return;
     for (int w = 1; w < kFinishWarps; ++w) v += s[w][lane];
     if (p.f32) {
-        if (p.acc[which]) v += static_cast<const float*>(p.acc[which])[c];
-        static_cast<float*>(p.out[which])[c] = v;
+        if (acc) v += static_cast<const float*>(acc)[c];
+        static_cast<float*>(out)[c] = v;
     } else {
-        if (p.acc[which]) v += bf16_one(static_cast<const uint16_t*>(p.acc[which])[c]);
-        static_cast<uint16_t*>(p.out[which])[c] = to_bf16(v);
+        if (acc) v += bf16_one(static_cast<const uint16_t*>(acc)[c]);
+        static_cast<uint16_t*>(out)[c] = to_bf16(v);
     }
 }
 
 // ---- launches ---------------------------------------------------------------------------
 constexpr int kWidestNorm = 16384;
 
-// How a matrix is shared out: lanes of a warp (32 at most) or a CTA of `threads` to a
-// row, pieces a thread, rows at a time, CTAs.
+// How a matrix is shared out: lanes of a warp or warps to a row, pieces a thread, threads
+// of a CTA (one an SM), CTAs: no more teams to a CTA than give every SM some.
 struct NormShape {
-    bool cta;
-    int lanes, per, threads, take;
-    int64_t grid;
+    bool many;
+    int lanes, warps, per, threads, most;   // most: threads that the kernel is made for
+    int64_t teams, grid;   // teams of a CTA
 };
 static NormShape norm_shape(int64_t rows, int64_t cols) {
     NormShape s{};
     const int64_t groups = (cols + 7) / 8, sms = sm_count();
-    s.cta = groups > 64;
-    if (s.cta) {
-        s.per = groups <= 512 ? 1 : groups <= 1024 ? 2 : 4;
-        s.threads = (int)((groups + s.per * 32 - 1) / (s.per * 32) * 32);
-        s.lanes = 32;
-    } else {
-        s.per = groups <= 32 ? 1 : 2;
-        s.threads = 256;
-        s.lanes = 1;
-        while (s.lanes * s.per < groups) s.lanes *= 2;
-    }
-    // CTAs that are resident together, and no more rows at a time than give each a pass
-    const int64_t resident = sms * (s.cta ? (s.threads <= 128 ? 4 : s.threads <= 256 ? 2 : 1) : 2);
-    const int most = s.cta ? 4 / s.per : 2, teams = s.cta ? 1 : s.threads / s.lanes;
-    int64_t take = (rows + resident * teams - 1) / (resident * teams);
-    s.take = (int)(take < 1 ? 1 : take > most ? most : take);
-    s.grid = (rows + (int64_t)s.take * teams - 1) / ((int64_t)s.take * teams);
-    if (s.grid > resident) s.grid = resident;
+    s.many = groups > 128;
+    s.per = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
+    s.warps = s.many ? (int)((groups + 127) / 128) : 1;
+    s.lanes = 1;
+    while (!s.many && s.lanes < 32 && s.lanes * s.per < groups) s.lanes *= 2;
+    // 12 warps with registers to spare; the widest rows need 16, of 128 registers a thread
+    s.most = s.warps > 12 ? 512 : 384;
+    const int64_t in_warp = s.many ? 1 : 32 / s.lanes, most = s.many ? s.most / 32 / s.warps : s.most / 32 * in_warp;
+    int64_t teams = (rows + sms - 1) / sms;
+    teams = (teams + in_warp - 1) / in_warp * in_warp;   // whole warps
+    s.teams = teams > most ? most : teams;
+    s.threads = (int)(s.many ? s.teams * s.warps * 32 : s.teams / in_warp * 32);
+    s.grid = (rows + s.teams - 1) / s.teams;
+    if (s.grid > sms) s.grid = sms;
     return s;
 }
 // Parts that the weights' gradients are summed in.
@@ -621,30 +758,72 @@ static int64_t norm_parts(int64_t rows, int64_t cols) {
     return norm_shape(rows, cols).grid;
 }
 
+// Lays out the slots for a row of up to three streams (sizes of an element, 0 where
+// absent) and as many rows ahead, at most three, as shared memory holds; its bytes.
+constexpr int kNormSharedMemory = 226 * 1024;
+static int lay_slots(NormParams& p, const NormShape& s, bool vec, const int (&sizes)[3]) {
+    uint32_t at = 0, places = 0;
+    for (int i = 0; i < 3; ++i) {
+        p.at[i] = at;
+        places += s.per * sizes[i] / 2;
+        if (sizes[i]) at += (uint32_t)((p.cols * sizes[i] + 15) / 16 * 16 + 16);
+    }
+    p.part_bytes = vec ? 16 : at;
+    p.slot = vec ? places * 16 * s.most : at * (uint32_t)s.teams;
+    const int64_t own = (p.rows + s.grid * s.teams - 1) / (s.grid * s.teams);   // rows of a team
+    p.ahead = (int32_t)(kNormSharedMemory / p.slot) - 1;
+    if (p.ahead > 3) p.ahead = 3;
+    if (p.ahead >= own) p.ahead = (int32_t)own - 1;
+    return (int)p.slot * (p.ahead + 1);
+}
+
+// Has a kernel run with an SM's memory split as its neighbours have it, most of it shared:
+// a change of the split between two kernels waits for the SM to be empty.
+static int keep_split(const void* kernel, Done& done) {
+    int dev = 0;
+    if (!device_below(64, &dev)) return ZERO_ECUDA;
+    if (done[dev].load(std::memory_order_acquire)) return ZERO_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) {
+        note_cuda_error(e);
+        (void)cudaGetLastError();
+        return ZERO_ECUDA;
+    }
+    done[dev].store(true, std::memory_order_release);
+    return ZERO_OK;
+}
+
+template <bool kF32, bool kVec, int kPer, int kThreads, bool kMany>
+static int launch_norm(NormParams& p, const NormShape& s, cudaStream_t stream) {
+    static Done done;
+    void (*const kernel)(NormParams) = norm_kernel<kF32, kVec, kPer, kThreads, kMany>;
+    const int size = kF32 ? 4 : 2, smem = lay_slots(p, s, kVec, {size, p.residual ? size : 0, 0});
+    if (smem > 46 * 1024)
+        if (const int rc = allow_smem((const void*)kernel, kNormSharedMemory, done)) return rc;
+    return launch_dense(kernel, dim3((unsigned)s.grid), s.threads, 1, true, smem, stream, p);
+}
+template <bool kF32, bool kDyF32, bool kVec, int kPer, int kThreads, bool kMany>
+static int launch_norm_grad(NormParams& p, const NormShape& s, cudaStream_t stream) {
+    static Done done;
+    void (*const kernel)(NormParams) = norm_grad_kernel<kF32, kDyF32, kVec, kPer, kThreads, kMany>;
+    const int size = kF32 ? 4 : 2, sums = p.part ? kPer * 32 * s.threads : 0;   // the teams' sums, after the last row
+    int smem = lay_slots(p, s, kVec, {size, kDyF32 ? 4 : 2, p.residual ? size : 0});
+    if (smem < sums) smem = sums;
+    if (smem > 46 * 1024)
+        if (const int rc = allow_smem((const void*)kernel, kNormSharedMemory, done)) return rc;
+    return launch_dense(kernel, dim3((unsigned)s.grid), s.threads, 1, true, smem, stream, p);
+}
 template <bool kF32, bool kVec>
-static int launch_norm(const NormParams& p, const NormShape& s, cudaStream_t stream) {
-    void (*kernel)(NormParams) = !s.cta ? (s.per == 1 ? norm_kernel<kF32, kVec, 1, false> : norm_kernel<kF32, kVec, 2, false>)
-                                 : s.per == 1 ? norm_kernel<kF32, kVec, 1, true>
-                                 : s.per == 2 ? norm_kernel<kF32, kVec, 2, true>
-                                              : norm_kernel<kF32, kVec, 4, true>;
-    return launch_dense(kernel, dim3((unsigned)s.grid), s.threads, 1, true, 0, stream, p);
+static int launch_norm(NormParams& p, const NormShape& s, cudaStream_t stream) {
+    if (s.many) return s.most > 384 ? launch_norm<kF32, kVec, 4, 512, true>(p, s, stream) : launch_norm<kF32, kVec, 4, 384, true>(p, s, stream);
+    return s.per == 1 ? launch_norm<kF32, kVec, 1, 384, false>(p, s, stream)
+           : s.per == 2 ? launch_norm<kF32, kVec, 2, 384, false>(p, s, stream) : launch_norm<kF32, kVec, 4, 384, false>(p, s, stream);
 }
 template <bool kF32, bool kDyF32, bool kVec>
-static int launch_norm_grad(const NormParams& p, const NormShape& s, cudaStream_t stream) {
-    void (*kernel)(NormParams) = !s.cta ? (s.per == 1 ? norm_grad_kernel<kF32, kDyF32, kVec, 1, false> : norm_grad_kernel<kF32, kDyF32, kVec, 2, false>)
-                                 : s.per == 1 ? norm_grad_kernel<kF32, kDyF32, kVec, 1, true>
-                                 : s.per == 2 ? norm_grad_kernel<kF32, kDyF32, kVec, 2, true>
-                                              : norm_grad_kernel<kF32, kDyF32, kVec, 4, true>;
-    const int smem = s.cta ? (s.per > 2 ? s.per * 64 * s.threads : 0) : s.per * 32 * s.threads;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) {
-            note_cuda_error(e);
-            (void)cudaGetLastError();
-            return ZERO_ECUDA;
-        }
-    }
-    return launch_dense(kernel, dim3((unsigned)s.grid), s.threads, 1, true, smem, stream, p);
+static int launch_norm_grad(NormParams& p, const NormShape& s, cudaStream_t stream) {
+    if (s.many) return s.most > 384 ? launch_norm_grad<kF32, kDyF32, kVec, 4, 512, true>(p, s, stream) : launch_norm_grad<kF32, kDyF32, kVec, 4, 384, true>(p, s, stream);
+    return s.per == 1 ? launch_norm_grad<kF32, kDyF32, kVec, 1, 384, false>(p, s, stream)
+           : s.per == 2 ? launch_norm_grad<kF32, kDyF32, kVec, 2, 384, false>(p, s, stream) : launch_norm_grad<kF32, kDyF32, kVec, 4, 384, false>(p, s, stream);
 }
 
 static bool dtype_ok(int32_t d) { return d == ZERO_BF16 || d == ZERO_F32; }
@@ -687,7 +866,7 @@ extern "C" int zero_layer_norm(int64_t rows, int64_t cols, const void* x, int64_
     const bool vec = cols % 8 == 0 && rows_aligned16(x, ldx, size) && rows_aligned16(y, ldy, dtype_size(y_dtype)) &&
                      (!residual || (rows_aligned16(residual, ldr, size) && rows_aligned16(sum, lds, size)));
     const NormShape shape = norm_shape(rows, cols);
-    p.lanes = shape.lanes; p.take = shape.take;
+    p.lanes = shape.lanes; p.warps = shape.warps;
     if (dtype == ZERO_F32) return vec ? launch_norm<true, true>(p, shape, s) : launch_norm<true, false>(p, shape, s);
     return vec ? launch_norm<false, true>(p, shape, s) : launch_norm<false, false>(p, shape, s);
 }
@@ -758,7 +937,7 @@ extern "C" int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, 
         const bool vec = cols % 8 == 0 && rows_aligned16(x, ldx, size) && rows_aligned16(dy, lddy, dtype_size(dy_dtype)) &&
                          rows_aligned16(dx, lddx, size) && (!residual || rows_aligned16(residual, ldr, size));
         const NormShape shape = norm_shape(rows, cols);
-        p.lanes = shape.lanes; p.take = shape.take;
+        p.lanes = shape.lanes; p.warps = shape.warps;
         if (!f32)
             rc = vec ? launch_norm_grad<false, false, true>(p, shape, s) : launch_norm_grad<false, false, false>(p, shape, s);
         else if (dy_f32)
@@ -767,6 +946,8 @@ extern "C" int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, 
             rc = vec ? launch_norm_grad<true, false, true>(p, shape, s) : launch_norm_grad<true, false, false>(p, shape, s);
     }
     if (rc != ZERO_OK || !weights) return rc;
+    static Done split;
+    if (const int kept = keep_split((const void*)norm_finish_kernel, split)) return kept;
     FinishParams q{};
     q.part = p.part; q.parts = (int32_t)parts; q.cols = (int32_t)cols;
     q.acc[0] = dgamma_acc; q.acc[1] = dbeta_acc;

@@ -714,13 +714,6 @@ constexpr int kSoftSmem = 1024 + kStageBytes + 2 * (256 * 144) + 128;
 // would reach past the operand's own memory its elements come one by one.
 constexpr int kRawPitch = 144, kRawBytes = 256 * kRawPitch;   // 128 rows of A, 128 of B
 
-__device__ __forceinline__ void copy_block(uint32_t dst, uintptr_t src, bool want) {   // zeros where not wanted
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(want ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
-
 __device__ __noinline__ void fetch_block(uint32_t dst, uintptr_t at, uintptr_t begin, uintptr_t end) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll

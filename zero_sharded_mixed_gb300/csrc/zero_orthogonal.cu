@@ -87,25 +87,24 @@ __device__ __forceinline__ void source8(const SourceParams& p, int64_t at, int n
 
 // The sum over the CTA in a fixed order, to every thread.
 __device__ __forceinline__ double block_sum(double v) {
-    __shared__ double part[kSourceThreads / 32];
+    __shared__ double part[32];
     for (int o = 16; o; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
     v = 0.0;
-    for (int w = 0; w < kSourceThreads / 32; ++w) v += part[w];
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) v += part[w];
     return v;
 }
 
-// Squares are summed in fp32 by a thread where none can leave fp32's range, else in
-// fp64, and in fp64 over the threads.
-__global__ void __launch_bounds__(kSourceThreads) orthogonal_norm_kernel(const SourceParams p) {
-    await_predecessor();
-    const int64_t from = (int64_t)blockIdx.y * p.stride;
+// The sum of squares of every `share`-th group of eight from `first`, a thread's own:
+// in fp32 where none can leave fp32's range, else in fp64, and in fp64 over the threads.
+__device__ __forceinline__ double squares(const SourceParams& p, int z, uint32_t first, uint32_t share) {
+    const int64_t from = (int64_t)z * p.stride;
     float sum = 0.0f;
     double far = 0.0;
     const uint32_t all = (uint32_t)p.rows * (uint32_t)p.groups;
-    for (uint32_t g = blockIdx.x * kSourceThreads + threadIdx.x; g < all; g += gridDim.x * kSourceThreads) {
+    for (uint32_t g = first; g < all; g += share) {
         const uint32_t row = g / (uint32_t)p.groups, c = (g - row * (uint32_t)p.groups) * 8;
         float v[8], most = 0.0f, s = 0.0f;
         source8(p, from + (int64_t)row * p.ldx + c, p.cols - (int)c, v);
@@ -121,26 +120,28 @@ __global__ void __launch_bounds__(kSourceThreads) orthogonal_norm_kernel(const S
             for (int k = 0; k < 8; ++k) far += (double)v[k] * (double)v[k];
         }
     }
-    const double t = block_sum((double)sum + far);
-    if (threadIdx.x == 0) p.norm[(int64_t)blockIdx.y * p.parts + blockIdx.x] = t;
+    return (double)sum + far;
 }
 
 // hi + lo / 2^11 = x 2^(12 - e) with e the norm's exponent, and scale = 2^e / norm: the
 // power of two costs a bf16 x no bit, and the first step's products take in the scale.
-__global__ void __launch_bounds__(kSourceThreads) orthogonal_source_kernel(const SourceParams p) {
-    await_predecessor();
-    double t = 0.0;
-    for (int i = threadIdx.x; i < p.parts; i += kSourceThreads) t += p.norm[(int64_t)blockIdx.y * p.parts + i];
-    const double norm = sqrt(block_sum(t)) + (double)p.eps;
+// One thread forms them (fp64 is slow: by all threads of a CTA it took 8 us).
+struct SourceScale {
+    float f1, f2, scale;   // f1 f2 = 2^(12 - e), in two parts for want of range
+};
+__device__ __noinline__ SourceScale source_scale(double sum, float eps) {
+    const double norm = sqrt(sum) + (double)eps;
     int e = 0;
     const double f = norm > 0.0 && norm < INFINITY ? frexp(norm, &e) : norm;
-    if (blockIdx.x == 0 && threadIdx.x == 0)   // of zeros, zeros; of what is not finite, NaN
-        p.scale[blockIdx.y] = norm == 0.0 ? 0.0f : norm < INFINITY ? (float)(1.0 / f) : NAN;
     const int k = 12 - e;
-    const float f1 = ldexpf(1.0f, k / 2), f2 = ldexpf(1.0f, k - k / 2);
-    const int64_t from = (int64_t)blockIdx.y * p.stride, to = (int64_t)blockIdx.y * p.to;
+    // of zeros, zeros; of what is not finite, NaN
+    return SourceScale{ldexpf(1.0f, k / 2), ldexpf(1.0f, k - k / 2), norm == 0.0 ? 0.0f : norm < INFINITY ? (float)(1.0 / f) : NAN};
+}
+__device__ __forceinline__ void parts_of(const SourceParams& p, int z, const SourceScale& s, uint32_t first, uint32_t share) {
+    const float f1 = s.f1, f2 = s.f2;
+    const int64_t from = (int64_t)z * p.stride, to = (int64_t)z * p.to;
     const uint32_t all = (uint32_t)p.rows * (uint32_t)p.groups;
-    for (uint32_t g = blockIdx.x * kSourceThreads + threadIdx.x; g < all; g += gridDim.x * kSourceThreads) {
+    for (uint32_t g = first; g < all; g += share) {
         const uint32_t row = g / (uint32_t)p.groups, c = (g - row * (uint32_t)p.groups) * 8;
         float v[8], r[8];
         source8(p, from + (int64_t)row * p.ldx + c, p.cols - (int)c, v);
@@ -156,21 +157,37 @@ __global__ void __launch_bounds__(kSourceThreads) orthogonal_source_kernel(const
     }
 }
 
+__global__ void __launch_bounds__(kSourceThreads) orthogonal_norm_kernel(const SourceParams p) {
+    await_predecessor();
+    const double t = block_sum(squares(p, blockIdx.y, blockIdx.x * kSourceThreads + threadIdx.x, gridDim.x * kSourceThreads));
+    if (threadIdx.x == 0) p.norm[(int64_t)blockIdx.y * p.parts + blockIdx.x] = t;
+}
+
+__global__ void __launch_bounds__(kSourceThreads) orthogonal_source_kernel(const SourceParams p) {
+    await_predecessor();
+    __shared__ SourceScale scale;
+    double t = 0.0;
+    for (int i = threadIdx.x; i < p.parts; i += kSourceThreads) t += p.norm[(int64_t)blockIdx.y * p.parts + i];
+    t = block_sum(t);
+    if (threadIdx.x == 0) {
+        scale = source_scale(t, p.eps);
+        if (blockIdx.x == 0) p.scale[blockIdx.y] = scale.scale;
+    }
+    __syncthreads();
+    parts_of(p, blockIdx.y, scale, blockIdx.x * kSourceThreads + threadIdx.x, gridDim.x * kSourceThreads);
+}
+
 // ---- products --------------------------------------------------------------------------------
 // Pairs of CTAs on 256 x bn tiles, as for the large dense products: warp 0 copies, warp 1
 // of the even CTA issues, warps 4..19 end the last tile meanwhile.  A symmetric result is
 // computed for the tiles that reach below its diagonal and written to both sides.
 enum Step { kGram, kSquare, kApply };
 
-struct StepParams {
-    CUtensorMap map_a, map_b;
-    int32_t rows, cols, depth;             // of the result, and the reduced dimension
-    int32_t tiles_n, tiles, all;           // column tiles; tiles a matrix, and of the batch
-    int32_t bn, k_blocks;
-    bool a_mn, b_mn;
+// What the end of a step reads and writes.
+struct StepEnding {
+    int32_t rows, cols;                    // of the result
     bool first, tall;                      // first: X = scale * hi
-    // what the end reads and writes: ld and stride a matrix, of all of them
-    int64_t ld, stride;
+    int64_t ld, stride;                    // rows of a matrix, and matrices, of all of c and d
     const uint16_t* c_hi;                  // kSquare: A; kApply: X
     const uint16_t* c_lo;                  // or null
     uint16_t* d_hi;                        // A, B or the next X
@@ -180,6 +197,14 @@ struct StepParams {
     float2* factors; int64_t factor_stride;   // a + B_ii - fp16(B_ii), a + B_ii
     const float* scale;
     float a, b, c;
+};
+struct StepParams {
+    CUtensorMap map_a, map_b;
+    int32_t depth;                         // the reduced dimension
+    int32_t tiles_n, tiles, all;           // column tiles; tiles a matrix, and of the batch
+    int32_t bn, k_blocks;
+    bool a_mn, b_mn;
+    StepEnding e;
 };
 
 constexpr int kStageBytes = 32768;      // 128 rows of A and 128 of B, 64 reduced elements each
@@ -211,7 +236,7 @@ __device__ __forceinline__ Place place_of(const StepParams& p, int t) {
     return w;
 }
 __device__ __forceinline__ int width_of(const StepParams& p, int tn) {   // columns of the tile, up to a multiple of 32
-    const int left = p.cols - tn * p.bn;
+    const int left = p.e.cols - tn * p.bn;
     return left >= p.bn ? p.bn : (left + 31) / 32 * 32;
 }
 
@@ -230,19 +255,19 @@ struct StepEnd {
     uint4 hi[2], lo[2];
     float2 f[2];
     float s;
-    __device__ __forceinline__ void load(const StepParams& p, const Place& w, int row0, int col0) {
+    __device__ __forceinline__ void load(const StepEnding& p, int z, int row0, int col0) {
         const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
-        s = p.first ? p.scale[w.z] : 1.0f;
+        s = p.first ? p.scale[z] : 1.0f;
         if constexpr (kStep != kGram) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int row = row0 + i + 8 * h;
-                const int64_t at = w.z * p.stride + row * p.ld + col0 + 8 * j;
+                const int64_t at = z * p.stride + row * p.ld + col0 + 8 * j;
                 hi[h] = lo[h] = make_uint4(0u, 0u, 0u, 0u);
                 if (row < p.rows) {
                     hi[h] = *reinterpret_cast<const uint4*>(p.c_hi + at);
                     if (kStep == kApply && p.c_lo) lo[h] = *reinterpret_cast<const uint4*>(p.c_lo + at);
-                    if (kStep == kApply && !p.tall) f[h] = p.factors[w.z * p.factor_stride + row];
+                    if (kStep == kApply && !p.tall) f[h] = p.factors[z * p.factor_stride + row];
                 }
             }
         }
@@ -254,7 +279,7 @@ struct StepEnd {
         if (i < rows_left) *reinterpret_cast<uint4*>(q + i * ld + 8 * j) = make_uint4(a[0], a[1], a[2], a[3]);
         if (i + 8 < rows_left) *reinterpret_cast<uint4*>(q + (i + 8) * ld + 8 * j) = make_uint4(b[0], b[1], b[2], b[3]);
     }
-    __device__ __forceinline__ void finish(const StepParams& p, const Place& w, int row0, int col0, bool mirror, float (&v)[4][4]) {
+    __device__ __forceinline__ void finish(const StepEnding& p, int z, int row0, int col0, bool mirror, float (&v)[4][4]) {
         const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
         if constexpr (kStep == kGram) {
             const float t = s * s * (kA / (kX * kX));
@@ -270,12 +295,12 @@ struct StepEnd {
                 if (kStep == kApply) quad_transpose(lo[h]);
             }
             const uint32_t x[2][4] = {{hi[0].x, hi[0].y, hi[0].z, hi[0].w}, {hi[1].x, hi[1].y, hi[1].z, hi[1].w}};
-            const uint32_t z[2][4] = {{lo[0].x, lo[0].y, lo[0].z, lo[0].w}, {lo[1].x, lo[1].y, lo[1].z, lo[1].w}};
+            const uint32_t y2[2][4] = {{lo[0].x, lo[0].y, lo[0].z, lo[0].w}, {lo[1].x, lo[1].y, lo[1].z, lo[1].w}};
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 float4 fc;   // factors of two columns
                 if (kStep == kApply && p.tall)
-                    fc = *reinterpret_cast<const float4*>(p.factors + w.z * p.factor_stride + col0 + 8 * g + 2 * j);
+                    fc = *reinterpret_cast<const float4*>(p.factors + z * p.factor_stride + col0 + 8 * g + 2 * j);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float2 t = unpack_f16x2(x[h][g]);
@@ -283,7 +308,7 @@ struct StepEnd {
                         v[g][2 * h] = p.b * t.x + v[g][2 * h] * (p.c / kA);
                         v[g][2 * h + 1] = p.b * t.y + v[g][2 * h + 1] * (p.c / kA);
                     } else {
-                        const float2 u = unpack_f16x2(z[h][g]);
+                        const float2 u = unpack_f16x2(y2[h][g]);
                         const float2 f0 = p.tall ? make_float2(fc.x, fc.y) : f[h], f1 = p.tall ? make_float2(fc.z, fc.w) : f[h];
                         v[g][2 * h] = s * (f0.x * t.x + (f0.y * (1.0f / kLo)) * u.x + v[g][2 * h] * (1.0f / kA));
                         v[g][2 * h + 1] = s * (f1.x * t.y + (f1.y * (1.0f / kLo)) * u.y + v[g][2 * h + 1] * (1.0f / kA));
@@ -292,7 +317,7 @@ struct StepEnd {
             }
         }
         if (kStep == kApply && p.y) {
-            uint16_t* q = p.y + w.z * p.y_stride + row0 * p.ldy + col0;
+            uint16_t* q = p.y + z * p.y_stride + row0 * p.ldy + col0;
             if (p.y_vec && col0 + 32 <= p.cols) {
                 uint32_t a[4], b[4];
 #pragma unroll
@@ -319,11 +344,11 @@ struct StepEnd {
                 for (int c = 0; c < 4; ++c) {
                     const int row = row0 + i + 8 * (c >> 1), col = col0 + 8 * g + 2 * j + (c & 1);
                     if (row == col && row < p.rows)
-                        p.factors[w.z * p.factor_stride + row] =
+                        p.factors[z * p.factor_stride + row] =
                             make_float2(p.a + (v[g][c] - round_f16(v[g][c])) * (1.0f / kA), p.a + v[g][c] * (1.0f / kA));
                 }
         }
-        const int64_t at = w.z * p.stride + row0 * p.ld + col0;
+        const int64_t at = z * p.stride + row0 * p.ld + col0;
         uint32_t a[4], b[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -349,7 +374,7 @@ struct StepEnd {
             quad_transpose(g2);
             const int col = col0 + 8 * j + i;
             if (col < p.cols) {
-                uint16_t* q = p.d_hi + w.z * p.stride + col * p.ld + row0;
+                uint16_t* q = p.d_hi + z * p.stride + col * p.ld + row0;
                 *reinterpret_cast<uint4*>(q) = make_uint4(e[0], e[1], e[2], e[3]);
                 *reinterpret_cast<uint4*>(q + 8) = make_uint4(g2[0], g2[1], g2[2], g2[3]);
             }
@@ -493,10 +518,10 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
                 const int col0 = w.tn * p.bn + (first + u) * 32;
                 StepEnd<kStep> end;
                 float v[4][4];
-                if (row0 < p.rows) end.load(p, w, row0, col0);
+                if (row0 < p.e.rows) end.load(p.e, w.z, row0, col0);
                 tmem_load_fragment(lanes + buf * 256 + (first + u) * 32, v);
                 if (u + 1 == units) release_accumulator(acc_empty + buf);   // this warp's last read
-                if (row0 < p.rows) end.finish(p, w, row0, col0, mirror, v);
+                if (row0 < p.e.rows) end.finish(p.e, w.z, row0, col0, mirror, v);
             }
             if (units == 0) release_accumulator(acc_empty + buf);   // a narrow last tile: no unit for this warp
         }
@@ -555,7 +580,7 @@ template <Step kStep>
 static int launch_step(StepParams& q, const Matrices& a, bool a_mn, const Matrices& b, bool b_mn, cudaStream_t s) {
     static Done done;
     if (const int rc = allow_smem((const void*)orthogonal_step_kernel<kStep>, kStepSmem, done)) return rc;
-    const StepPlan plan = plan_step(kStep, q.rows, q.cols, q.depth, a.batch);
+    const StepPlan plan = plan_step(kStep, q.e.rows, q.e.cols, q.depth, a.batch);
     if (!plan.bn) return ZERO_ERANGE;
     q.bn = plan.bn;
     q.tiles_n = plan.tiles_n;
@@ -658,40 +683,49 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     src.lo = f32 ? at(w.lo[0]) : nullptr;
     src.ld = w.ldx; src.to = rows * w.ldx;
     src.eps = eps;
+    const Matrices gram{at(w.a), side, side, w.lds, batch}, poly{at(w.b), side, side, w.lds, batch};
+    const Matrices first{at(w.hi[0]), rows, cols, w.ldx, batch}, second{at(w.hi[1]), rows, cols, w.ldx, batch};
+    StepEnding e{};
+    e.tall = tall;
+    e.factors = reinterpret_cast<float2*>(base + w.factors); e.factor_stride = w.lds;
+    e.scale = src.scale;
+    e.a = coefficients[0]; e.b = coefficients[1]; e.c = coefficients[2];
+    const int32_t longer = (int32_t)(tall ? rows : cols);
+    // the end of a step of iteration i
+    const auto ending = [&](Step step, int i) {
+        StepEnding d = e;
+        if (step == kApply) {
+            d.rows = (int32_t)rows; d.cols = (int32_t)cols;
+            d.ld = w.ldx; d.stride = rows * w.ldx;
+            d.first = i == 0;
+            d.c_hi = at(w.hi[i & 1]);
+            d.c_lo = i == 0 && !f32 ? nullptr : at(w.lo[i & 1]);
+            d.d_hi = at(w.hi[~i & 1]);
+            d.d_lo = at(w.lo[~i & 1]);
+        } else {
+            d.rows = d.cols = (int32_t)side;
+            d.ld = w.lds; d.stride = side * w.lds;
+            d.first = step == kGram && i == 0;
+            d.c_hi = at(w.a);
+            d.d_hi = at(step == kGram ? w.a : w.b);
+        }
+        return d;
+    };
+    const bool y_vec = rows_aligned16(y, ldy, 2) && (batch == 1 || y_stride % 8 == 0);
     const dim3 grid((unsigned)w.parts, (unsigned)batch);
     if (const int rc = launch_dense(orthogonal_norm_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
     if (const int rc = launch_dense(orthogonal_source_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
-
-    const Matrices gram{at(w.a), side, side, w.lds, batch}, poly{at(w.b), side, side, w.lds, batch};
     for (int i = 0; i < steps; ++i) {
-        const Matrices now{at(w.hi[i & 1]), rows, cols, w.ldx, batch};
+        const Matrices& now = i & 1 ? second : first;
         StepParams q{};
-        q.tall = tall;
-        q.factors = reinterpret_cast<float2*>(base + w.factors); q.factor_stride = w.lds;
-        q.scale = src.scale;
-        q.a = coefficients[0]; q.b = coefficients[1]; q.c = coefficients[2];
-        q.ld = w.lds; q.stride = side * w.lds;
-        q.rows = q.cols = (int32_t)side;
-        q.depth = (int32_t)(tall ? rows : cols);
-        q.first = i == 0;
-        q.d_hi = at(w.a);
+        q.e = ending(kGram, i);
+        q.depth = longer;
         if (const int rc = launch_step<kGram>(q, now, tall, now, tall, s)) return rc;
+        q.e = ending(kSquare, i);
         q.depth = (int32_t)side;
-        q.first = false;
-        q.c_hi = at(w.a);
-        q.d_hi = at(w.b);
         if (const int rc = launch_step<kSquare>(q, gram, false, gram, false, s)) return rc;
-        q.rows = (int32_t)rows; q.cols = (int32_t)cols;
-        q.ld = w.ldx; q.stride = rows * w.ldx;
-        q.first = i == 0;
-        q.c_hi = now.p;
-        q.c_lo = i == 0 && !f32 ? nullptr : at(w.lo[i & 1]);
-        q.d_hi = at(w.hi[~i & 1]);
-        q.d_lo = at(w.lo[~i & 1]);
-        if (i + 1 == steps) {
-            q.y = y; q.ldy = ldy; q.y_stride = batch > 1 ? y_stride : 0;
-            q.y_vec = rows_aligned16(y, ldy, 2) && (batch == 1 || y_stride % 8 == 0);
-        }
+        q.e = ending(kApply, i);
+        if (i + 1 == steps) q.e.y = y, q.e.ldy = ldy, q.e.y_stride = batch > 1 ? y_stride : 0, q.e.y_vec = y_vec;
         // wide: B X, X read along its rows; tall: X B, B being its own transpose
         if (const int rc = tall ? launch_step<kApply>(q, now, false, poly, false, s) : launch_step<kApply>(q, poly, false, now, true, s)) return rc;
     }
