@@ -410,8 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
             turn ^= 1;   // written again after the next row's barrier
             middle = w[0].base;
             off = squares = 0.0f;
+#pragma unroll 4
             for (int i = 0; i < p.warps; ++i) off += w[i].n * (w[i].base - middle + w[i].off);
             off *= 1.0f / (float)p.cols;
+#pragma unroll 4
             for (int i = 0; i < p.warps; ++i) {
                 const float t = w[i].base - middle + w[i].off - off;
                 squares += w[i].squares + w[i].n * t * t;
@@ -473,9 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         for (int k = 0; k < 4; ++k) sum_g[j][k] = sum_b[j][k] = both(0.0f);
     }
     const float share = 1.0f / (float)p.cols;
+    float mean_ahead = row < p.rows ? p.mean[row] : 0.0f, rstd_ahead = row < p.rows ? p.rstd[row] : 0.0f;
     for (; row - back < p.rows; row += stride, dx += dx_hop, xs.next_row(), ds.next_row(), rs.next_row()) {
         const bool has = kMany || row < p.rows;
-        const float mean = has ? p.mean[row] : 0.0f, rstd = has ? p.rstd[row] : 0.0f;
+        const float mean = mean_ahead, rstd = rstd_ahead;
+        if (row + stride < p.rows) mean_ahead = p.mean[row + stride], rstd_ahead = p.rstd[row + stride];
         const uint8_t* slot = ring.next(m, send);
         const float2 move = both(-mean), scale = both(rstd);
         float2 v1 = both(0.0f), v2 = both(0.0f);
@@ -499,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
             const float2* w = stats[turn] + which * p.warps;
             turn ^= 1;   // written again after the next row's barrier
             v[0] = v[1] = 0.0f;
+#pragma unroll 4
             for (int i = 0; i < p.warps; ++i) v[0] += w[i].x, v[1] += w[i].y;
         }
         if (!has) continue;
@@ -732,16 +737,17 @@ struct NormShape {
     int lanes, warps, per, threads, most;   // most: threads that the kernel is made for
     int64_t teams, grid;   // teams of a CTA
 };
-static NormShape norm_shape(int64_t rows, int64_t cols) {
+static NormShape norm_shape(int64_t rows, int64_t cols, bool vec) {
     NormShape s{};
     const int64_t groups = (cols + 7) / 8, sms = sm_count();
-    s.many = groups > 128;
-    s.per = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
-    s.warps = s.many ? (int)((groups + 127) / 128) : 1;
+    // element by element takes more registers: fewer pieces a thread
+    s.per = groups <= 32 ? 1 : groups <= 64 || (!vec && groups <= 1024) ? 2 : 4;
+    s.many = groups > 32 * s.per;
+    s.warps = s.many ? (int)((groups + 32 * s.per - 1) / (32 * s.per)) : 1;
     s.lanes = 1;
     while (!s.many && s.lanes < 32 && s.lanes * s.per < groups) s.lanes *= 2;
     // 12 warps with registers to spare; the widest rows need 16, of 128 registers a thread
-    s.most = s.warps > 12 ? 512 : 384;
+    s.most = s.warps > 12 || (s.many && s.per == 2) ? 512 : 384;
     const int64_t in_warp = s.many ? 1 : 32 / s.lanes, most = s.many ? s.most / 32 / s.warps : s.most / 32 * in_warp;
     int64_t teams = (rows + sms - 1) / sms;
     teams = (teams + in_warp - 1) / in_warp * in_warp;   // whole warps
@@ -751,11 +757,11 @@ static NormShape norm_shape(int64_t rows, int64_t cols) {
     if (s.grid > sms) s.grid = sms;
     return s;
 }
-// Parts that the weights' gradients are summed in.
+// The most parts that the weights' gradients are summed in.
 static int64_t norm_parts(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
-    if (cols > kWidestNorm) return rows < 64 ? rows : 64;
-    return norm_shape(rows, cols).grid;
+    const int64_t most = cols > kWidestNorm ? 64 : sm_count();
+    return rows < most ? rows : most;
 }
 
 // Lays out the slots for a row of up to three streams (sizes of an element, 0 where
@@ -815,12 +821,16 @@ static int launch_norm_grad(NormParams& p, const NormShape& s, cudaStream_t stre
 }
 template <bool kF32, bool kVec>
 static int launch_norm(NormParams& p, const NormShape& s, cudaStream_t stream) {
+    if constexpr (!kVec)
+        if (s.many && s.per == 2) return launch_norm<kF32, kVec, 2, 512, true>(p, s, stream);
     if (s.many) return s.most > 384 ? launch_norm<kF32, kVec, 4, 512, true>(p, s, stream) : launch_norm<kF32, kVec, 4, 384, true>(p, s, stream);
     return s.per == 1 ? launch_norm<kF32, kVec, 1, 384, false>(p, s, stream)
            : s.per == 2 ? launch_norm<kF32, kVec, 2, 384, false>(p, s, stream) : launch_norm<kF32, kVec, 4, 384, false>(p, s, stream);
 }
 template <bool kF32, bool kDyF32, bool kVec>
 static int launch_norm_grad(NormParams& p, const NormShape& s, cudaStream_t stream) {
+    if constexpr (!kVec)
+        if (s.many && s.per == 2) return launch_norm_grad<kF32, kDyF32, kVec, 2, 512, true>(p, s, stream);
     if (s.many) return s.most > 384 ? launch_norm_grad<kF32, kDyF32, kVec, 4, 512, true>(p, s, stream) : launch_norm_grad<kF32, kDyF32, kVec, 4, 384, true>(p, s, stream);
     return s.per == 1 ? launch_norm_grad<kF32, kDyF32, kVec, 1, 384, false>(p, s, stream)
            : s.per == 2 ? launch_norm_grad<kF32, kDyF32, kVec, 2, 384, false>(p, s, stream) : launch_norm_grad<kF32, kDyF32, kVec, 4, 384, false>(p, s, stream);
@@ -865,7 +875,7 @@ extern "C" int zero_layer_norm(int64_t rows, int64_t cols, const void* x, int64_
     }
     const bool vec = cols % 8 == 0 && rows_aligned16(x, ldx, size) && rows_aligned16(y, ldy, dtype_size(y_dtype)) &&
                      (!residual || (rows_aligned16(residual, ldr, size) && rows_aligned16(sum, lds, size)));
-    const NormShape shape = norm_shape(rows, cols);
+    const NormShape shape = norm_shape(rows, cols, vec);
     p.lanes = shape.lanes; p.warps = shape.warps;
     if (dtype == ZERO_F32) return vec ? launch_norm<true, true>(p, shape, s) : launch_norm<true, false>(p, shape, s);
     return vec ? launch_norm<false, true>(p, shape, s) : launch_norm<false, false>(p, shape, s);
@@ -902,7 +912,7 @@ extern "C" int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, 
             return ZERO_EALIGN;
     }
     if (cols == 0 || (rows == 0 && !weights)) return ZERO_OK;
-    const int64_t parts = weights ? norm_parts(rows, cols) : 0;
+    int64_t parts = weights ? norm_parts(rows, cols) : 0;
     if (parts) {
         if (!workspace) return ZERO_EINVAL;
         if (!aligned16(workspace)) return ZERO_EALIGN;
@@ -936,8 +946,9 @@ extern "C" int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, 
     } else {
         const bool vec = cols % 8 == 0 && rows_aligned16(x, ldx, size) && rows_aligned16(dy, lddy, dtype_size(dy_dtype)) &&
                          rows_aligned16(dx, lddx, size) && (!residual || rows_aligned16(residual, ldr, size));
-        const NormShape shape = norm_shape(rows, cols);
+        const NormShape shape = norm_shape(rows, cols, vec);
         p.lanes = shape.lanes; p.warps = shape.warps;
+        if (parts) parts = shape.grid;
         if (!f32)
             rc = vec ? launch_norm_grad<false, false, true>(p, shape, s) : launch_norm_grad<false, false, false>(p, shape, s);
         else if (dy_f32)
