@@ -530,42 +530,43 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         }
     }
     if (!p.part) return;
-    // the teams' sums to shared memory, 8 kPer floats a thread, and in order to the parts
-    float* all = reinterpret_cast<float*>(slots);
-    const int width = 8 * kPer * m.size;
     float* part = p.part + (int64_t)blockIdx.x * p.cols;
     const int64_t half = (int64_t)gridDim.x * p.cols;
+    // pair i of this thread's columns, from column c
+    const auto column_of = [&](int i) { return kVec ? 8 * (m.t + m.size * (i / 4)) + 2 * (i % 4) : m.t + m.size * 2 * i; };
+    const auto put = [&](int h, int i, float2 v) {
+        const int c = column_of(i);
+        if constexpr (kVec) {
+            if (c < p.cols) *reinterpret_cast<float2*>(part + h * half + c) = v;
+        } else {
+            if (c < p.cols) part[h * half + c] = v.x;
+            if (c + m.size < p.cols) part[h * half + c + m.size] = v.y;
+        }
+    };
+    if (teams == 1) {
+#pragma unroll
+        for (int i = 0; i < 4 * kPer; ++i) {
+            put(0, i, sum_g[i / 4][i % 4]);
+            put(1, i, sum_b[i / 4][i % 4]);
+        }
+        return;
+    }
+    // several teams: their sums to shared memory, each team's pairs side by side, and added
+    // in order, a team a share of the pairs
+    float2* all = reinterpret_cast<float2*>(slots);
+    const int width = 4 * kPer * m.size;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         __syncthreads();   // the rows, or the first half, have been read
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 v = h ? sum_b[j][k] : sum_g[j][k];
-                float* q = all + which * width;
-                if constexpr (kVec) {
-                    // two floats at a time, the pairs of a piece `size` apart: no two lanes share a bank
-                    *reinterpret_cast<float2*>(q + 2 * (m.t + m.size * (4 * j + k))) = v;
-                } else {
-                    q[column<false>(m, j, 2 * k)] = v.x;
-                    q[column<false>(m, j, 2 * k + 1)] = v.y;
-                }
-            }
+        for (int i = 0; i < 4 * kPer; ++i) all[which * width + m.t + m.size * i] = h ? sum_b[i / 4][i % 4] : sum_g[i / 4][i % 4];
         __syncthreads();
-        // the pairs (or columns) of thread m.t of a team, shared out to the teams
-        for (int i = which; i < (kVec ? 4 : 8) * kPer; i += teams) {
-            const int c = kVec ? 8 * (m.t + m.size * (i / 4)) + 2 * (i % 4) : m.t + m.size * i;
-            if (c >= p.cols) break;
-            if constexpr (kVec) {
-                float2 s = both(0.0f);
-                for (int t = 0; t < teams; ++t) s = add2(s, *reinterpret_cast<const float2*>(all + t * width + 2 * (m.t + m.size * i)));
-                *reinterpret_cast<float2*>(part + h * half + c) = s;
-            } else {
-                float s = 0.0f;
-                for (int t = 0; t < teams; ++t) s += all[t * width + c];
-                part[h * half + c] = s;
-            }
+#pragma unroll 4
+        for (int i = which; i < 4 * kPer; i += teams) {
+            float2 s = both(0.0f);
+#pragma unroll 4
+            for (int t = 0; t < teams; ++t) s = add2(s, all[t * width + m.t + m.size * i]);
+            put(h, i, s);
         }
     }
 }
@@ -711,8 +712,16 @@ __global__ void __launch_bounds__(32 * kFinishWarps) norm_finish_kernel(const Fi
     float v = 0.0f;
     if (c < p.cols) {
         const float* q = p.part + (int64_t)blockIdx.y * p.parts * p.cols + c;
-#pragma unroll 10
-        for (int i = warp; i < p.parts; i += kFinishWarps) v += q[(int64_t)i * p.cols];
+        for (int i0 = warp; i0 < p.parts; i0 += kFinishWarps * 10) {   // 10 loads in flight: the parts of 152 CTAs at once
+            float t[10];
+#pragma unroll
+            for (int k = 0; k < 10; ++k) {
+                const int i = i0 + kFinishWarps * k;
+                t[k] = i < p.parts ? q[(int64_t)i * p.cols] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 10; ++k) v += t[k];
+        }
     }
     s[warp][lane] = v;
     __syncthreads();
