@@ -67,60 +67,79 @@ struct SourceParams {
 };
 constexpr int kSourceThreads = 256;
 
-__device__ __forceinline__ void source8(const SourceParams& p, int64_t at, int n, float (&v)[8]) {
-    if (p.vec) {
-        uint4 u[2];
-        if (p.f32) {
-            u[0] = ld_live_u4(static_cast<const float*>(p.x) + at);
-            u[1] = ld_live_u4(static_cast<const float*>(p.x) + at + 4);
-            raw8<true>(u, v);
-        } else {
-            u[0] = ld_live_u4(static_cast<const uint16_t*>(p.x) + at);
-            raw8<false>(u, v);
+// Groups of eight that a thread has in flight.
+constexpr int kFlying = 4;
+
+struct SourceGroup {
+    uint4 u[2];
+    int32_t row, col;   // col < 0: none
+    __device__ __forceinline__ void load(const SourceParams& p, int64_t from, uint32_t g, uint32_t all) {
+        row = (int32_t)(g / (uint32_t)p.groups);
+        col = g < all ? (int32_t)(g - (uint32_t)row * (uint32_t)p.groups) * 8 : -1;
+        u[0] = u[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (col < 0) return;
+        const int64_t at = from + row * p.ldx + col;
+        if (p.vec) {
+            const char* q = static_cast<const char*>(p.x) + at * (p.f32 ? 4 : 2);
+            u[0] = ld_live_u4(q);
+            if (p.f32) u[1] = ld_live_u4(q + 16);
+            return;
         }
-        return;
-    }
+        const int n = p.cols - col;
+        uint32_t w[8];   // fp32, or bf16 in the upper halves
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        v[k] = k >= n ? 0.0f : p.f32 ? static_cast<const float*>(p.x)[at + k] : bf16_one(static_cast<const uint16_t*>(p.x)[at + k]);
+        for (int k = 0; k < 8; ++k)
+            w[k] = k >= n ? 0u : p.f32 ? static_cast<const uint32_t*>(p.x)[at + k] : (uint32_t)static_cast<const uint16_t*>(p.x)[at + k] << 16;
+        u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        u[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    __device__ __forceinline__ void get(const SourceParams& p, float (&v)[8]) const {
+        if (p.f32 || !p.vec)
+            raw8<true>(u, v);
+        else
+            raw8<false>(u, v);
+    }
+};
+
+// Over a warp; fp64 additions are few an SM, so only where they are needed.
+__device__ __forceinline__ double warp_sum(float near, double far) {
+    for (int o = 16; o; o /= 2) near += __shfl_xor_sync(0xffffffffu, near, o);
+    if (__any_sync(0xffffffffu, far != 0.0)) {   // or NaN
+        for (int o = 16; o; o /= 2) far += __shfl_xor_sync(0xffffffffu, far, o);
+        return (double)near + far;
+    }
+    return (double)near;
 }
 
-// The sum over the CTA in a fixed order, to every thread.
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double part[32];
-    for (int o = 16; o; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = 0.0;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) v += part[w];
-    return v;
-}
-
-// The sum of squares of every `share`-th group of eight from `first`, a thread's own:
-// in fp32 where none can leave fp32's range, else in fp64, and in fp64 over the threads.
+// The sum of squares of every `share`-th group of eight from `first`, over a warp's threads:
+// in fp32 where none can leave its range, else in fp64.
 __device__ __forceinline__ double squares(const SourceParams& p, int z, uint32_t first, uint32_t share) {
     const int64_t from = (int64_t)z * p.stride;
     float sum = 0.0f;
     double far = 0.0;
     const uint32_t all = (uint32_t)p.rows * (uint32_t)p.groups;
-    for (uint32_t g = first; g < all; g += share) {
-        const uint32_t row = g / (uint32_t)p.groups, c = (g - row * (uint32_t)p.groups) * 8;
-        float v[8], most = 0.0f, s = 0.0f;
-        source8(p, from + (int64_t)row * p.ldx + c, p.cols - (int)c, v);
+    for (uint32_t g = first; g < all; g += kFlying * share) {
+        SourceGroup x[kFlying];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            most = fmaxf(most, fabsf(v[k]));
-            s += v[k] * v[k];
-        }
-        if ((most > 1e-12f && most < 1e16f && s == s) || (most == 0.0f && s == 0.0f)) {
-            sum += s;
-        } else {
+        for (int i = 0; i < kFlying; ++i) x[i].load(p, from, g + i * share, all);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) far += (double)v[k] * (double)v[k];
+        for (int i = 0; i < kFlying; ++i) {
+            float v[8], most = 0.0f, s = 0.0f;
+            x[i].get(p, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                most = fmaxf(most, fabsf(v[k]));
+                s += v[k] * v[k];
+            }
+            if ((most > 1e-12f && most < 1e16f && s == s) || (most == 0.0f && s == 0.0f)) {
+                sum += s;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) far += (double)v[k] * (double)v[k];
+            }
         }
     }
-    return (double)sum + far;
+    return warp_sum(sum, far);
 }
 
 // hi + lo / 2^11 = x 2^(12 - e) with e the norm's exponent, and scale = 2^e / norm: the
@@ -141,37 +160,52 @@ __device__ __forceinline__ void parts_of(const SourceParams& p, int z, const Sou
     const float f1 = s.f1, f2 = s.f2;
     const int64_t from = (int64_t)z * p.stride, to = (int64_t)z * p.to;
     const uint32_t all = (uint32_t)p.rows * (uint32_t)p.groups;
-    for (uint32_t g = first; g < all; g += share) {
-        const uint32_t row = g / (uint32_t)p.groups, c = (g - row * (uint32_t)p.groups) * 8;
-        float v[8], r[8];
-        source8(p, from + (int64_t)row * p.ldx + c, p.cols - (int)c, v);
+    for (uint32_t g = first; g < all; g += kFlying * share) {
+        SourceGroup x[kFlying];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = v[j] * f1 * f2;
-            r[j] = (v[j] - round_f16(v[j])) * kLo;
+        for (int i = 0; i < kFlying; ++i) x[i].load(p, from, g + i * share, all);
+#pragma unroll
+        for (int i = 0; i < kFlying; ++i) {
+            if (x[i].col < 0) break;
+            float v[8], r[8];
+            x[i].get(p, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = v[j] * f1 * f2;
+                r[j] = (v[j] - round_f16(v[j])) * kLo;
+            }
+            const int64_t at = to + x[i].row * p.ld + x[i].col;
+            *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+            if (p.lo)
+                *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
         }
-        const int64_t at = to + (int64_t)row * p.ld + c;
-        *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
-        if (p.lo)
-            *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
     }
 }
 
 __global__ void __launch_bounds__(kSourceThreads) orthogonal_norm_kernel(const SourceParams p) {
     await_predecessor();
-    const double t = block_sum(squares(p, blockIdx.y, blockIdx.x * kSourceThreads + threadIdx.x, gridDim.x * kSourceThreads));
-    if (threadIdx.x == 0) p.norm[(int64_t)blockIdx.y * p.parts + blockIdx.x] = t;
+    __shared__ double part[kSourceThreads / 32];
+    const double mine = squares(p, blockIdx.y, blockIdx.x * kSourceThreads + threadIdx.x, gridDim.x * kSourceThreads);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        for (int w = 0; w < kSourceThreads / 32; ++w) t += part[w];
+        p.norm[(int64_t)blockIdx.y * p.parts + blockIdx.x] = t;
+    }
 }
 
 __global__ void __launch_bounds__(kSourceThreads) orthogonal_source_kernel(const SourceParams p) {
     await_predecessor();
     __shared__ SourceScale scale;
-    double t = 0.0;
-    for (int i = threadIdx.x; i < p.parts; i += kSourceThreads) t += p.norm[(int64_t)blockIdx.y * p.parts + i];
-    t = block_sum(t);
-    if (threadIdx.x == 0) {
-        scale = source_scale(t, p.eps);
-        if (blockIdx.x == 0) p.scale[blockIdx.y] = scale.scale;
+    if (threadIdx.x < 32) {   // one warp adds the parts, every CTA in the same order
+        double t = 0.0;
+        for (int i = threadIdx.x; i < p.parts; i += 32) t += p.norm[(int64_t)blockIdx.y * p.parts + i];
+        t = warp_sum(0.0f, t);
+        if (threadIdx.x == 0) {
+            scale = source_scale(t, p.eps);
+            if (blockIdx.x == 0) p.scale[blockIdx.y] = scale.scale;
+        }
     }
     __syncthreads();
     parts_of(p, blockIdx.y, scale, blockIdx.x * kSourceThreads + threadIdx.x, gridDim.x * kSourceThreads);
@@ -604,12 +638,12 @@ constexpr int64_t kLongest = (int64_t)1 << 30;
 static int orthogonal_space(int64_t batch, int64_t rows, int64_t cols, OrthogonalSpace* w) {
     const int64_t side = rows < cols ? rows : cols, longer = rows < cols ? cols : rows;
     // a side's square and a matrix's groups of eight are counted in 31 bits, a batch's bytes in 62
-    if (longer > kLongest || side > 32768 || rows * ((cols + 7) / 8) > INT32_MAX / 2) return ZERO_ERANGE;
+    if (longer > kLongest || side > 32768 || rows * ((cols + 7) / 8) > INT32_MAX / 4) return ZERO_ERANGE;
     w->ldx = (cols + 63) / 64 * 64;
     w->lds = (side + 63) / 64 * 64;
     const int64_t x = rows * w->ldx * 2, a = side * w->lds * 2;
-    const int64_t groups = rows * ((cols + 7) / 8), most = 1024;
-    w->parts = (groups + 4 * kSourceThreads - 1) / (4 * kSourceThreads);
+    const int64_t groups = rows * ((cols + 7) / 8), most = batch > 32 ? 32 : 1024 / batch;   // some CTAs an SM, of the batch
+    w->parts = (groups + 2 * kFlying * kSourceThreads - 1) / (2 * kFlying * kSourceThreads);
     if (w->parts > most) w->parts = most;
     if (batch > ((int64_t)1 << 60) / (4 * x + 2 * a + 16 * w->lds + 16 * w->parts + 4096)) return ZERO_ERANGE;
     int64_t at = 0;
