@@ -99,6 +99,37 @@ struct SourceGroup {
         else
             raw8<false>(u, v);
     }
+    // Squares: in fp32 where none can leave its range, else in fp64.
+    __device__ __forceinline__ void square(const SourceParams& p, float& near, double& far) const {
+        float v[8], most = 0.0f, s = 0.0f;
+        get(p, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            most = fmaxf(most, fabsf(v[k]));
+            s += v[k] * v[k];
+        }
+        if ((most > 1e-12f && most < 1e16f && s == s) || (most == 0.0f && s == 0.0f)) {
+            near += s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) far += (double)v[k] * (double)v[k];
+        }
+    }
+    // hi + lo / 2^11 = x f1 f2.
+    __device__ __forceinline__ void part(const SourceParams& p, int64_t to, float f1, float f2) const {
+        if (col < 0) return;
+        float v[8], r[8];
+        get(p, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = v[j] * f1 * f2;
+            r[j] = (v[j] - round_f16(v[j])) * kLo;
+        }
+        const int64_t at = to + row * p.ld + col;
+        *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+        if (p.lo)
+            *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
+    }
 };
 
 // Over a warp; fp64 additions are few an SM, so only where they are needed.
@@ -123,21 +154,7 @@ __device__ __forceinline__ double squares(const SourceParams& p, int z, uint32_t
 #pragma unroll
         for (int i = 0; i < kFlying; ++i) x[i].load(p, from, g + i * share, all);
 #pragma unroll
-        for (int i = 0; i < kFlying; ++i) {
-            float v[8], most = 0.0f, s = 0.0f;
-            x[i].get(p, v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                most = fmaxf(most, fabsf(v[k]));
-                s += v[k] * v[k];
-            }
-            if ((most > 1e-12f && most < 1e16f && s == s) || (most == 0.0f && s == 0.0f)) {
-                sum += s;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) far += (double)v[k] * (double)v[k];
-            }
-        }
+        for (int i = 0; i < kFlying; ++i) x[i].square(p, sum, far);
     }
     return warp_sum(sum, far);
 }
@@ -165,20 +182,7 @@ __device__ __forceinline__ void parts_of(const SourceParams& p, int z, const Sou
 #pragma unroll
         for (int i = 0; i < kFlying; ++i) x[i].load(p, from, g + i * share, all);
 #pragma unroll
-        for (int i = 0; i < kFlying; ++i) {
-            if (x[i].col < 0) break;
-            float v[8], r[8];
-            x[i].get(p, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = v[j] * f1 * f2;
-                r[j] = (v[j] - round_f16(v[j])) * kLo;
-            }
-            const int64_t at = to + x[i].row * p.ld + x[i].col;
-            *reinterpret_cast<uint4*>(p.hi + at) = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
-            if (p.lo)
-                *reinterpret_cast<uint4*>(p.lo + at) = make_uint4(pack_f16x2(r[0], r[1]), pack_f16x2(r[2], r[3]), pack_f16x2(r[4], r[5]), pack_f16x2(r[6], r[7]));
-        }
+        for (int i = 0; i < kFlying; ++i) x[i].part(p, to, f1, f2);
     }
 }
 
@@ -209,6 +213,44 @@ __global__ void __launch_bounds__(kSourceThreads) orthogonal_source_kernel(const
     }
     __syncthreads();
     parts_of(p, blockIdx.y, scale, blockIdx.x * kSourceThreads + threadIdx.x, gridDim.x * kSourceThreads);
+}
+
+// Both in one, for a matrix that the threads of a cluster of eight hold: read once, and a
+// launch less (4 us).
+constexpr int kHeldThreads = 1024, kHeldCtas = 8;
+constexpr int64_t kHeldGroups = (int64_t)kFlying * kHeldThreads * kHeldCtas;
+
+__global__ void __launch_bounds__(kHeldThreads, 1) orthogonal_held_kernel(const SourceParams p) {
+    __shared__ double part[kHeldThreads / 32], total;
+    __shared__ SourceScale scale;
+    await_predecessor();
+    const int z = blockIdx.x / kHeldCtas, rank = blockIdx.x % kHeldCtas;
+    const uint32_t all = (uint32_t)p.rows * (uint32_t)p.groups, share = kHeldCtas * kHeldThreads;
+    SourceGroup x[kFlying];
+#pragma unroll
+    for (int i = 0; i < kFlying; ++i) x[i].load(p, (int64_t)z * p.stride, rank * kHeldThreads + threadIdx.x + i * share, all);
+    float near = 0.0f;
+    double far = 0.0;
+#pragma unroll
+    for (int i = 0; i < kFlying; ++i) x[i].square(p, near, far);
+    const double mine = warp_sum(near, far);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = mine;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const double t = warp_sum(0.0f, part[threadIdx.x]);
+        if (threadIdx.x == 0) total = t;
+    }
+    cluster_sync();
+    if (threadIdx.x == 0) {   // every CTA in the same order
+        double t = 0.0;
+        for (int i = 0; i < kHeldCtas; ++i) t += peer_load_double(peer_addr(smem_addr(&total), i));
+        scale = source_scale(t, p.eps);
+        if (rank == 0) p.scale[z] = scale.scale;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFlying; ++i) x[i].part(p, (int64_t)z * p.to, scale.f1, scale.f2);
+    cluster_started();   // the totals are read before their CTAs end
 }
 
 // ---- products --------------------------------------------------------------------------------
@@ -407,7 +449,7 @@ struct StepEnd {
             quad_transpose(e);
             quad_transpose(g2);
             const int col = col0 + 8 * j + i;
-            if (col < p.cols) {
+            if (col < p.cols && row0 < p.rows) {
                 uint16_t* q = p.d_hi + z * p.stride + col * p.ld + row0;
                 *reinterpret_cast<uint4*>(q) = make_uint4(e[0], e[1], e[2], e[3]);
                 *reinterpret_cast<uint4*>(q + 8) = make_uint4(g2[0], g2[1], g2[2], g2[3]);
@@ -544,25 +586,48 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             const int chunks_n = width_of(p, w.tn) / 32, first = (h >> 1) * ((chunks_n + 1) / 2);
             const int units = h >> 1 ? chunks_n - first : (chunks_n + 1) / 2;   // of this warp
             const int row0 = w.tm * 256 + (int)rank * 128 + q * 32 + (h & 1) * 16, buf = use & 1;
-            const bool mirror = (w.tn + 1) * p.bn <= w.tm * 256;
-            if (!step_wait(acc_full + buf, (use / 2) & 1)) break;
-            tcgen05_fence_after();
+            const bool mirror = (w.tn + 1) * p.bn <= w.tm * 256, mine = row0 < p.e.rows;
+            const int col_first = w.tn * p.bn + first * 32;
+            // what a unit's end reads is on its way while the unit before it, or the
+            // tile's product, is finished
+            StepEnd<kStep> end{}, next{};
+            if (use > 0 && mine && units > 0) end.load(p.e, w.z, row0, col_first);
+            float v[4][4] = {};
+            bool ok = true;
+            // before the first tile the end goes once through rows that do not exist, so that
+            // its instructions are there when the product is (0.4 us of a launch)
 #pragma unroll 1
-            for (int u = 0; u < units; ++u) {
-                const int col0 = w.tn * p.bn + (first + u) * 32;
-                StepEnd<kStep> end;
-                float v[4][4];
-                if (row0 < p.e.rows) end.load(p.e, w.z, row0, col0);
-                tmem_load_fragment(lanes + buf * 256 + (first + u) * 32, v);
-                if (u + 1 == units) release_accumulator(acc_empty + buf);   // this warp's last read
-                if (row0 < p.e.rows) end.finish(p.e, w.z, row0, col0, mirror, v);
+            for (int u = use == 0 ? -1 : 0; u < units; ++u) {
+                const bool warm = u < 0;
+                const int col0 = warm ? w.tn * p.bn : col_first + u * 32;
+                if (!warm) {
+                    if (u == 0) {
+                        if (!(ok = step_wait(acc_full + buf, (use / 2) & 1))) break;
+                        tcgen05_fence_after();
+                    }
+                    tmem_load_fragment(lanes + buf * 256 + (first + u) * 32, v);
+                    if (u + 1 == units)
+                        release_accumulator(acc_empty + buf);   // this warp's last read
+                    else if (mine)
+                        next.load(p.e, w.z, row0, col0 + 32);
+                }
+                if (mine || warm) end.finish(p.e, w.z, warm ? p.e.rows : row0, col0, mirror, v);
+                if (warm && mine && units > 0) next.load(p.e, w.z, row0, col_first);
+                end = next;
             }
-            if (units == 0) release_accumulator(acc_empty + buf);   // a narrow last tile: no unit for this warp
+            if (!ok) break;
+            if (units == 0) {   // a narrow last tile: no unit for this warp
+                if (!step_wait(acc_full + buf, (use / 2) & 1)) break;
+                release_accumulator(acc_empty + buf);
+            }
         }
     }
+    // the CTAs part when both are done with the tensor memories and each other's barriers;
+    // their stores are ordered by the kernel's end alone (waiting for them here as well
+    // took 0.7 us a launch)
     tcgen05_fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_started();
     tcgen05_fence_after();
     if (warp == 2) tmem_free<true>(tmem, 512);
 }
@@ -746,9 +811,13 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
         return d;
     };
     const bool y_vec = rows_aligned16(y, ldy, 2) && (batch == 1 || y_stride % 8 == 0);
-    const dim3 grid((unsigned)w.parts, (unsigned)batch);
-    if (const int rc = launch_dense(orthogonal_norm_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
-    if (const int rc = launch_dense(orthogonal_source_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
+    if (rows * (int64_t)src.groups <= kHeldGroups) {
+        if (const int rc = launch_dense(orthogonal_held_kernel, dim3((unsigned)(kHeldCtas * batch)), kHeldThreads, kHeldCtas, true, 0, s, src)) return rc;
+    } else {
+        const dim3 grid((unsigned)w.parts, (unsigned)batch);
+        if (const int rc = launch_dense(orthogonal_norm_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
+        if (const int rc = launch_dense(orthogonal_source_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
+    }
     for (int i = 0; i < steps; ++i) {
         const Matrices& now = i & 1 ? second : first;
         StepParams q{};

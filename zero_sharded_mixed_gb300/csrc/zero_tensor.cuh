@@ -196,6 +196,11 @@ __device__ __forceinline__ float peer_load1(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
+__device__ __forceinline__ double peer_load_double(uint32_t addr) {
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr));
+    return v;
+}
 
 // ---- tensor-map copies -------------------------------------------------------------
 // A box of the matrix at column x (a multiple of 8 elements: copies start on 16-byte
