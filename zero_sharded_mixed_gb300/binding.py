@@ -690,8 +690,11 @@ def _matrix(t, name, rows, cols, dtypes):
 def _vector(t, name, n, code):
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    if isinstance(t, torch.Tensor):
+        if t.numel() == n and t.is_cuda and t.dtype == _SRC_DT[code] and t.is_contiguous():
+            return t.data_ptr()
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
     return _tensor(t, name, _SRC_DT[code], n)
 
 

@@ -5,7 +5,10 @@
 reduce bucket size, the number of gradient-accumulation steps, the clipping
 threshold, the optimizer (AdamW with lr, betas, eps, weight_decay) and the
 precision (bf16), and a "WarmupDecayLR" learning-rate scheduler; "Offload and
-ZeRO++" adds zero_quantized_weights and zero_quantized_gradients.  ``ZeroConfig.from_dict`` reads those keys, refuses
+ZeRO++" adds zero_quantized_weights and zero_quantized_gradients.  Beside AdamW the
+optimizer may be Muon (an addition of this library: lr, momentum, nesterov, ns_steps,
+weight_decay, and betas and eps for the vectors, which AdamW moves), at stages 1 and 2
+without clipping or 8-bit gradients.  ``ZeroConfig.from_dict`` reads those keys, refuses
 what the library does not do (fp16 loss scaling, offload, another optimizer),
 and lists the keys it did not use instead of failing on them.
 """
@@ -30,6 +33,10 @@ class ZeroConfig:
     betas: tuple = (0.9, 0.999)
     eps: float = 1e-8
     weight_decay: float = 0.0
+    optimizer: str = "adamw"                  # or "muon": matrices by orthogonalised momentum
+    momentum: float = 0.95                    # muon
+    nesterov: bool = True                     # muon
+    ns_steps: int = 5                         # muon: steps of the orthogonalisation
     zero_quantized_weights: bool = False      # stage 3: 8-bit weight gathers
     zero_quantized_gradients: bool = False    # 8-bit gradient reduce-scatter
     overlap_comm: bool = False                # stage 3: gathers one unit ahead on a side stream
@@ -52,6 +59,15 @@ class ZeroConfig:
             raise ValueError("zero_quantized_weights applies to stage 3 (the weight all-gather)")
         if not (0.0 <= self.betas[0] < 1.0 and 0.0 <= self.betas[1] < 1.0):
             raise ValueError(f"betas must lie in [0, 1), got {self.betas!r}")
+        if self.optimizer not in ("adamw", "muon"):
+            raise ValueError(f"optimizer {self.optimizer!r}: this library implements AdamW and Muon")
+        if self.optimizer == "muon":
+            if self.stage == 3:
+                raise ValueError("Muon needs whole matrices where they are updated: stages 1 and 2")
+            if self.gradient_clipping > 0 or self.zero_quantized_gradients:
+                raise ValueError("Muon is not combined with gradient_clipping or zero_quantized_gradients")
+            if not (0.0 <= self.momentum < 1.0 and 1 <= self.ns_steps <= 100):
+                raise ValueError("Muon needs a momentum in [0, 1) and 1 to 100 ns_steps")
         if self.scheduler is not None:
             sc = self.scheduler
             if not (0 <= sc["warmup_steps"] < sc["total_steps"]):
@@ -81,8 +97,8 @@ class ZeroConfig:
         if not (cfg.get("bf16") or {"enabled": True}).get("enabled", True):
             raise ValueError("this library keeps weights and gradients in bf16: bf16.enabled must be true")
         opt = cfg.get("optimizer") or {"type": "AdamW", "params": {}}
-        if str(opt.get("type", "AdamW")).lower() != "adamw":
-            raise ValueError(f"optimizer {opt.get('type')!r}: this library implements AdamW")
+        if str(opt.get("type", "AdamW")).lower() not in ("adamw", "muon"):
+            raise ValueError(f"optimizer {opt.get('type')!r}: this library implements AdamW and Muon")
         p = opt.get("params", {})
         scheduler = None
         if cfg.get("scheduler") is not None:
@@ -110,6 +126,10 @@ class ZeroConfig:
             betas=tuple(float(b) for b in p.get("betas", (0.9, 0.999))),
             eps=float(p.get("eps", 1e-8)),
             weight_decay=float(p.get("weight_decay", 0.0)),
+            optimizer=str(opt.get("type", "AdamW")).lower(),
+            momentum=float(p.get("momentum", 0.95)),
+            nesterov=bool(p.get("nesterov", True)),
+            ns_steps=int(p.get("ns_steps", 5)),
             zero_quantized_weights=bool(zo.get("zero_quantized_weights", False)),
             zero_quantized_gradients=bool(zo.get("zero_quantized_gradients", False)),
             overlap_comm=bool(zo.get("overlap_comm", False)),

@@ -9,7 +9,9 @@ sequence of library calls (step.py) that one training step needs:
   Stage 1 accumulates each rank's full gradient locally and reduce-scatters
   once; stage 2 reduce-scatters every micro-batch ("ZeRO and FSDP", the
   paragraph on gradient accumulation).  The last micro-batch is fused into the
-  update unless clipping needs the whole gradient's norm first.
+  update unless clipping needs the whole gradient's norm first.  With the Muon
+  optimizer it takes the tensors' shapes as well: matrices move by their
+  orthogonalised momentum, everything else by AdamW.
 * ``Zero3Engine`` (stage 3, per unit): ``gather(i, phase)`` before a unit's
   forward (phase "fwd") or backward ("bwd"), ``release(i, phase)`` after,
   ``backward(i, grads, micro)`` with the unit's gradient, ``step()`` at the
@@ -83,7 +85,8 @@ class ZeroEngine(_Tracing):
     """Stages 1 and 2 over n_dp simulated ranks of one flat parameter vector."""
 
     def __init__(self, numels, n_dp: int, config: ZeroConfig, master: torch.Tensor | None = None,
-                 device="cuda", align: int = 8):
+                 device="cuda", align: int = 8, shapes=None):
+        """shapes: the tensors' shapes, for the Muon optimizer alone."""
         if config.stage not in (1, 2):
             raise ValueError("ZeroEngine runs stages 1 and 2; use Zero3Engine for stage 3")
         self.cfg = config
@@ -92,8 +95,17 @@ class ZeroEngine(_Tracing):
         if config.zero_quantized_gradients and config.stage == 1 and self.K > 1:
             raise ValueError("stage 1 accumulates locally before it communicates: quantized "
                              "gradients apply to stage 2 or to one micro-batch")
-        self.L = L = zb.zero_layout(numels, n_dp, align, config.reduce_bucket_size)
+        L, offsets = zb.zero_layout(numels, n_dp, align, config.reduce_bucket_size, with_offsets=True)
+        self.L = L
         P = L.padded_n
+        self.muon = None
+        if config.optimizer == "muon":
+            if shapes is None:
+                raise ValueError("the Muon optimizer needs the tensors' shapes")
+            shapes = [tuple(s) for s in shapes]
+            if [torch.Size(s).numel() for s in shapes] != self.numels:
+                raise ValueError("shapes and numels disagree")
+            self.muon = zs.MuonStep(L, offsets, shapes, device)
         self.master = torch.zeros(P, device=device) if master is None else master
         self.m = torch.zeros(P, device=device)
         self.v = torch.zeros(P, device=device)
@@ -120,6 +132,8 @@ class ZeroEngine(_Tracing):
         held = [self.master, self.m, self.v, self.out] + (self.acc or []) + ([self.A] if self.A is not None else [])
         if self.qg is not None:
             held += [self.qg.q, self.qg.scales]
+        if self.muon is not None:
+            held += [self.muon.update, self.muon.workspace]
         return held
 
     @property
@@ -134,7 +148,7 @@ class ZeroEngine(_Tracing):
         rows = [grads[r] for r in range(self.L.n_dp)]
         first = self.micro == 0
         last = self.micro == self.K - 1
-        if self.K == 1 or (last and self.norm is None):
+        if self.K == 1 or (last and self.norm is None and self.muon is None):
             self._last = rows             # fused into step(), or the one micro-batch of a step
         elif self.cfg.stage == 1:
             zs.zero1_accumulate_micro(self.L, rows, self.acc, first)
@@ -159,7 +173,14 @@ class ZeroEngine(_Tracing):
         L, cfg, K = self.L, self.cfg, self.K
         hp = _hp(cfg, self.t + 1)
         n = L.n_dp
-        if self.norm is not None:
+        if self.muon is not None:
+            if K == 1:
+                srcs, dtype = self._last, zb.ZERO_BF16
+            else:
+                srcs, dtype = [self.A] if cfg.stage == 2 else self.acc, zb.ZERO_F32
+            self.muon.run(srcs, dtype, float(n * K), self.master, self.m, self.v, self.out, hp, cfg.lr_at(self.t + 1),
+                          cfg.momentum, cfg.nesterov, cfg.ns_steps)
+        elif self.norm is not None:
             # clipping: the norm of the whole mean gradient first, then the clipped update
             if K == 1 and self.qg is None:
                 zs.zero12_step_clipped(L, self._last, self.master, self.m, self.v, self.out, hp,

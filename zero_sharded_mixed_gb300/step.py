@@ -3,8 +3,8 @@ step, the two gradient-accumulation orders, clipping by the global norm, the
 ZeRO-3 per-unit gather / release / reduce-scatter / update sequence with a
 two-slot ring of gathered buffers (and its prefetching variant), the ZeRO++
 8-bit weight and gradient paths, steps fed from pinned host memory, and
-per-step scalars in device memory for steps replayed from a CUDA graph.  No
-arithmetic happens here; every element is touched only by the library's
+per-step scalars in device memory for steps replayed from a CUDA graph, and the
+step by orthogonalised momentum (Muon).  No arithmetic happens here; every element is touched only by the library's
 kernels.
 
 Buffer conventions (simulated ranks in one GPU):
@@ -105,6 +105,99 @@ class GraphStep:
 
     def replay(self):
         self.graph.replay()
+
+
+# --------------------------------------------------------------------------
+# a step by orthogonalised momentum (Muon)
+# --------------------------------------------------------------------------
+
+def _runs(ranges):
+    """Ranges in order, those that touch joined."""
+    out = []
+    for s, e in ranges:
+        if s == e:
+            continue
+        if out and out[-1][1] == s:
+            out[-1] = (out[-1][0], e)
+        else:
+            out.append((s, e))
+    return out
+
+
+def _batches(offsets, size: int, most: int):
+    """(first, count, stride) of equal matrices at equal distances, at most `most` each."""
+    out = []
+    for o in offsets:
+        if out:
+            first, count, stride = out[-1]
+            if count < most and (count == 1 or o == first + count * stride) and o - first >= size:
+                out[-1] = (first, count + 1, o - first if count == 1 else stride)
+                continue
+        out.append((o, 1, size))
+    return out
+
+
+class MuonStep:
+    """One step of the flat parameter vector in which the matrices (shapes of two
+    dimensions) move by their orthogonalised momentum and everything else by
+    AdamW.  The ranks' gradients are reduced into the owners' momentum m, whose
+    bf16 form is gathered into `update`, orthogonalised there matrix by matrix
+    (equal matrices at equal distances in one call), and moves the owners'
+    master weights, which are cast and gathered.  A matrix of n rows and k
+    columns moves by lr * 0.2 * sqrt(max(n, k)) times its orthogonal factor,
+    which is about AdamW's size, so that one lr serves both (Liu et al., "Muon
+    is scalable for LLM training", 2025).  `workspace_bytes` bounds what a call
+    takes beside one matrix's need.  v of the matrices is not touched."""
+
+    SCALE = 0.2
+
+    def __init__(self, L, offsets, shapes, device="cuda", workspace_bytes: int = 1 << 30):
+        if len(shapes) != len(offsets):
+            raise ValueError(f"need a shape for each of {len(offsets)} tensors, got {len(shapes)}")
+        self.L = L
+        shapes = [tuple(int(x) for x in s) for s in shapes]
+        sizes = []
+        for o, s in zip(offsets, shapes):
+            n = 1
+            for x in s:
+                n *= x
+            sizes.append(n)
+            if o + n > L.n:
+                raise ValueError(f"a tensor of shape {s} at {o} leaves the vector of {L.n} elements")
+        spans = [(o, o + n) for o, n in zip(offsets, sizes)]
+        self.matrices = [(o, s) for o, s, n in zip(offsets, shapes, sizes) if len(s) == 2 and n]
+        matrix = {o for o, _ in self.matrices}
+        self.matrix_runs = _runs([r for r in spans if r[0] in matrix and r[1] > r[0]])
+        self.vector_runs = _runs([r for r in spans if r[0] not in matrix or r[0] == r[1]])
+        self.update = torch.zeros(L.padded_n, dtype=torch.bfloat16, device=device)
+        by_shape = {}
+        for o, s in self.matrices:
+            by_shape.setdefault(s, []).append(o)
+        self.batches, need = [], 0
+        for (n, k), at in by_shape.items():
+            one = zb.zero_orthogonalize_workspace(1, n, k)
+            for first, count, stride in _batches(at, n * k, max(1, workspace_bytes // one)):
+                need = max(need, zb.zero_orthogonalize_workspace(count, n, k))
+                self.batches.append(self.update.as_strided((count, n, k), (stride, k, 1), first))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+
+    def run(self, srcs, src_dtype, divisor, master, m, v, out, adamw: zb.ZeroAdamW, lr: float, momentum: float,
+            nesterov: bool = True, ns_steps: int = 5, stream=None):
+        """srcs: every rank's bf16 gradients, or fp32 sums of them; divisor: what makes
+        them a mean.  adamw.sched, if set, gives lr to the matrices as well."""
+        L, sched = self.L, getattr(adamw, "_sched_tensor", None)
+        for s, e in self.vector_runs:
+            zb.zero_reduce_scatter_adamw(L, srcs, src_dtype, 0, divisor, 0, L.n_dp, s, e, master, m, v, out,
+                                         zb.ZERO_OUT_FULL, adamw, stream)
+        hp = zb.ZeroMuon.make(lr, momentum, adamw.weight_decay, 1.0, nesterov, sched)
+        for s, e in self.matrix_runs:
+            zb.zero_reduce_scatter_momentum(L, srcs, src_dtype, 0, divisor, 0, L.n_dp, s, e, m, self.update,
+                                            zb.ZERO_OUT_FULL, hp, stream)
+        for x in self.batches:
+            zb.zero_orthogonalize(x, x, steps=ns_steps, workspace=self.workspace, stream=stream)
+        for o, (n, k) in self.matrices:
+            hp = zb.ZeroMuon.make(lr, momentum, adamw.weight_decay, self.SCALE * max(n, k) ** 0.5, nesterov, sched)
+            zb.zero_muon_update(L, self.update, 0, 0, L.n_dp, o, o + n * k, master, out, zb.ZERO_OUT_FULL, hp, stream)
 
 
 # --------------------------------------------------------------------------
