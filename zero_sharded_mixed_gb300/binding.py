@@ -920,11 +920,10 @@ def zero_reduce_scatter_momentum(L: ZeroLayout, srcs, src_dtype: int, src_base: 
         state_need = end - rank_begin * L.shard
         out_need = end if out_mode == ZERO_OUT_FULL else state_need
     arr, n = _src_array(srcs, _SRC_DT.get(src_dtype, None), src_need, pinned_ok=True)
-    rc = load().zero_reduce_scatter_momentum(
-        ctypes.byref(L), arr, n, int(src_dtype), int(src_base), float(divisor), int(rank_begin), int(rank_end),
-        int(begin), int(end), _tensor(m, "m", torch.float32, state_need), _tensor(u, "u", torch.bfloat16, out_need),
-        int(out_mode), ctypes.byref(hp), _stream_ptr(stream))
-    _check(rc, "zero_reduce_scatter_momentum")
+    _check(load().zero_reduce_scatter_momentum(L, arr, n, src_dtype, src_base, divisor, rank_begin, rank_end, begin, end,
+                                               _tensor(m, "m", torch.float32, state_need),
+                                               _tensor(u, "u", torch.bfloat16, out_need), out_mode, hp, _stream_ptr(stream)),
+           "zero_reduce_scatter_momentum")
 
 
 def zero_muon_update(L: ZeroLayout, update: torch.Tensor, update_base: int, rank_begin: int, rank_end: int,
@@ -938,11 +937,10 @@ def zero_muon_update(L: ZeroLayout, update: torch.Tensor, update_base: int, rank
         up_need = end - update_base
         state_need = end - rank_begin * L.shard
         out_need = end if out_mode == ZERO_OUT_FULL else state_need
-    rc = load().zero_muon_update(
-        ctypes.byref(L), _tensor(update, "update", torch.bfloat16, up_need), int(update_base), int(rank_begin),
-        int(rank_end), int(begin), int(end), _tensor(master, "master", torch.float32, state_need),
-        _tensor(out, "out", torch.bfloat16, out_need), int(out_mode), ctypes.byref(hp), _stream_ptr(stream))
-    _check(rc, "zero_muon_update")
+    _check(load().zero_muon_update(L, _tensor(update, "update", torch.bfloat16, up_need), update_base, rank_begin, rank_end,
+                                   begin, end, _tensor(master, "master", torch.float32, state_need),
+                                   _tensor(out, "out", torch.bfloat16, out_need), out_mode, hp, _stream_ptr(stream)),
+           "zero_muon_update")
 
 
 def zero_orthogonalize_workspace(batch: int, rows: int, cols: int) -> int:

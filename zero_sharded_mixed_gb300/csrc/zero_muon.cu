@@ -192,7 +192,7 @@ extern "C" int zero_reduce_scatter_momentum(const zero_layout_t* L, const void* 
     if (begin == end) return ZERO_OK;
     for (int r = 0; r < n_src; ++r)
         if (check_source_ptr(src[r])) return ZERO_EINVAL;
-    if (const int rc = check_target_ptrs(t)) return rc;
+    if (check_device_ptr(t.w) || check_device_ptr(t.out)) return ZERO_EINVAL;
     p.m = t.w;
     p.u = t.out;
     p.n = t.n;
@@ -225,8 +225,7 @@ extern "C" int zero_muon_update(const zero_layout_t* L, const uint16_t* update, 
     if (!update || update_base > begin || update_base < 0) return ZERO_EINVAL;
     if (check_aligned(update, 2)) return ZERO_EALIGN;
     if (begin == end) return ZERO_OK;
-    if (check_device_ptr(update) || (p.h.sched && check_device_ptr(p.h.sched))) return ZERO_EINVAL;
-    if (const int rc = check_target_ptrs(t)) return rc;
+    if (check_device_ptr(update) || (p.h.sched && check_device_ptr(p.h.sched)) || check_device_ptr(t.w) || check_device_ptr(t.out)) return ZERO_EINVAL;
     p.o = update + (begin - update_base);
     p.w = t.w;
     p.out = t.out;

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kHeldThreads, 1) orthogonal_held_kernel(const 
 // ---- products --------------------------------------------------------------------------------
 // Pairs of CTAs on 256 x bn tiles, as for the large dense products: warp 0 copies, warp 1
 // of the even CTA issues, warps 4..19 end the last tile meanwhile.  A symmetric result is
-// computed for the tiles that reach below its diagonal and written to both sides.
+// computed for the tiles that reach above its diagonal and written to both sides.
 enum Step { kGram, kSquare, kApply };
 
 // What the end of a step reads and writes.
@@ -292,22 +292,34 @@ constexpr int kStepSmem = 1024 + kStages * kStageBytes + 256;
 struct Place {
     int z, tm, tn;
 };
+// The order of the tiles.  kApply goes through X once: a wide X column by column, a tall
+// one row by row, the rows or columns of B together.  A symmetric result has of row tile
+// i the column tiles from its own columns on, so that the narrow last tiles are as many
+// as can be; and its matrices are taken last to first, since what the last step wrote
+// last is still in L2 (and what this one read last will be when X is read again).
 template <Step kStep>
 __device__ __forceinline__ Place place_of(const StepParams& p, int t) {
     Place w;
     w.z = t / p.tiles;
     t -= w.z * p.tiles;
     if (kStep == kApply) {
-        w.tm = t / p.tiles_n;
-        w.tn = t - w.tm * p.tiles_n;
-    } else {   // row tile i has the column tiles up to its own columns' end
+        if (p.e.tall) {
+            w.tm = t / p.tiles_n;
+            w.tn = t - w.tm * p.tiles_n;
+        } else {
+            const int tiles_m = (p.e.rows + 255) / 256;
+            w.tn = t / tiles_m;
+            w.tm = t - w.tn * tiles_m;
+        }
+    } else {
         const int step = 256 / p.bn;
-        int n = step < p.tiles_n ? step : p.tiles_n;
+        int n = p.tiles_n;
         for (w.tm = 0; t >= n; ++w.tm) {
             t -= n;
-            n = n + step < p.tiles_n ? n + step : p.tiles_n;
+            n -= step;
         }
-        w.tn = t;
+        w.tn = w.tm * step + t;
+        w.z = p.all / p.tiles - 1 - w.z;
     }
     return w;
 }
@@ -342,18 +354,21 @@ struct StepEnd {
                 hi[h] = lo[h] = make_uint4(0u, 0u, 0u, 0u);
                 if (row < p.rows) {
                     hi[h] = *reinterpret_cast<const uint4*>(p.c_hi + at);
-                    if (kStep == kApply && p.c_lo) lo[h] = *reinterpret_cast<const uint4*>(p.c_lo + at);
+                    if (kStep == kApply && p.c_lo) lo[h] = ld_live_u4(p.c_lo + at);   // read once
                     if (kStep == kApply && !p.tall) f[h] = p.factors[z * p.factor_stride + row];
                 }
             }
         }
     }
+    template <bool kOnce = false>   // kOnce: nothing else reads it soon
     __device__ __forceinline__ static void store(uint16_t* q, int64_t ld, int rows_left, uint32_t (&a)[4], uint32_t (&b)[4]) {
         const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
         quad_transpose(a);
         quad_transpose(b);
-        if (i < rows_left) *reinterpret_cast<uint4*>(q + i * ld + 8 * j) = make_uint4(a[0], a[1], a[2], a[3]);
-        if (i + 8 < rows_left) *reinterpret_cast<uint4*>(q + (i + 8) * ld + 8 * j) = make_uint4(b[0], b[1], b[2], b[3]);
+        uint4* to = reinterpret_cast<uint4*>(q + i * ld + 8 * j);
+        uint4* below = reinterpret_cast<uint4*>(q + (i + 8) * ld + 8 * j);
+        if (i < rows_left) kOnce ? __stcs(to, make_uint4(a[0], a[1], a[2], a[3])) : (void)(*to = make_uint4(a[0], a[1], a[2], a[3]));
+        if (i + 8 < rows_left) kOnce ? __stcs(below, make_uint4(b[0], b[1], b[2], b[3])) : (void)(*below = make_uint4(b[0], b[1], b[2], b[3]));
     }
     __device__ __forceinline__ void finish(const StepEnding& p, int z, int row0, int col0, bool mirror, float (&v)[4][4]) {
         const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
@@ -439,7 +454,7 @@ struct StepEnd {
                 e[g] = pack_f16x2((v[g][0] - t.x) * kLo, (v[g][1] - t.y) * kLo);
                 g2[g] = pack_f16x2((v[g][2] - u.x) * kLo, (v[g][3] - u.y) * kLo);
             }
-            store(p.d_lo + at, p.ld, p.rows - row0, e, g2);
+            store<true>(p.d_lo + at, p.ld, p.rows - row0, e, g2);
         } else if (mirror) {
             // transposed, a lane has two rows of column i of each group of eight: after the
             // exchange, column 8 j + i and all eight rows
@@ -586,7 +601,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             const int chunks_n = width_of(p, w.tn) / 32, first = (h >> 1) * ((chunks_n + 1) / 2);
             const int units = h >> 1 ? chunks_n - first : (chunks_n + 1) / 2;   // of this warp
             const int row0 = w.tm * 256 + (int)rank * 128 + q * 32 + (h & 1) * 16, buf = use & 1;
-            const bool mirror = (w.tn + 1) * p.bn <= w.tm * 256, mine = row0 < p.e.rows;
+            const bool mirror = w.tn * p.bn >= (w.tm + 1) * 256, mine = row0 < p.e.rows;
             const int col_first = w.tn * p.bn + first * 32;
             // what a unit's end reads is on its way while the unit before it, or the
             // tile's product, is finished
@@ -665,7 +680,7 @@ static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, 
         int64_t tiles = tm * tn;
         if (step != kApply) {
             tiles = 0;
-            for (int64_t i = 1; i <= tm; ++i) tiles += i * (256 / bn) < tn ? i * (256 / bn) : tn;
+            for (int64_t i = 0; i < tm; ++i) tiles += tn - i * (256 / bn);
         }
         if (tiles > INT32_MAX / 4 / batch) continue;
         const int64_t waves = (tiles * batch + pairs - 1) / pairs;
