@@ -792,22 +792,6 @@ static int lay_slots(NormParams& p, const NormShape& s, bool vec, const int (&si
     return (int)p.slot * (p.ahead + 1);
 }
 
-// Has a kernel run with an SM's memory split as its neighbours have it, most of it shared:
-// a change of the split between two kernels waits for the SM to be empty.
-static int keep_split(const void* kernel, Done& done) {
-    int dev = 0;
-    if (!device_below(64, &dev)) return ZERO_ECUDA;
-    if (done[dev].load(std::memory_order_acquire)) return ZERO_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) {
-        note_cuda_error(e);
-        (void)cudaGetLastError();
-        return ZERO_ECUDA;
-    }
-    done[dev].store(true, std::memory_order_release);
-    return ZERO_OK;
-}
-
 template <bool kF32, bool kVec, int kPer, int kThreads, bool kMany>
 static int launch_norm(NormParams& p, const NormShape& s, cudaStream_t stream) {
     static Done done;
@@ -966,8 +950,6 @@ extern "C" int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, 
             rc = vec ? launch_norm_grad<true, false, true>(p, shape, s) : launch_norm_grad<true, false, false>(p, shape, s);
     }
     if (rc != ZERO_OK || !weights) return rc;
-    static Done split;
-    if (const int kept = keep_split((const void*)norm_finish_kernel, split)) return kept;
     FinishParams q{};
     q.part = p.part; q.parts = (int32_t)parts; q.cols = (int32_t)cols;
     q.acc[0] = dgamma_acc; q.acc[1] = dbeta_acc;

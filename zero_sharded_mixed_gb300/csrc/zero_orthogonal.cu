@@ -690,19 +690,25 @@ static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, 
     return best;
 }
 
+// A step's launch but for its end, which changes from iteration to iteration: formed
+// before the first launch, so that a call that cannot be made has launched nothing.
 template <Step kStep>
-static int launch_step(StepParams& q, const Matrices& a, bool a_mn, const Matrices& b, bool b_mn, cudaStream_t s) {
+static int prepare_step(StepParams& q, int64_t rows, int64_t cols, int64_t depth, const Matrices& a, bool a_mn, const Matrices& b, bool b_mn) {
     static Done done;
     if (const int rc = allow_smem((const void*)orthogonal_step_kernel<kStep>, kStepSmem, done)) return rc;
-    const StepPlan plan = plan_step(kStep, q.e.rows, q.e.cols, q.depth, a.batch);
+    const StepPlan plan = plan_step(kStep, rows, cols, depth, a.batch);
     if (!plan.bn) return ZERO_ERANGE;
+    q.depth = (int32_t)depth;
     q.bn = plan.bn;
     q.tiles_n = plan.tiles_n;
     q.tiles = (int32_t)plan.tiles;
     q.all = (int32_t)(plan.tiles * a.batch);
-    q.k_blocks = (q.depth + 63) / 64;
+    q.k_blocks = (int32_t)((depth + 63) / 64);
     q.a_mn = a_mn; q.b_mn = b_mn;
-    if (!make_map3(a, a_mn ? 64 : 128, &q.map_a) || !make_map3(b, b_mn ? 64 : q.bn / 2, &q.map_b)) return ZERO_ECUDA;
+    return make_map3(a, a_mn ? 64 : 128, &q.map_a) && make_map3(b, b_mn ? 64 : q.bn / 2, &q.map_b) ? ZERO_OK : ZERO_ECUDA;
+}
+template <Step kStep>
+static int launch_step(const StepParams& q, cudaStream_t s) {
     const int64_t pairs = sm_pairs();
     return launch_dense(orthogonal_step_kernel<kStep>, dim3((unsigned)(2 * (q.all < pairs ? q.all : pairs))), kStepThreads, 2, true, kStepSmem,
                         s, q);
@@ -804,7 +810,7 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     e.factors = reinterpret_cast<float2*>(base + w.factors); e.factor_stride = w.lds;
     e.scale = src.scale;
     e.a = coefficients[0]; e.b = coefficients[1]; e.c = coefficients[2];
-    const int32_t longer = (int32_t)(tall ? rows : cols);
+    const int64_t longer = tall ? rows : cols;
     // the end of a step of iteration i
     const auto ending = [&](Step step, int i) {
         StepEnding d = e;
@@ -825,7 +831,18 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
         }
         return d;
     };
-    const bool y_vec = rows_aligned16(y, ldy, 2) && (batch == 1 || y_stride % 8 == 0);
+    // X stands in two places in turn
+    StepParams gram_step[2]{}, square_step{}, apply_step[2]{};
+    if (const int rc = prepare_step<kSquare>(square_step, side, side, side, gram, false, gram, false)) return rc;
+    for (int i = 0; i < 2; ++i) {
+        const Matrices& now = i ? second : first;
+        if (const int rc = prepare_step<kGram>(gram_step[i], side, side, longer, now, tall, now, tall)) return rc;
+        // wide: B X, X read along its rows; tall: X B, B being its own transpose
+        if (const int rc = tall ? prepare_step<kApply>(apply_step[i], rows, cols, side, now, false, poly, false)
+                                : prepare_step<kApply>(apply_step[i], rows, cols, side, poly, false, now, true))
+            return rc;
+    }
+
     if (rows * (int64_t)src.groups <= kHeldGroups) {
         if (const int rc = launch_dense(orthogonal_held_kernel, dim3((unsigned)(kHeldCtas * batch)), kHeldThreads, kHeldCtas, true, 0, s, src)) return rc;
     } else {
@@ -834,18 +851,17 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
         if (const int rc = launch_dense(orthogonal_source_kernel, grid, kSourceThreads, 1, true, 0, s, src)) return rc;
     }
     for (int i = 0; i < steps; ++i) {
-        const Matrices& now = i & 1 ? second : first;
-        StepParams q{};
-        q.e = ending(kGram, i);
-        q.depth = longer;
-        if (const int rc = launch_step<kGram>(q, now, tall, now, tall, s)) return rc;
-        q.e = ending(kSquare, i);
-        q.depth = (int32_t)side;
-        if (const int rc = launch_step<kSquare>(q, gram, false, gram, false, s)) return rc;
-        q.e = ending(kApply, i);
-        if (i + 1 == steps) q.e.y = y, q.e.ldy = ldy, q.e.y_stride = batch > 1 ? y_stride : 0, q.e.y_vec = y_vec;
-        // wide: B X, X read along its rows; tall: X B, B being its own transpose
-        if (const int rc = tall ? launch_step<kApply>(q, now, false, poly, false, s) : launch_step<kApply>(q, poly, false, now, true, s)) return rc;
+        StepParams &g = gram_step[i & 1], &a = apply_step[i & 1];
+        g.e = ending(kGram, i);
+        if (const int rc = launch_step<kGram>(g, s)) return rc;
+        square_step.e = ending(kSquare, i);
+        if (const int rc = launch_step<kSquare>(square_step, s)) return rc;
+        a.e = ending(kApply, i);
+        if (i + 1 == steps) {
+            a.e.y = y; a.e.ldy = ldy; a.e.y_stride = batch > 1 ? y_stride : 0;
+            a.e.y_vec = rows_aligned16(y, ldy, 2) && (batch == 1 || y_stride % 8 == 0);
+        }
+        if (const int rc = launch_step<kApply>(a, s)) return rc;
     }
     return ZERO_OK;
 }
