@@ -109,6 +109,20 @@ def test_in_place(zlib, cuda_device, shape):
     assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("shape", [(48, 80), (270, 131)])
+def test_side_by_side(zlib, cuda_device, shape):
+    """Matrices that are column blocks of a wider one, orthogonalised one by one, in place too."""
+    rows, cols = shape
+    x = _x((3, rows, cols), BF, 2).cuda()
+    y = _run(zlib, x)
+    wide = torch.full((rows, 3 * cols + 5), dp.SENTINEL, dtype=BF, device="cuda")
+    blocks = wide[:, :3 * cols].view(rows, 3, cols).transpose(0, 1)
+    blocks.copy_(x)
+    ws = torch.empty(zlib.zero_orthogonalize_workspace(3, *shape), dtype=torch.uint8, device="cuda")
+    zlib.zero_orthogonalize(blocks, blocks, workspace=ws)
+    assert torch.equal(blocks, y) and bool((wide[:, 3 * cols:] == dp.SENTINEL).all())
+
+
 @pytest.mark.parametrize("shape", [(24, 40), (300, 270)])
 @pytest.mark.parametrize("steps,coefficients", [(1, (1.5, -0.5, 0.0)), (8, (1.5, -0.5, 0.0)), (3, (2.0, -1.5, 0.5)), (1, npl.NS), (2, npl.NS),
                                                 (0, npl.NS)])

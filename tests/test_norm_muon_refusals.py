@@ -90,7 +90,8 @@ def test_layer_norm_grad(lib, kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     ({}, OK), ({"dtype": 1}, OK), ({"xs": 0}, OK), ({"y": A}, OK), ({"eps": 0.0}, OK), ({"batch": 1, "xs": -5, "ys": 0}, OK), ({"rows": 300, "xs": 21600, "ys": 21600}, OK),
-    ({"x": A + 2, "ldx": 73, "xs": 9999}, OK),
+    ({"x": A + 2, "ldx": 73, "xs": 9999}, OK), ({"ldy": 144, "ys": 72}, OK), ({"ldy": 143, "ys": 72}, EINVAL), ({"ldy": 144, "ys": 71}, EINVAL),
+    ({"ys": -1}, EINVAL),
     ({"batch": -1}, EINVAL), ({"rows": -1}, EINVAL), ({"cols": -1}, EINVAL), ({"dtype": 2}, EINVAL), ({"steps": 0}, EINVAL), ({"steps": 101}, EINVAL),
     ({"co": None}, EINVAL), ({"co": (1.0, NAN, 0.0)}, EINVAL), ({"co": (INF, 1.0, 0.0)}, EINVAL), ({"eps": -1.0}, EINVAL), ({"eps": NAN}, EINVAL),
     ({"x": None}, EINVAL), ({"y": None}, EINVAL), ({"ws": None}, EINVAL), ({"ldx": 71}, EINVAL), ({"ldy": 71}, EINVAL), ({"xs": -1}, EINVAL),

@@ -774,8 +774,10 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     if (const int rc = check_matrix(y, rows, cols, ldy, ZERO_BF16)) return rc;
     if (batch > 1) {
         const int64_t most = INT64_MAX / 8 / batch, extent = (rows - 1) * ldy + cols;
-        if (x_stride < 0 || y_stride < extent) return ZERO_EINVAL;   // results that overlap
+        if (x_stride < 0 || y_stride < 0) return ZERO_EINVAL;
         if (x_stride > most || y_stride > most) return ZERO_ERANGE;
+        // results lie one behind the other, or side by side in the rows of a wider matrix
+        if (y_stride < extent && (y_stride < cols || (batch - 1) * y_stride + cols > ldy)) return ZERO_EINVAL;
     }
     if (batch > 65535) return ZERO_ERANGE;
     OrthogonalSpace w{};
