@@ -602,19 +602,20 @@ int zero_rope(const zero_rope_plan_t* plan, int64_t tokens, int64_t heads, int64
  *   residual and sum are NULL (both or neither);
  *   y = (h - mean) rstd gamma + beta, mean and 1 / sqrt(variance + eps) over a row.
  *   x, residual and sum are dtype, y is dtype or bf16, gamma and beta (or NULL: 1, 0)
- *   bf16 [cols], mean and rstd (or NULL) fp32 [rows].  sum may be x or residual itself
- *   (same ld); outputs overlap no other argument.
+ *   bf16 [cols], mean and rstd (or NULL) fp32 [rows].  sum may be x or residual itself,
+ *   and y be x (same type and ld); outputs overlap nothing else.
  * zero_layer_norm_grad: with xhat = (x - mean) rstd and g = dy gamma,
  *   dx = residual + rstd (g - avg(g) - xhat avg(g xhat)), averages over a row;
  *   dgamma = dgamma_acc + sum over rows of dy xhat,  dbeta = dbeta_acc + sum of dy.
  *   x is what was normalised (the forward call's sum, where it had a residual), mean and
  *   rstd what it kept; x, residual (or NULL) and dx are dtype, dy is dtype or bf16, the
  *   weights' gradients and accumulators (each or all NULL) weight_dtype.  dx may be
- *   residual itself (same ld), dgamma dgamma_acc, dbeta dbeta_acc.
+ *   residual, dy or x itself (same type and ld), dgamma dgamma_acc, dbeta dbeta_acc.
  *   workspace: device, 16-byte aligned, of zero_layer_norm_grad_workspace bytes for these
  *   sizes on the current device; needed where dgamma or dbeta is asked for.  Calls that
  *   share one must not overlap on the GPU.
- * Sums are fp32 in an order that sizes and device fix: results repeat.  No columns: the
+ * Sums are fp32 in an order that sizes and device fix: results repeat.  A row's sum and
+ * the sum of its squared deviations have to lie in fp32's range.  No columns: the
  * calls do nothing; no rows: the weights' gradients are their accumulators, or 0.
  * Errors: ZERO_EINVAL (negative size, ld below the columns, types, eps negative or not
  *   finite, a null or non-device pointer, residual without sum), ZERO_ERANGE (more than
@@ -653,7 +654,7 @@ int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, int64_t ldd
  *   (the Gram matrix of the shorter side).  With (3.4445, -4.7750, 2.0315) and 5 steps the
  *   singular values of U come to within about 0.3 of 1 and its singular vectors stay.
  *   x is x_dtype, matrices x_stride elements apart (any stride >= 0), y bf16, y_stride
- *   apart and not overlapping; rows ldx and ldy apart.  y may be x itself.  Any
+ *   apart, one behind the other or side by side in rows of ldy; rows ldx and ldy apart.  y may be x itself.  Any
  *   element-aligned place.  A matrix of zeros gives zeros; one that is not finite NaN.
  *   The products take fp16 operands with fp32 sums, on two fp16 numbers for each element
  *   of X: with steps and coefficients like these the result is about 1e-3 off the exact

@@ -112,6 +112,47 @@ def test_forward_special_rows(zlib, cuda_device):
     assert abs(float(rstd[3]) * 1e-5 ** 0.5 - 1) < 1e-5
 
 
+@pytest.mark.parametrize("cols", [3, 24, 57, 513, 1601, 6400, 17001])
+@pytest.mark.parametrize("value", [3.3e10, -7.1e13, 1e17])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_forward_rows_of_one_large_value(zlib, cuda_device, cols, value, out):
+    """No deviation: rounding must not make the variance negative.  The number that stands
+    for the mean at first is off by at most 2^-17 of the value (64 additions and the
+    share), what corrects it by 2^-17 of that, and eps alone makes rstd at most eps^-1/2."""
+    x = torch.full((3, cols), value, device="cuda")
+    x[1] = 1.0
+    y, stat = torch.empty(3, cols, dtype=out, device="cuda"), torch.empty(2, 3, device="cuda")
+    zlib.zero_layer_norm(x, y, eps=1e-5, mean=stat[0], rstd=stat[1])
+    assert bool((y.double().abs() <= 2.0 ** -34 * x.double().abs() * 1.01e-5 ** -0.5).all())
+    assert bool((stat[1] <= 1.001 * 1e-5 ** -0.5).all()) and bool((stat[1] > 0).all())
+    dp.close(stat[0].cpu(), x[:, 0].cpu().double(), 2.0 ** -23 * x[:, 0].cpu().double().abs(), "mean")
+
+
+@pytest.mark.parametrize("shape", [(70, 16), (257, 65), (333, 1600), (77, 1601), (31, 6401), (3, 16391), (5, 16392), (9, 20001)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_in_place(zlib, cuda_device, shape, dtype):
+    """y over x; dx over dy, over x and over the residual: as beside them."""
+    x, res, gamma, beta, dy = (t.cuda() for t in _inputs(*shape, dtype, 6))
+    dy = dy.to(dtype)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(shape[0], device="cuda"), torch.empty(shape[0], device="cuda")
+    ws = torch.empty(zlib.zero_layer_norm_grad_workspace(*shape), dtype=torch.uint8, device="cuda")
+    zlib.zero_layer_norm(x, y, gamma, beta, mean=mean, rstd=rstd)
+    over = x.clone()
+    zlib.zero_layer_norm(over, over, gamma, beta)
+    assert torch.equal(over, y)
+
+    def grads(dy, x, res, dx):
+        dg, db = torch.empty(shape[1], device="cuda"), torch.empty(shape[1], device="cuda")
+        zlib.zero_layer_norm_grad(dy, x, mean, rstd, dx, gamma, residual=res, dgamma=dg, dbeta=db, workspace=ws)
+        return dx, dg, db
+
+    want = grads(dy, x, res, dx)
+    for i in range(3):
+        args = [t.clone() for t in (dy, x, res)]
+        assert all(torch.equal(a, b) for a, b in zip(grads(*args, args[i]), want)), i
+
+
 def test_forward_in_place_sum(zlib, cuda_device):
     x, res, gamma, beta, _ = (t.cuda() for t in _inputs(120, 1600, BF, 4))
     for cols in (1600, 40):

@@ -845,7 +845,7 @@ def zero_layer_norm(x, y, gamma=None, beta=None, eps: float = 1e-5, residual=Non
     """sum = x + residual (both or neither given) and y = (sum - mean) rstd gamma + beta
     over the rows of a matrix; mean and rstd (fp32, one a row), if given, receive the
     statistics for the gradient.  x, residual and sum are bf16 or fp32 alike, y the same
-    or bf16, gamma and beta bf16."""
+    or bf16, gamma and beta bf16.  sum may be x or residual itself, y may be x."""
     rows, cols = _sizes(x, "x")
     xp, ldx, code = _matrix(x, "x", rows, cols, _DT_CODE)
     yp, ldy, ycode = _matrix(y, "y", rows, cols, _DT_CODE)
@@ -874,9 +874,10 @@ def zero_layer_norm_grad(dy, x, mean, rstd, dx, gamma=None, residual=None, dgamm
                          dgamma_acc=None, dbeta_acc=None, workspace=None, stream=None):
     """dx = residual + the gradient of zero_layer_norm by its input x (the sum, where it
     had a residual), dgamma = dgamma_acc + and dbeta = dbeta_acc + those by its weights.
-    x, residual and dx are bf16 or fp32 alike, dy the same or bf16; dgamma, dbeta and
-    what they are added to (which may be themselves) have one type.  workspace: a CUDA
-    tensor of zero_layer_norm_grad_workspace(rows, cols) bytes, where dgamma or dbeta is given."""
+    x, residual and dx (which may be residual, dy or x itself) are bf16 or fp32 alike,
+    dy the same or bf16; dgamma, dbeta and what they are added to (which may be
+    themselves) have one type.  workspace: a CUDA tensor of
+    zero_layer_norm_grad_workspace(rows, cols) bytes, where dgamma or dbeta is given."""
     rows, cols = _sizes(x, "x")
     xp, ldx, code = _matrix(x, "x", rows, cols, _DT_CODE)
     dp, lddy, dcode = _matrix(dy, "dy", rows, cols, _DT_CODE)

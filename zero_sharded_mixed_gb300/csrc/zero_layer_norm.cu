@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
                 squares += w[i].squares + w[i].n * t * t;
             }
         }
+        if (squares < 0.0f) squares = 0.0f;   // rounding, where all columns are alike; not of NaN
         const float rstd = 1.0f / sqrtf(squares * (1.0f / (float)p.cols) + p.eps);
         if (!has) continue;
         if (m.t == 0) {
@@ -636,7 +637,8 @@ __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormParam
             v[1] += d * d;
         }
         cta_sums<2>(v, sums, turn);
-        const float off = v[0] * share, rstd = 1.0f / sqrtf(v[1] * share - off * off + p.eps);
+        const float off = v[0] * share, square = v[1] * share - off * off;
+        const float rstd = 1.0f / sqrtf((square < 0.0f ? 0.0f : square) + p.eps);   // as above
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[row] = mean + off;
             if (p.rstd) p.rstd[row] = rstd;
@@ -931,11 +933,12 @@ extern "C" int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, 
         // the sums are empty
     } else if (cols > kWidestNorm) {
         const int64_t most = 4 * (int64_t)sm_count();
-        rc = launch_dense(!f32 ? norm_grad_wide_kernel<false, false> : dy_f32 ? norm_grad_wide_kernel<true, true> : norm_grad_wide_kernel<true, false>,
-                          dim3((unsigned)(rows < most ? rows : most)), kWideThreads, 1, true, 0, s, p);
-        if (rc == ZERO_OK && parts)
+        if (parts)   // first: dx may be dy or x
             rc = launch_dense(!f32 ? norm_columns_kernel<false, false> : dy_f32 ? norm_columns_kernel<true, true> : norm_columns_kernel<true, false>,
                               dim3((unsigned)((cols + 255) / 256), (unsigned)parts), 256, 1, true, 0, s, p);
+        if (rc == ZERO_OK)
+            rc = launch_dense(!f32 ? norm_grad_wide_kernel<false, false> : dy_f32 ? norm_grad_wide_kernel<true, true> : norm_grad_wide_kernel<true, false>,
+                              dim3((unsigned)(rows < most ? rows : most)), kWideThreads, 1, true, 0, s, p);
     } else {
         const bool vec = cols % 8 == 0 && rows_aligned16(x, ldx, size) && rows_aligned16(dy, lddy, dtype_size(dy_dtype)) &&
                          rows_aligned16(dx, lddx, size) && (!residual || rows_aligned16(residual, ldr, size));
