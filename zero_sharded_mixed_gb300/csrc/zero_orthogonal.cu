@@ -257,20 +257,24 @@ __global__ void __launch_bounds__(kHeldThreads, 1) orthogonal_held_kernel(const 
 // Pairs of CTAs on 256 x bn tiles, as for the large dense products: warp 0 copies, warp 1
 // of the even CTA issues, warps 4..19 end the last tile meanwhile.  A symmetric result is
 // computed for the tiles that reach above its diagonal and written to both sides.
-enum Step { kGram, kSquare, kApply };
+enum Step { kGram, kSquare, kApplyWide, kApplyTall };
+constexpr bool applies(Step s) { return s == kApplyWide || s == kApplyTall; }
+template <Step kStep> constexpr bool kApplies = applies(kStep);
 
 // What the end of a step reads and writes.
 struct StepEnding {
     int32_t rows, cols;                    // of the result
-    bool first, tall;                      // first: X = scale * hi
+    bool first;                            // X = scale * (hi + lo / 2^11)
     int64_t ld, stride;                    // rows of a matrix, and matrices, of all of c and d
-    const uint16_t* c_hi;                  // kSquare: A; kApply: X
+    const uint16_t* c_hi;                  // kSquare: A; else X
     const uint16_t* c_lo;                  // or null
     uint16_t* d_hi;                        // A, B or the next X
     uint16_t* d_lo;
-    uint16_t* y; int64_t ldy, y_stride;    // kApply, last: bf16 in place of d
+    uint16_t* y; int64_t ldy, y_stride;    // the last X: bf16 in place of d
     bool y_vec;
-    float2* factors; int64_t factor_stride;   // a + B_ii - fp16(B_ii), a + B_ii
+    float* f_hi;                           // scale (a + B_ii - fp16(B_ii))
+    float* f_lo;                           // scale (a + B_ii) / 2^11
+    int64_t factor_stride;
     const float* scale;
     float a, b, c;
 };
@@ -287,12 +291,13 @@ constexpr int kStageBytes = 32768;      // 128 rows of A and 128 of B, 64 reduce
 constexpr int kStages = 6;
 constexpr int kEndWarps = 16;
 constexpr int kStepThreads = 128 + 32 * kEndWarps;
-constexpr int kStepSmem = 1024 + kStages * kStageBytes + 256;
+constexpr int kUnitBytes = 1024;        // 16 rows x 32 columns: an ending warp has two, for hi and lo
+constexpr int kStepSmem = 1024 + kStages * kStageBytes + 256 + kEndWarps * 2 * kUnitBytes;
 
 struct Place {
     int z, tm, tn;
 };
-// The order of the tiles.  kApply goes through X once: a wide X column by column, a tall
+// The order of the tiles.  X' goes through X once: a wide X column by column, a tall
 // one row by row, the rows or columns of B together.  A symmetric result has of row tile
 // i the column tiles from its own columns on, so that the narrow last tiles are as many
 // as can be; and its matrices are taken last to first, since what the last step wrote
@@ -302,15 +307,13 @@ __device__ __forceinline__ Place place_of(const StepParams& p, int t) {
     Place w;
     w.z = t / p.tiles;
     t -= w.z * p.tiles;
-    if (kStep == kApply) {
-        if (p.e.tall) {
-            w.tm = t / p.tiles_n;
-            w.tn = t - w.tm * p.tiles_n;
-        } else {
-            const int tiles_m = (p.e.rows + 255) / 256;
-            w.tn = t / tiles_m;
-            w.tm = t - w.tn * tiles_m;
-        }
+    if constexpr (kStep == kApplyTall) {
+        w.tm = t / p.tiles_n;
+        w.tn = t - w.tm * p.tiles_n;
+    } else if constexpr (kStep == kApplyWide) {
+        const int tiles_m = (p.e.rows + 255) / 256;
+        w.tn = t / tiles_m;
+        w.tm = t - w.tn * tiles_m;
     } else {
         const int step = 256 / p.bn;
         int n = p.tiles_n;
@@ -328,102 +331,174 @@ __device__ __forceinline__ int width_of(const StepParams& p, int tn) {   // colu
     return left >= p.bn ? p.bn : (left + 31) / 32 * 32;
 }
 
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
-    uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
+// A unit of 16 rows x 32 columns of 16 bits is ended by a warp.  In registers a lane 4 i + j
+// has the pairs of columns 8 g + 2 j, + 1 of rows i + 8 h, as the accumulator gives them
+// (v[g][2 h], v[g][2 h + 1]); memory is read and written in 16-byte vectors, columns 8 j
+// .. + 7 of those rows.  One becomes the other in the warp's own shared memory, by
+// the matrix loads and stores: rows of 64 bytes whose vectors are exchanged so that neither
+// side has two accesses to a bank.  (By shuffles and selections that took 16 instructions
+// for four, and a third of the time of a product that reads and writes both halves of X.)
+struct UnitPlace {
+    uint32_t base, vec, frag, turned;   // shared addresses: of this lane's vector, of the row it names to a matrix access, of that in the transpose
+    __device__ __forceinline__ explicit UnitPlace(uint32_t base) : base(base) {
+        const uint32_t lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3, g = lane >> 3, r = lane & 7;
+        vec = base + i * 64 + 16 * (j ^ (i >> 1 & 3));
+        frag = base + r * 64 + 16 * (g ^ (r >> 1 & 3));
+        turned = base + lane * 32 + 16 * (r >> 2);   // rows of 32 bytes: of column `lane`
+    }
+};
+__device__ __forceinline__ void unit_store(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 unit_load(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void matrix_load(uint32_t at, uint32_t (&f)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void matrix_store(uint32_t at, const uint32_t (&f)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
+}
+__device__ __forceinline__ void matrix_store_turned(uint32_t at, const uint32_t (&f)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
 }
 
-// 16 rows x 32 columns of the result from row0, col0, a warp together: lane 4 i + j has
-// columns 8 g + 2 j, + 1 of rows i (v[g][0..1]) and i + 8 (v[g][2..3]).  What moves in
-// 16-byte vectors, a lane a group of eight, is exchanged between the four lanes of a row.
 // Matrices of the workspace have rows of whole units, so that only rows are checked.
 template <Step kStep>
 struct StepEnd {
-    uint4 hi[2], lo[2];
-    float2 f[2];
-    float s;
-    __device__ __forceinline__ void load(const StepEnding& p, int z, int row0, int col0) {
-        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
+    uint4 hi[2], lo[2];            // a unit's on their way, this lane's vectors
+    float s, f_hi[2], f_lo[2];     // of a tile: the scale; kApplyWide: the rows' factors; kApplyTall: [0] of the unit's column `lane`, on their way
+    __device__ __forceinline__ void tile(const StepEnding& p, int z, int row0) {
         s = p.first ? p.scale[z] : 1.0f;
-        if constexpr (kStep != kGram) {
+        if constexpr (kStep == kApplyWide) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int row = row0 + i + 8 * h;
-                const int64_t at = z * p.stride + row * p.ld + col0 + 8 * j;
-                hi[h] = lo[h] = make_uint4(0u, 0u, 0u, 0u);
-                if (row < p.rows) {
-                    hi[h] = *reinterpret_cast<const uint4*>(p.c_hi + at);
-                    if (kStep == kApply && p.c_lo) lo[h] = ld_live_u4(p.c_lo + at);   // read once
-                    if (kStep == kApply && !p.tall) f[h] = p.factors[z * p.factor_stride + row];
-                }
+                const int row = row0 + ((threadIdx.x & 31) >> 2) + 8 * h;
+                const int64_t at = z * p.factor_stride + row;
+                f_hi[h] = row < p.rows ? p.f_hi[at] : 0.0f;
+                f_lo[h] = row < p.rows ? p.f_lo[at] : 0.0f;
             }
         }
     }
-    template <bool kOnce = false>   // kOnce: nothing else reads it soon
-    __device__ __forceinline__ static void store(uint16_t* q, int64_t ld, int rows_left, uint32_t (&a)[4], uint32_t (&b)[4]) {
-        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
-        quad_transpose(a);
-        quad_transpose(b);
-        uint4* to = reinterpret_cast<uint4*>(q + i * ld + 8 * j);
-        uint4* below = reinterpret_cast<uint4*>(q + (i + 8) * ld + 8 * j);
-        if (i < rows_left) kOnce ? __stcs(to, make_uint4(a[0], a[1], a[2], a[3])) : (void)(*to = make_uint4(a[0], a[1], a[2], a[3]));
-        if (i + 8 < rows_left) kOnce ? __stcs(below, make_uint4(b[0], b[1], b[2], b[3])) : (void)(*below = make_uint4(b[0], b[1], b[2], b[3]));
+    __device__ __forceinline__ void load(const StepEnding& p, int z, int row0, int col0) {
+        if constexpr (kStep != kGram) {
+            const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
+            const int64_t at = z * p.stride + (row0 + i) * p.ld + col0 + 8 * j;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                hi[h] = lo[h] = make_uint4(0u, 0u, 0u, 0u);
+                if (row0 + i + 8 * h < p.rows) {
+                    hi[h] = *reinterpret_cast<const uint4*>(p.c_hi + at + 8 * h * p.ld);
+                    if (kApplies<kStep> && p.c_lo) lo[h] = ld_live_u4(p.c_lo + at + 8 * h * p.ld);   // read once
+                }
+            }
+        }
+        if constexpr (kStep == kApplyTall) {
+            const int64_t at = z * p.factor_stride + col0 + (threadIdx.x & 31);
+            f_hi[0] = p.f_hi[at];
+            f_lo[0] = p.f_lo[at];
+        }
     }
-    __device__ __forceinline__ void finish(const StepEnding& p, int z, int row0, int col0, bool mirror, float (&v)[4][4]) {
+    // What has been loaded, to shared memory: the registers are free for the next unit's.
+    __device__ __forceinline__ void put(const UnitPlace& u) const {
+        if constexpr (kStep != kGram) {
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                unit_store(u.vec + 512 * h, hi[h]);
+                if (kApplies<kStep>) unit_store(u.vec + kUnitBytes + 512 * h, lo[h]);
+            }
+            __syncwarp();
+        }
+    }
+    template <bool kOnce = false>   // kOnce: nothing else reads it soon
+    __device__ __forceinline__ static void store(uint32_t from, uint16_t* q, int64_t ld, int rows_left) {
         const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 v = unit_load(from + 512 * h);
+            uint4* to = reinterpret_cast<uint4*>(q + (i + 8 * h) * ld + 8 * j);
+            if (i + 8 * h < rows_left) kOnce ? __stcs(to, v) : (void)(*to = v);
+        }
+    }
+    __device__ __forceinline__ void finish(const StepEnding& p, const UnitPlace& u, int z, int row0, int col0, bool mirror, float2 factors, float (&v)[4][4]) const {
+        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
+        float2 w[2][4];   // the result's pairs
         if constexpr (kStep == kGram) {
             const float t = s * s * (kA / (kX * kX));
 #pragma unroll
             for (int g = 0; g < 4; ++g)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[g][c] *= t;
+                for (int h = 0; h < 2; ++h) w[h][g] = __fmul2_rn(make_float2(v[g][2 * h], v[g][2 * h + 1]), make_float2(t, t));
         }
-        if constexpr (kStep != kGram) {
+        if constexpr (kStep == kSquare) {
+            const float2 b = make_float2(p.b, p.b), c = make_float2(p.c / kA, p.c / kA);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                quad_transpose(hi[h]);
-                if (kStep == kApply) quad_transpose(lo[h]);
-            }
-            const uint32_t x[2][4] = {{hi[0].x, hi[0].y, hi[0].z, hi[0].w}, {hi[1].x, hi[1].y, hi[1].z, hi[1].w}};
-            const uint32_t y2[2][4] = {{lo[0].x, lo[0].y, lo[0].z, lo[0].w}, {lo[1].x, lo[1].y, lo[1].z, lo[1].w}};
+                uint32_t x[4];
+                matrix_load(u.frag + 512 * h, x);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float4 fc;   // factors of two columns
-                if (kStep == kApply && p.tall)
-                    fc = *reinterpret_cast<const float4*>(p.factors + z * p.factor_stride + col0 + 8 * g + 2 * j);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 t = unpack_f16x2(x[h][g]);
-                    if constexpr (kStep == kSquare) {
-                        v[g][2 * h] = p.b * t.x + v[g][2 * h] * (p.c / kA);
-                        v[g][2 * h + 1] = p.b * t.y + v[g][2 * h + 1] * (p.c / kA);
-                    } else {
-                        const float2 u = unpack_f16x2(y2[h][g]);
-                        const float2 f0 = p.tall ? make_float2(fc.x, fc.y) : f[h], f1 = p.tall ? make_float2(fc.z, fc.w) : f[h];
-                        v[g][2 * h] = s * (f0.x * t.x + (f0.y * (1.0f / kLo)) * u.x + v[g][2 * h] * (1.0f / kA));
-                        v[g][2 * h + 1] = s * (f1.x * t.y + (f1.y * (1.0f / kLo)) * u.y + v[g][2 * h + 1] * (1.0f / kA));
-                    }
-                }
+                for (int g = 0; g < 4; ++g)
+                    w[h][g] = __ffma2_rn(b, unpack_f16x2(x[g]), __fmul2_rn(make_float2(v[g][2 * h], v[g][2 * h + 1]), c));
             }
         }
-        if (kStep == kApply && p.y) {
-            uint16_t* q = p.y + z * p.y_stride + row0 * p.ldy + col0;
-            if (p.y_vec && col0 + 32 <= p.cols) {
-                uint32_t a[4], b[4];
+        if constexpr (kApplies<kStep>) {
+            uint32_t x[2][4], y[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                matrix_load(u.frag + 512 * h, x[h]);
+                matrix_load(u.frag + kUnitBytes + 512 * h, y[h]);
+            }
+            float2 c_hi[4], c_lo[4];   // kApplyTall: two columns' factors
+            if constexpr (kStep == kApplyTall) {
+                const uint32_t row = u.base + (threadIdx.x & 31) * 4, from = u.base + 8 * j;
+                __syncwarp();
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(row), "f"(factors.x) : "memory");
+                asm volatile("st.shared.b32 [%0 + 128], %1;" ::"r"(row), "f"(factors.y) : "memory");
+                __syncwarp();
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    a[g] = pack_bf16x2(v[g][0] * (1.0f / kX), v[g][1] * (1.0f / kX));
-                    b[g] = pack_bf16x2(v[g][2] * (1.0f / kX), v[g][3] * (1.0f / kX));
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(c_hi[g].x), "=f"(c_hi[g].y) : "r"(from + 32 * g) : "memory");
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2 + 128];" : "=f"(c_lo[g].x), "=f"(c_lo[g].y) : "r"(from + 32 * g) : "memory");
                 }
-                store(q, p.ldy, p.rows - row0, a, b);
+            }
+            const float2 c = make_float2(s * (1.0f / kA), s * (1.0f / kA));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float2 a = kStep == kApplyTall ? c_hi[g] : make_float2(f_hi[h], f_hi[h]);
+                    const float2 b = kStep == kApplyTall ? c_lo[g] : make_float2(f_lo[h], f_lo[h]);
+                    const float2 t = __ffma2_rn(b, unpack_f16x2(y[h][g]), __fmul2_rn(c, make_float2(v[g][2 * h], v[g][2 * h + 1])));
+                    w[h][g] = __ffma2_rn(a, unpack_f16x2(x[h][g]), t);
+                }
+        }
+        if constexpr (kStep != kGram) __syncwarp();   // what was loaded has been read
+        uint32_t d[2][4];
+        if (kApplies<kStep> && p.y) {
+            const float2 c = make_float2(1.0f / kX, 1.0f / kX);
+            uint16_t* q = p.y + z * p.y_stride + row0 * p.ldy + col0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float2 t = __fmul2_rn(w[h][g], c);
+                    d[h][g] = pack_bf16x2(t.x, t.y);
+                }
+            if (p.y_vec && col0 + 32 <= p.cols) {
+                matrix_store(u.frag, d[0]);
+                matrix_store(u.frag + 512, d[1]);
+                __syncwarp();
+                store(u.vec, q, p.ldy, p.rows - row0);
             } else {
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int row = i + 8 * (c >> 1), col = 8 * g + 2 * j + (c & 1);
-                        if (row0 + row < p.rows && col0 + col < p.cols) q[row * p.ldy + col] = to_bf16(v[g][c] * (1.0f / kX));
+                        if (row0 + row < p.rows && col0 + col < p.cols) q[row * p.ldy + col] = (uint16_t)(d[c >> 1][g] >> 16 * (c & 1));
                     }
             }
             return;
@@ -434,43 +509,49 @@ struct StepEnd {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int row = row0 + i + 8 * (c >> 1), col = col0 + 8 * g + 2 * j + (c & 1);
-                    if (row == col && row < p.rows)
-                        p.factors[z * p.factor_stride + row] =
-                            make_float2(p.a + (v[g][c] - round_f16(v[g][c])) * (1.0f / kA), p.a + v[g][c] * (1.0f / kA));
+                    const float t = c & 1 ? w[c >> 1][g].y : w[c >> 1][g].x;
+                    if (row == col && row < p.rows) {
+                        p.f_hi[z * p.factor_stride + row] = s * (p.a + (t - round_f16(t)) * (1.0f / kA));
+                        p.f_lo[z * p.factor_stride + row] = s * ((p.a + t * (1.0f / kA)) * (1.0f / kLo));
+                    }
                 }
         }
         const int64_t at = z * p.stride + row0 * p.ld + col0;
-        uint32_t a[4], b[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            a[g] = pack_f16x2(v[g][0], v[g][1]);
-            b[g] = pack_f16x2(v[g][2], v[g][3]);
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) d[h][g] = pack_f16x2(w[h][g].x, w[h][g].y);
+            matrix_store(u.frag + 512 * h, d[h]);
         }
-        if (kStep == kApply) {
-            uint32_t e[4], g2[4];
+        if constexpr (kApplies<kStep>) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float2 t = unpack_f16x2(a[g]), u = unpack_f16x2(b[g]);
-                e[g] = pack_f16x2((v[g][0] - t.x) * kLo, (v[g][1] - t.y) * kLo);
-                g2[g] = pack_f16x2((v[g][2] - u.x) * kLo, (v[g][3] - u.y) * kLo);
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float2 t = unpack_f16x2(d[h][g]);
+                    const float2 r = __fmul2_rn(__fadd2_rn(w[h][g], make_float2(-t.x, -t.y)), make_float2(kLo, kLo));
+                    d[h][g] = pack_f16x2(r.x, r.y);
+                }
+                matrix_store(u.frag + kUnitBytes + 512 * h, d[h]);
             }
-            store<true>(p.d_lo + at, p.ld, p.rows - row0, e, g2);
         } else if (mirror) {
-            // transposed, a lane has two rows of column i of each group of eight: after the
-            // exchange, column 8 j + i and all eight rows
-            uint32_t e[4], g2[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) e[g] = transpose8x8(a[g]), g2[g] = transpose8x8(b[g]);
-            quad_transpose(e);
-            quad_transpose(g2);
-            const int col = col0 + 8 * j + i;
+            matrix_store_turned(u.turned + kUnitBytes, d[0]);
+            matrix_store_turned((u.turned + kUnitBytes) ^ 16, d[1]);
+        }
+        __syncwarp();
+        store(u.vec, p.d_hi + at, p.ld, p.rows - row0);
+        if constexpr (kApplies<kStep>) {
+            store<true>(u.vec + kUnitBytes, p.d_lo + at, p.ld, p.rows - row0);
+        } else if (mirror) {   // a lane has a column, of sixteen rows
+            const int col = col0 + (threadIdx.x & 31);
+            const uint4 e0 = unit_load(u.turned + kUnitBytes), e1 = unit_load((u.turned + kUnitBytes) ^ 16);
             if (col < p.cols && row0 < p.rows) {
-                uint16_t* q = p.d_hi + z * p.stride + col * p.ld + row0;
-                *reinterpret_cast<uint4*>(q) = make_uint4(e[0], e[1], e[2], e[3]);
-                *reinterpret_cast<uint4*>(q + 8) = make_uint4(g2[0], g2[1], g2[2], g2[3]);
+                uint4* q = reinterpret_cast<uint4*>(p.d_hi + z * p.stride + col * p.ld + row0);
+                q[0] = e0;
+                q[1] = e1;
             }
         }
-        store(p.d_hi + at, p.ld, p.rows - row0, a, b);
+        if constexpr (kStep == kGram) __syncwarp();   // read before the next unit's is written
     }
 };
 
@@ -591,49 +672,59 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             (void)mbar_wait_bounded(drained, 0, kWaitCycles / 8);
         }
     } else if (warp >= 4) {
-        // units of 16 rows x 32 columns: of its 32 rows this warp ends one half, over one
-        // half of the columns, side by side so that whole lines are written together
-        const int q = warp & 3, h = (warp - 4) / 4;
+        // of its 32 rows this warp ends one half, over one half of the columns, side by
+        // side so that whole lines are written together
+        const int q = warp & 3, h = (warp - 4) / 4, row_in = (int)rank * 128 + q * 32 + (h & 1) * 16;
         const uint32_t lanes = tmem + ((uint32_t)(q * 32 + (h & 1) * 16) << 16);
+        const UnitPlace at(smem_addr(smem + kStages * kStageBytes + 256 + (warp - 4) * 2 * kUnitBytes));
+        const auto share = [&](const Place& w, int* first) {   // this warp's units of a tile, and the first
+            const int all = width_of(p, w.tn) / 32;
+            *first = (h >> 1) * ((all + 1) / 2);
+            return h >> 1 ? all - *first : (all + 1) / 2;
+        };
+        StepEnd<kStep> end{};
+        float v[4][4] = {};
+        // before the first tile the end goes once through rows that do not exist, so that
+        // its instructions are there when the product is (0.4 us of a launch)
+        if (pair < p.all) {
+            const Place w = place_of<kStep>(p, pair);
+            int first;
+            const int units = share(w, &first), row0 = w.tm * 256 + row_in;
+            end.put(at);
+            if (row0 < p.e.rows && units > 0) {
+                end.tile(p.e, w.z, row0);
+                end.load(p.e, w.z, row0, w.tn * p.bn + first * 32);
+            }
+            end.finish(p.e, at, w.z, p.e.rows, w.tn * p.bn, w.tn * p.bn >= (w.tm + 1) * 256, make_float2(0.0f, 0.0f), v);
+        }
         int use = 0;
         for (int t = pair; t < p.all; t += pairs, ++use) {
             const Place w = place_of<kStep>(p, t);
-            const int chunks_n = width_of(p, w.tn) / 32, first = (h >> 1) * ((chunks_n + 1) / 2);
-            const int units = h >> 1 ? chunks_n - first : (chunks_n + 1) / 2;   // of this warp
-            const int row0 = w.tm * 256 + (int)rank * 128 + q * 32 + (h & 1) * 16, buf = use & 1;
-            const bool mirror = w.tn * p.bn >= (w.tm + 1) * 256, mine = row0 < p.e.rows;
-            const int col_first = w.tn * p.bn + first * 32;
-            // what a unit's end reads is on its way while the unit before it, or the
-            // tile's product, is finished
-            StepEnd<kStep> end{}, next{};
-            if (use > 0 && mine && units > 0) end.load(p.e, w.z, row0, col_first);
-            float v[4][4] = {};
-            bool ok = true;
-            // before the first tile the end goes once through rows that do not exist, so that
-            // its instructions are there when the product is (0.4 us of a launch)
+            int first;
+            const int units = share(w, &first), row0 = w.tm * 256 + row_in, buf = use & 1, col_first = w.tn * p.bn + first * 32;
+            const bool mirror = w.tn * p.bn >= (w.tm + 1) * 256, mine = row0 < p.e.rows && units > 0;
+            if (!step_wait(acc_full + buf, (use / 2) & 1)) break;
+            tcgen05_fence_after();
+            if (mine) {
 #pragma unroll 1
-            for (int u = use == 0 ? -1 : 0; u < units; ++u) {
-                const bool warm = u < 0;
-                const int col0 = warm ? w.tn * p.bn : col_first + u * 32;
-                if (!warm) {
-                    if (u == 0) {
-                        if (!(ok = step_wait(acc_full + buf, (use / 2) & 1))) break;
-                        tcgen05_fence_after();
-                    }
+                for (int u = 0; u < units; ++u) {
+                    end.put(at);
+                    const float2 factors = make_float2(end.f_hi[0], end.f_lo[0]);
+                    if (u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
                     tmem_load_fragment(lanes + buf * 256 + (first + u) * 32, v);
-                    if (u + 1 == units)
-                        release_accumulator(acc_empty + buf);   // this warp's last read
-                    else if (mine)
-                        next.load(p.e, w.z, row0, col0 + 32);
+                    if (u + 1 == units) release_accumulator(acc_empty + buf);   // this warp's last read
+                    end.finish(p.e, at, w.z, row0, col_first + u * 32, mirror, factors, v);
                 }
-                if (mine || warm) end.finish(p.e, w.z, warm ? p.e.rows : row0, col0, mirror, v);
-                if (warm && mine && units > 0) next.load(p.e, w.z, row0, col_first);
-                end = next;
-            }
-            if (!ok) break;
-            if (units == 0) {   // a narrow last tile: no unit for this warp
-                if (!step_wait(acc_full + buf, (use / 2) & 1)) break;
+            } else {
                 release_accumulator(acc_empty + buf);
+            }
+            if (t + pairs < p.all) {   // what the next tile's end reads first is on its way before that tile's product
+                const Place n = place_of<kStep>(p, t + pairs);
+                int next;
+                if (share(n, &next) > 0 && n.tm * 256 + row_in < p.e.rows) {
+                    end.tile(p.e, n.z, n.tm * 256 + row_in);
+                    end.load(p.e, n.z, n.tm * 256 + row_in, n.tn * p.bn + next * 32);
+                }
             }
         }
     }
@@ -675,10 +766,10 @@ static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, 
     const int64_t pairs = sm_pairs(), k_blocks = (depth + 63) / 64, tm = (rows + 255) / 256;
     StepPlan best{0, 0, 0};
     int64_t least = INT64_MAX;
-    for (int bn = 256; bn >= 32; bn = step == kApply ? bn - 32 : bn / 2) {
+    for (int bn = 256; bn >= 32; bn = applies(step) ? bn - 32 : bn / 2) {
         const int64_t tn = (cols + bn - 1) / bn;
         int64_t tiles = tm * tn;
-        if (step != kApply) {
+        if (!applies(step)) {
             tiles = 0;
             for (int64_t i = 0; i < tm; ++i) tiles += tn - i * (256 / bn);
         }
@@ -741,7 +832,7 @@ static int orthogonal_space(int64_t batch, int64_t rows, int64_t cols, Orthogona
     for (int i = 0; i < 2; ++i) w->hi[i] = take(batch * x), w->lo[i] = take(batch * x);
     w->a = take(batch * a);
     w->b = take(batch * a);
-    w->factors = take(batch * w->lds * (int64_t)sizeof(float2));
+    w->factors = take(2 * batch * w->lds * (int64_t)sizeof(float));
     w->norm = take(batch * w->parts * 8);
     w->scale = take(batch * 4);
     w->bytes = at;
@@ -808,18 +899,17 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     const Matrices gram{at(w.a), side, side, w.lds, batch}, poly{at(w.b), side, side, w.lds, batch};
     const Matrices first{at(w.hi[0]), rows, cols, w.ldx, batch}, second{at(w.hi[1]), rows, cols, w.ldx, batch};
     StepEnding e{};
-    e.tall = tall;
-    e.factors = reinterpret_cast<float2*>(base + w.factors); e.factor_stride = w.lds;
+    e.f_hi = reinterpret_cast<float*>(base + w.factors); e.f_lo = e.f_hi + batch * w.lds; e.factor_stride = w.lds;
     e.scale = src.scale;
     e.a = coefficients[0]; e.b = coefficients[1]; e.c = coefficients[2];
     const int64_t longer = tall ? rows : cols;
     // the end of a step of iteration i
     const auto ending = [&](Step step, int i) {
         StepEnding d = e;
-        if (step == kApply) {
+        d.first = i == 0;
+        if (applies(step)) {
             d.rows = (int32_t)rows; d.cols = (int32_t)cols;
             d.ld = w.ldx; d.stride = rows * w.ldx;
-            d.first = i == 0;
             d.c_hi = at(w.hi[i & 1]);
             d.c_lo = i == 0 && !f32 ? nullptr : at(w.lo[i & 1]);
             d.d_hi = at(w.hi[~i & 1]);
@@ -827,7 +917,6 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
         } else {
             d.rows = d.cols = (int32_t)side;
             d.ld = w.lds; d.stride = side * w.lds;
-            d.first = step == kGram && i == 0;
             d.c_hi = at(w.a);
             d.d_hi = at(step == kGram ? w.a : w.b);
         }
@@ -840,8 +929,8 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
         const Matrices& now = i ? second : first;
         if (const int rc = prepare_step<kGram>(gram_step[i], side, side, longer, now, tall, now, tall)) return rc;
         // wide: B X, X read along its rows; tall: X B, B being its own transpose
-        if (const int rc = tall ? prepare_step<kApply>(apply_step[i], rows, cols, side, now, false, poly, false)
-                                : prepare_step<kApply>(apply_step[i], rows, cols, side, poly, false, now, true))
+        if (const int rc = tall ? prepare_step<kApplyTall>(apply_step[i], rows, cols, side, now, false, poly, false)
+                                : prepare_step<kApplyWide>(apply_step[i], rows, cols, side, poly, false, now, true))
             return rc;
     }
 
@@ -858,12 +947,12 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
         if (const int rc = launch_step<kGram>(g, s)) return rc;
         square_step.e = ending(kSquare, i);
         if (const int rc = launch_step<kSquare>(square_step, s)) return rc;
-        a.e = ending(kApply, i);
+        a.e = ending(tall ? kApplyTall : kApplyWide, i);
         if (i + 1 == steps) {
             a.e.y = y; a.e.ldy = ldy; a.e.y_stride = batch > 1 ? y_stride : 0;
             a.e.y_vec = rows_aligned16(y, ldy, 2) && (batch == 1 || y_stride % 8 == 0);
         }
-        if (const int rc = launch_step<kApply>(a, s)) return rc;
+        if (const int rc = tall ? launch_step<kApplyTall>(a, s) : launch_step<kApplyWide>(a, s)) return rc;
     }
     return ZERO_OK;
 }
