@@ -11,9 +11,8 @@
 // lies below 2^-11 of its largest directions, which the iteration raises (3.4 times a
 // step): a momentum of low rank with a faint rest came out 2 % off, 16 % in bf16.  So X is
 // held as the sum of two fp16 numbers, `hi` and `lo` (22 bits), of which the products take
-// `hi`, and what they do to `lo` is put in by B's diagonal, its largest part:
-//   X' = (a + B_ii - fp16(B_ii)) hi + (a + B_ii) lo + fp16(B) hi
-// the first factor also taking back the rounding of the diagonal.  Against 64 bits:
+// `hi`, and what they do to `lo` is put in by B's diagonal, its largest part, which is not
+// rounded either:  X' = (a + B_ii) (hi + lo) + fp16(B - diagonal) hi.  Against 64 bits:
 // 0.3e-3 to 1e-3 of the result by norm (2.5e-3 for 40 x 100 with two directions a
 // thousand times above the rest), before the 1.7e-3 of its own rounding to bf16.
 #include <cuda_fp16.h>
@@ -272,16 +271,16 @@ struct StepEnding {
     uint16_t* d_lo;
     uint16_t* y; int64_t ldy, y_stride;    // the last X: bf16 in place of d
     bool y_vec;
-    float* f_hi;                           // scale (a + B_ii - fp16(B_ii))
-    float* f_lo;                           // scale (a + B_ii) / 2^11
-    int64_t factor_stride;
+    float* factors; int64_t factor_stride; // scale (a + B_ii)
+    bool turned;                           // kSquare: rows of d in the order of turned_row
     const float* scale;
     float a, b, c;
 };
 struct StepParams {
     CUtensorMap map_a, map_b;
     int32_t depth;                         // the reduced dimension
-    int32_t tiles_n, tiles, all;           // column tiles; tiles a matrix, and of the batch
+    int32_t tiles_n, tiles, full, all;     // column tiles; tiles a matrix of which `full` counts the batch's; and with narrow ones after those
+    int32_t lights;                        // narrow tiles for pairs with one full tile less
     int32_t bn, k_blocks;
     bool a_mn, b_mn;
     StepEnding e;
@@ -300,32 +299,67 @@ struct Place {
 // The order of the tiles.  X' goes through X once: a wide X column by column, a tall
 // one row by row, the rows or columns of B together.  A symmetric result has of row tile
 // i the column tiles from its own columns on, so that the narrow last tiles are as many
-// as can be; and its matrices are taken last to first, since what the last step wrote
-// last is still in L2 (and what this one read last will be when X is read again).
+// as can be, and those of the whole batch come last (Turns); its matrices are taken last
+// to first, since what the last step wrote last is still in L2 (and what this one read
+// last will be when X is read again), the narrow tiles first to last for the same reason.
 template <Step kStep>
 __device__ __forceinline__ Place place_of(const StepParams& p, int t) {
     Place w;
-    w.z = t / p.tiles;
-    t -= w.z * p.tiles;
-    if constexpr (kStep == kApplyTall) {
-        w.tm = t / p.tiles_n;
-        w.tn = t - w.tm * p.tiles_n;
-    } else if constexpr (kStep == kApplyWide) {
-        const int tiles_m = (p.e.rows + 255) / 256;
-        w.tn = t / tiles_m;
-        w.tm = t - w.tn * tiles_m;
-    } else {
+    if constexpr (kApplies<kStep>) {
+        w.z = t / p.tiles;
+        t -= w.z * p.tiles;
+        if constexpr (kStep == kApplyTall) {
+            w.tm = t / p.tiles_n;
+            w.tn = t - w.tm * p.tiles_n;
+        } else {
+            const int tiles_m = (p.e.rows + 255) / 256;
+            w.tn = t / tiles_m;
+            w.tm = t - w.tn * tiles_m;
+        }
+    } else if (t < p.full) {
         const int step = 256 / p.bn;
-        int n = p.tiles_n;
+        int n = p.e.cols / p.bn;   // full tiles of a row of tiles
+        w.z = t / p.tiles;
+        t -= w.z * p.tiles;
+        w.z = p.full / p.tiles - 1 - w.z;
         for (w.tm = 0; t >= n; ++w.tm) {
             t -= n;
             n -= step;
         }
         w.tn = w.tm * step + t;
-        w.z = p.all / p.tiles - 1 - w.z;
+    } else {
+        const int tiles_m = (p.e.rows + 255) / 256;
+        t -= p.full;
+        w.z = t / tiles_m;
+        w.tm = t - w.z * tiles_m;
+        w.tn = p.tiles_n - 1;
     }
     return w;
 }
+// A pair's tiles: every so many of the full ones; then of the narrow ones, which take half
+// to three quarters of the time, the first `lights` are for those pairs that have had one
+// full tile less, and the rest for all in turn, those first.  (In one order for all
+// 12 x 4800 x 1600 took the pairs up to five full tiles' time where 4.0 are the mean.)
+struct Turns {
+    int pair, pairs, own, lights, light, place;
+    __device__ __forceinline__ explicit Turns(const StepParams& p) : pair(blockIdx.x / 2), pairs(gridDim.x / 2) {
+        const int more = p.full % pairs;   // pairs with one more
+        own = p.full / pairs + (pair < more ? 1 : 0);
+        light = pairs - more;
+        place = pair >= more ? pair - more : pair + light;   // in the order for narrow tiles
+        lights = place < light && place < p.lights ? (p.lights - place + light - 1) / light : 0;
+    }
+    __device__ __forceinline__ int tile(const StepParams& p, int i) const {   // its i-th, or -1
+        if (i < own) return pair + i * pairs;
+        i -= own;
+        if (i < lights) return p.full + place + i * light;
+        const int t = p.full + p.lights + place + (i - lights) * pairs;
+        return t < p.all ? t : -1;
+    }
+};
+// Where row r of B stands for a tall X: X B then has the columns 8 j .. + 7 of every 32 in
+// one lane's eight accumulators, as X is read and written.
+__device__ __forceinline__ int turned_row(int r) { return (r & ~31) | (r >> 1 & 3) << 3 | (r >> 3 & 3) << 1 | (r & 1); }
 __device__ __forceinline__ int width_of(const StepParams& p, int tn) {   // columns of the tile, up to a multiple of 32
     const int left = p.e.cols - tn * p.bn;
     return left >= p.bn ? p.bn : (left + 31) / 32 * 32;
@@ -336,8 +370,9 @@ __device__ __forceinline__ int width_of(const StepParams& p, int tn) {   // colu
 // (v[g][2 h], v[g][2 h + 1]); memory is read and written in 16-byte vectors, columns 8 j
 // .. + 7 of those rows.  One becomes the other in the warp's own shared memory, by
 // the matrix loads and stores: rows of 64 bytes whose vectors are exchanged so that neither
-// side has two accesses to a bank.  (By shuffles and selections that took 16 instructions
-// for four, and a third of the time of a product that reads and writes both halves of X.)
+// side has two accesses to a bank.  X B of a tall X has its columns in the order of memory
+// (turned_row) and needs none of this, which shared memory, busy with the operands, made
+// the bound of a short product's end.
 struct UnitPlace {
     uint32_t base, vec, frag, turned;   // shared addresses: of this lane's vector, of the row it names to a matrix access, of that in the transpose
     __device__ __forceinline__ explicit UnitPlace(uint32_t base) : base(base) {
@@ -368,17 +403,17 @@ __device__ __forceinline__ void matrix_store_turned(uint32_t at, const uint32_t 
 // Matrices of the workspace have rows of whole units, so that only rows are checked.
 template <Step kStep>
 struct StepEnd {
-    uint4 hi[2], lo[2];            // a unit's on their way, this lane's vectors
-    float s, f_hi[2], f_lo[2];     // of a tile: the scale; kApplyWide: the rows' factors; kApplyTall: [0] of the unit's column `lane`, on their way
+    static constexpr bool kTall = kStep == kApplyTall;
+    uint4 hi[2], lo[2];   // a unit's on their way, this lane's vectors
+    float4 f[2];          // kTall: the factors of their columns
+    float s, f_row[2];    // of a tile: the scale; kApplyWide: the rows' factors
     __device__ __forceinline__ void tile(const StepEnding& p, int z, int row0) {
         s = p.first ? p.scale[z] : 1.0f;
         if constexpr (kStep == kApplyWide) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int row = row0 + ((threadIdx.x & 31) >> 2) + 8 * h;
-                const int64_t at = z * p.factor_stride + row;
-                f_hi[h] = row < p.rows ? p.f_hi[at] : 0.0f;
-                f_lo[h] = row < p.rows ? p.f_lo[at] : 0.0f;
+                f_row[h] = row < p.rows ? p.factors[z * p.factor_stride + row] : 0.0f;
             }
         }
     }
@@ -393,39 +428,29 @@ struct StepEnd {
                     hi[h] = *reinterpret_cast<const uint4*>(p.c_hi + at + 8 * h * p.ld);
                     if (kApplies<kStep> && p.c_lo) lo[h] = ld_live_u4(p.c_lo + at + 8 * h * p.ld);   // read once
                 }
+                if constexpr (kTall) f[h] = *reinterpret_cast<const float4*>(p.factors + z * p.factor_stride + col0 + 8 * j + 4 * h);
             }
-        }
-        if constexpr (kStep == kApplyTall) {
-            const int64_t at = z * p.factor_stride + col0 + (threadIdx.x & 31);
-            f_hi[0] = p.f_hi[at];
-            f_lo[0] = p.f_lo[at];
         }
     }
     // What has been loaded, to shared memory: the registers are free for the next unit's.
     __device__ __forceinline__ void put(const UnitPlace& u) const {
-        if constexpr (kStep != kGram) {
+        if constexpr (kStep == kSquare || kStep == kApplyWide) {
             __syncwarp();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 unit_store(u.vec + 512 * h, hi[h]);
-                if (kApplies<kStep>) unit_store(u.vec + kUnitBytes + 512 * h, lo[h]);
+                if (kStep == kApplyWide) unit_store(u.vec + kUnitBytes + 512 * h, lo[h]);
             }
             __syncwarp();
         }
     }
-    template <bool kOnce = false>   // kOnce: nothing else reads it soon
-    __device__ __forceinline__ static void store(uint32_t from, uint16_t* q, int64_t ld, int rows_left) {
-        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint4 v = unit_load(from + 512 * h);
-            uint4* to = reinterpret_cast<uint4*>(q + (i + 8 * h) * ld + 8 * j);
-            if (i + 8 * h < rows_left) kOnce ? __stcs(to, v) : (void)(*to = v);
-        }
+    // kOnce: nothing else reads it soon.
+    template <bool kOnce>
+    __device__ __forceinline__ static void write(uint16_t* q, const uint4& v) {
+        kOnce ? __stcs(reinterpret_cast<uint4*>(q), v) : (void)(*reinterpret_cast<uint4*>(q) = v);
     }
-    __device__ __forceinline__ void finish(const StepEnding& p, const UnitPlace& u, int z, int row0, int col0, bool mirror, float2 factors, float (&v)[4][4]) const {
-        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
-        float2 w[2][4];   // the result's pairs
+    // The result's pairs, from the accumulators and what was loaded.
+    __device__ __forceinline__ void form(const StepEnding& p, const UnitPlace& u, const float (&v)[4][4], float2 (&w)[2][4]) const {
         if constexpr (kStep == kGram) {
             const float t = s * s * (kA / (kX * kX));
 #pragma unroll
@@ -445,37 +470,40 @@ struct StepEnd {
             }
         }
         if constexpr (kApplies<kStep>) {
-            uint32_t x[2][4], y[2][4];
+            const float2 c = make_float2(s * (1.0f / kA), s * (1.0f / kA)), l = make_float2(1.0f / kLo, 1.0f / kLo);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                matrix_load(u.frag + 512 * h, x[h]);
-                matrix_load(u.frag + kUnitBytes + 512 * h, y[h]);
-            }
-            float2 c_hi[4], c_lo[4];   // kApplyTall: two columns' factors
-            if constexpr (kStep == kApplyTall) {
-                const uint32_t row = u.base + (threadIdx.x & 31) * 4, from = u.base + 8 * j;
-                __syncwarp();
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(row), "f"(factors.x) : "memory");
-                asm volatile("st.shared.b32 [%0 + 128], %1;" ::"r"(row), "f"(factors.y) : "memory");
-                __syncwarp();
+                uint32_t x[4] = {hi[h].x, hi[h].y, hi[h].z, hi[h].w}, y[4] = {lo[h].x, lo[h].y, lo[h].z, lo[h].w};
+                if constexpr (!kTall) {
+                    matrix_load(u.frag + 512 * h, x);
+                    matrix_load(u.frag + kUnitBytes + 512 * h, y);
+                }
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(c_hi[g].x), "=f"(c_hi[g].y) : "r"(from + 32 * g) : "memory");
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2 + 128];" : "=f"(c_lo[g].x), "=f"(c_lo[g].y) : "r"(from + 32 * g) : "memory");
+                    const float4 e = f[g / 2];
+                    const float2 a = !kTall ? make_float2(f_row[h], f_row[h]) : g & 1 ? make_float2(e.z, e.w) : make_float2(e.x, e.y);
+                    w[h][g] = __ffma2_rn(a, __ffma2_rn(l, unpack_f16x2(y[g]), unpack_f16x2(x[g])),
+                                         __fmul2_rn(c, make_float2(v[g][2 * h], v[g][2 * h + 1])));
                 }
             }
-            const float2 c = make_float2(s * (1.0f / kA), s * (1.0f / kA));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float2 a = kStep == kApplyTall ? c_hi[g] : make_float2(f_hi[h], f_hi[h]);
-                    const float2 b = kStep == kApplyTall ? c_lo[g] : make_float2(f_lo[h], f_lo[h]);
-                    const float2 t = __ffma2_rn(b, unpack_f16x2(y[h][g]), __fmul2_rn(c, make_float2(v[g][2 * h], v[g][2 * h + 1])));
-                    w[h][g] = __ffma2_rn(a, unpack_f16x2(x[h][g]), t);
-                }
         }
-        if constexpr (kStep != kGram) __syncwarp();   // what was loaded has been read
+        if constexpr (kStep == kSquare || kStep == kApplyWide) __syncwarp();   // what was loaded has been read
+    }
+    // Eight of a row out of the four lanes that have them, both rows.
+    __device__ __forceinline__ static void gather(const UnitPlace& u, uint32_t area, const uint32_t (&d)[2][4]) {
+        if constexpr (!kTall) {
+            matrix_store(u.frag + area, d[0]);
+            matrix_store(u.frag + area + 512, d[1]);
+        }
+    }
+    __device__ __forceinline__ static uint4 row_of(const UnitPlace& u, uint32_t area, const uint32_t (&d)[2][4], int h) {
+        if constexpr (kTall)
+            return make_uint4(d[h][0], d[h][1], d[h][2], d[h][3]);
+        else
+            return unit_load(u.vec + area + 512 * h);
+    }
+    __device__ __forceinline__ static void finish(const StepEnding& p, const UnitPlace& u, float s, int z, int row0, int col0, bool mirror, float2 (&w)[2][4]) {
+        const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
         uint32_t d[2][4];
         if (kApplies<kStep> && p.y) {
             const float2 c = make_float2(1.0f / kX, 1.0f / kX);
@@ -488,16 +516,19 @@ struct StepEnd {
                     d[h][g] = pack_bf16x2(t.x, t.y);
                 }
             if (p.y_vec && col0 + 32 <= p.cols) {
-                matrix_store(u.frag, d[0]);
-                matrix_store(u.frag + 512, d[1]);
+                gather(u, 0, d);
                 __syncwarp();
-                store(u.vec, q, p.ldy, p.rows - row0);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 e = row_of(u, 0, d, h);
+                    if (row0 + i + 8 * h < p.rows) write<false>(q + (i + 8 * h) * p.ldy + 8 * j, e);
+                }
             } else {
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int row = i + 8 * (c >> 1), col = 8 * g + 2 * j + (c & 1);
+                        const int row = i + 8 * (c >> 1), col = (kTall ? 8 * j + 2 * g : 8 * g + 2 * j) + (c & 1);
                         if (row0 + row < p.rows && col0 + col < p.cols) q[row * p.ldy + col] = (uint16_t)(d[c >> 1][g] >> 16 * (c & 1));
                     }
             }
@@ -509,44 +540,50 @@ struct StepEnd {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int row = row0 + i + 8 * (c >> 1), col = col0 + 8 * g + 2 * j + (c & 1);
-                    const float t = c & 1 ? w[c >> 1][g].y : w[c >> 1][g].x;
+                    float& t = c & 1 ? w[c >> 1][g].y : w[c >> 1][g].x;
                     if (row == col && row < p.rows) {
-                        p.f_hi[z * p.factor_stride + row] = s * (p.a + (t - round_f16(t)) * (1.0f / kA));
-                        p.f_lo[z * p.factor_stride + row] = s * ((p.a + t * (1.0f / kA)) * (1.0f / kLo));
+                        p.factors[z * p.factor_stride + row] = s * (p.a + t * (1.0f / kA));
+                        t = 0.0f;
                     }
                 }
         }
-        const int64_t at = z * p.stride + row0 * p.ld + col0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int g = 0; g < 4; ++g) d[h][g] = pack_f16x2(w[h][g].x, w[h][g].y);
-            matrix_store(u.frag + 512 * h, d[h]);
-        }
+        gather(u, 0, d);
+        uint32_t r[2][4];
         if constexpr (kApplies<kStep>) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const float2 t = unpack_f16x2(d[h][g]);
-                    const float2 r = __fmul2_rn(__fadd2_rn(w[h][g], make_float2(-t.x, -t.y)), make_float2(kLo, kLo));
-                    d[h][g] = pack_f16x2(r.x, r.y);
+                    const float2 e = __fmul2_rn(__fadd2_rn(w[h][g], make_float2(-t.x, -t.y)), make_float2(kLo, kLo));
+                    r[h][g] = pack_f16x2(e.x, e.y);
                 }
-                matrix_store(u.frag + kUnitBytes + 512 * h, d[h]);
-            }
+            gather(u, kUnitBytes, r);
         } else if (mirror) {
             matrix_store_turned(u.turned + kUnitBytes, d[0]);
             matrix_store_turned((u.turned + kUnitBytes) ^ 16, d[1]);
         }
-        __syncwarp();
-        store(u.vec, p.d_hi + at, p.ld, p.rows - row0);
-        if constexpr (kApplies<kStep>) {
-            store<true>(u.vec + kUnitBytes, p.d_lo + at, p.ld, p.rows - row0);
-        } else if (mirror) {   // a lane has a column, of sixteen rows
+        if constexpr (!kTall) __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = row0 + i + 8 * h;
+            const int64_t at = z * p.stride + (kStep == kSquare && p.turned ? turned_row(row) : row) * p.ld + col0 + 8 * j;
+            const uint4 e = row_of(u, 0, d, h);
+            if (row < p.rows) write<false>(p.d_hi + at, e);
+            if constexpr (kApplies<kStep>) {
+                const uint4 l = row_of(u, kUnitBytes, r, h);
+                if (row < p.rows) write<true>(p.d_lo + at, l);
+            }
+        }
+        if (!kApplies<kStep> && mirror) {   // a lane has a column, of sixteen rows
             const int col = col0 + (threadIdx.x & 31);
             const uint4 e0 = unit_load(u.turned + kUnitBytes), e1 = unit_load((u.turned + kUnitBytes) ^ 16);
             if (col < p.cols && row0 < p.rows) {
-                uint4* q = reinterpret_cast<uint4*>(p.d_hi + z * p.stride + col * p.ld + row0);
+                uint4* q = reinterpret_cast<uint4*>(p.d_hi + z * p.stride + (kStep == kSquare && p.turned ? turned_row(col) : col) * p.ld + row0);
                 q[0] = e0;
                 q[1] = e1;
             }
@@ -577,7 +614,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
 
     const int warp = uniform_warp();
     const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const Turns turns(p);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -608,7 +645,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
         int s = 0;
         uint32_t round = 0;
         bool ok = true;
-        for (int t = pair; ok && t < p.all; t += pairs) {
+        for (int n = 0, t; ok && (t = turns.tile(p, n)) >= 0; ++n) {
             const Place w = place_of<kStep>(p, t);
             const int row = w.tm * 256 + (int)rank * 128;
             const int col = w.tn * p.bn + (int)rank * (width_of(p, w.tn) / 2);
@@ -644,7 +681,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
         uint32_t round = 0;
         bool ok = true;
         const uint32_t a_step = descriptor_step(p.a_mn), b_step = descriptor_step(p.b_mn);
-        for (int t = pair; ok && t < p.all; t += pairs, ++use) {
+        for (int t; ok && (t = turns.tile(p, use)) >= 0; ++use) {
             const Place w = place_of<kStep>(p, t);
             const uint32_t idesc = instruction_descriptor(256, width_of(p, w.tn), p.a_mn, p.b_mn, false);
             const int buf = use & 1;
@@ -683,49 +720,48 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             return h >> 1 ? all - *first : (all + 1) / 2;
         };
         StepEnd<kStep> end{};
-        float v[4][4] = {};
-        // before the first tile the end goes once through rows that do not exist, so that
-        // its instructions are there when the product is (0.4 us of a launch)
-        if (pair < p.all) {
-            const Place w = place_of<kStep>(p, pair);
+        const auto begin = [&](const Place& w) {   // what a tile's end reads first on its way
             int first;
-            const int units = share(w, &first), row0 = w.tm * 256 + row_in;
-            end.put(at);
-            if (row0 < p.e.rows && units > 0) {
-                end.tile(p.e, w.z, row0);
-                end.load(p.e, w.z, row0, w.tn * p.bn + first * 32);
+            if (share(w, &first) > 0 && w.tm * 256 + row_in < p.e.rows) {
+                end.tile(p.e, w.z, w.tm * 256 + row_in);
+                end.load(p.e, w.z, w.tm * 256 + row_in, w.tn * p.bn + first * 32);
             }
-            end.finish(p.e, at, w.z, p.e.rows, w.tn * p.bn, w.tn * p.bn >= (w.tm + 1) * 256, make_float2(0.0f, 0.0f), v);
+        };
+        int t = turns.tile(p, 0);
+        float v[4][4] = {};
+        float2 r[2][4];
+        if (t >= 0) {
+            // before the first tile the end goes once through rows that do not exist, so that
+            // its instructions are there when the product is (0.4 us of a launch)
+            const Place w = place_of<kStep>(p, t);
+            end.put(at);
+            end.form(p.e, at, v, r);
+            end.finish(p.e, at, 0.0f, w.z, p.e.rows, w.tn * p.bn, w.tn * p.bn >= (w.tm + 1) * 256, r);
+            begin(w);
         }
-        int use = 0;
-        for (int t = pair; t < p.all; t += pairs, ++use) {
+        for (int use = 0; t >= 0; ++use) {
             const Place w = place_of<kStep>(p, t);
             int first;
             const int units = share(w, &first), row0 = w.tm * 256 + row_in, buf = use & 1, col_first = w.tn * p.bn + first * 32;
             const bool mirror = w.tn * p.bn >= (w.tm + 1) * 256, mine = row0 < p.e.rows && units > 0;
+            t = turns.tile(p, use + 1);
             if (!step_wait(acc_full + buf, (use / 2) & 1)) break;
             tcgen05_fence_after();
             if (mine) {
 #pragma unroll 1
                 for (int u = 0; u < units; ++u) {
                     end.put(at);
-                    const float2 factors = make_float2(end.f_hi[0], end.f_lo[0]);
-                    if (u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
+                    if (!StepEnd<kStep>::kTall && u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
                     tmem_load_fragment(lanes + buf * 256 + (first + u) * 32, v);
                     if (u + 1 == units) release_accumulator(acc_empty + buf);   // this warp's last read
-                    end.finish(p.e, at, w.z, row0, col_first + u * 32, mirror, factors, v);
+                    end.form(p.e, at, v, r);
+                    if (StepEnd<kStep>::kTall && u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
+                    end.finish(p.e, at, end.s, w.z, row0, col_first + u * 32, mirror, r);
                 }
             } else {
                 release_accumulator(acc_empty + buf);
             }
-            if (t + pairs < p.all) {   // what the next tile's end reads first is on its way before that tile's product
-                const Place n = place_of<kStep>(p, t + pairs);
-                int next;
-                if (share(n, &next) > 0 && n.tm * 256 + row_in < p.e.rows) {
-                    end.tile(p.e, n.z, n.tm * 256 + row_in);
-                    end.load(p.e, n.z, n.tm * 256 + row_in, n.tn * p.bn + next * 32);
-                }
-            }
+            if (t >= 0) begin(place_of<kStep>(p, t));
         }
     }
     // the CTAs part when both are done with the tensor memories and each other's barriers;
@@ -742,41 +778,48 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
 // A batch of equal matrices of the workspace: rows `ld` apart, 16-byte aligned.
 struct Matrices {
     const uint16_t* p;
-    int64_t rows, cols, ld, batch;
+    int64_t rows, cols, ld, stride, batch;
 };
 static bool make_map3(const Matrices& m, int box_rows, CUtensorMap* map) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.batch};
-    const cuuint64_t pitch[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.ld * m.rows) * 2};
+    const cuuint64_t pitch[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)m.stride * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(m.p), dims, pitch, box, unit,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The tile width with the least estimated time: waves of pairs, each a tile's blocks
-// (bound by the tensor core, or for narrow tiles by shared memory) and the part of its
-// end that nothing hides.  A symmetric result takes widths that divide 256.
+// The tile width with the least estimated time: a tile's blocks (bound by the tensor core,
+// or for narrow tiles by shared memory) and the part of its end that nothing hides, as
+// often as the busiest pair has them.  A symmetric result takes widths that divide 256.
 struct StepPlan {
-    int64_t tiles;
+    int64_t tiles, full, all, lights;
     int bn, tiles_n;
 };
 static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, int64_t batch) {
-    const int64_t pairs = sm_pairs(), k_blocks = (depth + 63) / 64, tm = (rows + 255) / 256;
-    StepPlan best{0, 0, 0};
+    const int64_t k_blocks = (depth + 63) / 64, tm = (rows + 255) / 256;
+    const auto time_of = [&](int64_t width) { return 1500 + k_blocks * (2 * width > 256 + width ? 2 * width : 256 + width) + 24 * width; };
+    StepPlan best{};
     int64_t least = INT64_MAX;
     for (int bn = 256; bn >= 32; bn = applies(step) ? bn - 32 : bn / 2) {
         const int64_t tn = (cols + bn - 1) / bn;
-        int64_t tiles = tm * tn;
+        int64_t tiles = tm * tn, narrow = 0;
         if (!applies(step)) {
             tiles = 0;
-            for (int64_t i = 0; i < tm; ++i) tiles += tn - i * (256 / bn);
+            for (int64_t n = cols / bn; n > 0; n -= 256 / bn) tiles += n;
+            narrow = cols % bn ? tm : 0;
         }
-        if (tiles > INT32_MAX / 4 / batch) continue;
-        const int64_t waves = (tiles * batch + pairs - 1) / pairs;
-        const int64_t cycles = waves * (1500 + k_blocks * (2 * bn > 256 + bn ? 2 * bn : 256 + bn) + 24 * bn);
-        if (cycles < least) least = cycles, best = StepPlan{tiles, bn, (int)tn};
+        if (tiles + narrow > INT32_MAX / 4 / batch) continue;
+        StepPlan q{tiles, tiles * batch, (tiles + narrow) * batch, 0, bn, (int)tn};
+        const int64_t pairs = q.all < sm_pairs() ? q.all : sm_pairs(), more = q.full % pairs, light = pairs - more;
+        const int64_t whole = time_of(bn), part = time_of((cols % bn + 31) / 32 * 32), fit = (whole + part / 2) / part;
+        q.lights = q.all - q.full < (fit > 1 ? fit : 1) * light ? q.all - q.full : (fit > 1 ? fit : 1) * light;
+        int64_t cycles = q.full / pairs * whole + (q.lights + light - 1) / light * part;
+        if (more && cycles < (q.full / pairs + 1) * whole) cycles = (q.full / pairs + 1) * whole;
+        cycles += (q.all - q.full - q.lights + pairs - 1) / pairs * part;
+        if (cycles < least) least = cycles, best = q;
     }
     return best;
 }
@@ -793,7 +836,9 @@ static int prepare_step(StepParams& q, int64_t rows, int64_t cols, int64_t depth
     q.bn = plan.bn;
     q.tiles_n = plan.tiles_n;
     q.tiles = (int32_t)plan.tiles;
-    q.all = (int32_t)(plan.tiles * a.batch);
+    q.full = (int32_t)plan.full;
+    q.all = (int32_t)plan.all;
+    q.lights = (int32_t)plan.lights;
     q.k_blocks = (int32_t)((depth + 63) / 64);
     q.a_mn = a_mn; q.b_mn = b_mn;
     return make_map3(a, a_mn ? 64 : 128, &q.map_a) && make_map3(b, b_mn ? 64 : q.bn / 2, &q.map_b) ? ZERO_OK : ZERO_ECUDA;
@@ -807,7 +852,7 @@ static int launch_step(const StepParams& q, cudaStream_t s) {
 
 // Where everything stands in the workspace.
 struct OrthogonalSpace {
-    int64_t ldx, lds, parts;                       // rows of X; of A and B
+    int64_t ldx, lds, square, parts;               // rows of X; rows of A and B, and their elements
     int64_t hi[2], lo[2], a, b, factors, norm, scale, bytes;
 };
 constexpr int64_t kLongest = (int64_t)1 << 30;
@@ -818,7 +863,8 @@ static int orthogonal_space(int64_t batch, int64_t rows, int64_t cols, Orthogona
     if (longer > kLongest || side > 32768 || rows * ((cols + 7) / 8) > INT32_MAX / 4) return ZERO_ERANGE;
     w->ldx = (cols + 63) / 64 * 64;
     w->lds = (side + 63) / 64 * 64;
-    const int64_t x = rows * w->ldx * 2, a = side * w->lds * 2;
+    w->square = (side + 31) / 32 * 32 * w->lds;   // turned_row moves rows within groups of 32
+    const int64_t x = rows * w->ldx * 2, a = w->square * 2;
     const int64_t groups = rows * ((cols + 7) / 8), most = batch > 32 ? 32 : 1024 / batch;   // some CTAs an SM, of the batch
     w->parts = (groups + 2 * kFlying * kSourceThreads - 1) / (2 * kFlying * kSourceThreads);
     if (w->parts > most) w->parts = most;
@@ -832,7 +878,7 @@ static int orthogonal_space(int64_t batch, int64_t rows, int64_t cols, Orthogona
     for (int i = 0; i < 2; ++i) w->hi[i] = take(batch * x), w->lo[i] = take(batch * x);
     w->a = take(batch * a);
     w->b = take(batch * a);
-    w->factors = take(2 * batch * w->lds * (int64_t)sizeof(float));
+    w->factors = take(batch * w->lds * (int64_t)sizeof(float));
     w->norm = take(batch * w->parts * 8);
     w->scale = take(batch * 4);
     w->bytes = at;
@@ -896,10 +942,12 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     src.lo = f32 ? at(w.lo[0]) : nullptr;
     src.ld = w.ldx; src.to = rows * w.ldx;
     src.eps = eps;
-    const Matrices gram{at(w.a), side, side, w.lds, batch}, poly{at(w.b), side, side, w.lds, batch};
-    const Matrices first{at(w.hi[0]), rows, cols, w.ldx, batch}, second{at(w.hi[1]), rows, cols, w.ldx, batch};
+    const Matrices gram{at(w.a), side, side, w.lds, w.square, batch};
+    const Matrices poly{at(w.b), tall ? (side + 31) / 32 * 32 : side, side, w.lds, w.square, batch};
+    const Matrices first{at(w.hi[0]), rows, cols, w.ldx, src.to, batch}, second{at(w.hi[1]), rows, cols, w.ldx, src.to, batch};
     StepEnding e{};
-    e.f_hi = reinterpret_cast<float*>(base + w.factors); e.f_lo = e.f_hi + batch * w.lds; e.factor_stride = w.lds;
+    e.factors = reinterpret_cast<float*>(base + w.factors); e.factor_stride = w.lds;
+    e.turned = tall;
     e.scale = src.scale;
     e.a = coefficients[0]; e.b = coefficients[1]; e.c = coefficients[2];
     const int64_t longer = tall ? rows : cols;
@@ -916,7 +964,7 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
             d.d_lo = at(w.lo[~i & 1]);
         } else {
             d.rows = d.cols = (int32_t)side;
-            d.ld = w.lds; d.stride = side * w.lds;
+            d.ld = w.lds; d.stride = w.square;
             d.c_hi = at(w.a);
             d.d_hi = at(step == kGram ? w.a : w.b);
         }
