@@ -748,17 +748,19 @@ struct NormShape {
     int lanes, warps, per, threads, most;   // most: threads that the kernel is made for
     int64_t teams, grid;   // teams of a CTA
 };
-static NormShape norm_shape(int64_t rows, int64_t cols, bool vec) {
+static NormShape norm_shape(int64_t rows, int64_t cols, bool vec, bool grad) {
     NormShape s{};
     const int64_t groups = (cols + 7) / 8, sms = sm_count();
-    // element by element takes more registers: fewer pieces a thread
-    s.per = groups <= 32 ? 1 : groups <= 64 || (!vec && groups <= 1024) ? 2 : 4;
+    // a gradient element by element takes more registers: fewer pieces a thread
+    // (2048 x 4097 bf16 44 us with two, 53 with four; forward 31 with four, 40 with two)
+    s.per = groups <= 32 ? 1 : groups <= 64 || (!vec && grad && groups <= 1024) ? 2 : 4;
     s.many = groups > 32 * s.per;
     s.warps = s.many ? (int)((groups + 32 * s.per - 1) / (32 * s.per)) : 1;
     s.lanes = 1;
     while (!s.many && s.lanes < 32 && s.lanes * s.per < groups) s.lanes *= 2;
-    // 12 warps with registers to spare; the widest rows need 16, of 128 registers a thread
-    s.most = s.warps > 12 || (s.many && s.per == 2) ? 512 : 384;
+    // 12 warps with registers to spare (8192 x 1600 bf16 19 and 25 us, with 16 warps 24 and
+    // 32); 16, of 128 registers a thread, for the widest rows and element by element
+    s.most = s.many && (s.warps > 12 || s.per == 2 || (!vec && !grad)) ? 512 : 384;
     const int64_t in_warp = s.many ? 1 : 32 / s.lanes, most = s.many ? s.most / 32 / s.warps : s.most / 32 * in_warp;
     int64_t teams = (rows + sms - 1) / sms;
     teams = (teams + in_warp - 1) / in_warp * in_warp;   // whole warps
@@ -816,19 +818,21 @@ static int launch_norm_grad(NormParams& p, const NormShape& s, cudaStream_t stre
 }
 template <bool kF32, bool kVec>
 static int launch_norm(NormParams& p, const NormShape& s, cudaStream_t stream) {
-    if constexpr (!kVec)
-        if (s.many && s.per == 2) return launch_norm<kF32, kVec, 2, 512, true>(p, s, stream);
-    if (s.many) return s.most > 384 ? launch_norm<kF32, kVec, 4, 512, true>(p, s, stream) : launch_norm<kF32, kVec, 4, 384, true>(p, s, stream);
+    if constexpr (kVec)
+        if (s.many && s.most == 384) return launch_norm<kF32, kVec, 4, 384, true>(p, s, stream);
+    if (s.many) return launch_norm<kF32, kVec, 4, 512, true>(p, s, stream);
     return s.per == 1 ? launch_norm<kF32, kVec, 1, 384, false>(p, s, stream)
            : s.per == 2 ? launch_norm<kF32, kVec, 2, 384, false>(p, s, stream) : launch_norm<kF32, kVec, 4, 384, false>(p, s, stream);
 }
 template <bool kF32, bool kDyF32, bool kVec>
 static int launch_norm_grad(NormParams& p, const NormShape& s, cudaStream_t stream) {
-    if constexpr (!kVec)
+    if constexpr (!kVec) {
         if (s.many && s.per == 2) return launch_norm_grad<kF32, kDyF32, kVec, 2, 512, true>(p, s, stream);
+    } else {
+        if (!s.many && s.per == 4) return launch_norm_grad<kF32, kDyF32, kVec, 4, 384, false>(p, s, stream);
+    }
     if (s.many) return s.most > 384 ? launch_norm_grad<kF32, kDyF32, kVec, 4, 512, true>(p, s, stream) : launch_norm_grad<kF32, kDyF32, kVec, 4, 384, true>(p, s, stream);
-    return s.per == 1 ? launch_norm_grad<kF32, kDyF32, kVec, 1, 384, false>(p, s, stream)
-           : s.per == 2 ? launch_norm_grad<kF32, kDyF32, kVec, 2, 384, false>(p, s, stream) : launch_norm_grad<kF32, kDyF32, kVec, 4, 384, false>(p, s, stream);
+    return s.per == 1 ? launch_norm_grad<kF32, kDyF32, kVec, 1, 384, false>(p, s, stream) : launch_norm_grad<kF32, kDyF32, kVec, 2, 384, false>(p, s, stream);
 }
 
 static bool dtype_ok(int32_t d) { return d == ZERO_BF16 || d == ZERO_F32; }
@@ -870,7 +874,7 @@ extern "C" int zero_layer_norm(int64_t rows, int64_t cols, const void* x, int64_
     }
     const bool vec = cols % 8 == 0 && rows_aligned16(x, ldx, size) && rows_aligned16(y, ldy, dtype_size(y_dtype)) &&
                      (!residual || (rows_aligned16(residual, ldr, size) && rows_aligned16(sum, lds, size)));
-    const NormShape shape = norm_shape(rows, cols, vec);
+    const NormShape shape = norm_shape(rows, cols, vec, false);
     p.lanes = shape.lanes; p.warps = shape.warps;
     if (dtype == ZERO_F32) return vec ? launch_norm<true, true>(p, shape, s) : launch_norm<true, false>(p, shape, s);
     return vec ? launch_norm<false, true>(p, shape, s) : launch_norm<false, false>(p, shape, s);
@@ -942,7 +946,7 @@ extern "C" int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, 
     } else {
         const bool vec = cols % 8 == 0 && rows_aligned16(x, ldx, size) && rows_aligned16(dy, lddy, dtype_size(dy_dtype)) &&
                          rows_aligned16(dx, lddx, size) && (!residual || rows_aligned16(residual, ldr, size));
-        const NormShape shape = norm_shape(rows, cols, vec);
+        const NormShape shape = norm_shape(rows, cols, vec, true);
         p.lanes = shape.lanes; p.warps = shape.warps;
         if (parts) parts = shape.grid;
         if (!f32)
