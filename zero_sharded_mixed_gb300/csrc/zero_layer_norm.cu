@@ -39,18 +39,23 @@ struct NormParams {
 };
 
 // ---- a thread's eight columns (a piece), of which it has up to kPer -----------------------
-// kVec: rows on 16-byte boundaries of whole pieces, columns 8 (t + team j) .. + 7.
-// Otherwise column t + team (8 j + k), so that the team's accesses fall together.
+// Rows on 16-byte boundaries of whole pieces: bf16 columns 8 (t + team j) .. + 7, fp32 two
+// quads, 4 (t + team 2 j) .. + 3 and 4 (t + team (2 j + 1)) .. + 3, so that either way a
+// team's accesses of 16 bytes lie side by side (eight fp32 columns to a thread would fetch
+// each sector of 32 bytes twice: 8192 x 1600 fp32 took 44 and 50 us, for 31 and 37).
+// Otherwise (kLoose) column t + team (8 j + k), for the same reason.
+enum Lay { kLoose, kEights, kQuads };
+__host__ __device__ constexpr Lay lay_of(bool vec, bool f32) { return !vec ? kLoose : f32 ? kQuads : kEights; }
 struct Team {
-    int t, size, have;   // this thread, the threads, the pieces (kVec) or elements that this one has
+    int t, size, have;   // this thread, the threads, the pieces, quads or elements that this one has
 };
-template <bool kVec>
+template <Lay kLay>
 __device__ __forceinline__ int column(const Team& m, int j, int k) {
-    return kVec ? 8 * (m.t + m.size * j) + k : m.t + m.size * (8 * j + k);
+    return kLay == kEights ? 8 * (m.t + m.size * j) + k : kLay == kQuads ? 4 * (m.t + m.size * (2 * j + k / 4)) + k % 4 : m.t + m.size * (8 * j + k);
 }
-template <bool kVec>
+template <Lay kLay>
 __device__ __forceinline__ bool exists(const Team& m, int j, int k) {   // k 0: any of the piece
-    return (kVec ? j : 8 * j + k) < m.have;
+    return (kLay == kEights ? j : kLay == kQuads ? 2 * j + k / 4 : 8 * j + k) < m.have;
 }
 
 // Pairs of fp32 operations in one instruction: the kernels are bound by how many they issue
@@ -96,9 +101,11 @@ constexpr int kMostWarps = 16;   // of a CTA, and of a team
 // bytes of the neighbours' on either side, from byte `at` of its slot, and reads elements
 // from there; where a block would reach past the matrix's own memory its elements come
 // one by one.
-template <bool kF32, bool kVec, int kPer, int kPitch, int kAt>
+template <bool kF32, Lay kLay, int kPer, int kPitch, int kAt>
 struct Stream {
     static constexpr int kSize = kF32 ? 4 : 2, kPlaces = kF32 ? 2 : 1;
+    static constexpr bool kVec = kLay != kLoose;
+    static_assert(!kF32 || kLay != kEights);
     using T = typename std::conditional<kF32, float, uint16_t>::type;
     const T* to_send;   // the next row to send: kVec this thread's first piece of it
     int64_t hop;
@@ -108,7 +115,7 @@ struct Stream {
     __device__ __forceinline__ Stream(const void* q, int64_t ld, uint32_t at, int64_t row, int64_t stride, int64_t rows, int cols, const Team& m)
         : hop(stride * ld), at(at) {
         const T* p = static_cast<const T*>(q);
-        to_send = p + row * ld + (kVec ? 8 * m.t : 0);
+        to_send = p + row * ld + column<kLay>(Team{kVec ? m.t : 0, 0, 0}, 0, 0);
         if constexpr (!kVec) {
             shift = (uint32_t)(reinterpret_cast<uintptr_t>(to_send) & 15);
             turn = (uint32_t)(hop * kSize) & 15;
@@ -121,10 +128,20 @@ struct Stream {
         if constexpr (kVec) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
-                if (!exists<true>(m, j, 0)) break;
+                if (!exists<kLay>(m, j, 0)) break;
+                if constexpr (kLay == kEights) {
+                    copy_block(slot + kPitch * (kAt + j), reinterpret_cast<uintptr_t>(to_send + 8 * m.size * j), true);
+                } else {
 #pragma unroll
-                for (int i = 0; i < kPlaces; ++i)
-                    copy_block(slot + kPitch * (kAt + j * kPlaces + i), reinterpret_cast<uintptr_t>(to_send + 8 * m.size * j) + 16 * i, true);
+                    for (int i = 0; i < 2; ++i) {
+                        if (!exists<kLay>(m, j, 4 * i)) break;
+                        const uintptr_t from = reinterpret_cast<uintptr_t>(to_send + 4 * m.size * (2 * j + i));
+                        if constexpr (kF32)
+                            copy_block(slot + kPitch * (kAt + 2 * j + i), from, true);
+                        else
+                            copy_half_block(slot + kPitch * (kAt + j) + 8 * i, from);
+                    }
+                }
             }
         } else {
             const uintptr_t from = reinterpret_cast<uintptr_t>(to_send), first = from & ~(uintptr_t)15, last = from + cols * kSize;
@@ -153,18 +170,20 @@ struct Stream {
         if constexpr (kVec) {
 #pragma unroll
             for (int i = 0; i < kPlaces; ++i) {
-                const uint4 u = *reinterpret_cast<const uint4*>(slot + kPitch * (kAt + j * kPlaces + i));
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (kLay == kEights || i == 0 || exists<kLay>(m, j, 4)) u = *reinterpret_cast<const uint4*>(slot + kPitch * (kAt + j * kPlaces + i));
+                if (kLay == kQuads && !kF32 && !exists<kLay>(m, j, 4)) u.z = u.w = 0u;
                 v.w[4 * i] = u.x; v.w[4 * i + 1] = u.y; v.w[4 * i + 2] = u.z; v.w[4 * i + 3] = u.w;
             }
         } else {
-            const T* q = reinterpret_cast<const T*>(slot + at + shift) + column<false>(m, j, 0);
+            const T* q = reinterpret_cast<const T*>(slot + at + shift) + column<kLoose>(m, j, 0);
             uint32_t e[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 if constexpr (kF32)
-                    e[k] = exists<false>(m, j, k) ? __float_as_uint(q[m.size * k]) : 0u;
+                    e[k] = exists<kLoose>(m, j, k) ? __float_as_uint(q[m.size * k]) : 0u;
                 else
-                    e[k] = exists<false>(m, j, k) ? q[m.size * k] : 0u;
+                    e[k] = exists<kLoose>(m, j, k) ? q[m.size * k] : 0u;
             }
 #pragma unroll
             for (int k = 0; k < (kF32 ? 8 : 4); ++k) v.w[k] = kF32 ? e[k] : e[(2 * k) % 8] | e[(2 * k + 1) % 8] << 16;
@@ -173,17 +192,25 @@ struct Stream {
     }
 };
 
-// A piece to a row, q: kVec this thread's first piece of it, else its first column.
-template <bool kVec, bool kF32>
+// A piece to a row, q: its first column that this thread has.
+template <Lay kLay, bool kF32>
 __device__ __forceinline__ void store_words(void* q, const Team& m, int j, const Words<kF32>& v) {
-    if constexpr (kVec) {
-        uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(q) + m.size * j * (kF32 ? 32 : 16));
-        to[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
-        if constexpr (kF32) to[1] = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
+    if constexpr (kLay == kEights) {
+        *reinterpret_cast<uint4*>(static_cast<char*>(q) + m.size * j * 16) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    } else if constexpr (kLay == kQuads) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!exists<kLay>(m, j, 4 * i)) break;
+            char* to = static_cast<char*>(q) + m.size * (2 * j + i) * (kF32 ? 16 : 8);
+            if constexpr (kF32)
+                *reinterpret_cast<uint4*>(to) = make_uint4(v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]);
+            else
+                *reinterpret_cast<uint2*>(to) = make_uint2(v.w[2 * i], v.w[2 * i + 1]);
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            if (!exists<false>(m, j, k)) break;
+            if (!exists<kLay>(m, j, k)) break;
             if constexpr (kF32)
                 static_cast<uint32_t*>(q)[m.size * (8 * j + k)] = v.w[k];
             else
@@ -191,40 +218,46 @@ __device__ __forceinline__ void store_words(void* q, const Team& m, int j, const
         }
     }
 }
-template <bool kVec>
+template <Lay kLay>
 __device__ __forceinline__ void store_pairs(void* q, bool f32, const Team& m, int j, const float2 (&v)[4]) {
-    if (f32) {
+    if (kLay != kEights && f32) {
         Words<true> w;
 #pragma unroll
         for (int k = 0; k < 4; ++k) w.w[2 * k] = __float_as_uint(v[k].x), w.w[2 * k + 1] = __float_as_uint(v[k].y);
-        store_words<kVec, true>(q, m, j, w);
+        if constexpr (kLay != kEights) store_words<kLay, true>(q, m, j, w);
     } else {
         Words<false> w;
 #pragma unroll
         for (int k = 0; k < 4; ++k) w.w[k] = pack_bf16x2(v[k].x, v[k].y);
-        store_words<kVec, false>(q, m, j, w);
+        store_words<kLay, false>(q, m, j, w);
     }
 }
 // This thread's place in a row of an output, and the bytes from one row of the team to the next.
-template <bool kVec>
+template <Lay kLay>
 __device__ __forceinline__ char* output(void* q, int64_t ld, int size, int64_t row, const Team& m) {
-    return static_cast<char*>(q) + (row * ld + (kVec ? 8 : 1) * m.t) * size;
+    return static_cast<char*>(q) + (row * ld + column<kLay>(m, 0, 0)) * size;
 }
 
 // A piece of gamma or beta as bf16 pairs; `fill` (a pair) where the vector is absent.
-template <bool kVec>
+template <Lay kLay>
 __device__ __forceinline__ Words<false> weight_piece(const uint16_t* w, bool vec, const Team& m, int j, uint32_t fill) {
     Words<false> v;
     if (!w) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) v.w[k] = fill;
-    } else if (kVec && vec) {
-        const uint4 u = exists<true>(m, j, 0) ? *reinterpret_cast<const uint4*>(w + column<true>(m, j, 0)) : make_uint4(0u, 0u, 0u, 0u);
+    } else if (kLay == kEights && vec) {
+        const uint4 u = exists<kLay>(m, j, 0) ? *reinterpret_cast<const uint4*>(w + column<kLay>(m, j, 0)) : make_uint4(0u, 0u, 0u, 0u);
         v.w[0] = u.x; v.w[1] = u.y; v.w[2] = u.z; v.w[3] = u.w;
+    } else if (kLay == kQuads && vec) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint2 u = exists<kLay>(m, j, 4 * i) ? *reinterpret_cast<const uint2*>(w + column<kLay>(m, j, 4 * i)) : make_uint2(0u, 0u);
+            v.w[2 * i] = u.x; v.w[2 * i + 1] = u.y;
+        }
     } else {
         uint32_t e[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = exists<kVec>(m, j, k) ? w[column<kVec>(m, j, k)] : 0u;
+        for (int k = 0; k < 8; ++k) e[k] = exists<kLay>(m, j, k) ? w[column<kLay>(m, j, k)] : 0u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) v.w[k] = e[2 * k] | e[2 * k + 1] << 16;
     }
@@ -234,12 +267,12 @@ constexpr uint32_t kOnes = 0x3f803f80u;
 
 // ---- teams ----------------------------------------------------------------------------
 // kMany: several warps; else `lanes` lanes (a power of two) of one.
-template <bool kVec, bool kMany>
+template <Lay kLay, bool kMany>
 __device__ __forceinline__ Team team_of(const NormParams& p, int* which, int* teams) {
     const int size = kMany ? 32 * p.warps : p.lanes;
     *which = threadIdx.x / size;
     *teams = blockDim.x / size;
-    const int t = threadIdx.x - *which * size, all = kVec ? p.cols / 8 : p.cols;
+    const int t = threadIdx.x - *which * size, all = kLay == kEights ? p.cols / 8 : kLay == kQuads ? p.cols / 4 : p.cols;
     return Team{t, size, all > t ? (all - t + size - 1) / size : 0};
 }
 __device__ __forceinline__ void team_barrier(int which, int threads) {
@@ -331,15 +364,16 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
     __shared__ WarpStats stats[2][kMostWarps];
     constexpr int kSize = kF32 ? 4 : 2;
     await_predecessor();
+    constexpr Lay kLay = lay_of(kVec, kF32);
     int which, teams, turn = 0;
-    const Team m = team_of<kVec, kMany>(p, &which, &teams);
+    const Team m = team_of<kLay, kMany>(p, &which, &teams);
     const int64_t stride = (int64_t)gridDim.x * teams;
     // teams of one warp shuffle together: all go on until the first of them has no row
     const int back = kMany ? 0 : threadIdx.x % 32 / p.lanes;
     int64_t row = (int64_t)blockIdx.x * teams + which;
     constexpr int kPlaces = kPer * (kF32 ? 2 : 1);
-    Stream<kF32, kVec, kPer, 16 * kThreads, 0> xs(p.x, p.ldx, p.at[0], row, stride, p.rows, p.cols, m);
-    Stream<kF32, kVec, kPer, 16 * kThreads, kPlaces> rs(p.residual, p.ldr, p.at[1], row, stride, p.rows, p.cols, m);
+    Stream<kF32, kLay, kPer, 16 * kThreads, 0> xs(p.x, p.ldx, p.at[0], row, stride, p.rows, p.cols, m);
+    Stream<kF32, kLay, kPer, 16 * kThreads, kPlaces> rs(p.residual, p.ldr, p.at[1], row, stride, p.rows, p.cols, m);
     int64_t sent = row;
     const auto send = [&](uint32_t slot) {
         if (sent < p.rows) {
@@ -349,17 +383,17 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
         sent += stride;
     };
     Ring<kVec, kMany> ring(reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes), p.slot, p.ahead, which, send);
-    char* sum = output<kVec>(p.sum, p.lds, kSize, row, m);
-    char* y = output<kVec>(p.y, p.ldy, p.y_f32 ? 4 : 2, row, m);
+    char* sum = output<kLay>(p.sum, p.lds, kSize, row, m);
+    char* y = output<kLay>(p.y, p.ldy, p.y_f32 ? 4 : 2, row, m);
     const int64_t sum_hop = stride * p.lds * kSize, y_hop = stride * p.ldy * (p.y_f32 ? 4 : 2);
     Words<false> gamma[kPer], beta[kPer];
     float n = 0.0f;   // this warp's columns, or the team's
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        gamma[j] = weight_piece<kVec>(p.gamma, p.weights_vec, m, j, kOnes);
-        beta[j] = weight_piece<kVec>(p.beta, p.weights_vec, m, j, 0u);
+        gamma[j] = weight_piece<kLay>(p.gamma, p.weights_vec, m, j, kOnes);
+        beta[j] = weight_piece<kLay>(p.beta, p.weights_vec, m, j, 0u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) n += exists<kVec>(m, j, k) ? 1.0f : 0.0f;
+        for (int k = 0; k < 8; ++k) n += exists<kLay>(m, j, k) ? 1.0f : 0.0f;
     }
     {
         float t[1] = {n};
@@ -373,11 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
         float2 h[kPer][4], s2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (!has || !exists<kVec>(m, j, 0)) break;
+            if (!has || !exists<kLay>(m, j, 0)) break;
             Words<kF32> x = xs.get(slot, m, j);
             if (p.residual) {
                 x.add(rs.get(slot, m, j));   // as kept, and as the gradient will read it
-                store_words<kVec, kF32>(sum, m, j, x);
+                store_words<kLay, kF32>(sum, m, j, x);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {   // an absent column is 0
@@ -391,11 +425,12 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
         float2 d1 = both(0.0f), d2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {   // from here on h is the distance from base
-            if (!has || !exists<kVec>(m, j, 0)) break;
+            if (!has || !exists<kLay>(m, j, 0)) break;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 h[j][k] = add2(h[j][k], both(-base));
-                if (!kVec) h[j][k] = make_float2(exists<kVec>(m, j, 2 * k) ? h[j][k].x : 0.0f, exists<kVec>(m, j, 2 * k + 1) ? h[j][k].y : 0.0f);
+                if (kLay == kQuads && k >= 2 && !exists<kLay>(m, j, 4)) h[j][k] = both(0.0f);
+                if (!kVec) h[j][k] = make_float2(exists<kLay>(m, j, 2 * k) ? h[j][k].x : 0.0f, exists<kLay>(m, j, 2 * k + 1) ? h[j][k].y : 0.0f);
                 d1 = add2(d1, h[j][k]);
                 d2 = fma2(h[j][k], h[j][k], d2);
             }
@@ -429,10 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
         const float2 move = both(base - middle - off), scale = both(rstd);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (!exists<kVec>(m, j, 0)) break;
+            if (!exists<kLay>(m, j, 0)) break;
 #pragma unroll
             for (int k = 0; k < 4; ++k) h[j][k] = fma2(mul2(add2(h[j][k], move), scale), gamma[j].pair(k), beta[j].pair(k));
-            store_pairs<kVec>(y, p.y_f32, m, j, h[j]);
+            store_pairs<kLay>(y, p.y_f32, m, j, h[j]);
         }
     }
 }
@@ -446,15 +481,16 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
     __shared__ float2 stats[2][kMostWarps];
     constexpr int kSize = kF32 ? 4 : 2;
     await_predecessor();
+    constexpr Lay kLay = lay_of(kVec, kF32);
     int which, teams, turn = 0;
-    const Team m = team_of<kVec, kMany>(p, &which, &teams);
+    const Team m = team_of<kLay, kMany>(p, &which, &teams);
     const int64_t stride = (int64_t)gridDim.x * teams;
     const int back = kMany ? 0 : threadIdx.x % 32 / p.lanes;
     int64_t row = (int64_t)blockIdx.x * teams + which;
     constexpr int kXPlaces = kPer * (kF32 ? 2 : 1), kDyPlaces = kPer * (kDyF32 ? 2 : 1);
-    Stream<kF32, kVec, kPer, 16 * kThreads, 0> xs(p.x, p.ldx, p.at[0], row, stride, p.rows, p.cols, m);
-    Stream<kDyF32, kVec, kPer, 16 * kThreads, kXPlaces> ds(p.dy, p.lddy, p.at[1], row, stride, p.rows, p.cols, m);
-    Stream<kF32, kVec, kPer, 16 * kThreads, kXPlaces + kDyPlaces> rs(p.residual, p.ldr, p.at[2], row, stride, p.rows, p.cols, m);
+    Stream<kF32, kLay, kPer, 16 * kThreads, 0> xs(p.x, p.ldx, p.at[0], row, stride, p.rows, p.cols, m);
+    Stream<kDyF32, kLay, kPer, 16 * kThreads, kXPlaces> ds(p.dy, p.lddy, p.at[1], row, stride, p.rows, p.cols, m);
+    Stream<kF32, kLay, kPer, 16 * kThreads, kXPlaces + kDyPlaces> rs(p.residual, p.ldr, p.at[2], row, stride, p.rows, p.cols, m);
     int64_t sent = row;
     const auto send = [&](uint32_t slot) {
         if (sent < p.rows) {
@@ -465,13 +501,13 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         sent += stride;
     };
     Ring<kVec, kMany> ring(reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes), p.slot, p.ahead, which, send);
-    char* dx = output<kVec>(p.y, p.ldy, kSize, row, m);
+    char* dx = output<kLay>(p.y, p.ldy, kSize, row, m);
     const int64_t dx_hop = stride * p.ldy * kSize;
     Words<false> gamma[kPer];
     float2 sum_g[kPer][4], sum_b[kPer][4];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        gamma[j] = weight_piece<kVec>(p.gamma, p.weights_vec, m, j, kOnes);
+        gamma[j] = weight_piece<kLay>(p.gamma, p.weights_vec, m, j, kOnes);
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum_g[j][k] = sum_b[j][k] = both(0.0f);
     }
@@ -486,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         float2 v1 = both(0.0f), v2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (!has || !exists<kVec>(m, j, 0)) break;
+            if (!has || !exists<kLay>(m, j, 0)) break;
             const Words<kF32> x = xs.get(slot, m, j);
             const Words<kDyF32> dy = ds.get(slot, m, j);
 #pragma unroll
@@ -511,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         const float2 m1 = both(-v[0] * share), m2 = both(-v[1] * share);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (!exists<kVec>(m, j, 0)) break;
+            if (!exists<kLay>(m, j, 0)) break;
             const Words<kF32> x = xs.get(slot, m, j);
             const Words<kDyF32> dy = ds.get(slot, m, j);
             float2 out[4];
@@ -527,14 +563,14 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
 #pragma unroll
                 for (int k = 0; k < 4; ++k) out[k] = add2(out[k], r.pair(k));
             }
-            store_pairs<kVec>(dx, kF32, m, j, out);
+            store_pairs<kLay>(dx, kF32, m, j, out);
         }
     }
     if (!p.part) return;
     float* part = p.part + (int64_t)blockIdx.x * p.cols;
     const int64_t half = (int64_t)gridDim.x * p.cols;
     // pair i of this thread's columns, from column c
-    const auto column_of = [&](int i) { return kVec ? 8 * (m.t + m.size * (i / 4)) + 2 * (i % 4) : m.t + m.size * 2 * i; };
+    const auto column_of = [&](int i) { return column<kLay>(m, i / 4, 2 * (i % 4)); };
     const auto put = [&](int h, int i, float2 v) {
         const int c = column_of(i);
         if constexpr (kVec) {
