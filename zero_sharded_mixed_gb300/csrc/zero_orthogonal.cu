@@ -55,6 +55,7 @@ __device__ __forceinline__ float round_f16(float x) { return __half2float(__floa
 struct SourceParams {
     const void* x; int64_t ldx, stride;
     int32_t rows, cols, groups;        // groups of eight columns a row
+    uint32_t inverse, shift;           // g / groups = g inverse >> shift, for the groups of a matrix (fewer than 2^29)
     int32_t parts;
     bool f32, vec;
     double* norm;                      // [batch][parts]
@@ -73,7 +74,7 @@ struct SourceGroup {
     uint4 u[2];
     int32_t row, col;   // col < 0: none
     __device__ __forceinline__ void load(const SourceParams& p, int64_t from, uint32_t g, uint32_t all) {
-        row = (int32_t)(g / (uint32_t)p.groups);
+        row = (int32_t)((uint64_t)g * p.inverse >> p.shift);
         col = g < all ? (int32_t)(g - (uint32_t)row * (uint32_t)p.groups) * 8 : -1;
         u[0] = u[1] = make_uint4(0u, 0u, 0u, 0u);
         if (col < 0) return;
@@ -148,10 +149,10 @@ __device__ __forceinline__ double squares(const SourceParams& p, int z, uint32_t
     float sum = 0.0f;
     double far = 0.0;
     const uint32_t all = (uint32_t)p.rows * (uint32_t)p.groups;
-    for (uint32_t g = first; g < all; g += kFlying * share) {
+    for (uint32_t g = first; g < all; g += kFlying * share) {   // from the end, so that the beginning is in L2 when it is read again
         SourceGroup x[kFlying];
 #pragma unroll
-        for (int i = 0; i < kFlying; ++i) x[i].load(p, from, g + i * share, all);
+        for (int i = 0; i < kFlying; ++i) x[i].load(p, from, all - 1 - (g + i * share), all);   // wraps past `all` where there is none
 #pragma unroll
         for (int i = 0; i < kFlying; ++i) x[i].square(p, sum, far);
     }
@@ -934,6 +935,10 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     src.x = x; src.ldx = ldx; src.stride = batch > 1 ? x_stride : 0;
     src.rows = (int32_t)rows; src.cols = (int32_t)cols; src.groups = (int32_t)((cols + 7) / 8);
     src.parts = (int32_t)w.parts;
+    int bits = 0;   // 2^bits >= groups: an error below groups / 2^(29 + bits) a group is none after 2^29 of them
+    while (((int64_t)1 << bits) < src.groups) ++bits;
+    src.shift = 29 + bits;
+    src.inverse = (uint32_t)((((uint64_t)1 << src.shift) + src.groups - 1) / src.groups);
     src.f32 = f32;
     src.vec = cols % 8 == 0 && rows_aligned16(x, ldx, f32 ? 4 : 2) && (batch == 1 || x_stride * (f32 ? 4 : 2) % 16 == 0);
     src.norm = reinterpret_cast<double*>(base + w.norm);
