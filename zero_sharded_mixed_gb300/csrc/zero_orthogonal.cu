@@ -866,7 +866,7 @@ static int orthogonal_space(int64_t batch, int64_t rows, int64_t cols, Orthogona
     w->lds = (side + 63) / 64 * 64;
     w->square = (side + 31) / 32 * 32 * w->lds;   // turned_row moves rows within groups of 32
     const int64_t x = rows * w->ldx * 2, a = w->square * 2;
-    const int64_t groups = rows * ((cols + 7) / 8), most = batch > 32 ? 32 : 1024 / batch;   // some CTAs an SM, of the batch
+    const int64_t groups = rows * ((cols + 7) / 8), most = batch > 32 ? 32 : 608 / batch;   // four CTAs an SM, of the batch
     w->parts = (groups + 2 * kFlying * kSourceThreads - 1) / (2 * kFlying * kSourceThreads);
     if (w->parts > most) w->parts = most;
     if (batch > ((int64_t)1 << 60) / (4 * x + 2 * a + 16 * w->lds + 16 * w->parts + 4096)) return ZERO_ERANGE;
