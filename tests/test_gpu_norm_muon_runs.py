@@ -12,14 +12,14 @@ BF, F32 = torch.bfloat16, torch.float32
 
 
 class Unit:
-    """Norm, product, gradient of both: the buffers of one pass."""
+    """Norm, product, gradient of both: the buffers of one pass.  dt: of the residual stream."""
 
-    def __init__(self, zlib, rows, d, n, seed):
+    def __init__(self, zlib, rows, d, n, seed, dt=BF):
         g = torch.Generator(device="cuda").manual_seed(seed)
         new = lambda *s, dt=BF: torch.empty(*s, dtype=dt, device="cuda")   # noqa: E731
         rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)   # noqa: E731
-        self.z, self.x, self.r, self.w, self.gamma, self.beta, self.dy = zlib, rnd(rows, d), rnd(rows, d), rnd(n, d) * 0.05, 1 + rnd(d) * 0.1, rnd(d), rnd(rows, n)
-        self.s, self.h, self.y, self.dh, self.dx = new(rows, d), new(rows, d), new(rows, n), new(rows, d), new(rows, d)
+        self.z, self.x, self.r, self.w, self.gamma, self.beta, self.dy = zlib, rnd(rows, d).to(dt), rnd(rows, d).to(dt), rnd(n, d) * 0.05, 1 + rnd(d) * 0.1, rnd(d), rnd(rows, n)
+        self.s, self.h, self.y, self.dh, self.dx = new(rows, d, dt=dt), new(rows, d), new(rows, n), new(rows, d), new(rows, d, dt=dt)
         self.mean, self.rstd, self.dg, self.db, self.dw = new(rows, dt=F32), new(rows, dt=F32), new(d), new(d), new(n, d)
         self.ws = new(zlib.zero_layer_norm_grad_workspace(rows, d), dt=torch.uint8)
         self.o, self.ows = new(n, d), new(zlib.zero_orthogonalize_workspace(1, n, d), dt=torch.uint8)
@@ -55,8 +55,9 @@ def test_chain_against_64_bits(zlib, cuda_device):
     _close(u.o, u.dw.cpu())
 
 
-def test_two_streams_at_once(zlib, cuda_device):
-    units = [Unit(zlib, 500 + 77 * i, 320, 200, i) for i in range(2)]
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_two_streams_at_once(zlib, cuda_device, dt):
+    units = [Unit(zlib, 500 + 77 * i, 320, 200, i, dt) for i in range(2)]
     refs = []
     for u in units:
         u.run()
@@ -77,8 +78,10 @@ def test_two_streams_at_once(zlib, cuda_device):
     assert torch.equal(units[0].h, refs[0][1])
 
 
-def test_captured_and_replayed(zlib, cuda_device):
-    u, other = Unit(zlib, 700, 257, 129, 3), Unit(zlib, 700, 257, 129, 4)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("d", [256, 257])
+def test_captured_and_replayed(zlib, cuda_device, d, dt):
+    u, other = Unit(zlib, 700, d, 129, 3, dt), Unit(zlib, 700, d, 129, 4, dt)
     want = []
     for v in (u, other):
         v.run()
