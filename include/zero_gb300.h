@@ -683,7 +683,7 @@ int zero_muon_update(const zero_layout_t* L, const uint16_t* update, int64_t upd
 /* ---- status ---------------------------------------------------------------
  * Synchronizes `stream` and returns ZERO_ECUDA if it (or an earlier launch on
  * this thread) failed; ZERO_ETIMEOUT if a bounded device-side wait (the
- * mbarrier waits of the TMA-staged update, of the linear calls and of zero_orthogonalize) gave up since the last check -- the
+ * mbarrier waits of the TMA-staged update, of the linear, layer norm and orthogonalize calls) gave up since the last check -- the
  * kernel that gave up recorded it, drained its own copies and returned, so
  * the context stays usable; the record is cleared by this call.  ZERO_ERANGE
  * if a zero_schedule_advance found its index past the table since the last

@@ -18,6 +18,24 @@
 
 namespace zgb {
 
+__device__ int g_norm_status;   // ZERO_OK, or ZERO_ETIMEOUT once a bounded wait gave up
+
+int take_norm_status() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_norm_status, sizeof v) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ZERO_ECUDA;
+    }
+    if (v != ZERO_OK) {
+        const int zero = ZERO_OK;
+        if (cudaMemcpyToSymbol(g_norm_status, &zero, sizeof zero) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return ZERO_ECUDA;
+        }
+    }
+    return v == ZERO_OK ? ZERO_OK : ZERO_ETIMEOUT;
+}
+
 struct NormParams {
     int64_t rows;
     int32_t cols, lanes, warps;            // lanes of a team within a warp, or warps of a team
@@ -88,6 +106,7 @@ struct Words {
 };
 
 constexpr int kMostWarps = 16;   // of a CTA, and of a team
+constexpr int kMostAhead = 3;    // rows on their way
 
 // A matrix's rows on their way through shared memory: asynchronous copies, some rows
 // ahead of their turn, keep the memory busy behind the sums over the team.  A stream goes
@@ -160,6 +179,30 @@ struct Stream {
                 }
             }
         }
+        to_send += hop;
+    }
+    // One thread: the row's blocks as they lie, in one copy, but those that reach past the
+    // matrix's own memory, whose elements come one by one; the copy's bytes, then the copy.
+    uintptr_t start, stop;
+    __device__ __forceinline__ uint32_t send_edges(uint32_t slot, int cols) {
+        const uintptr_t from = reinterpret_cast<uintptr_t>(to_send), first = from & ~(uintptr_t)15, last = from + cols * kSize;
+        start = first >= begin ? first : first + 16;
+        stop = (last + 15) & ~(uintptr_t)15;
+        if (stop > end) stop -= 16;
+        const auto put = [&](uintptr_t e) {
+            const uint32_t to = slot + at + (uint32_t)(e - first);
+            if constexpr (kF32)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(*reinterpret_cast<const uint32_t*>(e)) : "memory");
+            else
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"(*reinterpret_cast<const uint16_t*>(e)) : "memory");
+        };
+        for (uintptr_t e = from; e < start; e += kSize) put(e);
+        for (uintptr_t e = stop; e < last; e += kSize) put(e);
+        return (uint32_t)(stop - start);
+    }
+    __device__ __forceinline__ void send_whole(uint8_t* slot, uint64_t* bar) {
+        const uintptr_t first = reinterpret_cast<uintptr_t>(to_send) & ~(uintptr_t)15;
+        bulk_g2s(slot + at + (start - first), reinterpret_cast<const void*>(start), (uint32_t)(stop - start), bar);
         to_send += hop;
     }
     __device__ __forceinline__ void next_row() {   // to read
@@ -483,11 +526,67 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
 // there, 14 at the memory's full rate, 1.5 for the CTAs' sums and 4 for the second kernel.
 // Rows of few CTAs' worth are bound by one row's way through a CTA, 2.5 us of sums, barrier
 // and second pass (1021 x 6401 fp32 27 us for 66 MB, 1021 x 6400 19).
+// The ring for teams of warps and rows off the grid: each row comes in one bulk copy a
+// stream, by a thread of the team each; next() waits for those alone, and refill() is called
+// once a row after a barrier of the team that follows next(), when the row before has been
+// read.  (With copies by all threads and a barrier more, 2048 x 4097 bf16 took 44 us for
+// 36, 1021 x 6401 fp32 27 for 24.8.  Forward, where fewer streams come, it was no gain.)
+struct BulkRing {
+    uint8_t* base;
+    uint64_t* full;   // of the slots
+    uint32_t size;
+    int ahead, which, i = 0, last = 0;
+    uint32_t phase = 0;
+    template <class Send>
+    __device__ __forceinline__ BulkRing(uint8_t* base, uint32_t size, int ahead, int which, uint64_t* full, Send send)
+        : base(base), full(full), size(size), ahead(ahead), which(which) {
+        for (int a = 0; a < ahead; ++a) send(base + a * size, full + a);
+    }
+    // null: the copy did not come in time
+    template <class Send>
+    __device__ __forceinline__ const uint8_t* next(const Team& m, Send send) {
+        if (ahead == 0) {
+            team_barrier(which, m.size);   // the last row has been read
+            send(base, full);
+        }
+        const bool there = warp_wait(full + i, phase, &g_norm_status);
+        if (!there)   // copies in flight land before the CTA ends
+            for (int k = 0; k <= ahead; ++k) (void)mbar_wait_bounded(full + k, k < i ? phase ^ 1 : phase, kWaitCycles / 8);
+        const uint8_t* here = there ? base + i * size : nullptr;
+        last = i ? i - 1 : ahead;
+        if (i == ahead) i = 0, phase ^= 1;
+        else ++i;
+        return here;
+    }
+    template <class Send>
+    __device__ __forceinline__ void refill(Send send) {
+        if (ahead) send(base + last * size, full + last);
+    }
+};
+// A stream's part of a send, by one thread.
+template <class S>
+__device__ __forceinline__ void send_row(uint8_t* slot, uint64_t* bar, int cols, S& s) {
+    fence_async_shared();   // the slot's readers are done
+    mbar_arrive_expect_tx(bar, s.send_edges(smem_addr(slot), cols));
+    s.send_whole(slot, bar);
+}
+__device__ __forceinline__ void bulk_ring_start(uint64_t (&full)[kMostWarps / 2][kMostAhead + 1], int streams) {
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < kMostWarps / 2; ++t)
+            for (int i = 0; i <= kMostAhead; ++i) mbar_init(&full[t][i], streams);
+        fence_barrier_init();
+    }
+    __syncthreads();
+}
+
 template <bool kF32, bool kDyF32, bool kVec, int kPer, int kThreads, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams p) {
     extern __shared__ uint4 slots[];
     __shared__ float2 stats[2][kMostWarps];
     constexpr int kSize = kF32 ? 4 : 2;
+    constexpr bool kBulk = kMany && !kVec;
+    __shared__ uint64_t full[kMostWarps / 2][kMostAhead + 1];
+    if constexpr (kBulk) bulk_ring_start(full, p.residual ? 3 : 2);
     await_predecessor();
     constexpr Lay kLay = lay_of(kVec, kF32);
     int which, teams, turn = 0;
@@ -500,15 +599,27 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
     Stream<kDyF32, kLay, kPer, 16 * kThreads, kXPlaces> ds(p.dy, p.lddy, p.at[1], row, stride, p.rows, p.cols, m);
     Stream<kF32, kLay, kPer, 16 * kThreads, kXPlaces + kDyPlaces> rs(p.residual, p.ldr, p.at[2], row, stride, p.rows, p.cols, m);
     int64_t sent = row;
-    const auto send = [&](uint32_t slot) {
+    const auto send = [&](auto slot, auto... bar) {
         if (sent < p.rows) {
-            xs.send(slot, m, p.cols);
-            ds.send(slot, m, p.cols);
-            if (p.residual) rs.send(slot, m, p.cols);
+            if constexpr (kBulk) {
+                if (m.t == 0) send_row(slot, bar..., p.cols, xs);
+                if (m.t == 32) send_row(slot, bar..., p.cols, ds);
+                if (m.t == (p.warps > 2 ? 64 : 0) && p.residual) send_row(slot, bar..., p.cols, rs);
+            } else {
+                xs.send(slot, m, p.cols);
+                ds.send(slot, m, p.cols);
+                if (p.residual) rs.send(slot, m, p.cols);
+            }
         }
         sent += stride;
     };
-    Ring<kVec, kMany> ring(reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes), p.slot, p.ahead, which, send);
+    auto ring = [&] {
+        uint8_t* base = reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes);
+        if constexpr (kBulk)
+            return BulkRing(base, p.slot, p.ahead, which, full[which], send);
+        else
+            return Ring<kVec, kMany>(base, p.slot, p.ahead, which, send);
+    }();
     char* dx = output<kLay>(p.y, p.ldy, kSize, row, m);
     const int64_t dx_hop = stride * p.ldy * kSize;
     Words<false> gamma[kPer];
@@ -526,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         const float mean = mean_ahead, rstd = rstd_ahead;
         if (row + stride < p.rows) mean_ahead = p.mean[row + stride], rstd_ahead = p.rstd[row + stride];
         const uint8_t* slot = ring.next(m, send);
+        if (kBulk && !slot) return;
         const float2 move = both(-mean), scale = both(rstd);
         float2 v1 = both(0.0f), v2 = both(0.0f);
 #pragma unroll
@@ -545,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         if constexpr (kMany) {
             if ((threadIdx.x & 31) == 0) stats[turn][threadIdx.x / 32] = make_float2(v[0], v[1]);
             team_barrier(which, m.size);
+            if constexpr (kBulk) ring.refill(send);
             const float2* w = stats[turn] + which * p.warps;
             turn ^= 1;   // written again after the next row's barrier
             v[0] = v[1] = 0.0f;
@@ -836,7 +949,7 @@ static int lay_slots(NormParams& p, const NormShape& s, bool vec, const int (&si
     p.slot = vec ? places * 16 * s.most : at * (uint32_t)s.teams;
     const int64_t own = (p.rows + s.grid * s.teams - 1) / (s.grid * s.teams);   // rows of a team
     p.ahead = (int32_t)(kNormSharedMemory / p.slot) - 1;
-    if (p.ahead > 3) p.ahead = 3;
+    if (p.ahead > kMostAhead) p.ahead = kMostAhead;
     if (p.ahead >= own) p.ahead = (int32_t)own - 1;
     return (int)p.slot * (p.ahead + 1);
 }

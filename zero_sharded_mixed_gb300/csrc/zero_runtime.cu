@@ -13,8 +13,9 @@ namespace zgb {
 int take_qgrad_status();
 // The same for the waits of the products' kernels (zero_linear.cu).
 int take_linear_status();
-// And of the orthogonalisation's (zero_orthogonal.cu).
+// And of the orthogonalisation's (zero_orthogonal.cu) and the layer norm's (zero_layer_norm.cu).
 int take_orthogonal_status();
+int take_norm_status();
 }  // namespace zgb
 
 namespace zgb {
@@ -130,6 +131,7 @@ extern "C" int zero_status_check(void* stream) {
     const int rq = zgb::take_qgrad_status();    // the same for the 8-bit gradient kernels' waits
     const int rl = zgb::take_linear_status();   // and for those of the products
     const int ro = zgb::take_orthogonal_status();   // and of the orthogonalisation
+    const int rn = zgb::take_norm_status();     // and of the layer norm
     const int rs = zgb::take_schedule_status();  // ZERO_ERANGE if a schedule index left its table
-    return rc != ZERO_OK ? rc : rq != ZERO_OK ? rq : rl != ZERO_OK ? rl : ro != ZERO_OK ? ro : rs;
+    return rc != ZERO_OK ? rc : rq != ZERO_OK ? rq : rl != ZERO_OK ? rl : ro != ZERO_OK ? ro : rn != ZERO_OK ? rn : rs;
 }
