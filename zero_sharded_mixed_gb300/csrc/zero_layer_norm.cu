@@ -414,6 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
     constexpr Lay kLay = lay_of(kVec, kF32);
     int which, teams, turn = 0;
     const Team m = team_of<kLay, kMany>(p, &which, &teams);
+    // a team is no larger than it has to be: the first half of the pieces is there (2048 x 4097
+    // bf16 27 us forward; 31 where that is asked for each)
+    __builtin_assume(m.have >= kPer / 2 * (kLay == kEights ? 1 : kLay == kQuads ? 2 : 8));
     const int64_t stride = (int64_t)gridDim.x * teams;
     // teams of one warp shuffle together: all go on until the first of them has no row
     const int back = kMany ? 0 : threadIdx.x % 32 / p.lanes;
@@ -591,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
     constexpr Lay kLay = lay_of(kVec, kF32);
     int which, teams, turn = 0;
     const Team m = team_of<kLay, kMany>(p, &which, &teams);
+    __builtin_assume(m.have >= kPer / 2 * (kLay == kEights ? 1 : kLay == kQuads ? 2 : 8));
     const int64_t stride = (int64_t)gridDim.x * teams;
     const int back = kMany ? 0 : threadIdx.x % 32 / p.lanes;
     int64_t row = (int64_t)blockIdx.x * teams + which;
