@@ -397,9 +397,9 @@ struct Ring {
 // means and squares, the means as differences from the first warp's, so that a mean far
 // from the deviations costs no digits: all that is kept of it is one fp32 number `base`
 // and the small distance from there.
-// Bound by memory where there is a residual (8192 x 1600 bf16 19 us, 5.6 TB/s; fp32 31 us,
-// 5.9 TB/s; the first row comes after 3 us), by instructions without one (bf16 15.5 us for
-// half of the bytes) and element by element (8192 x 1601 40 us); one row 2.9 us, a launch
+// Bound by memory where there is a residual (8192 x 1600 bf16 18.3 us, 5.7 TB/s; fp32 31 us,
+// 5.9 TB/s; the first row comes after 3 us), by instructions without one (bf16 15 us for
+// half of the bytes) and element by element (8192 x 1601 35 us); one row 2.7 us, a launch
 // and two latencies.
 struct WarpStats {
     float n, base, off, squares;   // columns, a number near their mean, the mean's distance from it, squared deviations
@@ -525,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
 // ---- backward -----------------------------------------------------------------------
 // Each thread sums dy xhat and dy of its columns down its team's rows, the CTA its teams,
 // a second kernel the CTAs, every time in the same order.
-// 8192 x 1600 bf16 with a residual takes 25 us for 105 MB: 3.7 until the first rows are
+// 8192 x 1600 bf16 with a residual takes 24 us for 105 MB: 3.7 until the first rows are
 // there, 14 at the memory's full rate, 1.5 for the CTAs' sums and 4 for the second kernel.
-// Rows of few CTAs' worth are bound by one row's way through a CTA, 2.5 us of sums, barrier
-// and second pass (1021 x 6401 fp32 27 us for 66 MB, 1021 x 6400 19).
+// Rows of few CTAs' worth are bound by one row's way through a CTA, 2 us of sums, barrier
+// and second pass (1021 x 6401 fp32 23 us for 66 MB, 1021 x 6400 18).
 // The ring for teams of warps and rows off the grid: each row comes in one bulk copy a
 // stream, by a thread of the team each; next() waits for those alone, and refill() is called
 // once a row after a barrier of the team that follows next(), when the row before has been
@@ -914,14 +914,14 @@ static NormShape norm_shape(int64_t rows, int64_t cols, bool vec, bool grad) {
     NormShape s{};
     const int64_t groups = (cols + 7) / 8, sms = sm_count();
     // a gradient element by element takes more registers: fewer pieces a thread
-    // (2048 x 4097 bf16 44 us with two, 53 with four; forward 31 with four, 40 with two)
+    // (2048 x 4097 bf16 44 us with two where four took 53; forward 31 with four, 40 with two)
     s.per = groups <= 32 ? 1 : groups <= 64 || (!vec && grad && groups <= 1024) ? 2 : 4;
     s.many = groups > 32 * s.per;
     s.warps = s.many ? (int)((groups + 32 * s.per - 1) / (32 * s.per)) : 1;
     s.lanes = 1;
     while (!s.many && s.lanes < 32 && s.lanes * s.per < groups) s.lanes *= 2;
-    // 12 warps with registers to spare (8192 x 1600 bf16 19 and 25 us, with 16 warps 24 and
-    // 32); 16, of 128 registers a thread, for the widest rows and element by element
+    // 12 warps with registers to spare (8192 x 1600 bf16 19 and 25 us where 16 warps took 24
+    // and 32); 16, of 128 registers a thread, for the widest rows and element by element
     s.most = s.many && (s.warps > 12 || s.per == 2 || (!vec && !grad)) ? 512 : 384;
     const int64_t in_warp = s.many ? 1 : 32 / s.lanes, most = s.many ? s.most / 32 / s.warps : s.most / 32 * in_warp;
     int64_t teams = (rows + sms - 1) / sms;
