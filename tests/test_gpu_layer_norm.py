@@ -19,6 +19,7 @@ SHAPES = [  # rows, cols
     (1, 1), (3, 2), (5, 7), (1, 8), (9, 8), (70, 16), (33, 24), (1, 64), (257, 65), (19, 200), (1000, 256), (7, 257), (2, 511), (300, 512),
     (1, 520), (45, 1023), (1, 1600), (333, 1600), (1300, 1600), (77, 1601), (5, 4096), (700, 4097), (3, 4104), (31, 6401), (1, 8192),
     (40, 8200), (200, 11008), (2, 16384), (3, 16391), (5, 16392), (2, 33000),
+    (1, 1601), (152, 2049), (153, 2049), (400, 2050), (305, 6401), (1, 8191), (460, 4099),   # rows of a CTA from one on, off the grid
 ]
 
 
