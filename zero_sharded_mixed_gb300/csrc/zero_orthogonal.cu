@@ -647,9 +647,6 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
     await_predecessor();
     const uint32_t tmem = *tmem_slot;
 
-    const int b_boxes = p.b_mn ? (p.bn / 2 + 63) / 64 : 1;
-    const uint32_t stage_bytes = 16384u + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)p.bn * 64u);
-
     if (warp == 0) {
         int s = 0;
         uint32_t round = 0;
@@ -657,7 +654,9 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
         for (int n = 0, t; ok && (t = turns.tile(p, n)) >= 0; ++n) {
             const Place w = place_of<kStep>(p, t);
             const int row = w.tm * 256 + (int)rank * 128;
-            const int col = w.tn * p.bn + (int)rank * (width_of(p, w.tn) / 2);
+            const int half = width_of(p, w.tn) / 2, col = w.tn * p.bn + (int)rank * half;
+            const int b_boxes = p.b_mn ? (half + 63) / 64 : 1;
+            const uint32_t stage_bytes = 16384u + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)p.bn * 64u);
             for (int kb = 0; kb < p.k_blocks; ++kb) {
                 if (round > 0 && !(ok = step_wait(empty + s, (round - 1) & 1))) break;
                 const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384;

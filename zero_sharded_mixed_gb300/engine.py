@@ -86,7 +86,8 @@ class ZeroEngine(_Tracing):
 
     def __init__(self, numels, n_dp: int, config: ZeroConfig, master: torch.Tensor | None = None,
                  device="cuda", align: int = 8, shapes=None):
-        """shapes: the tensors' shapes, for the Muon optimizer alone."""
+        """shapes: the tensors' shapes, for the Muon optimizer alone; a tensor that AdamW is
+        to move, as an embedding, is given with one dimension."""
         if config.stage not in (1, 2):
             raise ValueError("ZeroEngine runs stages 1 and 2; use Zero3Engine for stage 3")
         self.cfg = config
