@@ -624,6 +624,8 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
     const int warp = uniform_warp();
     const uint32_t rank = cluster_rank();
     const Turns turns(p);
+    const int t_first = turns.tile(p, 0);   // every pair has one; placed before the wait below
+    const Place first_place = place_of<kStep>(p, t_first);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -651,8 +653,8 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
         int s = 0;
         uint32_t round = 0;
         bool ok = true;
-        for (int n = 0, t; ok && (t = turns.tile(p, n)) >= 0; ++n) {
-            const Place w = place_of<kStep>(p, t);
+        for (int n = 0, t = t_first; ok && t >= 0; t = turns.tile(p, ++n)) {
+            const Place w = n == 0 ? first_place : place_of<kStep>(p, t);
             const int row = w.tm * 256 + (int)rank * 128;
             const int half = width_of(p, w.tn) / 2, col = w.tn * p.bn + (int)rank * half;
             const int b_boxes = p.b_mn ? (half + 63) / 64 : 1;
@@ -689,8 +691,8 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
         uint32_t round = 0;
         bool ok = true;
         const uint32_t a_step = descriptor_step(p.a_mn), b_step = descriptor_step(p.b_mn);
-        for (int t; ok && (t = turns.tile(p, use)) >= 0; ++use) {
-            const Place w = place_of<kStep>(p, t);
+        for (int t = t_first; ok && t >= 0; t = turns.tile(p, ++use)) {
+            const Place w = use == 0 ? first_place : place_of<kStep>(p, t);
             const uint32_t idesc = instruction_descriptor(256, width_of(p, w.tn), p.a_mn, p.b_mn, false);
             const int buf = use & 1;
             if (use >= 2 && !(ok = step_wait(acc_empty + buf, (use / 2 - 1) & 1))) break;
@@ -735,13 +737,13 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
                 end.load(p.e, w.z, w.tm * 256 + row_in, w.tn * p.bn + first * 32);
             }
         };
-        int t = turns.tile(p, 0);
+        int t = t_first;
         float v[4][4] = {};
         float2 r[2][4];
         if (t >= 0) {
             // before the first tile the end goes once through rows that do not exist, so that
             // its instructions are there when the product is (0.4 us of a launch)
-            const Place w = place_of<kStep>(p, t);
+            const Place w = first_place;
             end.put(at);
             end.form(p.e, at, v, r);
             end.finish(p.e, at, 0.0f, w.z, p.e.rows, w.tn * p.bn, w.tn * p.bn >= (w.tm + 1) * 256, r);
