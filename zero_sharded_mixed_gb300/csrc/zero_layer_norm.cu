@@ -410,7 +410,6 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
     extern __shared__ uint4 slots[];
     __shared__ WarpStats stats[2][kMostWarps];
     constexpr int kSize = kF32 ? 4 : 2;
-    await_predecessor();
     constexpr Lay kLay = lay_of(kVec, kF32);
     int which, teams, turn = 0;
     const Team m = team_of<kLay, kMany>(p, &which, &teams);
@@ -432,10 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
         }
         sent += stride;
     };
-    Ring<kVec, kMany> ring(reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes), p.slot, p.ahead, which, send);
     char* sum = output<kLay>(p.sum, p.lds, kSize, row, m);
     char* y = output<kLay>(p.y, p.ldy, p.y_f32 ? 4 : 2, row, m);
     const int64_t sum_hop = stride * p.lds * kSize, y_hop = stride * p.ldy * (p.y_f32 ? 4 : 2);
+    await_predecessor();
+    Ring<kVec, kMany> ring(reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes), p.slot, p.ahead, which, send);
     Words<false> gamma[kPer], beta[kPer];
     float n = 0.0f;   // this warp's columns, or the team's
 #pragma unroll
@@ -590,7 +590,6 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
     constexpr bool kBulk = kMany && !kVec;
     __shared__ uint64_t full[kMostWarps / 2][kMostAhead + 1];
     if constexpr (kBulk) bulk_ring_start(full, p.residual ? 3 : 2);
-    await_predecessor();
     constexpr Lay kLay = lay_of(kVec, kF32);
     int which, teams, turn = 0;
     const Team m = team_of<kLay, kMany>(p, &which, &teams);
@@ -617,6 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         }
         sent += stride;
     };
+    char* dx = output<kLay>(p.y, p.ldy, kSize, row, m);
+    const int64_t dx_hop = stride * p.ldy * kSize;
+    await_predecessor();
     auto ring = [&] {
         uint8_t* base = reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes);
         if constexpr (kBulk)
@@ -624,8 +626,6 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         else
             return Ring<kVec, kMany>(base, p.slot, p.ahead, which, send);
     }();
-    char* dx = output<kLay>(p.y, p.ldy, kSize, row, m);
-    const int64_t dx_hop = stride * p.ldy * kSize;
     Words<false> gamma[kPer];
     float2 sum_g[kPer][4], sum_b[kPer][4];
 #pragma unroll

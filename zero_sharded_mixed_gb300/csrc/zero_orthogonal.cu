@@ -17,6 +17,7 @@
 // thousand times above the rest), before the 1.7e-3 of its own rounding to bf16.
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cmath>
 
 #include "zero_dense.cuh"
@@ -163,17 +164,24 @@ __device__ __forceinline__ double squares(const SourceParams& p, int z, uint32_t
 
 // hi + lo / 2^11 = x 2^(12 - e) with e the norm's exponent, and scale = 2^e / norm: the
 // power of two costs a bf16 x no bit, and the first step's products take in the scale.
-// One thread forms them (fp64 is slow: by all threads of a CTA it took 8 us).
+// One thread forms them, in fp32 beside the exponents (fp64 is slow: its root and quotient
+// took 0.4 us more, by all threads of a CTA 8 us).
 struct SourceScale {
     float f1, f2, scale;   // f1 f2 = 2^(12 - e), in two parts for want of range
 };
 __device__ __noinline__ SourceScale source_scale(double sum, float eps) {
-    const double norm = sqrt(sum) + (double)eps;
-    int e = 0;
-    const double f = norm > 0.0 && norm < INFINITY ? frexp(norm, &e) : norm;
-    const int k = 12 - e;
-    // of zeros, zeros; of what is not finite, NaN
-    return SourceScale{ldexpf(1.0f, k / 2), ldexpf(1.0f, k - k / 2), norm == 0.0 ? 0.0f : norm < INFINITY ? (float)(1.0 / f) : NAN};
+    if (!(sum < INFINITY)) return SourceScale{64.0f, 64.0f, NAN};   // of what is not finite, NaN
+    // sum = m 4^k with 1 <= m < 4, norm = n 2^e
+    const int hi = __double2hiint(sum), k = ((hi >> 20) - 1023) >> 1;
+    const int of_eps = eps > 0.0f ? ilogbf(eps) : INT_MIN;
+    int e = sum > 0.0 && k > of_eps ? k : of_eps;
+    if (e == INT_MIN) return SourceScale{64.0f, 64.0f, 0.0f};   // of zeros, zeros
+    float n = eps > 0.0f ? ldexpf(eps, -e) : 0.0f;
+    if (sum > 0.0) n += ldexpf(sqrtf((float)__hiloint2double(hi - 2 * k * (1 << 20), __double2loint(sum))), k - e);
+    // 1 <= n < 4
+    for (; n >= 1.0f; ++e) n *= 0.5f;
+    const int f = 12 - e;
+    return SourceScale{ldexpf(1.0f, f / 2), ldexpf(1.0f, f - f / 2), 1.0f / n};
 }
 __device__ __forceinline__ void parts_of(const SourceParams& p, int z, const SourceScale& s, uint32_t first, uint32_t share) {
     const float f1 = s.f1, f2 = s.f2;
@@ -244,9 +252,14 @@ __global__ void __launch_bounds__(kHeldThreads, 1) orthogonal_held_kernel(const 
     }
     cluster_sync();
     if (threadIdx.x == 0) {   // every CTA in the same order
-        double t = 0.0;
-        for (int i = 0; i < kHeldCtas; ++i) t += peer_load_double(peer_addr(smem_addr(&total), i));
-        scale = source_scale(t, p.eps);
+        double t[kHeldCtas];
+#pragma unroll
+        for (int i = 0; i < kHeldCtas; ++i) t[i] = peer_load_double(peer_addr(smem_addr(&total), i));
+#pragma unroll
+        for (int o = 1; o < kHeldCtas; o *= 2)
+#pragma unroll
+            for (int i = 0; i < kHeldCtas; i += 2 * o) t[i] += t[i + o];
+        scale = source_scale(t[0], p.eps);
         if (rank == 0) p.scale[z] = scale.scale;
     }
     __syncthreads();
@@ -263,8 +276,9 @@ __global__ void __launch_bounds__(kHeldThreads, 1) orthogonal_held_kernel(const 
 // cycles each, 32768 being the products' own) and at the clock that the power limit leaves,
 // 1.4 to 1.5 GHz: 2.1 ms for 3.11 TFLOP.  At 12 x 4800 x 1600 X' moves 740 MB besides, 216
 // to 238 us a step for 184 of products at that clock.  Small ones are bound by latency:
-// 256 x 256 takes 4.2 us a product, 1.1 from one kernel's end to the next one's first load,
-// 1.0 until that arrives, 0.9 for products and their commit, 0.4 to 0.9 for the end.
+// 256 x 256 takes 3.6 us a product, 1.1 from one kernel's end to the next one's first load,
+// 1.0 until that arrives, 0.9 for products and their commit, 0.4 to 0.9 for the end (and
+// 0.35 more where the first tile's place is found after the wait for the kernel before).
 enum Step { kGram, kSquare, kApplyWide, kApplyTall };
 constexpr bool applies(Step s) { return s == kApplyWide || s == kApplyTall; }
 template <Step kStep> constexpr bool kApplies = applies(kStep);
@@ -804,7 +818,7 @@ static bool make_map3(const Matrices& m, int box_rows, CUtensorMap* map) {
 // The tile width with the least estimated time: a tile's blocks (bound by the tensor core,
 // or for narrow tiles by shared memory) and the part of its end that nothing hides, as
 // often as the busiest pair has them.  A symmetric result takes widths that divide 256.
-// 256 x 256 takes 64 us in tiles of 32 columns and 106 in tiles of 256; 2048 x 8192 461 as
+// 256 x 256 takes 58 us in tiles of 32 columns and 100 in tiles of 256; 2048 x 8192 461 as
 // planned, 500 with 128 for all, 561 with 256, 1469 with 32.
 struct StepPlan {
     int64_t tiles, full, all, lights;
