@@ -109,6 +109,18 @@ def test_in_place(zlib, cuda_device, shape):
     assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("shape", [(64, 11008), (11008, 64), (1, 5000), (17, 4100), (300, 6000), (6003, 301), (512, 2048), (3, 40, 9000), (5, 4999, 33),
+                                   (2, 260, 3001)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_long_axes(zlib, cuda_device, shape, dtype):
+    """Few tiles over a long axis, whose sums are formed in parts."""
+    x = _x(shape, dtype, 11)
+    y = _run(zlib, x.cuda())
+    zlib.zero_status_check()
+    _close(y, x)
+    assert torch.equal(_run(zlib, x.cuda()), y)
+
+
 @pytest.mark.parametrize("shape", [(48, 80), (270, 131)])
 def test_side_by_side(zlib, cuda_device, shape):
     """Matrices that are column blocks of a wider one, orthogonalised one by one, in place too."""

@@ -245,8 +245,9 @@ inline int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, i
 // before its first access to global memory, until its predecessor has ended and its
 // writes are visible.  Kernels without these two calls (other libraries', this
 // library's update) are unaffected before and after.  Saves about 2 us a launch.
+__device__ __forceinline__ void start_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void await_predecessor() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    start_successor();
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 

@@ -276,9 +276,10 @@ __global__ void __launch_bounds__(kHeldThreads, 1) orthogonal_held_kernel(const 
 // cycles each, 32768 being the products' own) and at the clock that the power limit leaves,
 // 1.4 to 1.5 GHz: 2.1 ms for 3.11 TFLOP.  At 12 x 4800 x 1600 X' moves 740 MB besides, 216
 // to 238 us a step for 184 of products at that clock.  Small ones are bound by latency:
-// 256 x 256 takes 3.6 us a product, 1.1 from one kernel's end to the next one's first load,
+// 256 x 256 takes 3.4 us a product: some 1 from one kernel's end to the next one's first load,
 // 1.0 until that arrives, 0.9 for products and their commit, 0.4 to 0.9 for the end (and
-// 0.35 more where the first tile's place is found after the wait for the kernel before).
+// 0.5 more where the first tile's place and the end's first pass come after the wait for the
+// kernel before).
 enum Step { kGram, kSquare, kApplyWide, kApplyTall };
 constexpr bool applies(Step s) { return s == kApplyWide || s == kApplyTall; }
 template <Step kStep> constexpr bool kApplies = applies(kStep);
@@ -296,6 +297,7 @@ struct StepEnding {
     bool y_vec;
     float* factors; int64_t factor_stride; // scale (a + B_ii)
     bool turned;                           // kSquare: rows of d in the order of turned_row
+    float* partial; int64_t partial_stride;   // kGram of few tiles and a long sum: its parts, as matrices of fp32, or null
     const float* scale;
     float a, b, c;
 };
@@ -305,6 +307,7 @@ struct StepParams {
     int32_t tiles_n, tiles, full, all;     // column tiles; tiles a matrix of which `full` counts the batch's; and with narrow ones after those
     int32_t lights;                        // narrow tiles for pairs with one full tile less
     int32_t bn, k_blocks;
+    int32_t splits, share;                 // kGram: parts of the sum, and their blocks
     bool a_mn, b_mn;
     StepEnding e;
 };
@@ -317,7 +320,7 @@ constexpr int kUnitBytes = 1024;        // 16 rows x 32 columns: an ending warp 
 constexpr int kStepSmem = 1024 + kStages * kStageBytes + 256 + kEndWarps * 2 * kUnitBytes;
 
 struct Place {
-    int z, tm, tn;
+    int z, tm, tn, part;
 };
 // The order of the tiles.  X' goes through X once: a wide X column by column, a tall
 // one row by row, the rows or columns of B together.  A symmetric result has of row tile
@@ -328,6 +331,7 @@ struct Place {
 template <Step kStep>
 __device__ __forceinline__ Place place_of(const StepParams& p, int t) {
     Place w;
+    w.part = 0;
     if constexpr (kApplies<kStep>) {
         w.z = t / p.tiles;
         t -= w.z * p.tiles;
@@ -357,7 +361,18 @@ __device__ __forceinline__ Place place_of(const StepParams& p, int t) {
         w.tm = t - w.z * tiles_m;
         w.tn = p.tiles_n - 1;
     }
+    if (kStep == kGram && p.splits > 1) {
+        const int z = w.z / p.splits;
+        w.part = w.z - z * p.splits;
+        w.z = z;
+    }
     return w;
+}
+// The blocks of a tile's sum.
+template <Step kStep>
+__device__ __forceinline__ void blocks_of(const StepParams& p, const Place& w, int* from, int* to) {
+    *from = kStep == kGram ? w.part * p.share : 0;
+    *to = kStep == kGram && *from + p.share < p.k_blocks ? *from + p.share : p.k_blocks;
 }
 // A pair's tiles: every so many of the full ones; then of the narrow ones, which take half
 // to three quarters of the time, the first `lights` are for those pairs that have had one
@@ -525,8 +540,19 @@ struct StepEnd {
         else
             return unit_load(u.vec + area + 512 * h);
     }
-    __device__ __forceinline__ static void finish(const StepEnding& p, const UnitPlace& u, float s, int z, int row0, int col0, bool mirror, float2 (&w)[2][4]) {
+    __device__ __forceinline__ static void finish(const StepEnding& p, const UnitPlace& u, float s, int z, int part, int row0, int col0, bool mirror, float2 (&w)[2][4]) {
         const int i = (threadIdx.x & 31) >> 2, j = threadIdx.x & 3;
+        if (kStep == kGram && p.partial) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = row0 + i + 8 * h;
+                float* q = p.partial + part * p.partial_stride + z * p.stride + row * p.ld + col0 + 2 * j;
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    if (row < p.rows) *reinterpret_cast<float2*>(q + 8 * g) = w[h][g];
+            }
+            return;
+        }
         uint32_t d[2][4];
         if (kApplies<kStep> && p.y) {
             const float2 c = make_float2(1.0f / kX, 1.0f / kX);
@@ -660,9 +686,10 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
     __syncthreads();
     cluster_started();
     tcgen05_fence_after();
-    await_predecessor();
+    start_successor();
     const uint32_t tmem = *tmem_slot;
 
+    // the copying and the ending warps wait for the kernel before, each as late as it can
     if (warp == 0) {
         int s = 0;
         uint32_t round = 0;
@@ -673,7 +700,10 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             const int half = width_of(p, w.tn) / 2, col = w.tn * p.bn + (int)rank * half;
             const int b_boxes = p.b_mn ? (half + 63) / 64 : 1;
             const uint32_t stage_bytes = 16384u + (p.b_mn ? (uint32_t)b_boxes * kSubTileBytes : (uint32_t)p.bn * 64u);
-            for (int kb = 0; kb < p.k_blocks; ++kb) {
+            int from, to;
+            blocks_of<kStep>(p, w, &from, &to);
+            if (n == 0) await_predecessor();
+            for (int kb = from; kb < to; ++kb) {
                 if (round > 0 && !(ok = step_wait(empty + s, (round - 1) & 1))) break;
                 const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + 16384;
                 const uint32_t bar = peer_addr(smem_addr(full + s), 0);
@@ -712,7 +742,9 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             if (use >= 2 && !(ok = step_wait(acc_empty + buf, (use / 2 - 1) & 1))) break;
             tcgen05_fence_after();
             const uint32_t d = tmem + buf * 256;
-            for (int kb = 0; kb < p.k_blocks; ++kb) {
+            int from, to;
+            blocks_of<kStep>(p, w, &from, &to);
+            for (int kb = from; kb < to; ++kb) {
                 if (!(ok = step_wait(full + s, round & 1))) break;
                 tcgen05_fence_after();
                 const uint32_t a = smem_addr(smem + s * kStageBytes);
@@ -721,7 +753,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
                 if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)   // the last step of all may end early
-                        if (left > 16 * i) mma_bf16<true>(d, da + i * a_step, db + i * b_step, idesc, kb > 0 || i > 0);
+                        if (left > 16 * i) mma_bf16<true>(d, da + i * a_step, db + i * b_step, idesc, kb > from || i > 0);
                     mma_commit<true>(empty + s);
                 }
                 if (++s == kStages) s = 0, ++round;
@@ -756,11 +788,13 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
         float2 r[2][4];
         if (t >= 0) {
             // before the first tile the end goes once through rows that do not exist, so that
-            // its instructions are there when the product is (0.4 us of a launch)
+            // its instructions are there when the product is (0.4 us of a launch); it reads
+            // and writes no global memory
             const Place w = first_place;
             end.put(at);
             end.form(p.e, at, v, r);
-            end.finish(p.e, at, 0.0f, w.z, p.e.rows, w.tn * p.bn, w.tn * p.bn >= (w.tm + 1) * 256, r);
+            end.finish(p.e, at, 0.0f, w.z, w.part, p.e.rows, w.tn * p.bn, w.tn * p.bn >= (w.tm + 1) * 256, r);
+            await_predecessor();
             begin(w);
         }
         for (int use = 0; t >= 0; ++use) {
@@ -780,7 +814,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
                     if (u + 1 == units) release_accumulator(acc_empty + buf);   // this warp's last read
                     end.form(p.e, at, v, r);
                     if (StepEnd<kStep>::kTall && u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
-                    end.finish(p.e, at, end.s, w.z, row0, col_first + u * 32, mirror, r);
+                    end.finish(p.e, at, end.s, w.z, w.part, row0, col_first + u * 32, mirror, r);
                 }
             } else {
                 release_accumulator(acc_empty + buf);
@@ -796,6 +830,30 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
     cluster_started();
     tcgen05_fence_after();
     if (warp == 2) tmem_free<true>(tmem, 512);
+}
+
+// The parts of a split Gram product added in order (they carry their factor already), eight
+// columns a thread.
+struct JoinParams {
+    const float* partial; int64_t partial_stride, square;
+    int32_t splits, side, lds;
+    uint16_t* d;
+};
+__global__ void __launch_bounds__(256) orthogonal_join_kernel(const JoinParams p) {
+    await_predecessor();
+    const int groups = p.lds / 8, g = blockIdx.x * 256 + threadIdx.x, row = g / groups, col = (g - row * groups) * 8;
+    if (row >= p.side) return;
+    const float* q = p.partial + blockIdx.y * p.square;
+    float v[8] = {};
+    q += (int64_t)row * p.lds + col;
+#pragma unroll 8
+    for (int i = 0; i < p.splits; ++i, q += p.partial_stride) {
+        const float4 a = *reinterpret_cast<const float4*>(q), b = *reinterpret_cast<const float4*>(q + 4);
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    *reinterpret_cast<uint4*>(p.d + blockIdx.y * p.square + (int64_t)row * p.lds + col) =
+        make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
 }
 
 // ---- launches ------------------------------------------------------------------------------
@@ -818,13 +876,13 @@ static bool make_map3(const Matrices& m, int box_rows, CUtensorMap* map) {
 // The tile width with the least estimated time: a tile's blocks (bound by the tensor core,
 // or for narrow tiles by shared memory) and the part of its end that nothing hides, as
 // often as the busiest pair has them.  A symmetric result takes widths that divide 256.
-// 256 x 256 takes 58 us in tiles of 32 columns and 100 in tiles of 256; 2048 x 8192 461 as
+// 256 x 256 takes 55 us in tiles of 32 columns and some 97 in tiles of 256; 2048 x 8192 461 as
 // planned, 500 with 128 for all, 561 with 256, 1469 with 32.
 struct StepPlan {
-    int64_t tiles, full, all, lights;
+    int64_t tiles, full, all, lights, cycles;
     int bn, tiles_n;
 };
-static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, int64_t batch) {
+static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, int64_t batch, int64_t most) {
     const int64_t k_blocks = (depth + 63) / 64, tm = (rows + 255) / 256;
     const auto time_of = [&](int64_t width) { return 1500 + k_blocks * (2 * width > 256 + width ? 2 * width : 256 + width) + 24 * width; };
     StepPlan best{};
@@ -838,14 +896,35 @@ static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, 
             narrow = cols % bn ? tm : 0;
         }
         if (tiles + narrow > INT32_MAX / 4 / batch) continue;
-        StepPlan q{tiles, tiles * batch, (tiles + narrow) * batch, 0, bn, (int)tn};
-        const int64_t pairs = q.all < sm_pairs() ? q.all : sm_pairs(), more = q.full % pairs, light = pairs - more;
+        StepPlan q{tiles, tiles * batch, (tiles + narrow) * batch, 0, 0, bn, (int)tn};
+        const int64_t pairs = q.all < most ? q.all : most, more = q.full % pairs, light = pairs - more;
         const int64_t whole = time_of(bn), part = time_of((cols % bn + 31) / 32 * 32), fit = (whole + part / 2) / part;
         q.lights = q.all - q.full < (fit > 1 ? fit : 1) * light ? q.all - q.full : (fit > 1 ? fit : 1) * light;
         int64_t cycles = q.full / pairs * whole + (q.lights + light - 1) / light * part;
         if (more && cycles < (q.full / pairs + 1) * whole) cycles = (q.full / pairs + 1) * whole;
         cycles += (q.all - q.full - q.lights + pairs - 1) / pairs * part;
-        if (cycles < least) least = cycles, best = q;
+        if (cycles < least) least = q.cycles = cycles, best = q;
+    }
+    return best;
+}
+
+// Parts of a Gram product's sum, where few tiles would leave most pairs idle over a long
+// axis: what saves a tenth at least, the join included, which takes 5 us of a product.
+// (64 x 11008 takes 92 us, 203 in one part; 256 x 2048 84, 92 in parts.)  Sides of one row of
+// tiles, whose parts are whole: with more, half of the parts come from across the diagonal,
+// and 1024 x 8192 took 350 us for 270.  Reckoned for the device that this is made for, so
+// that the workspace does not depend on the current one.
+constexpr int kMostSplits = 16;
+static int gram_splits(int64_t side, int64_t longer, int64_t batch, int64_t square) {
+    const int64_t blocks = (longer + 63) / 64, one = plan_step(kGram, side, side, longer, batch, 76).cycles;
+    int best = 1;
+    if (side > 256) return best;
+    int64_t least = one - one / 10;
+    for (int n = 2; n <= kMostSplits && n <= blocks / 4; ++n) {
+        const int64_t share = (blocks + n - 1) / n;
+        if ((n - 1) * share >= blocks || n * batch * square > ((int64_t)1 << 24) || n * batch > 65535) continue;
+        const int64_t cycles = plan_step(kGram, side, side, share * 64, batch * n, 76).cycles + 9000 + 300 * n;
+        if (cycles < least) least = cycles, best = n;
     }
     return best;
 }
@@ -853,10 +932,11 @@ static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, 
 // A step's launch but for its end, which changes from iteration to iteration: formed
 // before the first launch, so that a call that cannot be made has launched nothing.
 template <Step kStep>
-static int prepare_step(StepParams& q, int64_t rows, int64_t cols, int64_t depth, const Matrices& a, bool a_mn, const Matrices& b, bool b_mn) {
+static int prepare_step(StepParams& q, int64_t rows, int64_t cols, int64_t depth, const Matrices& a, bool a_mn, const Matrices& b, bool b_mn, int splits = 1) {
     static Done done;
     if (const int rc = allow_smem((const void*)orthogonal_step_kernel<kStep>, kStepSmem, done)) return rc;
-    const StepPlan plan = plan_step(kStep, rows, cols, depth, a.batch);
+    const int64_t blocks = (depth + 63) / 64, share = (blocks + splits - 1) / splits;
+    const StepPlan plan = plan_step(kStep, rows, cols, share * 64 < depth ? share * 64 : depth, a.batch * splits, sm_pairs());
     if (!plan.bn) return ZERO_ERANGE;
     q.depth = (int32_t)depth;
     q.bn = plan.bn;
@@ -865,7 +945,9 @@ static int prepare_step(StepParams& q, int64_t rows, int64_t cols, int64_t depth
     q.full = (int32_t)plan.full;
     q.all = (int32_t)plan.all;
     q.lights = (int32_t)plan.lights;
-    q.k_blocks = (int32_t)((depth + 63) / 64);
+    q.k_blocks = (int32_t)blocks;
+    q.splits = splits;
+    q.share = (int32_t)share;
     q.a_mn = a_mn; q.b_mn = b_mn;
     return make_map3(a, a_mn ? 64 : 128, &q.map_a) && make_map3(b, b_mn ? 64 : q.bn / 2, &q.map_b) ? ZERO_OK : ZERO_ECUDA;
 }
@@ -879,7 +961,8 @@ static int launch_step(const StepParams& q, cudaStream_t s) {
 // Where everything stands in the workspace.
 struct OrthogonalSpace {
     int64_t ldx, lds, square, parts;               // rows of X; rows of A and B, and their elements
-    int64_t hi[2], lo[2], a, b, factors, norm, scale, bytes;
+    int64_t hi[2], lo[2], a, b, factors, norm, scale, partial, bytes;
+    int splits;                                    // of the Gram products' sums
 };
 constexpr int64_t kLongest = (int64_t)1 << 30;
 
@@ -907,6 +990,8 @@ static int orthogonal_space(int64_t batch, int64_t rows, int64_t cols, Orthogona
     w->factors = take(batch * w->lds * (int64_t)sizeof(float));
     w->norm = take(batch * w->parts * 8);
     w->scale = take(batch * 4);
+    w->splits = gram_splits(side, longer, batch, w->square);
+    w->partial = take(w->splits > 1 ? w->splits * batch * w->square * 4 : 0);
     w->bytes = at;
     return ZERO_OK;
 }
@@ -997,6 +1082,10 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
             d.ld = w.lds; d.stride = w.square;
             d.c_hi = at(w.a);
             d.d_hi = at(step == kGram ? w.a : w.b);
+            if (step == kGram && w.splits > 1) {
+                d.partial = reinterpret_cast<float*>(base + w.partial);
+                d.partial_stride = batch * w.square;
+            }
         }
         return d;
     };
@@ -1005,7 +1094,7 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     if (const int rc = prepare_step<kSquare>(square_step, side, side, side, gram, false, gram, false)) return rc;
     for (int i = 0; i < 2; ++i) {
         const Matrices& now = i ? second : first;
-        if (const int rc = prepare_step<kGram>(gram_step[i], side, side, longer, now, tall, now, tall)) return rc;
+        if (const int rc = prepare_step<kGram>(gram_step[i], side, side, longer, now, tall, now, tall, w.splits)) return rc;
         // wide: B X, X read along its rows; tall: X B, B being its own transpose
         if (const int rc = tall ? prepare_step<kApplyTall>(apply_step[i], rows, cols, side, now, false, poly, false)
                                 : prepare_step<kApplyWide>(apply_step[i], rows, cols, side, poly, false, now, true))
@@ -1023,6 +1112,13 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
         StepParams &g = gram_step[i & 1], &a = apply_step[i & 1];
         g.e = ending(kGram, i);
         if (const int rc = launch_step<kGram>(g, s)) return rc;
+        if (w.splits > 1) {
+            JoinParams j{};
+            j.partial = g.e.partial; j.partial_stride = g.e.partial_stride; j.square = w.square;
+            j.splits = w.splits; j.side = (int32_t)side; j.lds = (int32_t)w.lds;
+            j.d = at(w.a);
+            if (const int rc = launch_dense(orthogonal_join_kernel, dim3((unsigned)((side * w.lds / 8 + 255) / 256), (unsigned)batch), 256, 1, true, 0, s, j)) return rc;
+        }
         square_step.e = ending(kSquare, i);
         if (const int rc = launch_step<kSquare>(square_step, s)) return rc;
         a.e = ending(tall ? kApplyTall : kApplyWide, i);
