@@ -658,8 +658,14 @@ int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, int64_t ldd
  *   element-aligned place.  A matrix of zeros gives zeros; one that is not finite NaN.
  *   The products take fp16 operands with fp32 sums, on two fp16 numbers for each element
  *   of X: with steps and coefficients like these the result is about 1e-3 off the exact
- *   one by norm (4e-3 at most, small matrices of a few strong directions), beside its
- *   rounding to bf16.  Singular values have to stay below 2 from
+ *   one by norm, beside its rounding to bf16 (1.7e-3).  Small matrices and directions of
+ *   very different strength cost more; the most that was found, over any number of equal
+ *   directions above a rest of 0.1 to 1e-4 of them, rows alike or scaled by factors of e:
+ *     shorter side     1..7    8..15   16..39  40..127  128 on
+ *     x in bf16        1.5e-2  1.3e-2  1e-2    1e-2     7.5e-3
+ *     x in fp32        1.3e-2  7e-3    6e-3    3e-3     2e-3
+ *   (Rounding such a matrix to bf16 before the call moves its result by 1e-2 to 0.5; one
+ *   that is exact in bf16 may be given in fp32.)  Singular values have to stay below 2 from
  *   step to step (coefficients that let them grow run into fp16's range, and NaN).
  *   workspace: device, 128-byte aligned, of zero_orthogonalize_workspace bytes; its
  *   contents on entry do not matter.  Calls that share one must not overlap on the GPU.

@@ -13,8 +13,10 @@
 // held as the sum of two fp16 numbers, `hi` and `lo` (22 bits), of which the products take
 // `hi`, and what they do to `lo` is put in by B's diagonal, its largest part, which is not
 // rounded either:  X' = (a + B_ii) (hi + lo) + fp16(B - diagonal) hi.  Against 64 bits:
-// 0.3e-3 to 1e-3 of the result by norm (2.5e-3 for 40 x 100 with two directions a
-// thousand times above the rest), before the 1.7e-3 of its own rounding to bf16.
+// 0.3e-3 to 1e-3 of the result by norm, before the 1.7e-3 of its own rounding to bf16;
+// with directions of very different strength up to 7e-3 for a bf16 matrix of 128 rows and
+// 1.2e-2 for one of 8, whose rounding to bf16 before the call has moved the result by ten
+// times that and more, and up to 2e-3 and 7e-3 for an fp32 one (StepEnd).
 #include <cuda_fp16.h>
 
 #include <climits>
@@ -63,6 +65,7 @@ struct SourceParams {
     bool f32, vec;
     double* norm;                      // [batch][parts]
     float* scale;                      // [batch]: X = scale * hi
+    float* even;                       // [batch], set to 1 for the first step; or null
     uint16_t* hi;
     uint16_t* lo;                      // null: hi is exact
     int64_t ld, to;                    // of hi and lo: row and matrix stride
@@ -218,7 +221,10 @@ __global__ void __launch_bounds__(kSourceThreads) orthogonal_source_kernel(const
         t = warp_sum(0.0f, t);
         if (threadIdx.x == 0) {
             scale = source_scale(t, p.eps);
-            if (blockIdx.x == 0) p.scale[blockIdx.y] = scale.scale;
+            if (blockIdx.x == 0) {
+                p.scale[blockIdx.y] = scale.scale;
+                if (p.even) p.even[blockIdx.y] = 1.0f;
+            }
         }
     }
     __syncthreads();
@@ -260,7 +266,10 @@ __global__ void __launch_bounds__(kHeldThreads, 1) orthogonal_held_kernel(const 
 #pragma unroll
             for (int i = 0; i < kHeldCtas; i += 2 * o) t[i] += t[i + o];
         scale = source_scale(t[0], p.eps);
-        if (rank == 0) p.scale[z] = scale.scale;
+        if (rank == 0) {
+            p.scale[z] = scale.scale;
+            if (p.even) p.even[z] = 1.0f;
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -299,6 +308,7 @@ struct StepEnding {
     bool turned;                           // kSquare: rows of d in the order of turned_row
     float* partial; int64_t partial_stride;   // kGram of few tiles and a long sum: its parts, as matrices of fp32, or null
     const float* scale;
+    float* even; float* even_next;         // kEven: how alike the singular values are, of this iteration and of the next
     float a, b, c;
 };
 struct StepParams {
@@ -439,14 +449,26 @@ __device__ __forceinline__ void matrix_store_turned(uint32_t at, const uint32_t 
 }
 
 // Matrices of the workspace have rows of whole units, so that only rows are checked.
-template <Step kStep>
+// kEven (an fp32 input): what stands for B in its product with lo.  Where some singular values
+// are far below the others, B is near zero on their vectors, but its diagonal, which holds a
+// share of the others' part, is not, and moves them by rounding errors of the large ones: 3 %
+// for 300 x 500 with one direction above a rest of 1e-4.  Leaving the product out errs along
+// the large directions alone, by 2^-12 of their own size, which costs matrices of equal
+// directions more (1.3e-3 for 0.8e-3).  So the diagonal stands for B where all rows of A have
+// most of themselves on theirs, (A_ii)^2 > (A A)_ii / 2 (3/4 for fewer than eight rows, of
+// which one faint direction in three leaves two thirds: 2.3e-2 for 9e-3), and else nothing
+// does.  The least of a matrix's rows decides, since a row that one large direction has for
+// itself looks well alone.
+template <Step kStep, bool kEven>
 struct StepEnd {
     static constexpr bool kTall = kStep == kApplyTall;
     uint4 hi[2], lo[2];   // a unit's on their way, this lane's vectors
     float4 f[2];          // kTall: the factors of their columns
     float s, f_row[2];    // of a tile: the scale; kApplyWide: the rows' factors
+    bool alike;           // kEven: whether the diagonal stands for B on lo
     __device__ __forceinline__ void tile(const StepEnding& p, int z, int row0) {
         s = p.first ? p.scale[z] : 1.0f;
+        if constexpr (kEven && kApplies<kStep>) alike = p.even[z] > ((p.rows < p.cols ? p.rows : p.cols) < 8 ? 0.75f : 0.5f);
         if constexpr (kStep == kApplyWide) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -487,8 +509,10 @@ struct StepEnd {
     __device__ __forceinline__ static void write(uint16_t* q, const uint4& v) {
         kOnce ? __stcs(reinterpret_cast<uint4*>(q), v) : (void)(*reinterpret_cast<uint4*>(q) = v);
     }
+    // Whether a unit meets the diagonal.
+    __device__ __forceinline__ static bool on_diagonal(int row0, int col0) { return row0 < col0 + 32 && col0 < row0 + 16; }
     // The result's pairs, from the accumulators and what was loaded.
-    __device__ __forceinline__ void form(const StepEnding& p, const UnitPlace& u, const float (&v)[4][4], float2 (&w)[2][4]) const {
+    __device__ __forceinline__ void form(const StepEnding& p, const UnitPlace& u, int z, int row0, int col0, const float (&v)[4][4], float2 (&w)[2][4]) const {
         if constexpr (kStep == kGram) {
             const float t = s * s * (kA / (kX * kX));
 #pragma unroll
@@ -498,6 +522,7 @@ struct StepEnd {
         }
         if constexpr (kStep == kSquare) {
             const float2 b = make_float2(p.b, p.b), c = make_float2(p.c / kA, p.c / kA);
+            float least = 1.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t x[4];
@@ -505,6 +530,21 @@ struct StepEnd {
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
                     w[h][g] = __ffma2_rn(b, unpack_f16x2(x[g]), __fmul2_rn(make_float2(v[g][2 * h], v[g][2 * h + 1]), c));
+                if (kEven && on_diagonal(row0, col0)) {
+                    const int row = row0 + ((threadIdx.x & 31) >> 2) + 8 * h;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 d = unpack_f16x2(x[g]);
+                            const float a = k ? d.y : d.x, aa = v[g][2 * h + k];   // A_ii, (A A)_ii
+                            if (row == col0 + 8 * g + 2 * (int)(threadIdx.x & 3) + k && row < p.rows && aa > 0.0f) least = fminf(least, a * a / aa);
+                        }
+                }
+            }
+            if (kEven && on_diagonal(row0, col0)) {   // floats from 0 on are in the order of their bits
+                const uint32_t bits = __reduce_min_sync(0xffffffffu, __float_as_uint(least));
+                if ((threadIdx.x & 31) == 0 && bits < __float_as_uint(1.0f)) atomicMin(reinterpret_cast<uint32_t*>(p.even) + z, bits);
             }
         }
         if constexpr (kApplies<kStep>) {
@@ -520,8 +560,13 @@ struct StepEnd {
                 for (int g = 0; g < 4; ++g) {
                     const float4 e = f[g / 2];
                     const float2 a = !kTall ? make_float2(f_row[h], f_row[h]) : g & 1 ? make_float2(e.z, e.w) : make_float2(e.x, e.y);
-                    w[h][g] = __ffma2_rn(a, __ffma2_rn(l, unpack_f16x2(y[g]), unpack_f16x2(x[g])),
-                                         __fmul2_rn(c, make_float2(v[g][2 * h], v[g][2 * h + 1])));
+                    const float2 product = __fmul2_rn(c, make_float2(v[g][2 * h], v[g][2 * h + 1]));
+                    if constexpr (kEven) {
+                        const float2 low = __fmul2_rn(l, alike ? a : make_float2(s * p.a, s * p.a));
+                        w[h][g] = __ffma2_rn(a, unpack_f16x2(x[g]), __ffma2_rn(low, unpack_f16x2(y[g]), product));
+                    } else {
+                        w[h][g] = __ffma2_rn(a, __ffma2_rn(l, unpack_f16x2(y[g]), unpack_f16x2(x[g])), product);
+                    }
                 }
             }
         }
@@ -583,7 +628,7 @@ struct StepEnd {
             }
             return;
         }
-        if (kStep == kSquare && row0 < col0 + 32 && col0 < row0 + 16) {   // the unit meets the diagonal
+        if (kStep == kSquare && on_diagonal(row0, col0)) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -593,6 +638,7 @@ struct StepEnd {
                     if (row == col && row < p.rows) {
                         p.factors[z * p.factor_stride + row] = s * (p.a + t * (1.0f / kA));
                         t = 0.0f;
+                        if (kEven && row == 0) p.even_next[z] = 1.0f;
                     }
                 }
         }
@@ -650,7 +696,7 @@ __device__ __forceinline__ void release_accumulator(uint64_t* bar) {
 
 __device__ __forceinline__ bool step_wait(uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, &g_orthogonal_status); }
 
-template <Step kStep>
+template <Step kStep, bool kEven>
 __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const __grid_constant__ StepParams p) {
     extern __shared__ uint8_t raw_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
@@ -775,7 +821,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             *first = (h >> 1) * ((all + 1) / 2);
             return h >> 1 ? all - *first : (all + 1) / 2;
         };
-        StepEnd<kStep> end{};
+        StepEnd<kStep, kEven> end{};
         const auto begin = [&](const Place& w) {   // what a tile's end reads first on its way
             int first;
             if (share(w, &first) > 0 && w.tm * 256 + row_in < p.e.rows) {
@@ -792,7 +838,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             // and writes no global memory
             const Place w = first_place;
             end.put(at);
-            end.form(p.e, at, v, r);
+            end.form(p.e, at, w.z, p.e.rows, w.tn * p.bn, v, r);
             end.finish(p.e, at, 0.0f, w.z, w.part, p.e.rows, w.tn * p.bn, w.tn * p.bn >= (w.tm + 1) * 256, r);
             await_predecessor();
             begin(w);
@@ -809,11 +855,11 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
 #pragma unroll 1
                 for (int u = 0; u < units; ++u) {
                     end.put(at);
-                    if (!StepEnd<kStep>::kTall && u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
+                    if (!end.kTall && u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
                     tmem_load_fragment(lanes + buf * 256 + (first + u) * 32, v);
                     if (u + 1 == units) release_accumulator(acc_empty + buf);   // this warp's last read
-                    end.form(p.e, at, v, r);
-                    if (StepEnd<kStep>::kTall && u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
+                    end.form(p.e, at, w.z, row0, col_first + u * 32, v, r);
+                    if (end.kTall && u + 1 < units) end.load(p.e, w.z, row0, col_first + u * 32 + 32);
                     end.finish(p.e, at, end.s, w.z, w.part, row0, col_first + u * 32, mirror, r);
                 }
             } else {
@@ -931,10 +977,10 @@ static int gram_splits(int64_t side, int64_t longer, int64_t batch, int64_t squa
 
 // A step's launch but for its end, which changes from iteration to iteration: formed
 // before the first launch, so that a call that cannot be made has launched nothing.
-template <Step kStep>
+template <Step kStep, bool kEven = false>
 static int prepare_step(StepParams& q, int64_t rows, int64_t cols, int64_t depth, const Matrices& a, bool a_mn, const Matrices& b, bool b_mn, int splits = 1) {
     static Done done;
-    if (const int rc = allow_smem((const void*)orthogonal_step_kernel<kStep>, kStepSmem, done)) return rc;
+    if (const int rc = allow_smem((const void*)orthogonal_step_kernel<kStep, kEven>, kStepSmem, done)) return rc;
     const int64_t blocks = (depth + 63) / 64, share = (blocks + splits - 1) / splits;
     const StepPlan plan = plan_step(kStep, rows, cols, share * 64 < depth ? share * 64 : depth, a.batch * splits, sm_pairs());
     if (!plan.bn) return ZERO_ERANGE;
@@ -951,17 +997,17 @@ static int prepare_step(StepParams& q, int64_t rows, int64_t cols, int64_t depth
     q.a_mn = a_mn; q.b_mn = b_mn;
     return make_map3(a, a_mn ? 64 : 128, &q.map_a) && make_map3(b, b_mn ? 64 : q.bn / 2, &q.map_b) ? ZERO_OK : ZERO_ECUDA;
 }
-template <Step kStep>
+template <Step kStep, bool kEven = false>
 static int launch_step(const StepParams& q, cudaStream_t s) {
     const int64_t pairs = sm_pairs();
-    return launch_dense(orthogonal_step_kernel<kStep>, dim3((unsigned)(2 * (q.all < pairs ? q.all : pairs))), kStepThreads, 2, true, kStepSmem,
+    return launch_dense(orthogonal_step_kernel<kStep, kEven>, dim3((unsigned)(2 * (q.all < pairs ? q.all : pairs))), kStepThreads, 2, true, kStepSmem,
                         s, q);
 }
 
 // Where everything stands in the workspace.
 struct OrthogonalSpace {
     int64_t ldx, lds, square, parts;               // rows of X; rows of A and B, and their elements
-    int64_t hi[2], lo[2], a, b, factors, norm, scale, partial, bytes;
+    int64_t hi[2], lo[2], a, b, factors, norm, scale, even, partial, bytes;
     int splits;                                    // of the Gram products' sums
 };
 constexpr int64_t kLongest = (int64_t)1 << 30;
@@ -990,6 +1036,7 @@ static int orthogonal_space(int64_t batch, int64_t rows, int64_t cols, Orthogona
     w->factors = take(batch * w->lds * (int64_t)sizeof(float));
     w->norm = take(batch * w->parts * 8);
     w->scale = take(batch * 4);
+    w->even = take(2 * batch * 4);
     w->splits = gram_splits(side, longer, batch, w->square);
     w->partial = take(w->splits > 1 ? w->splits * batch * w->square * 4 : 0);
     w->bytes = at;
@@ -1053,6 +1100,8 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     src.vec = cols % 8 == 0 && rows_aligned16(x, ldx, f32 ? 4 : 2) && (batch == 1 || x_stride * (f32 ? 4 : 2) % 16 == 0);
     src.norm = reinterpret_cast<double*>(base + w.norm);
     src.scale = reinterpret_cast<float*>(base + w.scale);
+    float* const even = f32 ? reinterpret_cast<float*>(base + w.even) : nullptr;   // [2][batch], of odd and even iterations
+    src.even = even;
     src.hi = at(w.hi[0]);
     src.lo = f32 ? at(w.lo[0]) : nullptr;
     src.ld = w.ldx; src.to = rows * w.ldx;
@@ -1070,6 +1119,10 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     const auto ending = [&](Step step, int i) {
         StepEnding d = e;
         d.first = i == 0;
+        if (even) {
+            d.even = even + (i & 1) * batch;
+            d.even_next = even + (~i & 1) * batch;
+        }
         if (applies(step)) {
             d.rows = (int32_t)rows; d.cols = (int32_t)cols;
             d.ld = w.ldx; d.stride = rows * w.ldx;
@@ -1091,13 +1144,13 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
     };
     // X stands in two places in turn
     StepParams gram_step[2]{}, square_step{}, apply_step[2]{};
-    if (const int rc = prepare_step<kSquare>(square_step, side, side, side, gram, false, gram, false)) return rc;
+    if (const int rc = (f32 ? prepare_step<kSquare, true> : prepare_step<kSquare, false>)(square_step, side, side, side, gram, false, gram, false, 1)) return rc;
     for (int i = 0; i < 2; ++i) {
         const Matrices& now = i ? second : first;
         if (const int rc = prepare_step<kGram>(gram_step[i], side, side, longer, now, tall, now, tall, w.splits)) return rc;
         // wide: B X, X read along its rows; tall: X B, B being its own transpose
-        if (const int rc = tall ? prepare_step<kApplyTall>(apply_step[i], rows, cols, side, now, false, poly, false)
-                                : prepare_step<kApplyWide>(apply_step[i], rows, cols, side, poly, false, now, true))
+        if (const int rc = tall ? (f32 ? prepare_step<kApplyTall, true> : prepare_step<kApplyTall, false>)(apply_step[i], rows, cols, side, now, false, poly, false, 1)
+                                : (f32 ? prepare_step<kApplyWide, true> : prepare_step<kApplyWide, false>)(apply_step[i], rows, cols, side, poly, false, now, true, 1))
             return rc;
     }
 
@@ -1120,13 +1173,15 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
             if (const int rc = launch_dense(orthogonal_join_kernel, dim3((unsigned)((side * w.lds / 8 + 255) / 256), (unsigned)batch), 256, 1, true, 0, s, j)) return rc;
         }
         square_step.e = ending(kSquare, i);
-        if (const int rc = launch_step<kSquare>(square_step, s)) return rc;
+        if (const int rc = (f32 ? launch_step<kSquare, true> : launch_step<kSquare, false>)(square_step, s)) return rc;
         a.e = ending(tall ? kApplyTall : kApplyWide, i);
         if (i + 1 == steps) {
             a.e.y = y; a.e.ldy = ldy; a.e.y_stride = batch > 1 ? y_stride : 0;
             a.e.y_vec = rows_aligned16(y, ldy, 2) && (batch == 1 || y_stride % 8 == 0);
         }
-        if (const int rc = tall ? launch_step<kApplyTall>(a, s) : launch_step<kApplyWide>(a, s)) return rc;
+        if (const int rc = tall ? (f32 ? launch_step<kApplyTall, true> : launch_step<kApplyTall, false>)(a, s)
+                                : (f32 ? launch_step<kApplyWide, true> : launch_step<kApplyWide, false>)(a, s))
+            return rc;
     }
     return ZERO_OK;
 }
