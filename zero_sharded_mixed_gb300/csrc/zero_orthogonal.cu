@@ -735,7 +735,8 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
     start_successor();
     const uint32_t tmem = *tmem_slot;
 
-    // the copying and the ending warps wait for the kernel before, each as late as it can
+    // the copying, the issuing and the ending warps wait for the kernel before, each as late as
+    // it can: the limits of their other waits then count this kernel's time alone
     if (warp == 0) {
         int s = 0;
         uint32_t round = 0;
@@ -790,6 +791,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) orthogonal_step_kernel(const 
             const uint32_t d = tmem + buf * 256;
             int from, to;
             blocks_of<kStep>(p, w, &from, &to);
+            if (use == 0) await_predecessor();
             for (int kb = from; kb < to; ++kb) {
                 if (!(ok = step_wait(full + s, round & 1))) break;
                 tcgen05_fence_after();
