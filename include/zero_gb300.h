@@ -698,7 +698,9 @@ int zero_status_check(void* stream);
 
 /* Launches one CTA that waits on an mbarrier nothing ever completes, bounded
  * by limit_cycles SM cycles (1 .. 2^32): the wait gives up, records
- * ZERO_ETIMEOUT for zero_status_check and the kernel returns.  For testing the
+ * ZERO_ETIMEOUT for zero_status_check and the kernel returns; and one in which a
+ * wait shared by several warps, as in zero_layer_norm_grad, gives up for one of
+ * them and ends in time for another, within twice that.  For testing the
  * failure path of bounded waits without faulting or hanging the GPU.
  * ZERO_EINVAL for a limit out of range. */
 int zero_selftest_bounded_wait(int64_t limit_cycles, void* stream);

@@ -1,4 +1,4 @@
-"""Bounded waits count their own kernel's time alone."""
+"""Bounded waits count their own kernel's time alone, and give up in order."""
 import math
 
 import pytest
@@ -31,3 +31,30 @@ def test_a_long_predecessor_is_no_timeout(zlib, cuda_device):
         zlib.zero_orthogonalize(u, after, workspace=ws)
         zlib.zero_status_check()
         assert torch.equal(after, alone)
+
+
+def test_a_team_gives_up_together(zlib, cuda_device):
+    """A wait that gives up in one warp and ends in time in another: both leave their ring, and
+    the gradient whose ring that is goes on as before."""
+    g = torch.Generator().manual_seed(2)
+    rows, cols = 300, 1601   # off the 16-byte grid, a row to several warps
+    x, dy = (torch.randn(rows, cols, generator=g).to(BF).cuda() for _ in range(2))
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    zlib.zero_layer_norm(x, y, mean=mean, rstd=rstd)
+    ws = torch.empty(zlib.zero_layer_norm_grad_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+
+    def grad():
+        out = [torch.empty_like(x), *(torch.empty(cols, device="cuda") for _ in range(2))]
+        zlib.zero_layer_norm_grad(dy, x, mean, rstd, out[0], dgamma=out[1], dbeta=out[2], workspace=ws)
+        return out
+
+    before = grad()
+    zlib.zero_status_check()
+    for limit in (1, 50_000, 2_000_000):
+        zlib.zero_selftest_bounded_wait(limit)
+        with pytest.raises(zlib.ZeroError) as e:
+            zlib.zero_status_check()
+        assert e.value.code == zlib.ZERO_ETIMEOUT
+        after = grad()
+        zlib.zero_status_check()
+        assert all(torch.equal(a, b) for a, b in zip(after, before))

@@ -534,32 +534,43 @@ __global__ void __launch_bounds__(kThreads, 1) norm_kernel(const NormParams p) {
 // once a row after a barrier of the team that follows next(), when the row before has been
 // read.  (With copies by all threads and a barrier more, 2048 x 4097 bf16 took 44 us for
 // 36, 1021 x 6401 fp32 27 for 24.8.  Forward, where fewer streams come, it was no gain.)
+// A wait that gives up is the team's matter, since one warp's may end just before the copy
+// comes and another's after: the warp goes on to that barrier as if the row were there, and
+// behind it all of them see its mark and leave.  (A warp that left by itself would leave the
+// others at the barrier for good.)  Marks of two rows in turn, as the sums.
 struct BulkRing {
     uint8_t* base;
     uint64_t* full;   // of the slots
+    int* gave_up;     // [2], the team's; 0 at first
     uint32_t size;
     int ahead, which, i = 0, last = 0;
     uint32_t phase = 0;
     template <class Send>
-    __device__ __forceinline__ BulkRing(uint8_t* base, uint32_t size, int ahead, int which, uint64_t* full, Send send)
-        : base(base), full(full), size(size), ahead(ahead), which(which) {
+    __device__ __forceinline__ BulkRing(uint8_t* base, uint32_t size, int ahead, int which, uint64_t* full, int* gave_up, Send send)
+        : base(base), full(full), gave_up(gave_up), size(size), ahead(ahead), which(which) {
         for (int a = 0; a < ahead; ++a) send(base + a * size, full + a);
     }
-    // null: the copy did not come in time
     template <class Send>
-    __device__ __forceinline__ const uint8_t* next(const Team& m, Send send) {
+    __device__ __forceinline__ const uint8_t* next(const Team& m, int turn, Send send, long long limit = kWaitCycles) {
         if (ahead == 0) {
             team_barrier(which, m.size);   // the last row has been read
             send(base, full);
         }
-        const bool there = warp_wait(full + i, phase, &g_norm_status);
-        if (!there)   // copies in flight land before the CTA ends
-            for (int k = 0; k <= ahead; ++k) (void)mbar_wait_bounded(full + k, k < i ? phase ^ 1 : phase, kWaitCycles / 8);
-        const uint8_t* here = there ? base + i * size : nullptr;
+        if (!warp_wait(full + i, phase, &g_norm_status, limit)) gave_up[turn] = 1;
+        const uint8_t* here = base + i * size;
         last = i ? i - 1 : ahead;
         if (i == ahead) i = 0, phase ^= 1;
         else ++i;
         return here;
+    }
+    // Behind the barrier: whether the team leaves.  Copies in flight land before the CTA ends.
+    __device__ __forceinline__ bool leaves(int turn, long long limit = kWaitCycles) {
+        if (!gave_up[turn]) return false;
+        const int now = i ? i - 1 : ahead;   // the slot that was waited for; none is on its way to `last`
+        (void)mbar_wait_bounded(full + now, i ? phase : phase ^ 1, limit / 8);
+        for (int k = 0; k <= ahead; ++k)
+            if (k != now && k != last) (void)mbar_wait_bounded(full + k, k < i ? phase ^ 1 : phase, limit / 8);
+        return true;
     }
     template <class Send>
     __device__ __forceinline__ void refill(Send send) {
@@ -573,14 +584,20 @@ __device__ __forceinline__ void send_row(uint8_t* slot, uint64_t* bar, int cols,
     mbar_arrive_expect_tx(bar, s.send_edges(smem_addr(slot), cols));
     s.send_whole(slot, bar);
 }
-__device__ __forceinline__ void bulk_ring_start(uint64_t (&full)[kMostWarps / 2][kMostAhead + 1], int streams) {
-    if (threadIdx.x == 0) {
-        for (int t = 0; t < kMostWarps / 2; ++t)
-            for (int i = 0; i <= kMostAhead; ++i) mbar_init(&full[t][i], streams);
-        fence_barrier_init();
+struct BulkRings {   // of a CTA's teams
+    uint64_t full[kMostWarps / 2][kMostAhead + 1];
+    int gave_up[kMostWarps / 2][2];
+    __device__ __forceinline__ void start(int streams) {
+        if (threadIdx.x == 0) {
+            for (int t = 0; t < kMostWarps / 2; ++t) {
+                for (int i = 0; i <= kMostAhead; ++i) mbar_init(&full[t][i], streams);
+                gave_up[t][0] = gave_up[t][1] = 0;
+            }
+            fence_barrier_init();
+        }
+        __syncthreads();
     }
-    __syncthreads();
-}
+};
 
 template <bool kF32, bool kDyF32, bool kVec, int kPer, int kThreads, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams p) {
@@ -588,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
     __shared__ float2 stats[2][kMostWarps];
     constexpr int kSize = kF32 ? 4 : 2;
     constexpr bool kBulk = kMany && !kVec;
-    __shared__ uint64_t full[kMostWarps / 2][kMostAhead + 1];
-    if constexpr (kBulk) bulk_ring_start(full, p.residual ? 3 : 2);
+    __shared__ BulkRings rings;
+    if constexpr (kBulk) rings.start(p.residual ? 3 : 2);
     constexpr Lay kLay = lay_of(kVec, kF32);
     int which, teams, turn = 0;
     const Team m = team_of<kLay, kMany>(p, &which, &teams);
@@ -622,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
     auto ring = [&] {
         uint8_t* base = reinterpret_cast<uint8_t*>(slots) + (kVec ? threadIdx.x * p.part_bytes : which * p.part_bytes);
         if constexpr (kBulk)
-            return BulkRing(base, p.slot, p.ahead, which, full[which], send);
+            return BulkRing(base, p.slot, p.ahead, which, rings.full[which], rings.gave_up[which], send);
         else
             return Ring<kVec, kMany>(base, p.slot, p.ahead, which, send);
     }();
@@ -640,8 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         const bool has = kMany || row < p.rows;
         const float mean = mean_ahead, rstd = rstd_ahead;
         if (row + stride < p.rows) mean_ahead = p.mean[row + stride], rstd_ahead = p.rstd[row + stride];
-        const uint8_t* slot = ring.next(m, send);
-        if (kBulk && !slot) return;
+        const uint8_t* slot;
+        if constexpr (kBulk)
+            slot = ring.next(m, turn, send);
+        else
+            slot = ring.next(m, send);
         const float2 move = both(-mean), scale = both(rstd);
         float2 v1 = both(0.0f), v2 = both(0.0f);
 #pragma unroll
@@ -661,7 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
         if constexpr (kMany) {
             if ((threadIdx.x & 31) == 0) stats[turn][threadIdx.x / 32] = make_float2(v[0], v[1]);
             team_barrier(which, m.size);
-            if constexpr (kBulk) ring.refill(send);
+            if constexpr (kBulk) {
+                if (ring.leaves(turn)) break;
+                ring.refill(send);
+            }
             const float2* w = stats[turn] + which * p.warps;
             turn ^= 1;   // written again after the next row's barrier
             v[0] = v[1] = 0.0f;
@@ -731,6 +754,34 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_kernel(const NormParams
             put(h, i, s);
         }
     }
+}
+
+// The ring's failure path by itself: a team of two warps waits for a copy that nothing sends.
+// One gives up at `limit` cycles; a third warp arrives in the copy's place half as long after
+// that, before the other gives up.  Both have to leave.
+__global__ void __launch_bounds__(96) norm_wait_selftest_kernel(long long limit) {
+    __shared__ BulkRings rings;
+    __shared__ uint4 slot;
+    rings.start(1);
+    const long long begin = clock64();
+    const Team m{(int)threadIdx.x, 64, 0};
+    if (threadIdx.x < 64) {
+        const long long mine = threadIdx.x < 32 ? limit : 2 * limit;
+        const auto send = [](auto...) {};
+        BulkRing ring(reinterpret_cast<uint8_t*>(&slot), sizeof slot, 1, 0, rings.full[0], rings.gave_up[0], send);
+        for (int turn = 0;; turn ^= 1) {
+            (void)ring.next(m, turn, send, mine);
+            team_barrier(0, m.size);
+            if (ring.leaves(turn, mine)) break;
+        }
+    } else if (threadIdx.x == 64) {
+        while (clock64() - begin < limit + limit / 2) __nanosleep(1000);
+        mbar_arrive(&rings.full[0][0]);
+    }
+}
+int launch_norm_wait_selftest(int64_t limit, cudaStream_t s) {
+    norm_wait_selftest_kernel<<<1, 96, 0, s>>>(limit);
+    return launch_status();
 }
 
 // ---- rows of more than 16384 columns ---------------------------------------------------

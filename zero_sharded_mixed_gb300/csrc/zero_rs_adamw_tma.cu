@@ -383,6 +383,8 @@ __global__ void bounded_wait_selftest_kernel(long long limit) {
     if (!ok && threadIdx.x == 0) atomicExch(&g_device_status, ZERO_ETIMEOUT);
 }
 
+int launch_norm_wait_selftest(int64_t limit, cudaStream_t s);   // zero_layer_norm.cu
+
 int take_device_status() {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof v) != cudaSuccess) {
@@ -404,5 +406,6 @@ int take_device_status() {
 extern "C" int zero_selftest_bounded_wait(int64_t limit_cycles, void* stream) {
     if (limit_cycles < 1 || limit_cycles > (1ll << 32)) return ZERO_EINVAL;
     zgb::bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_cycles);
-    return zgb::launch_status();
+    if (const int rc = zgb::launch_status()) return rc;
+    return zgb::launch_norm_wait_selftest(limit_cycles, static_cast<cudaStream_t>(stream));
 }

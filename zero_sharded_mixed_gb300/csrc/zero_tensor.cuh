@@ -257,9 +257,9 @@ constexpr long long kWaitCycles = 1ll << 31;   // SM cycles (about a second) bef
 
 // For a converged warp that goes on as a whole: every lane gets the same answer.  A
 // wait that gives up leaves ZERO_ETIMEOUT in *status, device memory.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, long long limit = kWaitCycles) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitCycles))) return true;
+    if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit))) return true;
     atomicExch(status, ZERO_ETIMEOUT);
     return false;
 }
