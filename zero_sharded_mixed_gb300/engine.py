@@ -232,11 +232,13 @@ class ZeroEngine(_Tracing):
         if self.micro:
             raise RuntimeError("save_checkpoint() between micro-batches: finish the step first")
         return ck.save(dirpath, self.L, self.numels, self.master, self.m, self.v, self.t,
-                       _hp(self.cfg, max(1, self.t)), out_bf16=self.out)
+                       _hp(self.cfg, max(1, self.t)), out_bf16=self.out, optimizer=self.cfg.optimizer)
 
     def load_checkpoint(self, dirpath) -> int:
-        """Restore the state saved by save_checkpoint; returns the step count."""
-        self.t = ck.restore(dirpath, self.L, self.master, self.m, self.v, out_bf16=self.out)
+        """Restore the state saved by save_checkpoint under the same optimizer; returns
+        the step count."""
+        self.t = ck.restore(dirpath, self.L, self.master, self.m, self.v, out_bf16=self.out,
+                            optimizer=self.cfg.optimizer)
         self.micro = 0
         self._last = None
         return self.t
