@@ -150,6 +150,7 @@ class MuonStep:
     takes beside one matrix's need.  v of the matrices is not touched."""
 
     SCALE = 0.2
+    MOST = 65535   # matrices that a call takes
 
     def __init__(self, L, offsets, shapes, device="cuda", workspace_bytes: int = 1 << 30):
         if len(shapes) != len(offsets):
@@ -176,7 +177,7 @@ class MuonStep:
         self.batches, need = [], 0
         for (n, k), at in by_shape.items():
             one = zb.zero_orthogonalize_workspace(1, n, k)
-            for first, count, stride in _batches(at, n * k, max(1, workspace_bytes // one)):
+            for first, count, stride in _batches(at, n * k, min(self.MOST, max(1, workspace_bytes // one))):
                 need = max(need, zb.zero_orthogonalize_workspace(count, n, k))
                 self.batches.append(self.update.as_strided((count, n, k), (stride, k, 1), first))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
