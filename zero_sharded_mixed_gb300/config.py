@@ -33,10 +33,6 @@ class ZeroConfig:
     betas: tuple = (0.9, 0.999)
     eps: float = 1e-8
     weight_decay: float = 0.0
-    optimizer: str = "adamw"                  # or "muon": matrices by orthogonalised momentum
-    momentum: float = 0.95                    # muon
-    nesterov: bool = True                     # muon
-    ns_steps: int = 5                         # muon: steps of the orthogonalisation
     zero_quantized_weights: bool = False      # stage 3: 8-bit weight gathers
     zero_quantized_gradients: bool = False    # 8-bit gradient reduce-scatter
     overlap_comm: bool = False                # stage 3: gathers one unit ahead on a side stream
@@ -45,6 +41,10 @@ class ZeroConfig:
     # WarmupDecayLR: {"min_lr", "max_lr", "warmup_steps", "total_steps"}, or None for a constant lr
     scheduler: dict | None = None
     ignored: list = field(default_factory=list)
+    optimizer: str = "adamw"                  # or "muon": matrices by orthogonalised momentum
+    momentum: float = 0.95                    # muon
+    nesterov: bool = True                     # muon
+    ns_steps: int = 5                         # muon: steps of the orthogonalisation
 
     def __post_init__(self):
         if self.stage not in (1, 2, 3):
