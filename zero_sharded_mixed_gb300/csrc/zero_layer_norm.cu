@@ -10,6 +10,7 @@
 // (16384 columns), whose threads hold the same columns, up to 32, of every row they see,
 // so that gamma, beta and the sums of the weights' gradients stay in registers.  Rows to
 // come are copied to shared memory ahead of their turn.  Everything is fp32.
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -19,8 +20,10 @@
 namespace zgb {
 
 __device__ int g_norm_status;   // ZERO_OK, or ZERO_ETIMEOUT once a bounded wait gave up
+static std::atomic<bool> g_norm_waits;   // whether a kernel with such waits was launched: a status check asks no others
 
 int take_norm_status() {
+    if (!g_norm_waits.load()) return ZERO_OK;
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_norm_status, sizeof v) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -780,6 +783,7 @@ __global__ void __launch_bounds__(96) norm_wait_selftest_kernel(long long limit)
     }
 }
 int launch_norm_wait_selftest(int64_t limit, cudaStream_t s) {
+    g_norm_waits.store(true);
     norm_wait_selftest_kernel<<<1, 96, 0, s>>>(limit);
     return launch_status();
 }
@@ -1021,6 +1025,7 @@ static int launch_norm(NormParams& p, const NormShape& s, cudaStream_t stream) {
 template <bool kF32, bool kDyF32, bool kVec, int kPer, int kThreads, bool kMany>
 static int launch_norm_grad(NormParams& p, const NormShape& s, cudaStream_t stream) {
     static Done done;
+    if (kMany && !kVec) g_norm_waits.store(true);
     void (*const kernel)(NormParams) = norm_grad_kernel<kF32, kDyF32, kVec, kPer, kThreads, kMany>;
     const int size = kF32 ? 4 : 2, sums = p.part ? kPer * 32 * s.threads : 0;   // the teams' sums, after the last row
     int smem = lay_slots(p, s, kVec, {size, kDyF32 ? 4 : 2, p.residual ? size : 0});

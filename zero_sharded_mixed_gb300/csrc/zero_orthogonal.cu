@@ -28,8 +28,10 @@
 namespace zgb {
 
 __device__ int g_orthogonal_status;   // ZERO_OK, or ZERO_ETIMEOUT once a bounded wait gave up
+static std::atomic<bool> g_orthogonal_waits;   // whether there was a call: a status check asks no others
 
 int take_orthogonal_status() {
+    if (!g_orthogonal_waits.load()) return ZERO_OK;
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_orthogonal_status, sizeof v) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -1156,6 +1158,7 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
             return rc;
     }
 
+    g_orthogonal_waits.store(true);
     if (rows * (int64_t)src.groups <= kHeldGroups) {
         if (const int rc = launch_dense(orthogonal_held_kernel, dim3((unsigned)(kHeldCtas * batch)), kHeldThreads, kHeldCtas, true, 0, s, src)) return rc;
     } else {
