@@ -673,7 +673,8 @@ int zero_layer_norm_grad(int64_t rows, int64_t cols, const void* dy, int64_t ldd
  * Errors: ZERO_EINVAL (as zero_reduce_scatter_adamw; momentum outside [0, 1), nesterov
  *   not 0 or 1, a value that is not finite; steps outside 1..100, eps negative, null
  *   coefficients, results that overlap), ZERO_ERANGE (n_src > ZERO_MAX_SRC; a shorter side above
- *   32768, 2^33 elements a matrix, 65535 matrices, workspace too small), ZERO_EALIGN, ZERO_ECUDA. */
+ *   32768, a longer one above 2^30, a matrix of 2^29 groups of eight columns (2^32 elements)
+ *   or more, more than 65535 matrices, workspace too small), ZERO_EALIGN, ZERO_ECUDA. */
 int zero_reduce_scatter_momentum(const zero_layout_t* L, const void* const* src, int32_t n_src, int32_t src_dtype,
                                  int64_t src_base, float divisor, int32_t rank_begin, int32_t rank_end,
                                  int64_t begin, int64_t end, float* m, uint16_t* u, int32_t out_mode,
