@@ -598,6 +598,16 @@ struct StepEnd {
                 for (int g = 0; g < 4; ++g)
                     if (row < p.rows) *reinterpret_cast<float2*>(q + 8 * g) = w[h][g];
             }
+            if (!mirror) return;
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {   // few, beside sums of as many terms
+                const int row = row0 + i + 8 * (k >> 3), col = col0 + 8 * (k >> 1 & 3) + 2 * j + (k & 1);
+                float t = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+                    if (n == k) t = n & 1 ? w[n >> 3][n >> 1 & 3].y : w[n >> 3][n >> 1 & 3].x;
+                if (row < p.rows && col < p.cols) p.partial[part * p.partial_stride + z * p.stride + col * p.ld + row] = t;
+            }
             return;
         }
         uint32_t d[2][4];
@@ -889,19 +899,27 @@ struct JoinParams {
     int32_t splits, side, lds;
     uint16_t* d;
 };
+// kRuns: in runs of 64, for the digits of long sums (the count took 0.6 us where there are few).
+template <bool kRuns>
 __global__ void __launch_bounds__(256) orthogonal_join_kernel(const JoinParams p) {
     await_predecessor();
     const int groups = p.lds / 8, g = blockIdx.x * 256 + threadIdx.x, row = g / groups, col = (g - row * groups) * 8;
     if (row >= p.side) return;
     const float* q = p.partial + blockIdx.y * p.square;
-    float v[8] = {};
+    float v[8] = {}, all[8] = {};
     q += (int64_t)row * p.lds + col;
 #pragma unroll 8
     for (int i = 0; i < p.splits; ++i, q += p.partial_stride) {
         const float4 a = *reinterpret_cast<const float4*>(q), b = *reinterpret_cast<const float4*>(q + 4);
         v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
         v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+        if (kRuns && i % 64 == 63)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) all[k] += v[k], v[k] = 0.0f;
     }
+    if (kRuns)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += all[k];
     *reinterpret_cast<uint4*>(p.d + blockIdx.y * p.square + (int64_t)row * p.lds + col) =
         make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
 }
@@ -958,25 +976,34 @@ static StepPlan plan_step(Step step, int64_t rows, int64_t cols, int64_t depth, 
     return best;
 }
 
-// Parts of a Gram product's sum, where few tiles would leave most pairs idle over a long
+// Parts of a Gram product's sum.  First, where few tiles would leave most pairs idle over a long
 // axis: what saves a tenth at least, the join included, which takes 5 us of a product.
-// (64 x 11008 takes 92 us, 203 in one part; 256 x 2048 84, 92 in parts.)  Sides of one row of
-// tiles, whose parts are whole: with more, half of the parts come from across the diagonal,
-// and 1024 x 8192 took 350 us for 270.  Reckoned for the device that this is made for, so
-// that the workspace does not depend on the current one.
+// (64 x 11008 takes 92 us, 203 in one part.)  Only for sides of one row of tiles, whose parts
+// are whole.  Reckoned for the device that this is made for, so that the workspace does not
+// depend on the current one.
+// Second, as many as keep a part's sum to kLongestRun blocks at any size: the tensor core's sums
+// are cut, not rounded, and lose 7e-8 of themselves for every block, so that a row of 2^28 came
+// out 12 % off in 16 parts.
 constexpr int kMostSplits = 16;
+constexpr int64_t kLongestRun = 1024;
 static int gram_splits(int64_t side, int64_t longer, int64_t batch, int64_t square) {
-    const int64_t blocks = (longer + 63) / 64, one = plan_step(kGram, side, side, longer, batch, 76).cycles;
-    int best = 1;
-    if (side > 256) return best;
-    int64_t least = one - one / 10;
-    for (int n = 2; n <= kMostSplits && n <= blocks / 4; ++n) {
-        const int64_t share = (blocks + n - 1) / n;
-        if ((n - 1) * share >= blocks || n * batch * square > ((int64_t)1 << 24) || n * batch > 65535) continue;
-        const int64_t cycles = plan_step(kGram, side, side, share * 64, batch * n, 76).cycles + 9000 + 300 * n;
-        if (cycles < least) least = cycles, best = n;
+    const int64_t blocks = (longer + 63) / 64, fewest = (blocks + kLongestRun - 1) / kLongestRun;
+    int64_t best = 1;
+    if (side <= 256) {
+        const int64_t one = plan_step(kGram, side, side, longer, batch, 76).cycles;
+        int64_t least = one - one / 10;
+        for (int n = 2; n <= kMostSplits && n <= blocks / 4; ++n) {
+            const int64_t share = (blocks + n - 1) / n;
+            if ((n - 1) * share >= blocks || n * batch * square > ((int64_t)1 << 24) || n * batch > 65535) continue;
+            const int64_t cycles = plan_step(kGram, side, side, share * 64, batch * n, 76).cycles + 9000 + 300 * n;
+            if (cycles < least) least = cycles, best = n;
+        }
     }
-    return best;
+    if (best < fewest) {   // none of them empty
+        const int64_t share = (blocks + fewest - 1) / fewest;
+        best = (blocks + share - 1) / share;
+    }
+    return (int)best;
 }
 
 // A step's launch but for its end, which changes from iteration to iteration: formed
@@ -1175,7 +1202,7 @@ extern "C" int zero_orthogonalize(int64_t batch, int64_t rows, int64_t cols, con
             j.partial = g.e.partial; j.partial_stride = g.e.partial_stride; j.square = w.square;
             j.splits = w.splits; j.side = (int32_t)side; j.lds = (int32_t)w.lds;
             j.d = at(w.a);
-            if (const int rc = launch_dense(orthogonal_join_kernel, dim3((unsigned)((side * w.lds / 8 + 255) / 256), (unsigned)batch), 256, 1, true, 0, s, j)) return rc;
+            if (const int rc = launch_dense(w.splits > 64 ? orthogonal_join_kernel<true> : orthogonal_join_kernel<false>, dim3((unsigned)((side * w.lds / 8 + 255) / 256), (unsigned)batch), 256, 1, true, 0, s, j)) return rc;
         }
         square_step.e = ending(kSquare, i);
         if (const int rc = (f32 ? launch_step<kSquare, true> : launch_step<kSquare, false>)(square_step, s)) return rc;
