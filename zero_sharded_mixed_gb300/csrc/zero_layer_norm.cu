@@ -401,9 +401,9 @@ struct Ring {
 // from the deviations costs no digits: all that is kept of it is one fp32 number `base`
 // and the small distance from there.
 // Bound by memory where there is a residual (8192 x 1600 bf16 18.3 us, 5.7 TB/s; fp32 31 us,
-// 5.9 TB/s; the first row comes after 3 us), by instructions without one (bf16 15 us for
-// half of the bytes) and element by element (8192 x 1601 35 us); one row 2.7 us, a launch
-// and two latencies.
+// 5.9 TB/s; the first row comes after 3 us), by latency without one (bf16 15 us for half of
+// the bytes: 12 warps an SM issue in 44 % of the slots) and element by element (8192 x 1601
+// 35 us); one row 2.5 us, a launch and two latencies.
 struct WarpStats {
     float n, base, off, squares;   // columns, a number near their mean, the mean's distance from it, squared deviations
 };
@@ -789,7 +789,9 @@ int launch_norm_wait_selftest(int64_t limit, cudaStream_t s) {
 }
 
 // ---- rows of more than 16384 columns ---------------------------------------------------
-// A CTA a row, in three passes (two backward) over it, the later ones out of L2.
+// A CTA a row, in three passes (two backward) over it, the later ones out of L2, element by
+// element (700 x 20000 bf16 with a residual 77 us, gradient with the weights' 96, for 17 us of
+// bytes).
 constexpr int kWideThreads = 512;
 
 // Sums over the CTA in a fixed order, to every thread: one barrier, two buffers in turn.
@@ -998,8 +1000,9 @@ struct NormShape {
 static NormShape norm_shape(int64_t rows, int64_t cols, bool vec, bool grad) {
     NormShape s{};
     const int64_t groups = (cols + 7) / 8, sms = sm_count();
-    // a gradient element by element takes more registers: fewer pieces a thread
-    // (2048 x 4097 bf16 44 us with two where four took 53; forward 31 with four, 40 with two)
+    // a gradient element by element takes more registers: fewer pieces a thread (2048 x 4097
+    // bf16 35 us with two where four took 39, 8192 x 1601 41 and 49; forward 27 with four, 32
+    // with two, but 8192 x 1601 35 and 34)
     s.per = groups <= 32 ? 1 : groups <= 64 || (!vec && grad && groups <= 1024) ? 2 : 4;
     s.many = groups > 32 * s.per;
     s.warps = s.many ? (int)((groups + 32 * s.per - 1) / (32 * s.per)) : 1;

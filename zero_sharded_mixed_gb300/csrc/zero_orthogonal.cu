@@ -944,7 +944,7 @@ static bool make_map3(const Matrices& m, int box_rows, CUtensorMap* map) {
 // The tile width with the least estimated time: a tile's blocks (bound by the tensor core,
 // or for narrow tiles by shared memory) and the part of its end that nothing hides, as
 // often as the busiest pair has them.  A symmetric result takes widths that divide 256.
-// 256 x 256 takes 55 us in tiles of 32 columns and some 97 in tiles of 256; 2048 x 8192 461 as
+// 256 x 256 takes 57 us in tiles of 32 columns and some 97 in tiles of 256; 2048 x 8192 461 as
 // planned, 500 with 128 for all, 561 with 256, 1469 with 32.
 struct StepPlan {
     int64_t tiles, full, all, lights, cycles;
