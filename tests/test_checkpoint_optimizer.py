@@ -39,7 +39,8 @@ def test_the_name_is_kept_and_checked(tmp_path):
         assert ck.consolidate(path)["step"] == 3
 
 
-def test_a_checkpoint_without_a_name_is_adamws(tmp_path):
+def test_a_checkpoint_without_a_name_goes_with_any(tmp_path):
+    """As those written before there was one, of either optimizer; resharded it has none still."""
     L = zb.zero_layout(NUMELS, 2)
     _save(tmp_path, L)
     path = os.path.join(tmp_path, ck.META)
@@ -49,9 +50,10 @@ def test_a_checkpoint_without_a_name_is_adamws(tmp_path):
     with open(path, "w") as f:
         json.dump(meta, f)
     got = [torch.zeros(L.padded_n) for _ in range(3)]
-    assert ck.restore(tmp_path, L, *got, optimizer="adamw") == 3
-    with pytest.raises(ValueError):
-        ck.restore(tmp_path, L, *got, optimizer="muon")
+    for name in ("adamw", "muon", None):
+        assert ck.restore(tmp_path, L, *got, optimizer=name) == 3
+    ck.reshard(tmp_path, tmp_path / "3", 3)
+    assert ck.load_meta(tmp_path / "3").get("optimizer") is None
 
 
 @pytest.mark.gpu

@@ -93,11 +93,11 @@ def payload_crc(path) -> int:
 
 
 def save(dirpath, L: zb.ZeroLayout, numels, master, m, v, step: int, hp: zb.ZeroAdamW,
-         out_bf16=None, rank_begin: int = 0, optimizer: str = "adamw"):
+         out_bf16=None, rank_begin: int = 0, optimizer: str | None = "adamw"):
     """Save the owners rank_begin.. of layout L: ``master``/``m``/``v`` hold their
     shards back to back (device or host tensors); ``out_bf16`` (optional, the
     full flat bf16 buffer) adds each rank's bf16 weights.  ``optimizer`` names what m
-    and v are the moments of ("adamw" or "muon").  Returns the metadata."""
+    and v are the moments of ("adamw" or "muon"; None: not known).  Returns the metadata."""
     os.makedirs(dirpath, exist_ok=True)
     S = L.shard
     n_ranks = master.numel() // S if S else 0
@@ -156,13 +156,13 @@ def restore(dirpath, L: zb.ZeroLayout, master, m, v, rank_begin: int = 0, out_bf
             optimizer: str | None = None) -> int:
     """Load the shards of owners rank_begin.. into ``master``/``m``/``v`` (and the
     bf16 weights into ``out_bf16``); the layout must match the checkpoint's, and so
-    must its optimizer where one is given (a checkpoint that names none is AdamW's).
+    must its optimizer where one is given (older checkpoints name none: any goes).
     Returns the step to continue from."""
     meta = load_meta(dirpath)
     if (meta["n"], meta["n_dp"], meta["shard"]) != (L.n, L.n_dp, L.shard):
         raise ValueError("the checkpoint was saved for another layout: reshard it first")
-    saved = meta.get("optimizer", "adamw")
-    if optimizer is not None and saved != optimizer:
+    saved = meta.get("optimizer")
+    if None not in (optimizer, saved) and saved != optimizer:
         raise ValueError(f"the checkpoint holds the moments of {saved!r}, not of {optimizer!r}: "
                          "consolidate it to go on from its weights alone")
     S = L.shard
@@ -219,7 +219,7 @@ def reshard(dir_in, dir_out, n_dp: int, align: int | None = None, bucket: int | 
     hp = zb.ZeroAdamW.make(a["lr"], a["beta1"], a["beta2"], a["eps"], a["weight_decay"],
                            max(1, meta["step"]))
     return save(dir_out, L, numels, *(torch.from_numpy(padded[k]) for k in ("master", "m", "v")),
-                meta["step"], hp, optimizer=meta.get("optimizer", "adamw"))
+                meta["step"], hp, optimizer=meta.get("optimizer"))
 
 
 # --------------------------------------------------------------------------
